@@ -10,7 +10,11 @@ moe_forward, moe_forward_host, moe_forward_stack, moe_forward_stack_steps, moe_f
 moe_load_router, moe_debug_router_logits, moe_set_batched_numerics, moe_set_swiglu, moe_get_status,
 moe_debug_dequant, moe_debug_route, moe_debug_stack_trace, moe_debug_forward_f32,
 moe_debug_set_wait, moe_last_bytes, moe_expert_bytes, moe_last_launches, moe_last_error,
-moe_forward_noalloc, moe_debug_stream_weights, moe_destroy.
+moe_forward_noalloc, moe_debug_stream_weights, moe_destroy; and the operators around the expert
+block: moe_ops_create, moe_ops_get_status, moe_ops_destroy, moe_kv_write, moe_kv_read,
+moe_attention, moe_linear, moe_sample.  Those take torch tensors and read sizes and strides from
+them; moe_kv_cache_of, moe_kv_batch_of and moe_linear_of make the descriptors that a program
+builds once and keeps (with the tensors, which they keep alive).
 """
 from __future__ import annotations
 
@@ -34,6 +38,10 @@ MOE_LOAD_GATE_UP_INTERLEAVED = 1
 MOE_LOAD_TRANSPOSED = 2
 MOE_BATCHED_MXFP4 = 0
 MOE_BATCHED_BF16 = 1
+MOE_KV_E4M3 = 1
+MOE_KV_INT8 = 2
+MOE_DT_F32 = 0
+MOE_DT_BF16 = 1
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_create", "moe_load_experts", "moe_load_experts_ex", "moe_forward", "moe_forward_host",
@@ -43,7 +51,9 @@ EXPORTS = ("moe_create", "moe_load_experts", "moe_load_experts_ex", "moe_forward
            "moe_debug_stack_trace", "moe_debug_mx_quantize", "moe_debug_batched_h",
            "moe_debug_forward_f32", "moe_debug_set_wait",
            "moe_last_bytes", "moe_expert_bytes", "moe_last_launches", "moe_last_error",
-           "moe_forward_noalloc", "moe_debug_stream_weights", "moe_destroy")
+           "moe_forward_noalloc", "moe_debug_stream_weights", "moe_destroy",
+           "moe_ops_create", "moe_ops_get_status", "moe_ops_destroy", "moe_kv_write", "moe_kv_read",
+           "moe_attention", "moe_linear", "moe_sample")
 
 
 class MoeError(RuntimeError):
@@ -57,6 +67,28 @@ class moe_config(ctypes.Structure):
                 ("num_experts", ctypes.c_int), ("num_layers", ctypes.c_int),
                 ("max_tokens", ctypes.c_int), ("max_top_k", ctypes.c_int),
                 ("format", ctypes.c_int), ("group", ctypes.c_int), ("has_bias", ctypes.c_int)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("block", ctypes.c_int),
+                ("format", ctypes.c_int)]
+
+
+class moe_kv_batch(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("table_stride", ctypes.c_int)]
+
+
+class moe_linear_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("format", ctypes.c_int),
+                ("group", ctypes.c_int)]
+
+
+class moe_sample_params(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("u", ctypes.c_void_p)]
 
 
 _lib = None
@@ -125,6 +157,23 @@ def lib() -> ctypes.CDLL:
         L.moe_forward_noalloc.restype = i
         L.moe_destroy.argtypes = [p]
         L.moe_destroy.restype = None
+        cache, batch = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch)
+        L.moe_ops_create.argtypes = [ctypes.POINTER(p)]
+        L.moe_ops_create.restype = i
+        L.moe_ops_get_status.argtypes = [p, p]
+        L.moe_ops_get_status.restype = i
+        L.moe_ops_destroy.argtypes = [p]
+        L.moe_ops_destroy.restype = None
+        L.moe_kv_write.argtypes = [p, cache, batch, p, ll, p, ll, p]
+        L.moe_kv_write.restype = i
+        L.moe_kv_read.argtypes = [p, cache, batch, p, ll, p, ll, p]
+        L.moe_kv_read.restype = i
+        L.moe_attention.argtypes = [p, cache, batch, p, ll, i, ctypes.c_float, i, p, p, p, p]
+        L.moe_attention.restype = i
+        L.moe_linear.argtypes = [p, ctypes.POINTER(moe_linear_weights), p, ll, i, p, ll, i, p]
+        L.moe_linear.restype = i
+        L.moe_sample.argtypes = [p, p, i, ll, i, i, ctypes.POINTER(moe_sample_params), p, p, p]
+        L.moe_sample.restype = i
         _lib = L
     return _lib
 
@@ -288,3 +337,160 @@ def moe_forward_noalloc(cfg: moe_config, gu_codes, gu_scales, gu_bias, dn_codes,
 
 def moe_destroy(h) -> None:
     lib().moe_destroy(h)
+
+
+# ------------------------------------------- operators around the expert block
+
+def _need(t, name, dtype, dims):
+    """A CUDA tensor of that type and number of dimensions, its last dimension
+    contiguous: what the C call, which sees only an address, takes it for."""
+    if not t.is_cuda or t.dim() != dims or t.dtype is not dtype or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: a CUDA tensor of {dtype} with {dims} dimensions, the last one contiguous, is needed "
+                         f"(got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device})")
+    return t
+
+
+def _dense(t, name, dtype, dims):
+    if not _need(t, name, dtype, dims).is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed (shape {tuple(t.shape)}, strides {t.stride()})")
+    return t
+
+
+def moe_ops_create() -> int:
+    h = ctypes.c_void_p()
+    _check(lib().moe_ops_create(ctypes.byref(h)))
+    return h.value
+
+
+def moe_ops_get_status(o, stream=None) -> int:
+    return lib().moe_ops_get_status(o, _stream(stream))
+
+
+def moe_ops_destroy(o) -> None:
+    lib().moe_ops_destroy(o)
+
+
+def moe_kv_cache_of(codes, scales, block, head_dim, format) -> moe_kv_cache:
+    """The cache in codes uint8 [num_blocks][kv_heads][2][block * head_dim] and scales fp32
+    [num_blocks][kv_heads][2]."""
+    import torch
+    _dense(codes, "codes", torch.uint8, 4)
+    _dense(scales, "scales", torch.float32, 3)
+    nb, heads = codes.shape[:2]
+    if tuple(codes.shape[2:]) != (2, block * head_dim) or tuple(scales.shape) != (nb, heads, 2):
+        raise ValueError(f"moe_kv_cache_of: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not a cache of "
+                         f"blocks of {block} tokens with head_dim {head_dim}")
+    c = moe_kv_cache(codes.data_ptr(), scales.data_ptr(), nb, heads, head_dim, block, format)
+    c.tensors = (codes, scales)
+    return c
+
+
+def moe_kv_batch_of(cu, kv_len, table, n_tokens) -> moe_kv_batch:
+    """The batch in int32 cu [n_seqs + 1], kv_len [n_seqs] and table [n_seqs][table_stride]."""
+    import torch
+    _dense(cu, "cu", torch.int32, 1)
+    _dense(kv_len, "kv_len", torch.int32, 1)
+    _dense(table, "table", torch.int32, 2)
+    n = kv_len.shape[0]
+    if cu.shape[0] != n + 1 or table.shape[0] != n:
+        raise ValueError(f"moe_kv_batch_of: cu {tuple(cu.shape)}, kv_len {tuple(kv_len.shape)} and table {tuple(table.shape)} "
+                         "do not describe the same sequences")
+    b = moe_kv_batch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n, n_tokens, table.shape[1])
+    b.tensors = (cu, kv_len, table)
+    return b
+
+
+def _rows(t, width):
+    """Address and row stride of a tensor whose rows of `width` elements are contiguous (the stride of a single row is
+    arbitrary in torch)."""
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def _kv_rows(t, name, cache, batch):
+    import torch
+    _need(t, name, torch.bfloat16, 3)
+    H, D = cache.kv_heads, cache.head_dim
+    if tuple(t.shape) != (batch.n_tokens, H, D) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: rows [{batch.n_tokens}][{H}][{D}] with contiguous heads are needed (got {tuple(t.shape)}, "
+                         f"strides {t.stride()})")
+    return _rows(t, H * D)
+
+
+def moe_kv_write(o, cache, batch, k, v, stream=None):
+    kp, ks = _kv_rows(k, "k", cache, batch)
+    vp, vs = _kv_rows(v, "v", cache, batch)
+    return _check(lib().moe_kv_write(o, cache, batch, kp, ks, vp, vs, _stream(stream)))
+
+
+def moe_kv_read(o, cache, batch, k, v, stream=None):
+    kp, ks = _kv_rows(k, "k", cache, batch)
+    vp, vs = _kv_rows(v, "v", cache, batch)
+    return _check(lib().moe_kv_read(o, cache, batch, kp, ks, vp, vs, _stream(stream)))
+
+
+def moe_attention(o, cache, batch, q, out, lse=None, sinks=None, window=0, scale=None, stream=None):
+    """q bf16 [n_tokens][q_heads][head_dim] (rows may be strided), out like it and contiguous, lse fp32
+    [n_tokens][q_heads], sinks fp32 [q_heads]; scale defaults to head_dim ** -0.5."""
+    import torch
+    _need(q, "q", torch.bfloat16, 3)
+    _dense(out, "out", torch.bfloat16, 3)
+    T, heads, D = q.shape
+    if T != batch.n_tokens or D != cache.head_dim or (heads > 1 and q.stride(1) != D) or out.shape != q.shape:
+        raise ValueError(f"moe_attention: q {tuple(q.shape)} (strides {q.stride()}) and out {tuple(out.shape)} are not "
+                         f"{batch.n_tokens} rows of heads of {cache.head_dim}")
+    if lse is not None and tuple(_dense(lse, "lse", torch.float32, 2).shape) != (T, heads):
+        raise ValueError(f"moe_attention: lse {tuple(lse.shape)} is not [{T}][{heads}]")
+    if sinks is not None and _dense(sinks, "sinks", torch.float32, 1).shape[0] != heads:
+        raise ValueError(f"moe_attention: sinks {tuple(sinks.shape)} is not [{heads}]")
+    qp, qs = _rows(q, heads * D)
+    return _check(lib().moe_attention(o, cache, batch, qp, qs, heads, D ** -0.5 if scale is None else scale,
+                                      window, _ptr(sinks), out.data_ptr(), _ptr(lse), _stream(stream)))
+
+
+def moe_linear_of(codes, scales, bias, format, group) -> moe_linear_weights:
+    """Weights in codes uint8 [rows][cols / 2], scales uint8 [rows][cols / 32] (MXFP4) or fp16 [rows][cols / group]
+    (int4), bias bf16 [rows] or None."""
+    import torch
+    _dense(codes, "codes", torch.uint8, 2)
+    _dense(scales, "scales", torch.uint8 if format == MOE_FMT_MXFP4 else torch.float16, 2)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    if scales.shape[0] != rows or scales.shape[1] * group != cols:
+        raise ValueError(f"moe_linear_of: scales {tuple(scales.shape)} are not one per {group} of [{rows}][{cols}]")
+    if bias is not None and _dense(bias, "bias", torch.bfloat16, 1).shape[0] != rows:
+        raise ValueError(f"moe_linear_of: bias {tuple(bias.shape)} is not [{rows}]")
+    w = moe_linear_weights(codes.data_ptr(), scales.data_ptr(), _ptr(bias), rows, cols, format, group)
+    w.tensors = (codes, scales, bias)
+    return w
+
+
+def moe_linear(o, w, x, out, stream=None):
+    """x bf16 [M][cols], out fp32 or bf16 [M][rows]; the rows of both may be strided."""
+    import torch
+    _need(x, "x", torch.bfloat16, 2)
+    bf = out.dtype is torch.bfloat16
+    _need(out, "out", torch.bfloat16 if bf else torch.float32, 2)
+    M = x.shape[0]
+    if x.shape[1] != w.cols or out.shape[0] != M or out.shape[1] != w.rows:
+        raise ValueError(f"moe_linear: x {tuple(x.shape)} and out {tuple(out.shape)} do not fit weights [{w.rows}][{w.cols}]")
+    xp, xs = _rows(x, w.cols)
+    op, os_ = _rows(out, w.rows)
+    return _check(lib().moe_linear(o, w, xp, xs, M, op, os_,
+                                   MOE_DT_BF16 if bf else MOE_DT_F32, _stream(stream)))
+
+
+def moe_sample(o, logits, temperature, top_k, top_p, min_p, u, token, logprob=None, stream=None):
+    """logits fp32 or bf16 [M][V] (rows may be strided); temperature, top_p, min_p, u fp32 [M] and top_k int32 [M], each
+    but u possibly None; token int32 [M], logprob fp32 [M] or None."""
+    import torch
+    bf = logits.dtype is torch.bfloat16
+    _need(logits, "logits", torch.bfloat16 if bf else torch.float32, 2)
+    M, V = logits.shape
+    f, n = torch.float32, torch.int32
+    for t, name, dtype in ((temperature, "temperature", f), (top_k, "top_k", n), (top_p, "top_p", f), (min_p, "min_p", f),
+                           (u, "u", f), (token, "token", n), (logprob, "logprob", f)):
+        if t is not None and _dense(t, name, dtype, 1).shape[0] != M:
+            raise ValueError(f"moe_sample: {name} {tuple(t.shape)} is not [{M}]")
+    par = moe_sample_params(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u))
+    lp, ls = _rows(logits, V)
+    return _check(lib().moe_sample(o, lp, MOE_DT_BF16 if bf else MOE_DT_F32, ls, M, V, par,
+                                   _ptr(token), _ptr(logprob), _stream(stream)))

@@ -413,6 +413,163 @@ int moe_forward_noalloc(const moe_config* cfg, const void* gu_codes, const void*
 /* Release a handle and all device memory it owns.  NULL is a no-op. */
 void moe_destroy(moe_handle* h);
 
+/* ======================================================================
+ * The operators around the expert block in a decode step, and in the prompt
+ * before it: an 8-bit paged key/value cache, attention over it, projections
+ * with 4-bit weights, and sampling.  The pages name them as the rest of the
+ * decode ("Sovereign gpt-oss-20B (MXFP4) on Apple Silicon", sections 1 and 3:
+ * attention with sinks and a sliding window, the LM head; the "greedy, KV"
+ * decode loop of "Single-stream int4 decode of a 30B MoE").
+ *
+ * All tensors, the cache and the weights among them, are the caller's device
+ * memory, borrowed for the work that a call enqueues.  A moe_ops handle holds
+ * the workspace and a status word; the conventions at the top of this file
+ * (status codes, checks before anything is enqueued, streams, one thread and
+ * one stream at a time per handle, nothing allocated by a call, no host work
+ * that depends on device values) hold for it too.  Each call is one launch and can be captured in a CUDA graph.  What a device-side check finds (metadata that does not describe the
+ * batch, a block number outside the cache) sets MOE_ERR_DEVICE_FAULT in the
+ * handle's status word and skips that sequence or block.
+ * ====================================================================== */
+
+typedef struct moe_ops moe_ops;
+
+/* A handle on the current device: allocates the workspace (a few MB, whatever
+ * the sizes of later calls). */
+int moe_ops_create(moe_ops** out);
+
+/* Synchronise `stream`; return (and clear) the handle's device status: MOE_OK,
+ * MOE_ERR_DEVICE_FAULT or MOE_ERR_DEVICE_TIMEOUT, or MOE_ERR_CUDA. */
+int moe_ops_get_status(moe_ops* o, void* stream);
+
+/* Release the workspace.  NULL is a no-op. */
+void moe_ops_destroy(moe_ops* o);
+
+/* An 8-bit paged cache of one layer: num_blocks blocks of `block` tokens each,
+ * with one fp32 scale for each (block, head, K or V).
+ *   codes  u8 [num_blocks][kv_heads][2][block * head_dim], 16-byte aligned:
+ *          K codes as [block][head_dim], then V codes as [head_dim][block]
+ *          (transposed: attention multiplies V along the tokens);
+ *   scales fp32 [num_blocks][kv_heads][2] (K, V), 8-byte aligned.
+ * A value is its code times the scale.  MOE_KV_INT8: codes -127..127.
+ * MOE_KV_E4M3: OCP FP8 E4M3 codes (no NaN is ever written) and scales that
+ * are powers of two.  block 32, 64 or 128; head_dim 64 or 128; kv_heads
+ * 1..256. */
+typedef enum { MOE_KV_E4M3 = 1, MOE_KV_INT8 = 2 } moe_kv_format;
+typedef struct {
+    void* codes;
+    float* scales;
+    int num_blocks, kv_heads, head_dim, block, format;
+} moe_kv_cache;
+
+/* A batch of tokens of several sequences, all device arrays of int32:
+ *   cu     [n_seqs + 1]: tokens cu[b] .. cu[b+1] - 1 of the batch belong to
+ *          sequence b (0 <= cu[b] <= cu[b+1] <= n_tokens);
+ *   kv_len [n_seqs]: the sequence's cached tokens, the batch's own included:
+ *          they are its last ones, at positions kv_len - n .. kv_len - 1;
+ *   table  [n_seqs][table_stride]: the cache block of each `block` positions
+ *          (only entries below ceil(kv_len / block) are read).
+ * n_seqs 1..1024, n_tokens 1..2^20; a sequence may have no tokens. */
+typedef struct {
+    const int* cu;
+    const int* kv_len;
+    const int* table;
+    int n_seqs, n_tokens, table_stride;
+} moe_kv_batch;
+
+/* Quantise the batch's keys and values (bf16 [n_tokens][kv_heads][head_dim],
+ * rows k_stride / v_stride elements apart) into the cache.  For each (block,
+ * head) and K and V apart, with a the largest finite magnitude among the new
+ * values (at least 2^-100):
+ *   INT8 scale a / 127 (rounded to fp32); E4M3: the smallest 2^e with
+ *   a <= 448 * 2^e;
+ *   a block whose first token is written takes that scale, and its unwritten
+ *   tokens get code 0; a block that already holds earlier tokens of the
+ *   sequence keeps its scale, or takes the new one if that is larger: then the
+ *   earlier tokens' codes c become round(c * (old * (1 / new)));
+ *   code = round(x * (1 / scale)), to nearest even, saturating; a NaN becomes
+ *   0 and an infinity the largest code.
+ * (1 / scale and the products are single fp32 operations.)  Sequences must
+ * not share a block that is written.  The rows are 16-byte aligned and the
+ * strides multiples of 8. */
+int moe_kv_write(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k_bf16,
+                 long long k_stride, const void* v_bf16, long long v_stride, void* stream);
+
+/* Read the batch's tokens back: code * scale, rounded to bf16, into rows
+ * k_stride / v_stride elements apart.  Conditions as for moe_kv_write; the
+ * same batch names the tokens (so cu and kv_len of another batch, say all of
+ * a prefix, read those). */
+int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, void* k_bf16,
+                long long k_stride, void* v_bf16, long long v_stride, void* stream);
+
+/* Attention of the batch's tokens over the cache (which holds their own keys
+ * and values already).  q bf16 [n_tokens][q_heads][head_dim], rows q_stride
+ * elements apart (16-byte aligned, a multiple of 8); query head h reads kv
+ * head h / (q_heads / kv_heads); q_heads a multiple of kv_heads, at most 1024.
+ * The token at position i sees positions j <= i, and with window > 0 only
+ * j > i - window.  s_j = scale q . k_j;
+ *   out = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink - m)),
+ * m the largest of them, sinks fp32 [q_heads] or NULL (no such term).
+ * out bf16 [n_tokens][q_heads][head_dim], contiguous, 16-byte aligned; must not
+ * overlap q (checked).  lse fp32 [n_tokens][q_heads] or NULL: m + log of the
+ * denominator.  A row of which nothing is visible (its blocks are missing)
+ * is 0, with the sink (or -inf) as its lse.
+ * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
+ * of each row, codes are exact in f16, and e^(s_j - m) enters the second
+ * product as f16. */
+int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
+                  long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,
+                  float* lse, void* stream);
+
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+
+/* A matrix of 4-bit weights W [rows][cols], format and group as in moe_config:
+ *   codes  u8 [rows][cols/2]; scales u8 [rows][cols/32] (MXFP4) or fp16
+ *          [rows][cols/group] (int4); both 16-byte aligned;
+ *   bias   bf16 [rows] or NULL.
+ * cols a multiple of 32 (MXFP4) or of group (int4: 32, 64, 128 or 256), at most
+ * 32768; rows 1..2^24. */
+typedef struct {
+    const void* codes;
+    const void* scales;
+    const void* bias;
+    int rows, cols, format, group;
+} moe_linear_weights;
+
+/* out[m] = W x[m] + bias for M = 1..64 tokens (the decode projections and the
+ * LM head; "Single-stream int4 decode of a 30B MoE", sections 1 and 6: packed
+ * int4 dequantised on chip).  x bf16 [M][cols], rows x_stride elements apart
+ * (16-byte aligned, a multiple of 8); out fp32 or bf16 [M][rows], rows
+ * out_stride elements apart.  x enters as f16 after an exact power-of-two
+ * rescale per token, weights are exact in f16, sums are fp32.  x and out must
+ * not overlap. */
+int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long long x_stride, int M, void* out,
+               long long out_stride, int out_type, void* stream);
+
+/* Per-row device arrays [M]; every one but u may be NULL. */
+typedef struct {
+    const float* temperature;   /* NULL: 1.  <= 0 (or NaN): the largest logit, lowest index first */
+    const int* top_k;           /* <= 0 or >= V: off */
+    const float* top_p;         /* >= 1: off; <= 0: the first token alone */
+    const float* min_p;         /* <= 0: off; > 1 counts as 1 */
+    const float* u;             /* in [0, 1); clamped to [0, 1 - 2^-24] */
+} moe_sample_params;
+
+/* One token for each of M rows of logits [M][V] (fp32 or bf16, rows `stride`
+ * elements apart), V 1..2^19.  Order: larger logit first, ties to the lower
+ * index; NaN counts as -inf.  With l* the largest logit and z = (l - l*) *
+ * (1 / T), a token's weight is round(e^z * 2^31), an integer, so that sums are
+ * exact in any order.  Kept are, one filter after another:
+ *   top-k: the first k;
+ *   top-p: the shortest prefix of those whose weights reach top_p times the sum
+ *          of all of those (product in fp64, at least one token);
+ *   min-p: those whose weight is at least min_p * 2^31.
+ * token[m]: the first kept one, by index, at which the running sum of weights
+ * exceeds u times their sum.  logprob[m] (or NULL): z - log(sum / 2^31) of that
+ * token; 0 where T <= 0.  A row of -inf only gives its lowest index and
+ * logprob -inf; with +inf among the logits only those have weight. */
+int moe_sample(moe_ops* o, const void* logits, int logits_type, long long stride, int M, int V,
+               const moe_sample_params* p, int* token, float* logprob, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,174 @@
+"""Attention over the 8-bit paged cache against its formula in 64 bits."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import bit_moe_decode_02_gb300 as moe  # noqa: E402
+from ops_testlib import Cache, attention, handle, i32, ok  # noqa: E402
+
+FMTS = [moe.MOE_KV_E4M3, moe.MOE_KV_INT8]
+
+
+def check(c, new, lens, heads, window=0, sinks=None, scale=None, qscale=1.0, seed=0, q=None):
+    o = handle()
+    T = sum(new)
+    if q is None:
+        g = torch.Generator(device="cuda").manual_seed(seed + 17)
+        q = (torch.randn(T, heads, c.D, generator=g, device="cuda") * qscale).bfloat16()
+    scale = c.D ** -0.5 if scale is None else scale
+    out = torch.full((T, heads, c.D), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, heads), 9.0, device="cuda")
+    moe.moe_attention(o, c.desc, c.batch(new, lens), q, out, lse, sinks, window, scale)
+    ok(o)
+    want, wlse, bound = attention(c, new, lens, q, scale, window, sinks)
+    err = (out.double() - want).abs()
+    assert torch.isfinite(out).all()
+    assert (err <= bound).all(), (err / bound).max().item()
+    s_mag = max(1.0, float(q.abs().max()) * 8 * c.D * abs(scale))
+    assert ((lse.double() - wlse).abs() <= 2.0 ** -19 * (s_mag + wlse.abs())).all()
+    return out, lse
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk", [32, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(8, 8), (16, 2), (6, 2), (20, 1), (64, 2)])
+def test_decode(fmt, blk, D, heads, kv):
+    """One token per sequence, caches from a single token on, ends inside a block whose unused tokens hold large codes."""
+    lens = [1, 2, blk - 1, blk, blk + 1, 333, 1000, 7 * blk]
+    c = Cache(lens, kv, D, blk, fmt, seed=1).fill(seed=blk + D + heads, poison=True)
+    check(c, [1] * len(lens), lens, heads)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length", [4096, 40001])
+def test_one_long_sequence(fmt, D, length):
+    c = Cache([length], 2, D, 64, fmt).fill(seed=length)
+    check(c, [1], [length], 16, sinks=torch.randn(16, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk,D", [(32, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("heads,kv", [(4, 4), (16, 2), (10, 1)])
+@pytest.mark.parametrize("window", [0, 1, 50, 200])
+def test_ragged_prompts(fmt, blk, D, heads, kv, window):
+    """Sequences with no, one and many new tokens in one batch, with and without what came before."""
+    new = [0, 1, 300, 17, 2, 129, 64]
+    had = [40, 700, 0, 1, 129, 511, 64]
+    lens = [a + b for a, b in zip(new, had)]
+    c = Cache(lens, kv, D, blk, fmt, seed=2).fill(seed=blk + heads, poison=True)
+    check(c, new, lens, heads, window=window, sinks=torch.randn(heads, device="cuda") * 3)
+
+
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 5000])
+def test_windows(window):
+    lens = [1, 64, 65, 130, 1000, 4097]
+    c = Cache(lens, 2, 64, 64, moe.MOE_KV_E4M3).fill(seed=window)
+    check(c, [1] * 6, lens, 16, window=window)
+    check(c, [1, 2, 3, 4, 5, 6], lens, 16, window=window)
+
+
+def test_many_sequences():
+    n = 700
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(1, 400, (n,), generator=g).tolist()
+    c = Cache(lens, 1, 64, 64, moe.MOE_KV_INT8).fill(seed=1)
+    check(c, [1] * n, lens, 8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_extreme_scores(fmt):
+    """Softmaxes that are nearly one-hot, queries near both ends of bf16's range, a query of zeros, scale of either sign."""
+    lens = [200, 1500]
+    c = Cache(lens, 2, 64, 64, fmt).fill(seed=3)
+    check(c, [1, 1], lens, 8, qscale=30.0)
+    check(c, [1, 1], lens, 8, qscale=2.0 ** 100, scale=2.0 ** -103)
+    check(c, [1, 1], lens, 8, qscale=2.0 ** -110, scale=2.0 ** 107)
+    check(c, [3, 40], lens, 8, scale=-0.3)
+    check(c, [3, 40], lens, 8, scale=0.0)
+    check(c, [1, 20], lens, 8, q=torch.zeros(21, 8, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_block_scales_of_very_different_size():
+    """Neighbouring blocks whose scales are 2^20 apart, in K (a few keys take all) and in V."""
+    c = Cache([640], 1, 128, 64, moe.MOE_KV_E4M3).fill(seed=8)
+    c.scales[:, :, 1] *= torch.pow(2.0, torch.arange(c.scales.shape[0], device="cuda")[:, None] % 3 * 10.0)
+    check(c, [1], [640], 4)
+    check(c, [100], [640], 4)
+
+
+def test_sinks_of_any_size():
+    c = Cache([100, 3], 2, 64, 64, moe.MOE_KV_E4M3).fill(seed=5)
+    for value in (-math.inf, -1e30, 0.0, 60.0, 1e30):
+        s = torch.full((4,), value, device="cuda")
+        check(c, [1, 3], [100, 3], 4, sinks=s)
+
+
+def test_missing_blocks_leave_rows_empty():
+    """A row none of whose blocks exist is zero, its lse the sink (or -inf); the status word says so."""
+    o = handle()
+    for new in (1, 40):
+        for sinks in (None, torch.tensor([0.5, -2.0], device="cuda")):
+            c = Cache([40, 200], 1, 64, 64, moe.MOE_KV_E4M3).fill(seed=6)
+            q = torch.randn(2 * new, 2, 64, device="cuda").bfloat16()
+            out, lse = torch.full_like(q, 5.0), torch.full((2 * new, 2), 5.0, device="cuda")
+            c.dtable[0, 0] = -1
+            moe.moe_attention(o, c.desc, c.batch([new, new], [40, 200]), q, out, lse, sinks)
+            assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
+            assert (out[:new] == 0).all()
+            want = torch.full((2,), -math.inf, device="cuda") if sinks is None else sinks
+            assert torch.allclose(lse[:new], want.expand(new, 2), rtol=0, atol=1e-6)
+            ref, _, bound = attention(c, [0, new], [40, 200], q[new:], 64 ** -0.5, 0, sinks)
+            assert ((out[new:].double() - ref).abs() <= bound).all()
+
+
+def test_bad_metadata_sets_the_status():
+    o = handle()
+    c = Cache([100, 100], 1, 64, 64, moe.MOE_KV_E4M3).fill(seed=6)
+    q = torch.randn(2, 2, 64, device="cuda").bfloat16()
+    out = torch.zeros_like(q)
+    for cu, lens in (([0, 2, 1], [100, 100]), ([0, 1, 3], [100, 100]), ([0, 1, 2], [100, 0]), ([0, 1, 2], [1 << 30, 100])):
+        moe.moe_attention(o, c.desc, moe.moe_kv_batch_of(i32(cu), i32(lens), c.dtable, 2), q, out)
+        assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
+    check(c, [1, 1], [100, 100], 2)
+
+
+def test_strided_queries_and_repeats():
+    """Queries inside a fused projection's rows; the same call twice gives the same bits."""
+    o = handle()
+    lens = [3000, 50, 1]
+    c = Cache(lens, 2, 64, 64, moe.MOE_KV_INT8).fill(seed=7)
+    fused = torch.randn(3, 16 + 4, 64, device="cuda").bfloat16()
+    q = fused[:, :16]
+    a, la = check(c, [1, 1, 1], lens, 16, q=q)
+    for _ in range(3):
+        out, lse = torch.empty_like(a), torch.empty_like(la)
+        moe.moe_attention(o, c.desc, c.batch([1, 1, 1], lens), q, out, lse)
+        assert torch.equal(out, a) and torch.equal(lse, la)
+    moe.moe_attention(o, c.desc, c.batch([1, 1, 1], lens), q, out)        # no lse wanted
+    assert torch.equal(out, a)
+
+
+def test_in_a_graph():
+    o = handle()
+    lens = [500, 70]
+    c = Cache(lens, 2, 64, 64, moe.MOE_KV_E4M3).fill(seed=9)
+    q = torch.randn(2, 8, 64, device="cuda").bfloat16()
+    out, b = torch.empty_like(q), c.batch([1, 1], lens)
+    moe.moe_attention(o, c.desc, b, q, out)
+    want = out.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_attention(o, c.desc, b, q, out)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
