@@ -3,6 +3,29 @@
 // out_i = sum_j e^{s_ij - m_i} v_j / (sum_j e^{s_ij - m_i} + e^{sink - m_i}),
 // s_ij = scale q_i . k_j over the keys j that token i sees: its own position
 // and before it, and with a window only the last `window` of them.
+//
+// decode_attn_kernel: one pass over the keys with a running maximum and sum.
+// Bound by HBM: every visible code byte is read once for the (token, head)
+// rows that share it, 16 at a time (an m16n8k16 MMA's rows).
+//  - Work.  A tile is one cache block of one item (sequence, 16-row tile, kv
+//    head); all tiles of the call, in order, are cut into equal contiguous runs,
+//    one for each group of warps, whatever the lengths: the lengths are on the
+//    device, so the cut is made there.  Runs that end inside an item leave
+//    partial results, which are joined in a fixed order (results do not depend
+//    on timing): within a CTA, then by the last CTA to arrive at an item's
+//    counter.
+//  - Loads.  A block's K and V codes of one head are contiguous: one bulk copy
+//    per tile into the group's ring (192 KB in flight per SM), its scales with
+//    an 8-byte cp.async on the same barrier.
+//  - Operands.  Codes are exact in f16, so both products are f16 MMAs with fp32
+//    sums.  The order of the summed index of an MMA is free: d for Q K^T and
+//    the tokens for P V are taken so that a thread's operand bytes are
+//    contiguous (16 of K, 8 of the transposed V) and the scores a thread holds
+//    are exactly the probabilities that it feeds to the second product.
+//  - Scales.  K's multiplies the scores.  V's enters the exponent: O is kept in
+//    units of a reference scale, p' = 2^(s - m + log2(vs / ref)), and changes
+//    unit only when a block's scale leaves [ref / 2, 2 ref]; the running maximum
+//    likewise moves only when a score passes it by 2^8 (p' <= 2^9 in f16).
 #include <cstdint>
 
 #include "kv_device.cuh"
@@ -11,76 +34,713 @@
 namespace moe {
 namespace {
 
-// One warp per (token, query head), one key at a time.
-__global__ void __launch_bounds__(128) attention_simple_kernel(AttnArgs a)
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 16;                 // rows of an item: (token, query head of the kv head) pairs
+constexpr int kSub = 32;                  // tokens of a block that one warp takes
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.0e38f;         // running maximum of a row that has seen no key
+constexpr float kSlack = 8.0f;            // log2 units that a score may pass the kept maximum by
+
+typedef long long i64;
+
+// fp32 workspace: partial results of the groups' first and last items, then of the CTAs'.
+constexpr int kMaxGroups = 8;
+__host__ __device__ constexpr i64 slot_floats() { return kRows * 128 + 2 * kRows; }
+
+struct Item {
+    int b, c0, n, len;   // sequence
+    int rt, h;           // row tile, kv head
+    int jlo, jhi;        // its blocks
+    i64 t0;              // its first tile
+};
+
+__device__ __forceinline__ void block_range(const AttnArgs& a, int n, int len, int rt, int& jlo, int& jhi)
 {
-    const KvView& c = a.c;
-    const int tok = blockIdx.x, lane = threadIdx.x & 31, hq = blockIdx.y * 4 + (threadIdx.x >> 5);
-    if (hq >= a.q_heads)
+    const int r0 = rt * kRows, r1 = min(r0 + kRows, n * a.group) - 1;
+    const int p0 = len - n + r0 / a.group, p1 = len - n + r1 / a.group;
+    jhi = p1 / a.c.blk;
+    jlo = a.window > 0 && p0 >= a.window ? (p0 - a.window + 1) / a.c.blk : 0;
+}
+
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, int n) { return (n * a.group + kRows - 1) / kRows; }
+
+__device__ __forceinline__ i64 tiles_of(const AttnArgs& a, int b)
+{
+    int c0, n, len;
+    if (!kv::sequence(a.c, b, c0, n, len)) {
+        atomicExch(a.c.status, MOE_ERR_DEVICE_FAULT);
+        return 0;
+    }
+    i64 t = 0;
+    for (int rt = 0, nrt = row_tiles(a, n); rt < nrt; ++rt) {
+        int lo, hi;
+        block_range(a, n, len, rt, lo, hi);
+        t += hi - lo + 1;
+    }
+    return t * a.c.H;
+}
+
+// The item that holds tile t, from the prefix sums of the sequences' tiles.
+__device__ __forceinline__ void find_item(const AttnArgs& a, const i64* pre, i64 t, Item& it)
+{
+    int lo = 0, hi = a.c.n_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pre[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    it.b = lo;
+    kv::sequence(a.c, lo, it.c0, it.n, it.len);
+    i64 at = pre[lo];
+    for (it.rt = 0;; ++it.rt) {
+        block_range(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+        const i64 here = (i64)(it.jhi - it.jlo + 1) * a.c.H;
+        if (t < at + here)
+            break;
+        at += here;
+    }
+    const int nb = it.jhi - it.jlo + 1;
+    it.h = (int)((t - at) / nb);
+    it.t0 = at + (i64)it.h * nb;
+}
+
+__device__ __forceinline__ void next_item(const AttnArgs& a, const i64* pre, Item& it)
+{
+    it.t0 += it.jhi - it.jlo + 1;
+    if (++it.h < a.c.H)
         return;
-    const int h = hq / a.group, D = c.D, per = D / 32;
-    int b = -1, c0 = 0, n = 0, len = 0;
-    for (int i = 0; i < c.n_seqs; ++i) {
-        int x0, xn, xl;
-        if (!kv::sequence(c, i, x0, xn, xl)) {
+    it.h = 0;
+    if (++it.rt < row_tiles(a, it.n)) {
+        block_range(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+        return;
+    }
+    find_item(a, pre, it.t0, it);
+}
+
+// Four code bytes -> two f16 pairs, exact.
+template <int FMT>
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    if constexpr (FMT == MOE_KV_E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+    } else {
+        // v + 128 below f16's 1024: 0x64uu is 1024 + uu
+        w ^= 0x80808080u;
+        const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+        __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+        lo = *reinterpret_cast<uint32_t*>(&x);
+        hi = *reinterpret_cast<uint32_t*>(&y);
+    }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads)
+{
+    if (threads == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// One row's final value from its sums: the sink joins the denominator.
+struct Final {
+    float mul, lse;
+};
+__device__ __forceinline__ Final finish(float m, float l, const float* sinks, int hq)
+{
+    float M = m;
+    if (sinks) {
+        const float ms = sinks[hq] * kLog2e;
+        M = fmaxf(m, ms);
+        l = l * ex2(m - M) + (ms == M ? 1.0f : ex2(ms - M));
+    }
+    Final f;
+    f.mul = l > 0.0f ? ex2(m - M) / l : 0.0f;
+    f.lse = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    return f;
+}
+
+// Where row r of an item goes.
+struct Place {
+    int c0, r0, h;   // first token of the sequence in the batch, first row of the tile, kv head
+    int nrows;
+};
+__device__ __forceinline__ void store_row4(const AttnArgs& a, const Place& p, int r, int col, float4 v, const Final& f)
+{
+    const int row = p.r0 + r, tok = p.c0 + row / a.group, hq = p.h * a.group + row % a.group;
+    const i64 at = ((i64)tok * a.q_heads + hq) * a.c.D + col;
+    uint2 o;
+    o.x = tc::f2bf16_rne(v.x * f.mul) | (uint32_t)tc::f2bf16_rne(v.y * f.mul) << 16;
+    o.y = tc::f2bf16_rne(v.z * f.mul) | (uint32_t)tc::f2bf16_rne(v.w * f.mul) << 16;
+    *reinterpret_cast<uint2*>(a.out + at) = o;
+    if (a.lse && col == 0)
+        a.lse[(i64)tok * a.q_heads + hq] = f.lse;
+}
+
+struct Piece {           // an unfinished item of a group
+    i64 t0, t1;          // the item's tiles
+    Place p;
+    int used;
+};
+
+template <int D, int FMT, int BLK>
+struct Decode {
+    static constexpr int GW = BLK / kSub;            // warps of a group
+    static constexpr int NG = kWarps / GW;           // groups of a CTA
+    static constexpr int STAGE = 2 * BLK * D;        // bytes of a tile
+    static constexpr int NS = D == 64 ? 6 : 3;       // stages of a group's ring: 192 KB per CTA in all
+    static constexpr int OFF_HDR = NG * NS * STAGE;                    // per stage: two scales, valid
+    static constexpr int OFF_BAR = OFF_HDR + NG * NS * 16;
+    static constexpr int OFF_ML = OFF_BAR + NG * NS * 16;              // full and empty barriers
+    static constexpr int OFF_PIECE = OFF_ML + kWarps * kRows * 8;
+    static constexpr int OFF_PRE = OFF_PIECE + NG * 2 * (int)sizeof(Piece);
+    static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 8; }
+};
+
+template <int D, int FMT, int BLK>
+__global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
+{
+    using C = Decode<D, FMT, BLK>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ i64 scan[kWarps];
+    __shared__ int s_flag;
+    i64* pre = reinterpret_cast<i64*>(sm + C::OFF_PRE);
+    Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
+    float2* mls = reinterpret_cast<float2*>(sm + C::OFF_ML);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int grp = warp / C::GW, sub = warp % C::GW;
+    int* status = a.c.status;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR) + grp * C::NS * 2;
+    uint64_t* empty = full + C::NS;
+    if (sub == 0 && lane < C::NS) {
+        tc::mbar_init(full + lane, 2);
+        tc::mbar_init(empty + lane, C::GW);
+    }
+    if (tid < 2 * C::NG)
+        pieces[tid].used = 0;
+
+    // prefix sums of the sequences' tiles: four sequences a thread
+    {
+        i64 v[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = 0;
+            const int b = 4 * tid + i;
+            if (b < a.c.n_seqs)
+                v[i] = tiles_of(a, b);
+            sum += v[i];
+        }
+        i64 incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const i64 x = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o)
+                incl += x;
+        }
+        if (lane == 31)
+            scan[warp] = incl;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        __syncthreads();
+        i64 at = incl - sum;
+        for (int w = 0; w < warp; ++w)
+            at += scan[w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = 4 * tid + i;
+            if (b <= a.c.n_seqs)
+                pre[b] = at;
+            at += v[i];
+        }
+        if (tid == kThreads - 1 && a.c.n_seqs == 4 * kThreads)
+            pre[a.c.n_seqs] = at;
+        __syncthreads();
+    }
+    const i64 N = pre[a.c.n_seqs];
+    const int G = (int)min((i64)gridDim.x, N);                // CTAs with work
+    if ((int)blockIdx.x >= G)
+        return;
+    const i64 TG = (i64)G * C::NG, gid = (i64)blockIdx.x * C::NG + grp;
+    const i64 t_begin = N * gid / TG, t_end = N * (gid + 1) / TG;
+    const i64 ct0 = N * blockIdx.x / G, ct1 = N * (blockIdx.x + 1) / G;
+
+    uint8_t* ring = sm + grp * C::NS * C::STAGE;
+    float* hdr = reinterpret_cast<float*>(sm + C::OFF_HDR) + grp * C::NS * 4;
+    const uint64_t pol = tc::l2_evict_first();
+    float* slots = ws + (i64)gridDim.x * 2 * slot_floats() + gid * 2 * slot_floats();   // this group's two
+
+    // the tile stream: warp 0 of the group keeps its own place in it, NS - 1 tiles ahead
+    Item pit{};
+    i64 pt = t_begin;
+    int pj = 0, pid = 0;
+    auto table_at = [&](const Item& it, int j) { return a.c.table[(i64)it.b * a.c.table_stride + j]; };
+    auto produce = [&]() {
+        const int st = (int)((pt - t_begin) % C::NS);
+        const i64 round = (pt - t_begin) / C::NS;
+        if (round > 0)
+            tc::mbar_wait(empty + st, (uint32_t)((round - 1) & 1), status);
+        const bool valid = pid >= 0 && pid < a.c.num_blocks;
+        if (lane == 0) {
+            float* hd = hdr + st * 4;
+            hd[2] = valid ? 1.0f : 0.0f;
+            if (valid) {
+                const i64 at = ((i64)pid * a.c.H + pit.h) * 2;
+                tc::mbar_expect_tx(full + st, C::STAGE);
+                tc::bulk_copy_hint(ring + st * C::STAGE, a.c.codes + at * (BLK * D), C::STAGE, full + st, pol);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::su32(hd)), "l"(a.c.scales + at) : "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::su32(full + st)) : "memory");
+            } else {
+                atomicExch(status, MOE_ERR_DEVICE_FAULT);
+                tc::mbar_arrive(full + st);
+                tc::mbar_arrive(full + st);
+            }
+        }
+        __syncwarp();
+        if (++pt < t_end) {
+            if (++pj > pit.jhi) {
+                next_item(a, pre, pit);
+                pj = pit.jlo;
+            }
+            pid = table_at(pit, pj);     // used by the next call, a tile later
+        }
+    };
+
+    if (t_begin < t_end) {
+        Item it;
+        find_item(a, pre, t_begin, it);
+        int j = it.jlo + (int)(t_begin - it.t0);
+        if (sub == 0) {
+            pit = it;
+            pj = j;
+            pid = table_at(it, j);
+            for (int i = 0; i < C::NS - 1 && pt < t_end; ++i)
+                produce();
+        }
+        const int r = lane >> 2, c = lane & 3;
+        i64 t = t_begin;
+        while (t < t_end) {
+            // ---- an item, or the part of it in this group's run
+            const i64 item_end = it.t0 + it.jhi - it.jlo + 1, seg_end = min(item_end, t_end);
+            const int rows = min(kRows, it.n * a.group - it.rt * kRows);
+            uint32_t qf[D / 16][4];
+            float f[2];                  // score = sum * block's scale * f
+            int plo[2], phi[2];          // first and last visible position of this thread's two rows
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = it.rt * kRows + r + 8 * e, i = row / a.group;
+                const bool in = r + 8 * e < rows;
+                phi[e] = in ? it.len - it.n + i : -1;
+                plo[e] = in && a.window > 0 ? phi[e] - a.window + 1 : 0;
+                uint32_t w[D / 64][8];
+                if (in) {
+                    const uint16_t* q = a.q + (i64)(it.c0 + i) * a.q_stride + (i64)(it.h * a.group + row % a.group) * D + 16 * c;
+#pragma unroll
+                    for (int ch = 0; ch < D / 64; ++ch) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(q + 64 * ch), y = *reinterpret_cast<const uint4*>(q + 64 * ch + 8);
+                        w[ch][0] = x.x, w[ch][1] = x.y, w[ch][2] = x.z, w[ch][3] = x.w;
+                        w[ch][4] = y.x, w[ch][5] = y.y, w[ch][6] = y.z, w[ch][7] = y.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[ch][k] = 0;
+                }
+                uint32_t big = 0;        // largest finite magnitude of the row
+#pragma unroll
+                for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t x = w[ch][k] & 0x7fffu, y = w[ch][k] >> 16 & 0x7fffu;
+                        big = max(big, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
+                    }
+                big = max(big, __shfl_xor_sync(~0u, big, 1));
+                big = max(big, __shfl_xor_sync(~0u, big, 2));
+                // scaled by 2^up the row's largest is in [2^13, 2^15): exact in f16 down to 2^-37 of it
+                const int up = 14 + 127 - max((int)(big >> 7), 1);
+                const float u0 = __uint_as_float((uint32_t)(127 + up / 2) << 23), u1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+                f[e] = ldexpf(fabsf(a.scale) * kLog2e, -up);
+                const float sg = a.scale < 0.0f ? -u0 : u0;
+#pragma unroll
+                for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float x = __uint_as_float(w[ch][k] << 16) * sg * u1, y = __uint_as_float(w[ch][k] & 0xffff0000u) * sg * u1;
+                        qf[ch * 4 + k / 2][(k & 1) * 2 + e] = pack_f16(x, y);
+                    }
+            }
+            float o[D / 8][4], m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[i][k] = 0.0f;
+            float ref = 0.0f, vmax = 0.0f;
+            // positions that every row of the tile sees
+            const int all_lo = a.window > 0 ? it.len - it.n + (it.rt * kRows + rows - 1) / a.group - a.window + 1 : 0;
+            const int all_hi = it.len - it.n + it.rt * kRows / a.group;
+
+            int st = 0;
+            for (; t < seg_end; ++t, ++j) {
+                st = (int)((t - t_begin) % C::NS);
+                tc::mbar_wait(full + st, (uint32_t)((t - t_begin) / C::NS & 1), status);
+                const float4 hd = *reinterpret_cast<const float4*>(hdr + st * 4);
+                const uint8_t* kt = ring + st * C::STAGE + sub * kSub * D;
+                const uint8_t* vt = ring + st * C::STAGE + BLK * D + sub * kSub;
+                const int p0 = j * BLK + sub * kSub;     // position of this warp's first token
+                if (hd.z != 0.0f) {
+                    float s[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s[i][k] = 0.0f;
+                    // token of column n of score tile i: 8 (n / 2) + 2 i + n % 2
+                    const uint8_t* kp = kt + (8 * (r >> 1) + (r & 1)) * D + 16 * c;
+#pragma unroll
+                    for (int ch = 0; ch < D / 64; ++ch) {
+                        uint4 kw[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            kw[i] = *reinterpret_cast<const uint4*>(kp + 2 * i * D + 64 * ch);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w = k == 0 ? kw[i].x : k == 1 ? kw[i].y : k == 2 ? kw[i].z : kw[i].w;
+                                uint32_t b0, b1;
+                                to_f16<FMT>(w, b0, b1);
+                                mma16816(s[i], qf[ch * 4 + k], b0, b1);
+                            }
+                    }
+                    const float cs[2] = {hd.x * f[0], hd.x * f[1]};
+                    const bool whole = p0 >= all_lo && p0 + kSub - 1 <= all_hi;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s[i][k] *= cs[k >> 1];
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int p = p0 + 8 * c + 2 * i + (k & 1), e = k >> 1;
+                                if (p < plo[e] || p > phi[e])
+                                    s[i][k] = -INFINITY;
+                            }
+                    }
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k >> 1] = fmaxf(mx[k >> 1], s[i][k]);
+                    const float vs = hd.y;
+                    const bool unit = !(vs <= 2.0f * ref && vs >= 0.5f * ref);
+                    if (__any_sync(~0u, unit || mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+                        // a new maximum, or a new unit of O
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
+                            const float mn = fmaxf(m[e], mx[e]);
+                            al[e] = ex2(m[e] - mn);
+                            m[e] = mn;
+                            l[e] *= al[e];
+                        }
+                        if (unit) {
+                            vmax = fmaxf(vmax, vs);
+                            const float now = fmaxf(fmaxf(vs, vmax * 9.094947017729282e-13f), 7.52316384526264e-37f);   // 2^-40, 2^-120
+                            const float ch = ref / now;
+                            ref = now;
+                            al[0] *= ch;
+                            al[1] *= ch;
+                        }
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            o[i][0] *= al[0];
+                            o[i][1] *= al[0];
+                            o[i][2] *= al[1];
+                            o[i][3] *= al[1];
+                        }
+                    }
+                    const float ratio = fmaxf(vs / ref, 8.673617379884035e-19f);   // 2^-60
+                    const float lr = __log2f(ratio), back = 1.0f / ratio;
+                    const float mm[2] = {m[0] - lr, m[1] - lr};
+                    float sum[2] = {0.0f, 0.0f};
+                    uint32_t pf[2][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float p[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            p[k] = ex2(s[i][k] - mm[k >> 1]);
+                            sum[k >> 1] += p[k];
+                        }
+                        pf[i >> 1][(i & 1) * 2] = pack_f16(p[0], p[1]);
+                        pf[i >> 1][(i & 1) * 2 + 1] = pack_f16(p[2], p[3]);
+                    }
+                    l[0] += sum[0] * back;
+                    l[1] += sum[1] * back;
+                    const uint8_t* vp = vt + r * BLK + 8 * c;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vp + 8 * i * BLK);
+                        uint32_t b0, b1;
+                        to_f16<FMT>(w.x, b0, b1);
+                        mma16816(o[i], pf[0], b0, b1);
+                        to_f16<FMT>(w.y, b0, b1);
+                        mma16816(o[i], pf[1], b0, b1);
+                    }
+                }
+                if (t + 1 < seg_end) {
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(empty + st);
+                    if (sub == 0 && pt < t_end)
+                        produce();
+                }
+            }
+
+            // ---- join the group's warps in the stage they have just read
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(~0u, l[e], 1);
+                l[e] += __shfl_xor_sync(~0u, l[e], 2);
+                if (c == 0)
+                    mls[warp * kRows + r + 8 * e] = make_float2(m[e], l[e]);
+            }
+            group_sync(1 + grp, C::GW * 32);
+            float* od = reinterpret_cast<float*>(ring + st * C::STAGE);
+            // column group i of row x lies at i ^ (x % 8)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * D + (i ^ r) * 8 + 2 * c) =
+                        make_float2(o[i][2 * e] * ref, o[i][2 * e + 1] * ref);
+            group_sync(1 + grp, C::GW * 32);
+            const bool done = it.t0 >= t_begin && item_end <= t_end;
+            const int which = it.t0 < t_begin || t_begin == it.t0 ? 0 : 1;   // the group's first item, or its last
+            const Place place{it.c0, it.rt * kRows, it.h, rows};
+            float* slot = slots + which * slot_floats();
+            for (int x = sub * 32 + lane; x < rows * (D / 4); x += C::GW * 32) {
+                const int row = x / (D / 4), col = x % (D / 4) * 4;
+                float M = kNone, L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < C::GW; ++w)
+                    M = fmaxf(M, mls[(grp * C::GW + w) * kRows + row].x);
+                float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int w = 0; w < C::GW; ++w) {
+                    const float2 ml = mls[(grp * C::GW + w) * kRows + row];
+                    const float wt = ex2(ml.x - M);
+                    L += ml.y * wt;
+                    const float4 y = *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7));
+                    v.x += y.x * wt, v.y += y.y * wt, v.z += y.z * wt, v.w += y.w * wt;
+                }
+                if (done) {
+                    store_row4(a, place, row, col, v, finish(M, L, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
+                } else {
+                    __stcg(reinterpret_cast<float4*>(slot + row * D + col), v);
+                    if (col == 0)
+                        __stcg(reinterpret_cast<float2*>(slot + kRows * D + 2 * row), make_float2(M, L));
+                }
+            }
+            if (!done && sub == 0 && lane == 0) {
+                Piece& p = pieces[grp * 2 + which];
+                p.t0 = it.t0;
+                p.t1 = item_end;
+                p.p = place;
+                p.used = 1;
+            }
+            tc::fence_proxy_async_smem();
+            group_sync(1 + grp, C::GW * 32);
             if (lane == 0)
-                atomicExch(c.status, MOE_ERR_DEVICE_FAULT);
-            continue;
-        }
-        if (tok >= x0 && tok < x0 + xn) {
-            b = i;
-            c0 = x0;
-            n = xn;
-            len = xl;
-        }
-    }
-    if (b < 0)
-        return;
-    const int pos = len - n + (tok - c0);
-    const int j0 = a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
-    float q[4], o[4] = {0, 0, 0, 0};
-    for (int e = 0; e < per; ++e)
-        q[e] = tc::bf16f(a.q[(long long)tok * a.q_stride + (long long)hq * D + lane * per + e]);
-    float m = a.sinks ? a.sinks[hq] : -INFINITY, l = a.sinks ? 1.0f : 0.0f;
-    for (int j = j0; j <= pos; ++j) {
-        const int id = kv::physical(c, b, j / c.blk);
-        if (id < 0)
-            continue;
-        const long long at = ((long long)id * c.H + h) * 2;
-        const uint8_t* kc = c.codes + at * c.blk * D;
-        const uint8_t* vc = kc + (long long)c.blk * D;
-        const int r = j % c.blk;
-        float s = 0.0f, d4[4];
-        for (int e = 0; e < per; ++e) {
-            kv::decode4(kc[r * D + lane * per + e], c.fmt, d4);
-            s += q[e] * d4[0];
-        }
-        for (int x = 16; x; x >>= 1)
-            s += __shfl_xor_sync(~0u, s, x);
-        s *= c.scales[at] * a.scale;
-        const float mn = fmaxf(m, s), al = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-        l = l * al + p;
-        m = mn;
-        const float vs = c.scales[at + 1] * p;
-        for (int e = 0; e < per; ++e) {
-            kv::decode4(vc[(lane * per + e) * c.blk + r], c.fmt, d4);
-            o[e] = o[e] * al + vs * d4[0];
+                tc::mbar_arrive(empty + st);
+            if (sub == 0 && pt < t_end)
+                produce();
+            if (t < t_end) {
+                next_item(a, pre, it);
+                j = it.jlo;
+            }
         }
     }
-    for (int e = 0; e < per; ++e)
-        a.out[((long long)tok * a.q_heads + hq) * D + lane * per + e] = tc::f2bf16_rne(l > 0.0f ? o[e] / l : 0.0f);
-    if (a.lse && lane == 0)
-        a.lse[(long long)tok * a.q_heads + hq] = l > 0.0f ? m + logf(l) : -INFINITY;
+
+    // ---- join the groups' pieces, in the order of their tiles
+    __threadfence_block();
+    __syncthreads();
+    const float* gslots = ws + (i64)gridDim.x * 2 * slot_floats() + (i64)blockIdx.x * C::NG * 2 * slot_floats();
+    float* cslots = ws + (i64)blockIdx.x * 2 * slot_floats();
+    int across[2] = {0, 0};
+    Piece cross[2];
+    for (int first = 0; first < 2 * C::NG;) {
+        if (!pieces[first].used) {
+            ++first;
+            continue;
+        }
+        const Piece p = pieces[first];
+        int last = first + 1;
+        while (last < 2 * C::NG && (!pieces[last].used || pieces[last].t0 == p.t0))
+            ++last;
+        const bool done = p.t0 >= ct0 && p.t1 <= ct1;
+        const int which = p.t0 < ct0 ? 0 : 1;
+        for (int x = tid; x < p.p.nrows * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), col = x % (D / 4) * 4;
+            float M = kNone, L = 0.0f;
+            float4 v = make_float4(0, 0, 0, 0);
+            for (int k = first; k < last; ++k) {
+                if (!pieces[k].used)
+                    continue;
+                const float* s = gslots + k * slot_floats();
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
+                const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
+                M = mn;
+                L = L * w0 + ml.y * w1;
+                v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
+            }
+            if (done) {
+                store_row4(a, p.p, row, col, v, finish(M, L, a.sinks, p.p.h * a.group + (p.p.r0 + row) % a.group));
+            } else {
+                float* s = cslots + which * slot_floats();
+                __stcg(reinterpret_cast<float4*>(s + row * D + col), v);
+                if (col == 0)
+                    __stcg(reinterpret_cast<float2*>(s + kRows * D + 2 * row), make_float2(M, L));
+            }
+        }
+        if (!done) {
+            across[which] = 1;
+            cross[which] = p;
+        }
+        first = last;
+    }
+
+    // ---- items that span CTAs: the last one to arrive joins them all
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (!across[which])
+            continue;
+        const Piece p = cross[which];
+        const int ca = (int)(((p.t0 + 1) * G - 1) / N), cb = (int)((p.t1 * G - 1) / N);   // CTAs of its first and last tile
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            const unsigned old = atomicAdd(cnt + ca, 1u);
+            s_flag = old == (unsigned)(cb - ca);
+            if (s_flag)
+                cnt[ca] = 0;
+        }
+        __syncthreads();
+        const int lastone = s_flag;
+        __syncthreads();
+        if (!lastone)
+            continue;
+        __threadfence();
+        for (int x = tid; x < p.p.nrows * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), col = x % (D / 4) * 4;
+            float M = kNone, L = 0.0f;
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int k = ca; k <= cb; ++k) {
+                const float* s = ws + ((i64)k * 2 + (k == ca)) * slot_floats();
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
+                const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
+                M = mn;
+                L = L * w0 + ml.y * w1;
+                v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
+            }
+            store_row4(a, p.p, row, col, v, finish(M, L, a.sinks, p.p.h * a.group + (p.p.r0 + row) % a.group));
+        }
+    }
+}
+
+template <int D, int FMT, int BLK>
+cudaError_t prepare_one()
+{
+    return cudaFuncSetAttribute(decode_attn_kernel<D, FMT, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Decode<D, FMT, BLK>::smem(kMaxSeqs));
+}
+
+template <int D, int FMT>
+cudaError_t prepare_blocks()
+{
+    cudaError_t e;
+    if ((e = prepare_one<D, FMT, 32>()) != cudaSuccess || (e = prepare_one<D, FMT, 64>()) != cudaSuccess)
+        return e;
+    return prepare_one<D, FMT, 128>();
+}
+
+template <int D, int FMT, int BLK>
+void launch_one(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    unsigned* cnt = reinterpret_cast<unsigned*>(a.ws);
+    decode_attn_kernel<D, FMT, BLK><<<num_sms, kThreads, Decode<D, FMT, BLK>::smem(a.c.n_seqs), s>>>(
+        a, reinterpret_cast<float*>(a.ws + 4096), cnt);
+}
+
+template <int D, int FMT>
+void launch_blocks(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    if (a.c.blk == 32)
+        launch_one<D, FMT, 32>(a, num_sms, s);
+    else if (a.c.blk == 64)
+        launch_one<D, FMT, 64>(a, num_sms, s);
+    else
+        launch_one<D, FMT, 128>(a, num_sms, s);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int) { return 256; }
-cudaError_t prepare_attention_kernels() { return cudaSuccess; }
-
-cudaError_t launch_attention(const AttnArgs& a, int, cudaStream_t s)
+size_t attention_workspace_bytes(int num_sms)
 {
-    attention_simple_kernel<<<dim3(a.c.n_tokens, (a.q_heads + 3) / 4), 128, 0, s>>>(a);
+    return 4096 + (size_t)num_sms * 2 * (1 + kMaxGroups) * slot_floats() * sizeof(float);
+}
+
+cudaError_t prepare_attention_kernels()
+{
+    cudaError_t e;
+    if ((e = prepare_blocks<64, MOE_KV_E4M3>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_INT8>()) != cudaSuccess ||
+        (e = prepare_blocks<128, MOE_KV_E4M3>()) != cudaSuccess)
+        return e;
+    return prepare_blocks<128, MOE_KV_INT8>();
+}
+
+cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    if (a.c.D == 64)
+        a.c.fmt == MOE_KV_E4M3 ? launch_blocks<64, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<64, MOE_KV_INT8>(a, num_sms, s);
+    else
+        a.c.fmt == MOE_KV_E4M3 ? launch_blocks<128, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<128, MOE_KV_INT8>(a, num_sms, s);
     return cudaGetLastError();
 }
 
