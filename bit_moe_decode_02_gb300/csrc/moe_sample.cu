@@ -8,17 +8,19 @@
 //
 // One cluster of CTAs per row, each with a contiguous part of the vocabulary.
 //  1. The largest logit (one read from HBM; later passes find the row in L1 / L2).
-//  2. With top-k or top-p: a histogram, in 1/32 steps of z, of counts and weights;
-//     its prefix sums name the bin in which the kept set ends.  z is a monotone
-//     function of the logit, so bins are runs of the order.  Tokens of weight 0
-//     cannot be drawn and are left out.
-//  3. If the bins up to that one hold at most 1,024 tokens (top-k up to some
-//     hundreds, peaked rows), they are gathered and sorted in one CTA, which ends
-//     the row.  Else the bin is narrowed by histograms of its keys until the last
-//     member's key (the logit's order-preserving bits) is known, and how many of
-//     the tokens that share it are in.
-//  4. Sums of kept weights per CTA and warp, in the vocabulary's order; the warp in
-//     whose part the target lies walks it.
+//  2. With top-k or top-p: how many tokens there are in each 1/256 of z.  z is a
+//     monotone function of the logit, so bins are runs of the order: top-k ends in a
+//     bin that the counts name, top-p in one that the counts times the bins' middle
+//     weights name but for a relative 1e-4.
+//  3. One pass adds up the weights before and between those bins (per warp, in the
+//     vocabulary's order) and gathers the bins' own tokens, which one CTA sorts: the
+//     last member of the kept set is found exactly.  Where all tokens that may be
+//     kept are in the list (top-k of some hundreds, peaked rows), that CTA draws.
+//  4. Else the warp in whose part the target lies walks it.
+// Rows whose bins hold more than 1,024 tokens (thousands of equal logits, high
+// temperatures) find the last member by histograms of counts and weights that
+// narrow a bin down to one key (the logit's order-preserving bits), and how many of
+// the tokens that share the key are in; those take a few more passes.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -36,6 +38,8 @@ constexpr int kMostCluster = 16;
 constexpr int kMostPart = 65536;           // tokens of a CTA: a bin's sum of 16-bit halves fits 32 bits
 constexpr int kSlackPart = 32 * 32 * 8;    // a CTA's part may be this much above an equal share
 constexpr int kBins = 768;                 // of 1/32 of z: weights are 0 from z = -22.2 on
+constexpr int kFine = 5760;               // of 1/256 of z
+constexpr int kFinePer = (kFine + kThreads - 1) / kThreads;
 constexpr int kList = kThreads;
 typedef unsigned long long u64;
 
@@ -54,26 +58,32 @@ __device__ __forceinline__ float key_value(uint32_t k)
 
 struct Row {
     float top, inv_t;
-    __device__ __forceinline__ float z(float l) const
-    {
-        return l == top ? 0.0f : !(l > -INFINITY) || top == INFINITY ? -INFINITY : __fmul_rn(__fsub_rn(l, top), inv_t);
-    }
+    // -inf and NaN logits: -inf or NaN, of weight 0 and in no bin
+    __device__ __forceinline__ float z(float l) const { return l == top ? 0.0f : __fmul_rn(__fsub_rn(l, top), inv_t); }
     __device__ __forceinline__ static uint32_t weight(float z) { return __float2uint_rn(expf(z) * 2147483648.0f); }
+    __device__ __forceinline__ static int fine(float z) { return z > -(float)kFine / 256.0f ? (int)(z * -256.0f) : kFine; }
+    __device__ __forceinline__ static float fine_middle(int b) { return ((float)b + 0.5f) * (-1.0f / 256.0f); }
     __device__ __forceinline__ static int bin(float z) { return z > -(float)kBins / 32.0f ? (int)(z * -32.0f) : kBins - 1; }
 };
 
 struct Shared {
     u64 best[kMostCluster];                // largest (key, lowest index) of each CTA
-    u64 red[kWarps];
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];       // this CTA's histogram: counts, halves of weights
-    uint32_t tcnt[kBins];                  // the row's, inclusive prefix sums
-    u64 tw[kBins];
-    u64 list[kList];
-    u64 part_sum[kMostCluster], warp_sum[kWarps];
-    uint32_t part_ties[kMostCluster], warp_ties[kWarps];
+    u64 red[kWarps], red2[kWarps];
+    union {
+        uint32_t fine[kFinePer * kThreads];          // this CTA's counts; then the row's, as prefix sums
+        struct {
+            uint32_t cnt[kBins], lo[kBins], hi[kBins];   // this CTA's histogram: counts, halves of weights
+            uint32_t tcnt[kBins];          // the row's, inclusive prefix sums
+            u64 tw[kBins];
+        };
+    };
+    uint32_t share[(kFine + 1) / 2];       // the row's counts in this CTA's share of the bins (two CTAs or more)
+    u64 list[kList];                       // the first CTA's: gathered tokens, as key and complement of the index
+    u64 warp_sum[kWarps], part_sum[kMostCluster], part_raw[kMostCluster], part_mid[kMostCluster];
+    uint32_t warp_ties[kWarps], part_ties[kMostCluster];
     uint32_t nlist;
-    int found;
-    uint32_t found_key;
+    int found, kbin, pbin[2];
+    u64 about, last;
 };
 
 template <class T>
@@ -136,63 +146,82 @@ struct Part {
     const uint8_t* base;      // 16-byte aligned
     int lead, V, v0, v1;
 
-    // f(value, index) for each element of vector v (index -1: no element)
-    template <class F>
-    __device__ __forceinline__ void visit(int v, F f) const
+    __device__ __forceinline__ uint4 load(int v) const
     {
         const int i0 = v * VEC - lead;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (v < v1) {
-            if (i0 >= 0 && i0 + VEC <= V) {
-                q = *reinterpret_cast<const uint4*>(base + (long long)v * 16);
-            } else {
-                // the row's ends: only its own elements are read
-                uint32_t w[4] = {0, 0, 0, 0};
+        if (v >= v1)
+            return make_uint4(0, 0, 0, 0);
+        if (i0 >= 0 && i0 + VEC <= V)
+            return __ldg(reinterpret_cast<const uint4*>(base + (long long)v * 16));
+        // the row's ends: only its own elements are read
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (i0 + e >= 0 && i0 + e < V) {
-                        if (BF16)
-                            w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(base + (long long)v * 16)[e] << 16 * (e & 1);
-                        else
-                            w[e] = reinterpret_cast<const uint32_t*>(base + (long long)v * 16)[e];
-                    }
-                q = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < VEC; ++e)
+            if (i0 + e >= 0 && i0 + e < V) {
+                if (BF16)
+                    w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(base + (long long)v * 16)[e] << 16 * (e & 1);
+                else
+                    w[e] = reinterpret_cast<const uint32_t*>(base + (long long)v * 16)[e];
             }
-        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // f(value, index) for each element of vector v (index -1: no element)
+    template <class F>
+    __device__ __forceinline__ void take(int v, uint4 q, F f) const
+    {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float x = BF16 ? __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]);
-            const int i = i0 + e;
+            const int i = v * VEC - lead + e;
             f(x, v < v1 && i >= 0 && i < V ? i : -1);
         }
     }
     template <class F>
+    __device__ __forceinline__ void visit(int v, F f) const { take(v, load(v), f); }
+    // all of the warp's elements, with the next loads out before the last are used
+    template <class F>
     __device__ __forceinline__ void each(F f) const
     {
-        const int lane = threadIdx.x & 31;
-#pragma unroll 4
-        for (int v = v0 + lane; v < v1; v += 32)
-            visit(v, f);
+        constexpr int U = BF16 ? 2 : 4;
+        for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32 * U) {
+            uint4 q[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                q[k] = load(v + 32 * k);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                take(v + 32 * k, q[k], f);
+        }
     }
 };
+
+__device__ __forceinline__ u64 warp_sum(u64 v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
+    cl.barrier_arrive();                     // waited for before the first access to another CTA's memory
     const int c = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / c, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    cl.barrier_arrive();                     // waited for before the first access to another CTA's memory
     Part<BF16> part;
+    int per;                                 // vectors of a warp
     {
         const uint8_t* p = static_cast<const uint8_t*>(a.logits) + (long long)row * a.stride * (BF16 ? 2 : 4);
         part.lead = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (BF16 ? 2 : 4);
         part.base = p - part.lead * (BF16 ? 2 : 4);
         part.V = a.V;
-        const int nv = (a.V + part.lead + part.VEC - 1) / part.VEC, per = ((nv + c * kWarps - 1) / (c * kWarps) + 31) / 32 * 32;
+        const int nv = (a.V + part.lead + part.VEC - 1) / part.VEC;
+        per = ((nv + c * kWarps - 1) / (c * kWarps) + 31) / 32 * 32;
         part.v0 = min((rank * kWarps + warp) * per, nv);
         part.v1 = min(part.v0 + per, nv);
     }
@@ -212,10 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     }
     if (lane == 0)
         sh.red[warp] = best;
-    for (int i = tid; i < kBins; i += kThreads)
-        sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
-    if (tid == 0)
+    for (int i = tid; i < kFinePer * kThreads; i += kThreads)
+        sh.fine[i] = 0;
+    if (tid == 0) {
         sh.nlist = 0;
+        sh.kbin = sh.pbin[0] = sh.pbin[1] = kFine;
+        sh.last = 0;
+    }
     __syncthreads();
     if (warp == 0) {
         best = sh.red[lane];
@@ -245,14 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         return;
     }
     r.inv_t = __fdiv_rn(1.0f, fmaxf(T, 1e-30f));
-    int k = a.p.top_k ? a.p.top_k[row] : 0;
+    const int k = a.p.top_k ? a.p.top_k[row] : 0;
     const float tp = a.p.top_p ? a.p.top_p[row] : 1.0f, mp = a.p.min_p ? a.p.min_p[row] : 0.0f, uu = a.p.u[row];
     const bool by_p = tp < 1.0f;
-    const double least = (double)fminf(fmaxf(mp, 0.0f), 1.0f) * 2147483648.0;
-    const double u = uu > 0.0f ? fmin((double)uu, 1.0 - 5.9604644775390625e-08) : 0.0;
+    // integers take the place of fp64 products: w >= x as w >= ceil(x), and below cum > x as cum > floor(x)
+    const uint32_t least = (uint32_t)ceil((double)fminf(fmaxf(mp, 0.0f), 1.0f) * 2147483648.0);
     auto need_of = [&](u64 total) {
         const double need = ceil((double)tp * (double)total);
         return need >= 1.0 ? (u64)need : 1ull;
+    };
+    auto target_of = [&](u64 total) {
+        return (u64)((uu > 0.0f ? fmin((double)uu, 1.0 - 5.9604644775390625e-08) : 0.0) * (double)total);
     };
     auto answer = [&](int i, float l, u64 total) {
         a.token[row] = i;
@@ -260,298 +295,417 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             a.logprob[row] = r.z(l) - logf((float)total * 4.656612873077393e-10f);
     };
 
-    uint32_t key = 0;                        // the kept set: larger keys, and the first `ties` tokens with this one
-    uint32_t ties = 0xffffffffu;
+    // the kept set: all tokens if `all`; else, as key and complement of the index,
+    // those from `last` on; else (last == 0) larger keys than `key` and the first
+    // `ties` tokens that have it
+    bool all = true;
+    u64 last = 0;
+    uint32_t key = 0, ties = 0;
     if ((k > 0 && k < a.V) || by_p) {
-        // the row's histogram from the CTAs', as prefix sums
-        auto join = [&](int bins) {
-            cl.sync();
-            u64 w = 0, n = 0;
-            if (tid < bins) {
-                uint32_t lo[kMostCluster], hi[kMostCluster], cn[kMostCluster];
-#pragma unroll
-                for (int i = 0; i < kMostCluster; ++i) {
-                    lo[i] = hi[i] = cn[i] = 0;
-                    if (i < c) {
-                        const Shared* s = cl.map_shared_rank(&sh, i);
-                        lo[i] = s->lo[tid];
-                        hi[i] = s->hi[tid];
-                        cn[i] = s->cnt[tid];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kMostCluster; ++i) {
-                    w += (u64)lo[i] + ((u64)hi[i] << 16);
-                    n += cn[i];
-                }
-            }
-            w = block_scan(w, sh.red);
-            n = block_scan(n, sh.red);
-            if (tid < bins) {
-                sh.tw[tid] = w;
-                sh.tcnt[tid] = (uint32_t)n;
-            }
-            __syncthreads();
-        };
-        auto add = [&](int b, uint32_t w) {
-            atomicAdd(&sh.cnt[b], 1u);
-            atomicAdd(&sh.lo[b], w & 0xffffu);
-            atomicAdd(&sh.hi[b], w >> 16);
-        };
-        // first of `bins` prefix sums that reaches `need`
-        auto first_of = [&](bool weights, u64 need, int bins) {
-            if (tid < bins) {
-                const u64 x = weights ? sh.tw[tid] : sh.tcnt[tid], before = tid ? (weights ? sh.tw[tid - 1] : sh.tcnt[tid - 1]) : 0;
-                if (x >= need && before < need)
-                    sh.found = tid;
-            }
-            __syncthreads();
-            const int b = sh.found;
-            __syncthreads();
-            return b;
-        };
-
-        // ---- 2. histogram of z
+        // ---- 2. counts in 1/256 of z
         part.each([&](float l, int i) {
-            if (i < 0)
-                return;
-            const float z = r.z(l != l ? -INFINITY : l);
-            const uint32_t w = Row::weight(z);
-            if (w)
-                add(Row::bin(z), w);
+            const int b = Row::fine(r.z(l));
+            if (i >= 0 && b < kFine)
+                atomicAdd(&sh.fine[b], 1u);
         });
-        join(kBins);
-        const uint32_t all = sh.tcnt[kBins - 1];
-        const bool by_k = k > 0 && (uint32_t)k < all;
-        int bin = kBins - 1;
-        if (by_k)
-            bin = first_of(false, k, kBins);
-        else if (by_p)
-            bin = first_of(true, need_of(sh.tw[kBins - 1]), kBins);
-        const uint32_t n = sh.tcnt[bin];
-        if (n <= kList) {
-            // ---- 3a. few tokens: one CTA sorts them
+        const int share = (kFine + c - 1) / c;
+        if (c > 1) {
+            // every CTA adds up its share of the bins, then takes all shares
+            cl.sync();
+            for (int b = tid; b < share && rank * share + b < kFine; b += kThreads) {
+                uint32_t n = 0;
+                for (int i = 0; i < c; ++i)
+                    n += cl.map_shared_rank(&sh, i)->fine[rank * share + b];
+                sh.share[b] = n;
+            }
+            cl.sync();
+        } else {
+            __syncthreads();
+        }
+        uint32_t n[kFinePer], nsum = 0;
+        u64 w[kFinePer], wsum = 0;
+#pragma unroll
+        for (int j = 0; j < kFinePer; ++j) {
+            const int b = tid * kFinePer + j;
+            n[j] = b >= kFine ? 0 : c > 1 ? cl.map_shared_rank(&sh, b / share)->share[b % share] : sh.fine[b];
+            w[j] = n[j] * (u64)Row::weight(Row::fine_middle(b));
+            nsum += n[j];
+            wsum += w[j];
+        }
+        const u64 nb = block_scan((u64)nsum, sh.red) - nsum, wb = block_scan(wsum, sh.red2) - wsum;
+        const bool by_k = k > 0 && (u64)k < sh.red[kWarps - 1];
+        u64 about = sh.red2[kWarps - 1];     // weight of what top-k leaves, but for the bins' width
+        if (by_k) {
+            u64 x = nb, y = wb;
+#pragma unroll
+            for (int j = 0; j < kFinePer; ++j) {
+                if (x < (u64)k && x + n[j] >= (u64)k) {
+                    sh.kbin = tid * kFinePer + j;
+                    sh.about = y + ((u64)k - x) * Row::weight(Row::fine_middle(tid * kFinePer + j));
+                }
+                x += n[j];
+                y += w[j];
+            }
+            __syncthreads();
+            about = sh.about;
+        }
+        if (by_p) {
+            const double share_p = (double)fmaxf(tp, 0.0f) * (double)about;
+            const u64 t0 = max((u64)(share_p * 0.9999), 1ull), t1 = max((u64)(share_p * 1.0001), 1ull);
+            u64 y = wb;
+#pragma unroll
+            for (int j = 0; j < kFinePer; ++j) {
+                if (y < t0 && y + w[j] >= t0)
+                    sh.pbin[0] = tid * kFinePer + j;
+                if (y < t1 && y + w[j] >= t1)
+                    sh.pbin[1] = tid * kFinePer + j;
+                y += w[j];
+            }
+        }
+        {
+            uint32_t x = (uint32_t)nb;
+#pragma unroll
+            for (int j = 0; j < kFinePer; ++j) {
+                x += n[j];
+                sh.fine[tid * kFinePer + j] = x;   // no other CTA reads them any more
+            }
+        }
+        __syncthreads();
+        auto through = [&](int b) -> uint32_t { return b < 0 ? 0u : sh.fine[min(b, kFine - 1)]; };
+        const int kb = sh.kbin;
+        // the bands to gather: bins p0 .. p1, and kb if it is apart from them
+        int p0 = by_p ? min(sh.pbin[0], kb) : kb;
+        const int p1 = by_p ? min(sh.pbin[1], kb) : kb;
+        const bool apart = by_k && p1 < kb;
+        const uint32_t n_k = apart ? through(kb) - through(kb - 1) : 0;
+        const bool alone = through(p1) + n_k <= kList;       // the list takes all that may be kept
+        if (alone)
+            p0 = 0;
+        const uint32_t before = through(p0 - 1), n_p = through(p1) - before, n_list = n_p + n_k, before_k = through(kb - 1);
+        all = !by_k && !by_p;                                // fewer tokens than k have weight
+        if (!all && n_list <= kList) {
+            // ---- 3. weights before and between the bands; their tokens into the first CTA's list
+            const bool sums = !alone || (by_p && (!by_k || apart));
+            u64 kept = 0, raw = 0, mid = 0;
             part.each([&](float l, int i) {
-                if (i < 0)
-                    return;
-                const float z = r.z(l != l ? -INFINITY : l);
-                if (Row::bin(z) <= bin && Row::weight(z)) {
+                const float z = r.z(l);
+                const int b = i < 0 ? kFine : Row::fine(z);
+                if (b < p0 || (b > p1 && b < kb)) {
+                    if (sums) {
+                        const uint32_t x = Row::weight(z);
+                        if (b > p1) {
+                            mid += x;
+                        } else {
+                            raw += x;
+                            kept += x >= least ? x : 0;
+                        }
+                    }
+                } else if (b < kFine && (b <= p1 || (apart && b == kb))) {
                     const uint32_t at = atomicAdd(cl.map_shared_rank(&sh.nlist, 0), 1u);
                     *cl.map_shared_rank(&sh.list[at], 0) = (u64)order_key(l) << 32 | (0xffffffffu - (uint32_t)i);
                 }
             });
+            if (sums) {
+                kept = warp_sum(kept);
+                raw = warp_sum(raw);
+                mid = warp_sum(mid);
+                if (lane == 0) {
+                    sh.warp_sum[warp] = kept;
+                    sh.red[warp] = raw;
+                    sh.red2[warp] = mid;
+                }
+                __syncthreads();
+                if (warp == 0) {
+                    raw = warp_sum(sh.red[lane]);
+                    mid = warp_sum(sh.red2[lane]);
+                    if (lane == 0) {
+                        *cl.map_shared_rank(&sh.part_raw[rank], 0) = raw;
+                        *cl.map_shared_rank(&sh.part_mid[rank], 0) = mid;
+                    }
+                }
+            }
             cl.sync();
-            if (rank)
+            bool found = true;
+            if (rank == 0) {
+                raw = mid = 0;
+                if (sums)
+                    for (int i = 0; i < c; ++i) {
+                        raw += sh.part_raw[i];
+                        mid += sh.part_mid[i];
+                    }
+                int n2 = 32;
+                while (n2 < (int)n_list)
+                    n2 <<= 1;
+                u64 e = tid < (int)n_list ? sh.list[tid] : 0;
+                __syncthreads();
+                e = block_sort(e, n2, true, sh.list);
+                // this thread's place in the order, and its weight if top-k takes it
+                const uint32_t at = tid < (int)n_p ? before + tid : before_k + (tid - n_p);
+                u64 x = tid < (int)n_list && (!by_k || at < (uint32_t)k) ? Row::weight(r.z(key_value((uint32_t)(e >> 32)))) : 0;
+                const u64 own = x, cum = block_scan(tid < (int)n_p ? x : 0, sh.red);
+                const u64 in_band = sh.red[kWarps - 1];
+                bool in = x != 0;
+                if (by_p) {
+                    block_scan(tid < (int)n_p ? 0 : x, sh.red2);
+                    const u64 need = need_of(raw + in_band + mid + sh.red2[kWarps - 1]);
+                    in = in && tid < (int)n_p && raw + cum - own < need;
+                    found = raw < need && raw + in_band >= need;     // the share is reached within the band
+                }
+                __syncthreads();
+                sh.list[tid] = e;
+                if (in)
+                    atomicMax(&sh.last, ~e);                          // the last one has the largest complement
+                __syncthreads();
+                if (alone && found) {
+                    if (!in || x < least)
+                        x = 0;
+                    // by index, the kept ones first
+                    u64 by_index = x ? (u64)(0xffffffffu - (uint32_t)e) << 32 | x : ~0ull << 32;
+                    by_index = block_sort(by_index, n2, false, sh.list);
+                    x = tid < n2 ? by_index & 0xffffffffu : 0;
+                    const u64 run = block_scan(x, sh.red);
+                    const u64 total = sh.red[kWarps - 1], target = target_of(total);
+                    if (x && run > target && run - x <= target) {
+                        const int i = (int)(by_index >> 32);
+                        answer(i, BF16 ? tc::bf16f(static_cast<const uint16_t*>(a.logits)[row * a.stride + i])
+                                       : static_cast<const float*>(a.logits)[row * a.stride + i], total);
+                    }
+                }
+                last = ~sh.last;
+                __syncthreads();
+                if (tid < c)
+                    *cl.map_shared_rank(&sh.last, tid) = found ? last : 0;
+            }
+            cl.sync();
+            last = sh.last;
+            if (alone && last)
                 return;
-            int n2 = 32;
-            while (n2 < (int)n)
-                n2 <<= 1;
-            u64 e = tid < (int)n ? sh.list[tid] : 0;
-            __syncthreads();
-            e = block_sort(e, n2, true, sh.list);
-            u64 w = tid < (int)n && (!by_k || tid < k) ? Row::weight(r.z(key_value((uint32_t)(e >> 32)))) : 0;
-            u64 cum = block_scan(w, sh.red);
-            if (by_p) {
-                // of all tokens that top-k leaves: with it, they are in the list
-                const u64 total = by_k ? sh.red[kWarps - 1] : sh.tw[kBins - 1];
-                if (cum - w >= need_of(total))
-                    w = 0;
+            if (last) {
+                // the list's kept tokens join their warps' sums
+                const Shared* s0 = cl.map_shared_rank(&sh, 0);
+                if (tid < (int)n_list) {
+                    const u64 e = s0->list[tid];
+                    const uint32_t x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
+                    const int g = ((int)(0xffffffffu - (uint32_t)e) + part.lead) / part.VEC / per;
+                    if (e >= last && x >= least && g / kWarps == rank)
+                        atomicAdd(&sh.warp_sum[g % kWarps], (u64)x);
+                }
+                if (tid < kWarps)
+                    sh.warp_ties[tid] = 0;
             }
-            if ((double)w < least)
-                w = 0;
-            // by index: the kept ones first
-            u64 by_index = w ? (u64)(0xffffffffu - (uint32_t)e) << 32 | w : ~0ull << 32;
-            __syncthreads();
-            by_index = block_sort(by_index, n2, false, sh.list);
-            w = tid < n2 ? by_index & 0xffffffffu : 0;
-            cum = block_scan(w, sh.red);
-            const u64 total = sh.red[kWarps - 1];
-            const double target = u * (double)total;
-            if (w && (double)cum > target && (double)(cum - w) <= target) {
-                const int i = (int)(by_index >> 32);
-                const float l = BF16 ? tc::bf16f(static_cast<const uint16_t*>(a.logits)[row * a.stride + i])
-                                     : static_cast<const float*>(a.logits)[row * a.stride + i];
-                answer(i, l, total);
-            }
-            return;
         }
-
-        // ---- 3b. narrow the bin by its keys, first for k, then for p
-        // smallest key whose bin is at most b
-        auto lowest_key = [&](int b) {
-            uint32_t lo = 0, hi = (uint32_t)(best >> 32);       // hi is in bin 0
-            while (lo < hi) {
-                const uint32_t mid = lo + (hi - lo) / 2;
-                const float f = key_value(mid);
-                if (f == f && f > -INFINITY && Row::bin(r.z(f)) <= b)
-                    hi = mid;
-                else
-                    lo = mid + 1;
-            }
-            return lo;
-        };
-        u64 total = sh.tw[kBins - 1];
-        for (int what = 0; what < 2; ++what) {
-            const bool weights = what == 1;
-            if (weights ? !by_p : !by_k)
-                continue;
-            const u64 need = weights ? need_of(total) : (u64)k;
-            const int b = first_of(weights, need, kBins);
-            u64 wab = b ? sh.tw[b - 1] : 0, nab = b ? sh.tcnt[b - 1] : 0;      // weight and count above the range
-            uint32_t lo = lowest_key(b);
-            u64 range = (b ? (u64)lowest_key(b - 1) : (best >> 32) + 1) - lo;  // keys lo .. lo + range - 1
-            // the z histogram is needed again for p
-            const u64 keep_w = tid < kBins ? sh.tw[tid] : 0;
-            const uint32_t keep_n = tid < kBins ? sh.tcnt[tid] : 0;
-            u64 rest;
-            while (true) {
-                const u64 width = (range + kBins - 1) / kBins;
+        if (!all && !last) {
+            // ---- many tokens in a bin: narrow it by its keys, first for k, then for p
+            // the row's histogram from the CTAs', as prefix sums
+            auto join = [&]() {
+                cl.sync();
+                u64 w = 0, n = 0;
+                if (tid < kBins)
+                    for (int i = 0; i < c; ++i) {
+                        const Shared* s = cl.map_shared_rank(&sh, i);
+                        w += (u64)s->lo[tid] + ((u64)s->hi[tid] << 16);
+                        n += s->cnt[tid];
+                    }
+                w = block_scan(w, sh.red);
+                n = block_scan(n, sh.red);
+                if (tid < kBins) {
+                    sh.tw[tid] = w;
+                    sh.tcnt[tid] = (uint32_t)n;
+                }
+                __syncthreads();
+            };
+            auto clear = [&]() {
                 cl.sync();
                 for (int i = tid; i < kBins; i += kThreads)
                     sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
                 __syncthreads();
-                part.each([&](float l, int i) {
-                    if (i < 0)
-                        return;
-                    const uint32_t kk = order_key(l);
-                    if (kk < lo || kk - lo >= range)
-                        return;
-                    const uint32_t w = Row::weight(r.z(key_value(kk)));
-                    if (w)
-                        add(kBins - 1 - (int)((kk - lo) / (uint32_t)width), w);  // larger keys first
-                });
-                join(kBins);
-                rest = need - (weights ? wab : nab);
-                const int s = first_of(weights, rest, kBins);
-                const u64 w0 = s ? sh.tw[s - 1] : 0, n0 = s ? sh.tcnt[s - 1] : 0;
-                const uint32_t here = sh.tcnt[s] - (uint32_t)n0;
-                wab += w0;
-                nab += n0;
-                rest -= weights ? w0 : n0;
-                const uint32_t from = (uint32_t)(kBins - 1 - s) * (uint32_t)width;
-                lo += from;
-                range = range - from < width ? range - from : width;
-                if (range == 1) {
-                    const u64 w = Row::weight(r.z(key_value(lo)));
-                    key = lo;
-                    ties = weights ? (uint32_t)((rest + w - 1) / w) : (uint32_t)rest;
-                    ties = min(ties, here);
-                    total = wab + ties * w;
-                    break;
+            };
+            auto add = [&](int b, uint32_t w) {
+                atomicAdd(&sh.cnt[b], 1u);
+                atomicAdd(&sh.lo[b], w & 0xffffu);
+                atomicAdd(&sh.hi[b], w >> 16);
+            };
+            // first prefix sum that reaches `need`
+            auto first_of = [&](bool weights, u64 need) {
+                if (tid < kBins) {
+                    const u64 x = weights ? sh.tw[tid] : sh.tcnt[tid], before = tid ? (weights ? sh.tw[tid - 1] : sh.tcnt[tid - 1]) : 0;
+                    if (x >= need && before < need)
+                        sh.found = tid;
+                }
+                __syncthreads();
+                const int b = sh.found;
+                __syncthreads();
+                return b;
+            };
+            // smallest key whose bin is at most b
+            auto lowest_key = [&](int b) {
+                uint32_t lo = 0, hi = (uint32_t)(best >> 32);       // hi is in bin 0
+                while (lo < hi) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    const float z = r.z(key_value(mid));
+                    if (z == z && Row::bin(z) <= b)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                return lo;
+            };
+            clear();
+            part.each([&](float l, int i) {
+                const float z = r.z(l);
+                const uint32_t w = i < 0 ? 0 : Row::weight(z);
+                if (w)
+                    add(Row::bin(z), w);
+            });
+            join();
+            const u64 keep_w = tid < kBins ? sh.tw[tid] : 0;
+            const uint32_t keep_n = tid < kBins ? sh.tcnt[tid] : 0;
+            u64 total = sh.tw[kBins - 1];
+            const bool cut_k = by_k && (uint32_t)k < sh.tcnt[kBins - 1];
+            all = !cut_k && !by_p;
+            for (int what = 0; what < 2; ++what) {
+                const bool weights = what == 1;
+                if (weights ? !by_p : !cut_k)
+                    continue;
+                __syncthreads();
+                if (tid < kBins) {
+                    sh.tw[tid] = keep_w;
+                    sh.tcnt[tid] = keep_n;
+                }
+                __syncthreads();
+                const u64 need = weights ? need_of(total) : (u64)k;
+                const int b = first_of(weights, need);
+                u64 wab = b ? sh.tw[b - 1] : 0, nab = b ? sh.tcnt[b - 1] : 0;      // weight and count above the range
+                uint32_t lo = lowest_key(b);
+                u64 range = (b ? (u64)lowest_key(b - 1) : (best >> 32) + 1) - lo;  // keys lo .. lo + range - 1
+                while (true) {
+                    const uint32_t width = (uint32_t)((range + kBins - 1) / kBins);
+                    clear();
+                    part.each([&](float l, int i) {
+                        const uint32_t kk = order_key(l);
+                        if (i < 0 || kk < lo || kk - lo >= range)
+                            return;
+                        const uint32_t w = Row::weight(r.z(l));
+                        if (w)
+                            add(kBins - 1 - (int)((kk - lo) / width), w);   // larger keys first
+                    });
+                    join();
+                    u64 rest = need - (weights ? wab : nab);
+                    const int s = first_of(weights, rest);
+                    const u64 w0 = s ? sh.tw[s - 1] : 0, n0 = s ? sh.tcnt[s - 1] : 0;
+                    const uint32_t here = sh.tcnt[s] - (uint32_t)n0;
+                    wab += w0;
+                    nab += n0;
+                    rest -= weights ? w0 : n0;
+                    const uint32_t from = (uint32_t)(kBins - 1 - s) * width;
+                    lo += from;
+                    range = range - from < width ? range - from : width;
+                    if (range == 1) {
+                        const u64 w = Row::weight(r.z(key_value(lo)));
+                        key = lo;
+                        ties = weights ? (uint32_t)((rest + w - 1) / w) : (uint32_t)rest;
+                        ties = min(ties, here);
+                        total = wab + ties * w;
+                        break;
+                    }
                 }
             }
-            __syncthreads();
-            if (tid < kBins) {
-                sh.tw[tid] = keep_w;
-                sh.tcnt[tid] = keep_n;
-            }
-            __syncthreads();
         }
     }
 
     // ---- 4. kept weights in the vocabulary's order
-    u64 sum = 0;
-    uint32_t eq = 0;
-    const bool cut = ties != 0xffffffffu;
-    auto kept = [&](float l) -> uint32_t {       // weight of a token above the cut
-        const uint32_t w = Row::weight(r.z(l));
-        return (double)w >= least ? w : 0;
-    };
-    part.each([&](float l, int i) {
-        if (i < 0)
-            return;
-        const uint32_t kk = order_key(l);
-        if (cut && kk <= key)
-            eq += kk == key;
-        else
-            sum += kept(key_value(kk));
-    });
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sum += __shfl_xor_sync(~0u, sum, o);
-        eq += __shfl_xor_sync(~0u, eq, o);
-    }
-    if (lane == 0) {
-        sh.warp_sum[warp] = sum;
-        sh.warp_ties[warp] = eq;
+    const bool cut = !all && !last;
+    if (!last) {
+        u64 sum = 0;
+        uint32_t eq = 0;
+        part.each([&](float l, int i) {
+            const uint32_t w = i < 0 ? 0 : Row::weight(r.z(l));
+            bool above = w >= least;
+            if (cut) {
+                const uint32_t kk = order_key(l);
+                eq += i >= 0 && kk == key;
+                above = above && kk > key;
+            }
+            sum += above ? w : 0;
+        });
+        sum = warp_sum(sum);
+        eq = __reduce_add_sync(~0u, eq);
+        if (lane == 0) {
+            sh.warp_sum[warp] = sum;
+            sh.warp_ties[warp] = eq;
+        }
     }
     __syncthreads();
     if (warp == 0) {
-        u64 s = sh.warp_sum[lane];
-        uint32_t n = sh.warp_ties[lane];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s += __shfl_xor_sync(~0u, s, o);
-            n += __shfl_xor_sync(~0u, n, o);
-        }
+        const u64 s = warp_sum(sh.warp_sum[lane]);
+        const uint32_t n = __reduce_add_sync(~0u, sh.warp_ties[lane]);
         if (lane < c) {
             *cl.map_shared_rank(&sh.part_sum[rank], lane) = s;
             *cl.map_shared_rank(&sh.part_ties[rank], lane) = n;
         }
     }
     cl.sync();
-    const u64 wtie = cut ? kept(key_value(key)) : 0;
-    u64 total = 0, before = 0;
-    uint32_t tie0 = 0, seen = 0;                 // ties before this CTA, and so far
+    u64 wtie = 0;
+    if (cut) {
+        wtie = Row::weight(r.z(key_value(key)));
+        wtie = wtie >= least ? wtie : 0;
+    }
+    u64 total = 0, cum = 0;
+    uint32_t seen = 0, tie0 = 0;                 // ties so far, and before this CTA
     for (int i = 0; i < c; ++i) {
-        const uint32_t in = min(sh.part_ties[i], ties - min(ties, seen));
         if (i == rank) {
-            before = total;
+            cum = total;
             tie0 = seen;
         }
-        total += sh.part_sum[i] + in * wtie;
+        total += sh.part_sum[i] + min(sh.part_ties[i], ties - min(ties, seen)) * wtie;
         seen += sh.part_ties[i];
     }
-    const double target = u * (double)total;
+    const u64 target = target_of(total);
     // the warp that holds the target
-    u64 cum = before;
-    seen = tie0;
-    for (int w = 0; w < warp; ++w) {
-        cum += sh.warp_sum[w] + min(sh.warp_ties[w], ties - min(ties, seen)) * wtie;
-        seen += sh.warp_ties[w];
-    }
-    const u64 own = sh.warp_sum[warp] + min(sh.warp_ties[warp], ties - min(ties, seen)) * wtie;
-    if ((double)cum > target || !((double)(cum + own) > target))
+    const uint32_t wt = sh.warp_ties[lane], wts = warp_scan(wt) - wt + tie0;
+    const u64 ws = sh.warp_sum[lane] + min(wt, ties - min(ties, wts)) * wtie, wss = warp_scan(ws);
+    const u64 end = cum + __shfl_sync(~0u, wss, warp);
+    cum += __shfl_sync(~0u, wss - ws, warp);
+    seen = __shfl_sync(~0u, wts, warp);
+    if (cum > target || end <= target)
         return;
     for (int v = part.v0; v < part.v1; v += 32) {
         uint32_t w[Part<BF16>::VEC], vl = 0, nl = 0;
         float val[Part<BF16>::VEC];
-        int idx[Part<BF16>::VEC], j = 0;
+        int j = 0;
         u64 s = 0;
         part.visit(v + lane, [&](float l, int i) {
             const uint32_t kk = order_key(l);
             const bool tie = i >= 0 && cut && kk == key;
+            const bool in = i >= 0 && (all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key));
+            const uint32_t x = in ? Row::weight(r.z(l)) : 0;
             nl += tie;
             vl |= (uint32_t)tie << j;
-            w[j] = i < 0 || (cut && kk <= key) ? 0 : kept(key_value(kk));
-            val[j] = key_value(kk);
-            idx[j] = i;
+            w[j] = x >= least ? x : 0;
+            val[j] = l;
             s += w[j++];
         });
         const uint32_t ti = warp_scan(nl), tn = __shfl_sync(~0u, ti, 31);
         uint32_t rk = seen + ti - nl;            // ties before this lane's
-        if (vl)
 #pragma unroll
-            for (int e = 0; e < Part<BF16>::VEC; ++e)
-                if (vl >> e & 1) {
-                    if (rk++ < ties) {
-                        w[e] = (uint32_t)wtie;
-                        s += wtie;
-                    }
-                }
+        for (int e = 0; e < Part<BF16>::VEC; ++e)
+            if ((vl >> e & 1) && rk++ < ties) {
+                w[e] = (uint32_t)wtie;
+                s += wtie;
+            }
         const u64 si = warp_scan(s), sn = __shfl_sync(~0u, si, 31);
         u64 at = cum + si - s;
-        if ((double)at <= target && (double)(at + s) > target) {
+        if (at <= target && at + s > target) {
 #pragma unroll
             for (int e = 0; e < Part<BF16>::VEC; ++e) {
-                if ((double)at <= target && (double)(at + w[e]) > target)
-                    answer(idx[e], val[e], total);
+                if (at <= target && at + w[e] > target)
+                    answer((v + lane) * Part<BF16>::VEC - part.lead + e, val[e], total);
                 at += w[e];
             }
         }
         cum += sn;
         seen += tn;
-        if ((double)cum > target)
+        if (cum > target)
             break;
     }
 }
