@@ -146,36 +146,36 @@ struct Part {
     const uint8_t* base;      // 16-byte aligned
     int lead, V, v0, v1;
 
+    // Vector v; -inf, which has no weight, where there is no element.
     __device__ __forceinline__ uint4 load(int v) const
     {
         const int i0 = v * VEC - lead;
-        if (v >= v1)
-            return make_uint4(0, 0, 0, 0);
-        if (i0 >= 0 && i0 + VEC <= V)
+        if (v < v1 && i0 >= 0 && i0 + VEC <= V)
             return __ldg(reinterpret_cast<const uint4*>(base + (long long)v * 16));
         // the row's ends: only its own elements are read
-        uint32_t w[4] = {0, 0, 0, 0};
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (i0 + e >= 0 && i0 + e < V) {
-                if (BF16)
-                    w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(base + (long long)v * 16)[e] << 16 * (e & 1);
-                else
-                    w[e] = reinterpret_cast<const uint32_t*>(base + (long long)v * 16)[e];
-            }
+        for (int e = 0; e < 4; ++e)
+            w[e] = BF16 ? 0xff80ff80u : 0xff800000u;
+        if (v < v1)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (i0 + e >= 0 && i0 + e < V) {
+                    if (BF16)
+                        w[e >> 1] = __byte_perm(w[e >> 1], reinterpret_cast<const uint16_t*>(base + (long long)v * 16)[e], e & 1 ? 0x5410 : 0x3254);
+                    else
+                        w[e] = reinterpret_cast<const uint32_t*>(base + (long long)v * 16)[e];
+                }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // f(value, index) for each element of vector v (index -1: no element)
+    // f(value, index) for each element of vector v
     template <class F>
     __device__ __forceinline__ void take(int v, uint4 q, F f) const
     {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float x = BF16 ? __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]);
-            const int i = v * VEC - lead + e;
-            f(x, v < v1 && i >= 0 && i < V ? i : -1);
-        }
+        for (int e = 0; e < VEC; ++e)
+            f(BF16 ? __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]), v * VEC - lead + e);
     }
     template <class F>
     __device__ __forceinline__ void visit(int v, F f) const { take(v, load(v), f); }
@@ -227,13 +227,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     }
 
     // ---- 1. the largest logit, lowest index first
-    u64 best = 0;
-    part.each([&](float l, int i) {
-        if (i >= 0) {
-            const u64 k = (u64)order_key(l) << 32 | (0xffffffffu - (uint32_t)i);
-            best = k > best ? k : best;
-        }
-    });
+    u64 best;
+    {
+        float m = -INFINITY;
+        int at = 0;                          // a row of -inf (or NaN): index 0
+        part.each([&](float l, int i) {
+            if (l > m) {
+                m = l;
+                at = i;
+            }
+        });
+        best = (u64)order_key(m) << 32 | (0xffffffffu - (uint32_t)at);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const u64 x = __shfl_xor_sync(~0u, best, o);
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         // ---- 2. counts in 1/256 of z
         part.each([&](float l, int i) {
             const int b = Row::fine(r.z(l));
-            if (i >= 0 && b < kFine)
+            if (b < kFine)
                 atomicAdd(&sh.fine[b], 1u);
         });
         const int share = (kFine + c - 1) / c;
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             u64 kept = 0, raw = 0, mid = 0;
             part.each([&](float l, int i) {
                 const float z = r.z(l);
-                const int b = i < 0 ? kFine : Row::fine(z);
+                const int b = Row::fine(z);
                 if (b < p0 || (b > p1 && b < kb)) {
                     if (sums) {
                         const uint32_t x = Row::weight(z);
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             clear();
             part.each([&](float l, int i) {
                 const float z = r.z(l);
-                const uint32_t w = i < 0 ? 0 : Row::weight(z);
+                const uint32_t w = Row::weight(z);
                 if (w)
                     add(Row::bin(z), w);
             });
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     clear();
                     part.each([&](float l, int i) {
                         const uint32_t kk = order_key(l);
-                        if (i < 0 || kk < lo || kk - lo >= range)
+                        if (kk < lo || kk - lo >= range)
                             return;
                         const uint32_t w = Row::weight(r.z(l));
                         if (w)
@@ -619,14 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         u64 sum = 0;
         uint32_t eq = 0;
         part.each([&](float l, int i) {
-            const uint32_t w = i < 0 ? 0 : Row::weight(r.z(l));
-            bool above = w >= least;
+            const uint32_t w = Row::weight(r.z(l));
             if (cut) {
                 const uint32_t kk = order_key(l);
-                eq += i >= 0 && kk == key;
-                above = above && kk > key;
+                eq += kk == key;
+                sum += w >= least && kk > key ? w : 0;
+            } else {
+                sum += w >= least ? w : 0;
             }
-            sum += above ? w : 0;
         });
         sum = warp_sum(sum);
         eq = __reduce_add_sync(~0u, eq);
@@ -676,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         u64 s = 0;
         part.visit(v + lane, [&](float l, int i) {
             const uint32_t kk = order_key(l);
-            const bool tie = i >= 0 && cut && kk == key;
-            const bool in = i >= 0 && (all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key));
+            const bool tie = cut && kk == key;
+            const bool in = (all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key));
             const uint32_t x = in ? Row::weight(r.z(l)) : 0;
             nl += tie;
             vl |= (uint32_t)tie << j;
