@@ -10,8 +10,8 @@
 //  1. The largest logit (one read from HBM; later passes find the row in L1 / L2).
 //  2. With top-k or top-p: how many tokens there are in each 1/256 of z.  z is a
 //     monotone function of the logit, so bins are runs of the order: top-k ends in a
-//     bin that the counts name, top-p in one that the counts times the bins' middle
-//     weights name but for a relative 1e-4.
+//     bin that the counts name, top-p in one of the few that the counts times the bins'
+//     middle weights leave open.
 //  3. One pass adds up the weights before and between those bins (per warp, in the
 //     vocabulary's order) and gathers the bins' own tokens, which one CTA sorts: the
 //     last member of the kept set is found exactly.  Where all tokens that may be
@@ -34,9 +34,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMostCluster = 16;
-constexpr int kMostPart = 65536;           // tokens of a CTA: a bin's sum of 16-bit halves fits 32 bits
-constexpr int kSlackPart = 32 * 32 * 8;    // a CTA's part may be this much above an equal share
+constexpr int kMostCluster = 8;
+constexpr int kMostVectors = 32 * 32 * kWarps;   // 16-byte vectors of a CTA's part: 32 rows of 32 a warp
 constexpr int kBins = 768;                 // of 1/32 of z: weights are 0 from z = -22.2 on
 constexpr int kFine = 5760;               // of 1/256 of z
 constexpr int kFinePer = (kFine + kThreads - 1) / kThreads;
@@ -72,18 +71,21 @@ struct Shared {
     union {
         uint32_t fine[kFinePer * kThreads];          // this CTA's counts; then the row's, as prefix sums
         struct {
-            uint32_t cnt[kBins], lo[kBins], hi[kBins];   // this CTA's histogram: counts, halves of weights
+            uint32_t cnt[kBins], w0[kBins], w1[kBins], w2[kBins];   // this CTA's histogram: counts, and sums of the
+                                           // weights' bits 0..10, 11..21, 22..31 (none can pass 32 bits)
             uint32_t tcnt[kBins];          // the row's, inclusive prefix sums
             u64 tw[kBins];
         };
     };
-    uint32_t share[(kFine + 1) / 2];       // the row's counts in this CTA's share of the bins (two CTAs or more)
+    uint32_t share[kFinePer * kThreads / 2];   // the row's counts in this CTA's share of the bins (two CTAs or more)
     u64 list[kList];                       // the first CTA's: gathered tokens, as key and complement of the index
     u64 warp_sum[kWarps], part_sum[kMostCluster], part_raw[kMostCluster], part_mid[kMostCluster];
-    uint32_t warp_ties[kWarps], part_ties[kMostCluster];
+    u64 row_sum[kWarps];
+    uint32_t warp_ties[kWarps], part_ties[kMostCluster], row_ties[kWarps];
     uint32_t nlist;
     int found, kbin, pbin[2];
-    u64 about, last;
+    float sq[kWarps];
+    u64 about, last, said;                 // said: what one thread computes for all
 };
 
 template <class T>
@@ -115,20 +117,20 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* red)
     return v;
 }
 
-// Bitonic sort of the CTA's values (one a thread, n a power of two from 32 on),
-// ascending or descending.
-__device__ __forceinline__ u64 block_sort(u64 v, int n, bool descending, u64* buf)
+// Bitonic sort of the values of the first n threads (one each, n a power of two from
+// 32 on), ascending or descending; for those threads alone.
+__device__ __forceinline__ u64 sort_first(u64 v, int n, bool descending, u64* buf)
 {
     const int tid = threadIdx.x;
+    auto sync = [n]() { asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory"); };
     for (int k = 2; k <= n; k <<= 1)
         for (int j = k >> 1; j; j >>= 1) {
             u64 o;
             if (j >= 32) {
-                __syncthreads();
-                if (tid < n)
-                    buf[tid] = v;
-                __syncthreads();
-                o = tid < n ? buf[tid ^ j] : v;
+                sync();
+                buf[tid] = v;
+                sync();
+                o = buf[tid ^ j];
             } else {
                 o = __shfl_xor_sync(~0u, v, j);
             }
@@ -226,6 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         part.v1 = min(part.v0 + per, nv);
     }
 
+    const float T = a.p.temperature ? a.p.temperature[row] : 1.0f;
+    const int k = a.p.top_k ? a.p.top_k[row] : 0;
+    const float tp = a.p.top_p ? a.p.top_p[row] : 1.0f, mp = a.p.min_p ? a.p.min_p[row] : 0.0f, uu = a.p.u[row];
+    const bool by_p = tp < 1.0f;
+
     // ---- 1. the largest logit, lowest index first
     u64 best;
     {
@@ -272,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 
     Row r;
     r.top = key_value((uint32_t)(best >> 32));
-    const float T = a.p.temperature ? a.p.temperature[row] : 1.0f;
     if (!(T > 0.0f) || r.top == -INFINITY) {
         if (rank == 0 && tid == 0) {
             a.token[row] = (int)(0xffffffffu - (uint32_t)best);
@@ -282,17 +288,24 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         return;
     }
     r.inv_t = __fdiv_rn(1.0f, fmaxf(T, 1e-30f));
-    const int k = a.p.top_k ? a.p.top_k[row] : 0;
-    const float tp = a.p.top_p ? a.p.top_p[row] : 1.0f, mp = a.p.min_p ? a.p.min_p[row] : 0.0f, uu = a.p.u[row];
-    const bool by_p = tp < 1.0f;
-    // integers take the place of fp64 products: w >= x as w >= ceil(x), and below cum > x as cum > floor(x)
-    const uint32_t least = (uint32_t)ceil((double)fminf(fmaxf(mp, 0.0f), 1.0f) * 2147483648.0);
+    // w >= min_p * 2^31 in integers (the fp32 product is exact)
+    const uint32_t least = (uint32_t)ceilf(fminf(fmaxf(mp, 0.0f), 1.0f) * 2147483648.0f);
+    // fp64 is slow here: one thread computes such a product for all, and sums are
+    // compared as integers (cum >= x as cum >= ceil(x), cum > x as cum > floor(x))
     auto need_of = [&](u64 total) {
         const double need = ceil((double)tp * (double)total);
         return need >= 1.0 ? (u64)need : 1ull;
     };
     auto target_of = [&](u64 total) {
         return (u64)((uu > 0.0f ? fmin((double)uu, 1.0 - 5.9604644775390625e-08) : 0.0) * (double)total);
+    };
+    auto one_for_all = [&](auto f, u64 x) {
+        if (tid == 0)
+            sh.said = f(x);
+        __syncthreads();
+        const u64 v = sh.said;
+        __syncthreads();
+        return v;
     };
     auto answer = [&](int i, float l, u64 total) {
         a.token[row] = i;
@@ -313,29 +326,43 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             if (b < kFine)
                 atomicAdd(&sh.fine[b], 1u);
         });
-        const int share = (kFine + c - 1) / c;
+        const int tps = (kThreads + c - 1) / c;              // threads whose bins one CTA adds up
         if (c > 1) {
             // every CTA adds up its share of the bins, then takes all shares
             cl.sync();
-            for (int b = tid; b < share && rank * share + b < kFine; b += kThreads) {
+            for (int b = tid; b < tps * kFinePer && rank * tps * kFinePer + b < kFine; b += kThreads) {
                 uint32_t n = 0;
+#pragma unroll 4
                 for (int i = 0; i < c; ++i)
-                    n += cl.map_shared_rank(&sh, i)->fine[rank * share + b];
+                    n += cl.map_shared_rank(&sh, i)->fine[rank * tps * kFinePer + b];
                 sh.share[b] = n;
             }
             cl.sync();
-        } else {
-            __syncthreads();
+            for (int b = tid; b < kFine; b += kThreads) {
+                const int from = b / (tps * kFinePer);
+                sh.fine[b] = cl.map_shared_rank(&sh, from)->share[b - from * tps * kFinePer];
+            }
         }
+        __syncthreads();
         uint32_t n[kFinePer], nsum = 0;
         u64 w[kFinePer], wsum = 0;
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kFinePer; ++j)
+            n[j] = tid * kFinePer + j < kFine ? sh.fine[tid * kFinePer + j] : 0;
 #pragma unroll
         for (int j = 0; j < kFinePer; ++j) {
-            const int b = tid * kFinePer + j;
-            n[j] = b >= kFine ? 0 : c > 1 ? cl.map_shared_rank(&sh, b / share)->share[b % share] : sh.fine[b];
-            w[j] = n[j] * (u64)Row::weight(Row::fine_middle(b));
+            w[j] = n[j] * (u64)Row::weight(Row::fine_middle(tid * kFinePer + j));
             nsum += n[j];
             wsum += w[j];
+            sq += (float)w[j] * (float)w[j];
+        }
+        if (by_p) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                sq += __shfl_xor_sync(~0u, sq, o);
+            if (lane == 0)
+                sh.sq[warp] = sq;
         }
         const u64 nb = block_scan((u64)nsum, sh.red) - nsum, wb = block_scan(wsum, sh.red2) - wsum;
         const bool by_k = k > 0 && (u64)k < sh.red[kWarps - 1];
@@ -355,8 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             about = sh.about;
         }
         if (by_p) {
-            const double share_p = (double)fmaxf(tp, 0.0f) * (double)about;
-            const u64 t0 = max((u64)(share_p * 0.9999), 1ull), t1 = max((u64)(share_p * 1.0001), 1ull);
+            // a bin's tokens may lie anywhere in it: its weight is off by up to 2^-9, 2^-9.8
+            // in the mean square.  Four times what that makes of independent bins
+            sq = 0.0f;
+            for (int i = 0; i < kWarps; ++i)
+                sq += sh.sq[i];
+            const float share_p = fmaxf(tp, 0.0f) * (float)about, off = 0.0046f * sqrtf(sq) + 1e-5f * (float)about;
+            const u64 t0 = (u64)fmaxf(share_p - off, 1.0f), t1 = (u64)fmaxf(share_p + off, 1.0f);
             u64 y = wb;
 #pragma unroll
             for (int j = 0; j < kFinePer; ++j) {
@@ -441,23 +473,45 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 int n2 = 32;
                 while (n2 < (int)n_list)
                     n2 <<= 1;
-                u64 e = tid < (int)n_list ? sh.list[tid] : 0;
-                __syncthreads();
-                e = block_sort(e, n2, true, sh.list);
+                u64 e;
+                const bool few = n_list <= kThreads / 4;
+                if (few) {
+                    // each place in the order by counting what is before it, four threads an entry
+                    const int i = tid >> 2;
+                    e = i < (int)n_list ? sh.list[i] : 0;
+                    int place = 0;
+                    for (int j = tid & 3; j < (int)n_list; j += 4)
+                        place += sh.list[j] > e;
+                    place += __shfl_xor_sync(~0u, place, 1);
+                    place += __shfl_xor_sync(~0u, place, 2);
+                    __syncthreads();
+                    if (i < (int)n_list && (tid & 3) == 0)
+                        sh.list[place] = e;
+                    __syncthreads();
+                    e = tid < (int)n_list ? sh.list[tid] : 0;
+                } else {
+                    e = tid < (int)n_list ? sh.list[tid] : 0;
+                    __syncthreads();
+                    if (tid < n2)
+                        e = sort_first(e, n2, true, sh.list);
+                }
                 // this thread's place in the order, and its weight if top-k takes it
                 const uint32_t at = tid < (int)n_p ? before + tid : before_k + (tid - n_p);
-                u64 x = tid < (int)n_list && (!by_k || at < (uint32_t)k) ? Row::weight(r.z(key_value((uint32_t)(e >> 32)))) : 0;
-                const u64 own = x, cum = block_scan(tid < (int)n_p ? x : 0, sh.red);
-                const u64 in_band = sh.red[kWarps - 1];
+                u64 x = 0;
+                if (tid < (int)n_list && (!by_k || at < (uint32_t)k))
+                    x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
                 bool in = x != 0;
                 if (by_p) {
-                    block_scan(tid < (int)n_p ? 0 : x, sh.red2);
-                    const u64 need = need_of(raw + in_band + mid + sh.red2[kWarps - 1]);
+                    const u64 own = tid < (int)n_p ? x : 0, cum = block_scan(own, sh.red);
+                    const u64 in_band = sh.red[kWarps - 1];
+                    block_scan(x - own, sh.red2);
+                    const u64 need = one_for_all(need_of, raw + in_band + mid + sh.red2[kWarps - 1]);
                     in = in && tid < (int)n_p && raw + cum - own < need;
                     found = raw < need && raw + in_band >= need;     // the share is reached within the band
                 }
                 __syncthreads();
-                sh.list[tid] = e;
+                if (!few && tid < n2)
+                    sh.list[tid] = e;
                 if (in)
                     atomicMax(&sh.last, ~e);                          // the last one has the largest complement
                 __syncthreads();
@@ -465,11 +519,31 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     if (!in || x < least)
                         x = 0;
                     // by index, the kept ones first
-                    u64 by_index = x ? (u64)(0xffffffffu - (uint32_t)e) << 32 | x : ~0ull << 32;
-                    by_index = block_sort(by_index, n2, false, sh.list);
-                    x = tid < n2 ? by_index & 0xffffffffu : 0;
-                    const u64 run = block_scan(x, sh.red);
-                    const u64 total = sh.red[kWarps - 1], target = target_of(total);
+                    u64 by_index = x ? (u64)(0xffffffffu - (uint32_t)e) << 32 | x : ~0ull << 32, run = 0, total = 0;
+                    if (few) {
+                        if (tid < (int)n_list)
+                            sh.list[tid] = by_index;
+                        __syncthreads();
+                        by_index = tid >> 2 < (int)n_list ? sh.list[tid >> 2] : 0;
+                        for (int j = tid & 3; j < (int)n_list; j += 4) {
+                            const u64 y = sh.list[j], add = y & 0xffffffffu;
+                            total += add;
+                            run += y <= by_index ? add : 0;
+                        }
+#pragma unroll
+                        for (int o = 1; o <= 2; o <<= 1) {
+                            total += __shfl_xor_sync(~0u, total, o);
+                            run += __shfl_xor_sync(~0u, run, o);
+                        }
+                        x = tid & 3 ? 0 : by_index & 0xffffffffu;
+                    } else {
+                        if (tid < n2)
+                            by_index = sort_first(by_index, n2, false, sh.list);
+                        x = tid < n2 ? by_index & 0xffffffffu : 0;
+                        run = block_scan(x, sh.red);
+                        total = sh.red[kWarps - 1];
+                    }
+                    const u64 target = one_for_all(target_of, total);
                     if (x && run > target && run - x <= target) {
                         const int i = (int)(by_index >> 32);
                         answer(i, BF16 ? tc::bf16f(static_cast<const uint16_t*>(a.logits)[row * a.stride + i])
@@ -508,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 if (tid < kBins)
                     for (int i = 0; i < c; ++i) {
                         const Shared* s = cl.map_shared_rank(&sh, i);
-                        w += (u64)s->lo[tid] + ((u64)s->hi[tid] << 16);
+                        w += (u64)s->w0[tid] + ((u64)s->w1[tid] << 11) + ((u64)s->w2[tid] << 22);
                         n += s->cnt[tid];
                     }
                 w = block_scan(w, sh.red);
@@ -522,13 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             auto clear = [&]() {
                 cl.sync();
                 for (int i = tid; i < kBins; i += kThreads)
-                    sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+                    sh.cnt[i] = sh.w0[i] = sh.w1[i] = sh.w2[i] = 0;
                 __syncthreads();
             };
             auto add = [&](int b, uint32_t w) {
                 atomicAdd(&sh.cnt[b], 1u);
-                atomicAdd(&sh.lo[b], w & 0xffffu);
-                atomicAdd(&sh.hi[b], w >> 16);
+                atomicAdd(&sh.w0[b], w & 0x7ffu);
+                atomicAdd(&sh.w1[b], w >> 11 & 0x7ffu);
+                atomicAdd(&sh.w2[b], w >> 22);
             };
             // first prefix sum that reaches `need`
             auto first_of = [&](bool weights, u64 need) {
@@ -578,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     sh.tcnt[tid] = keep_n;
                 }
                 __syncthreads();
-                const u64 need = weights ? need_of(total) : (u64)k;
+                const u64 need = weights ? one_for_all(need_of, total) : (u64)k;
                 const int b = first_of(weights, need);
                 u64 wab = b ? sh.tw[b - 1] : 0, nab = b ? sh.tcnt[b - 1] : 0;      // weight and count above the range
                 uint32_t lo = lowest_key(b);
@@ -665,72 +740,85 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         total += sh.part_sum[i] + min(sh.part_ties[i], ties - min(ties, seen)) * wtie;
         seen += sh.part_ties[i];
     }
-    const u64 target = target_of(total);
-    // the warp that holds the target
+    const u64 target = one_for_all(target_of, total);
+    // the warp in whose vectors the target lies (a lane for each warp)
     const uint32_t wt = sh.warp_ties[lane], wts = warp_scan(wt) - wt + tie0;
-    const u64 ws = sh.warp_sum[lane] + min(wt, ties - min(ties, wts)) * wtie, wss = warp_scan(ws);
-    const u64 end = cum + __shfl_sync(~0u, wss, warp);
-    cum += __shfl_sync(~0u, wss - ws, warp);
-    seen = __shfl_sync(~0u, wts, warp);
-    if (cum > target || end <= target)
+    const u64 ws = sh.warp_sum[lane] + min(wt, ties - min(ties, wts)) * wtie, wss = warp_scan(ws) + cum;
+    const unsigned hit = __ballot_sync(~0u, wss > target && wss - ws <= target);
+    if (!hit)
         return;
-    for (int v = part.v0; v < part.v1; v += 32) {
-        uint32_t w[Part<BF16>::VEC], vl = 0, nl = 0;
-        float val[Part<BF16>::VEC];
+    const int tw = __ffs(hit) - 1;
+    cum = __shfl_sync(~0u, wss - ws, tw);
+    seen = __shfl_sync(~0u, wts, tw);
+    Part<BF16> seg = part;
+    seg.v0 = (rank * kWarps + tw) * per;
+    seg.v1 = min(seg.v0 + per, (a.V + part.lead + part.VEC - 1) / part.VEC);
+    // its rows of 32 vectors (at most 32: kMostVectors), one a warp
+    uint32_t w[Part<BF16>::VEC], vl = 0, nl = 0;
+    float val[Part<BF16>::VEC];
+    u64 s = 0;
+    auto row_of = [&](int x) {
         int j = 0;
-        u64 s = 0;
-        part.visit(v + lane, [&](float l, int i) {
+        vl = nl = 0;
+        s = 0;
+        seg.visit(seg.v0 + 32 * x + lane, [&](float l, int i) {
             const uint32_t kk = order_key(l);
             const bool tie = cut && kk == key;
-            const bool in = (all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key));
-            const uint32_t x = in ? Row::weight(r.z(l)) : 0;
+            const bool in = all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key);
+            const uint32_t y = in ? Row::weight(r.z(l)) : 0;
             nl += tie;
             vl |= (uint32_t)tie << j;
-            w[j] = x >= least ? x : 0;
+            w[j] = y >= least ? y : 0;
             val[j] = l;
             s += w[j++];
         });
-        const uint32_t ti = warp_scan(nl), tn = __shfl_sync(~0u, ti, 31);
-        uint32_t rk = seen + ti - nl;            // ties before this lane's
-#pragma unroll
-        for (int e = 0; e < Part<BF16>::VEC; ++e)
-            if ((vl >> e & 1) && rk++ < ties) {
-                w[e] = (uint32_t)wtie;
-                s += wtie;
-            }
-        const u64 si = warp_scan(s), sn = __shfl_sync(~0u, si, 31);
-        u64 at = cum + si - s;
-        if (at <= target && at + s > target) {
-#pragma unroll
-            for (int e = 0; e < Part<BF16>::VEC; ++e) {
-                if (at <= target && at + w[e] > target)
-                    answer((v + lane) * Part<BF16>::VEC - part.lead + e, val[e], total);
-                at += w[e];
-            }
+    };
+    row_of(warp);
+    {
+        const u64 rs = warp_sum(s);
+        const uint32_t rt = __reduce_add_sync(~0u, nl);
+        if (lane == 0) {
+            sh.row_sum[warp] = rs;
+            sh.row_ties[warp] = rt;
         }
-        cum += sn;
-        seen += tn;
-        if (cum > target)
-            break;
+    }
+    __syncthreads();
+    const uint32_t rt = sh.row_ties[lane], rts = warp_scan(rt) - rt + seen;
+    const u64 rs = sh.row_sum[lane] + min(rt, ties - min(ties, rts)) * wtie, rss = warp_scan(rs) + cum;
+    const int trow = __ffs(__ballot_sync(~0u, rss > target && rss - rs <= target)) - 1;
+    if (warp != trow)
+        return;
+    cum = __shfl_sync(~0u, rss - rs, trow);
+    seen = __shfl_sync(~0u, rts, trow);
+    uint32_t rk = seen + warp_scan(nl) - nl;     // ties before this lane's
+#pragma unroll
+    for (int e = 0; e < Part<BF16>::VEC; ++e)
+        if ((vl >> e & 1) && rk++ < ties) {
+            w[e] = (uint32_t)wtie;
+            s += wtie;
+        }
+    u64 at = cum + warp_scan(s) - s;
+    if (at <= target && at + s > target) {
+#pragma unroll
+        for (int e = 0; e < Part<BF16>::VEC; ++e) {
+            if (at <= target && at + w[e] > target)
+                answer((seg.v0 + 32 * warp + lane) * Part<BF16>::VEC - part.lead + e, val[e], total);
+            at += w[e];
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t prepare_sample_kernels()
-{
-    const cudaError_t e = cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-}
+cudaError_t prepare_sample_kernels() { return cudaSuccess; }
 
 cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s)
 {
-    // CTAs a row: as many as leave every row its own SMs, up to 8 (a cluster of 16
-    // may find no room), each with at least 2,048 tokens; and no more tokens a CTA
-    // than its histogram takes (16 only above 458,752 tokens)
+    // CTAs a row: as few as take it; more while every row keeps its own SMs and a
+    // CTA at least 2,048 tokens
+    const int vectors = a.V / (a.logits_type == MOE_DT_BF16 ? 8 : 4) + 2;
     int c = 1;
-    while ((c < 8 && 2ll * c * a.M <= num_sms && a.V >= 2 * c * 2048) ||
-           (c < kMostCluster && a.V > c * (kMostPart - kSlackPart)))
+    while (c < kMostCluster && (vectors > c * kMostVectors || (2ll * c * a.M <= num_sms && a.V >= 2 * c * 2048)))
         c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.M * c);
