@@ -400,51 +400,56 @@ def moe_kv_batch_of(cu, kv_len, table, n_tokens) -> moe_kv_batch:
     return b
 
 
-def _rows(t, width):
-    """Address and row stride of a tensor whose rows of `width` elements are contiguous (the stride of a single row is
-    arbitrary in torch)."""
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+def _raw_stream(stream, t):
+    """The stream's handle; None: the current stream of the tensor's device (asked for by its handle alone: building a
+    torch.cuda.Stream takes as long as a launch)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _kv_rows(t, name, cache, batch):
+def _heads(t, name, T, H, D):
+    """Address and row stride of bf16 rows [T][H][D] with contiguous heads."""
     import torch
-    _need(t, name, torch.bfloat16, 3)
-    H, D = cache.kv_heads, cache.head_dim
-    if tuple(t.shape) != (batch.n_tokens, H, D) or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name}: rows [{batch.n_tokens}][{H}][{D}] with contiguous heads are needed (got {tuple(t.shape)}, "
-                         f"strides {t.stride()})")
-    return _rows(t, H * D)
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.shape != (T, H, D) or st[2] != 1 or (st[1] != D and H > 1):
+        raise ValueError(f"{name}: CUDA bf16 rows [{T}][{H}][{D}] with contiguous heads are needed (got {t.dtype} "
+                         f"{tuple(t.shape)}, strides {st}, on {t.device})")
+    return t.data_ptr(), st[0] if T > 1 else H * D
 
 
 def moe_kv_write(o, cache, batch, k, v, stream=None):
-    kp, ks = _kv_rows(k, "k", cache, batch)
-    vp, vs = _kv_rows(v, "v", cache, batch)
-    return _check(lib().moe_kv_write(o, cache, batch, kp, ks, vp, vs, _stream(stream)))
+    T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
+    kp, ks = _heads(k, "k", T, H, D)
+    vp, vs = _heads(v, "v", T, H, D)
+    return _check(lib().moe_kv_write(o, cache, batch, kp, ks, vp, vs, _raw_stream(stream, k)))
 
 
 def moe_kv_read(o, cache, batch, k, v, stream=None):
-    kp, ks = _kv_rows(k, "k", cache, batch)
-    vp, vs = _kv_rows(v, "v", cache, batch)
-    return _check(lib().moe_kv_read(o, cache, batch, kp, ks, vp, vs, _stream(stream)))
+    T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
+    kp, ks = _heads(k, "k", T, H, D)
+    vp, vs = _heads(v, "v", T, H, D)
+    return _check(lib().moe_kv_read(o, cache, batch, kp, ks, vp, vs, _raw_stream(stream, k)))
 
 
 def moe_attention(o, cache, batch, q, out, lse=None, sinks=None, window=0, scale=None, stream=None):
     """q bf16 [n_tokens][q_heads][head_dim] (rows may be strided), out like it and contiguous, lse fp32
     [n_tokens][q_heads], sinks fp32 [q_heads]; scale defaults to head_dim ** -0.5."""
     import torch
-    _need(q, "q", torch.bfloat16, 3)
-    _dense(out, "out", torch.bfloat16, 3)
-    T, heads, D = q.shape
-    if T != batch.n_tokens or D != cache.head_dim or (heads > 1 and q.stride(1) != D) or out.shape != q.shape:
-        raise ValueError(f"moe_attention: q {tuple(q.shape)} (strides {q.stride()}) and out {tuple(out.shape)} are not "
-                         f"{batch.n_tokens} rows of heads of {cache.head_dim}")
-    if lse is not None and tuple(_dense(lse, "lse", torch.float32, 2).shape) != (T, heads):
-        raise ValueError(f"moe_attention: lse {tuple(lse.shape)} is not [{T}][{heads}]")
-    if sinks is not None and _dense(sinks, "sinks", torch.float32, 1).shape[0] != heads:
-        raise ValueError(f"moe_attention: sinks {tuple(sinks.shape)} is not [{heads}]")
-    qp, qs = _rows(q, heads * D)
-    return _check(lib().moe_attention(o, cache, batch, qp, qs, heads, D ** -0.5 if scale is None else scale,
-                                      window, _ptr(sinks), out.data_ptr(), _ptr(lse), _stream(stream)))
+    T, heads, D = batch.n_tokens, q.shape[1] if q.dim() == 3 else 0, cache.head_dim
+    qp, qs = _heads(q, "q", T, heads, D)
+    op, _ = _heads(out, "out", T, heads, D)
+    if not out.is_contiguous():
+        raise ValueError(f"moe_attention: out must be contiguous (strides {out.stride()})")
+    if lse is not None and (lse.shape != (T, heads) or lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous()):
+        raise ValueError(f"moe_attention: lse must be a contiguous CUDA fp32 tensor [{T}][{heads}]")
+    if sinks is not None and (sinks.shape != (heads,) or sinks.dtype is not torch.float32 or not sinks.is_cuda or
+                              not sinks.is_contiguous()):
+        raise ValueError(f"moe_attention: sinks must be a contiguous CUDA fp32 tensor [{heads}]")
+    return _check(lib().moe_attention(o, cache, batch, qp, qs, heads, D ** -0.5 if scale is None else scale, window,
+                                      None if sinks is None else sinks.data_ptr(), op, None if lse is None else lse.data_ptr(),
+                                      _raw_stream(stream, q)))
 
 
 def moe_linear_of(codes, scales, bias, format, group) -> moe_linear_weights:
@@ -466,16 +471,24 @@ def moe_linear_of(codes, scales, bias, format, group) -> moe_linear_weights:
 def moe_linear(o, w, x, out, stream=None):
     """x bf16 [M][cols], out fp32 or bf16 [M][rows]; the rows of both may be strided."""
     import torch
-    _need(x, "x", torch.bfloat16, 2)
-    bf = out.dtype is torch.bfloat16
-    _need(out, "out", torch.bfloat16 if bf else torch.float32, 2)
+    rows, cols, kind = w.rows, w.cols, out.dtype
+    sx, so = x.stride(), out.stride()
     M = x.shape[0]
-    if x.shape[1] != w.cols or out.shape[0] != M or out.shape[1] != w.rows:
-        raise ValueError(f"moe_linear: x {tuple(x.shape)} and out {tuple(out.shape)} do not fit weights [{w.rows}][{w.cols}]")
-    xp, xs = _rows(x, w.cols)
-    op, os_ = _rows(out, w.rows)
-    return _check(lib().moe_linear(o, w, xp, xs, M, op, os_,
-                                   MOE_DT_BF16 if bf else MOE_DT_F32, _stream(stream)))
+    if (x.shape != (M, cols) or x.dtype is not torch.bfloat16 or not x.is_cuda or sx[1] != 1 or out.shape != (M, rows) or
+            (kind is not torch.bfloat16 and kind is not torch.float32) or not out.is_cuda or (so[1] != 1 and rows > 1)):
+        raise ValueError(f"moe_linear: x bf16 [M][{cols}] and out fp32 or bf16 [M][{rows}] on the GPU with contiguous rows are "
+                         f"needed (got {x.dtype} {tuple(x.shape)} strides {sx}, {kind} {tuple(out.shape)} strides {so})")
+    return _check(lib().moe_linear(o, w, x.data_ptr(), sx[0] if M > 1 else cols, M, out.data_ptr(), so[0] if M > 1 else rows,
+                                   MOE_DT_BF16 if kind is torch.bfloat16 else MOE_DT_F32, _raw_stream(stream, x)))
+
+
+def _per_row(t, name, dtype, M):
+    if t is None:
+        return None
+    if t.shape != (M,) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"moe_sample: {name} must be a contiguous CUDA tensor of {dtype} [{M}] (got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device})")
+    return t.data_ptr()
 
 
 def moe_sample(o, logits, temperature, top_k, top_p, min_p, u, token, logprob=None, stream=None):
@@ -485,12 +498,9 @@ def moe_sample(o, logits, temperature, top_k, top_p, min_p, u, token, logprob=No
     bf = logits.dtype is torch.bfloat16
     _need(logits, "logits", torch.bfloat16 if bf else torch.float32, 2)
     M, V = logits.shape
-    f, n = torch.float32, torch.int32
-    for t, name, dtype in ((temperature, "temperature", f), (top_k, "top_k", n), (top_p, "top_p", f), (min_p, "min_p", f),
-                           (u, "u", f), (token, "token", n), (logprob, "logprob", f)):
-        if t is not None and _dense(t, name, dtype, 1).shape[0] != M:
-            raise ValueError(f"moe_sample: {name} {tuple(t.shape)} is not [{M}]")
-    par = moe_sample_params(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u))
-    lp, ls = _rows(logits, V)
-    return _check(lib().moe_sample(o, lp, MOE_DT_BF16 if bf else MOE_DT_F32, ls, M, V, par,
-                                   _ptr(token), _ptr(logprob), _stream(stream)))
+    f = torch.float32
+    par = moe_sample_params(_per_row(temperature, "temperature", f, M), _per_row(top_k, "top_k", torch.int32, M),
+                            _per_row(top_p, "top_p", f, M), _per_row(min_p, "min_p", f, M), _per_row(u, "u", f, M))
+    return _check(lib().moe_sample(o, logits.data_ptr(), MOE_DT_BF16 if bf else MOE_DT_F32, logits.stride(0) if M > 1 else V, M, V,
+                                   par, _per_row(token, "token", torch.int32, M), _per_row(logprob, "logprob", f, M),
+                                   _raw_stream(stream, logits)))
