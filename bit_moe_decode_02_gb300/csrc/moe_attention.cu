@@ -28,19 +28,18 @@
 //    likewise moves only when a score passes it by 2^8 (p' <= 2^9 in f16).
 #include <cstdint>
 
-#include "kv_device.cuh"
-#include "tc_ptx.cuh"
+#include "attn_device.cuh"
 
 namespace moe {
 namespace {
 
+using namespace attn;
+
+constexpr int kPromptRows = 64;           // more rows than this go to the prompt kernel
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an item: (token, query head of the kv head) pairs
 constexpr int kSub = 32;                  // tokens of a block that one warp takes
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -3.0e38f;         // running maximum of a row that has seen no key
-constexpr float kSlack = 8.0f;            // log2 units that a score may pass the kept maximum by
 
 typedef long long i64;
 
@@ -120,25 +119,6 @@ __device__ __forceinline__ void next_item(const AttnArgs& a, const i64* pre, Ite
     find_item(a, pre, it.t0, it);
 }
 
-// Four code bytes -> two f16 pairs, exact.
-template <int FMT>
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
-{
-    if constexpr (FMT == MOE_KV_E4M3) {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi) : "r"(w));
-    } else {
-        // v + 128 below f16's 1024: 0x64uu is 1024 + uu
-        w ^= 0x80808080u;
-        const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-        const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-        __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off), y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-        lo = *reinterpret_cast<uint32_t*>(&x);
-        hi = *reinterpret_cast<uint32_t*>(&y);
-    }
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -147,43 +127,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void group_sync(int id, int threads)
 {
     if (threads == 32)
         __syncwarp();
     else
         asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// One row's final value from its sums: the sink joins the denominator.
-struct Final {
-    float mul, lse;
-};
-__device__ __forceinline__ Final finish(float m, float l, const float* sinks, int hq)
-{
-    float M = m;
-    if (sinks) {
-        const float ms = sinks[hq] * kLog2e;
-        M = fmaxf(m, ms);
-        l = l * ex2(m - M) + (ms == M ? 1.0f : ex2(ms - M));
-    }
-    Final f;
-    f.mul = l > 0.0f ? ex2(m - M) / l : 0.0f;
-    f.lse = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    return f;
 }
 
 // Where row r of an item goes.
@@ -376,24 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
 #pragma unroll
                 for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t x = w[ch][k] & 0x7fffu, y = w[ch][k] >> 16 & 0x7fffu;
-                        big = max(big, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        big = max(big, big_of(w[ch][k]));
                 big = max(big, __shfl_xor_sync(~0u, big, 1));
                 big = max(big, __shfl_xor_sync(~0u, big, 2));
-                // scaled by 2^up the row's largest is in [2^13, 2^15): exact in f16 down to 2^-37 of it
-                const int up = 14 + 127 - max((int)(big >> 7), 1);
-                const float u0 = __uint_as_float((uint32_t)(127 + up / 2) << 23), u1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
-                f[e] = ldexpf(fabsf(a.scale) * kLog2e, -up);
-                const float sg = a.scale < 0.0f ? -u0 : u0;
+                const RowScale rs = row_scale(big, a.scale);
+                f[e] = rs.f;
 #pragma unroll
                 for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float x = __uint_as_float(w[ch][k] << 16) * sg * u1, y = __uint_as_float(w[ch][k] & 0xffff0000u) * sg * u1;
-                        qf[ch * 4 + k / 2][(k & 1) * 2 + e] = pack_f16(x, y);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        qf[ch * 4 + k / 2][(k & 1) * 2 + e] = scale_pair(w[ch][k], rs);
             }
             float o[D / 8][4], m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -478,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                         }
                         if (unit) {
                             vmax = fmaxf(vmax, vs);
-                            const float now = fmaxf(fmaxf(vs, vmax * 9.094947017729282e-13f), 7.52316384526264e-37f);   // 2^-40, 2^-120
+                            const float now = new_unit(vs, vmax);
                             const float ch = ref / now;
                             ref = now;
                             al[0] *= ch;
@@ -732,16 +674,26 @@ cudaError_t prepare_attention_kernels()
     if ((e = prepare_blocks<64, MOE_KV_E4M3>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_INT8>()) != cudaSuccess ||
         (e = prepare_blocks<128, MOE_KV_E4M3>()) != cudaSuccess)
         return e;
-    return prepare_blocks<128, MOE_KV_INT8>();
+    if ((e = prepare_blocks<128, MOE_KV_INT8>()) != cudaSuccess)
+        return e;
+    return prepare_prompt_kernels();
 }
 
-cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
+cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     if (a.c.D == 64)
         a.c.fmt == MOE_KV_E4M3 ? launch_blocks<64, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<64, MOE_KV_INT8>(a, num_sms, s);
     else
         a.c.fmt == MOE_KV_E4M3 ? launch_blocks<128, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<128, MOE_KV_INT8>(a, num_sms, s);
     return cudaGetLastError();
+}
+
+cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    // rows of a (sequence, kv head) on average: the decode kernel reads the cache
+    // once for 16 of them, the prompt kernel once for 256
+    const long long rows = (long long)a.c.n_tokens * a.group / a.c.n_seqs;
+    return rows > kPromptRows ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
 }  // namespace moe

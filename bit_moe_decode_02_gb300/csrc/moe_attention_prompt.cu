@@ -1,0 +1,504 @@
+// moe_attention_prompt.cu -- attention of many tokens over the 8-bit paged cache
+// (prompts and their chunks), on tcgen05.
+//
+// Bound by the tensor pipe: 4 D multiply-adds a (row, key) pair, both products as
+// kind::f16 MMAs of 128 rows with fp32 accumulators in tensor memory.
+//  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
+//    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
+//    the tiles, whatever their number.
+//  - Roles (16 warps).  Warp 0 streams the raw codes of a tile's blocks (bulk copies,
+//    K and V apart) and their scales.  Warps 4-7 make them the f16 operands, in the
+//    canonical K-major order, exactly: K as it lies, V as it lies too (transposed in
+//    the cache).  Warps 1 and 2 issue the MMAs, one for each row tile.  Warps 8-11
+//    and 12-15 do the softmax, a thread a row: while one tile's is under way, the
+//    other's MMAs run.
+//  - Tensor memory: S0 S1 O0 O1, 128 columns each.  P replaces the scores it comes
+//    from, as f16, and is the second product's A operand from there.
+//  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
+//    scores, V's enters the exponent; O is rescaled in tensor memory only where a
+//    row's maximum grows by more than 2^8, or the unit changes.
+#include <cstdint>
+
+#include "attn_device.cuh"
+
+namespace moe {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;                // of a CTA
+constexpr int kKeys = 128;                // of a tile
+constexpr int kRing = 8;                  // tiles whose scales are kept
+
+template <int D, int BLK>
+struct Layout {
+    static constexpr int NB = kKeys / BLK;                // cache blocks of a tile
+    static constexpr int OP = kKeys * D * 2;              // bytes of an f16 operand: Q tile, K tile, V tile
+    static constexpr int RAW = kKeys * D;                 // bytes of a tile's K or V codes
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * OP;
+    static constexpr int OFF_V = OFF_K + 2 * OP;
+    static constexpr int OFF_RAW = OFF_V + 2 * OP;
+    static constexpr int OFF_SC = OFF_RAW + 2 * RAW;      // [kRing][4] (K scale, V scale), K scale < 0: no block
+    static constexpr int OFF_BAR = OFF_SC + kRing * 4 * 8;
+    static constexpr int SMEM = OFF_BAR + 24 * 8;   // 225 KB for D = 128, of 227
+};
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+#define MOE_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define MOE_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+
+// 32 columns of this warp's 32 lanes
+__device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : MOE_R8(r, 0), MOE_R8(r, 8), MOE_R8(r, 16), MOE_R8(r, 24) : "r"(t) : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t t, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+                 ::MOE_I8(r, 0), MOE_I8(r, 8), MOE_I8(r, 16), MOE_I8(r, 24), "r"(t) : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+                 ::MOE_I8(r, 0), MOE_I8(r, 8), "r"(t) : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A CTA's rows: the idx-th group of 256 rows, counted over the sequences and,
+// within one, over its row tiles (the last, which see the most keys, first) and
+// kv heads.  One warp computes it; false: there is no such group.
+struct Work {
+    int b, c0, n, len;
+    int rt, h;
+};
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int idx, Work& w)
+{
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int b0 = 0; b0 < a.c.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        int c0 = 0, n = 0, len = 0;
+        if (b < a.c.n_seqs && !kv::sequence(a.c, b, c0, n, len)) {
+            atomicExch(a.c.status, MOE_ERR_DEVICE_FAULT);
+            n = 0;
+        }
+        const int cnt = (n * a.group + kRows - 1) / kRows * a.c.H;
+        int incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const unsigned hit = __ballot_sync(~0u, idx < base + incl);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            w.b = b0 + src;
+            w.c0 = __shfl_sync(~0u, c0, src);
+            w.n = __shfl_sync(~0u, n, src);
+            w.len = __shfl_sync(~0u, len, src);
+            const int at = idx - base - __shfl_sync(~0u, incl - cnt, src), tiles = __shfl_sync(~0u, cnt, src) / a.c.H;
+            w.rt = tiles - 1 - at / a.c.H;
+            w.h = at % a.c.H;
+            return true;
+        }
+        base += __shfl_sync(~0u, incl, 31);
+    }
+    return false;
+}
+
+template <int D, int FMT, int BLK>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
+{
+    using L = Layout<D, BLK>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* status = a.c.status;
+    Work w;
+    if (!find_work(a, blockIdx.x, w))
+        return;
+
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
+    uint64_t *raw_full = bar, *raw_empty = bar + 2, *k_full = bar + 4, *k_empty = bar + 6, *v_full = bar + 8, *v_empty = bar + 10;
+    uint64_t *s_full = bar + 12, *p_full = bar + 14, *o_full = bar + 16, *q_full = bar + 18;
+    float2* sc = reinterpret_cast<float2*>(sm + L::OFF_SC);
+
+    const int rows = min(w.n * a.group - w.rt * kRows, kRows), na = rows > 128 ? 2 : 1;     // row tiles with rows
+    const int i0 = w.rt * kRows / a.group, i1 = (w.rt * kRows + rows - 1) / a.group;        // first and last token
+    const int pos0 = w.len - w.n + i0, pos1 = w.len - w.n + i1;
+    const int tile0 = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kKeys : 0, nt = pos1 / kKeys - tile0 + 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(raw_full + i, 1);
+            tc::mbar_init(raw_empty + i, 128);
+            tc::mbar_init(k_full + i, 128);
+            tc::mbar_init(k_empty + i, na);
+            tc::mbar_init(v_full + i, 128);
+            tc::mbar_init(v_empty + i, na);
+            tc::mbar_init(s_full + i, 1);
+            tc::mbar_init(p_full + i, 128);
+            tc::mbar_init(o_full + i, 1);
+        }
+        tc::mbar_init(q_full, 256);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::su32(&tmem_base)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        // ---- raw codes and scales of each tile's blocks
+        const int jhi = pos1 / BLK;
+        auto block_of = [&](int t) {
+            const int j = (tile0 + t) * L::NB + lane;
+            return lane < L::NB && t < nt && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
+        };
+        auto scales_of = [&](int id) {
+            return id >= 0 ? *reinterpret_cast<const float2*>(a.c.scales + ((long long)id * a.c.H + w.h) * 2) : make_float2(-1.0f, 0.0f);
+        };
+        int id = block_of(0);
+        float2 s = scales_of(id);
+        for (int t = 0; t < nt; ++t) {
+            if (lane < L::NB)
+                sc[(t % kRing) * 4 + lane] = s;
+            const int next = block_of(t + 1);
+            const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * (BLK * D);
+            const int have = __popc(__ballot_sync(~0u, id >= 0));
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                if (t >= 1)
+                    tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_expect_tx(raw_full + v, (uint32_t)have * (BLK * D));
+                __syncwarp();
+                if (id >= 0)
+                    tc::bulk_copy(sm + L::OFF_RAW + v * L::RAW + lane * (BLK * D), src + v * (BLK * D), BLK * D, raw_full + v);
+            }
+            id = next;
+            s = scales_of(id);
+        }
+    } else if (warp <= 2) {
+        // ---- MMAs of row tile x
+        const int x = warp - 1;
+        if (x < na) {
+            const uint32_t base_desc = (1u << 4) | ((uint32_t)(128 >> 4) << 24);     // fp32 sums, f16 operands, 128 rows
+            const uint32_t id_s = base_desc | ((uint32_t)(kKeys >> 3) << 17), id_o = base_desc | ((uint32_t)(D >> 3) << 17);
+            const uint32_t ts = tmem + x * 128, to = tmem + 256 + x * 128;
+            const uint32_t qa = tc::su32(sm + L::OFF_Q + x * L::OP);
+            auto scores = [&](int t) {
+                const int st = t & 1;
+                tc::mbar_wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
+                tc::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t kb = tc::su32(sm + L::OFF_K + st * L::OP);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(ts, tc::smem_desc(qa + 256 * k, 128, D * 16), tc::smem_desc(kb + 256 * k, 128, D * 16), id_s, k > 0);
+                    tc::tc_commit(s_full + x);
+                    tc::tc_commit(k_empty + st);
+                }
+                __syncwarp();
+            };
+            tc::mbar_wait(q_full, 0, status);
+            scores(0);
+            for (int t = 0; t < nt; ++t) {
+                const int st = t & 1;
+                tc::mbar_wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
+                tc::mbar_wait(p_full + x, (uint32_t)(t & 1), status);
+                tc::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t vb = tc::su32(sm + L::OFF_V + st * L::OP);
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(to, ts + 8 * k, tc::smem_desc(vb + 256 * k, 128, 2048), id_o, t > 0 || k > 0);
+                    tc::tc_commit(v_empty + st);
+                    if (t + 1 == nt)
+                        tc::tc_commit(o_full + x);
+                }
+                __syncwarp();
+                if (t + 1 < nt)
+                    scores(t + 1);
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---- codes -> f16 operands (zero where there is no block)
+        const int ct = tid - 128;
+        for (int t = 0; t < nt; ++t) {
+            const int st = t & 1;
+            const float2* tsc = sc + (t % kRing) * 4;
+            tc::mbar_wait(raw_full, (uint32_t)(t & 1), status);
+            if (t >= 2)
+                tc::mbar_wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
+            {
+                // K: this thread's token; its 16-code pieces in an order that spreads the banks
+                const uint8_t* raw = sm + L::OFF_RAW + ct * D;
+                uint8_t* out = sm + L::OFF_K + st * L::OP + (ct >> 3) * (D * 16) + (ct & 7) * 16;
+                const bool have = tsc[ct / BLK].x >= 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const int q = (i + ct / (128 / D)) & (D / 16 - 1);
+                    uint4 c = make_uint4(0, 0, 0, 0);
+                    uint32_t h[8];
+                    if (have)
+                        c = *reinterpret_cast<const uint4*>(raw + 16 * q);
+                    to_f16<FMT>(c.x, h[0], h[1]);
+                    to_f16<FMT>(c.y, h[2], h[3]);
+                    to_f16<FMT>(c.z, h[4], h[5]);
+                    to_f16<FMT>(c.w, h[6], h[7]);
+                    *reinterpret_cast<uint4*>(out + 256 * q) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(out + 256 * q + 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(k_full + st);
+            tc::mbar_arrive(raw_empty);
+
+            tc::mbar_wait(raw_full + 1, (uint32_t)(t & 1), status);
+            if (t >= 2)
+                tc::mbar_wait(v_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
+            {
+                // V: this thread's d, 16 tokens at a time
+                const int d = ct & (D - 1), part = ct / D;
+                const uint8_t* raw = sm + L::OFF_RAW + L::RAW + d * BLK;
+                uint8_t* out = sm + L::OFF_V + st * L::OP + (d >> 3) * 2048 + (d & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const int q = ((i + d / (128 / BLK)) & (D / 16 - 1)) + part * (D / 16);
+                    const int b = q * 16 / BLK;
+                    uint4 c = make_uint4(0, 0, 0, 0);
+                    uint32_t h[8];
+                    if (tsc[b].x >= 0.0f)
+                        c = *reinterpret_cast<const uint4*>(raw + b * (BLK * D) + q * 16 % BLK);
+                    to_f16<FMT>(c.x, h[0], h[1]);
+                    to_f16<FMT>(c.y, h[2], h[3]);
+                    to_f16<FMT>(c.z, h[4], h[5]);
+                    to_f16<FMT>(c.w, h[6], h[7]);
+                    *reinterpret_cast<uint4*>(out + 256 * q) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(out + 256 * q + 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(v_full + st);
+            tc::mbar_arrive(raw_empty + 1);
+        }
+    } else if (warp >= 8) {
+        // ---- softmax: a thread a row
+        const int x = (warp - 8) >> 2, r = tid & 127, row = w.rt * kRows + x * 128 + r;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // this warp's quarter of the tensor memory's lanes
+        const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
+        const bool in = x * 128 + r < rows;
+        const int i = row / a.group, hq = w.h * a.group + row % a.group;
+        float f;
+        {
+            // the query row: f16, scaled, in the canonical order
+            uint32_t big = 0;
+            const uint4* q = reinterpret_cast<const uint4*>(a.q + (long long)(w.c0 + i) * a.q_stride + (long long)hq * D);
+            if (in)
+#pragma unroll 4
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 v = q[k];
+                    big = max(max(max(big, big_of(v.x)), max(big_of(v.y), big_of(v.z))), big_of(v.w));
+                }
+            const RowScale rs = row_scale(big, a.scale);
+            f = rs.f;
+            uint8_t* out = sm + L::OFF_Q + x * L::OP + (r >> 3) * (D * 16) + (r & 7) * 16;
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+                const uint4 v = in ? q[k] : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(out + 128 * k) =
+                    make_uint4(scale_pair(v.x, rs), scale_pair(v.y, rs), scale_pair(v.z, rs), scale_pair(v.w, rs));
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(q_full);
+        }
+        if (x < na) {
+            const int phi = in ? w.len - w.n + i : -1, plo = in && a.window > 0 ? phi - a.window + 1 : 0;
+            // positions that all rows of this tile see
+            const int all_hi = w.len - w.n + (w.rt * kRows + x * 128) / a.group;
+            const int all_lo = a.window > 0 ? w.len - w.n + (w.rt * kRows + min(rows, x * 128 + 128) - 1) / a.group - a.window + 1 : 0;
+            float m = kNone, l = 0.0f, ref = 0.0f, vmax = 0.0f;
+            for (int t = 0; t < nt; ++t) {
+                const int p0 = (tile0 + t) * kKeys;
+                tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
+                tc::tc_fence_after();
+                float ks[L::NB], vs[L::NB], top = 0.0f;
+                bool whole = p0 >= all_lo && p0 + kKeys - 1 <= all_hi;
+                bool unit = false;
+#pragma unroll
+                for (int b = 0; b < L::NB; ++b) {
+                    const float2 v = sc[(t % kRing) * 4 + b];
+                    ks[b] = v.x;
+                    vs[b] = v.y;
+                    top = fmaxf(top, v.y);
+                    whole = whole && v.x >= 0.0f;
+                }
+                unit = !(top <= 2.0f * ref && top >= 0.5f * ref);
+                // scores of 32 keys of this row, -inf where it does not see them
+                auto take = [&](int ch, uint32_t (&v)[32]) {
+                    tm_ld32(ts + 32 * ch, v);
+                    tc::tc_wait_ld();
+                    if (!whole) {
+                        const bool have = ks[ch * 32 / BLK] >= 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int p = p0 + 32 * ch + k;
+                            if (!have || p < plo || p > phi)
+                                v[k] = 0xff800000u;
+                        }
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t v[32];
+                    take(ch, v);
+                    float y = __uint_as_float(v[0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k)
+                        y = fmaxf(y, __uint_as_float(v[k]));
+                    mx = fmaxf(mx, y * fmaxf(ks[ch * 32 / BLK] * f, 1e-37f));
+                }
+                if (__any_sync(~0u, unit || mx > m + kSlack)) {
+                    const float mn = fmaxf(m, mx);
+                    float al = ex2(m - mn);
+                    m = mn;
+                    l *= al;
+                    if (unit) {
+                        vmax = fmaxf(vmax, top);
+                        const float now = new_unit(top, vmax);
+                        al *= ref / now;
+                        ref = now;
+                    }
+                    if (t > 0)
+#pragma unroll
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t v[32];
+                            tm_ld32(to + 32 * ch, v);
+                            tc::tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                            tm_st32(to + 32 * ch, v);
+                        }
+                }
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    const int b = ch * 32 / BLK;
+                    const float c = fmaxf(ks[b] * f, 1e-37f), ratio = fmaxf(vs[b] / ref, 8.673617379884035e-19f);   // 2^-60
+                    const float mm = m - __log2f(ratio);
+                    uint32_t v[32], p[16];
+                    take(ch, v);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float y = ex2(fmaf(__uint_as_float(v[k]), c, -mm)), z = ex2(fmaf(__uint_as_float(v[k + 1]), c, -mm));
+                        sum += y + z;
+                        p[k / 2] = pack_f16(y, z);
+                    }
+                    l += sum / ratio;
+                    tm_st16(ts + 16 * ch, p);
+                }
+                tm_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(p_full + x);
+            }
+            // ---- the row's result
+            tc::mbar_wait(o_full + x, 0, status);
+            tc::tc_fence_after();
+            const Final fin = finish(m, l, a.sinks, hq < a.q_heads ? hq : 0);
+            const float mul = fin.mul * ref;
+            uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D;
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t v[32];
+                tm_ld32(to + 32 * ch, v);
+                tc::tc_wait_ld();
+                if (in)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = tc::f2bf16_rne(__uint_as_float(v[k + 2 * e]) * mul) |
+                                   (uint32_t)tc::f2bf16_rne(__uint_as_float(v[k + 2 * e + 1]) * mul) << 16;
+                        *reinterpret_cast<uint4*>(out + 32 * ch + k) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+            }
+            if (a.lse && in)
+                a.lse[(long long)(w.c0 + i) * a.q_heads + hq] = fin.lse;
+        }
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == 3)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+typedef void (*Kernel)(AttnArgs);
+
+template <int D, int FMT>
+Kernel pick(int blk)
+{
+    return blk == 32 ? prompt_attn_kernel<D, FMT, 32> : blk == 64 ? prompt_attn_kernel<D, FMT, 64> : prompt_attn_kernel<D, FMT, 128>;
+}
+Kernel kernel_for(int d, int fmt, int blk)
+{
+    if (d == 64)
+        return fmt == MOE_KV_E4M3 ? pick<64, MOE_KV_E4M3>(blk) : pick<64, MOE_KV_INT8>(blk);
+    return fmt == MOE_KV_E4M3 ? pick<128, MOE_KV_E4M3>(blk) : pick<128, MOE_KV_INT8>(blk);
+}
+int smem_of(int d) { return d == 64 ? Layout<64, 64>::SMEM : Layout<128, 64>::SMEM; }   // whatever the block
+
+}  // namespace
+
+cudaError_t prepare_prompt_kernels()
+{
+    for (int d = 64; d <= 128; d *= 2)
+        for (int fmt : {MOE_KV_E4M3, MOE_KV_INT8})
+            for (int blk = 32; blk <= 128; blk *= 2) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel_for(d, fmt, blk), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(d));
+                if (e != cudaSuccess)
+                    return e;
+            }
+    return cudaSuccess;
+}
+
+cudaError_t launch_attention_prompt(const AttnArgs& a, int, cudaStream_t s)
+{
+    // an upper bound on the groups of 256 rows: CTAs beyond the last one end at once
+    const long long groups = ((long long)a.c.n_tokens * a.group / kRows + a.c.n_seqs) * a.c.H;
+    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)groups, kThreads, smem_of(a.c.D), s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

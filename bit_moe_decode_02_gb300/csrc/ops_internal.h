@@ -52,6 +52,8 @@ struct AttnArgs {
     uint8_t* ws;
 };
 cudaError_t prepare_attention_kernels();
+cudaError_t prepare_prompt_kernels();
+cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s);
 
 struct LinearArgs {
