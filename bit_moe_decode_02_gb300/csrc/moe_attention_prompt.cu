@@ -82,7 +82,42 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&r)[16])
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
                  ::MOE_I8(r, 0), MOE_I8(r, 8), "r"(t) : "memory");
 }
+#define MOE_IO8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+// Waits for this thread's loads; names the registers, so that no use of them is moved above it.
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : MOE_IO8(r, 0), MOE_IO8(r, 8), MOE_IO8(r, 16), MOE_IO8(r, 24)::"memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+          "l"(reinterpret_cast<const unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // A CTA's rows: the idx-th group of 256 rows, counted over the sequences and,
 // within one, over its row tiles (the last, which see the most keys, first) and
@@ -349,24 +384,68 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 const int p0 = (tile0 + t) * kKeys;
                 tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
-                float ks[L::NB], vs[L::NB], top = 0.0f;
+                float top = 0.0f;
                 bool whole = p0 >= all_lo && p0 + kKeys - 1 <= all_hi;
-                bool unit = false;
 #pragma unroll
                 for (int b = 0; b < L::NB; ++b) {
                     const float2 v = sc[(t % kRing) * 4 + b];
-                    ks[b] = v.x;
-                    vs[b] = v.y;
                     top = fmaxf(top, v.y);
                     whole = whole && v.x >= 0.0f;
                 }
-                unit = !(top <= 2.0f * ref && top >= 0.5f * ref);
-                // scores of 32 keys of this row, -inf where it does not see them
-                auto take = [&](int ch, uint32_t (&v)[32]) {
-                    tm_ld32(ts + 32 * ch, v);
-                    tc::tc_wait_ld();
+                uint32_t buf[2][32];
+                tm_ld32(ts, buf[0]);
+                // O, and what this tile has put into P so far, times al: a new maximum or a new unit
+                auto rescale = [&](float al, int done) {
+                    if (t > 0)
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t v[32];
+                            tm_ld32(to + 32 * ch, v);
+                            tm_wait_ld(v);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                            tm_st32(to + 32 * ch, v);
+                        }
+                    if (done) {
+                        tm_wait_st();
+                        const __half2 a2 = __float2half2_rn(al);
+#pragma unroll 1
+                        for (int ch = 0; ch < done; ch += 2) {
+                            uint32_t v[32];
+                            tm_ld32(ts + 16 * ch, v);
+                            tm_wait_ld(v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&v[k]), a2), z = __hmul2(*reinterpret_cast<__half2*>(&v[k + 16]), a2);
+                                v[k] = *reinterpret_cast<uint32_t*>(&y);
+                                if (ch + 1 < done)
+                                    v[k + 16] = *reinterpret_cast<uint32_t*>(&z);
+                            }
+                            tm_st32(ts + 16 * ch, v);
+                        }
+                        tm_wait_st();
+                    }
+                };
+                if (!(top <= 2.0f * ref && top >= 0.5f * ref)) {        // the same for the whole warp
+                    vmax = fmaxf(vmax, top);
+                    const float now = new_unit(top, vmax);
+                    rescale(ref / now, 0);
+                    ref = now;
+                }
+                const float iref = rcp(ref);
+                float2 sum[L::NB];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t(&v)[32] = buf[ch & 1];
+                    tm_wait_ld(v);
+                    if (ch < 3)
+                        tm_ld32(ts + 32 * (ch + 1), buf[ch + 1 & 1]);
+                    const int b = ch * 32 / BLK;
+                    const float2 kv = sc[(t % kRing) * 4 + b];
+                    const float c = fmaxf(kv.x * f, 1e-37f);
                     if (!whole) {
-                        const bool have = ks[ch * 32 / BLK] >= 0.0f;
+                        const bool have = kv.x >= 0.0f;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const int p = p0 + 32 * ch + k;
@@ -374,58 +453,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                                 v[k] = 0xff800000u;
                         }
                     }
-                };
-                float mx = -INFINITY;
+                    float y[4];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t v[32];
-                    take(ch, v);
-                    float y = __uint_as_float(v[0]);
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 4]));
 #pragma unroll
-                    for (int k = 1; k < 32; ++k)
-                        y = fmaxf(y, __uint_as_float(v[k]));
-                    mx = fmaxf(mx, y * fmaxf(ks[ch * 32 / BLK] * f, 1e-37f));
-                }
-                if (__any_sync(~0u, unit || mx > m + kSlack)) {
-                    const float mn = fmaxf(m, mx);
-                    float al = ex2(m - mn);
-                    m = mn;
-                    l *= al;
-                    if (unit) {
-                        vmax = fmaxf(vmax, top);
-                        const float now = new_unit(top, vmax);
-                        al *= ref / now;
-                        ref = now;
+                    for (int k = 8; k < 32; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = fmaxf(fmaxf(y[e], __uint_as_float(v[k + e])), __uint_as_float(v[k + e + 4]));
+                    const float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * c;
+                    if (__any_sync(~0u, mx > m + kSlack)) {
+                        const float mn = fmaxf(m, mx), al = ex2(m - mn);
+                        if (ch < 3)
+                            tm_wait_ld(buf[ch + 1 & 1]);
+                        rescale(al, ch);
+                        m = mn;
+                        l *= al;
+#pragma unroll
+                        for (int e = 0; e <= b; ++e)
+                            if (e * BLK < ch * 32) {
+                                sum[e].x *= al;
+                                sum[e].y *= al;
+                            }
                     }
-                    if (t > 0)
-#pragma unroll
-                        for (int ch = 0; ch < D / 32; ++ch) {
-                            uint32_t v[32];
-                            tm_ld32(to + 32 * ch, v);
-                            tc::tc_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
-                            tm_st32(to + 32 * ch, v);
-                        }
-                }
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    const int b = ch * 32 / BLK;
-                    const float c = fmaxf(ks[b] * f, 1e-37f), ratio = fmaxf(vs[b] / ref, 8.673617379884035e-19f);   // 2^-60
-                    const float mm = m - __log2f(ratio);
-                    uint32_t v[32], p[16];
-                    take(ch, v);
-                    float sum = 0.0f;
+                    const float off = lg2(fmaxf(kv.y * iref, 8.673617379884035e-19f)) - m;    // 2^-60
+                    const float2 cc = make_float2(c, c), oo = make_float2(off, off);
+                    uint32_t p[16];
+                    float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const float y = ex2(fmaf(__uint_as_float(v[k]), c, -mm)), z = ex2(fmaf(__uint_as_float(v[k + 1]), c, -mm));
-                        sum += y + z;
-                        p[k / 2] = pack_f16(y, z);
+                        float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
+                        z.x = ex2(z.x);
+                        z.y = ex2(z.y);
+                        part = k ? add2(part, z) : z;
+                        p[k / 2] = pack_f16(z.x, z.y);
                     }
-                    l += sum / ratio;
+                    sum[b] = ch * 32 % BLK ? add2(sum[b], part) : part;
                     tm_st16(ts + 16 * ch, p);
                 }
+#pragma unroll
+                for (int b = 0; b < L::NB; ++b)
+                    l += (sum[b].x + sum[b].y) * rcp(fmaxf(sc[(t % kRing) * 4 + b].y * iref, 8.673617379884035e-19f));
                 tm_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(p_full + x);
