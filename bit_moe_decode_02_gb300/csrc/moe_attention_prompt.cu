@@ -9,7 +9,7 @@
 //  - Roles (16 warps).  Warp 0 streams the raw codes of a tile's blocks (bulk copies,
 //    K and V apart) and their scales.  Warps 4-7 make them the f16 operands, in the
 //    canonical K-major order, exactly: K as it lies, V as it lies too (transposed in
-//    the cache).  Warps 1 and 2 issue the MMAs, one for each row tile.  Warps 8-11
+//    the cache).  Warp 1 issues the MMAs.  Warps 8-11
 //    and 12-15 do the softmax, a thread a row: while one tile's is under way, the
 //    other's MMAs run.
 //  - Tensor memory: S0 S1 O0 O1, 128 columns each.  P replaces the scores it comes
@@ -240,47 +240,47 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             id = next;
             s = scales_of(id);
         }
-    } else if (warp <= 2) {
-        // ---- MMAs of row tile x
-        const int x = warp - 1;
-        if (x < na) {
-            const uint32_t base_desc = (1u << 4) | ((uint32_t)(128 >> 4) << 24);     // fp32 sums, f16 operands, 128 rows
-            const uint32_t id_s = base_desc | ((uint32_t)(kKeys >> 3) << 17), id_o = base_desc | ((uint32_t)(D >> 3) << 17);
-            const uint32_t ts = tmem + x * 128, to = tmem + 256 + x * 128;
-            const uint32_t qa = tc::su32(sm + L::OFF_Q + x * L::OP);
-            auto scores = [&](int t) {
-                const int st = t & 1;
-                tc::mbar_wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
-                tc::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t kb = tc::su32(sm + L::OFF_K + st * L::OP);
+    } else if (warp == 1) {
+        // ---- MMAs, the row tiles in turn: P V of a tile of keys and the scores of the
+        // next go out as that row tile's P is ready, so that its softmax and the other's
+        // MMAs come to overlap
+        const uint32_t base_desc = (1u << 4) | ((uint32_t)(128 >> 4) << 24);     // fp32 sums, f16 operands, 128 rows
+        const uint32_t id_s = base_desc | ((uint32_t)(kKeys >> 3) << 17), id_o = base_desc | ((uint32_t)(D >> 3) << 17);
+        const uint64_t qd = tc::smem_desc(tc::su32(sm + L::OFF_Q), 128, D * 16), kd = tc::smem_desc(tc::su32(sm + L::OFF_K), 128, D * 16);
+        const uint64_t vd = tc::smem_desc(tc::su32(sm + L::OFF_V), 128, 2048);
+        auto scores = [&](int x, int t) {
+            const int st = t & 1;
+            tc::mbar_wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
+            tc::tc_fence_after();
+            if (lane == 0) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(ts, tc::smem_desc(qa + 256 * k, 128, D * 16), tc::smem_desc(kb + 256 * k, 128, D * 16), id_s, k > 0);
-                    tc::tc_commit(s_full + x);
-                    tc::tc_commit(k_empty + st);
-                }
-                __syncwarp();
-            };
-            tc::mbar_wait(q_full, 0, status);
-            scores(0);
-            for (int t = 0; t < nt; ++t) {
-                const int st = t & 1;
-                tc::mbar_wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tmem + x * 128, qd + (x * L::OP + 256 * k >> 4), kd + (st * L::OP + 256 * k >> 4), id_s, k > 0);
+                tc::tc_commit(s_full + x);
+                tc::tc_commit(k_empty + st);
+            }
+            __syncwarp();
+        };
+        tc::mbar_wait(q_full, 0, status);
+        for (int x = 0; x < na; ++x)
+            scores(x, 0);
+        for (int t = 0; t < nt; ++t) {
+            const int st = t & 1;
+            tc::mbar_wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
+            for (int x = 0; x < na; ++x) {
                 tc::mbar_wait(p_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t vb = tc::su32(sm + L::OFF_V + st * L::OP);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(to, ts + 8 * k, tc::smem_desc(vb + 256 * k, 128, 2048), id_o, t > 0 || k > 0);
+                        mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
                     tc::tc_commit(v_empty + st);
                     if (t + 1 == nt)
                         tc::tc_commit(o_full + x);
                 }
                 __syncwarp();
                 if (t + 1 < nt)
-                    scores(t + 1);
+                    scores(x, t + 1);
             }
         }
     } else if (warp >= 4 && warp < 8) {
