@@ -45,17 +45,31 @@ struct Layout {
     static constexpr int SMEM = OFF_BAR + 24 * 8;   // 225 KB for D = 128, of 227
 };
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The whole warp executes these, one elected lane (`one` != 0) issues: outside a
+// branch the operands, the same in all lanes, stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(tc::su32(bar)), "r"(one) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(one));
+    return one;
 }
 
 #define MOE_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
@@ -248,16 +262,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         const uint32_t id_s = base_desc | ((uint32_t)(kKeys >> 3) << 17), id_o = base_desc | ((uint32_t)(D >> 3) << 17);
         const uint64_t qd = tc::smem_desc(tc::su32(sm + L::OFF_Q), 128, D * 16), kd = tc::smem_desc(tc::su32(sm + L::OFF_K), 128, D * 16);
         const uint64_t vd = tc::smem_desc(tc::su32(sm + L::OFF_V), 128, 2048);
+        const uint32_t one = elect_one();
         auto scores = [&](int x, int t) {
             const int st = t & 1;
             tc::mbar_wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
             tc::tc_fence_after();
-            if (lane == 0) {
+            {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + x * 128, qd + (x * L::OP + 256 * k >> 4), kd + (st * L::OP + 256 * k >> 4), id_s, k > 0);
-                tc::tc_commit(s_full + x);
-                tc::tc_commit(k_empty + st);
+                    mma_ss(one, tmem + x * 128, qd + (x * L::OP + 256 * k >> 4), kd + (st * L::OP + 256 * k >> 4), id_s, k > 0);
+                commit(one, s_full + x);
+                commit(one, k_empty + st);
             }
             __syncwarp();
         };
@@ -270,13 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             for (int x = 0; x < na; ++x) {
                 tc::mbar_wait(p_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
-                if (lane == 0) {
+                {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
-                    tc::tc_commit(v_empty + st);
+                        mma_ts(one, tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
+                    commit(one, v_empty + st);
                     if (t + 1 == nt)
-                        tc::tc_commit(o_full + x);
+                        commit(one, o_full + x);
                 }
                 __syncwarp();
                 if (t + 1 < nt)
