@@ -120,6 +120,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float lg2(float x)
 {
     float y;
@@ -201,13 +207,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(raw_full + i, 1);
-            tc::mbar_init(raw_empty + i, 128);
-            tc::mbar_init(k_full + i, 128);
+            tc::mbar_init(raw_empty + i, 4);
+            tc::mbar_init(k_full + i, 4);
             tc::mbar_init(k_empty + i, na);
-            tc::mbar_init(v_full + i, 128);
+            tc::mbar_init(v_full + i, 4);
             tc::mbar_init(v_empty + i, na);
             tc::mbar_init(s_full + i, 1);
-            tc::mbar_init(p_full + i, 128);
+            tc::mbar_init(p_full + i, 4);
             tc::mbar_init(o_full + i, 1);
         }
         tc::mbar_init(q_full, 256);
@@ -301,6 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     } else if (warp >= 4 && warp < 8) {
         // ---- codes -> f16 operands (zero where there is no block)
         const int ct = tid - 128;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        // a warp's writes (and reads of the raw codes) are done
+        auto arrive = [&](uint64_t* full, uint64_t* empty) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(full);
+                tc::mbar_arrive(empty);
+            }
+        };
         for (int t = 0; t < nt; ++t) {
             const int st = t & 1;
             const float2* tsc = sc + (t % kRing) * 4;
@@ -312,13 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 const uint8_t* raw = sm + L::OFF_RAW + ct * D;
                 uint8_t* out = sm + L::OFF_K + st * L::OP + (ct >> 3) * (D * 16) + (ct & 7) * 16;
                 const bool have = tsc[ct / BLK].x >= 0.0f;
+                uint4 w[D / 16];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    w[i] = *reinterpret_cast<const uint4*>(raw + 16 * ((i + ct / (128 / D)) & (D / 16 - 1)));
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int q = (i + ct / (128 / D)) & (D / 16 - 1);
-                    uint4 c = make_uint4(0, 0, 0, 0);
+                    const uint4 c = have ? w[i] : zero;
                     uint32_t h[8];
-                    if (have)
-                        c = *reinterpret_cast<const uint4*>(raw + 16 * q);
                     to_f16<FMT>(c.x, h[0], h[1]);
                     to_f16<FMT>(c.y, h[2], h[3]);
                     to_f16<FMT>(c.z, h[4], h[5]);
@@ -327,9 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     *reinterpret_cast<uint4*>(out + 256 * q + 128) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
             }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(k_full + st);
-            tc::mbar_arrive(raw_empty);
+            arrive(k_full + st, raw_empty);
 
             tc::mbar_wait(raw_full + 1, (uint32_t)(t & 1), status);
             if (t >= 2)
@@ -339,14 +355,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 const int d = ct & (D - 1), part = ct / D;
                 const uint8_t* raw = sm + L::OFF_RAW + L::RAW + d * BLK;
                 uint8_t* out = sm + L::OFF_V + st * L::OP + (d >> 3) * 2048 + (d & 7) * 16;
+                uint4 w[D / 16];
+                bool have[L::NB];
+#pragma unroll
+                for (int b = 0; b < L::NB; ++b)
+                    have[b] = tsc[b].x >= 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int q = ((i + d / (128 / BLK)) & (D / 16 - 1)) + part * (D / 16);
-                    const int b = q * 16 / BLK;
-                    uint4 c = make_uint4(0, 0, 0, 0);
+                    w[i] = *reinterpret_cast<const uint4*>(raw + q * 16 / BLK * (BLK * D) + q * 16 % BLK);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const int q = ((i + d / (128 / BLK)) & (D / 16 - 1)) + part * (D / 16);
+                    bool ok = have[0];
+#pragma unroll
+                    for (int b = 1; b < L::NB; ++b)
+                        ok = q * 16 / BLK == b ? have[b] : ok;
+                    const uint4 c = ok ? w[i] : zero;
                     uint32_t h[8];
-                    if (tsc[b].x >= 0.0f)
-                        c = *reinterpret_cast<const uint4*>(raw + b * (BLK * D) + q * 16 % BLK);
                     to_f16<FMT>(c.x, h[0], h[1]);
                     to_f16<FMT>(c.y, h[2], h[3]);
                     to_f16<FMT>(c.z, h[4], h[5]);
@@ -355,9 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     *reinterpret_cast<uint4*>(out + 256 * q + 128) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
             }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(v_full + st);
-            tc::mbar_arrive(raw_empty + 1);
+            arrive(v_full + st, raw_empty + 1);
         }
     } else if (warp >= 8) {
         // ---- softmax: a thread a row
@@ -409,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 }
                 uint32_t buf[2][32];
                 tm_ld32(ts, buf[0]);
+                tm_ld32(ts + 32, buf[1]);
                 // O, and what this tile has put into P so far, times al: a new maximum or a new unit
                 auto rescale = [&](float al, int done) {
                     if (t > 0)
@@ -451,68 +477,81 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 const float iref = rcp(ref);
                 float2 sum[L::NB];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t(&v)[32] = buf[ch & 1];
-                    tm_wait_ld(v);
-                    if (ch < 3)
-                        tm_ld32(ts + 32 * (ch + 1), buf[ch + 1 & 1]);
-                    const int b = ch * 32 / BLK;
-                    const float2 kv = sc[(t % kRing) * 4 + b];
-                    const float c = fmaxf(kv.x * f, 1e-37f);
-                    if (!whole) {
-                        const bool have = kv.x >= 0.0f;
+                for (int half = 0; half < 2; ++half) {
+                    // 64 keys: their maximum, then their probabilities; the next scores come in meanwhile
+                    float mx = -INFINITY, c[2];
+                    tm_wait_ld(buf[0]);
+                    tm_wait_ld(buf[1]);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int p = p0 + 32 * ch + k;
-                            if (!have || p < plo || p > phi)
-                                v[k] = 0xff800000u;
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t(&v)[32] = buf[g];
+                        const int ch = 2 * half + g;
+                        const float2 kv = sc[(t % kRing) * 4 + ch * 32 / BLK];
+                        c[g] = fmaxf(kv.x * f, 1e-37f);
+                        if (!whole) {
+                            const bool have = kv.x >= 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const int p = p0 + 32 * ch + k;
+                                if (!have || p < plo || p > phi)
+                                    v[k] = 0xff800000u;
+                            }
                         }
+                        float y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 4]));
+#pragma unroll
+                        for (int k = 8; k < 32; k += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = max3(y[e], __uint_as_float(v[k + e]), __uint_as_float(v[k + e + 4]));
+                        mx = fmaxf(mx, max3(fmaxf(y[0], y[1]), y[2], y[3]) * c[g]);
                     }
-                    float y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 4]));
-#pragma unroll
-                    for (int k = 8; k < 32; k += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = fmaxf(fmaxf(y[e], __uint_as_float(v[k + e])), __uint_as_float(v[k + e + 4]));
-                    const float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * c;
                     if (__any_sync(~0u, mx > m + kSlack)) {
                         const float mn = fmaxf(m, mx), al = ex2(m - mn);
-                        if (ch < 3)
-                            tm_wait_ld(buf[ch + 1 & 1]);
-                        rescale(al, ch);
+                        rescale(al, 2 * half);
                         m = mn;
                         l *= al;
+                        if (half)
 #pragma unroll
-                        for (int e = 0; e <= b; ++e)
-                            if (e * BLK < ch * 32) {
-                                sum[e].x *= al;
-                                sum[e].y *= al;
-                            }
+                            for (int e = 0; e < L::NB; ++e)
+                                if (e * BLK < 64) {
+                                    sum[e].x *= al;
+                                    sum[e].y *= al;
+                                }
                     }
-                    const float off = lg2(fmaxf(kv.y * iref, 8.673617379884035e-19f)) - m;    // 2^-60
-                    const float2 cc = make_float2(c, c), oo = make_float2(off, off);
-                    uint32_t p[16];
-                    float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
-                        z.x = ex2(z.x);
-                        z.y = ex2(z.y);
-                        part = k ? add2(part, z) : z;
-                        p[k / 2] = pack_f16(z.x, z.y);
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t(&v)[32] = buf[g];
+                        const int ch = 2 * half + g, b = ch * 32 / BLK;
+                        const float off = lg2(fmaxf(sc[(t % kRing) * 4 + b].y * iref, 8.673617379884035e-19f)) - m;    // 2^-60
+                        const float2 cc = make_float2(c[g], c[g]), oo = make_float2(off, off);
+                        uint32_t p[16];
+                        float2 part[2];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
+                            z.x = ex2(z.x);
+                            z.y = ex2(z.y);
+                            part[k / 2 & 1] = k > 2 ? add2(part[k / 2 & 1], z) : z;
+                            p[k / 2] = pack_f16(z.x, z.y);
+                        }
+                        if (half == 0)
+                            tm_ld32(ts + 64 + 32 * g, v);
+                        const float2 both = add2(part[0], part[1]);
+                        sum[b] = ch * 32 % BLK ? add2(sum[b], both) : both;
+                        tm_st16(ts + 16 * ch, p);
                     }
-                    sum[b] = ch * 32 % BLK ? add2(sum[b], part) : part;
-                    tm_st16(ts + 16 * ch, p);
                 }
 #pragma unroll
                 for (int b = 0; b < L::NB; ++b)
                     l += (sum[b].x + sum[b].y) * rcp(fmaxf(sc[(t % kRing) * 4 + b].y * iref, 8.673617379884035e-19f));
                 tm_wait_st();
                 tc::tc_fence_before();
-                tc::mbar_arrive(p_full + x);
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(p_full + x);
             }
             // ---- the row's result
             tc::mbar_wait(o_full + x, 0, status);
