@@ -80,10 +80,11 @@ __device__ __forceinline__ int physical(const KvView& c, int b, int j)
 // The scale of a block whose largest finite magnitude is amax.  INT8:
 // amax / 127.  E4M3: the smallest power of two with amax <= 448 * scale, so
 // that dividing by it is exact and nothing saturates.
-__device__ __forceinline__ float block_scale(float amax, int fmt)
+template <int FMT>
+__device__ __forceinline__ float block_scale(float amax)
 {
     const float a = fmaxf(amax, kTiny);
-    if (fmt == MOE_KV_INT8)
+    if constexpr (FMT == MOE_KV_INT8)
         return __fdiv_rn(a, 127.0f);
     const uint32_t u = __float_as_uint(a);
     return __uint_as_float(((u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u)) << 23);   // 448 = 1.75 * 2^8
@@ -91,18 +92,19 @@ __device__ __forceinline__ float block_scale(float amax, int fmt)
 
 // Four values, already divided by their scale, -> four code bytes, each value
 // rounded once to nearest even, saturating; NaN gives 0.
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, int fmt)
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
 {
     a = a == a ? a : 0.0f;
     b = b == b ? b : 0.0f;
     c = c == c ? c : 0.0f;
     d = d == d ? d : 0.0f;
-    if (fmt == MOE_KV_INT8) {
+    if constexpr (FMT == MOE_KV_INT8) {
         const int i0 = __float2int_rn(fminf(fmaxf(a, -127.0f), 127.0f)), i1 = __float2int_rn(fminf(fmaxf(b, -127.0f), 127.0f));
         const int i2 = __float2int_rn(fminf(fmaxf(c, -127.0f), 127.0f)), i3 = __float2int_rn(fminf(fmaxf(d, -127.0f), 127.0f));
         return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
     }
-    uint32_t r;
+    uint32_t r = 0;
     asm("{\n\t.reg .b16 lo, hi;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
@@ -112,9 +114,10 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
 }
 
 // Four code bytes -> their values in units of the scale (exact).
-__device__ __forceinline__ void decode4(uint32_t w, int fmt, float (&v)[4])
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4])
 {
-    if (fmt == MOE_KV_INT8) {
+    if constexpr (FMT == MOE_KV_INT8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             v[i] = (float)(int8_t)(w >> (8 * i));
@@ -129,6 +132,14 @@ __device__ __forceinline__ void decode4(uint32_t w, int fmt, float (&v)[4])
     v[1] = p.y;
     v[2] = q.x;
     v[3] = q.y;
+}
+
+// Two values -> bf16, nearest even, the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 }  // namespace kv

@@ -22,13 +22,14 @@ constexpr int kWriteThreads = 128;
 // holds earlier tokens, whose codes are rounded again where it grew), then
 // every new value is divided by it and rounded once.
 // Memory-bound: 2 bytes in and 1 out per value.
+template <int FMT, int D, int blk>
 __global__ void __launch_bounds__(kWriteThreads)
 kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __restrict__ vsrc, long long kstride,
                 long long vstride)
 {
     extern __shared__ uint32_t tile[];   // [blk][D/2 + 1] words of two bf16
     __shared__ float red[kWriteThreads / 32];
-    const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, D = c.D, blk = c.blk;
+    const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
     kv::Touched t;
     if (!kv::find_touched(c, blockIdx.x, t))
         return;
@@ -40,7 +41,7 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
     const uint16_t* src = which ? vsrc : ksrc;
     const long long stride = which ? vstride : kstride;
     src += (long long)(t.c0 - start + lo) * stride + (long long)h * D;
-    const int pitch = D / 2 + 1, vec = D / 8;
+    constexpr int pitch = D / 2 + 1, vec = D / 8;
 
     float amax = 0.0f;
     for (int i = tid; i < (hi - lo) * vec; i += kWriteThreads) {
@@ -69,7 +70,7 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
 
     float* sp = c.scales + ((long long)id * c.H + h) * 2 + which;
     const bool fresh = lo == 0;
-    float scale = kv::block_scale(amax, c.fmt), ratio = 0.0f;
+    float scale = kv::block_scale<FMT>(amax), ratio = 0.0f;
     const float old = fresh ? 0.0f : *sp;
     const bool grown = !fresh && scale > old;
     if (!fresh && !grown)
@@ -91,10 +92,10 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
             if (r < lo) {
                 const uint2 was = *p;
                 float v[4], u[4];
-                kv::decode4(was.x, c.fmt, v);
-                kv::decode4(was.y, c.fmt, u);
-                o.x = kv::encode4(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio, c.fmt);
-                o.y = kv::encode4(u[0] * ratio, u[1] * ratio, u[2] * ratio, u[3] * ratio, c.fmt);
+                kv::decode4<FMT>(was.x, v);
+                kv::decode4<FMT>(was.y, u);
+                o.x = kv::encode4<FMT>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+                o.y = kv::encode4<FMT>(u[0] * ratio, u[1] * ratio, u[2] * ratio, u[3] * ratio);
             } else if (r < hi) {
                 const uint32_t* w = tile + r * pitch + x * 4;
                 float v[8];
@@ -103,8 +104,8 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
                     v[2 * e] = __uint_as_float(w[e] << 16) * inv;
                     v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * inv;
                 }
-                o.x = kv::encode4(v[0], v[1], v[2], v[3], c.fmt);
-                o.y = kv::encode4(v[4], v[5], v[6], v[7], c.fmt);
+                o.x = kv::encode4<FMT>(v[0], v[1], v[2], v[3]);
+                o.y = kv::encode4<FMT>(v[4], v[5], v[6], v[7]);
             }
             *p = o;
         }
@@ -126,8 +127,8 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
                 uint32_t w = wa[e];
                 if (t0 < lo && grown) {
                     float v[4];
-                    kv::decode4(w, c.fmt, v);
-                    const uint32_t again = kv::encode4(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio, c.fmt);
+                    kv::decode4<FMT>(w, v);
+                    const uint32_t again = kv::encode4<FMT>(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
                     const uint32_t m = t0 + 4 <= lo ? ~0u : (1u << 8 * (lo - t0)) - 1;
                     w = (w & ~m) | (again & m);
                 }
@@ -143,7 +144,7 @@ kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __r
                             m |= 0xffu << 8 * b;
                         }
                     }
-                    w = (w & ~m) | (kv::encode4(v[0], v[1], v[2], v[3], c.fmt) & m);
+                    w = (w & ~m) | (kv::encode4<FMT>(v[0], v[1], v[2], v[3]) & m);
                 }
                 o[e] = w;
             }
@@ -156,11 +157,12 @@ constexpr int kReadThreads = 128;
 
 // One CTA per (touched block, head, K or V): codes times the scale, rounded
 // to bf16 once.  V comes back through 4 x 4 byte transposes in registers.
+template <int FMT, int D, int blk>
 __global__ void __launch_bounds__(kReadThreads)
 kv_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vdst, long long kstride, long long vstride)
 {
     extern __shared__ uint32_t tile[];   // V: [D][blk/4] words
-    const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x, D = c.D, blk = c.blk;
+    const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
     kv::Touched t;
     if (!kv::find_touched(c, blockIdx.x, t))
         return;
@@ -175,31 +177,32 @@ kv_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vds
     const long long stride = which ? vstride : kstride;
     dst += (long long)(t.c0 - start) * stride + (long long)h * D;   // row of the block's token 0
     if (which == 0) {
-        const int vec = D / 8;
+        constexpr int vec = D / 8;
         for (int i = tid; i < (hi - lo) * vec; i += kReadThreads) {
             const int r = lo + i / vec, x = i % vec;
             const uint2 w = *reinterpret_cast<const uint2*>(src + r * D + x * 8);
             float v[4], u[4];
-            kv::decode4(w.x, c.fmt, v);
-            kv::decode4(w.y, c.fmt, u);
+            kv::decode4<FMT>(w.x, v);
+            kv::decode4<FMT>(w.y, u);
             uint4 o;
-            o.x = tc::f2bf16_rne(v[0] * scale) | (uint32_t)tc::f2bf16_rne(v[1] * scale) << 16;
-            o.y = tc::f2bf16_rne(v[2] * scale) | (uint32_t)tc::f2bf16_rne(v[3] * scale) << 16;
-            o.z = tc::f2bf16_rne(u[0] * scale) | (uint32_t)tc::f2bf16_rne(u[1] * scale) << 16;
-            o.w = tc::f2bf16_rne(u[2] * scale) | (uint32_t)tc::f2bf16_rne(u[3] * scale) << 16;
+            o.x = kv::bf16x2(v[0] * scale, v[1] * scale);
+            o.y = kv::bf16x2(v[2] * scale, v[3] * scale);
+            o.z = kv::bf16x2(u[0] * scale, u[1] * scale);
+            o.w = kv::bf16x2(u[2] * scale, u[3] * scale);
             *reinterpret_cast<uint4*>(dst + r * stride + x * 8) = o;
         }
         return;
     }
     // word w of row d lies at w ^ (d / 4): the four rows of a transpose are
     // read by 32 lanes with few bank conflicts
-    const int wpr = blk / 4;
+    constexpr int wpr = blk / 4;
     for (int i = tid; i < D * wpr; i += kReadThreads) {
         const int d = i / wpr, w = i % wpr;
         tile[d * wpr + (w ^ (d >> 2 & (wpr - 1)))] = reinterpret_cast<const uint32_t*>(src)[i];
     }
     __syncthreads();
-    const int dq = D / 4, q0 = lo / 4, nq = (hi + 3) / 4 - q0;
+    constexpr int dq = D / 4;
+    const int q0 = lo / 4, nq = (hi + 3) / 4 - q0;
     for (int i = tid; i < dq * nq; i += kReadThreads) {
         const int d4 = i % dq, q = q0 + i / dq;
         uint32_t r[4];
@@ -216,10 +219,10 @@ kv_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vds
             if (tok < lo || tok >= hi)
                 continue;
             float v[4];
-            kv::decode4(col[k], c.fmt, v);
+            kv::decode4<FMT>(col[k], v);
             uint2 o;
-            o.x = tc::f2bf16_rne(v[0] * scale) | (uint32_t)tc::f2bf16_rne(v[1] * scale) << 16;
-            o.y = tc::f2bf16_rne(v[2] * scale) | (uint32_t)tc::f2bf16_rne(v[3] * scale) << 16;
+            o.x = kv::bf16x2(v[0] * scale, v[1] * scale);
+            o.y = kv::bf16x2(v[2] * scale, v[3] * scale);
             *reinterpret_cast<uint2*>(dst + tok * stride + d4 * 4) = o;
         }
     }
@@ -233,6 +236,28 @@ int touched_bound(const KvView& c)
     return (int)(most < c.n_tokens ? most : c.n_tokens);
 }
 
+typedef void (*WriteKernel)(KvView, const uint16_t*, const uint16_t*, long long, long long);
+typedef void (*ReadKernel)(KvView, uint16_t*, uint16_t*, long long, long long);
+
+template <int FMT, int D, int BLK>
+struct Kernels {
+    static WriteKernel get(const uint16_t*) { return kv_write_kernel<FMT, D, BLK>; }
+    static ReadKernel get(uint16_t*) { return kv_read_kernel<FMT, D, BLK>; }
+};
+template <int FMT, int D, class P>
+auto by_block(int blk, P tag)
+{
+    return blk == 32 ? Kernels<FMT, D, 32>::get(tag) : blk == 64 ? Kernels<FMT, D, 64>::get(tag) : Kernels<FMT, D, 128>::get(tag);
+}
+// The kernel of a cache's format, head size and block; the tag's type says write or read.
+template <class P>
+auto kernel_of(const KvView& c, P tag)
+{
+    if (c.fmt == MOE_KV_E4M3)
+        return c.D == 64 ? by_block<MOE_KV_E4M3, 64>(c.blk, tag) : by_block<MOE_KV_E4M3, 128>(c.blk, tag);
+    return c.D == 64 ? by_block<MOE_KV_INT8, 64>(c.blk, tag) : by_block<MOE_KV_INT8, 128>(c.blk, tag);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride,
@@ -240,7 +265,7 @@ cudaError_t launch_kv_write(const KvView& c, const uint16_t* k, const uint16_t* 
 {
     const dim3 grid(touched_bound(c), c.H, 2);
     const size_t smem = (size_t)c.blk * (c.D / 2 + 1) * 4;
-    kv_write_kernel<<<grid, kWriteThreads, smem, s>>>(c, k, v, k_stride, v_stride);
+    kernel_of(c, k)<<<grid, kWriteThreads, smem, s>>>(c, k, v, k_stride, v_stride);
     return cudaGetLastError();
 }
 
@@ -249,7 +274,7 @@ cudaError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, long long 
 {
     const dim3 grid(touched_bound(c), c.H, 2);
     const size_t smem = (size_t)c.blk * c.D;
-    kv_read_kernel<<<grid, kReadThreads, smem, s>>>(c, k, v, k_stride, v_stride);
+    kernel_of(c, k)<<<grid, kReadThreads, smem, s>>>(c, k, v, k_stride, v_stride);
     return cudaGetLastError();
 }
 
