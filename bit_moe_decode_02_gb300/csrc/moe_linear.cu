@@ -5,13 +5,15 @@
 //  - Operands.  m16n8k16 MMAs, 16 weight rows by 8 tokens, f16 with fp32 sums.  The
 //    order of the summed index is free: a thread's operand of a 32-column block
 //    is the 4 bytes of its eight consecutive columns.  E2M1 codes become f16
-//    pairs by conversion, exactly.  An int4 code q becomes 16 + q (its bits under
-//    an exponent: one shift and one logic operation a pair), and the sum starts
-//    at -24 sum(x) of the group, so what is added up is (q - 8) x.
-//  - Scales.  A group's sum is its own short chain of MMAs; the row's scale times
-//    the token's factor multiplies it into the fp32 total.
+//    pairs by conversion, exactly.  An int4 code q is taken as the f16 subnormal
+//    q 2^-24 that its bits are where they lie (q 2^-20 one nibble up, for which x
+//    is a sixteenth): one logic operation a pair and a shift for every four.
+//    The sum starts at -8 sum(x) 2^-24 of the group, so what is added up is (q - 8) x.
+//  - Scales.  A group's sum is its own short chain of MMAs; the row's scale
+//    multiplies it into the fp32 total.
 //  - x is scaled per token by a power of two (largest magnitude into [2^13,
-//    2^15)) and converted to f16 once per CTA: exact down to 2^-37 of it.
+//    2^15)) and converted to f16 once per CTA: exact down to 2^-37 of it (int4:
+//    2^-33 for the sixteenths).
 //  - Loads.  Each warp streams 16 rows by 256 columns a stage (2 KB, whole 128-byte
 //    lines) through its own ring with 16-byte cp.async, XOR-swizzled so that the
 //    operand reads have no bank conflicts; the caller's row pitch gives up to
@@ -59,16 +61,28 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp16(void* dst, const void* src)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::su32(dst)), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(void* dst, const void* src, int bytes)
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::su32(dst)), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4_part(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// max of each unsigned half
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Eight codes -> four f16 pairs: E2M1 in order; int4 as (i, i + 4), each 16 + q.
+// Eight codes -> four f16 pairs: E2M1 in order; int4 as codes (0, 4) 2^-24,
+// (1, 5) 2^-20, (2, 6) 2^-24, (3, 7) 2^-20.
 template <int FMT>
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4])
 {
@@ -78,13 +92,37 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4])
             "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
             : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
     } else {
-        h[0] = (w << 6 & 0x03c003c0u) | 0x4c004c00u;
-        h[1] = (w << 2 & 0x03c003c0u) | 0x4c004c00u;
-        h[2] = (w >> 2 & 0x03c003c0u) | 0x4c004c00u;
-        h[3] = (w >> 6 & 0x03c003c0u) | 0x4c004c00u;
+        h[0] = w & 0x000f000fu;
+        h[1] = w & 0x00f000f0u;
+        h[2] = w >> 8 & 0x000f000fu;
+        h[3] = w >> 8 & 0x00f000f0u;
     }
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds32(a)); }
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// E8M0 byte -> 2^(e - 127): 2^-127 for 0, NaN for 255.
+__device__ __forceinline__ float e8m0(int e) { return __int_as_float(max(e << 23, 0x400000) + (e + 1 >> 8)); }
+// Whether one of four bytes is 0 or 255.
+__device__ __forceinline__ bool odd_byte(uint32_t w) { return __vcmpeq4(w, 0u) | __vcmpeq4(w, 0xffffffffu); }
 // FMT, 32-column blocks of a group, 8-token tiles.
 template <int FMT, int SUBS, int NT>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan p)
@@ -96,119 +134,187 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     const int team = warp / p.ks, part = warp % p.ks, teams = kWarps / p.ks;
     const int nunits = (a.N + kRows - 1) / kRows, nsteps = (a.K + kCols - 1) / kCols;
     const int row_scale = FMT == MOE_FMT_MXFP4 ? a.K / 32 : 2 * (a.K / kGroup);   // bytes
-    uint8_t* ring = sm + p.off_ring + warp * p.stages * p.stage_bytes;
-    const uint8_t* scales = static_cast<const uint8_t*>(a.scales);
-    const long long scale_end = (long long)a.N * row_scale;
+    const uint32_t ring = tc::su32(sm + p.off_ring) + warp * p.stages * p.stage_bytes;
+    const int half_k = a.K / 2;
 
     // this warp's stream: its stages of each of its team's units
     const int stride = gridDim.x * teams;
-    int pu = blockIdx.x + team * gridDim.x, ps = part, pslot = 0;   // next to load
+    int pu = blockIdx.x + team * gridDim.x, ps = part;             // next to load
+    uint32_t pst = ring;
+    const uint32_t ring_end = ring + p.stages * p.stage_bytes;
+    const int l3 = lane >> 3, ch = lane & 7;
+    // rows l3, l3 + 4, l3 + 8, l3 + 12 of a stage, 16 bytes each
+    const uint32_t d0 = l3 * 128 + ((ch ^ l3) << 4), d1 = (l3 + 4) * 128 + ((ch ^ l3 ^ 4) << 4);
+    constexpr int kScaleCopies = (kRows * SW + 31) / 32;
+    int soff[kScaleCopies];                                         // a scale word's row offset, its word in the low bits
+#pragma unroll
+    for (int i = 0; i < kScaleCopies; ++i) {
+        const int k = lane + 32 * i;
+        soff[i] = k < kRows * SW ? k / SW * row_scale : -1;
+    }
+    const uint8_t *csrc = nullptr, *ssrc = nullptr;                 // the unit's codes (this lane's row) and scales
+    int prows = 0;
+    auto open_unit = [&]() {
+        prows = min(a.N - pu * kRows, kRows);
+        csrc = a.codes + (long long)pu * kRows * half_k + l3 * half_k + ch * 16;
+        ssrc = static_cast<const uint8_t*>(a.scales) + (long long)pu * kRows * row_scale;
+    };
     auto load = [&]() {
-        if (pu < nunits && ps < nsteps) {
-            uint8_t* st = ring + pslot * p.stage_bytes;
-            const int row0 = pu * kRows;
-            const uint8_t* src = a.codes + (long long)row0 * (a.K / 2) + ps * (kCols / 2);
-            const int ch = lane & 7, left = a.K / 2 - ps * (kCols / 2);
+        if (pu < nunits) {
+            const uint8_t* src = csrc + ps * (kCols / 2);
+            if (prows == kRows && (ps + 1) * kCols <= a.K) {
+                cp16(pst + d0, src);
+                cp16(pst + d1, src + 4 * half_k);
+                cp16(pst + d0 + 1024, src + 8 * half_k);
+                cp16(pst + d1 + 1024, src + 12 * half_k);
+            } else if (ps * (kCols / 2) + ch * 16 < half_k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int x = (lane >> 3) + 4 * i;
-                if (row0 + x < a.N && ch * 16 < left)
-                    cp16(st + x * 128 + ((ch ^ (x & 7)) << 4), src + (long long)x * (a.K / 2) + ch * 16);
+                for (int i = 0; i < 4; ++i)
+                    if (l3 + 4 * i < prows)
+                        cp16(pst + (i & 1 ? d1 : d0) + (i >> 1) * 1024, src + 4 * i * half_k);
             }
-            uint32_t* ss = reinterpret_cast<uint32_t*>(st + kCodeBytes);
 #pragma unroll
-            for (int i = 0; i < (kRows * SW + 31) / 32; ++i) {
-                const int k = lane + 32 * i, x = k / SW, w = k % SW;
-                const long long at = (((long long)(row0 + x) * row_scale + ps * SB) & ~3ll) + 4 * w;
-                if (k < kRows * SW && row0 + x < a.N && at < scale_end)
-                    cp4(ss + k, scales + at, (int)min(4ll, scale_end - at));
+            for (int i = 0; i < kScaleCopies; ++i) {
+                const int k = lane + 32 * i, at = (soff[i] + ps * SB & ~3) + 4 * (k % SW), end = prows * row_scale;
+                if (soff[i] >= 0) {
+                    if (at + 4 <= end)
+                        cp4(pst + kCodeBytes + 4 * k, ssrc + at);
+                    else if (at < end)
+                        cp4_part(pst + kCodeBytes + 4 * k, ssrc + at, end - at);
+                }
             }
-            pslot = pslot + 1 == p.stages ? 0 : pslot + 1;
+            pst += p.stage_bytes;
+            if (pst == ring_end)
+                pst = ring;
             ps += p.ks;
             if (ps >= nsteps) {
                 ps = part;
                 pu += stride;
+                open_unit();
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (part >= nsteps)
         pu = nunits;                            // fewer stages than warps: nothing for this one
+    open_unit();
     for (int i = 0; i < p.stages - 1; ++i)
         load();
 
-    // x: f16, scaled per token, and (int4) each group's sum
+    // x: f16, scaled per token, and (int4) each group's sum.  Pieces of 256 columns
+    // of a token, dealt over the warps
     float* fac = reinterpret_cast<float*>(sm + p.off_fac);
+    int* ups = reinterpret_cast<int*>(fac + 16);
+    uint32_t* bigs = reinterpret_cast<uint32_t*>(ups + 1);
     float* sums = reinterpret_cast<float*>(sm + p.off_sum);
-    const int groups = a.K / kGroup;
-    for (int m = warp; m < p.tokens; m += kWarps) {
-        const uint16_t* x = a.x + m * a.x_stride;
-        uint32_t big = 0;
-        for (int i = lane; i < a.K / 8; i += 32) {
-            const uint4 q = *reinterpret_cast<const uint4*>(x + 8 * i);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const int groups = a.K / kGroup, pieces = p.tokens * nsteps;
+    if (tid < 16)
+        bigs[tid] = 0;
+    __syncthreads();
+    // read once, eight pieces' loads at a time; bf16 waits where its f16 will lie
+    for (int i0 = warp; i0 < pieces; i0 += 8 * kWarps) {
+        uint4 q[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t u = w[k] & 0x7fffu, v = w[k] >> 16 & 0x7fffu;
-                big = max(big, max(u < 0x7f80u ? u : 0u, v < 0x7f80u ? v : 0u));
-            }
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kWarps, m = i / nsteps, k = i % nsteps * 32 + lane;
+            q[j] = make_uint4(0, 0, 0, 0);
+            if (i < pieces && k < a.K / 8)
+                q[j] = *reinterpret_cast<const uint4*>(a.x + m * a.x_stride + 8 * k);
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
-            big = max(big, __shfl_xor_sync(~0u, big, o));
-        const int up = 14 + 127 - max((int)(big >> 7), 1);
-        const float u0 = __uint_as_float((uint32_t)(127 + up / 2) << 23), u1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
-        if (lane == 0)
-            fac[m] = ldexpf(1.0f, -up);
-        for (int i0 = 0; i0 < a.K / 8; i0 += 32) {
-            const int i = i0 + lane;
-            uint4 o = make_uint4(0, 0, 0, 0);
-            float sum = 0.0f;
-            if (i < a.K / 8) {
-                const uint4 q = *reinterpret_cast<const uint4*>(x + 8 * i);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                __half h[8];
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kWarps, m = i / nsteps, k = i % nsteps * 32 + lane;
+            if (i >= pieces)
+                break;
+            const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+            uint32_t big = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float f = __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16) * u0 * u1;
-                    h[k] = __float2half_rn(f);
-                    sum += __half2float(h[k]);
+            for (int e = 0; e < 4; ++e)
+                big = max_u16x2(big, w[e] & 0x7fff7fffu);
+            big = max(big & 0xffffu, big >> 16);
+            if (big >= 0x7f80u) {
+                // NaN or infinity: the largest of the others
+                big = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t u = w[e] & 0x7fffu, v = w[e] >> 16 & 0x7fffu;
+                    big = max(big, max(u < 0x7f80u ? u : 0u, v < 0x7f80u ? v : 0u));
                 }
-                uint32_t* ow = &o.x;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2 t = FMT == MOE_FMT_MXFP4 ? __halves2half2(h[2 * k], h[2 * k + 1]) : __halves2half2(h[k], h[k + 4]);
-                    ow[k] = *reinterpret_cast<const uint32_t*>(&t);
-                }
-                *reinterpret_cast<uint4*>(sm + m * p.x_pitch + i * 16) = o;
             }
-            if constexpr (FMT == MOE_FMT_INT4) {
+            if (k < a.K / 8)
+                *reinterpret_cast<uint4*>(sm + m * p.x_pitch + k * 16) = q[j];
+            big = __reduce_max_sync(~0u, big);
+            if (lane == 0)
+                atomicMax(bigs + m, big);
+        }
+    }
+    __syncthreads();
+    auto up_of = [&](int m) { return 14 + 127 - max((int)(bigs[m] >> 7), 1); };
+    if (tid == 0) {
+        // the totals are kept in the units of the token that is scaled up least
+        int up = up_of(0);
+        for (int m = 1; m < p.tokens; ++m)
+            up = min(up, up_of(m));
+        *ups = up;
+        for (int m = 0; m < p.tokens; ++m)
+            fac[m] = ldexpf(1.0f, up - up_of(m));
+    }
+    for (int i = warp; i < pieces; i += kWarps) {
+        const int m = i / nsteps, k = i % nsteps * 32 + lane, up = up_of(m);
+        // 2^up in two factors, the second 1 but for the smallest tokens
+        const float u0 = __uint_as_float((uint32_t)(127 + min(up, 126)) << 23), u1 = __uint_as_float((uint32_t)(127 + max(up - 126, 0)) << 23);
+        float sum = 0.0f;
+        if (k < a.K / 8) {
+            const uint4 q = *reinterpret_cast<const uint4*>(sm + m * p.x_pitch + k * 16);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint4 o;
+            uint32_t* ow = &o.x;
+            float f[8];
 #pragma unroll
-                for (int s = 1; s < 4 * SUBS; s <<= 1)
-                    sum += __shfl_xor_sync(~0u, sum, s);
-                if (i < a.K / 8 && lane % (4 * SUBS) == 0)
-                    sums[m * groups + i / (4 * SUBS)] = -24.0f * sum;
+            for (int e = 0; e < 8; ++e)
+                f[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) * u0;
+            if (up > 126)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] *= u1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = FMT == MOE_FMT_INT4 && (e & 1) ? 0.0625f : 1.0f;
+                const __half2 t = FMT == MOE_FMT_MXFP4 ? __floats2half2_rn(f[2 * e], f[2 * e + 1]) : __floats2half2_rn(f[e] * y, f[e + 4] * y);
+                const float2 back = __half22float2(t);
+                sum += (back.x + back.y) * (FMT == MOE_FMT_INT4 && (e & 1) ? 16.0f : 1.0f);
+                ow[e] = *reinterpret_cast<const uint32_t*>(&t);
             }
+            *reinterpret_cast<uint4*>(sm + m * p.x_pitch + k * 16) = o;
+        }
+        if constexpr (FMT == MOE_FMT_INT4) {
+#pragma unroll
+            for (int x = 1; x < 4 * SUBS; x <<= 1)
+                sum += __shfl_xor_sync(~0u, sum, x);
+            if (k < a.K / 8 && lane % (4 * SUBS) == 0)
+                sums[m * groups + k / (4 * SUBS)] = sum * -4.76837158203125e-07f;    // -8 2^-24
         }
     }
     __syncthreads();
 
-    bool has[NT];                               // this thread's token of the operand exists
-    float tf[NT][2];
-    const uint8_t* xp[NT];
-    const float* sp[NT][2];
+    // tokens that do not exist read the last one's operands; their columns are not stored
+    uint32_t xp[NT], sp[NT][2], cp[8];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        has[i] = 8 * i + r < p.tokens;
-        xp[i] = sm + (8 * i + r) * p.x_pitch + 16 * c;
+        xp[i] = tc::su32(sm) + min(8 * i + r, p.tokens - 1) * p.x_pitch + 16 * c;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int m = 8 * i + 2 * c + k;
-            tf[i][k] = m < p.tokens ? fac[m] : 0.0f;
-            sp[i][k] = m < p.tokens ? sums + m * groups : nullptr;
-        }
+        for (int k = 0; k < 2; ++k)
+            sp[i][k] = tc::su32(sums) + min(8 * i + 2 * c + k, p.tokens - 1) * groups * 4;
     }
-    int slot = 0;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+        cp[b] = r * 128 + ((b ^ r) << 4) + 4 * c;          // a 32-column block's codes in a stage
+    const float unit = FMT == MOE_FMT_MXFP4 ? ldexpf(1.0f, -*ups) : 1.0f;
+    // int4's totals are in units of 2^-24 and of the token that is scaled up least: 2^(24 - up), in two factors
+    const int down = FMT == MOE_FMT_INT4 ? 24 - *ups : 0;
+    const float v0 = __uint_as_float((uint32_t)(127 + down / 2) << 23), v1 = __uint_as_float((uint32_t)(127 + down - down / 2) << 23);
+    uint32_t st = ring;
+    const int a0r = r * row_scale & 3, a1r = (r + 8) * row_scale & 3;
     for (int u = blockIdx.x + team * gridDim.x; u < nunits; u += stride) {
         float acc[NT][4];
 #pragma unroll
@@ -230,12 +336,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
             else
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
-            const uint8_t* st = ring + slot * p.stage_bytes;
-            slot = slot + 1 == p.stages ? 0 : slot + 1;
-            const uint8_t* ss = st + kCodeBytes;
-            const long long at0 = (long long)(u * kRows + r) * row_scale + s * SB, at1 = at0 + 8ll * row_scale;
-            const uint8_t* s0 = ss + r * SW * 4 + (at0 & 3);
-            const uint8_t* s1 = ss + (r + 8) * SW * 4 + (at1 & 3);
+            const int at0 = a0r + s * SB, at1 = a1r + s * SB;       // (low two bits)
+            const uint32_t s0 = st + kCodeBytes + r * SW * 4, s1 = s0 + 8 * SW * 4;
+            uint32_t e0[2], e1[2];                          // MXFP4: the two rows' eight scales
+            bool plain = true;
+            if constexpr (FMT == MOE_FMT_MXFP4) {
+                uint32_t v[3], y[3];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    v[k] = lds32(s0 + 4 * k);
+                    y[k] = lds32(s1 + 4 * k);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    e0[k] = __funnelshift_r(v[k], v[k + 1], 8 * (at0 & 3));
+                    e1[k] = __funnelshift_r(y[k], y[k + 1], 8 * (at1 & 3));
+                }
+                plain = !__any_sync(~0u, odd_byte(e0[0]) || odd_byte(e0[1]) || odd_byte(e1[0]) || odd_byte(e1[1]));
+            }
             const int ng = min(PER, (a.K - s * kCols) / kGroup);
             auto one_group = [&](int g) {
                 float part_sum[NT][4];
@@ -243,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                 for (int i = 0; i < NT; ++i) {
                     float z0 = 0.0f, z1 = 0.0f;
                     if constexpr (FMT == MOE_FMT_INT4) {
-                        z0 = sp[i][0] ? sp[i][0][s * PER + g] : 0.0f;
-                        z1 = sp[i][1] ? sp[i][1][s * PER + g] : 0.0f;
+                        z0 = lds_f32(sp[i][0] + (s * PER + g) * 4);
+                        z1 = lds_f32(sp[i][1] + (s * PER + g) * 4);
                     }
                     part_sum[i][0] = part_sum[i][2] = z0;
                     part_sum[i][1] = part_sum[i][3] = z1;
@@ -252,36 +370,38 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
                 for (int b = 0; b < SUBS; ++b) {
                     const int blk = g * SUBS + b;                   // 32-column block of the stage
-                    const int off = ((blk ^ r) << 4) + 4 * c;
                     uint32_t lo[4], hi[4];
-                    decode8<FMT>(*reinterpret_cast<const uint32_t*>(st + r * 128 + off), lo);
-                    decode8<FMT>(*reinterpret_cast<const uint32_t*>(st + (r + 8) * 128 + off), hi);
+                    decode8<FMT>(lds32(st + cp[blk]), lo);
+                    decode8<FMT>(lds32(st + cp[blk] + 1024), hi);
                     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (has[i])
-                            x = *reinterpret_cast<const uint4*>(xp[i] + (s * (kCols / 32) + blk) * 64);
+                        const uint4 x = lds128(xp[i] + s * (kCols * 2) + blk * 64);
                         mma16816(part_sum[i], a0, x.x, x.y);
                         mma16816(part_sum[i], a1, x.z, x.w);
                     }
                 }
                 float f0, f1;
                 if constexpr (FMT == MOE_FMT_MXFP4) {
-                    // 2^(e - 127): 2^-127 for e = 0, NaN for e = 255
-                    const int e0 = s0[g], e1 = s1[g];
-                    f0 = __int_as_float(max(e0 << 23, 0x400000) + (e0 + 1 >> 8));
-                    f1 = __int_as_float(max(e1 << 23, 0x400000) + (e1 + 1 >> 8));
+                    const uint32_t v = e0[g >> 2], y = e1[g >> 2];
+                    if (plain) {
+                        // the byte to bits 23..30
+                        f0 = __uint_as_float(__byte_perm(v, 0, 0x0444 | (g & 3) << 12) >> 1) * unit;
+                        f1 = __uint_as_float(__byte_perm(y, 0, 0x0444 | (g & 3) << 12) >> 1) * unit;
+                    } else {
+                        f0 = e8m0(v >> 8 * (g & 3) & 255) * unit;
+                        f1 = e8m0(y >> 8 * (g & 3) & 255) * unit;
+                    }
                 } else {
-                    f0 = __half2float(*reinterpret_cast<const __half*>(s0 + 2 * g));
-                    f1 = __half2float(*reinterpret_cast<const __half*>(s1 + 2 * g));
+                    f0 = __half2float(__ushort_as_half((unsigned short)lds_u16(s0 + (at0 & 3) + 2 * g)));
+                    f1 = __half2float(__ushort_as_half((unsigned short)lds_u16(s1 + (at1 & 3) + 2 * g)));
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    acc[i][0] += f0 * (tf[i][0] * part_sum[i][0]);
-                    acc[i][1] += f0 * (tf[i][1] * part_sum[i][1]);
-                    acc[i][2] += f1 * (tf[i][0] * part_sum[i][2]);
-                    acc[i][3] += f1 * (tf[i][1] * part_sum[i][3]);
+                    acc[i][0] += f0 * part_sum[i][0];
+                    acc[i][1] += f0 * part_sum[i][1];
+                    acc[i][2] += f1 * part_sum[i][2];
+                    acc[i][3] += f1 * part_sum[i][3];
                 }
             };
             if (ng == PER) {
@@ -289,10 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                 for (int g = 0; g < PER; ++g)
                     one_group(g);
             } else {
-                for (int g = 0; g < ng; ++g)
-                    one_group(g);
+#pragma unroll
+                for (int g = 0; g < PER - 1; ++g)
+                    if (g < ng)
+                        one_group(g);
             }
             __syncwarp();
+            st += p.stage_bytes;
+            if (st == ring_end)
+                st = ring;
         }
 
         // add up the team's parts
@@ -324,7 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     const int m = 8 * i + 2 * c + (k & 1);
                     if (m >= p.tokens)
                         continue;
-                    const float y = a.bias ? acc[i][k] + bias : acc[i][k];
+                    float y = acc[i][k] * fac[m];
+                    if constexpr (FMT == MOE_FMT_INT4)
+                        y = y * v0 * v1;
+                    y = a.bias ? y + bias : y;
                     const long long at = m * a.out_stride + row;
                     if (a.out_type == MOE_DT_BF16)
                         static_cast<uint16_t*>(a.out)[at] = tc::f2bf16_rne(y);
@@ -385,7 +513,7 @@ cudaError_t launch_linear(const LinearArgs& args, int num_sms, cudaStream_t s)
         if (a.fmt == MOE_FMT_INT4)
             off = align16(off + p.tokens * (a.K / a.group) * 4);
         p.off_fac = off;
-        off += 64;
+        off += 256;                       // factors, the common exponent, largest magnitudes
         p.off_red = off;
         off += kWarps * nt * 512;
         p.off_ring = (off + 127) / 128 * 128;
