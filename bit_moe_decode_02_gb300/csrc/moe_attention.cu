@@ -152,10 +152,38 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, const Place& p, in
         a.lse[(i64)tok * a.q_heads + hq] = f.lse;
 }
 
-struct Piece {           // an unfinished item of a group
+// Partial results joined one after another.
+struct Sum {
+    float m = kNone, l = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+    __device__ __forceinline__ void add(float2 ml, float4 y)
+    {
+        const float mn = fmaxf(m, ml.x), w0 = ex2(m - mn), w1 = ex2(ml.x - mn);
+        m = mn;
+        l = l * w0 + ml.y * w1;
+        v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
+    }
+    __device__ __forceinline__ void from_slot(const float* s, int D, int row, int col)
+    {
+        add(__ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row)), __ldcg(reinterpret_cast<const float4*>(s + row * D + col)));
+    }
+    __device__ __forceinline__ void to_slot(float* s, int D, int row, int col) const
+    {
+        __stcg(reinterpret_cast<float4*>(s + row * D + col), v);
+        if (col == 0)
+            __stcg(reinterpret_cast<float2*>(s + kRows * D + 2 * row), make_float2(m, l));
+    }
+};
+
+// A group's part of an item that is left for the CTA to finish: its first one if
+// that began in an earlier group's run (kSlot: joined over the group's warps, in
+// the group's slot), and its last (kStage: the warps' results still lie in the
+// stage that they read last).
+enum { kSlot = 1, kStage = 2 };
+struct Piece {
     i64 t0, t1;          // the item's tiles
     Place p;
-    int used;
+    int where, stage;
 };
 
 template <int D, int FMT, int BLK>
@@ -169,6 +197,7 @@ struct Decode {
     static constexpr int OFF_ML = OFF_BAR + NG * NS * 16;              // full and empty barriers
     static constexpr int OFF_PIECE = OFF_ML + kWarps * kRows * 8;
     static constexpr int OFF_PRE = OFF_PIECE + NG * 2 * (int)sizeof(Piece);
+    static constexpr int WHOLE = 2 * NG;             // items of at most so many tiles are not split over CTAs
     static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 8; }
 };
 
@@ -179,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ i64 scan[kWarps];
     __shared__ int s_flag;
+    __shared__ i64 s_run[2];
     i64* pre = reinterpret_cast<i64*>(sm + C::OFF_PRE);
     Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
     float2* mls = reinterpret_cast<float2*>(sm + C::OFF_ML);
@@ -192,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         tc::mbar_init(empty + lane, C::GW);
     }
     if (tid < 2 * C::NG)
-        pieces[tid].used = 0;
+        pieces[tid].where = 0;
 
     // prefix sums of the sequences' tiles: four sequences a thread
     {
@@ -234,14 +264,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     const int G = (int)min((i64)gridDim.x, N);                // CTAs with work
     if ((int)blockIdx.x >= G)
         return;
-    const i64 TG = (i64)G * C::NG, gid = (i64)blockIdx.x * C::NG + grp;
-    const i64 t_begin = N * gid / TG, t_end = N * (gid + 1) / TG;
-    const i64 ct0 = N * blockIdx.x / G, ct1 = N * (blockIdx.x + 1) / G;
+    // the CTA's run, by its ends' moves to the start of an item where that is short:
+    // a join over CTAs costs more than two more tiles a group
+    if (warp < 2) {
+        const i64 at = N * (blockIdx.x + warp) / G;
+        i64 end = at;
+        if (at < N) {
+            Item it;
+            find_item(a, pre, at, it);
+            if (it.jhi - it.jlo + 1 <= C::WHOLE)
+                end = it.t0;
+        }
+        if (lane == 0)
+            s_run[warp] = end;
+    }
+    __syncthreads();
+    const i64 ct0 = s_run[0], ct1 = s_run[1], gid = (i64)blockIdx.x * C::NG + grp;
+    if (ct0 == ct1)
+        return;
+    const i64 t_begin = ct0 + (ct1 - ct0) * grp / C::NG, t_end = ct0 + (ct1 - ct0) * (grp + 1) / C::NG;
 
     uint8_t* ring = sm + grp * C::NS * C::STAGE;
     float* hdr = reinterpret_cast<float*>(sm + C::OFF_HDR) + grp * C::NS * 4;
     const uint64_t pol = tc::l2_evict_first();
-    float* slots = ws + (i64)gridDim.x * 2 * slot_floats() + gid * 2 * slot_floats();   // this group's two
+    float* slot = ws + ((i64)gridDim.x * 2 + gid) * slot_floats();                      // this group's
 
     // the tile stream: warp 0 of the group keeps its own place in it, NS - 1 tiles ahead
     Item pit{};
@@ -489,109 +535,93 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 for (int e = 0; e < 2; ++e)
                     *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * D + (i ^ r) * 8 + 2 * c) =
                         make_float2(o[i][2 * e] * ref, o[i][2 * e + 1] * ref);
-            group_sync(1 + grp, C::GW * 32);
-            const bool done = it.t0 >= t_begin && item_end <= t_end;
-            const int which = it.t0 < t_begin || t_begin == it.t0 ? 0 : 1;   // the group's first item, or its last
             const Place place{it.c0, it.rt * kRows, it.h, rows};
-            float* slot = slots + which * slot_floats();
+            if (t == t_end) {
+                // the group's last: finished with the CTA's others
+                if (sub == 0 && lane == 0)
+                    pieces[grp * 2 + 1] = Piece{it.t0, item_end, place, kStage, st};
+                break;
+            }
+            group_sync(1 + grp, C::GW * 32);
+            const bool done = it.t0 >= t_begin;
             for (int x = sub * 32 + lane; x < rows * (D / 4); x += C::GW * 32) {
                 const int row = x / (D / 4), col = x % (D / 4) * 4;
-                float M = kNone, L = 0.0f;
+                Sum sum;
 #pragma unroll
                 for (int w = 0; w < C::GW; ++w)
-                    M = fmaxf(M, mls[(grp * C::GW + w) * kRows + row].x);
-                float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int w = 0; w < C::GW; ++w) {
-                    const float2 ml = mls[(grp * C::GW + w) * kRows + row];
-                    const float wt = ex2(ml.x - M);
-                    L += ml.y * wt;
-                    const float4 y = *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7));
-                    v.x += y.x * wt, v.y += y.y * wt, v.z += y.z * wt, v.w += y.w * wt;
-                }
-                if (done) {
-                    store_row4(a, place, row, col, v, finish(M, L, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
-                } else {
-                    __stcg(reinterpret_cast<float4*>(slot + row * D + col), v);
-                    if (col == 0)
-                        __stcg(reinterpret_cast<float2*>(slot + kRows * D + 2 * row), make_float2(M, L));
-                }
+                    sum.add(mls[(grp * C::GW + w) * kRows + row],
+                            *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+                if (done)
+                    store_row4(a, place, row, col, sum.v, finish(sum.m, sum.l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
+                else
+                    sum.to_slot(slot, D, row, col);
             }
-            if (!done && sub == 0 && lane == 0) {
-                Piece& p = pieces[grp * 2 + which];
-                p.t0 = it.t0;
-                p.t1 = item_end;
-                p.p = place;
-                p.used = 1;
-            }
+            if (!done && sub == 0 && lane == 0)
+                pieces[grp * 2] = Piece{it.t0, item_end, place, kSlot, 0};
             tc::fence_proxy_async_smem();
             group_sync(1 + grp, C::GW * 32);
             if (lane == 0)
                 tc::mbar_arrive(empty + st);
             if (sub == 0 && pt < t_end)
                 produce();
-            if (t < t_end) {
-                next_item(a, pre, it);
-                j = it.jlo;
-            }
+            next_item(a, pre, it);
+            j = it.jlo;
         }
     }
 
-    // ---- join the groups' pieces, in the order of their tiles
+    // ---- finish the groups' pieces, in the order of their tiles
     __threadfence_block();
     __syncthreads();
-    const float* gslots = ws + (i64)gridDim.x * 2 * slot_floats() + (i64)blockIdx.x * C::NG * 2 * slot_floats();
+    const float* gslots = ws + ((i64)gridDim.x * 2 + (i64)blockIdx.x * C::NG) * slot_floats();
     float* cslots = ws + (i64)blockIdx.x * 2 * slot_floats();
-    int across[2] = {0, 0};
-    Piece cross[2];
+    int across = 0, cross[2] = {0, 0};
     for (int first = 0; first < 2 * C::NG;) {
-        if (!pieces[first].used) {
+        if (!pieces[first].where) {
             ++first;
             continue;
         }
-        const Piece p = pieces[first];
+        const i64 t0 = pieces[first].t0;
+        const Place place = pieces[first].p;
         int last = first + 1;
-        while (last < 2 * C::NG && (!pieces[last].used || pieces[last].t0 == p.t0))
+        while (last < 2 * C::NG && (!pieces[last].where || pieces[last].t0 == t0))
             ++last;
-        const bool done = p.t0 >= ct0 && p.t1 <= ct1;
-        const int which = p.t0 < ct0 ? 0 : 1;
-        for (int x = tid; x < p.p.nrows * (D / 4); x += kThreads) {
+        const bool done = t0 >= ct0 && pieces[first].t1 <= ct1;
+        const int which = t0 < ct0 ? 0 : 1;
+        for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), col = x % (D / 4) * 4;
-            float M = kNone, L = 0.0f;
-            float4 v = make_float4(0, 0, 0, 0);
+            Sum sum;
+#pragma unroll 1
             for (int k = first; k < last; ++k) {
-                if (!pieces[k].used)
-                    continue;
-                const float* s = gslots + k * slot_floats();
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
-                const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
-                M = mn;
-                L = L * w0 + ml.y * w1;
-                v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
+                if (pieces[k].where == kSlot) {
+                    sum.from_slot(gslots + (k >> 1) * slot_floats(), D, row, col);
+                } else if (pieces[k].where == kStage) {
+                    const int g = k >> 1;
+                    const float* od = reinterpret_cast<const float*>(sm + (g * C::NS + pieces[k].stage) * C::STAGE);
+#pragma unroll
+                    for (int w = 0; w < C::GW; ++w)
+                        sum.add(mls[(g * C::GW + w) * kRows + row],
+                                *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+                }
             }
-            if (done) {
-                store_row4(a, p.p, row, col, v, finish(M, L, a.sinks, p.p.h * a.group + (p.p.r0 + row) % a.group));
-            } else {
-                float* s = cslots + which * slot_floats();
-                __stcg(reinterpret_cast<float4*>(s + row * D + col), v);
-                if (col == 0)
-                    __stcg(reinterpret_cast<float2*>(s + kRows * D + 2 * row), make_float2(M, L));
-            }
+            if (done)
+                store_row4(a, place, row, col, sum.v, finish(sum.m, sum.l, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
+            else
+                sum.to_slot(cslots + which * slot_floats(), D, row, col);
         }
         if (!done) {
-            across[which] = 1;
-            cross[which] = p;
+            across |= 1 << which;
+            cross[which] = first;
         }
         first = last;
     }
 
     // ---- items that span CTAs: the last one to arrive joins them all
-#pragma unroll
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        if (!across[which])
+        if (!(across >> which & 1))
             continue;
-        const Piece p = cross[which];
+        const Piece& p = pieces[cross[which]];
+        const Place place = p.p;
         const int ca = (int)(((p.t0 + 1) * G - 1) / N), cb = (int)((p.t1 * G - 1) / N);   // CTAs of its first and last tile
         __threadfence();
         __syncthreads();
@@ -602,27 +632,58 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 cnt[ca] = 0;
         }
         __syncthreads();
-        const int lastone = s_flag;
-        __syncthreads();
-        if (!lastone)
+        if (!s_flag)
             continue;
         __threadfence();
-        for (int x = tid; x < p.p.nrows * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), col = x % (D / 4) * 4;
+        // maxima and sums of every part and row, then their weights, in the ring
+        const int K = cb - ca + 1, rows = place.nrows;
+        float2* part = reinterpret_cast<float2*>(sm);                    // [K][kRows]; .x becomes the weight
+        float2* total = part + gridDim.x * kRows;                        // [kRows]
+        float4* acc = reinterpret_cast<float4*>(total + kRows);          // [kThreads]
+        auto slot_of = [&](int k) { return ws + ((i64)(ca + k) * 2 + (k == 0)) * slot_floats(); };
+        for (int i = tid; i < K * rows; i += kThreads)
+            part[i / rows * kRows + i % rows] = __ldcg(reinterpret_cast<const float2*>(slot_of(i / rows) + kRows * D + 2 * (i % rows)));
+        __syncthreads();
+        if (tid < rows) {
             float M = kNone, L = 0.0f;
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-            for (int k = ca; k <= cb; ++k) {
-                const float* s = ws + ((i64)k * 2 + (k == ca)) * slot_floats();
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
-                const float mn = fmaxf(M, ml.x), w0 = ex2(M - mn), w1 = ex2(ml.x - mn);
-                M = mn;
-                L = L * w0 + ml.y * w1;
-                v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
+            for (int k = 0; k < K; ++k)
+                M = fmaxf(M, part[k * kRows + tid].x);
+            for (int k = 0; k < K; ++k) {
+                const float2 ml = part[k * kRows + tid];
+                const float w = ex2(ml.x - M);
+                L += ml.y * w;
+                part[k * kRows + tid].x = w;
             }
-            store_row4(a, p.p, row, col, v, finish(M, L, a.sinks, p.p.h * a.group + (p.p.r0 + row) % a.group));
+            total[tid] = make_float2(M, L);
         }
+        __syncthreads();
+        // every 4 columns' parts summed by `split` threads, then those
+        const int n4 = rows * (D / 4), split = n4 <= kThreads / 2 ? kThreads / n4 : 1;
+        for (int x0 = 0; x0 < n4; x0 += kThreads) {
+            const int x = split > 1 ? tid % n4 : x0 + tid, from = split > 1 ? tid / n4 : 0;
+            float4 v = make_float4(0, 0, 0, 0);
+            const int row = x / (D / 4), col = x % (D / 4) * 4;
+            if (x < n4 && from < split) {
+#pragma unroll 8
+                for (int k = from; k < K; k += split) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + row * D + col));
+                    const float w = part[k * kRows + row].x;
+                    v.x += y.x * w, v.y += y.y * w, v.z += y.z * w, v.w += y.w * w;
+                }
+            }
+            if (split > 1) {
+                acc[tid] = v;
+                __syncthreads();
+                if (tid < n4)
+                    for (int f = 1; f < split; ++f) {
+                        const float4 y = acc[f * n4 + tid];
+                        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                    }
+            }
+            if (x < n4 && from == 0)
+                store_row4(a, place, row, col, v, finish(total[row].x, total[row].y, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
+        }
+        __syncthreads();
     }
 }
 
