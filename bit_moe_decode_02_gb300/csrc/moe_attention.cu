@@ -51,19 +51,21 @@ struct Item {
     int b, c0, n, len;   // sequence
     int rt, h;           // row tile, kv head
     int jlo, jhi;        // its blocks
-    i64 t0;              // its first tile
+    int t0;              // its first tile
 };
 
+template <int BLK>
 __device__ __forceinline__ void block_range(const AttnArgs& a, int n, int len, int rt, int& jlo, int& jhi)
 {
     const int r0 = rt * kRows, r1 = min(r0 + kRows, n * a.group) - 1;
     const int p0 = len - n + r0 / a.group, p1 = len - n + r1 / a.group;
-    jhi = p1 / a.c.blk;
-    jlo = a.window > 0 && p0 >= a.window ? (p0 - a.window + 1) / a.c.blk : 0;
+    jhi = p1 / BLK;
+    jlo = a.window > 0 && p0 >= a.window ? (p0 - a.window + 1) / BLK : 0;
 }
 
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int n) { return (n * a.group + kRows - 1) / kRows; }
 
+template <int BLK>
 __device__ __forceinline__ i64 tiles_of(const AttnArgs& a, int b)
 {
     int c0, n, len;
@@ -72,18 +74,41 @@ __device__ __forceinline__ i64 tiles_of(const AttnArgs& a, int b)
         return 0;
     }
     i64 t = 0;
+#pragma unroll 1
     for (int rt = 0, nrt = row_tiles(a, n); rt < nrt; ++rt) {
         int lo, hi;
-        block_range(a, n, len, rt, lo, hi);
+        block_range<BLK>(a, n, len, rt, lo, hi);
         t += hi - lo + 1;
     }
     return t * a.c.H;
 }
 
+// Sequence b's item that holds tile t >= pre[b].
+template <int BLK>
+__device__ __forceinline__ void item_in(const AttnArgs& a, const int* pre, int b, int t, Item& it)
+{
+    it.b = b;
+    kv::sequence(a.c, b, it.c0, it.n, it.len);
+    int at = pre[b];
+#pragma unroll 1
+    for (it.rt = 0;; ++it.rt) {
+        block_range<BLK>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+        const int here = (it.jhi - it.jlo + 1) * a.c.H;
+        if (t < at + here)
+            break;
+        at += here;
+    }
+    const int nb = it.jhi - it.jlo + 1;
+    it.h = (t - at) / nb;
+    it.t0 = at + it.h * nb;
+}
+
 // The item that holds tile t, from the prefix sums of the sequences' tiles.
-__device__ __forceinline__ void find_item(const AttnArgs& a, const i64* pre, i64 t, Item& it)
+template <int BLK>
+__device__ __forceinline__ void find_item(const AttnArgs& a, const int* pre, int t, Item& it)
 {
     int lo = 0, hi = a.c.n_seqs;
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (pre[mid] <= t)
@@ -91,32 +116,25 @@ __device__ __forceinline__ void find_item(const AttnArgs& a, const i64* pre, i64
         else
             hi = mid;
     }
-    it.b = lo;
-    kv::sequence(a.c, lo, it.c0, it.n, it.len);
-    i64 at = pre[lo];
-    for (it.rt = 0;; ++it.rt) {
-        block_range(a, it.n, it.len, it.rt, it.jlo, it.jhi);
-        const i64 here = (i64)(it.jhi - it.jlo + 1) * a.c.H;
-        if (t < at + here)
-            break;
-        at += here;
-    }
-    const int nb = it.jhi - it.jlo + 1;
-    it.h = (int)((t - at) / nb);
-    it.t0 = at + (i64)it.h * nb;
+    item_in<BLK>(a, pre, lo, t, it);
 }
 
-__device__ __forceinline__ void next_item(const AttnArgs& a, const i64* pre, Item& it)
+template <int BLK>
+__device__ __forceinline__ void next_item(const AttnArgs& a, const int* pre, Item& it)
 {
     it.t0 += it.jhi - it.jlo + 1;
     if (++it.h < a.c.H)
         return;
     it.h = 0;
     if (++it.rt < row_tiles(a, it.n)) {
-        block_range(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+        block_range<BLK>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
         return;
     }
-    find_item(a, pre, it.t0, it);
+    int b = it.b + 1;
+#pragma unroll 1
+    while (pre[b + 1] <= it.t0)
+        ++b;
+    item_in<BLK>(a, pre, b, it.t0, it);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -181,7 +199,7 @@ struct Sum {
 // stage that they read last).
 enum { kSlot = 1, kStage = 2 };
 struct Piece {
-    i64 t0, t1;          // the item's tiles
+    int t0, t1;          // the item's tiles
     Place p;
     int where, stage;
 };
@@ -198,7 +216,7 @@ struct Decode {
     static constexpr int OFF_PIECE = OFF_ML + kWarps * kRows * 8;
     static constexpr int OFF_PRE = OFF_PIECE + NG * 2 * (int)sizeof(Piece);
     static constexpr int WHOLE = 2 * NG;             // items of at most so many tiles are not split over CTAs
-    static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 8; }
+    static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 4; }
 };
 
 template <int D, int FMT, int BLK>
@@ -208,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ i64 scan[kWarps];
     __shared__ int s_flag;
-    __shared__ i64 s_run[2];
-    i64* pre = reinterpret_cast<i64*>(sm + C::OFF_PRE);
+    __shared__ int s_run[2];
+    int* pre = reinterpret_cast<int*>(sm + C::OFF_PRE);
     Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
     float2* mls = reinterpret_cast<float2*>(sm + C::OFF_ML);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -224,17 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     if (tid < 2 * C::NG)
         pieces[tid].where = 0;
 
-    // prefix sums of the sequences' tiles: four sequences a thread
+    // prefix sums of the sequences' tiles: up to four sequences a thread
+    i64 all;
     {
-        i64 v[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = 0;
-            const int b = 4 * tid + i;
-            if (b < a.c.n_seqs)
-                v[i] = tiles_of(a, b);
-            sum += v[i];
-        }
+        const int per = (a.c.n_seqs + kThreads - 1) / kThreads;
+        i64 sum = 0;
+#pragma unroll 1
+        for (int i = 0; i < per; ++i)
+            if (per * tid + i < a.c.n_seqs)
+                sum += tiles_of<BLK>(a, per * tid + i);
         i64 incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -247,31 +263,42 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         __syncthreads();
         i64 at = incl - sum;
-        for (int w = 0; w < warp; ++w)
-            at += scan[w];
+        all = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = 4 * tid + i;
-            if (b <= a.c.n_seqs)
-                pre[b] = at;
-            at += v[i];
+        for (int w = 0; w < kWarps; ++w) {
+            at += w < warp ? scan[w] : 0;
+            all += scan[w];
         }
-        if (tid == kThreads - 1 && a.c.n_seqs == 4 * kThreads)
-            pre[a.c.n_seqs] = at;
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) {
+            const int b = per * tid + i;
+            if (b < a.c.n_seqs) {
+                pre[b] = (int)at;
+                if (per > 1)
+                    at += tiles_of<BLK>(a, b);
+            }
+        }
+        if (tid == 0)
+            pre[a.c.n_seqs] = (int)all;
         __syncthreads();
     }
-    const i64 N = pre[a.c.n_seqs];
-    const int G = (int)min((i64)gridDim.x, N);                // CTAs with work
+    if (all > 0x7fffffff) {                                   // more than 2^31 tiles of 4 KB at least
+        if (tid == 0)
+            atomicExch(status, MOE_ERR_DEVICE_FAULT);
+        return;
+    }
+    const int N = (int)all, G = min((int)gridDim.x, N);       // CTAs with work
     if ((int)blockIdx.x >= G)
         return;
-    // the CTA's run, by its ends' moves to the start of an item where that is short:
-    // a join over CTAs costs more than two more tiles a group
+    // the CTA's run of tiles, its ends moved to the start of an item where that is
+    // short: a join over CTAs costs more than two more tiles a group
+    const int each = N / G, more = N - each * G;              // CTA c begins with tile c each + min(c, more)
     if (warp < 2) {
-        const i64 at = N * (blockIdx.x + warp) / G;
-        i64 end = at;
+        const int c = blockIdx.x + warp, at = c * each + min(c, more);
+        int end = at;
         if (at < N) {
             Item it;
-            find_item(a, pre, at, it);
+            find_item<BLK>(a, pre, at, it);
             if (it.jhi - it.jlo + 1 <= C::WHOLE)
                 end = it.t0;
         }
@@ -279,26 +306,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             s_run[warp] = end;
     }
     __syncthreads();
-    const i64 ct0 = s_run[0], ct1 = s_run[1], gid = (i64)blockIdx.x * C::NG + grp;
+    const int ct0 = s_run[0], ct1 = s_run[1], gid = blockIdx.x * C::NG + grp;
     if (ct0 == ct1)
         return;
-    const i64 t_begin = ct0 + (ct1 - ct0) * grp / C::NG, t_end = ct0 + (ct1 - ct0) * (grp + 1) / C::NG;
+    const int mine = (ct1 - ct0) / C::NG, left = (ct1 - ct0) % C::NG;
+    const int t_begin = ct0 + grp * mine + min(grp, left), t_end = t_begin + mine + (grp < left);
 
     uint8_t* ring = sm + grp * C::NS * C::STAGE;
     float* hdr = reinterpret_cast<float*>(sm + C::OFF_HDR) + grp * C::NS * 4;
     const uint64_t pol = tc::l2_evict_first();
-    float* slot = ws + ((i64)gridDim.x * 2 + gid) * slot_floats();                      // this group's
+    float* slot = ws + (i64)(gridDim.x * 2 + gid) * slot_floats();                      // this group's
 
     // the tile stream: warp 0 of the group keeps its own place in it, NS - 1 tiles ahead
     Item pit{};
-    i64 pt = t_begin;
-    int pj = 0, pid = 0;
+    int pt = t_begin, pj = 0, pid = 0, pst = 0, pround = 0;
     auto table_at = [&](const Item& it, int j) { return a.c.table[(i64)it.b * a.c.table_stride + j]; };
     auto produce = [&]() {
-        const int st = (int)((pt - t_begin) % C::NS);
-        const i64 round = (pt - t_begin) / C::NS;
-        if (round > 0)
-            tc::mbar_wait(empty + st, (uint32_t)((round - 1) & 1), status);
+        const int st = pst;
+        if (pround > 0)
+            tc::mbar_wait(empty + st, (uint32_t)((pround - 1) & 1), status);
+        if (++pst == C::NS) {
+            pst = 0;
+            ++pround;
+        }
         const bool valid = pid >= 0 && pid < a.c.num_blocks;
         if (lane == 0) {
             float* hd = hdr + st * 4;
@@ -318,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         __syncwarp();
         if (++pt < t_end) {
             if (++pj > pit.jhi) {
-                next_item(a, pre, pit);
+                next_item<BLK>(a, pre, pit);
                 pj = pit.jlo;
             }
             pid = table_at(pit, pj);     // used by the next call, a tile later
@@ -327,20 +357,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
 
     if (t_begin < t_end) {
         Item it;
-        find_item(a, pre, t_begin, it);
-        int j = it.jlo + (int)(t_begin - it.t0);
+        find_item<BLK>(a, pre, t_begin, it);
+        int j = it.jlo + t_begin - it.t0;
         if (sub == 0) {
             pit = it;
             pj = j;
             pid = table_at(it, j);
-            for (int i = 0; i < C::NS - 1 && pt < t_end; ++i)
-                produce();
         }
         const int r = lane >> 2, c = lane & 3;
-        i64 t = t_begin;
+        int t = t_begin, cst = 0;
+        uint32_t phase = 0;
         while (t < t_end) {
             // ---- an item, or the part of it in this group's run
-            const i64 item_end = it.t0 + it.jhi - it.jlo + 1, seg_end = min(item_end, t_end);
+            const int item_end = it.t0 + it.jhi - it.jlo + 1, seg_end = min(item_end, t_end);
             const int rows = min(kRows, it.n * a.group - it.rt * kRows);
             uint32_t qf[D / 16][4];
             float f[2];                  // score = sum * block's scale * f
@@ -396,8 +425,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
 
             int st = 0;
             for (; t < seg_end; ++t, ++j) {
-                st = (int)((t - t_begin) % C::NS);
-                tc::mbar_wait(full + st, (uint32_t)((t - t_begin) / C::NS & 1), status);
+                // fill the ring: at first all of it, then the stage of the tile before
+                if (sub == 0)
+#pragma unroll 1
+                    while (pt < t_end && pt < t + C::NS)
+                        produce();
+                st = cst;
+                tc::mbar_wait(full + st, phase, status);
+                if (++cst == C::NS) {
+                    cst = 0;
+                    phase ^= 1;
+                }
                 const float4 hd = *reinterpret_cast<const float4*>(hdr + st * 4);
                 const uint8_t* kt = ring + st * C::STAGE + sub * kSub * D;
                 const uint8_t* vt = ring + st * C::STAGE + BLK * D + sub * kSub;
@@ -513,8 +551,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                     __syncwarp();
                     if (lane == 0)
                         tc::mbar_arrive(empty + st);
-                    if (sub == 0 && pt < t_end)
-                        produce();
                 }
             }
 
@@ -562,9 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             group_sync(1 + grp, C::GW * 32);
             if (lane == 0)
                 tc::mbar_arrive(empty + st);
-            if (sub == 0 && pt < t_end)
-                produce();
-            next_item(a, pre, it);
+            next_item<BLK>(a, pre, it);
             j = it.jlo;
         }
     }
@@ -580,27 +614,46 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             ++first;
             continue;
         }
-        const i64 t0 = pieces[first].t0;
+        const int t0 = pieces[first].t0;
         const Place place = pieces[first].p;
-        int last = first + 1;
-        while (last < 2 * C::NG && (!pieces[last].where || pieces[last].t0 == t0))
+        int last = first + 1, nstage = pieces[first].where == kStage, slot_at = nstage ? -1 : first >> 1;
+        // the last pieces of some groups, and the first of the next one; or that alone
+        while (last < 2 * C::NG && (!pieces[last].where || pieces[last].t0 == t0)) {
+            nstage += pieces[last].where == kStage;
+            if (pieces[last].where == kSlot)
+                slot_at = last >> 1;
             ++last;
+        }
+        const int g0 = first >> 1;
         const bool done = t0 >= ct0 && pieces[first].t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), col = x % (D / 4) * 4;
+            const int row = x / (D / 4), col = x % (D / 4) * 4, at = ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
             Sum sum;
-#pragma unroll 1
-            for (int k = first; k < last; ++k) {
-                if (pieces[k].where == kSlot) {
-                    sum.from_slot(gslots + (k >> 1) * slot_floats(), D, row, col);
-                } else if (pieces[k].where == kStage) {
-                    const int g = k >> 1;
-                    const float* od = reinterpret_cast<const float*>(sm + (g * C::NS + pieces[k].stage) * C::STAGE);
-#pragma unroll
-                    for (int w = 0; w < C::GW; ++w)
-                        sum.add(mls[(g * C::GW + w) * kRows + row],
-                                *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+            if (slot_at >= 0)
+                sum.from_slot(gslots + slot_at * slot_floats(), D, row, col);
+            if (nstage) {
+                // all maxima first: the parts' weights then do not wait for one another
+                float M = sum.m;
+#pragma unroll 4
+                for (int w = g0 * C::GW; w < (last + 1 >> 1) * C::GW; ++w)
+                    if (pieces[w / C::GW * 2 + 1].where && pieces[w / C::GW * 2 + 1].t0 == t0)
+                        M = fmaxf(M, mls[w * kRows + row].x);
+                const float keep = ex2(sum.m - M);
+                sum.m = M;
+                sum.l *= keep;
+                sum.v.x *= keep, sum.v.y *= keep, sum.v.z *= keep, sum.v.w *= keep;
+#pragma unroll 4
+                for (int w = g0 * C::GW; w < (last + 1 >> 1) * C::GW; ++w) {
+                    const Piece& p = pieces[w / C::GW * 2 + 1];
+                    if (!p.where || p.t0 != t0)
+                        continue;
+                    const float* od = reinterpret_cast<const float*>(sm + (w / C::GW * C::NS + p.stage) * C::STAGE);
+                    const float2 ml = mls[w * kRows + row];
+                    const float4 y = *reinterpret_cast<const float4*>(od + (w % C::GW * kRows + row) * D + at);
+                    const float f = ex2(ml.x - M);
+                    sum.l += ml.y * f;
+                    sum.v.x += y.x * f, sum.v.y += y.y * f, sum.v.z += y.z * f, sum.v.w += y.w * f;
                 }
             }
             if (done)
@@ -616,13 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     }
 
     // ---- items that span CTAs: the last one to arrive joins them all
+    auto cta_of = [&](int t) {
+        const int big = more * (each + 1);
+        return t < big ? t / (each + 1) : more + (t - big) / each;
+    };
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         if (!(across >> which & 1))
             continue;
         const Piece& p = pieces[cross[which]];
         const Place place = p.p;
-        const int ca = (int)(((p.t0 + 1) * G - 1) / N), cb = (int)((p.t1 * G - 1) / N);   // CTAs of its first and last tile
+        const int ca = cta_of(p.t0), cb = cta_of(p.t1 - 1);               // of its first and last tile
         __threadfence();
         __syncthreads();
         if (tid == 0) {
