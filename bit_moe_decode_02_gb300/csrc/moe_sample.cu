@@ -100,6 +100,33 @@ __device__ __forceinline__ T warp_scan(T v)
     return v;
 }
 
+// Inclusive prefix sums over the CTA's threads, of two values at once; the totals stay
+// in red[kWarps - 1] and red2[kWarps - 1].
+__device__ __forceinline__ void block_scan2(u64& v, u64& w, u64* red, u64* red2)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(~0u, v, o), y = __shfl_up_sync(~0u, w, o);
+        v += lane >= o ? x : 0;
+        w += lane >= o ? y : 0;
+    }
+    if (lane == 31) {
+        red[warp] = v;
+        red2[warp] = w;
+    }
+    __syncthreads();
+    if (warp < 2) {
+        u64* r = warp ? red2 : red;
+        r[lane] = warp_scan(r[lane]);
+    }
+    __syncthreads();
+    if (warp) {
+        v += red[warp - 1];
+        w += red2[warp - 1];
+    }
+}
+
 // Inclusive prefix sums over the CTA's threads.
 __device__ __forceinline__ u64 block_scan(u64 v, u64* red)
 {
@@ -141,6 +168,27 @@ __device__ __forceinline__ u64 sort_first(u64 v, int n, bool descending, u64* bu
     return v;
 }
 
+// The vector at p whose first element is number i0 of a row of V: only the row's
+// own elements are read.
+template <bool BF16>
+__device__ __noinline__ uint4 load_end(const uint8_t* p, int i0, int V)
+{
+    constexpr int VEC = BF16 ? 8 : 4;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = BF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        if (i0 + e >= 0 && i0 + e < V) {
+            if (BF16)
+                w[e >> 1] = __byte_perm(w[e >> 1], reinterpret_cast<const uint16_t*>(p)[e], e & 1 ? 0x5410 : 0x3254);
+            else
+                w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <bool BF16>
 struct Part {
     // The warp's vectors of 16 bytes of the row; vector v holds elements v * VEC - lead ..
@@ -154,21 +202,7 @@ struct Part {
         const int i0 = v * VEC - lead;
         if (v < v1 && i0 >= 0 && i0 + VEC <= V)
             return __ldg(reinterpret_cast<const uint4*>(base + (long long)v * 16));
-        // the row's ends: only its own elements are read
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = BF16 ? 0xff80ff80u : 0xff800000u;
-        if (v < v1)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (i0 + e >= 0 && i0 + e < V) {
-                    if (BF16)
-                        w[e >> 1] = __byte_perm(w[e >> 1], reinterpret_cast<const uint16_t*>(base + (long long)v * 16)[e], e & 1 ? 0x5410 : 0x3254);
-                    else
-                        w[e] = reinterpret_cast<const uint32_t*>(base + (long long)v * 16)[e];
-                }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return load_end<BF16>(base + (long long)v * 16, v < v1 ? i0 : V, V);
     }
     // f(value, index) for each element of vector v
     template <class F>
@@ -181,19 +215,34 @@ struct Part {
     }
     template <class F>
     __device__ __forceinline__ void visit(int v, F f) const { take(v, load(v), f); }
-    // all of the warp's elements, with the next loads out before the last are used
-    template <class F>
+    // all of the warp's elements, U vectors a lane at a time.  U = 1 keeps the code of
+    // a pass small: it runs once, and a short call's time is that of fetching
+    // instructions; the next vector is on its way meanwhile
+    template <int U, class F>
     __device__ __forceinline__ void each(F f) const
     {
-        constexpr int U = BF16 ? 2 : 4;
-        for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32 * U) {
-            uint4 q[U];
+        const int first = v0 + (threadIdx.x & 31);
+        if constexpr (U > 1) {
+#pragma unroll 1
+            for (int v = first; v < v1; v += 32 * U) {
+                uint4 q[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                q[k] = load(v + 32 * k);
+                for (int k = 0; k < U; ++k)
+                    q[k] = load(v + 32 * k);
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                take(v + 32 * k, q[k], f);
+                for (int k = 0; k < U; ++k)
+                    take(v + 32 * k, q[k], f);
+            }
+        } else {
+            uint4 q = load(first), r = load(first + 32);
+#pragma unroll 1
+            for (int v = first; v < v1; v += 32) {
+                const uint4 now = q;
+                q = r;
+                if (v + 64 < v1)
+                    r = load(v + 64);
+                take(v, now, f);
+            }
         }
     }
 };
@@ -238,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     {
         float m = -INFINITY;
         int at = 0;                          // a row of -inf (or NaN): index 0
-        part.each([&](float l, int i) {
+        part.template each<BF16 ? 2 : 4>([&](float l, int i) {
             if (l > m) {
                 m = l;
                 at = i;
@@ -321,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     uint32_t key = 0, ties = 0;
     if ((k > 0 && k < a.V) || by_p) {
         // ---- 2. counts in 1/256 of z
-        part.each([&](float l, int i) {
+        part.template each<1>([&](float l, int i) {
             const int b = Row::fine(r.z(l));
             if (b < kFine)
                 atomicAdd(&sh.fine[b], 1u);
@@ -364,7 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             if (lane == 0)
                 sh.sq[warp] = sq;
         }
-        const u64 nb = block_scan((u64)nsum, sh.red) - nsum, wb = block_scan(wsum, sh.red2) - wsum;
+        u64 nb = nsum, wb = wsum;
+        block_scan2(nb, wb, sh.red, sh.red2);
+        nb -= nsum;
+        wb -= wsum;
         const bool by_k = k > 0 && (u64)k < sh.red[kWarps - 1];
         u64 about = sh.red2[kWarps - 1];     // weight of what top-k leaves, but for the bins' width
         if (by_k) {
@@ -424,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             // ---- 3. weights before and between the bands; their tokens into the first CTA's list
             const bool sums = !alone || (by_p && (!by_k || apart));
             u64 kept = 0, raw = 0, mid = 0;
-            part.each([&](float l, int i) {
+            part.template each<1>([&](float l, int i) {
                 const float z = r.z(l);
                 const int b = Row::fine(z);
                 if (b < p0 || (b > p1 && b < kb)) {
@@ -502,9 +554,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
                 bool in = x != 0;
                 if (by_p) {
-                    const u64 own = tid < (int)n_p ? x : 0, cum = block_scan(own, sh.red);
+                    const u64 own = tid < (int)n_p ? x : 0;
+                    u64 cum = own, rest = x - own;
+                    block_scan2(cum, rest, sh.red, sh.red2);
                     const u64 in_band = sh.red[kWarps - 1];
-                    block_scan(x - own, sh.red2);
                     const u64 need = one_for_all(need_of, raw + in_band + mid + sh.red2[kWarps - 1]);
                     in = in && tid < (int)n_p && raw + cum - own < need;
                     found = raw < need && raw + in_band >= need;     // the share is reached within the band
@@ -585,8 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                         w += (u64)s->w0[tid] + ((u64)s->w1[tid] << 11) + ((u64)s->w2[tid] << 22);
                         n += s->cnt[tid];
                     }
-                w = block_scan(w, sh.red);
-                n = block_scan(n, sh.red);
+                block_scan2(w, n, sh.red, sh.red2);
                 if (tid < kBins) {
                     sh.tw[tid] = w;
                     sh.tcnt[tid] = (uint32_t)n;
@@ -631,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 return lo;
             };
             clear();
-            part.each([&](float l, int i) {
+            part.template each<1>([&](float l, int i) {
                 const float z = r.z(l);
                 const uint32_t w = Row::weight(z);
                 if (w)
@@ -661,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 while (true) {
                     const uint32_t width = (uint32_t)((range + kBins - 1) / kBins);
                     clear();
-                    part.each([&](float l, int i) {
+                    part.template each<1>([&](float l, int i) {
                         const uint32_t kk = order_key(l);
                         if (kk < lo || kk - lo >= range)
                             return;
@@ -698,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     if (!last) {
         u64 sum = 0;
         uint32_t eq = 0;
-        part.each([&](float l, int i) {
+        part.template each<1>([&](float l, int i) {
             const uint32_t w = Row::weight(r.z(l));
             if (cut) {
                 const uint32_t kk = order_key(l);
@@ -817,8 +869,11 @@ cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s)
     // CTAs a row: as few as take it; more while every row keeps its own SMs and a
     // CTA at least 2,048 tokens
     const int vectors = a.V / (a.logits_type == MOE_DT_BF16 ? 8 : 4) + 2;
+    // (clusters of 8 find room beside one another on half of the SMs only: 16 rows of
+    // 8 CTAs took twice the time of 16 rows of 4)
     int c = 1;
-    while (c < kMostCluster && (vectors > c * kMostVectors || (2ll * c * a.M <= num_sms && a.V >= 2 * c * 2048)))
+    while (c < kMostCluster && (vectors > c * kMostVectors ||
+                                ((c < 4 ? 2ll : 4ll) * c * a.M <= num_sms && a.V >= 2 * c * 2048)))
         c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.M * c);
