@@ -60,8 +60,13 @@ struct Row {
     // -inf and NaN logits: -inf or NaN, of weight 0 and in no bin
     __device__ __forceinline__ float z(float l) const { return l == top ? 0.0f : __fmul_rn(__fsub_rn(l, top), inv_t); }
     __device__ __forceinline__ static uint32_t weight(float z) { return __float2uint_rn(expf(z) * 2147483648.0f); }
-    __device__ __forceinline__ static int fine(float z) { return z > -(float)kFine / 256.0f ? (int)(z * -256.0f) : kFine; }
-    __device__ __forceinline__ static float fine_middle(int b) { return ((float)b + 0.5f) * (-1.0f / 256.0f); }
+    // 1/256 of z that a finite logit lies nearest to; beyond kFine for -inf and NaN.
+    // Adding 2^23 rounds to an integer in the low bits
+    __device__ __forceinline__ uint32_t fine(float l) const
+    {
+        return __float_as_uint(__fmaf_rn(__fsub_rn(top, l), inv_t * 256.0f, 8388608.0f)) - 0x4b000000u;
+    }
+    __device__ __forceinline__ static float fine_middle(int b) { return (float)b * (-1.0f / 256.0f); }
     __device__ __forceinline__ static int bin(float z) { return z > -(float)kBins / 32.0f ? (int)(z * -32.0f) : kBins - 1; }
 };
 
@@ -204,14 +209,16 @@ struct Part {
             return __ldg(reinterpret_cast<const uint4*>(base + (long long)v * 16));
         return load_end<BF16>(base + (long long)v * 16, v < v1 ? i0 : V, V);
     }
-    // f(value, index) for each element of vector v
+    // f(values, index of the first) of vector v
     template <class F>
     __device__ __forceinline__ void take(int v, uint4 q, F f) const
     {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        float l[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-            f(BF16 ? __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]), v * VEC - lead + e);
+            l[e] = BF16 ? __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16) : __uint_as_float(w[e]);
+        f(l, v * VEC - lead);
     }
     template <class F>
     __device__ __forceinline__ void visit(int v, F f) const { take(v, load(v), f); }
@@ -255,12 +262,95 @@ __device__ __forceinline__ u64 warp_sum(u64 v)
     return v;
 }
 
+__device__ __forceinline__ u64 block_sum(u64 v, u64* red)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(red[threadIdx.x & 31]);
+}
+
+// Of the entries e of the threads that are `in`, largest first: the one at which
+// the running sum of f reaches `target` (which all of them together reach).
+// Rounds of 1,024 equal digits of the range that is left, till few are.
+__device__ __noinline__ u64 select_last(u64 e, bool in, u64 f, u64 target, Shared& sh)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t *lo = sh.fine, *hi = sh.fine + kThreads;
+#pragma unroll 1
+    while (true) {
+        u64 a = in ? e : ~0ull, b = in ? e : 0;
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) {
+            a = min(a, __shfl_xor_sync(~0u, a, o));
+            b = max(b, __shfl_xor_sync(~0u, b, o));
+        }
+        __syncthreads();
+        if (lane == 0) {
+            sh.red[warp] = a;
+            sh.red2[warp] = b;
+        }
+        lo[tid] = hi[tid] = 0;
+        if (tid == 0)
+            sh.nlist = 0;
+        __syncthreads();
+        a = sh.red[lane];
+        b = sh.red2[lane];
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) {
+            a = min(a, __shfl_xor_sync(~0u, a, o));
+            b = max(b, __shfl_xor_sync(~0u, b, o));
+        }
+        const int s = max(0, 54 - __clzll((long long)(b - a)));          // the range in 10 bits
+        const uint32_t d = in ? (uint32_t)((b - e) >> s) : 0;            // larger entries first
+        if (in) {
+            atomicAdd(lo + d, (uint32_t)f & 0xffffu);
+            atomicAdd(hi + d, (uint32_t)(f >> 16));
+        }
+        __syncthreads();
+        const u64 own = lo[tid] + ((u64)hi[tid] << 16), run = block_scan(own, sh.red);
+        if (run >= target && run - own < target) {
+            sh.found = tid;
+            sh.last = run - own;
+        }
+        __syncthreads();
+        in = in && d == (uint32_t)sh.found;
+        target -= sh.last;
+        if (__syncthreads_count(in) <= 64)
+            break;
+    }
+    // the few: each counts what is before it
+    u64* few = reinterpret_cast<u64*>(sh.fine);
+    u64* few_f = few + 64;
+    uint32_t at = 0;
+    if (in) {
+        at = atomicAdd(&sh.nlist, 1u);
+        few[at] = e;
+        few_f[at] = f;
+    }
+    __syncthreads();
+    if (in) {
+        u64 run = 0;
+        for (uint32_t j = 0; j < sh.nlist; ++j)
+            run += few[j] >= e ? few_f[j] : 0;
+        if (run >= target && run - f < target)
+            sh.last = e;
+    }
+    __syncthreads();
+    const u64 r = sh.last;
+    __syncthreads();
+    return r;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                     // waited for before the first access to another CTA's memory
+    constexpr int VEC = Part<BF16>::VEC;
     const int c = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / c, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -287,11 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     {
         float m = -INFINITY;
         int at = 0;                          // a row of -inf (or NaN): index 0
-        part.template each<BF16 ? 2 : 4>([&](float l, int i) {
-            if (l > m) {
-                m = l;
-                at = i;
-            }
+        part.template each<BF16 ? 2 : 4>([&](const float (&l)[VEC], int i) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (l[e] > m) {
+                    m = l[e];
+                    at = i + e;
+                }
         });
         best = (u64)order_key(m) << 32 | (0xffffffffu - (uint32_t)at);
     }
@@ -370,10 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     uint32_t key = 0, ties = 0;
     if ((k > 0 && k < a.V) || by_p) {
         // ---- 2. counts in 1/256 of z
-        part.template each<1>([&](float l, int i) {
-            const int b = Row::fine(r.z(l));
-            if (b < kFine)
-                atomicAdd(&sh.fine[b], 1u);
+        part.template each<2>([&](const float (&l)[VEC], int) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const uint32_t b = r.fine(l[e]);
+                if (b < (uint32_t)kFine)
+                    atomicAdd(&sh.fine[b], 1u);
+            }
         });
         const int tps = (kThreads + c - 1) / c;              // threads whose bins one CTA adds up
         if (c > 1) {
@@ -471,29 +566,57 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         if (alone)
             p0 = 0;
         const uint32_t before = through(p0 - 1), n_p = through(p1) - before, n_list = n_p + n_k, before_k = through(kb - 1);
-        all = !by_k && !by_p;                                // fewer tokens than k have weight
-        if (!all && n_list <= kList) {
+        const bool odd = r.top == INFINITY;                  // only infinities have weight, and none of them a bin
+        all = !by_k && !by_p && !odd;                        // fewer tokens than k have weight
+        if (!all && !odd && n_list <= kList) {
             // ---- 3. weights before and between the bands; their tokens into the first CTA's list
             const bool sums = !alone || (by_p && (!by_k || apart));
             u64 kept = 0, raw = 0, mid = 0;
-            part.template each<1>([&](float l, int i) {
-                const float z = r.z(l);
-                const int b = Row::fine(z);
-                if (b < p0 || (b > p1 && b < kb)) {
-                    if (sums) {
-                        const uint32_t x = Row::weight(z);
-                        if (b > p1) {
-                            mid += x;
-                        } else {
-                            raw += x;
-                            kept += x >= least ? x : 0;
-                        }
+            auto gather = [&](float l, int i) {
+                const uint32_t at = atomicAdd(cl.map_shared_rank(&sh.nlist, 0), 1u);
+                *cl.map_shared_rank(&sh.list[at], 0) = (u64)order_key(l) << 32 | (0xffffffffu - (uint32_t)i);
+            };
+            // bands q0 .. q0 + qn and qa; bins from `end` on are beyond top-k
+            const uint32_t q0 = p0, qn = min(p1, kFine - 1) - p0, qa = apart ? (uint32_t)kb : ~0u, end = by_k ? (uint32_t)kb + 1 : ~0u;
+            const bool floor = least > 0;
+            if (sums) {
+                u64 tot = 0;
+                part.template each<BF16 ? 1 : 2>([&](const float (&l)[VEC], int i) {
+                    uint32_t x[VEC], b[VEC];
+                    bool hit = false;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        b[e] = r.fine(l[e]);
+                        x[e] = Row::weight(r.z(l[e]));
+                        x[e] = b[e] < end ? x[e] : 0;
+                        tot += x[e];
+                        x[e] = b[e] < q0 ? x[e] : 0;
+                        raw += x[e];
+                        hit = hit || b[e] - q0 <= qn || b[e] == qa;
                     }
-                } else if (b < kFine && (b <= p1 || (apart && b == kb))) {
-                    const uint32_t at = atomicAdd(cl.map_shared_rank(&sh.nlist, 0), 1u);
-                    *cl.map_shared_rank(&sh.list[at], 0) = (u64)order_key(l) << 32 | (0xffffffffu - (uint32_t)i);
-                }
-            });
+                    if (floor)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            kept += x[e] >= least ? x[e] : 0;
+                    if (hit)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (b[e] - q0 <= qn || b[e] == qa)
+                                gather(l[e], i + e);
+                });
+                mid = tot - raw;                             // the bands' own weights are taken off below
+                if (!floor)
+                    kept = raw;
+            } else {
+                part.template each<2>([&](const float (&l)[VEC], int i) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const uint32_t b = r.fine(l[e]);
+                        if (b - q0 <= qn || b == qa)
+                            gather(l[e], i + e);
+                    }
+                });
+            }
             if (sums) {
                 kept = warp_sum(kept);
                 raw = warp_sum(raw);
@@ -525,49 +648,84 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 int n2 = 32;
                 while (n2 < (int)n_list)
                     n2 <<= 1;
-                u64 e;
+                u64 e = tid < (int)n_list ? sh.list[tid] : 0, x = 0;
+                bool in = false;
                 const bool few = n_list <= kThreads / 4;
-                if (few) {
-                    // each place in the order by counting what is before it, four threads an entry
-                    const int i = tid >> 2;
-                    e = i < (int)n_list ? sh.list[i] : 0;
-                    int place = 0;
-                    for (int j = tid & 3; j < (int)n_list; j += 4)
-                        place += sh.list[j] > e;
-                    place += __shfl_xor_sync(~0u, place, 1);
-                    place += __shfl_xor_sync(~0u, place, 2);
+                if (sums) {
+                    // the gathered tokens' weights were added to what lies between the bands
+                    u64 w = tid < (int)n_list ? Row::weight(r.z(key_value((uint32_t)(e >> 32)))) : 0;
+                    w = warp_sum(w);
+                    if (lane == 0)
+                        sh.red[warp] = w;
                     __syncthreads();
-                    if (i < (int)n_list && (tid & 3) == 0)
-                        sh.list[place] = e;
+                    mid -= warp_sum(sh.red[lane]);
                     __syncthreads();
-                    e = tid < (int)n_list ? sh.list[tid] : 0;
+                }
+                if (!alone && !(by_k && by_p && !apart)) {
+                    // only the last member is wanted: no order is needed
+                    const uint32_t key = (uint32_t)(e >> 32);
+                    const u64 w = tid < (int)n_list ? Row::weight(r.z(key_value(key))) : 0;
+                    const uint32_t b = r.fine(key_value(key));
+                    const bool first = tid < (int)n_list && b - q0 <= qn, second = tid < (int)n_list && !first;
+                    u64 cut_at;
+                    if (by_p) {
+                        u64 in_band = first ? w : 0, beyond = 0;
+                        if (apart) {
+                            const u64 lk = select_last(e, second, 1, (u64)k - before_k, sh);
+                            beyond = second && e >= lk ? w : 0;
+                        }
+                        in_band = block_sum(in_band, sh.red);
+                        beyond = block_sum(beyond, sh.red);
+                        const u64 need = one_for_all(need_of, raw + in_band + mid + beyond);
+                        found = raw < need && raw + in_band >= need;     // the share is reached within the band
+                        cut_at = found ? select_last(e, first, w, need - raw, sh) : ~0ull;
+                    } else {
+                        cut_at = select_last(e, first, 1, (u64)k - before, sh);
+                    }
+                    if (tid == 0)
+                        sh.last = ~cut_at;
+                    __syncthreads();
                 } else {
-                    e = tid < (int)n_list ? sh.list[tid] : 0;
+                    if (few) {
+                        // each place in the order by counting what is before it, four threads an entry
+                        const int i = tid >> 2;
+                        e = i < (int)n_list ? sh.list[i] : 0;
+                        int place = 0;
+                        for (int j = tid & 3; j < (int)n_list; j += 4)
+                            place += sh.list[j] > e;
+                        place += __shfl_xor_sync(~0u, place, 1);
+                        place += __shfl_xor_sync(~0u, place, 2);
+                        __syncthreads();
+                        if (i < (int)n_list && (tid & 3) == 0)
+                            sh.list[place] = e;
+                        __syncthreads();
+                        e = tid < (int)n_list ? sh.list[tid] : 0;
+                    } else {
+                        __syncthreads();
+                        if (tid < n2)
+                            e = sort_first(e, n2, true, sh.list);
+                    }
+                    // this thread's place in the order, and its weight if top-k takes it
+                    const uint32_t at = tid < (int)n_p ? before + tid : before_k + (tid - n_p);
+                    if (tid < (int)n_list && (!by_k || at < (uint32_t)k))
+                        x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
+                    in = x != 0;
+                    if (by_p) {
+                        const u64 own = tid < (int)n_p ? x : 0;
+                        u64 cum = own, rest = x - own;
+                        block_scan2(cum, rest, sh.red, sh.red2);
+                        const u64 in_band = sh.red[kWarps - 1];
+                        const u64 need = one_for_all(need_of, raw + in_band + mid + sh.red2[kWarps - 1]);
+                        in = in && tid < (int)n_p && raw + cum - own < need;
+                        found = raw < need && raw + in_band >= need;
+                    }
                     __syncthreads();
-                    if (tid < n2)
-                        e = sort_first(e, n2, true, sh.list);
+                    if (!few && tid < n2)
+                        sh.list[tid] = e;
+                    if (in)
+                        atomicMax(&sh.last, ~e);                      // the last one has the largest complement
+                    __syncthreads();
                 }
-                // this thread's place in the order, and its weight if top-k takes it
-                const uint32_t at = tid < (int)n_p ? before + tid : before_k + (tid - n_p);
-                u64 x = 0;
-                if (tid < (int)n_list && (!by_k || at < (uint32_t)k))
-                    x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
-                bool in = x != 0;
-                if (by_p) {
-                    const u64 own = tid < (int)n_p ? x : 0;
-                    u64 cum = own, rest = x - own;
-                    block_scan2(cum, rest, sh.red, sh.red2);
-                    const u64 in_band = sh.red[kWarps - 1];
-                    const u64 need = one_for_all(need_of, raw + in_band + mid + sh.red2[kWarps - 1]);
-                    in = in && tid < (int)n_p && raw + cum - own < need;
-                    found = raw < need && raw + in_band >= need;     // the share is reached within the band
-                }
-                __syncthreads();
-                if (!few && tid < n2)
-                    sh.list[tid] = e;
-                if (in)
-                    atomicMax(&sh.last, ~e);                          // the last one has the largest complement
-                __syncthreads();
                 if (alone && found) {
                     if (!in || x < least)
                         x = 0;
@@ -603,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                                        : static_cast<const float*>(a.logits)[row * a.stride + i], total);
                     }
                 }
-                last = ~sh.last;
+                last = ~sh.last;                     // (select_last left other things there before)
                 __syncthreads();
                 if (tid < c)
                     *cl.map_shared_rank(&sh.last, tid) = found ? last : 0;
@@ -683,17 +841,20 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 return lo;
             };
             clear();
-            part.template each<1>([&](float l, int i) {
-                const float z = r.z(l);
-                const uint32_t w = Row::weight(z);
-                if (w)
-                    add(Row::bin(z), w);
+            part.template each<1>([&](const float (&l)[VEC], int) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float z = r.z(l[e]);
+                    const uint32_t w = Row::weight(z);
+                    if (w)
+                        add(Row::bin(z), w);
+                }
             });
             join();
             const u64 keep_w = tid < kBins ? sh.tw[tid] : 0;
             const uint32_t keep_n = tid < kBins ? sh.tcnt[tid] : 0;
             u64 total = sh.tw[kBins - 1];
-            const bool cut_k = by_k && (uint32_t)k < sh.tcnt[kBins - 1];
+            const bool cut_k = k > 0 && (uint32_t)k < sh.tcnt[kBins - 1];
             all = !cut_k && !by_p;
             for (int what = 0; what < 2; ++what) {
                 const bool weights = what == 1;
@@ -713,13 +874,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 while (true) {
                     const uint32_t width = (uint32_t)((range + kBins - 1) / kBins);
                     clear();
-                    part.template each<1>([&](float l, int i) {
-                        const uint32_t kk = order_key(l);
-                        if (kk < lo || kk - lo >= range)
-                            return;
-                        const uint32_t w = Row::weight(r.z(l));
-                        if (w)
-                            add(kBins - 1 - (int)((kk - lo) / width), w);   // larger keys first
+                    part.template each<1>([&](const float (&l)[VEC], int) {
+#pragma unroll 1
+                        for (int e = 0; e < VEC; ++e) {
+                            const uint32_t kk = order_key(l[e]);
+                            if (kk < lo || kk - lo >= range)
+                                continue;
+                            const uint32_t w = Row::weight(r.z(l[e]));
+                            if (w)
+                                add(kBins - 1 - (int)((kk - lo) / width), w);   // larger keys first
+                        }
                     });
                     join();
                     u64 rest = need - (weights ? wab : nab);
@@ -750,16 +914,23 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     if (!last) {
         u64 sum = 0;
         uint32_t eq = 0;
-        part.template each<1>([&](float l, int i) {
-            const uint32_t w = Row::weight(r.z(l));
-            if (cut) {
-                const uint32_t kk = order_key(l);
-                eq += kk == key;
-                sum += w >= least && kk > key ? w : 0;
-            } else {
-                sum += w >= least ? w : 0;
-            }
-        });
+        if (cut)
+            part.template each<1>([&](const float (&l)[VEC], int) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t w = Row::weight(r.z(l[e])), kk = order_key(l[e]);
+                    eq += kk == key;
+                    sum += w >= least && kk > key ? w : 0;
+                }
+            });
+        else
+            part.template each<BF16 ? 1 : 2>([&](const float (&l)[VEC], int) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t w = Row::weight(r.z(l[e]));
+                    sum += w >= least ? w : 0;
+                }
+            });
         sum = warp_sum(sum);
         eq = __reduce_add_sync(~0u, eq);
         if (lane == 0) {
@@ -810,19 +981,21 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
     float val[Part<BF16>::VEC];
     u64 s = 0;
     auto row_of = [&](int x) {
-        int j = 0;
         vl = nl = 0;
         s = 0;
-        seg.visit(seg.v0 + 32 * x + lane, [&](float l, int i) {
-            const uint32_t kk = order_key(l);
-            const bool tie = cut && kk == key;
-            const bool in = all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)i)) >= last : kk > key);
-            const uint32_t y = in ? Row::weight(r.z(l)) : 0;
-            nl += tie;
-            vl |= (uint32_t)tie << j;
-            w[j] = y >= least ? y : 0;
-            val[j] = l;
-            s += w[j++];
+        seg.visit(seg.v0 + 32 * x + lane, [&](const float (&l)[VEC], int i) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const uint32_t kk = order_key(l[e]);
+                const bool tie = cut && kk == key;
+                const bool in = all || (last ? ((u64)kk << 32 | (0xffffffffu - (uint32_t)(i + e))) >= last : kk > key);
+                const uint32_t y = in ? Row::weight(r.z(l[e])) : 0;
+                nl += tie;
+                vl |= (uint32_t)tie << e;
+                w[e] = y >= least ? y : 0;
+                val[e] = l[e];
+                s += w[e];
+            }
         });
     };
     row_of(warp);

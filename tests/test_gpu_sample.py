@@ -172,6 +172,14 @@ def test_values_that_are_not_finite():
     assert tok[5] == 17
 
 
+def test_filters_among_infinities():
+    l = rows(3, 5000, 8)
+    l[:, 100] = l[:, 4000] = l[:, 4500] = math.inf
+    tok, lp = sample(l, None, [1, 2, 0], [1.0, 1.0, 0.5], None, [0.9] * 3)
+    assert tok.tolist() == [100, 4000, 4000]
+    assert np.allclose(lp, [0.0, -math.log(2), -math.log(2)], atol=1e-6)
+
+
 def test_ends_of_u_and_of_the_filters():
     l = rows(1, 1000, 2)
     kept = torch.sort(torch.topk(l[0], 10).indices).values.tolist()
