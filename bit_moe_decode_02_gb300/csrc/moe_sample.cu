@@ -13,11 +13,11 @@
 //     bin that the counts name, top-p in one of the few that the counts times the bins'
 //     middle weights leave open.
 //  3. One pass adds up the weights before and between those bins (per warp, in the
-//     vocabulary's order) and gathers the bins' own tokens, which one CTA sorts: the
-//     last member of the kept set is found exactly.  Where all tokens that may be
-//     kept are in the list (top-k of some hundreds, peaked rows), that CTA draws.
+//     vocabulary's order) and gathers the bins' own tokens in one CTA, which picks
+//     the last member of the kept set from them.  Where all tokens that may be kept
+//     are in the list (top-k of some hundreds, peaked rows), that CTA orders it and draws.
 //  4. Else the warp in whose part the target lies walks it.
-// Rows whose bins hold more than 1,024 tokens (thousands of equal logits, high
+// Rows whose bins hold more than 4,096 tokens (thousands of equal logits, high
 // temperatures) find the last member by histograms of counts and weights that
 // narrow a bin down to one key (the logit's order-preserving bits), and how many of
 // the tokens that share the key are in; those take a few more passes.
@@ -39,7 +39,9 @@ constexpr int kMostVectors = 32 * 32 * kWarps;   // 16-byte vectors of a CTA's p
 constexpr int kBins = 768;                 // of 1/32 of z: weights are 0 from z = -22.2 on
 constexpr int kFine = 5760;               // of 1/256 of z
 constexpr int kFinePer = (kFine + kThreads - 1) / kThreads;
-constexpr int kList = kThreads;
+constexpr int kSort = kThreads;            // tokens that one CTA orders, one a thread
+constexpr int kEach = 4;
+constexpr int kList = kEach * kThreads;    // tokens that the cut's last member is picked from
 typedef unsigned long long u64;
 
 // Larger float, larger key; NaN below everything, as -inf; -0 as +0.
@@ -272,25 +274,39 @@ __device__ __forceinline__ u64 block_sum(u64 v, u64* red)
     return warp_sum(red[threadIdx.x & 31]);
 }
 
-// Of the entries e of the threads that are `in`, largest first: the one at which
-// the running sum of f reaches `target` (which all of them together reach).
-// Rounds of 1,024 equal digits of the range that is left, till few are.
-__device__ __noinline__ u64 select_last(u64 e, bool in, u64 f, u64 target, Shared& sh)
+// Of the list's n entries that are `member`s, largest first: the one at which the
+// running sum of f reaches `target` (which all of them together reach).  Rounds of
+// 1,024 equal digits of the range that is left, till few are.
+template <class In, class F>
+__device__ __forceinline__ u64 select_last(int n, In member, F f, u64 target, Shared& sh)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *lo = sh.fine, *hi = sh.fine + kThreads;
+    u64 from = 0, to = ~0ull;                // what is left: from <= e <= to
 #pragma unroll 1
     while (true) {
-        u64 a = in ? e : ~0ull, b = in ? e : 0;
+        u64 a = ~0ull, b = 0;
+        int count = 0;
+#pragma unroll 1
+        for (int i = tid; i < n; i += kThreads) {
+            const u64 e = sh.list[i];
+            if (e >= from && e <= to && member(e)) {
+                a = min(a, e);
+                b = max(b, e);
+                ++count;
+            }
+        }
 #pragma unroll 1
         for (int o = 16; o; o >>= 1) {
             a = min(a, __shfl_xor_sync(~0u, a, o));
             b = max(b, __shfl_xor_sync(~0u, b, o));
         }
+        count = __reduce_add_sync(~0u, count);
         __syncthreads();
         if (lane == 0) {
             sh.red[warp] = a;
             sh.red2[warp] = b;
+            sh.warp_ties[warp] = count;
         }
         lo[tid] = hi[tid] = 0;
         if (tid == 0)
@@ -298,16 +314,26 @@ __device__ __noinline__ u64 select_last(u64 e, bool in, u64 f, u64 target, Share
         __syncthreads();
         a = sh.red[lane];
         b = sh.red2[lane];
+        count = __reduce_add_sync(~0u, sh.warp_ties[lane]);
 #pragma unroll 1
         for (int o = 16; o; o >>= 1) {
             a = min(a, __shfl_xor_sync(~0u, a, o));
             b = max(b, __shfl_xor_sync(~0u, b, o));
         }
-        const int s = max(0, 54 - __clzll((long long)(b - a)));          // the range in 10 bits
-        const uint32_t d = in ? (uint32_t)((b - e) >> s) : 0;            // larger entries first
-        if (in) {
-            atomicAdd(lo + d, (uint32_t)f & 0xffffu);
-            atomicAdd(hi + d, (uint32_t)(f >> 16));
+        from = a;
+        to = b;
+        if (count <= 64)
+            break;
+        const int s = max(0, 54 - __clzll((long long)(b - a)));          // the range in 10 bits; larger entries first
+#pragma unroll 1
+        for (int i = tid; i < n; i += kThreads) {
+            const u64 e = sh.list[i];
+            if (e >= from && e <= to && member(e)) {
+                const uint32_t d = (uint32_t)((b - e) >> s);
+                const u64 w = f(e);
+                atomicAdd(lo + d, (uint32_t)w & 0xffffu);
+                atomicAdd(hi + d, (uint32_t)(w >> 16));
+            }
         }
         __syncthreads();
         const u64 own = lo[tid] + ((u64)hi[tid] << 16), run = block_scan(own, sh.red);
@@ -316,26 +342,32 @@ __device__ __noinline__ u64 select_last(u64 e, bool in, u64 f, u64 target, Share
             sh.last = run - own;
         }
         __syncthreads();
-        in = in && d == (uint32_t)sh.found;
+        const u64 d = (u64)sh.found;
         target -= sh.last;
-        if (__syncthreads_count(in) <= 64)
-            break;
+        to = b - (d << s);
+        const u64 low = b - min((d << s) + ((1ull << s) - 1), b);
+        from = max(a, low);
+        __syncthreads();
     }
     // the few: each counts what is before it
     u64* few = reinterpret_cast<u64*>(sh.fine);
     u64* few_f = few + 64;
-    uint32_t at = 0;
-    if (in) {
-        at = atomicAdd(&sh.nlist, 1u);
-        few[at] = e;
-        few_f[at] = f;
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+        const u64 e = sh.list[i];
+        if (e >= from && e <= to && member(e)) {
+            const uint32_t at = atomicAdd(&sh.nlist, 1u);
+            few[at] = e;
+            few_f[at] = f(e);
+        }
     }
     __syncthreads();
-    if (in) {
+    if (tid < (int)sh.nlist) {
+        const u64 e = few[tid];
         u64 run = 0;
         for (uint32_t j = 0; j < sh.nlist; ++j)
             run += few[j] >= e ? few_f[j] : 0;
-        if (run >= target && run - f < target)
+        if (run >= target && run - few_f[tid] < target)
             sh.last = e;
     }
     __syncthreads();
@@ -347,7 +379,8 @@ __device__ __noinline__ u64 select_last(u64 e, bool in, u64 f, u64 target, Share
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 {
-    __shared__ Shared sh;
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    Shared& sh = *reinterpret_cast<Shared*>(dynamic);
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_arrive();                     // waited for before the first access to another CTA's memory
     constexpr int VEC = Part<BF16>::VEC;
@@ -562,13 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         const int p1 = by_p ? min(sh.pbin[1], kb) : kb;
         const bool apart = by_k && p1 < kb;
         const uint32_t n_k = apart ? through(kb) - through(kb - 1) : 0;
-        const bool alone = through(p1) + n_k <= kList;       // the list takes all that may be kept
+        const bool alone = through(p1) + n_k <= kSort;       // the list takes all that may be kept, in order
         if (alone)
             p0 = 0;
         const uint32_t before = through(p0 - 1), n_p = through(p1) - before, n_list = n_p + n_k, before_k = through(kb - 1);
         const bool odd = r.top == INFINITY;                  // only infinities have weight, and none of them a bin
         all = !by_k && !by_p && !odd;                        // fewer tokens than k have weight
-        if (!all && !odd && n_list <= kList) {
+        const bool mixed = by_k && by_p && !apart && !alone;  // top-k ends where top-p does: needs the order
+        if (!all && !odd && n_list <= (mixed ? kSort : kList)) {
             // ---- 3. weights before and between the bands; their tokens into the first CTA's list
             const bool sums = !alone || (by_p && (!by_k || apart));
             u64 kept = 0, raw = 0, mid = 0;
@@ -653,7 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 const bool few = n_list <= kThreads / 4;
                 if (sums) {
                     // the gathered tokens' weights were added to what lies between the bands
-                    u64 w = tid < (int)n_list ? Row::weight(r.z(key_value((uint32_t)(e >> 32)))) : 0;
+                    u64 w = 0;
+                    for (int i = tid; i < (int)n_list; i += kThreads)
+                        w += Row::weight(r.z(key_value((uint32_t)(sh.list[i] >> 32))));
                     w = warp_sum(w);
                     if (lane == 0)
                         sh.red[warp] = w;
@@ -661,26 +697,30 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     mid -= warp_sum(sh.red[lane]);
                     __syncthreads();
                 }
-                if (!alone && !(by_k && by_p && !apart)) {
+                if (!alone && !mixed) {
                     // only the last member is wanted: no order is needed
-                    const uint32_t key = (uint32_t)(e >> 32);
-                    const u64 w = tid < (int)n_list ? Row::weight(r.z(key_value(key))) : 0;
-                    const uint32_t b = r.fine(key_value(key));
-                    const bool first = tid < (int)n_list && b - q0 <= qn, second = tid < (int)n_list && !first;
+                    auto in_first = [&](u64 v) { return r.fine(key_value((uint32_t)(v >> 32))) - q0 <= qn; };
+                    auto weigh = [&](u64 v) -> u64 { return Row::weight(r.z(key_value((uint32_t)(v >> 32)))); };
+                    auto one = [](u64) -> u64 { return 1; };
                     u64 cut_at;
                     if (by_p) {
-                        u64 in_band = first ? w : 0, beyond = 0;
-                        if (apart) {
-                            const u64 lk = select_last(e, second, 1, (u64)k - before_k, sh);
-                            beyond = second && e >= lk ? w : 0;
+                        u64 in_band = 0, beyond = 0, lk = ~0ull;
+                        if (apart)
+                            lk = select_last((int)n_list, [&](u64 v) { return !in_first(v); }, one, (u64)k - before_k, sh);
+                        for (int i = tid; i < (int)n_list; i += kThreads) {
+                            const u64 v = sh.list[i];
+                            if (in_first(v))
+                                in_band += weigh(v);
+                            else if (v >= lk)
+                                beyond += weigh(v);
                         }
                         in_band = block_sum(in_band, sh.red);
                         beyond = block_sum(beyond, sh.red);
                         const u64 need = one_for_all(need_of, raw + in_band + mid + beyond);
                         found = raw < need && raw + in_band >= need;     // the share is reached within the band
-                        cut_at = found ? select_last(e, first, w, need - raw, sh) : ~0ull;
+                        cut_at = found ? select_last((int)n_list, in_first, weigh, need - raw, sh) : ~0ull;
                     } else {
-                        cut_at = select_last(e, first, 1, (u64)k - before, sh);
+                        cut_at = select_last((int)n_list, in_first, one, (u64)k - before, sh);
                     }
                     if (tid == 0)
                         sh.last = ~cut_at;
@@ -773,8 +813,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             if (last) {
                 // the list's kept tokens join their warps' sums
                 const Shared* s0 = cl.map_shared_rank(&sh, 0);
-                if (tid < (int)n_list) {
-                    const u64 e = s0->list[tid];
+                for (int i = tid; i < (int)n_list; i += kThreads) {
+                    const u64 e = s0->list[i];
                     const uint32_t x = Row::weight(r.z(key_value((uint32_t)(e >> 32))));
                     const int g = ((int)(0xffffffffu - (uint32_t)e) + part.lead) / part.VEC / per;
                     if (e >= last && x >= least && g / kWarps == rank)
@@ -1035,7 +1075,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 
 }  // namespace
 
-cudaError_t prepare_sample_kernels() { return cudaSuccess; }
+cudaError_t prepare_sample_kernels()
+{
+    const cudaError_t e = cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+}
 
 cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s)
 {
@@ -1051,6 +1095,7 @@ cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.M * c);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
