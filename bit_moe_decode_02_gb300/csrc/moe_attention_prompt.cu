@@ -1,19 +1,25 @@
 // moe_attention_prompt.cu -- attention of many tokens over the 8-bit paged cache
 // (prompts and their chunks), on tcgen05.
 //
-// Bound by the tensor pipe: 4 D multiply-adds a (row, key) pair, both products as
-// kind::f16 MMAs of 128 rows with fp32 accumulators in tensor memory.
+// 4 D multiply-adds a (row, key) pair, both products as kind::f16 MMAs of 128 rows
+// with fp32 accumulators in tensor memory.  What bounds it: a tile of 128 keys moves
+// 320 KB through shared memory (192 KB of it MMA operands), 2,500 cycles at 128
+// bytes a cycle, where the MMAs need 2,048; it takes 4,200, because a row tile's
+// softmax (2,300) and its MMAs (1,300) wait for one another and only the other row
+// tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
+// heads: 284 us, 963 TFLOP/s (0.52 of the measured bf16 rate).
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.
-//  - Roles (16 warps).  Warp 0 streams the raw codes of a tile's blocks (bulk copies,
+//  - Roles (24 warps).  Warp 0 streams the raw codes of a tile's blocks (bulk copies,
 //    K and V apart) and their scales.  Warps 4-7 make them the f16 operands, in the
 //    canonical K-major order, exactly: K as it lies, V as it lies too (transposed in
-//    the cache).  Warp 1 issues the MMAs.  Warps 8-11
-//    and 12-15 do the softmax, a thread a row: while one tile's is under way, the
-//    other's MMAs run.
+//    the cache).  Warp 1 issues the MMAs.  Warps 8-15 and 16-23 do the softmax of
+//    one row tile each, two threads a row with 64 keys each: while one tile's is
+//    under way, the other's MMAs run.
 //  - Tensor memory: S0 S1 O0 O1, 128 columns each.  P replaces the scores it comes
-//    from, as f16, and is the second product's A operand from there.
+//    from, as f16 (64 keys' in columns 0-31, the others' in 64-95), and is the second
+//    product's A operand from there.
 //  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
 //    scores, V's enters the exponent; O is rescaled in tensor memory only where a
 //    row's maximum grows by more than 2^8, or the unit changes.
@@ -26,7 +32,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kRows = 256;                // of a CTA
 constexpr int kKeys = 128;                // of a tile
 constexpr int kRing = 8;                  // tiles whose scales are kept
@@ -42,7 +48,8 @@ struct Layout {
     static constexpr int OFF_RAW = OFF_V + 2 * OP;
     static constexpr int OFF_SC = OFF_RAW + 2 * RAW;      // [kRing][4] (K scale, V scale), K scale < 0: no block
     static constexpr int OFF_BAR = OFF_SC + kRing * 4 * 8;
-    static constexpr int SMEM = OFF_BAR + 24 * 8;   // 225 KB for D = 128, of 227
+    static constexpr int OFF_MAX = OFF_BAR + 24 * 8;      // [2 row tiles][2 halves][128]
+    static constexpr int SMEM = OFF_MAX + 2 * 2 * 128 * 4;   // 226.4 KB for D = 128, of 227
 };
 
 // The whole warp executes these, one elected lane (`one` != 0) issues: outside a
@@ -213,10 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             tc::mbar_init(v_full + i, 4);
             tc::mbar_init(v_empty + i, na);
             tc::mbar_init(s_full + i, 1);
-            tc::mbar_init(p_full + i, 4);
+            tc::mbar_init(p_full + i, 8);
             tc::mbar_init(o_full + i, 1);
         }
-        tc::mbar_init(q_full, 256);
+        tc::mbar_init(q_full, 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 3) {
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(one, tmem + 256 + x * 128, tmem + x * 128 + 8 * k, vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
+                        mma_ts(one, tmem + 256 + x * 128, tmem + x * 128 + 8 * k + (k >= 4 ? 32 : 0), vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
                     commit(one, v_empty + st);
                     if (t + 1 == nt)
                         commit(one, o_full + x);
@@ -385,15 +392,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             arrive(v_full + st, raw_empty + 1);
         }
     } else if (warp >= 8) {
-        // ---- softmax: a thread a row
-        const int x = (warp - 8) >> 2, r = tid & 127, row = w.rt * kRows + x * 128 + r;
+        // ---- softmax: two threads a row, one for each 64 keys of a tile
+        const int x = (warp - 8) >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, row = w.rt * kRows + x * 128 + r;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;      // this warp's quarter of the tensor memory's lanes
-        const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
+        const uint32_t ts = tmem + x * 128 + half * 64 + lanes, to = tmem + 256 + x * 128 + half * (D / 2) + lanes;
         const bool in = x * 128 + r < rows;
         const int i = row / a.group, hq = w.h * a.group + row % a.group;
+        float* mine = reinterpret_cast<float*>(sm + L::OFF_MAX) + (x * 2 + half) * 128 + r;
+        const float* other = mine + (half ? -128 : 128);
+        // the two warps that share 32 rows
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + (warp & 3)) : "memory"); };
         float f;
         {
-            // the query row: f16, scaled, in the canonical order
+            // the query row: f16, scaled, in the canonical order; half of it each
             uint32_t big = 0;
             const uint4* q = reinterpret_cast<const uint4*>(a.q + (long long)(w.c0 + i) * a.q_stride + (long long)hq * D);
             if (in)
@@ -406,13 +417,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             f = rs.f;
             uint8_t* out = sm + L::OFF_Q + x * L::OP + (r >> 3) * (D * 16) + (r & 7) * 16;
 #pragma unroll 4
-            for (int k = 0; k < D / 8; ++k) {
+            for (int k = half * (D / 16); k < (half + 1) * (D / 16); ++k) {
                 const uint4 v = in ? q[k] : make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4*>(out + 128 * k) =
                     make_uint4(scale_pair(v.x, rs), scale_pair(v.y, rs), scale_pair(v.z, rs), scale_pair(v.w, rs));
             }
             tc::fence_proxy_async_smem();
-            tc::mbar_arrive(q_full);
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(q_full);
         }
         if (x < na) {
             const int phi = in ? w.len - w.n + i : -1, plo = in && a.window > 0 ? phi - a.window + 1 : 0;
@@ -420,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             const int all_hi = w.len - w.n + (w.rt * kRows + x * 128) / a.group;
             const int all_lo = a.window > 0 ? w.len - w.n + (w.rt * kRows + min(rows, x * 128 + 128) - 1) / a.group - a.window + 1 : 0;
             float m = kNone, l = 0.0f, ref = 0.0f, vmax = 0.0f;
+#pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 const int p0 = (tile0 + t) * kKeys;
                 tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
@@ -432,14 +446,54 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     top = fmaxf(top, v.y);
                     whole = whole && v.x >= 0.0f;
                 }
-                uint32_t buf[2][32];
-                tm_ld32(ts, buf[0]);
-                tm_ld32(ts + 32, buf[1]);
-                // O, and what this tile has put into P so far, times al: a new maximum or a new unit
-                auto rescale = [&](float al, int done) {
+                // scores of 32 keys of this row, -inf where it does not see them
+                auto take = [&](int g, uint32_t (&v)[32], float ks) {
+                    tm_ld32(ts + 32 * g, v);
+                    tm_wait_ld(v);
+                    if (!whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int p = p0 + 64 * half + 32 * g + k;
+                            if (ks < 0.0f || p < plo || p > phi)
+                                v[k] = 0xff800000u;
+                        }
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float ks = sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK].x;
+                    uint32_t v[32];
+                    take(g, v, ks);
+                    float y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 4]));
+#pragma unroll
+                    for (int k = 8; k < 32; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = max3(y[e], __uint_as_float(v[k + e]), __uint_as_float(v[k + e + 4]));
+                    mx = fmaxf(mx, max3(fmaxf(y[0], y[1]), y[2], y[3]) * fmaxf(ks * f, 1e-37f));
+                }
+                *mine = mx;
+                pair_sync();
+                mx = fmaxf(mx, *other);
+                const bool unit = !(top <= 2.0f * ref && top >= 0.5f * ref);            // the same for all warps
+                if (__any_sync(~0u, unit || mx > m + kSlack)) {                         // the same for both of a pair
+                    const float mn = fmaxf(m, mx);
+                    float al = ex2(m - mn);
+                    m = mn;
+                    l *= al;
+                    if (unit) {
+                        vmax = fmaxf(vmax, top);
+                        const float now = new_unit(top, vmax);
+                        al *= ref / now;
+                        ref = now;
+                    }
                     if (t > 0)
 #pragma unroll 1
-                        for (int ch = 0; ch < D / 32; ++ch) {
+                        for (int ch = 0; ch < D / 64; ++ch) {
                             uint32_t v[32];
                             tm_ld32(to + 32 * ch, v);
                             tm_wait_ld(v);
@@ -448,134 +502,61 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                                 v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
                             tm_st32(to + 32 * ch, v);
                         }
-                    if (done) {
-                        tm_wait_st();
-                        const __half2 a2 = __float2half2_rn(al);
-#pragma unroll 1
-                        for (int ch = 0; ch < done; ch += 2) {
-                            uint32_t v[32];
-                            tm_ld32(ts + 16 * ch, v);
-                            tm_wait_ld(v);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&v[k]), a2), z = __hmul2(*reinterpret_cast<__half2*>(&v[k + 16]), a2);
-                                v[k] = *reinterpret_cast<uint32_t*>(&y);
-                                if (ch + 1 < done)
-                                    v[k + 16] = *reinterpret_cast<uint32_t*>(&z);
-                            }
-                            tm_st32(ts + 16 * ch, v);
-                        }
-                        tm_wait_st();
-                    }
-                };
-                if (!(top <= 2.0f * ref && top >= 0.5f * ref)) {        // the same for the whole warp
-                    vmax = fmaxf(vmax, top);
-                    const float now = new_unit(top, vmax);
-                    rescale(ref / now, 0);
-                    ref = now;
                 }
                 const float iref = rcp(ref);
-                float2 sum[L::NB];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    // 64 keys: their maximum, then their probabilities; the next scores come in meanwhile
-                    float mx = -INFINITY, c[2];
-                    tm_wait_ld(buf[0]);
-                    tm_wait_ld(buf[1]);
+                for (int g = 0; g < 2; ++g) {
+                    const float2 kv = sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK];
+                    const float c = fmaxf(kv.x * f, 1e-37f), ratio = fmaxf(kv.y * iref, 8.673617379884035e-19f);   // 2^-60
+                    const float off = lg2(ratio) - m;
+                    uint32_t v[32], p[16];
+                    take(g, v, kv.x);
+                    const float2 cc = make_float2(c, c), oo = make_float2(off, off);
+                    float2 part[2];
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t(&v)[32] = buf[g];
-                        const int ch = 2 * half + g;
-                        const float2 kv = sc[(t % kRing) * 4 + ch * 32 / BLK];
-                        c[g] = fmaxf(kv.x * f, 1e-37f);
-                        if (!whole) {
-                            const bool have = kv.x >= 0.0f;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int p = p0 + 32 * ch + k;
-                                if (!have || p < plo || p > phi)
-                                    v[k] = 0xff800000u;
-                            }
-                        }
-                        float y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 4]));
-#pragma unroll
-                        for (int k = 8; k < 32; k += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = max3(y[e], __uint_as_float(v[k + e]), __uint_as_float(v[k + e + 4]));
-                        mx = fmaxf(mx, max3(fmaxf(y[0], y[1]), y[2], y[3]) * c[g]);
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
+                        z.x = ex2(z.x);
+                        z.y = ex2(z.y);
+                        part[k / 2 & 1] = k > 2 ? add2(part[k / 2 & 1], z) : z;
+                        p[k / 2] = pack_f16(z.x, z.y);
                     }
-                    if (__any_sync(~0u, mx > m + kSlack)) {
-                        const float mn = fmaxf(m, mx), al = ex2(m - mn);
-                        rescale(al, 2 * half);
-                        m = mn;
-                        l *= al;
-                        if (half)
-#pragma unroll
-                            for (int e = 0; e < L::NB; ++e)
-                                if (e * BLK < 64) {
-                                    sum[e].x *= al;
-                                    sum[e].y *= al;
-                                }
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t(&v)[32] = buf[g];
-                        const int ch = 2 * half + g, b = ch * 32 / BLK;
-                        const float off = lg2(fmaxf(sc[(t % kRing) * 4 + b].y * iref, 8.673617379884035e-19f)) - m;    // 2^-60
-                        const float2 cc = make_float2(c[g], c[g]), oo = make_float2(off, off);
-                        uint32_t p[16];
-                        float2 part[2];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
-                            z.x = ex2(z.x);
-                            z.y = ex2(z.y);
-                            part[k / 2 & 1] = k > 2 ? add2(part[k / 2 & 1], z) : z;
-                            p[k / 2] = pack_f16(z.x, z.y);
-                        }
-                        if (half == 0)
-                            tm_ld32(ts + 64 + 32 * g, v);
-                        const float2 both = add2(part[0], part[1]);
-                        sum[b] = ch * 32 % BLK ? add2(sum[b], both) : both;
-                        tm_st16(ts + 16 * ch, p);
-                    }
+                    const float2 both = add2(part[0], part[1]);
+                    l += (both.x + both.y) * rcp(ratio);
+                    tm_st16(ts + 16 * g, p);
                 }
-#pragma unroll
-                for (int b = 0; b < L::NB; ++b)
-                    l += (sum[b].x + sum[b].y) * rcp(fmaxf(sc[(t % kRing) * 4 + b].y * iref, 8.673617379884035e-19f));
                 tm_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(p_full + x);
             }
-            // ---- the row's result
+            // ---- the row's result, half of its columns each
+            pair_sync();                     // both have read the last maxima
+            *mine = l;
+            pair_sync();
+            l += *other;
             tc::mbar_wait(o_full + x, 0, status);
             tc::tc_fence_after();
-            const Final fin = finish(m, l, a.sinks, hq < a.q_heads ? hq : 0);
+            const Final fin = finish(m, l, a.sinks, hq);
             const float mul = fin.mul * ref;
-            uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D;
+            uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
-            for (int ch = 0; ch < D / 32; ++ch) {
+            for (int ch = 0; ch < D / 64; ++ch) {
                 uint32_t v[32];
                 tm_ld32(to + 32 * ch, v);
-                tc::tc_wait_ld();
+                tm_wait_ld(v);
                 if (in)
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[e] = tc::f2bf16_rne(__uint_as_float(v[k + 2 * e]) * mul) |
-                                   (uint32_t)tc::f2bf16_rne(__uint_as_float(v[k + 2 * e + 1]) * mul) << 16;
+                            o[e] = kv::bf16x2(__uint_as_float(v[k + 2 * e]) * mul, __uint_as_float(v[k + 2 * e + 1]) * mul);
                         *reinterpret_cast<uint4*>(out + 32 * ch + k) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
             }
-            if (a.lse && in)
+            if (a.lse && in && half == 0)
                 a.lse[(long long)(w.c0 + i) * a.q_heads + hq] = fin.lse;
         }
     }
