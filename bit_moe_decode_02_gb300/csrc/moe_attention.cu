@@ -35,7 +35,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int kPromptRows = 64;           // more rows than this go to the prompt kernel
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an item: (token, query head of the kv head) pairs
@@ -808,10 +807,16 @@ cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t
 
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
-    // rows of a (sequence, kv head) on average: the decode kernel reads the cache
-    // once for 16 of them, the prompt kernel once for 256
-    const long long rows = (long long)a.c.n_tokens * a.group / a.c.n_seqs;
-    return rows > kPromptRows ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
+    // Against 128 keys the decode kernel spends 0.62 us of an SM on 16 rows (D = 64;
+    // 0.86 for 128), spread over all SMs; the prompt kernel 1.45 us (2.2) on up to
+    // 128 rows and 1.4 times that on 256, on one SM each.  The ratio is 2.3 to 2.6,
+    // taken as 2.5.  Measured, decode / prompt kernel: 8 sequences of 4,000 keys, 64
+    // heads of 64 on 8: 64 rows 48 / 68 us, 106 rows 74 / 73, 217 rows 133 / 88; one
+    // such sequence, 432 rows: 57 / 81; 64 of them, 32 rows 140 / 180, 64 rows 263 / 182.
+    const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
+    const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
+    const long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
+    return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
 }  // namespace moe

@@ -67,6 +67,36 @@ def test_ragged_prompts(fmt, blk, D, heads, kv, window):
     check(c, new, lens, heads, window=window, sinks=torch.randn(heads, device="cuda") * 3)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk,D", [(32, 64), (32, 128), (64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("heads,kv", [(32, 32), (64, 8), (80, 8)])
+@pytest.mark.parametrize("window", [0, 1, 130])
+def test_ragged_prompts_of_many_heads(fmt, blk, D, heads, kv, window):
+    """As above with enough rows for the tensor-core path: row tiles that are full, partly full and absent."""
+    new = [0, 1, 300, 17, 2, 129, 64]
+    had = [40, 700, 0, 1, 129, 511, 64]
+    lens = [a + b for a, b in zip(new, had)]
+    c = Cache(lens, kv, D, blk, fmt, seed=2).fill(seed=blk + heads, poison=True)
+    check(c, new, lens, heads, window=window, sinks=torch.randn(heads, device="cuda") * 3 if window != 1 else None)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_with_block_scales_of_very_different_size(D):
+    """Scales 2^20 apart between neighbouring blocks, in V and then in K: O changes its unit at every tile, maxima jump."""
+    lens = [700, 1100]
+    for which in (1, 0):
+        c = Cache(lens, 16, D, 64, moe.MOE_KV_E4M3).fill(seed=8)
+        c.scales[:, :, which] *= torch.pow(2.0, torch.arange(c.scales.shape[0], device="cuda")[:, None] % 3 * (10.0 if which else 3.0))
+        check(c, [700, 400], lens, 32)
+
+
+def test_long_prompt_and_extreme_queries():
+    c = Cache([3000, 2500], 8, 64, 128, moe.MOE_KV_INT8).fill(seed=3)
+    check(c, [3000, 300], [3000, 2500], 16)
+    for qscale, scale in ((30.0, None), (2.0 ** 100, 2.0 ** -103), (2.0 ** -110, 2.0 ** 107), (1.0, -0.3), (1.0, 0.0)):
+        check(c, [900, 700], [3000, 2500], 16, qscale=qscale, scale=scale)
+
+
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 128, 5000])
 def test_windows(window):
     lens = [1, 64, 65, 130, 1000, 4097]
@@ -114,17 +144,17 @@ def test_sinks_of_any_size():
 def test_missing_blocks_leave_rows_empty():
     """A row none of whose blocks exist is zero, its lse the sink (or -inf); the status word says so."""
     o = handle()
-    for new in (1, 40):
-        for sinks in (None, torch.tensor([0.5, -2.0], device="cuda")):
-            c = Cache([40, 200], 1, 64, 64, moe.MOE_KV_E4M3).fill(seed=6)
-            q = torch.randn(2 * new, 2, 64, device="cuda").bfloat16()
-            out, lse = torch.full_like(q, 5.0), torch.full((2 * new, 2), 5.0, device="cuda")
+    for new, kv in ((1, 1), (40, 1), (40, 64)):
+        for sinks in (None, torch.linspace(0.5, -2.0, 2 * kv, device="cuda")):
+            c = Cache([40, 200], kv, 64, 64, moe.MOE_KV_E4M3).fill(seed=6)
+            q = torch.randn(2 * new, 2 * kv, 64, device="cuda").bfloat16()
+            out, lse = torch.full_like(q, 5.0), torch.full((2 * new, 2 * kv), 5.0, device="cuda")
             c.dtable[0, 0] = -1
             moe.moe_attention(o, c.desc, c.batch([new, new], [40, 200]), q, out, lse, sinks)
             assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
             assert (out[:new] == 0).all()
-            want = torch.full((2,), -math.inf, device="cuda") if sinks is None else sinks
-            assert torch.allclose(lse[:new], want.expand(new, 2), rtol=0, atol=1e-6)
+            want = torch.full((2 * kv,), -math.inf, device="cuda") if sinks is None else sinks
+            assert torch.allclose(lse[:new], want.expand(new, 2 * kv), rtol=0, atol=1e-6)
             ref, _, bound = attention(c, [0, new], [40, 200], q[new:], 64 ** -0.5, 0, sinks)
             assert ((out[new:].double() - ref).abs() <= bound).all()
 
