@@ -615,46 +615,50 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         }
         const int t0 = pieces[first].t0;
         const Place place = pieces[first].p;
-        int last = first + 1, nstage = pieces[first].where == kStage, slot_at = nstage ? -1 : first >> 1;
+        int last = first + 1, slot_at = pieces[first].where == kStage ? -1 : first >> 1;
         // the last pieces of some groups, and the first of the next one; or that alone
         while (last < 2 * C::NG && (!pieces[last].where || pieces[last].t0 == t0)) {
-            nstage += pieces[last].where == kStage;
             if (pieces[last].where == kSlot)
                 slot_at = last >> 1;
             ++last;
         }
-        const int g0 = first >> 1;
+        // the warps whose results lie in their groups' stages, a lane each
+        const Piece& mine_last = pieces[(lane & (kWarps - 1)) / C::GW * 2 + 1];
+        const unsigned warps = __ballot_sync(~0u, lane < kWarps && mine_last.where == kStage && mine_last.t0 == t0);
+        const int stage = mine_last.stage;
+        int ods[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            ods[w] = (w / C::GW * C::NS + __shfl_sync(~0u, stage, w)) * C::STAGE + w % C::GW * (kRows * D * 4);
         const bool done = t0 >= ct0 && pieces[first].t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), col = x % (D / 4) * 4, at = ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
+            const int row = x / (D / 4), col = x % (D / 4) * 4, at = row * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
             Sum sum;
             if (slot_at >= 0)
                 sum.from_slot(gslots + slot_at * slot_floats(), D, row, col);
-            if (nstage) {
-                // all maxima first: the parts' weights then do not wait for one another
-                float M = sum.m;
-#pragma unroll 4
-                for (int w = g0 * C::GW; w < (last + 1 >> 1) * C::GW; ++w)
-                    if (pieces[w / C::GW * 2 + 1].where && pieces[w / C::GW * 2 + 1].t0 == t0)
-                        M = fmaxf(M, mls[w * kRows + row].x);
-                const float keep = ex2(sum.m - M);
-                sum.m = M;
-                sum.l *= keep;
-                sum.v.x *= keep, sum.v.y *= keep, sum.v.z *= keep, sum.v.w *= keep;
-#pragma unroll 4
-                for (int w = g0 * C::GW; w < (last + 1 >> 1) * C::GW; ++w) {
-                    const Piece& p = pieces[w / C::GW * 2 + 1];
-                    if (!p.where || p.t0 != t0)
-                        continue;
-                    const float* od = reinterpret_cast<const float*>(sm + (w / C::GW * C::NS + p.stage) * C::STAGE);
-                    const float2 ml = mls[w * kRows + row];
-                    const float4 y = *reinterpret_cast<const float4*>(od + (w % C::GW * kRows + row) * D + at);
-                    const float f = ex2(ml.x - M);
-                    sum.l += ml.y * f;
+            // all maxima first: the parts' weights then do not wait for one another
+            float2 ml[kWarps];
+            float M = sum.m;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = mls[w * kRows + row];
+                if (!(warps >> w & 1))
+                    ml[w] = make_float2(kNone, 0.0f);
+                M = fmaxf(M, ml[w].x);
+            }
+            const float keep = ex2(sum.m - M);
+            sum.m = M;
+            sum.l *= keep;
+            sum.v.x *= keep, sum.v.y *= keep, sum.v.z *= keep, sum.v.w *= keep;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                if (warps >> w & 1) {
+                    const float4 y = *reinterpret_cast<const float4*>(sm + ods[w] + at * 4);
+                    const float f = ex2(ml[w].x - M);
+                    sum.l += ml[w].y * f;
                     sum.v.x += y.x * f, sum.v.y += y.y * f, sum.v.z += y.z * f, sum.v.w += y.w * f;
                 }
-            }
             if (done)
                 store_row4(a, place, row, col, sum.v, finish(sum.m, sum.l, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
             else
@@ -700,17 +704,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         for (int i = tid; i < K * rows; i += kThreads)
             part[i / rows * kRows + i % rows] = __ldcg(reinterpret_cast<const float2*>(slot_of(i / rows) + kRows * D + 2 * (i % rows)));
         __syncthreads();
-        if (tid < rows) {
+        // a warp takes a row, its lanes the parts
+        for (int row = warp; row < rows; row += kWarps) {
             float M = kNone, L = 0.0f;
-            for (int k = 0; k < K; ++k)
-                M = fmaxf(M, part[k * kRows + tid].x);
-            for (int k = 0; k < K; ++k) {
-                const float2 ml = part[k * kRows + tid];
-                const float w = ex2(ml.x - M);
-                L += ml.y * w;
-                part[k * kRows + tid].x = w;
+            for (int k = lane; k < K; k += 32)
+                M = fmaxf(M, part[k * kRows + row].x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+            for (int k = lane; k < K; k += 32) {
+                const float2 ml = part[k * kRows + row];
+                const float f = ex2(ml.x - M);
+                L += ml.y * f;
+                part[k * kRows + row].x = f;
             }
-            total[tid] = make_float2(M, L);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                L += __shfl_xor_sync(~0u, L, o);
+            if (lane == 0)
+                total[row] = make_float2(M, L);
         }
         __syncthreads();
         // every 4 columns' parts summed by `split` threads, then those

@@ -68,6 +68,8 @@ struct Row {
     {
         return __float_as_uint(__fmaf_rn(__fsub_rn(top, l), inv_t * 256.0f, 8388608.0f)) - 0x4b000000u;
     }
+    // z where the largest logit is finite: the same bits, from the difference that fine() takes
+    __device__ __forceinline__ float z_finite(float l) const { return -__fmul_rn(__fsub_rn(top, l), inv_t); }
     __device__ __forceinline__ static float fine_middle(int b) { return (float)b * (-1.0f / 256.0f); }
     __device__ __forceinline__ static int bin(float z) { return z > -(float)kBins / 32.0f ? (int)(z * -32.0f) : kBins - 1; }
 };
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
                         b[e] = r.fine(l[e]);
-                        x[e] = Row::weight(r.z(l[e]));
+                        x[e] = Row::weight(r.z_finite(l[e]));
                         x[e] = b[e] < end ? x[e] : 0;
                         tot += x[e];
                         x[e] = b[e] < q0 ? x[e] : 0;
