@@ -90,6 +90,7 @@ struct Shared {
     u64 list[kList];                       // the first CTA's: gathered tokens, as key and complement of the index
     u64 warp_sum[kWarps], part_sum[kMostCluster], part_raw[kMostCluster], part_mid[kMostCluster];
     u64 row_sum[kWarps];
+    uint4 left_range[kWarps];
     uint32_t warp_ties[kWarps], part_ties[kMostCluster], row_ties[kWarps];
     uint32_t nlist;
     int found, kbin, pbin[2];
@@ -278,60 +279,71 @@ __device__ __forceinline__ u64 block_sum(u64 v, u64* red)
 
 // Of the list's n entries that are `member`s, largest first: the one at which the
 // running sum of f reaches `target` (which all of them together reach).  Rounds of
-// 1,024 equal digits of the range that is left, till few are.
+// 1,024 equal digits of the range that is left, till few are: of the keys, and
+// once one key is left of the indexes.
 template <class In, class F>
 __device__ __forceinline__ u64 select_last(int n, In member, F f, u64 target, Shared& sh)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *lo = sh.fine, *hi = sh.fine + kThreads;
-    u64 from = 0, to = ~0ull;                // what is left: from <= e <= to
+    bool by_low = false;                      // the key is found: what is left has it
+    uint32_t key = 0, from = 0, to = ~0u;     // what is left: keys, or low words, from .. to
+    auto left = [&](u64 e) {
+        const uint32_t x = (uint32_t)(e >> 32), word = by_low ? (uint32_t)e : x;
+        return word >= from && word <= to && (!by_low || x == key) && member(e);
+    };
 #pragma unroll 1
     while (true) {
-        u64 a = ~0ull, b = 0;
-        int count = 0;
+        uint32_t ka = ~0u, kb = 0, la = ~0u, lb = 0, count = 0;
 #pragma unroll 1
         for (int i = tid; i < n; i += kThreads) {
             const u64 e = sh.list[i];
-            if (e >= from && e <= to && member(e)) {
-                a = min(a, e);
-                b = max(b, e);
+            if (left(e)) {
+                ka = min(ka, (uint32_t)(e >> 32));
+                kb = max(kb, (uint32_t)(e >> 32));
+                la = min(la, (uint32_t)e);
+                lb = max(lb, (uint32_t)e);
                 ++count;
             }
         }
-#pragma unroll 1
-        for (int o = 16; o; o >>= 1) {
-            a = min(a, __shfl_xor_sync(~0u, a, o));
-            b = max(b, __shfl_xor_sync(~0u, b, o));
-        }
-        count = __reduce_add_sync(~0u, count);
+        auto reduce = [&]() {
+            ka = __reduce_min_sync(~0u, ka);
+            kb = __reduce_max_sync(~0u, kb);
+            la = __reduce_min_sync(~0u, la);
+            lb = __reduce_max_sync(~0u, lb);
+            count = __reduce_add_sync(~0u, count);
+        };
+        reduce();
         __syncthreads();
         if (lane == 0) {
-            sh.red[warp] = a;
-            sh.red2[warp] = b;
+            sh.left_range[warp] = make_uint4(ka, kb, la, lb);
             sh.warp_ties[warp] = count;
         }
         lo[tid] = hi[tid] = 0;
         if (tid == 0)
             sh.nlist = 0;
         __syncthreads();
-        a = sh.red[lane];
-        b = sh.red2[lane];
-        count = __reduce_add_sync(~0u, sh.warp_ties[lane]);
-#pragma unroll 1
-        for (int o = 16; o; o >>= 1) {
-            a = min(a, __shfl_xor_sync(~0u, a, o));
-            b = max(b, __shfl_xor_sync(~0u, b, o));
+        {
+            const uint4 x = sh.left_range[lane];
+            ka = x.x, kb = x.y, la = x.z, lb = x.w;
+            count = sh.warp_ties[lane];
         }
-        from = a;
-        to = b;
+        reduce();
         if (count <= 64)
             break;
-        const int s = max(0, 54 - __clzll((long long)(b - a)));          // the range in 10 bits; larger entries first
+        if (ka == kb && !by_low) {
+            by_low = true;
+            key = ka;
+        }
+        const uint32_t a = by_low ? la : ka, b = by_low ? lb : kb;
+        from = a;
+        to = b;
+        const int s = max(0, 22 - __clz((int)(b - a)));          // the range in 10 bits; larger words first
 #pragma unroll 1
         for (int i = tid; i < n; i += kThreads) {
             const u64 e = sh.list[i];
-            if (e >= from && e <= to && member(e)) {
-                const uint32_t d = (uint32_t)((b - e) >> s);
+            if (left(e)) {
+                const uint32_t d = (b - (by_low ? (uint32_t)e : (uint32_t)(e >> 32))) >> s;
                 const u64 w = f(e);
                 atomicAdd(lo + d, (uint32_t)w & 0xffffu);
                 atomicAdd(hi + d, (uint32_t)(w >> 16));
@@ -344,32 +356,37 @@ __device__ __forceinline__ u64 select_last(int n, In member, F f, u64 target, Sh
             sh.last = run - own;
         }
         __syncthreads();
-        const u64 d = (u64)sh.found;
+        const uint32_t d = (uint32_t)sh.found << s;
         target -= sh.last;
-        to = b - (d << s);
-        const u64 low = b - min((d << s) + ((1ull << s) - 1), b);
-        from = max(a, low);
+        to = b - d;
+        from = max(a, b - min(d + ((1u << s) - 1), b));
         __syncthreads();
     }
-    // the few: each counts what is before it
+    // the few: what is before each is added up by 16 threads
     u64* few = reinterpret_cast<u64*>(sh.fine);
     u64* few_f = few + 64;
 #pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
         const u64 e = sh.list[i];
-        if (e >= from && e <= to && member(e)) {
+        if (left(e)) {
             const uint32_t at = atomicAdd(&sh.nlist, 1u);
             few[at] = e;
             few_f[at] = f(e);
         }
     }
     __syncthreads();
-    if (tid < (int)sh.nlist) {
-        const u64 e = few[tid];
+    {
+        static_assert(kThreads == 64 * 16, "16 threads for each of the few");
+        const uint32_t i = tid >> 4, m = sh.nlist;
+        const u64 e = few[i];
         u64 run = 0;
-        for (uint32_t j = 0; j < sh.nlist; ++j)
-            run += few[j] >= e ? few_f[j] : 0;
-        if (run >= target && run - few_f[tid] < target)
+#pragma unroll
+        for (uint32_t j = tid & 15; j < 64; j += 16)
+            run += j < m && few[j] >= e ? few_f[j] : 0;
+#pragma unroll
+        for (int o = 8; o; o >>= 1)
+            run += __shfl_xor_sync(~0u, run, o);
+        if (i < m && run >= target && run - few_f[i] < target)
             sh.last = e;
     }
     __syncthreads();
@@ -531,10 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
             n[j] = tid * kFinePer + j < kFine ? sh.fine[tid * kFinePer + j] : 0;
 #pragma unroll
         for (int j = 0; j < kFinePer; ++j) {
-            w[j] = n[j] * (u64)Row::weight(Row::fine_middle(tid * kFinePer + j));
+            const uint32_t x = Row::weight(Row::fine_middle(tid * kFinePer + j));
+            const float y = (float)n[j] * (float)x;
+            w[j] = n[j] * (u64)x;
             nsum += n[j];
             wsum += w[j];
-            sq += (float)w[j] * (float)w[j];
+            sq += y * y;
         }
         if (by_p) {
 #pragma unroll
@@ -717,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                                 beyond += weigh(v);
                         }
                         in_band = block_sum(in_band, sh.red);
-                        beyond = block_sum(beyond, sh.red);
+                        if (apart)
+                            beyond = block_sum(beyond, sh.red);
                         const u64 need = one_for_all(need_of, raw + in_band + mid + beyond);
                         found = raw < need && raw + in_band >= need;     // the share is reached within the band
                         cut_at = found ? select_last((int)n_list, in_first, weigh, need - raw, sh) : ~0ull;
