@@ -57,6 +57,8 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+constexpr uint32_t kFineBits = 0x4b000000u;   // 2^23 as a float
+
 struct Row {
     float top, inv_t;
     // -inf and NaN logits: -inf or NaN, of weight 0 and in no bin
@@ -64,9 +66,9 @@ struct Row {
     __device__ __forceinline__ static uint32_t weight(float z) { return __float2uint_rn(expf(z) * 2147483648.0f); }
     // 1/256 of z that a finite logit lies nearest to; beyond kFine for -inf and NaN.
     // Adding 2^23 rounds to an integer in the low bits
-    __device__ __forceinline__ uint32_t fine(float l) const
+    __device__ __forceinline__ uint32_t fine_bits(float l) const
     {
-        return __float_as_uint(__fmaf_rn(__fsub_rn(top, l), inv_t * 256.0f, 8388608.0f)) - 0x4b000000u;
+        return __float_as_uint(__fmaf_rn(__fsub_rn(top, l), inv_t * 256.0f, 8388608.0f));
     }
     // z where the largest logit is finite: the same bits, from the difference that fine() takes
     __device__ __forceinline__ float z_finite(float l) const { return -__fmul_rn(__fsub_rn(top, l), inv_t); }
@@ -517,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
         part.template each<2>([&](const float (&l)[VEC], int) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const uint32_t b = r.fine(l[e]);
-                if (b < (uint32_t)kFine)
-                    atomicAdd(&sh.fine[b], 1u);
+                const uint32_t b = r.fine_bits(l[e]);
+                if (b < kFineBits + kFine)
+                    atomicAdd(&sh.fine[b - kFineBits], 1u);
             }
         });
         const int tps = (kThreads + c - 1) / c;              // threads whose bins one CTA adds up
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 *cl.map_shared_rank(&sh.list[at], 0) = (u64)order_key(l) << 32 | (0xffffffffu - (uint32_t)i);
             };
             // bands q0 .. q0 + qn and qa; bins from `end` on are beyond top-k
-            const uint32_t q0 = p0, qn = min(p1, kFine - 1) - p0, qa = apart ? (uint32_t)kb : ~0u, end = by_k ? (uint32_t)kb + 1 : ~0u;
+            const uint32_t q0 = kFineBits + p0, qn = min(p1, kFine - 1) - p0, qa = apart ? kFineBits + kb : ~0u, end = by_k ? kFineBits + kb + 1 : ~0u;
             const bool floor = least > 0;
             if (sums) {
                 u64 tot = 0;
@@ -641,14 +643,20 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                     bool hit = false;
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        b[e] = r.fine(l[e]);
+                        b[e] = r.fine_bits(l[e]);
                         x[e] = Row::weight(r.z_finite(l[e]));
                         x[e] = b[e] < end ? x[e] : 0;
-                        tot += x[e];
-                        x[e] = b[e] < q0 ? x[e] : 0;
-                        raw += x[e];
                         hit = hit || b[e] - q0 <= qn || b[e] == qa;
                     }
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2)
+                        tot += (u64)x[e] + x[e + 1];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        x[e] = b[e] < q0 ? x[e] : 0;
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2)
+                        raw += (u64)x[e] + x[e + 1];
                     if (floor)
 #pragma unroll
                         for (int e = 0; e < VEC; ++e)
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 part.template each<2>([&](const float (&l)[VEC], int i) {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const uint32_t b = r.fine(l[e]);
+                        const uint32_t b = r.fine_bits(l[e]);
                         if (b - q0 <= qn || b == qa)
                             gather(l[e], i + e);
                     }
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a)
                 }
                 if (!alone && !mixed) {
                     // only the last member is wanted: no order is needed
-                    auto in_first = [&](u64 v) { return r.fine(key_value((uint32_t)(v >> 32))) - q0 <= qn; };
+                    auto in_first = [&](u64 v) { return r.fine_bits(key_value((uint32_t)(v >> 32))) - q0 <= qn; };
                     auto weigh = [&](u64 v) -> u64 { return Row::weight(r.z(key_value((uint32_t)(v >> 32)))); };
                     auto one = [](u64) -> u64 { return 1; };
                     u64 cut_at;
