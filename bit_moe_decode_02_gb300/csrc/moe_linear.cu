@@ -39,6 +39,7 @@ constexpr int kCodeBytes = kRows * kCols / 2;
 constexpr int kXBytes = 112 * 1024;        // most of x that a CTA keeps: two stages a warp still fit
 constexpr int kSmem = 224 * 1024;
 constexpr int kMostStages = 6;
+constexpr int kCluster = 4;                // CTAs that share their rows, where they do
 
 // Bytes of one row's scales in a stage, and the aligned 4-byte words that may hold them.
 __host__ __device__ constexpr int scale_bytes(int fmt, int group) { return fmt == MOE_FMT_MXFP4 ? kCols / 32 : 2 * kCols / group; }
@@ -46,10 +47,12 @@ __host__ __device__ constexpr int scale_words(int fmt, int group) { return scale
 
 struct Plan {
     int tokens;     // of this pass
-    int ks;         // warps that share 16 rows
+    int cs;         // CTAs of a cluster, which share all rows: each takes `steps` stages of columns
+    int steps;
+    int ks;         // warps of a CTA that share 16 rows
     int stages;
     int x_pitch;    // bytes of one token's x
-    int off_sum, off_fac, off_red, off_ring;
+    int off_sum, off_fac, off_red, off_join, off_ring;
     int stage_bytes;
 };
 
@@ -132,14 +135,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int team = warp / p.ks, part = warp % p.ks, teams = kWarps / p.ks;
-    const int nunits = (a.N + kRows - 1) / kRows, nsteps = (a.K + kCols - 1) / kCols;
+    uint32_t rank = 0;
+    if (p.cs > 1) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first join
+    }
+    // this CTA's columns, counted from the first of them
+    const int step0 = rank * p.steps, K = max(min(a.K - step0 * kCols, p.steps * kCols), 0);
+    const int nunits = (a.N + kRows - 1) / kRows, nsteps = (K + kCols - 1) / kCols;
     const int row_scale = FMT == MOE_FMT_MXFP4 ? a.K / 32 : 2 * (a.K / kGroup);   // bytes
     const uint32_t ring = tc::su32(sm + p.off_ring) + warp * p.stages * p.stage_bytes;
     const int half_k = a.K / 2;
 
     // this warp's stream: its stages of each of its team's units
-    const int stride = gridDim.x * teams;
-    int pu = blockIdx.x + team * gridDim.x, ps = part;             // next to load
+    const int nclusters = gridDim.x / p.cs, first = blockIdx.x / p.cs + team * nclusters, stride = nclusters * teams;
+    int pu = first, ps = part;                                     // next to load
     uint32_t pst = ring;
     const uint32_t ring_end = ring + p.stages * p.stage_bytes;
     const int l3 = lane >> 3, ch = lane & 7;
@@ -150,24 +160,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
     for (int i = 0; i < kScaleCopies; ++i) {
         const int k = lane + 32 * i;
-        soff[i] = k < kRows * SW ? k / SW * row_scale : -1;
+        soff[i] = k < kRows * SW ? k / SW * row_scale + step0 * SB : -1;
     }
     const uint8_t *csrc = nullptr, *ssrc = nullptr;                 // the unit's codes (this lane's row) and scales
     int prows = 0;
     auto open_unit = [&]() {
         prows = min(a.N - pu * kRows, kRows);
-        csrc = a.codes + (long long)pu * kRows * half_k + l3 * half_k + ch * 16;
+        csrc = a.codes + (long long)pu * kRows * half_k + l3 * half_k + step0 * (kCols / 2) + ch * 16;
         ssrc = static_cast<const uint8_t*>(a.scales) + (long long)pu * kRows * row_scale;
     };
     auto load = [&]() {
         if (pu < nunits) {
             const uint8_t* src = csrc + ps * (kCols / 2);
-            if (prows == kRows && (ps + 1) * kCols <= a.K) {
+            if (prows == kRows && (ps + 1) * kCols <= K) {
                 cp16(pst + d0, src);
                 cp16(pst + d1, src + 4 * half_k);
                 cp16(pst + d0 + 1024, src + 8 * half_k);
                 cp16(pst + d1 + 1024, src + 12 * half_k);
-            } else if (ps * (kCols / 2) + ch * 16 < half_k) {
+            } else if (ps * (kCols / 2) + ch * 16 < K / 2) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (l3 + 4 * i < prows)
@@ -207,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     int* ups = reinterpret_cast<int*>(fac + 16);
     uint32_t* bigs = reinterpret_cast<uint32_t*>(ups + 1);
     float* sums = reinterpret_cast<float*>(sm + p.off_sum);
-    const int groups = a.K / kGroup, pieces = p.tokens * nsteps;
+    const int groups = K / kGroup, pieces = p.tokens * nsteps;
+    const uint16_t* xsrc = a.x + step0 * kCols;
     if (tid < 16)
         bigs[tid] = 0;
     __syncthreads();
@@ -218,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + j * kWarps, m = i / nsteps, k = i % nsteps * 32 + lane;
             q[j] = make_uint4(0, 0, 0, 0);
-            if (i < pieces && k < a.K / 8)
-                q[j] = *reinterpret_cast<const uint4*>(a.x + m * a.x_stride + 8 * k);
+            if (i < pieces && k < K / 8)
+                q[j] = *reinterpret_cast<const uint4*>(xsrc + m * a.x_stride + 8 * k);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     big = max(big, max(u < 0x7f80u ? u : 0u, v < 0x7f80u ? v : 0u));
                 }
             }
-            if (k < a.K / 8)
+            if (k < K / 8)
                 *reinterpret_cast<uint4*>(sm + m * p.x_pitch + k * 16) = q[j];
             big = __reduce_max_sync(~0u, big);
             if (lane == 0)
@@ -250,21 +261,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     }
     __syncthreads();
     auto up_of = [&](int m) { return 14 + 127 - max((int)(bigs[m] >> 7), 1); };
-    if (tid == 0) {
+    if (warp == kWarps - 1) {
         // the totals are kept in the units of the token that is scaled up least
-        int up = up_of(0);
-        for (int m = 1; m < p.tokens; ++m)
-            up = min(up, up_of(m));
-        *ups = up;
-        for (int m = 0; m < p.tokens; ++m)
-            fac[m] = ldexpf(1.0f, up - up_of(m));
+        const int own = up_of(min(lane, p.tokens - 1)), up = __reduce_min_sync(~0u, own);
+        if (lane == 0)
+            *ups = up;
+        if (lane < p.tokens)
+            fac[lane] = ldexpf(1.0f, up - own);
     }
     for (int i = warp; i < pieces; i += kWarps) {
         const int m = i / nsteps, k = i % nsteps * 32 + lane, up = up_of(m);
         // 2^up in two factors, the second 1 but for the smallest tokens
         const float u0 = __uint_as_float((uint32_t)(127 + min(up, 126)) << 23), u1 = __uint_as_float((uint32_t)(127 + max(up - 126, 0)) << 23);
         float sum = 0.0f;
-        if (k < a.K / 8) {
+        if (k < K / 8) {
             const uint4 q = *reinterpret_cast<const uint4*>(sm + m * p.x_pitch + k * 16);
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
             uint4 o;
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
             for (int x = 1; x < 4 * SUBS; x <<= 1)
                 sum += __shfl_xor_sync(~0u, sum, x);
-            if (k < a.K / 8 && lane % (4 * SUBS) == 0)
+            if (k < K / 8 && lane % (4 * SUBS) == 0)
                 sums[m * groups + k / (4 * SUBS)] = sum * -4.76837158203125e-07f;    // -8 2^-24
         }
     }
@@ -315,14 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     const float v0 = __uint_as_float((uint32_t)(127 + down / 2) << 23), v1 = __uint_as_float((uint32_t)(127 + down - down / 2) << 23);
     uint32_t st = ring;
     const int a0r = r * row_scale & 3, a1r = (r + 8) * row_scale & 3;
-    for (int u = blockIdx.x + team * gridDim.x; u < nunits; u += stride) {
+    // the clusters' CTAs go through the same number of joins
+    const int rounds = p.cs > 1 ? (nunits + stride - 1) / stride : first < nunits ? (nunits - first + stride - 1) / stride : 0;
+    for (int round = 0, u = first; round < rounds; ++round, u += stride) {
+        const int my_steps = u < nunits ? nsteps : 0;
         float acc[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 acc[i][k] = 0.0f;
-        for (int s = part; s < nsteps; s += p.ks) {
+        for (int s = part; s < my_steps; s += p.ks) {
             load();
             // all groups but the youngest stages - 1 are complete
             if (p.stages == 6)
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
             else
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
-            const int at0 = a0r + s * SB, at1 = a1r + s * SB;       // (low two bits)
+            const int at0 = a0r + (step0 + s) * SB, at1 = a1r + (step0 + s) * SB;   // (low two bits)
             const uint32_t s0 = st + kCodeBytes + r * SW * 4, s1 = s0 + 8 * SW * 4;
             uint32_t e0[2], e1[2];                          // MXFP4: the two rows' eight scales
             bool plain = true;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                 }
                 plain = !__any_sync(~0u, odd_byte(e0[0]) || odd_byte(e0[1]) || odd_byte(e1[0]) || odd_byte(e1[1]));
             }
-            const int ng = min(PER, (a.K - s * kCols) / kGroup);
+            const int ng = min(PER, (K - s * kCols) / kGroup);
             auto one_group = [&](int g) {
                 float part_sum[NT][4];
 #pragma unroll
@@ -437,7 +450,51 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(p.ks * 32) : "memory");
         }
+        bool mine = part == 0 && u < nunits;
         if (part == 0)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // (a token that does not exist has any factor)
+                    acc[i][k] *= fac[min(8 * i + 2 * c + (k & 1), p.tokens - 1)];
+                    if constexpr (FMT == MOE_FMT_INT4)
+                        acc[i][k] = acc[i][k] * v0 * v1;
+                }
+        if (p.cs > 1) {
+            // the cluster's parts of the columns: CTA `team % cs` adds up a team's rows.  Two
+            // buffers in turn: a CTA is past its reads of one when it arrives for the other
+            const uint32_t slots = (teams + p.cs - 1) / p.cs, buf = (round & 1) * slots + team / p.cs;
+            const uint32_t join = tc::su32(sm + p.off_join) + buf * p.cs * (NT * 512) + lane * 16;
+            if (mine) {
+                uint32_t at;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(join + rank * (NT * 512)), "r"(team % p.cs));
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                                 ::"r"(at + i * 512), "f"(acc[i][0]), "f"(acc[i][1]), "f"(acc[i][2]), "f"(acc[i][3]) : "memory");
+            }
+            __syncwarp();
+            if (round == 0)
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            mine = mine && team % p.cs == (int)rank;
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][k] = 0.0f;
+                for (int w = 0; w < p.cs; ++w)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 v = lds128(join + w * (NT * 512) + i * 512);
+                        acc[i][0] += __uint_as_float(v.x), acc[i][1] += __uint_as_float(v.y);
+                        acc[i][2] += __uint_as_float(v.z), acc[i][3] += __uint_as_float(v.w);
+                    }
+            }
+        }
+        if (mine)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int row = u * kRows + r + (k >> 1) * 8;
@@ -449,10 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     const int m = 8 * i + 2 * c + (k & 1);
                     if (m >= p.tokens)
                         continue;
-                    float y = acc[i][k] * fac[m];
-                    if constexpr (FMT == MOE_FMT_INT4)
-                        y = y * v0 * v1;
-                    y = a.bias ? y + bias : y;
+                    const float y = a.bias ? acc[i][k] + bias : acc[i][k];
                     const long long at = m * a.out_stride + row;
                     if (a.out_type == MOE_DT_BF16)
                         static_cast<uint16_t*>(a.out)[at] = tc::f2bf16_rne(y);
@@ -484,7 +538,28 @@ int align16(int v) { return (v + 15) & ~15; }
 
 }  // namespace
 
-cudaError_t prepare_linear_kernels()
+// Clusters that run at once, 0 where there are none.
+int clusters_of(Kernel k)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = kCluster;
+    cfg.blockDim = kThreads;
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+cudaError_t prepare_linear_kernels(int* clusters)
 {
     for (int nt = 1; nt <= 2; ++nt)
         for (int i = 0; i < 5; ++i) {
@@ -493,52 +568,95 @@ cudaError_t prepare_linear_kernels()
             if (e != cudaSuccess)
                 return e;
         }
+    *clusters = clusters_of(kernel_for(MOE_FMT_MXFP4, 32, 2));
     return cudaSuccess;
 }
 
-cudaError_t launch_linear(const LinearArgs& args, int num_sms, cudaStream_t s)
+namespace {
+
+// Tokens of a pass (as many as fit in shared memory, 16 at most), the split of the
+// columns and the shared memory for `ctas` groups of cs CTAs; returns what all
+// passes are expected to take, in ns.  A round (every team's next 16 rows) costs
+// 900 per stage of the busiest warp, 400 more for a second tile of tokens, some 700
+// for a join in the CTA and 1,400 for one in the cluster; x costs 33 per KB that a
+// CTA takes in.  Fitted to 512..60,000 rows of 512..8,192 columns for 1, 8 and 16
+// tokens, every split: the choice is within 1 % of the best one on average, 12 % at
+// worst.
+long long plan(Plan& p, const LinearArgs& a, int cs, int ctas)
 {
-    // tokens in passes of at most 16, and of no more than fit in shared memory
-    // (one launch for 16 tokens of up to 3,520 columns)
-    LinearArgs a = args;
-    const int most = kXBytes / (2 * a.K + 128) < 16 ? kXBytes / (2 * a.K + 128) : 16;
-    for (int m0 = 0; m0 < args.M; m0 += most) {
-        Plan p{};
-        p.tokens = args.M - m0 < most ? args.M - m0 : most;
-        const int nt = p.tokens > 8 ? 2 : 1;
-        // pitch of 64 mod 128 bytes: two tokens' 64-byte pieces cover all banks
-        p.x_pitch = (2 * a.K + 63) / 128 * 128 + 64;
-        int off = p.tokens * p.x_pitch;
-        p.off_sum = off;
-        if (a.fmt == MOE_FMT_INT4)
-            off = align16(off + p.tokens * (a.K / a.group) * 4);
-        p.off_fac = off;
-        off += 256;                       // factors, the common exponent, largest magnitudes
-        p.off_red = off;
-        off += kWarps * nt * 512;
-        p.off_ring = (off + 127) / 128 * 128;
-        p.stage_bytes = kCodeBytes + (kRows * scale_words(a.fmt, a.group) * 4 + 127) / 128 * 128;
-        p.stages = (kSmem - p.off_ring) / (kWarps * p.stage_bytes);
-        if (p.stages > kMostStages)
-            p.stages = kMostStages;
-        // stages that the busiest warp goes through, for each split of the columns;
-        // a finer one costs a join, so it has to save a tenth
-        const int units = (a.N + kRows - 1) / kRows, steps = (a.K + kCols - 1) / kCols;
-        long long best = -1;
-        for (int ks = 1; ks <= kWarps && ks <= steps; ks *= 2) {
-            const long long teams = (long long)num_sms * (kWarps / ks);
-            const long long cost = (units + teams - 1) / teams * ((steps + ks - 1) / ks);
-            if (best < 0 || 10 * cost <= 9 * best) {
-                best = cost;
-                p.ks = ks;
-            }
+    const int units = (a.N + kRows - 1) / kRows, steps = (a.K + kCols - 1) / kCols;
+    p.cs = cs;
+    p.steps = (steps + cs - 1) / cs;
+    const int K = p.steps * kCols < a.K ? p.steps * kCols : a.K;
+    const int most = kXBytes / (2 * K + 128) < 16 ? kXBytes / (2 * K + 128) : 16;
+    p.tokens = a.M < most ? a.M : most;
+    const int nt = p.tokens > 8 ? 2 : 1;
+    long long best = -1;
+    for (int ks = 1; ks <= kWarps && ks <= p.steps; ks *= 2) {
+        const long long teams = (long long)ctas * (kWarps / ks), rounds = (units + teams - 1) / teams;
+        const int stages = (p.steps + ks - 1) / ks;
+        const long long cost = rounds * (stages * (nt == 1 ? 900 : 1300) + (ks > 1 ? 700 + 33 * ks : 0) + (cs > 1 ? 1400 : 0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.ks = ks;
         }
-        const int grid = units < num_sms ? units : num_sms;
+    }
+    // pitch of 64 mod 128 bytes: two tokens' 64-byte pieces cover all banks
+    p.x_pitch = (2 * K + 63) / 128 * 128 + 64;
+    int off = p.tokens * p.x_pitch;
+    p.off_sum = off;
+    if (a.fmt == MOE_FMT_INT4)
+        off = align16(off + p.tokens * (K / a.group) * 4);
+    p.off_fac = off;
+    off += 256;                       // factors, the common exponent, largest magnitudes
+    p.off_red = off;
+    off += kWarps * nt * 512;
+    p.off_join = off;
+    if (cs > 1)
+        off += 2 * ((kWarps / p.ks + cs - 1) / cs) * cs * nt * 512;
+    p.off_ring = (off + 127) / 128 * 128;
+    p.stage_bytes = kCodeBytes + (kRows * scale_words(a.fmt, a.group) * 4 + 127) / 128 * 128;
+    p.stages = (kSmem - p.off_ring) / (kWarps * p.stage_bytes);
+    if (p.stages > kMostStages)
+        p.stages = kMostStages;
+    return (a.M + most - 1) / most * (3500 + 33LL * p.tokens * K * 2 / 1024 + best);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& args, int num_sms, int clusters, cudaStream_t s)
+{
+    LinearArgs a = args;
+    Plan alone, shared;
+    bool clustered = false;
+    if (clusters > 0 && a.K > kCols)
+        clustered = plan(shared, a, kCluster, clusters) < plan(alone, a, 1, num_sms);
+    else
+        plan(alone, a, 1, num_sms);
+    const int most = clustered ? shared.tokens : alone.tokens, units = (a.N + kRows - 1) / kRows;
+    for (int m0 = 0; m0 < args.M; m0 += most) {
+        Plan p;
+        a.M = args.M - m0 < most ? args.M - m0 : most;
+        if (clustered)
+            plan(p, a, kCluster, clusters);
+        else
+            plan(p, a, 1, num_sms);
+        const int groups = clustered ? clusters : num_sms, grid = (units < groups ? units : groups) * p.cs;
+        const int nt = p.tokens > 8 ? 2 : 1;
         a.x = args.x + m0 * args.x_stride;
         a.out = static_cast<uint8_t*>(args.out) + m0 * args.out_stride * (args.out_type == MOE_DT_BF16 ? 2 : 4);
-        a.M = p.tokens;
-        kernel_for(a.fmt, a.group, nt)<<<grid, kThreads, p.off_ring + kWarps * p.stages * p.stage_bytes, s>>>(a, p);
-        const cudaError_t e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = p.cs;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = kThreads;
+        cfg.dynamicSmemBytes = p.off_ring + kWarps * p.stages * p.stage_bytes;
+        cfg.stream = s;
+        cfg.attrs = at;
+        cfg.numAttrs = p.cs > 1 ? 1 : 0;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(a.fmt, a.group, nt), a, p);
         if (e != cudaSuccess)
             return e;
     }

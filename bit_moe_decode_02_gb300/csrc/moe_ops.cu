@@ -93,7 +93,7 @@ int moe_ops_create(moe_ops** out)
                          cudaGetErrorString(e));
     }
     if ((e = cudaMemset(o->status, 0, sizeof(int))) != cudaSuccess || (e = cudaMemset(o->ws, 0, o->ws_bytes)) != cudaSuccess ||
-        (e = moe::prepare_attention_kernels()) != cudaSuccess || (e = moe::prepare_linear_kernels()) != cudaSuccess ||
+        (e = moe::prepare_attention_kernels()) != cudaSuccess || (e = moe::prepare_linear_kernels(&o->clusters)) != cudaSuccess ||
         (e = moe::prepare_sample_kernels()) != cudaSuccess || (e = cudaDeviceSynchronize()) != cudaSuccess) {
         moe_ops_destroy(o);
         return cuda_fail(e, "moe_ops_create");
@@ -235,7 +235,7 @@ int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long
     moe::LinearArgs a{static_cast<const uint8_t*>(w->codes), w->scales, static_cast<const uint16_t*>(w->bias), w->rows, w->cols,
                       w->format, w->group, static_cast<const uint16_t*>(x_bf16), x_stride, M, out, out_stride, out_type,
                       o->status};
-    const cudaError_t e = moe::launch_linear(a, o->num_sms, (cudaStream_t)stream);
+    const cudaError_t e = moe::launch_linear(a, o->num_sms, o->clusters, (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_linear");
 }
 

@@ -12,6 +12,7 @@
 struct moe_ops {
     int device = 0;
     int num_sms = 0;
+    int clusters = 0;            // of moe_linear's CTAs that run at once
     int* status = nullptr;       // device word, as a moe_handle's
     uint8_t* ws = nullptr;       // workspace of the calls, ws_bytes, zeroed once
     size_t ws_bytes = 0;
@@ -69,8 +70,8 @@ struct LinearArgs {
     int out_type;
     int* status;
 };
-cudaError_t prepare_linear_kernels();
-cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t s);
+cudaError_t prepare_linear_kernels(int* clusters);
+cudaError_t launch_linear(const LinearArgs& a, int num_sms, int clusters, cudaStream_t s);
 
 struct SampleArgs {
     const void* logits;
