@@ -126,8 +126,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
 __device__ __forceinline__ float e8m0(int e) { return __int_as_float(max(e << 23, 0x400000) + (e + 1 >> 8)); }
 // Whether one of four bytes is 0 or 255.
 __device__ __forceinline__ bool odd_byte(uint32_t w) { return __vcmpeq4(w, 0u) | __vcmpeq4(w, 0xffffffffu); }
-// FMT, 32-column blocks of a group, 8-token tiles.
-template <int FMT, int SUBS, int NT>
+
+// FMT, 32-column blocks of a group, 8-token tiles, whether a cluster's CTAs share rows.
+template <int FMT, int SUBS, int NT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan p)
 {
     constexpr int kGroup = 32 * SUBS, SB = scale_bytes(FMT, kGroup), SW = scale_words(FMT, kGroup);
@@ -136,19 +137,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int team = warp / p.ks, part = warp % p.ks, teams = kWarps / p.ks;
     uint32_t rank = 0;
-    if (p.cs > 1) {
+    if (SHARED) {
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first join
     }
     // this CTA's columns, counted from the first of them
-    const int step0 = rank * p.steps, K = max(min(a.K - step0 * kCols, p.steps * kCols), 0);
+    const int step0 = SHARED ? rank * p.steps : 0, K = SHARED ? max(min(a.K - step0 * kCols, p.steps * kCols), 0) : a.K;
     const int nunits = (a.N + kRows - 1) / kRows, nsteps = (K + kCols - 1) / kCols;
     const int row_scale = FMT == MOE_FMT_MXFP4 ? a.K / 32 : 2 * (a.K / kGroup);   // bytes
     const uint32_t ring = tc::su32(sm + p.off_ring) + warp * p.stages * p.stage_bytes;
     const int half_k = a.K / 2;
 
     // this warp's stream: its stages of each of its team's units
-    const int nclusters = gridDim.x / p.cs, first = blockIdx.x / p.cs + team * nclusters, stride = nclusters * teams;
+    const int cs = SHARED ? kCluster : 1, nclusters = gridDim.x / cs, first = blockIdx.x / cs + team * nclusters, stride = nclusters * teams;
     int pu = first, ps = part;                                     // next to load
     uint32_t pst = ring;
     const uint32_t ring_end = ring + p.stages * p.stage_bytes;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     uint32_t st = ring;
     const int a0r = r * row_scale & 3, a1r = (r + 8) * row_scale & 3;
     // the clusters' CTAs go through the same number of joins
-    const int rounds = p.cs > 1 ? (nunits + stride - 1) / stride : first < nunits ? (nunits - first + stride - 1) / stride : 0;
+    const int rounds = SHARED ? (nunits + stride - 1) / stride : first < nunits ? (nunits - first + stride - 1) / stride : 0;
     for (int round = 0, u = first; round < rounds; ++round, u += stride) {
         const int my_steps = u < nunits ? nsteps : 0;
         float acc[NT][4];
@@ -461,14 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     if constexpr (FMT == MOE_FMT_INT4)
                         acc[i][k] = acc[i][k] * v0 * v1;
                 }
-        if (p.cs > 1) {
+        if constexpr (SHARED) {
             // the cluster's parts of the columns: CTA `team % cs` adds up a team's rows.  Two
             // buffers in turn: a CTA is past its reads of one when it arrives for the other
-            const uint32_t slots = (teams + p.cs - 1) / p.cs, buf = (round & 1) * slots + team / p.cs;
-            const uint32_t join = tc::su32(sm + p.off_join) + buf * p.cs * (NT * 512) + lane * 16;
+            const uint32_t slots = (teams + cs - 1) / cs, buf = (round & 1) * slots + team / cs;
+            const uint32_t join = tc::su32(sm + p.off_join) + buf * cs * (NT * 512) + lane * 16;
             if (mine) {
                 uint32_t at;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(join + rank * (NT * 512)), "r"(team % p.cs));
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(join + rank * (NT * 512)), "r"(team % cs));
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
                     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
@@ -478,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
             if (round == 0)
                 asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-            mine = mine && team % p.cs == (int)rank;
+            mine = mine && team % cs == (int)rank;
             if (mine) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         acc[i][k] = 0.0f;
-                for (int w = 0; w < p.cs; ++w)
+                for (int w = 0; w < cs; ++w)
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const uint4 v = lds128(join + w * (NT * 512) + i * 512);
@@ -521,17 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 typedef void (*Kernel)(LinearArgs, Plan);
 
 template <int FMT, int SUBS>
-Kernel pick(int nt)
+Kernel pick(int nt, bool shared)
 {
-    return nt == 1 ? linear_kernel<FMT, SUBS, 1> : linear_kernel<FMT, SUBS, 2>;
+    if (shared)
+        return nt == 1 ? linear_kernel<FMT, SUBS, 1, true> : linear_kernel<FMT, SUBS, 2, true>;
+    return nt == 1 ? linear_kernel<FMT, SUBS, 1, false> : linear_kernel<FMT, SUBS, 2, false>;
 }
 
-Kernel kernel_for(int fmt, int group, int nt)
+Kernel kernel_for(int fmt, int group, int nt, bool shared)
 {
     if (fmt == MOE_FMT_MXFP4)
-        return pick<MOE_FMT_MXFP4, 1>(nt);
-    return group == 32 ? pick<MOE_FMT_INT4, 1>(nt) : group == 64 ? pick<MOE_FMT_INT4, 2>(nt)
-         : group == 128 ? pick<MOE_FMT_INT4, 4>(nt) : pick<MOE_FMT_INT4, 8>(nt);
+        return pick<MOE_FMT_MXFP4, 1>(nt, shared);
+    return group == 32 ? pick<MOE_FMT_INT4, 1>(nt, shared) : group == 64 ? pick<MOE_FMT_INT4, 2>(nt, shared)
+         : group == 128 ? pick<MOE_FMT_INT4, 4>(nt, shared) : pick<MOE_FMT_INT4, 8>(nt, shared);
 }
 
 int align16(int v) { return (v + 15) & ~15; }
@@ -562,13 +565,13 @@ int clusters_of(Kernel k)
 cudaError_t prepare_linear_kernels(int* clusters)
 {
     for (int nt = 1; nt <= 2; ++nt)
-        for (int i = 0; i < 5; ++i) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel_for(i ? MOE_FMT_INT4 : MOE_FMT_MXFP4, 16 << i, nt),
+        for (int i = 0; i < 10; ++i) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel_for(i / 2 ? MOE_FMT_INT4 : MOE_FMT_MXFP4, 16 << i / 2, nt, i & 1),
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             if (e != cudaSuccess)
                 return e;
         }
-    *clusters = clusters_of(kernel_for(MOE_FMT_MXFP4, 32, 2));
+    *clusters = clusters_of(kernel_for(MOE_FMT_MXFP4, 32, 2, true));
     return cudaSuccess;
 }
 
@@ -656,7 +659,7 @@ cudaError_t launch_linear(const LinearArgs& args, int num_sms, int clusters, cud
         cfg.stream = s;
         cfg.attrs = at;
         cfg.numAttrs = p.cs > 1 ? 1 : 0;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(a.fmt, a.group, nt), a, p);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_for(a.fmt, a.group, nt, clustered), a, p);
         if (e != cudaSuccess)
             return e;
     }
