@@ -137,3 +137,30 @@ def test_strided_rows_and_repeats():
     moe.moe_linear(o, w, x.contiguous(), z)
     ok(o)
     assert torch.equal(y, z)
+
+
+# Many tokens of many columns: four CTAs share the rows and split the columns in pieces of 256, the last of which
+# may be short or none.
+@pytest.mark.parametrize("fmt,group", [(F4, 32), (I4, 32), (I4, 64), (I4, 128), (I4, 256)])
+@pytest.mark.parametrize("rows,cols,M", [(40, 1280, 16), (1, 2048, 13), (700, 2304, 12), (2501, 4096, 16), (9, 8192, 16),
+                                         (33, 4096, 40), (20000, 4096, 16)])
+def test_columns_split_over_ctas(fmt, group, rows, cols, M):
+    check(rows, cols, M, fmt, group, bias=M % 2 == 0, out=torch.bfloat16 if rows % 2 else torch.float32, seed=rows + M)
+
+
+@pytest.mark.parametrize("cols", [1056, 2080, 4128, 8160])
+def test_columns_split_over_ctas_with_odd_ends(cols):
+    check(77, cols, 16, F4, 32, bias=True, seed=cols)
+    check(77, cols, 11, I4, 32, seed=cols + 1)
+
+
+@pytest.mark.parametrize("fmt,group", [(F4, 32), (I4, 64)])
+def test_parts_of_the_columns_of_other_sizes(fmt, group):
+    """Parts of a token that are zero, tiny or huge beside the others."""
+    x = torch.randn(16, 4096, device="cuda")
+    x[:, :1024] = 0
+    x[0:4, 1024:2048] *= 2.0 ** -60
+    x[2:6, 2048:] *= 2.0 ** 40
+    x[7] = 0
+    x[8, :3000] = 0
+    check(70, 4096, 16, fmt, group, x=x.bfloat16())
