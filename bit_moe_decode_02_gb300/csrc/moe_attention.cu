@@ -776,7 +776,7 @@ void launch_one(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     unsigned* cnt = reinterpret_cast<unsigned*>(a.ws);
     decode_attn_kernel<D, FMT, BLK><<<num_sms, kThreads, Decode<D, FMT, BLK>::smem(a.c.n_seqs), s>>>(
-        a, reinterpret_cast<float*>(a.ws + 4096), cnt);
+        a, reinterpret_cast<float*>(a.ws + kCounterBytes), cnt);
 }
 
 template <int D, int FMT>
@@ -794,7 +794,7 @@ void launch_blocks(const AttnArgs& a, int num_sms, cudaStream_t s)
 
 size_t attention_workspace_bytes(int num_sms)
 {
-    return 4096 + (size_t)num_sms * 2 * (1 + kMaxGroups) * slot_floats() * sizeof(float);
+    return kCounterBytes + (size_t)num_sms * (2 + kMaxGroups) * slot_floats() * sizeof(float);
 }
 
 cudaError_t prepare_attention_kernels()

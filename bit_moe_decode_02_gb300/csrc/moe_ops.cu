@@ -88,8 +88,9 @@ int moe_ops_create(moe_ops** out)
     if ((e = cudaMalloc(&o->status, sizeof(int))) != cudaSuccess || (e = cudaMalloc(&o->ws, o->ws_bytes)) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(o->status);
+        const int sms = o->num_sms;
         delete o;
-        return set_error(MOE_ERR_OOM, "moe_ops_create: workspace (%zu bytes) failed: %s", moe::attention_workspace_bytes(1),
+        return set_error(MOE_ERR_OOM, "moe_ops_create: workspace (%zu bytes) failed: %s", moe::attention_workspace_bytes(sms),
                          cudaGetErrorString(e));
     }
     if ((e = cudaMemset(o->status, 0, sizeof(int))) != cudaSuccess || (e = cudaMemset(o->ws, 0, o->ws_bytes)) != cudaSuccess ||
@@ -124,7 +125,9 @@ int moe_ops_get_status(moe_ops* o, void* stream)
         return cuda_fail(e, "moe_ops_get_status");
     if (st == 0)
         return MOE_OK;
+    // a call that gave up may have left joins half done
     if ((e = cudaMemsetAsync(o->status, 0, sizeof(int), s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(o->ws, 0, moe::kCounterBytes, s)) != cudaSuccess ||
         (e = cudaStreamSynchronize(s)) != cudaSuccess)
         return cuda_fail(e, "moe_ops_get_status");
     return set_error(st, st == MOE_ERR_DEVICE_FAULT ? "a batch's lengths or a block number were out of range"

@@ -14,12 +14,13 @@ struct moe_ops {
     int num_sms = 0;
     int clusters = 0;            // of moe_linear's CTAs that run at once
     int* status = nullptr;       // device word, as a moe_handle's
-    uint8_t* ws = nullptr;       // workspace of the calls, ws_bytes, zeroed once
+    uint8_t* ws = nullptr;       // workspace of the calls, ws_bytes: join counters (zero between calls), partial results
     size_t ws_bytes = 0;
 };
 
 namespace moe {
 
+constexpr int kCounterBytes = 4096;      // of a workspace: one join counter per CTA
 constexpr int kMaxSeqs = 1024;          // sequences of one batch
 constexpr int kMaxBatchQ = 1 << 20;     // tokens of one batch
 
