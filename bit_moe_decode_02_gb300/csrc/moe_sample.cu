@@ -21,6 +21,12 @@
 // temperatures) find the last member by histograms of counts and weights that
 // narrow a bin down to one key (the logit's order-preserving bits), and how many of
 // the tokens that share the key are in; those take a few more passes.
+// What bounds it: rows are read three times, from L2 after the first (5 to 12 us a pass
+// for 64 rows of 151,643, the last one's exponentials the longest); between passes a
+// cluster barrier (0.7 us), the bins' sums over the cluster and their prefix sums (5
+// us), and one CTA's choice of the last member (3 to 5 us).  Measured, one row of 32,000
+// and 64 rows of 151,643 fp32 logits: largest logit only 4.3 and 7.1 us, no filter 9.8
+// and 20, top-k 50 16 and 30, top-p 0.9 23 and 47, all filters mixed 20 and 57.
 #include <cooperative_groups.h>
 #include <cstdint>
 

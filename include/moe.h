@@ -426,19 +426,22 @@ void moe_destroy(moe_handle* h);
  * the workspace and a status word; the conventions at the top of this file
  * (status codes, checks before anything is enqueued, streams, one thread and
  * one stream at a time per handle, nothing allocated by a call, no host work
- * that depends on device values) hold for it too.  Each call is one launch and can be captured in a CUDA graph.  What a device-side check finds (metadata that does not describe the
+ * that depends on device values) hold for it too.  Each call is one launch
+ * (moe_linear: one for each pass of up to 16 tokens) and can be captured in a CUDA
+ * graph.  What a device-side check finds (metadata that does not describe the
  * batch, a block number outside the cache) sets MOE_ERR_DEVICE_FAULT in the
  * handle's status word and skips that sequence or block.
  * ====================================================================== */
 
 typedef struct moe_ops moe_ops;
 
-/* A handle on the current device: allocates the workspace (a few MB, whatever
- * the sizes of later calls). */
+/* A handle on the current device: allocates the workspace (12.7 MB on 152 SMs,
+ * whatever the sizes of later calls). */
 int moe_ops_create(moe_ops** out);
 
 /* Synchronise `stream`; return (and clear) the handle's device status: MOE_OK,
- * MOE_ERR_DEVICE_FAULT or MOE_ERR_DEVICE_TIMEOUT, or MOE_ERR_CUDA. */
+ * MOE_ERR_DEVICE_FAULT or MOE_ERR_DEVICE_TIMEOUT, or MOE_ERR_CUDA.  After a
+ * non-OK status the handle can be used again. */
 int moe_ops_get_status(moe_ops* o, void* stream);
 
 /* Release the workspace.  NULL is a no-op. */
@@ -451,8 +454,10 @@ void moe_ops_destroy(moe_ops* o);
  *          (transposed: attention multiplies V along the tokens);
  *   scales fp32 [num_blocks][kv_heads][2] (K, V), 8-byte aligned.
  * A value is its code times the scale.  MOE_KV_INT8: codes -127..127.
- * MOE_KV_E4M3: OCP FP8 E4M3 codes (no NaN is ever written) and scales that
- * are powers of two.  block 32, 64 or 128; head_dim 64 or 128; kv_heads
+ * MOE_KV_E4M3: OCP FP8 E4M3 codes and scales that are powers of two.  A cache
+ * holds no NaN code (0x7f, 0xff: none is ever written) and no scale that is negative,
+ * infinite or NaN; what attention makes of one is not defined, but stays in the
+ * sequences whose tables name the block.  block 32, 64 or 128; head_dim 64 or 128; kv_heads
  * 1..256. */
 typedef enum { MOE_KV_E4M3 = 1, MOE_KV_INT8 = 2 } moe_kv_format;
 typedef struct {
@@ -515,7 +520,8 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * is 0, with the sink (or -inf) as its lse.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
- * product as f16. */
+ * product as f16.  The (sequence, 16 rows, kv head, block) combinations of one call
+ * number less than 2^31 (else nothing is written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
                   long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,
                   float* lse, void* stream);
@@ -540,8 +546,9 @@ typedef struct {
  * int4 dequantised on chip).  x bf16 [M][cols], rows x_stride elements apart
  * (16-byte aligned, a multiple of 8); out fp32 or bf16 [M][rows], rows
  * out_stride elements apart.  x enters as f16 after an exact power-of-two
- * rescale per token, weights are exact in f16, sums are fp32.  x and out must
- * not overlap. */
+ * rescale of a token (or of a quarter of its columns), which keeps what is above
+ * 2^-37 of its largest element (int4: every other element above 2^-33); weights are
+ * exact in f16, sums are fp32.  x and out must not overlap. */
 int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long long x_stride, int M, void* out,
                long long out_stride, int out_type, void* stream);
 
