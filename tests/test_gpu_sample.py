@@ -33,7 +33,7 @@ def sample(logits, temperature=None, top_k=None, top_p=None, min_p=None, u=None,
     return tok.cpu().numpy(), lp.cpu().numpy() if logprob else None
 
 
-def judge(l, T, k, p, q, u, tok, lp):
+def agrees(l, T, k, p, q, u, tok, lp):
     """Whether `tok` is the definition's token for one row, within the exponential's error."""
     l = np.where(np.isnan(l), -np.inf, l).astype(np.float32)
     top = l.max()
@@ -79,7 +79,7 @@ def check(logits, T=None, k=None, p=None, q=None, seed=0, u=None):
     host = logits.float().cpu().numpy()
     g = lambda a, m, d: d if a is None else a[m]  # noqa: E731
     for m in range(M):
-        assert judge(host[m], g(T, m, 1.0), g(k, m, 0), g(p, m, None), g(q, m, 0.0), u[m], tok[m], lp[m]), (m, tok[m], lp[m])
+        assert agrees(host[m], g(T, m, 1.0), g(k, m, 0), g(p, m, None), g(q, m, 0.0), u[m], tok[m], lp[m]), (m, tok[m], lp[m])
 
 
 def rows(M, V, seed=0, sigma=2.5, dtype=torch.float32):
