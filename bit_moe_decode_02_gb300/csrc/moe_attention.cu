@@ -232,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ i64 scan[kWarps];
     __shared__ int s_flag;
-    __shared__ int s_run[2];
     int* pre = reinterpret_cast<int*>(sm + C::OFF_PRE);
     Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
     float2* mls = reinterpret_cast<float2*>(sm + C::OFF_ML);
@@ -296,27 +295,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     const int N = (int)all, G = min((int)gridDim.x, N);       // CTAs with work
     if ((int)blockIdx.x >= G)
         return;
-    // the CTA's run of tiles, its ends moved to the start of an item where that is
-    // short: a join over CTAs costs more than two more tiles a group
+    // The CTA's run of tiles, its ends moved to the start of an item where that is
+    // short: a join over CTAs costs more than two more tiles a group.  Lanes 0 and 1
+    // look the ends' items up, the others that of the group's first tile should
+    // neither end move; else all look again.
     const int each = N / G, more = N - each * G;              // CTA c begins with tile c each + min(c, more)
-    if (warp < 2) {
-        const int c = blockIdx.x + warp, at = c * each + min(c, more);
-        int end = at;
-        if (at < N) {
-            Item it;
-            find_item<BLK>(a, pre, at, it);
-            if (it.jhi - it.jlo + 1 <= C::WHOLE)
-                end = it.t0;
-        }
-        if (lane == 0)
-            s_run[warp] = end;
+    int ct0 = blockIdx.x * each + min((int)blockIdx.x, more), ct1 = ct0 + each + ((int)blockIdx.x < more);
+    int t_begin, t_end;
+    auto share = [&]() {
+        const int mine = (ct1 - ct0) / C::NG, left = (ct1 - ct0) % C::NG;
+        t_begin = ct0 + grp * mine + min(grp, left);
+        t_end = t_begin + mine + (grp < left);
+    };
+    share();
+    Item it;
+    int at = lane == 0 ? ct0 : lane == 1 ? ct1 : t_begin;
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+        find_item<BLK>(a, pre, min(at, N - 1), it);
+        if (again)
+            break;
+        const int end = at < N && it.jhi - it.jlo + 1 <= C::WHOLE ? it.t0 : at, guess = t_begin;
+        ct0 = __shfl_sync(~0u, end, 0);
+        ct1 = __shfl_sync(~0u, end, 1);
+        share();
+        at = t_begin;
+        if (at == guess)
+            break;
     }
-    __syncthreads();
-    const int ct0 = s_run[0], ct1 = s_run[1], gid = blockIdx.x * C::NG + grp;
     if (ct0 == ct1)
         return;
-    const int mine = (ct1 - ct0) / C::NG, left = (ct1 - ct0) % C::NG;
-    const int t_begin = ct0 + grp * mine + min(grp, left), t_end = t_begin + mine + (grp < left);
+    it.b = __shfl_sync(~0u, it.b, 2), it.c0 = __shfl_sync(~0u, it.c0, 2), it.n = __shfl_sync(~0u, it.n, 2);
+    it.len = __shfl_sync(~0u, it.len, 2), it.rt = __shfl_sync(~0u, it.rt, 2), it.h = __shfl_sync(~0u, it.h, 2);
+    it.jlo = __shfl_sync(~0u, it.jlo, 2), it.jhi = __shfl_sync(~0u, it.jhi, 2), it.t0 = __shfl_sync(~0u, it.t0, 2);
+    const int gid = blockIdx.x * C::NG + grp;
 
     uint8_t* ring = sm + grp * C::NS * C::STAGE;
     float* hdr = reinterpret_cast<float*>(sm + C::OFF_HDR) + grp * C::NS * 4;
@@ -361,9 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         }
     };
 
+    // at first all of the ring, then the stage of the tile before
+    auto fill = [&](int t) {
+        if (sub == 0)
+#pragma unroll 1
+            while (pt < t_end && pt < t + C::NS)
+                produce();
+    };
+
     if (t_begin < t_end) {
-        Item it;
-        find_item<BLK>(a, pre, t_begin, it);
         int j = it.jlo + t_begin - it.t0;
         if (sub == 0) {
             pit = it;
@@ -380,13 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             uint32_t qf[D / 16][4];
             float f[2];                  // score = sum * block's scale * f
             int plo[2], phi[2];          // first and last visible position of this thread's two rows
+            uint32_t qw[2][D / 64][8];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = it.rt * kRows + r + 8 * e, i = row / a.group;
                 const bool in = r + 8 * e < rows;
                 phi[e] = in ? it.len - it.n + i : -1;
                 plo[e] = in && a.window > 0 ? phi[e] - a.window + 1 : 0;
-                uint32_t w[D / 64][8];
+                uint32_t (&w)[D / 64][8] = qw[e];
                 if (in) {
                     const uint16_t* q = a.q + (i64)(it.c0 + i) * a.q_stride + (i64)(it.h * a.group + row % a.group) * D + 16 * c;
 #pragma unroll
@@ -402,21 +421,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                         for (int k = 0; k < 8; ++k)
                             w[ch][k] = 0;
                 }
-                uint32_t big = 0;        // largest finite magnitude of the row
+            }
+            // the ring is filled while they are on their way
+            fill(t);
+            {
 #pragma unroll
-                for (int ch = 0; ch < D / 64; ++ch)
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t big = 0;    // largest finite magnitude of the row
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        big = max(big, big_of(w[ch][k]));
-                big = max(big, __shfl_xor_sync(~0u, big, 1));
-                big = max(big, __shfl_xor_sync(~0u, big, 2));
-                const RowScale rs = row_scale(big, a.scale);
-                f[e] = rs.f;
+                    for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
-                for (int ch = 0; ch < D / 64; ++ch)
+                        for (int k = 0; k < 8; ++k)
+                            big = max(big, big_of(qw[e][ch][k]));
+                    big = max(big, __shfl_xor_sync(~0u, big, 1));
+                    big = max(big, __shfl_xor_sync(~0u, big, 2));
+                    const RowScale rs = row_scale(big, a.scale);
+                    f[e] = rs.f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        qf[ch * 4 + k / 2][(k & 1) * 2 + e] = scale_pair(w[ch][k], rs);
+                    for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            qf[ch * 4 + k / 2][(k & 1) * 2 + e] = scale_pair(qw[e][ch][k], rs);
+                }
             }
             float o[D / 8][4], m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -431,11 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
 
             int st = 0;
             for (; t < seg_end; ++t, ++j) {
-                // fill the ring: at first all of it, then the stage of the tile before
-                if (sub == 0)
-#pragma unroll 1
-                    while (pt < t_end && pt < t + C::NS)
-                        produce();
+                fill(t);
                 st = cst;
                 tc::mbar_wait(full + st, phase, status);
                 if (++cst == C::NS) {
@@ -615,29 +637,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     const float* gslots = ws + ((i64)gridDim.x * 2 + (i64)blockIdx.x * C::NG) * slot_floats();
     float* cslots = ws + (i64)blockIdx.x * 2 * slot_floats();
     int across = 0, cross[2] = {0, 0};
-    for (int first = 0; first < 2 * C::NG;) {
-        if (!pieces[first].where) {
-            ++first;
-            continue;
-        }
-        const int t0 = pieces[first].t0;
-        const Place place = pieces[first].p;
-        int last = first + 1, slot_at = pieces[first].where == kStage ? -1 : first >> 1;
-        // the last pieces of some groups, and the first of the next one; or that alone
-        while (last < 2 * C::NG && (!pieces[last].where || pieces[last].t0 == t0)) {
-            if (pieces[last].where == kSlot)
-                slot_at = last >> 1;
-            ++last;
-        }
+    // a piece a lane
+    const Piece own = pieces[min(lane, 2 * C::NG - 1)];
+    unsigned open = __ballot_sync(~0u, lane < 2 * C::NG && own.where);
+    while (open) {
+        const int first = __ffs(open) - 1, t0 = __shfl_sync(~0u, own.t0, first), t1 = __shfl_sync(~0u, own.t1, first);
+        const Place place{__shfl_sync(~0u, own.p.c0, first), __shfl_sync(~0u, own.p.r0, first), __shfl_sync(~0u, own.p.h, first),
+                          __shfl_sync(~0u, own.p.nrows, first)};
+        // the item's pieces: the last ones of some groups, in their stages, and the first of
+        // the next one, in its slot; or that alone
+        const bool of_it = (open >> lane & 1) && own.t0 == t0;
+        open &= ~__ballot_sync(~0u, of_it);
+        const unsigned in_slot = __ballot_sync(~0u, of_it && own.where == kSlot);
+        const int slot_at = in_slot ? (__ffs(in_slot) - 1) >> 1 : -1;
         // the warps whose results lie in their groups' stages, a lane each
-        const Piece& mine_last = pieces[(lane & (kWarps - 1)) / C::GW * 2 + 1];
-        const unsigned warps = __ballot_sync(~0u, lane < kWarps && mine_last.where == kStage && mine_last.t0 == t0);
-        const int stage = mine_last.stage;
+        const int piece_of = (lane & (kWarps - 1)) / C::GW * 2 + 1, stage = __shfl_sync(~0u, own.stage, piece_of);
+        const unsigned staged = __ballot_sync(~0u, of_it && own.where == kStage);
+        const unsigned warps = __ballot_sync(~0u, lane < kWarps && (staged >> piece_of & 1));
         int ods[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             ods[w] = (w / C::GW * C::NS + __shfl_sync(~0u, stage, w)) * C::STAGE + w % C::GW * (kRows * D * 4);
-        const bool done = t0 >= ct0 && pieces[first].t1 <= ct1;
+        const bool done = t0 >= ct0 && t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
             const int row = x / (D / 4), col = x % (D / 4) * 4, at = row * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
@@ -675,7 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             across |= 1 << which;
             cross[which] = first;
         }
-        first = last;
     }
 
     // ---- items that span CTAs: the last one to arrive joins them all
@@ -702,12 +722,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         if (!s_flag)
             continue;
         __threadfence();
-        // maxima and sums of every part and row, then their weights, in the ring
-        const int K = cb - ca + 1, rows = place.nrows;
+        // maxima and sums of every part and row, then their weights, in the ring; every 4
+        // columns' parts are summed by `split` threads, then those.  The first parts are
+        // on their way while the weights are worked out
+        const int K = cb - ca + 1, rows = place.nrows, n4 = rows * (D / 4), split = n4 <= kThreads / 2 ? kThreads / n4 : 1;
         float2* part = reinterpret_cast<float2*>(sm);                    // [K][kRows]; .x becomes the weight
         float2* total = part + gridDim.x * kRows;                        // [kRows]
         float4* acc = reinterpret_cast<float4*>(total + kRows);          // [kThreads]
         auto slot_of = [&](int k) { return ws + ((i64)(ca + k) * 2 + (k == 0)) * slot_floats(); };
+        constexpr int AHEAD = 8;
+        float4 y[AHEAD];
+        auto load_parts = [&](int x, int k0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (x < n4 && k0 + i * split < K)
+                    y[i] = __ldcg(reinterpret_cast<const float4*>(slot_of(k0 + i * split) + 4 * x));
+        };
+        const int from = split > 1 ? tid / n4 : 0, x_first = split > 1 ? (from < split ? tid % n4 : n4) : tid;
+        load_parts(x_first, from);
         for (int i = tid; i < K * rows; i += kThreads)
             part[i / rows * kRows + i % rows] = __ldcg(reinterpret_cast<const float2*>(slot_of(i / rows) + kRows * D + 2 * (i % rows)));
         __syncthreads();
@@ -732,20 +764,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 total[row] = make_float2(M, L);
         }
         __syncthreads();
-        // every 4 columns' parts summed by `split` threads, then those
-        const int n4 = rows * (D / 4), split = n4 <= kThreads / 2 ? kThreads / n4 : 1;
         for (int x0 = 0; x0 < n4; x0 += kThreads) {
-            const int x = split > 1 ? tid % n4 : x0 + tid, from = split > 1 ? tid / n4 : 0;
+            const int x = x0 + x_first, row = x / (D / 4), col = x % (D / 4) * 4;
             float4 v = make_float4(0, 0, 0, 0);
-            const int row = x / (D / 4), col = x % (D / 4) * 4;
-            if (x < n4 && from < split) {
-#pragma unroll 8
-                for (int k = from; k < K; k += split) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + row * D + col));
-                    const float w = part[k * kRows + row].x;
-                    v.x += y.x * w, v.y += y.y * w, v.z += y.z * w, v.w += y.w * w;
+            if (x0)
+                load_parts(x, from);
+            if (x < n4)
+                for (int k0 = from; k0 < K;) {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i)
+                        if (k0 + i * split < K) {
+                            const float w = part[(k0 + i * split) * kRows + row].x;
+                            v.x += y[i].x * w, v.y += y[i].y * w, v.z += y[i].z * w, v.w += y[i].w * w;
+                        }
+                    k0 += AHEAD * split;
+                    load_parts(x, k0);
                 }
-            }
             if (split > 1) {
                 acc[tid] = v;
                 __syncthreads();
