@@ -27,12 +27,12 @@
 //    unit only when a block's scale leaves [ref / 2, 2 ref]; the running maximum
 //    likewise moves only when a score passes it by 2^8 (p' <= 2^9 in f16).
 // Measured: 64 sequences of 12,000 tokens on average, 32 heads of 128 on 4 (INT8),
-// 155 us, 5.3 TB/s of codes, 0.78 of a plain copy's rate.  Two warps a scheduler (230
+// 154 us, 5.35 TB/s of codes, 0.79 of a plain copy's rate.  Two warps a scheduler (230
 // registers) are two chains of conversions and MMAs, which issue 0.4 instructions a
 // cycle: that, not the loads in flight, is what is left.  One sequence of 4,300
-// tokens, 64 heads of 64 on 8: 12.4 us, nearly all of it the way through: 1.5 us to
-// find the tiles, the first loads, a join in the CTA (2 us) and one over the CTAs (4);
-// the same heads within a window of 128, 4 sequences: 7.7 us.
+// tokens, 64 heads of 64 on 8: 11.4 us, nearly all of it the way through: 1.9 us to
+// find the tiles, 1.3 for the first loads, 0.9 for the tiles, a join in the CTA (1.1)
+// and one over the CTAs (5); the same heads within a window of 128, 4 sequences: 7.0 us.
 #include <cstdint>
 
 #include "attn_device.cuh"
