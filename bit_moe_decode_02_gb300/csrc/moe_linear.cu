@@ -34,36 +34,16 @@
 
 #include <cuda_fp16.h>
 
+#include "linear_plan.h"
 #include "ops_internal.h"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16;
+using namespace linear;
+
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;
-constexpr int kCols = 256;                 // columns of a stage
-constexpr int kCodeBytes = kRows * kCols / 2;
-constexpr int kXBytes = 112 * 1024;        // most of x that a CTA keeps: two stages a warp still fit
-constexpr int kSmem = 224 * 1024;
-constexpr int kMostStages = 6;
-constexpr int kCluster = 4;                // CTAs that share their rows, where they do
-
-// Bytes of one row's scales in a stage, and the aligned 4-byte words that may hold them.
-__host__ __device__ constexpr int scale_bytes(int fmt, int group) { return fmt == MOE_FMT_MXFP4 ? kCols / 32 : 2 * kCols / group; }
-__host__ __device__ constexpr int scale_words(int fmt, int group) { return scale_bytes(fmt, group) / 4 + 1; }
-
-struct Plan {
-    int tokens;     // of this pass
-    int cs;         // CTAs of a cluster, which share all rows: each takes `steps` stages of columns
-    int steps;
-    int ks;         // warps of a CTA that share 16 rows
-    int stages;
-    int x_pitch;    // bytes of one token's x
-    int off_sum, off_fac, off_red, off_join, off_ring;
-    int stage_bytes;
-};
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -546,10 +526,6 @@ Kernel kernel_for(int fmt, int group, int nt, bool shared)
          : group == 128 ? pick<MOE_FMT_INT4, 4>(nt, shared) : pick<MOE_FMT_INT4, 8>(nt, shared);
 }
 
-int align16(int v) { return (v + 15) & ~15; }
-
-}  // namespace
-
 // Clusters that run at once, 0 where there are none.
 int clusters_of(Kernel k)
 {
@@ -571,6 +547,8 @@ int clusters_of(Kernel k)
     return n;
 }
 
+}  // namespace
+
 cudaError_t prepare_linear_kernels(int* clusters)
 {
     for (int nt = 1; nt <= 2; ++nt)
@@ -584,76 +562,21 @@ cudaError_t prepare_linear_kernels(int* clusters)
     return cudaSuccess;
 }
 
-namespace {
-
-// Tokens of a pass (as many as fit in shared memory, 16 at most), the split of the
-// columns and the shared memory for `ctas` groups of cs CTAs; returns what all
-// passes are expected to take, in ns.  A round (every team's next 16 rows) costs
-// 900 per stage of the busiest warp, 400 more for a second tile of tokens, some 700
-// for a join in the CTA and 1,400 for one in the cluster; x costs 33 per KB that a
-// CTA takes in.  Fitted to 512..60,000 rows of 512..8,192 columns for 1, 8 and 16
-// tokens, every split: the choice is within 1 % of the best one on average, 12 % at
-// worst.
-long long plan(Plan& p, const LinearArgs& a, int cs, int ctas)
-{
-    const int units = (a.N + kRows - 1) / kRows, steps = (a.K + kCols - 1) / kCols;
-    p.cs = cs;
-    p.steps = (steps + cs - 1) / cs;
-    const int K = p.steps * kCols < a.K ? p.steps * kCols : a.K;
-    const int most = kXBytes / (2 * K + 128) < 16 ? kXBytes / (2 * K + 128) : 16;
-    p.tokens = a.M < most ? a.M : most;
-    const int nt = p.tokens > 8 ? 2 : 1;
-    long long best = -1;
-    for (int ks = 1; ks <= kWarps && ks <= p.steps; ks *= 2) {
-        const long long teams = (long long)ctas * (kWarps / ks), rounds = (units + teams - 1) / teams;
-        const int stages = (p.steps + ks - 1) / ks;
-        const long long cost = rounds * (stages * (nt == 1 ? 900 : 1300) + (ks > 1 ? 700 + 33 * ks : 0) + (cs > 1 ? 1400 : 0));
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.ks = ks;
-        }
-    }
-    // pitch of 64 mod 128 bytes: two tokens' 64-byte pieces cover all banks
-    p.x_pitch = (2 * K + 63) / 128 * 128 + 64;
-    int off = p.tokens * p.x_pitch;
-    p.off_sum = off;
-    if (a.fmt == MOE_FMT_INT4)
-        off = align16(off + p.tokens * (K / a.group) * 4);
-    p.off_fac = off;
-    off += 256;                       // factors, the common exponent, largest magnitudes
-    p.off_red = off;
-    off += kWarps * nt * 512;
-    p.off_join = off;
-    if (cs > 1)
-        off += 2 * ((kWarps / p.ks + cs - 1) / cs) * cs * nt * 512;
-    p.off_ring = (off + 127) / 128 * 128;
-    p.stage_bytes = kCodeBytes + (kRows * scale_words(a.fmt, a.group) * 4 + 127) / 128 * 128;
-    p.stages = (kSmem - p.off_ring) / (kWarps * p.stage_bytes);
-    if (p.stages > kMostStages)
-        p.stages = kMostStages;
-    return (a.M + most - 1) / most * (3500 + 33LL * p.tokens * K * 2 / 1024 + best);
-}
-
-}  // namespace
-
 cudaError_t launch_linear(const LinearArgs& args, int num_sms, int clusters, cudaStream_t s)
 {
     LinearArgs a = args;
-    Plan alone, shared;
-    bool clustered = false;
-    if (clusters > 0 && a.K > kCols)
-        clustered = plan(shared, a, kCluster, clusters) < plan(alone, a, 1, num_sms);
-    else
-        plan(alone, a, 1, num_sms);
-    const int most = clustered ? shared.tokens : alone.tokens, units = (a.N + kRows - 1) / kRows;
+    const Plan first = choose({a.N, a.K, a.fmt, a.group, a.M}, num_sms, clusters);
+    const bool clustered = first.cs > 1;
+    const int most = first.tokens, units = (a.N + kRows - 1) / kRows, groups = clustered ? clusters : num_sms;
+    if (most < 1)
+        return cudaErrorInvalidConfiguration;
     for (int m0 = 0; m0 < args.M; m0 += most) {
-        Plan p;
         a.M = args.M - m0 < most ? args.M - m0 : most;
-        if (clustered)
-            plan(p, a, kCluster, clusters);
-        else
-            plan(p, a, 1, num_sms);
-        const int groups = clustered ? clusters : num_sms, grid = (units < groups ? units : groups) * p.cs;
+        Plan p;
+        plan(p, {a.N, a.K, a.fmt, a.group, a.M}, first.cs, groups);
+        if (p.stages < kLeastStages || p.tokens < a.M)       // the kernel waits for all but the youngest stage
+            return cudaErrorInvalidConfiguration;
+        const int grid = (units < groups ? units : groups) * p.cs;
         const int nt = p.tokens > 8 ? 2 : 1;
         a.x = args.x + m0 * args.x_stride;
         a.out = static_cast<uint8_t*>(args.out) + m0 * args.out_stride * (args.out_type == MOE_DT_BF16 ? 2 : 4);
@@ -664,7 +587,7 @@ cudaError_t launch_linear(const LinearArgs& args, int num_sms, int clusters, cud
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.gridDim = grid;
         cfg.blockDim = kThreads;
-        cfg.dynamicSmemBytes = p.off_ring + kWarps * p.stages * p.stage_bytes;
+        cfg.dynamicSmemBytes = p.smem();
         cfg.stream = s;
         cfg.attrs = at;
         cfg.numAttrs = p.cs > 1 ? 1 : 0;

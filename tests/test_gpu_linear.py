@@ -164,3 +164,20 @@ def test_parts_of_the_columns_of_other_sizes(fmt, group):
     x[7] = 0
     x[8, :3000] = 0
     check(70, 4096, 16, fmt, group, x=x.bfloat16())
+
+
+# Wide matrices: x and the cluster's join buffer leave the rings little of the shared memory, so that the split that would
+# be fastest may not fit.
+@pytest.mark.parametrize("fmt,group", [(F4, 32), (I4, 32), (I4, 64)])
+@pytest.mark.parametrize("rows,cols", [(5120, 13824), (7168, 18432), (8192, 22016), (2560, 11296)])
+@pytest.mark.parametrize("M", [9, 13, 16, 40])
+def test_wide_matrices(fmt, group, rows, cols, M):
+    if cols % group:
+        cols += group - cols % group
+    check(rows, cols, M, fmt, group, bias=M % 2 == 0, out=torch.bfloat16 if M == 16 else torch.float32, seed=cols + M)
+
+
+@pytest.mark.parametrize("fmt,group,rows,cols,M", [(I4, 128, 16384, 17536, 16), (I4, 256, 16384, 17664, 15), (F4, 32, 16384, 16384, 16),
+                                                   (I4, 64, 40000, 14336, 64), (F4, 32, 300, 32768, 16), (I4, 256, 300, 32768, 16)])
+def test_widest_matrices(fmt, group, rows, cols, M):
+    check(rows, cols, M, fmt, group, seed=cols + M)
