@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     uint32_t rank = 0;
     if (SHARED) {
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first join
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // waited for before the first remote store
     }
     // this CTA's columns, counted from the first of them
     const int step0 = SHARED ? rank * p.steps : 0, K = SHARED ? max(min(a.K - step0 * kCols, p.steps * kCols), 0) : a.K;
@@ -456,6 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
             // buffers in turn: a CTA is past its reads of one when it arrives for the other
             const uint32_t slots = (teams + cs - 1) / cs, buf = (round & 1) * slots + team / cs;
             const uint32_t join = tc::su32(sm + p.off_join) + buf * cs * (NT * 512) + lane * 16;
+            if (round == 0) {
+                // another CTA's shared memory may be written once that CTA has started
+                __syncwarp();
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            }
             if (mine) {
                 uint32_t at;
                 asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(join + rank * (NT * 512)), "r"(team % cs));
@@ -465,8 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                                  ::"r"(at + i * 512), "f"(acc[i][0]), "f"(acc[i][1]), "f"(acc[i][2]), "f"(acc[i][3]) : "memory");
             }
             __syncwarp();
-            if (round == 0)
-                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
             mine = mine && team % cs == (int)rank;
             if (mine) {

@@ -181,3 +181,17 @@ def test_wide_matrices(fmt, group, rows, cols, M):
                                                    (I4, 64, 40000, 14336, 64), (F4, 32, 300, 32768, 16), (I4, 256, 300, 32768, 16)])
 def test_widest_matrices(fmt, group, rows, cols, M):
     check(rows, cols, M, fmt, group, seed=cols + M)
+
+
+@pytest.mark.parametrize("fmt,group", [(F4, 32), (I4, 64)])
+def test_clusters_with_a_cta_without_columns_repeat(fmt, group):
+    """1,280 columns are five pieces: two, two, one and none for a cluster's CTAs, the last of which is ready at once."""
+    o = handle()
+    _, _, _, w = make(40, 1280, fmt, group, True, 8)
+    x = torch.randn(16, 1280, device="cuda").bfloat16()
+    y = torch.empty(200, 16, 40, device="cuda")
+    for i in range(200):
+        moe.moe_linear(o, w, x, y[i])
+    ok(o)
+    assert torch.equal(y, y[:1].expand_as(y))
+    check(40, 1280, 16, fmt, group, bias=True, seed=8)

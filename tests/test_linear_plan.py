@@ -1,5 +1,5 @@
-"""moe_linear's plan, run on the host over the sizes that a call may have: every pass has a ring of at least two
-stages (one is loaded while one is read), fits in shared memory, and together they take all tokens."""
+"""moe_linear without a GPU: its plan, run on the host over the sizes that a call may have: every pass has a ring of at least two
+stages (one is loaded while one is read), fits in shared memory, and together they take all tokens; and the order of a cluster's first steps."""
 import os
 import subprocess
 
@@ -67,3 +67,12 @@ def test_every_size_has_a_plan_that_fits(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_a_cluster_has_started_before_its_memory_is_written():
+    """Every CTA arrives at the cluster's barrier as it starts; the first store to another CTA's shared memory comes after
+    the wait for those arrivals.  (The order is invisible in results: starting nearly always takes less than reading x.)"""
+    with open(os.path.join(build_ext.CSRC, "moe_linear.cu")) as f:
+        kernel = f.read()
+    arrive, wait, store = (kernel.index(w) for w in ("barrier.cluster.arrive", "barrier.cluster.wait", "st.shared::cluster"))
+    assert arrive < wait < store
