@@ -49,7 +49,7 @@ inline bool lay_out(Plan& p, const Size& a)
     if (a.fmt == MOE_FMT_INT4)
         off = (off + p.tokens * (K / a.group) * 4 + 15) & ~15;
     p.off_fac = off;
-    off += 256;                       // factors, the common exponent, largest magnitudes
+    off += 256;                       // factors, largest magnitudes
     p.off_red = off;
     off += kWarps * nt * 512;
     p.off_join = off;

@@ -203,9 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 
     // x: f16, scaled per token, and (int4) each group's sum.  Pieces of 256 columns
     // of a token, dealt over the warps
-    float* fac = reinterpret_cast<float*>(sm + p.off_fac);
-    int* ups = reinterpret_cast<int*>(fac + 16);
-    uint32_t* bigs = reinterpret_cast<uint32_t*>(ups + 1);
+    float2* fac = reinterpret_cast<float2*>(sm + p.off_fac);      // per token, what its totals are multiplied by
+    uint32_t* bigs = reinterpret_cast<uint32_t*>(fac + 16);
     float* sums = reinterpret_cast<float*>(sm + p.off_sum);
     const int groups = K / kGroup, pieces = p.tokens * nsteps;
     const uint16_t* xsrc = a.x + step0 * kCols;
@@ -251,13 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
     }
     __syncthreads();
     auto up_of = [&](int m) { return 14 + 127 - max((int)(bigs[m] >> 7), 1); };
-    if (warp == kWarps - 1) {
-        // the totals are kept in the units of the token that is scaled up least
-        const int own = up_of(min(lane, p.tokens - 1)), up = __reduce_min_sync(~0u, own);
-        if (lane == 0)
-            *ups = up;
-        if (lane < p.tokens)
-            fac[lane] = ldexpf(1.0f, up - own);
+    if (warp == kWarps - 1 && lane < p.tokens) {
+        // MXFP4: 2^-up, which joins the weights' scales.  int4: 2^(24 - up) in two factors
+        const int down = FMT == MOE_FMT_INT4 ? 24 - up_of(lane) : -up_of(lane), half = FMT == MOE_FMT_INT4 ? down / 2 : 0;
+        fac[lane] = make_float2(ldexpf(1.0f, down - half), ldexpf(1.0f, half));
     }
     for (int i = warp; i < pieces; i += kWarps) {
         const int m = i / nsteps, k = i % nsteps * 32 + lane, up = up_of(m);
@@ -309,10 +305,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
 #pragma unroll
     for (int b = 0; b < 8; ++b)
         cp[b] = r * 128 + ((b ^ r) << 4) + 4 * c;          // a 32-column block's codes in a stage
-    const float unit = FMT == MOE_FMT_MXFP4 ? ldexpf(1.0f, -*ups) : 1.0f;
-    // int4's totals are in units of 2^-24 and of the token that is scaled up least: 2^(24 - up), in two factors
-    const int down = FMT == MOE_FMT_INT4 ? 24 - *ups : 0;
-    const float v0 = __uint_as_float((uint32_t)(127 + down / 2) << 23), v1 = __uint_as_float((uint32_t)(127 + down - down / 2) << 23);
+    // MXFP4: a token's totals are kept in its own units all along, whatever the others' size: weights' scales reach
+    // from 2^-127 to 2^127, so that no unit for all tokens keeps every total in range
+    float unit[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            unit[i][k] = FMT == MOE_FMT_MXFP4 ? fac[min(8 * i + 2 * c + k, p.tokens - 1)].x : 1.0f;
     uint32_t st = ring;
     const int a0r = r * row_scale & 3, a1r = (r + 8) * row_scale & 3;
     // the clusters' CTAs go through the same number of joins
@@ -389,11 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                     const uint32_t v = e0[g >> 2], y = e1[g >> 2];
                     if (plain) {
                         // the byte to bits 23..30
-                        f0 = __uint_as_float(__byte_perm(v, 0, 0x0444 | (g & 3) << 12) >> 1) * unit;
-                        f1 = __uint_as_float(__byte_perm(y, 0, 0x0444 | (g & 3) << 12) >> 1) * unit;
+                        f0 = __uint_as_float(__byte_perm(v, 0, 0x0444 | (g & 3) << 12) >> 1);
+                        f1 = __uint_as_float(__byte_perm(y, 0, 0x0444 | (g & 3) << 12) >> 1);
                     } else {
-                        f0 = e8m0(v >> 8 * (g & 3) & 255) * unit;
-                        f1 = e8m0(y >> 8 * (g & 3) & 255) * unit;
+                        f0 = e8m0(v >> 8 * (g & 3) & 255);
+                        f1 = e8m0(y >> 8 * (g & 3) & 255);
                     }
                 } else {
                     f0 = __half2float(__ushort_as_half((unsigned short)lds_u16(s0 + (at0 & 3) + 2 * g)));
@@ -401,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    acc[i][0] += f0 * part_sum[i][0];
-                    acc[i][1] += f0 * part_sum[i][1];
-                    acc[i][2] += f1 * part_sum[i][2];
-                    acc[i][3] += f1 * part_sum[i][3];
+                    acc[i][0] += f0 * unit[i][0] * part_sum[i][0];
+                    acc[i][1] += f0 * unit[i][1] * part_sum[i][1];
+                    acc[i][2] += f1 * unit[i][0] * part_sum[i][2];
+                    acc[i][3] += f1 * unit[i][1] * part_sum[i][3];
                 }
             };
             if (ng == PER) {
@@ -441,16 +441,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, Plan 
             asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(p.ks * 32) : "memory");
         }
         bool mine = part == 0 && u < nunits;
-        if (part == 0)
+        if constexpr (FMT == MOE_FMT_INT4)
+            if (part == 0)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // (a token that does not exist has any factor)
-                    acc[i][k] *= fac[min(8 * i + 2 * c + (k & 1), p.tokens - 1)];
-                    if constexpr (FMT == MOE_FMT_INT4)
-                        acc[i][k] = acc[i][k] * v0 * v1;
-                }
+                    for (int k = 0; k < 4; ++k) {
+                        // (a token that does not exist has any factor)
+                        const float2 v = fac[min(8 * i + 2 * c + (k & 1), p.tokens - 1)];
+                        acc[i][k] = acc[i][k] * v.x * v.y;
+                    }
         if constexpr (SHARED) {
             // the cluster's parts of the columns: CTA `team % cs` adds up a team's rows.  Two
             // buffers in turn: a CTA is past its reads of one when it arrives for the other

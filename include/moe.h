@@ -548,7 +548,9 @@ typedef struct {
  * out_stride elements apart.  x enters as f16 after an exact power-of-two
  * rescale of a token (or of a quarter of its columns), which keeps what is above
  * 2^-37 of its largest element (int4: every other element above 2^-33); weights are
- * exact in f16, sums are fp32.  x and out must not overlap. */
+ * exact in f16, sums are fp32.  A token's result does not depend on the other
+ * tokens; a token with an infinity or NaN has no finite result (int4: NaN).  x and
+ * out must not overlap. */
 int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long long x_stride, int M, void* out,
                long long out_stride, int out_type, void* stream);
 

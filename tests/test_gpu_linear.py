@@ -195,3 +195,21 @@ def test_clusters_with_a_cta_without_columns_repeat(fmt, group):
     ok(o)
     assert torch.equal(y, y[:1].expand_as(y))
     check(40, 1280, 16, fmt, group, bias=True, seed=8)
+
+
+@pytest.mark.parametrize("fmt,group", [(F4, 32), (I4, 32), (I4, 256)])
+@pytest.mark.parametrize("M,cols", [(5, 512), (13, 768), (16, 4096), (11, 1280)])
+def test_tokens_of_very_different_size(fmt, group, M, cols):
+    """Finite tokens near both ends of bf16's range beside ordinary ones, as rows of memory that nothing has set may be:
+    each token's result keeps its own bound (the check's) whatever the others are; with clusters and without."""
+    g = torch.Generator(device="cuda").manual_seed(M + cols)
+    x = torch.randn(M, cols, generator=g, device="cuda") * 8
+    x[1] *= 2.0 ** -100
+    x[3] *= 2.0 ** -123
+    x[2, 17] = x[M - 1, cols - 3] = 2.0 ** 125
+    x = x.bfloat16()
+    y = check(70, cols, M, fmt, group, x=x, seed=3)
+    ordinary = [m for m in range(M) if m not in (1, 2, 3, M - 1)]
+    z = check(70, cols, M, fmt, group, x=torch.where(torch.isin(torch.arange(M, device="cuda"), torch.tensor(ordinary, device="cuda"))[:, None], x, 0.0),
+              seed=3)
+    assert torch.equal(y[ordinary], z[ordinary])
