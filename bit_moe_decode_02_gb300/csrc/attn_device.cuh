@@ -12,6 +12,10 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;         // running maximum of a row that has seen no key
 constexpr float kSlack = 8.0f;            // log2 units that a score may pass the kept maximum by
+// A probability p = e^(s - m) is 2^6 p in f16: at most 2^15 with the slack and a unit that is
+// off by 2, so that 11 bits are kept down to 2^-20 of the kept maximum and none below 2^-31
+constexpr float kRoom = 6.0f;
+constexpr float kUnroom = 0.015625f;      // 2^-6
 
 // Four code bytes -> two f16 pairs, exact.
 template <int FMT>
@@ -75,10 +79,11 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, const RowScale& r)
 }
 
 // The unit that O is kept in: it changes only when a block's V scale leaves
-// [ref / 2, 2 ref], and stays within 2^40 of the largest seen.
+// [ref / 2, 2 ref], and stays within 2^80 of the largest seen (O is below 2^44: 2^15 of a
+// probability, 2^9 of a code, 2^20 keys).
 __device__ __forceinline__ float new_unit(float vs, float vmax)
 {
-    return fmaxf(fmaxf(vs, vmax * 9.094947017729282e-13f), 7.52316384526264e-37f);   // 2^-40, 2^-120
+    return fmaxf(fmaxf(vs, vmax * 8.271806125530277e-25f), 7.52316384526264e-37f);   // 2^-80, 2^-120
 }
 
 // One row's final value from its sums: the sink joins the denominator.

@@ -22,7 +22,10 @@
 //    product's A operand from there.
 //  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
 //    scores, V's enters the exponent; O is rescaled in tensor memory only where a
-//    row's maximum grows by more than 2^8, or the unit changes.
+//    row's maximum grows by more than 2^8, or the unit changes.  The unit is the
+//    largest V scale of a tile, whether a row sees that block or not, which takes bits
+//    of the other blocks' probabilities: a tile whose V scales are more than 2^6 apart
+//    goes through as several, one block each.
 #include <cstdint>
 
 #include "attn_device.cuh"
@@ -35,7 +38,7 @@ using namespace attn;
 constexpr int kThreads = 768;
 constexpr int kRows = 256;                // of a CTA
 constexpr int kKeys = 128;                // of a tile
-constexpr int kRing = 8;                  // tiles whose scales are kept
+constexpr int kRing = 8;                  // tiles whose scales are kept: the loads are at most four ahead of the softmax
 
 template <int D, int BLK>
 struct Layout {
@@ -48,7 +51,8 @@ struct Layout {
     static constexpr int OFF_RAW = OFF_V + 2 * OP;
     static constexpr int OFF_SC = OFF_RAW + 2 * RAW;      // [kRing][4] (K scale, V scale), K scale < 0: no block
     static constexpr int OFF_BAR = OFF_SC + kRing * 4 * 8;
-    static constexpr int OFF_MAX = OFF_BAR + 24 * 8;      // [2 row tiles][2 halves][128]
+    static constexpr int OFF_INFO = OFF_BAR + 24 * 8;     // [kRing]: position of the first key, bit 0: the last tile
+    static constexpr int OFF_MAX = OFF_INFO + kRing * 4;  // [2 row tiles][2 halves][128]
     static constexpr int SMEM = OFF_MAX + 2 * 2 * 128 * 4;   // 226.4 KB for D = 128, of 227
 };
 
@@ -205,11 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     uint64_t *raw_full = bar, *raw_empty = bar + 2, *k_full = bar + 4, *k_empty = bar + 6, *v_full = bar + 8, *v_empty = bar + 10;
     uint64_t *s_full = bar + 12, *p_full = bar + 14, *o_full = bar + 16, *q_full = bar + 18;
     float2* sc = reinterpret_cast<float2*>(sm + L::OFF_SC);
+    int* info = reinterpret_cast<int*>(sm + L::OFF_INFO);
 
     const int rows = min(w.n * a.group - w.rt * kRows, kRows), na = rows > 128 ? 2 : 1;     // row tiles with rows
     const int i0 = w.rt * kRows / a.group, i1 = (w.rt * kRows + rows - 1) / a.group;        // first and last token
     const int pos0 = w.len - w.n + i0, pos1 = w.len - w.n + i1;
     const int tile0 = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kKeys : 0, nt = pos1 / kKeys - tile0 + 1;
+    // `info` says which tile is the last one; this bounds the loops should a wait have given up
+    const int most = nt * L::NB;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -247,23 +254,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         };
         int id = block_of(0);
         float2 s = scales_of(id);
-        for (int t = 0; t < nt; ++t) {
-            if (lane < L::NB)
-                sc[(t % kRing) * 4 + lane] = s;
-            const int next = block_of(t + 1);
+        int t = 0;
+#pragma unroll 1
+        for (int tile = 0; tile < nt; ++tile) {
+            const int next = block_of(tile + 1);
             const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * (BLK * D);
-            const int have = __popc(__ballot_sync(~0u, id >= 0));
+            // blocks with V scales far apart go one after another
+            bool split = false;
+            if constexpr (L::NB > 1) {
+                float big = id >= 0 ? s.y : 0.0f, small = big > 0.0f ? big : INFINITY;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                if (t >= 1)
-                    tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_expect_tx(raw_full + v, (uint32_t)have * (BLK * D));
-                __syncwarp();
-                if (id >= 0)
-                    tc::bulk_copy(sm + L::OFF_RAW + v * L::RAW + lane * (BLK * D), src + v * (BLK * D), BLK * D, raw_full + v);
+                for (int o = 1; o < L::NB; o <<= 1) {
+                    big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+                    small = fminf(small, __shfl_xor_sync(~0u, small, o));
+                }
+                split = __shfl_sync(~0u, big > 64.0f * small, 0);
             }
+            unsigned left = split ? __ballot_sync(~0u, id >= 0) : 0u;
+            do {
+                const unsigned now = split ? left & (~left + 1) : ~0u;
+                left &= ~now;
+                const bool have = id >= 0 && (now >> lane & 1);
+                if (lane < L::NB)
+                    sc[(t % kRing) * 4 + lane] = have ? s : make_float2(-1.0f, 0.0f);
+                if (lane == 0)
+                    info[t % kRing] = (tile0 + tile) * kKeys | (tile + 1 == nt && !left);
+                const int n = __popc(__ballot_sync(~0u, have));
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    if (t >= 1)
+                        tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_expect_tx(raw_full + v, (uint32_t)n * (BLK * D));
+                    __syncwarp();
+                    if (have)
+                        tc::bulk_copy(sm + L::OFF_RAW + v * L::RAW + lane * (BLK * D), src + v * (BLK * D), BLK * D, raw_full + v);
+                }
+                ++t;
+            } while (left);
             id = next;
             s = scales_of(id);
         }
@@ -292,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         tc::mbar_wait(q_full, 0, status);
         for (int x = 0; x < na; ++x)
             scores(x, 0);
-        for (int t = 0; t < nt; ++t) {
+        for (int t = 0; t < most; ++t) {
             const int st = t & 1;
+            const bool last = info[t % kRing] & 1;
             tc::mbar_wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
             for (int x = 0; x < na; ++x) {
                 tc::mbar_wait(p_full + x, (uint32_t)(t & 1), status);
@@ -303,13 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     for (int k = 0; k < kKeys / 16; ++k)
                         mma_ts(one, tmem + 256 + x * 128, tmem + x * 128 + 8 * k + (k >= 4 ? 32 : 0), vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
                     commit(one, v_empty + st);
-                    if (t + 1 == nt)
+                    if (last)
                         commit(one, o_full + x);
                 }
                 __syncwarp();
-                if (t + 1 < nt)
+                if (!last)
                     scores(x, t + 1);
             }
+            if (last)
+                break;
         }
     } else if (warp >= 4 && warp < 8) {
         // ---- codes -> f16 operands (zero where there is no block)
@@ -324,10 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 tc::mbar_arrive(empty);
             }
         };
-        for (int t = 0; t < nt; ++t) {
+        for (int t = 0; t < most; ++t) {
             const int st = t & 1;
             const float2* tsc = sc + (t % kRing) * 4;
             tc::mbar_wait(raw_full, (uint32_t)(t & 1), status);
+            const bool last = info[t % kRing] & 1;
             if (t >= 2)
                 tc::mbar_wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
             {
@@ -390,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 }
             }
             arrive(v_full + st, raw_empty + 1);
+            if (last)
+                break;
         }
     } else if (warp >= 8) {
         // ---- softmax: two threads a row, one for each 64 keys of a tile
@@ -434,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             const int all_lo = a.window > 0 ? w.len - w.n + (w.rt * kRows + min(rows, x * 128 + 128) - 1) / a.group - a.window + 1 : 0;
             float m = kNone, l = 0.0f, ref = 0.0f, vmax = 0.0f;
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
-                const int p0 = (tile0 + t) * kKeys;
+            for (int t = 0; t < most; ++t) {
                 tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
+                const int word = info[t % kRing], p0 = word & ~1;
                 float top = 0.0f;
                 bool whole = p0 >= all_lo && p0 + kKeys - 1 <= all_hi;
 #pragma unroll
@@ -508,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 for (int g = 0; g < 2; ++g) {
                     const float2 kv = sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK];
                     const float c = fmaxf(kv.x * f, 1e-37f), ratio = fmaxf(kv.y * iref, 8.673617379884035e-19f);   // 2^-60
-                    const float off = lg2(ratio) - m;
+                    const float off = lg2(ratio) - m + kRoom;
                     uint32_t v[32], p[16];
                     take(g, v, kv.x);
                     const float2 cc = make_float2(c, c), oo = make_float2(off, off);
@@ -530,16 +565,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(p_full + x);
+                if (word & 1)
+                    break;
             }
             // ---- the row's result, half of its columns each
             pair_sync();                     // both have read the last maxima
             *mine = l;
             pair_sync();
-            l += *other;
+            l = (l + *other) * kUnroom;
             tc::mbar_wait(o_full + x, 0, status);
             tc::tc_fence_after();
             const Final fin = finish(m, l, a.sinks, hq);
-            const float mul = fin.mul * ref;
+            const float mul = fin.mul * ref * kUnroom;
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {

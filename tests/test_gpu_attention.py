@@ -202,3 +202,30 @@ def test_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk", [32, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(32, 16), (2, 1)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_blocks_that_a_row_does_not_see_take_no_bits(fmt, blk, D, heads, kv, window):
+    """Prompts from position 0 whose later blocks have scales of V 2^20 apart, growing over the first tile of 128 keys; with a
+    window, every other block 2^20 larger: rows that see only small blocks are as exact as if the others were not there."""
+    lens = [700, 300]
+    c = Cache(lens, kv, D, blk, fmt, seed=4).fill(seed=9)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // blk)):
+            c.scales[int(c.table[b, j]), :, 1] *= 2.0 ** (20 * (j % 2) if window else 20 * min(j, 3))
+    check(c, lens, lens, heads, window=window)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk", [32, 64, 128])
+@pytest.mark.parametrize("heads,kv,new", [(32, 16, 650), (32, 16, 1), (2, 1, 40)])
+def test_a_much_larger_block_out_of_the_window(fmt, blk, heads, kv, new):
+    """A block of V that is 2^60 larger, which earlier rows of the same call see and later ones do not."""
+    c = Cache([700], kv, 64, blk, fmt, seed=4).fill(seed=10)
+    big = (700 - new) // blk
+    c.scales[int(c.table[0, big]), :, 1] *= 2.0 ** 60
+    check(c, [new], [700], heads, window=blk)
