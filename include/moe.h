@@ -520,7 +520,7 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * is 0, with the sink (or -inf) as its lse.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
- * product as f16.  The (sequence, 16 rows, kv head, block) combinations of one call
+ * product as 11 bits down to 2^-20, below that within 2^-31.  The (sequence, 16 rows, kv head, block) combinations of one call
  * number less than 2^31 (else nothing is written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
                   long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,

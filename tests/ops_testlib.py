@@ -125,8 +125,9 @@ class Cache:
         return k, w
 
 
-def attention(cache: Cache, new, kv_len, q, scale, window=0, sinks=None):
-    """(out, lse, bound) in float64.  bound: what an f16 probability, fp32 scores and one rounding to bf16 may cost."""
+def attention(cache: Cache, new, kv_len, q, scale, window=0, sinks=None, least=2.0 ** -24):
+    """(out, lse, bound) in float64.  bound: what an f16 probability, fp32 scores and one rounding to bf16 may cost; `least`:
+    what a key's probability may lose below f16's normal numbers."""
     outs, lses, bounds, at = [], [], [], 0
     Hq = q.shape[1]
     G = Hq // cache.H
@@ -155,7 +156,7 @@ def attention(cache: Cache, new, kv_len, q, scale, window=0, sinks=None):
         # a score is a sum of at most 128 fp32 products and their scaling: 2^-22 of its magnitudes' sum covers it, and as
         # much again the exponential's argument; p rounded to f16: 2^-11 of it, or 2^-25 where it is subnormal
         ds = mag.amax(-1, keepdim=True) * 2.0 ** -20
-        bound = half_ulp_bf16(o) * 1.01 + (2.0 ** -10.5 + 2 * ds) * (p @ v.abs()) + (see.double() @ v.abs()) * 2.0 ** -24 / l
+        bound = half_ulp_bf16(o) * 1.01 + (2.0 ** -10.5 + 2 * ds) * (p @ v.abs()) + (see.double() @ v.abs()) * least / l
         outs.append(o.permute(1, 0, 2))
         lses.append((m + l.log())[..., 0].permute(1, 0))
         bounds.append((bound + 1e-30).permute(1, 0, 2))

@@ -229,3 +229,28 @@ def test_a_much_larger_block_out_of_the_window(fmt, blk, heads, kv, new):
     big = (700 - new) // blk
     c.scales[int(c.table[0, big]), :, 1] *= 2.0 ** 60
     check(c, [new], [700], heads, window=blk)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk", [64, 128])
+@pytest.mark.parametrize("seqs,length,new,heads,kv", [(320, 500, 1, 1, 1), (1, 3000, 600, 32, 16)])
+def test_small_probabilities_add_up(fmt, blk, seqs, length, new, heads, kv):
+    """One key with a score 26.5 units of log2 above all others and a value of 0, as the first token of a long context may
+    be: the output is the sum of many probabilities of 2^-26.5, each of which may lose 2^-31 (2^-30 allowed)."""
+    o = handle()
+    c = Cache([length] * seqs, kv, 64, blk, fmt, seed=5).fill(seed=11)
+    first = torch.from_numpy(c.table[:, 0].astype("int64")).cuda()
+    c.codes[:, :, 0] = 0
+    c.scales[:, :, 0] = 1.0
+    c.codes[first, :, 0, 0] = 0x38 if fmt == moe.MOE_KV_E4M3 else 1           # 1.0 in the first dimension of token 0
+    c.codes[first, :, 1] = c.codes[first, :, 1].reshape(seqs, kv, 64, blk).index_fill(3, torch.tensor([0], device="cuda"), 0).flatten(2)
+    q = torch.zeros(seqs * new, heads, 64, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 18.375                                                       # 26.5 log2 units
+    out, lse = torch.empty_like(q), torch.empty(seqs * new, heads, device="cuda")
+    n, t = [new] * seqs, [length] * seqs
+    moe.moe_attention(o, c.desc, c.batch(n, t), q, out, lse, scale=1.0)
+    ok(o)
+    want, wlse, bound = attention(c, n, t, q, 1.0, least=2.0 ** -30)
+    err = (out.double() - want).abs()
+    assert (err <= bound).all(), (err / bound).max().item()
+    assert ((lse.double() - wlse).abs() <= 2.0 ** -19 * 32).all()
