@@ -243,11 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     const uint32_t tmem = tmem_base;
 
     if (warp == 0) {
-        // ---- raw codes and scales of each tile's blocks
-        const int jhi = pos1 / BLK;
+        // ---- raw codes and scales of each tile's blocks, of those that a row sees: a caller may
+        // have given the ones before a window to other sequences
+        const int jlo = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / BLK : 0, jhi = pos1 / BLK;
         auto block_of = [&](int t) {
             const int j = (tile0 + t) * L::NB + lane;
-            return lane < L::NB && t < nt && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
+            return lane < L::NB && t < nt && j >= jlo && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
         };
         auto scales_of = [&](int id) {
             return id >= 0 ? *reinterpret_cast<const float2*>(a.c.scales + ((long long)id * a.c.H + w.h) * 2) : make_float2(-1.0f, 0.0f);

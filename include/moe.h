@@ -511,7 +511,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * elements apart (16-byte aligned, a multiple of 8); query head h reads kv
  * head h / (q_heads / kv_heads); q_heads a multiple of kv_heads, at most 1024.
  * The token at position i sees positions j <= i, and with window > 0 only
- * j > i - window.  s_j = scale q . k_j;
+ * j > i - window; blocks wholly before the window of a sequence's first token of
+ * the batch are not read, and neither are their entries of the table.
+ * s_j = scale q . k_j;
  *   out = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink - m)),
  * m the largest of them, sinks fp32 [q_heads] or NULL (no such term).
  * out bf16 [n_tokens][q_heads][head_dim], contiguous, 16-byte aligned; must not
@@ -520,8 +522,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * is 0, with the sink (or -inf) as its lse.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
- * product as 11 bits down to 2^-20, below that within 2^-31.  The (sequence, 16 rows, kv head, block) combinations of one call
- * number less than 2^31 (else nothing is written, MOE_ERR_DEVICE_FAULT). */
+ * product as 11 bits down to 2^-20, below that within 2^-31.  The (sequence,
+ * 16 rows, kv head, block) combinations of one call number less than 2^31 (else
+ * nothing is written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
                   long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,
                   float* lse, void* stream);

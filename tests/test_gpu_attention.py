@@ -254,3 +254,22 @@ def test_small_probabilities_add_up(fmt, blk, seqs, length, new, heads, kv):
     err = (out.double() - want).abs()
     assert (err <= bound).all(), (err / bound).max().item()
     assert ((lse.double() - wlse).abs() <= 2.0 ** -19 * 32).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk", [32, 64, 128])
+@pytest.mark.parametrize("heads,kv", [(32, 16), (2, 1)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [600, 33, 400]])
+@pytest.mark.parametrize("gone", [-1, 0])
+def test_blocks_before_the_window_may_be_gone(fmt, blk, heads, kv, new, gone):
+    """Table entries before the window of the first new token, dropped or another's: no row needs them, and neither kernel
+    reports or reads them (block 0 holds values that would show)."""
+    lens, window = [1000, 333, 740], 50
+    c = Cache(lens, kv, 64, blk, fmt, seed=6)
+    c.table[c.table == 0] = max(set(range(1, c.codes.shape[0])) - set(c.table.flatten().tolist()))     # block 0 is another's
+    c.fill(seed=12)
+    c.scales[0] = 2.0 ** 100
+    c.dtable = i32(c.table.tolist())
+    for b, (n, t) in enumerate(zip(new, lens)):
+        c.dtable[b, :max(0, t - n - window + 1) // blk] = gone
+    check(c, new, lens, heads, window=window, sinks=torch.randn(heads, device="cuda"))
