@@ -293,12 +293,14 @@ kv_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vds
     }
 }
 
-// Upper bound on the blocks that a batch touches: a sequence with n >= 1 new
-// tokens touches at most (n - 1) / blk + 2, and no more than n.
-int touched_bound(const KvView& c)
+// CTAs along a grid's x: an upper bound on the blocks that a batch touches (a sequence
+// with n >= 1 new tokens touches at most (n - 1) / blk + 2, and no more than n), and one
+// more.  A CTA that finds its block stops at its sequence; the last one finds none, so
+// that it checks all sequences, or as many as end in one whose metadata is wrong.
+unsigned touched_grid(const KvView& c)
 {
     const long long most = (long long)c.n_tokens / c.blk + 2ll * c.n_seqs;
-    return (int)(most < c.n_tokens ? most : c.n_tokens);
+    return (unsigned)(most < c.n_tokens ? most : c.n_tokens) + 1;
 }
 
 typedef void (*WriteKernel)(KvView, const uint16_t*, const uint16_t*, long long, long long);
@@ -328,7 +330,7 @@ auto kernel_of(const KvView& c, P tag)
 cudaError_t launch_kv_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride,
                             long long v_stride, cudaStream_t s)
 {
-    const dim3 grid(touched_bound(c), c.H, 2);
+    const dim3 grid(touched_grid(c), c.H, 2);
     const size_t smem = (size_t)c.blk * (c.D / 2 + 1) * 4;
     kernel_of(c, k)<<<grid, kWriteThreads, smem, s>>>(c, k, v, k_stride, v_stride);
     return cudaGetLastError();
@@ -337,7 +339,7 @@ cudaError_t launch_kv_write(const KvView& c, const uint16_t* k, const uint16_t* 
 cudaError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride,
                            cudaStream_t s)
 {
-    const dim3 grid(touched_bound(c), c.H);
+    const dim3 grid(touched_grid(c), c.H);
     const size_t smem = (size_t)c.blk * c.D;
     kernel_of(c, k)<<<grid, kReadThreads, smem, s>>>(c, k, v, k_stride, v_stride);
     return cudaGetLastError();

@@ -216,3 +216,22 @@ def test_another_stream():
         moe.moe_kv_read(o, c.desc, b, rk, rv)
         assert moe.moe_ops_get_status(o) == 0
         assert ((rk.double() - k.double()).abs() <= 6.0 / 254 + 6 * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("n_seqs,last", [(33, 40), (33, 31), (100, 500), (65, -1)])
+def test_bad_metadata_past_the_blocks_of_the_batch(n_seqs, last):
+    """The first sequences account for every token of the batch; the metadata of the last one is wrong all the same."""
+    o = handle()
+    n = n_seqs - 1
+    c = Cache([10] * n_seqs, 1, 64, 64, moe.MOE_KV_INT8)
+    k, v = _values(n, 1, 64, 1)
+    cu = list(range(n)) + [n, last]
+    bad = moe.moe_kv_batch_of(torch.tensor(cu, dtype=torch.int32).cuda(), torch.tensor([10] * n_seqs, dtype=torch.int32).cuda(),
+                              c.dtable, n)
+    moe.moe_kv_write(o, c.desc, bad, k, v)
+    assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
+    moe.moe_kv_read(o, c.desc, bad, k.contiguous(), v.contiguous())
+    assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
+    q = torch.randn(n, 2, 64, device="cuda").bfloat16()
+    moe.moe_attention(o, c.desc, bad, q, torch.empty_like(q))
+    assert moe.moe_ops_get_status(o) == moe.MOE_ERR_DEVICE_FAULT
