@@ -86,7 +86,8 @@ __device__ __forceinline__ float new_unit(float vs, float vmax)
     return fmaxf(fmaxf(vs, vmax * 8.271806125530277e-25f), 7.52316384526264e-37f);   // 2^-80, 2^-120
 }
 
-// One row's final value from its sums: the sink joins the denominator.
+// One row's final value from its sums: the sink joins the denominator.  A row that
+// sees nothing has l = 0; a NaN (of the query, or the sink) goes through.
 struct Final {
     float mul, lse;
 };
@@ -99,8 +100,8 @@ __device__ __forceinline__ Final finish(float m, float l, const float* sinks, in
         l = l * ex2(m - M) + (ms == M ? 1.0f : ex2(ms - M));
     }
     Final f;
-    f.mul = l > 0.0f ? ex2(m - M) / l : 0.0f;
-    f.lse = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    f.mul = l == 0.0f ? 0.0f : ex2(m - M) / l;
+    f.lse = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     return f;
 }
 

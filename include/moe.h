@@ -519,7 +519,8 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * out bf16 [n_tokens][q_heads][head_dim], contiguous, 16-byte aligned; must not
  * overlap q (checked).  lse fp32 [n_tokens][q_heads] or NULL: m + log of the
  * denominator.  A row of which nothing is visible (its blocks are missing)
- * is 0, with the sink (or -inf) as its lse.
+ * is 0, with the sink (or -inf) as its lse.  A row whose q or sink has a NaN is NaN,
+ * and so is its lse; other rows are not touched by it.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
  * product as 11 bits down to 2^-20, below that within 2^-31.  The (sequence,

@@ -273,3 +273,30 @@ def test_blocks_before_the_window_may_be_gone(fmt, blk, heads, kv, new, gone):
     for b, (n, t) in enumerate(zip(new, lens)):
         c.dtable[b, :max(0, t - n - window + 1) // blk] = gone
     check(c, new, lens, heads, window=window, sinks=torch.randn(heads, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("heads,kv,new", [(32, 16, [600, 40]), (8, 2, [1, 3]), (8, 2, [1, 1])])
+def test_nan_queries_and_sinks(fmt, heads, kv, new):
+    """A NaN in one row's query, or in one head's sink, makes those rows' results and log-sum-exps NaN, and no others."""
+    o = handle()
+    lens, T = [1500, 700], sum(new)
+    c = Cache(lens, kv, 64, 64, fmt, seed=6).fill(seed=13)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    clean = torch.randn(T, heads, 64, generator=g, device="cuda").bfloat16()
+    sinks = torch.randn(heads, generator=g, device="cuda")
+    for what in ("q", "sink"):
+        q, s, bad = clean.clone(), sinks.clone(), torch.zeros(T, heads, dtype=torch.bool, device="cuda")
+        if what == "q":
+            q[0, 1, 5] = q[T - 1, heads - 1, 63] = float("nan")
+            bad[0, 1] = bad[T - 1, heads - 1] = True
+        else:
+            s[2] = float("nan")
+            bad[:, 2] = True
+        out, lse = torch.full_like(q, 9.0), torch.full((T, heads), 9.0, device="cuda")
+        moe.moe_attention(o, c.desc, c.batch(new, lens), q, out, lse, s)
+        ok(o)
+        assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+        want, wlse, bound = attention(c, new, lens, clean, 64 ** -0.5, 0, sinks)
+        assert ((out.double() - want).abs() <= bound)[~bad].all()
+        assert ((lse.double() - wlse).abs() <= 2.0 ** -19 * 64 * 8 * 5)[~bad].all()
