@@ -852,7 +852,7 @@ cudaError_t prepare_attention_kernels()
     return prepare_prompt_kernels();
 }
 
-cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t s)
+static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     if (a.c.D == 64)
         a.c.fmt == MOE_KV_E4M3 ? launch_blocks<64, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<64, MOE_KV_INT8>(a, num_sms, s);
