@@ -7,7 +7,7 @@
 // bytes a cycle, where the MMAs need 2,048; it takes 4,200, because a row tile's
 // softmax (2,300) and its MMAs (1,300) wait for one another and only the other row
 // tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
-// heads: 284 us, 963 TFLOP/s (0.52 of the measured bf16 rate).
+// heads: 287 us, 953 TFLOP/s (0.51 of the measured bf16 rate).
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.

@@ -52,12 +52,16 @@ __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w 
 // the block's new tokens sets the scale (never below the block's old one if it
 // holds earlier tokens, whose codes are rounded again where it grew), then
 // every new value is divided by it and rounded once.
-// Bound by HBM where prompts are written, 2 bytes in and 1 out per value: 6 prompts
-// of 2,700 tokens on average, 4 heads of 128 (48 MB), take 14.5 us, 3.3 TB/s, a launch
-// and a ragged end in it.  The instructions per value have to stay low (it issues on
-// 0.56 of the cycles), so blocks without NaN or infinity skip their handling.  One token
-// for each of 4 sequences is bound by latency, 2.8 us: sequence, block number, scale
-// and values are read one after another.
+// 6 prompts of 2,700 tokens on average, 4 heads of 128 (48 MB, 2 bytes in and 1 out per
+// value), take 14.5 us, 3.3 TB/s, half of a plain copy's rate: waiting for loads, not
+// HBM, bounds it (DRAM at 0.26 of its peak, the codes stay in L2; 10 of a warp's cycles
+// per instruction wait for global memory).  A thread's values go out four loads at a
+// time, behind the chain of metadata reads.  It issues on 0.56 of the cycles beside, so
+// blocks without NaN or infinity skip their handling.  One token for each of 4
+// sequences is bound by latency, 2.8 us: sequence, block number, scale and values are
+// read one after another.  Every CTA looks its sequence up 32 at a time, so many
+// sequences cost their square: one token each of 64, 256 and 1,024 sequences (8 heads
+// of 64) take 4.2, 14.5 and 121 us.
 template <int FMT, int D, int blk>
 __global__ void __launch_bounds__(kWriteThreads)
 kv_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __restrict__ vsrc, long long kstride,

@@ -1,7 +1,7 @@
 // moe_linear.cu -- y = x W^T + b for a few tokens, W in 4 bits (MXFP4, or int4
 // with group scales), in the caller's layout.
 //
-// Bound by HBM: K/2 bytes of codes a row, read once for up to 16 tokens.
+// Its floor is HBM's: K/2 bytes of codes a row, read once for up to 16 tokens.
 //  - Operands.  m16n8k16 MMAs, 16 weight rows by 8 tokens, f16 with fp32 sums.  The
 //    order of the summed index is free: a thread's operand of a 32-column block
 //    is the 4 bytes of its eight consecutive columns.  E2M1 codes become f16
@@ -13,7 +13,8 @@
 //    multiplies it into the fp32 total.
 //  - x is scaled per token by a power of two (largest magnitude into [2^13,
 //    2^15)) and converted to f16 once per CTA: exact down to 2^-37 of it (int4:
-//    2^-33 for the sixteenths).
+//    2^-33 for the sixteenths).  A token's totals stay in its own units: MXFP4 takes
+//    them into the weights' scales (1 to 2 % of the time), int4 multiplies at the end.
 //  - Loads.  Each warp streams 16 rows by 256 columns a stage (2 KB, whole 128-byte
 //    lines) through its own ring with 16-byte cp.async, XOR-swizzled so that the
 //    operand reads have no bank conflicts; the caller's row pitch gives up to
@@ -23,13 +24,15 @@
 //    the largest part of a small call is every CTA's own pass over x; there a
 //    cluster of four CTAs shares the rows, each with a quarter of the columns (and of
 //    x), and adds up through distributed shared memory.  The launch picks both by the
-//    expected time (plan()).
+//    expected time (plan(), linear_plan.h).
 // Measured: 4 tokens, 151,936 rows of 2,048 columns (int4, groups of 64) 36 us, 4.6
 // TB/s, 0.69 of a plain copy's rate: shared memory (0.67 busy) and issue slots (0.62)
 // run beside the loads.  One token, 5,120 rows of 2,880 (MXFP4) 7.3 us, 7.9 MB: 1.4 us
 // to start, 1.7 for x, 2.7 for the codes, 0.9 for the join.  13 tokens, 4,097 rows of
-// 4,096: 9.5 us, with one CTA to the rows 12.6 (7.0 of them x); 16 tokens, 16,384 rows
-// of 8,192: 33 us, 77 in the three passes that fit one CTA's shared memory.
+// 4,096: 9.5 us, with one CTA to the rows 12.6 (7.0 of them x).  More tokens of wide
+// matrices (MXFP4) take passes, each of which reads all of W: 16,384 rows of 8,192, 16
+// tokens in one, 37 us; 8,192 rows of 8,192, 8 tokens 18 us, 64 tokens in four 84;
+// 5,120 rows of 13,824, 9 tokens 26 us, 16 tokens in two 47, 64 tokens in five 133.
 #include <cstdint>
 
 #include <cuda_fp16.h>

@@ -25,8 +25,9 @@
 // for 64 rows of 151,643, the last one's exponentials the longest); between passes a
 // cluster barrier (0.7 us), the bins' sums over the cluster and their prefix sums (5
 // us), and one CTA's choice of the last member (3 to 5 us).  Measured, one row of 32,000
-// and 64 rows of 151,643 fp32 logits: largest logit only 4.3 and 7.1 us, no filter 9.8
-// and 20, top-k 50 16 and 30, top-p 0.9 23 and 47, all filters mixed 20 and 57.
+// and 64 rows of 151,643 fp32 logits, others in each call: largest logit only 4.8 and
+// 10.3 us, no filter 10 and 22, top-k 50 16 and 32, top-p 0.9 23 and 44, all filters
+// mixed 20 and 57.
 #include <cooperative_groups.h>
 #include <cstdint>
 
