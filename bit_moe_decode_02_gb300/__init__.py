@@ -12,9 +12,10 @@ moe_debug_dequant, moe_debug_route, moe_debug_stack_trace, moe_debug_forward_f32
 moe_debug_set_wait, moe_last_bytes, moe_expert_bytes, moe_last_launches, moe_last_error,
 moe_forward_noalloc, moe_debug_stream_weights, moe_destroy; and the operators around the expert
 block: moe_ops_create, moe_ops_get_status, moe_ops_destroy, moe_kv_write, moe_kv_read,
-moe_attention, moe_linear, moe_sample.  Those take torch tensors and read sizes and strides from
-them; moe_kv_cache_of, moe_kv_batch_of and moe_linear_of make the descriptors that a program
-builds once and keeps (with the tensors, which they keep alive).
+moe_attention, moe_kv_plan, moe_rope_turns, moe_rope, moe_linear, moe_lora, moe_sample.  Those take
+torch tensors and read sizes and strides from them; moe_kv_cache_of, moe_kv_batch_of, moe_kv_pool_of,
+moe_rope_of, moe_linear_of and moe_lora_of make the descriptors that a program builds once and keeps
+(with the tensors, which they keep alive).
 """
 from __future__ import annotations
 
@@ -42,6 +43,12 @@ MOE_KV_E4M3 = 1
 MOE_KV_INT8 = 2
 MOE_DT_F32 = 0
 MOE_DT_BF16 = 1
+MOE_ROPE_HALF = 0
+MOE_ROPE_INTERLEAVED = 1
+MOE_ROPE_PLAIN = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_PARTS = 2
+MOE_ROPE_WAVELENGTH = 3
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_create", "moe_load_experts", "moe_load_experts_ex", "moe_forward", "moe_forward_host",
@@ -53,7 +60,7 @@ EXPORTS = ("moe_create", "moe_load_experts", "moe_load_experts_ex", "moe_forward
            "moe_last_bytes", "moe_expert_bytes", "moe_last_launches", "moe_last_error",
            "moe_forward_noalloc", "moe_debug_stream_weights", "moe_destroy",
            "moe_ops_create", "moe_ops_get_status", "moe_ops_destroy", "moe_kv_write", "moe_kv_read",
-           "moe_attention", "moe_linear", "moe_sample")
+           "moe_attention", "moe_linear", "moe_sample", "moe_kv_plan", "moe_rope_turns", "moe_rope", "moe_lora")
 
 
 class MoeError(RuntimeError):
@@ -84,6 +91,28 @@ class moe_linear_weights(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("format", ctypes.c_int),
                 ("group", ctypes.c_int)]
+
+
+class moe_kv_pool(ctypes.Structure):
+    _fields_ = [("ring", ctypes.c_void_p), ("table", ctypes.c_void_p), ("ring_size", ctypes.c_int),
+                ("n_seqs", ctypes.c_int), ("table_stride", ctypes.c_int), ("block", ctypes.c_int)]
+
+
+class moe_rope_config(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("length", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+class moe_rope_table(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("mscale", ctypes.c_float)]
+
+
+class moe_lora_weights(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_adapters", ctypes.c_int), ("rank", ctypes.c_int), ("rows", ctypes.c_int),
+                ("cols", ctypes.c_int)]
 
 
 class moe_sample_params(ctypes.Structure):
@@ -174,6 +203,14 @@ def lib() -> ctypes.CDLL:
         L.moe_linear.restype = i
         L.moe_sample.argtypes = [p, p, i, ll, i, i, ctypes.POINTER(moe_sample_params), p, p, p]
         L.moe_sample.restype = i
+        L.moe_kv_plan.argtypes = [p, ctypes.POINTER(moe_kv_pool), p, p, p, i, p, p, p, p, p, p, p, p]
+        L.moe_kv_plan.restype = i
+        L.moe_rope_turns.argtypes = [ctypes.POINTER(moe_rope_config), p]
+        L.moe_rope_turns.restype = i
+        L.moe_rope.argtypes = [p, ctypes.POINTER(moe_rope_table), p, i, i, i, p, ll, i, p, ll, p, ll, i, p, ll, p]
+        L.moe_rope.restype = i
+        L.moe_lora.argtypes = [p, ctypes.POINTER(moe_lora_weights), p, p, ll, i, p, ll, p, ll, i, p]
+        L.moe_lora.restype = i
         _lib = L
     return _lib
 
@@ -450,6 +487,131 @@ def moe_attention(o, cache, batch, q, out, lse=None, sinks=None, window=0, scale
     return _check(lib().moe_attention(o, cache, batch, qp, qs, heads, D ** -0.5 if scale is None else scale, window,
                                       None if sinks is None else sinks.data_ptr(), op, None if lse is None else lse.data_ptr(),
                                       _raw_stream(stream, q)))
+
+
+def moe_kv_pool_of(ring, table, block) -> moe_kv_pool:
+    """The pool of free blocks in ring int32 [number of blocks], with the block tables int32 [n_seqs][table_stride]."""
+    import torch
+    _dense(ring, "ring", torch.int32, 1)
+    _dense(table, "table", torch.int32, 2)
+    c = moe_kv_pool(ring.data_ptr(), table.data_ptr(), ring.shape[0], table.shape[0], table.shape[1], block)
+    c.tensors = (ring, table)
+    return c
+
+
+def moe_kv_plan(o, pool, n_new, kv_len, state, cu, kv_len_out, state_out, admitted=None, seq=None, position=None, slot=None,
+                n_tokens=None, stream=None):
+    """n_new, kv_len, kv_len_out int32 [n_seqs], state, state_out int32 [2], cu int32 [n_seqs + 1], admitted int32 [1], seq and
+    position int32 and slot int64 [n_tokens]; n_tokens (their length) has to be given where all three are None."""
+    import torch
+    i, n = torch.int32, pool.n_seqs
+    for t in (seq, position, slot):
+        if t is not None and n_tokens is None:
+            n_tokens = t.shape[0]
+    if n_tokens is None:
+        raise ValueError("moe_kv_plan: n_tokens is needed where seq, position and slot are None")
+
+    def at(t, name, dtype, size, optional=False):
+        if t is None and optional:
+            return None
+        if t.shape != (size,) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"moe_kv_plan: {name} must be a contiguous CUDA tensor of {dtype} [{size}] (got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device})")
+        return t.data_ptr()
+    return _check(lib().moe_kv_plan(o, pool, at(n_new, "n_new", i, n), at(kv_len, "kv_len", i, n), at(state, "state", i, 2), n_tokens,
+                                    at(cu, "cu", i, n + 1), at(kv_len_out, "kv_len_out", i, n), at(state_out, "state_out", i, 2),
+                                    at(admitted, "admitted", i, 1, True), at(seq, "seq", i, n_tokens, True),
+                                    at(position, "position", i, n_tokens, True), at(slot, "slot", torch.int64, n_tokens, True),
+                                    _raw_stream(stream, n_new)))
+
+
+def moe_rope_turns(rot_dim, base, scaling=MOE_ROPE_PLAIN, factor=1.0, length=0.0, low=0.0, high=0.0):
+    """Each pair's turns a position, as 64-bit fractions: a numpy array of uint64 [rot_dim / 2]."""
+    import numpy as np
+    out = np.empty(max(int(rot_dim) // 2, 1), np.uint64)
+    c = moe_rope_config(rot_dim, scaling, base, factor, length, low, high)
+    _check(lib().moe_rope_turns(ctypes.byref(c), out.ctypes.data))
+    return out
+
+
+def moe_rope_of(rot_dim, base, layout=MOE_ROPE_HALF, scaling=MOE_ROPE_PLAIN, factor=1.0, length=0.0, low=0.0, high=0.0, mscale=1.0,
+                device="cuda") -> moe_rope_table:
+    """The table of a configuration, on the device (see include/moe.h)."""
+    import numpy as np
+    import torch
+    t = torch.from_numpy(moe_rope_turns(rot_dim, base, scaling, factor, length, low, high).view(np.int64)).to(device)
+    r = moe_rope_table(t.data_ptr(), rot_dim, layout, mscale)
+    r.tensors = (t,)
+    return r
+
+
+def moe_rope(o, rope, position, q, k=None, q_out=None, k_out=None, stream=None):
+    """q [T][q_heads][head_dim], k [T][k_heads][head_dim] or None, of bf16 or fp32; q_out, k_out like them (None: in place);
+    position int32 [T].  Rows may be strided, heads are contiguous."""
+    import torch
+    if position.dim() != 1 or position.dtype is not torch.int32 or not position.is_cuda or not position.is_contiguous():
+        raise ValueError(f"moe_rope: position must be a contiguous CUDA int32 tensor [T] (got {position.dtype} "
+                         f"{tuple(position.shape)} on {position.device})")
+    T, kind = position.shape[0], q.dtype
+    if kind is not torch.bfloat16 and kind is not torch.float32:
+        raise ValueError(f"moe_rope: q must be bf16 or fp32 (got {kind})")
+
+    def rows(t, name, like=None):
+        st = t.stride()
+        if (t.dim() != 3 or t.shape[0] != T or t.dtype is not kind or not t.is_cuda or (like is not None and t.shape != like.shape) or
+                t.shape[2] != q.shape[2] or st[2] != 1 or (st[1] != t.shape[2] and t.shape[1] > 1)):
+            raise ValueError(f"moe_rope: {name} must be CUDA rows [{T}][heads][head_dim] of {kind} with contiguous heads (got {t.dtype} "
+                             f"{tuple(t.shape)}, strides {st}, on {t.device})")
+        return t.data_ptr(), st[0] if T > 1 else t.shape[1] * t.shape[2]
+    qp, qs = rows(q, "q")
+    op, os_ = (qp, qs) if q_out is None else rows(q_out, "q_out", q)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("moe_rope: k_out without k")
+        kp, ks, kh, lp, ls = None, 0, 0, None, 0
+    else:
+        kp, ks = rows(k, "k")
+        kh = k.shape[1]
+        lp, ls = (kp, ks) if k_out is None else rows(k_out, "k_out", k)
+    return _check(lib().moe_rope(o, rope, position.data_ptr(), T, q.shape[2], MOE_DT_BF16 if kind is torch.bfloat16 else MOE_DT_F32,
+                                 qp, qs, q.shape[1], op, os_, kp, ks, kh, lp, ls, _raw_stream(stream, q)))
+
+
+def moe_lora_of(a, b, scale=None) -> moe_lora_weights:
+    """Adapters in a bf16 [n_adapters][rank][cols], b bf16 [n_adapters][rows][rank], scale fp32 [n_adapters] or None."""
+    import torch
+    _dense(a, "a", torch.bfloat16, 3)
+    _dense(b, "b", torch.bfloat16, 3)
+    n, rank, cols = a.shape
+    if b.shape[0] != n or b.shape[2] != rank:
+        raise ValueError(f"moe_lora_of: a {tuple(a.shape)} and b {tuple(b.shape)} are not adapters of one rank")
+    if scale is not None and _dense(scale, "scale", torch.float32, 1).shape[0] != n:
+        raise ValueError(f"moe_lora_of: scale {tuple(scale.shape)} is not [{n}]")
+    w = moe_lora_weights(a.data_ptr(), b.data_ptr(), _ptr(scale), n, rank, b.shape[1], cols)
+    w.tensors = (a, b, scale)
+    return w
+
+
+def moe_lora(o, w, index, x, y, out=None, stream=None):
+    """x bf16 [M][cols], y fp32 or bf16 [M][rows] or None (0), out like y (None: y, in place); rows may be strided; index int32
+    [M], -1: no adapter."""
+    import torch
+    out = y if out is None else out
+    M, rows, cols, kind = x.shape[0], w.rows, w.cols, out.dtype
+    if index.shape != (M,) or index.dtype is not torch.int32 or not index.is_cuda or not index.is_contiguous():
+        raise ValueError(f"moe_lora: index must be a contiguous CUDA int32 tensor [{M}] (got {index.dtype} {tuple(index.shape)} on "
+                         f"{index.device})")
+    if x.shape != (M, cols) or x.dtype is not torch.bfloat16 or not x.is_cuda or x.stride(1) != 1:
+        raise ValueError(f"moe_lora: x must be CUDA bf16 rows [M][{cols}] (got {x.dtype} {tuple(x.shape)}, strides {x.stride()})")
+    for t, name in ((y, "y"), (out, "out")):
+        if t is not None and (t.shape != (M, rows) or t.dtype is not kind or kind not in (torch.bfloat16, torch.float32) or not t.is_cuda or
+                              (t.stride(1) != 1 and rows > 1)):
+            raise ValueError(f"moe_lora: {name} must be CUDA fp32 or bf16 rows [{M}][{rows}], y and out of one type (got {t.dtype} "
+                             f"{tuple(t.shape)}, strides {t.stride()})")
+    row = lambda t, n: t.stride(0) if M > 1 else n         # noqa: E731
+    return _check(lib().moe_lora(o, w, index.data_ptr(), x.data_ptr(), row(x, cols), M, None if y is None else y.data_ptr(),
+                                 0 if y is None else row(y, rows), out.data_ptr(), row(out, rows),
+                                 MOE_DT_BF16 if kind is torch.bfloat16 else MOE_DT_F32, _raw_stream(stream, x)))
 
 
 def moe_linear_of(codes, scales, bias, format, group) -> moe_linear_weights:

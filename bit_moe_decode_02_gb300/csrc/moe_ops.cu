@@ -68,6 +68,43 @@ int check_rows(const char* who, const char* name, const void* p, long long strid
     return MOE_OK;
 }
 
+size_t workspace_bytes(int num_sms)
+{
+    const size_t a = moe::attention_workspace_bytes(num_sms), l = moe::kCounterBytes + moe::lora_workspace_bytes();
+    return a > l ? a : l;
+}
+
+// As check_rows, for rows of `size`-byte elements.
+int check_rows_of(const char* who, const char* name, const void* p, long long stride, long long width, int size)
+{
+    if (!p)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: %s must not be NULL", who, name);
+    if (!aligned(p, 16) || stride % (16 / size))
+        return set_error(MOE_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned with a stride of a multiple of 16 bytes", who, name);
+    if (stride < width)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: the stride of %s (%lld) is less than a row (%lld)", who, name, stride, width);
+    return MOE_OK;
+}
+
+// Rows of a tensor: `n` of them, `width` elements each, `stride` elements apart.
+struct Rows {
+    const void* p;
+    long long stride, width;
+};
+// Whether two tensors' rows share a byte.  Rows that lie within one another's
+// strides (parts of a fused projection) do not where their columns do not.
+bool rows_overlap(const Rows& a, const Rows& b, int n, int size)
+{
+    if (!overlap(a.p, ((n - 1) * a.stride + a.width) * size, b.p, ((n - 1) * b.stride + b.width) * size))
+        return false;
+    if (n == 1 || a.stride != b.stride)
+        return true;
+    const long long pitch = a.stride * size;
+    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % pitch;
+    d += d < 0 ? pitch : 0;
+    return !(d >= a.width * size && pitch - d >= b.width * size);
+}
+
 }  // namespace
 
 int moe_ops_create(moe_ops** out)
@@ -84,13 +121,13 @@ int moe_ops_create(moe_ops** out)
         delete o;
         return cuda_fail(e, "moe_ops_create");
     }
-    o->ws_bytes = moe::attention_workspace_bytes(o->num_sms);
+    o->ws_bytes = workspace_bytes(o->num_sms);
     if ((e = cudaMalloc(&o->status, sizeof(int))) != cudaSuccess || (e = cudaMalloc(&o->ws, o->ws_bytes)) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(o->status);
         const int sms = o->num_sms;
         delete o;
-        return set_error(MOE_ERR_OOM, "moe_ops_create: workspace (%zu bytes) failed: %s", moe::attention_workspace_bytes(sms),
+        return set_error(MOE_ERR_OOM, "moe_ops_create: workspace (%zu bytes) failed: %s", workspace_bytes(sms),
                          cudaGetErrorString(e));
     }
     if ((e = cudaMemset(o->status, 0, sizeof(int))) != cudaSuccess || (e = cudaMemset(o->ws, 0, o->ws_bytes)) != cudaSuccess ||
@@ -130,7 +167,7 @@ int moe_ops_get_status(moe_ops* o, void* stream)
         (e = cudaMemsetAsync(o->ws, 0, moe::kCounterBytes, s)) != cudaSuccess ||
         (e = cudaStreamSynchronize(s)) != cudaSuccess)
         return cuda_fail(e, "moe_ops_get_status");
-    return set_error(st, st == MOE_ERR_DEVICE_FAULT ? "a batch's lengths or a block number were out of range"
+    return set_error(st, st == MOE_ERR_DEVICE_FAULT ? "a batch's lengths, a block or an adapter number were out of range"
                                                     : "a device-side wait gave up");
 }
 
@@ -264,4 +301,170 @@ int moe_sample(moe_ops* o, const void* logits, int logits_type, long long stride
     moe::SampleArgs a{logits, logits_type, stride, M, V, *p, token, logprob};
     const cudaError_t e = moe::launch_sample(a, o->num_sms, (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_sample");
+}
+
+int moe_rope_turns(const moe_rope_config* c, unsigned long long* turns)
+{
+    if (!c || !turns)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: the configuration and turns must not be NULL");
+    if (c->rot_dim < 2 || c->rot_dim > 512 || c->rot_dim % 2)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: rot_dim=%d must be even, 2..512", c->rot_dim);
+    if (c->scaling < MOE_ROPE_PLAIN || c->scaling > MOE_ROPE_WAVELENGTH)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: unknown scaling %d", c->scaling);
+    if (!(c->base > 1.0) || !std::isfinite(c->base))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: base must be finite and above 1");
+    if (c->scaling != MOE_ROPE_PLAIN && (!(c->factor > 0.0) || !std::isfinite(c->factor)))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: factor must be finite and positive");
+    if (c->scaling > MOE_ROPE_LINEAR && (!(c->length > 0.0) || !(c->low > 0.0) || !(c->high > c->low) || !std::isfinite(c->length) ||
+                                         !std::isfinite(c->high)))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: length and low must be positive and high above low, all finite");
+    const double pi = 3.14159265358979323846;
+    for (int i = 0; i < c->rot_dim / 2; ++i) {
+        double f = std::pow(c->base, -2.0 * i / c->rot_dim);
+        const double slow = f / c->factor;
+        if (c->scaling == MOE_ROPE_LINEAR) {
+            f = slow;
+        } else if (c->scaling == MOE_ROPE_PARTS) {
+            auto at = [&](double n) { return c->rot_dim * std::log(c->length / (2.0 * pi * n)) / (2.0 * std::log(c->base)); };
+            const double lo = std::fmax(at(c->high), 0.0), hi = std::fmin(at(c->low), c->rot_dim / 2 - 1.0);
+            const double x = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            f = f * (1.0 - x) + slow * x;
+        } else if (c->scaling == MOE_ROPE_WAVELENGTH) {
+            const double x = std::fmin(std::fmax((c->length * f / (2.0 * pi) - c->low) / (c->high - c->low), 0.0), 1.0);
+            f = f * x + slow * (1.0 - x);
+        }
+        // f / 2 pi in two doubles, its fraction times 2^64
+        const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;      // 1 / 2 pi
+        const double p = f * hi, rest = std::fma(f, hi, -p) + f * lo, frac = p - std::floor(p);
+        const unsigned long long whole = (unsigned long long)std::ldexp(frac, 64);
+        turns[i] = whole + (unsigned long long)std::llrint(std::ldexp(rest, 64));
+    }
+    return MOE_OK;
+}
+
+int moe_rope(moe_ops* o, const moe_rope_table* r, const int* position, int n_tokens, int head_dim, int type, const void* q,
+             long long q_stride, int q_heads, void* q_out, long long q_out_stride, const void* k, long long k_stride, int k_heads,
+             void* k_out, long long k_out_stride, void* stream)
+{
+    if (!o || !r || !r->turns || !position)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: the handle, the table and position must not be NULL");
+    if (type != MOE_DT_F32 && type != MOE_DT_BF16)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: unknown type %d", type);
+    if (r->layout != MOE_ROPE_HALF && r->layout != MOE_ROPE_INTERLEAVED)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: unknown layout %d", r->layout);
+    if (head_dim < 8 || head_dim > 512 || head_dim % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: head_dim=%d must be a multiple of 8, at most 512", head_dim);
+    if (r->rot_dim < 2 || r->rot_dim > head_dim || r->rot_dim % 2)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: rot_dim=%d must be even, 2..head_dim", r->rot_dim);
+    if (!std::isfinite(r->mscale))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: mscale must be finite");
+    if (n_tokens < 1 || n_tokens > moe::kMaxBatchQ)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: n_tokens=%d out of range 1..%d", n_tokens, moe::kMaxBatchQ);
+    if (q_heads < 1 || q_heads > 1024 || k_heads < 0 || k_heads > 1024)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: q_heads=%d out of range 1..1024 or k_heads=%d out of range 0..1024", q_heads, k_heads);
+    if (!aligned(r->turns, 8) || !aligned(position, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: turns must be 8-byte and position 4-byte aligned");
+    const int size = type == MOE_DT_BF16 ? 2 : 4;
+    const Rows in[2] = {{q, q_stride, (long long)q_heads * head_dim}, {k, k_stride, (long long)k_heads * head_dim}};
+    const Rows out[2] = {{q_out, q_out_stride, in[0].width}, {k_out, k_out_stride, in[1].width}};
+    const char* const names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
+    const int n = k_heads ? 2 : 1;
+    for (int i = 0; i < n; ++i) {
+        int rc = check_rows_of("moe_rope", names[i][0], in[i].p, in[i].stride, in[i].width, size);
+        if (rc == MOE_OK)
+            rc = check_rows_of("moe_rope", names[i][1], out[i].p, out[i].stride, out[i].width, size);
+        if (rc != MOE_OK)
+            return rc;
+    }
+    bool same[2] = {false, false};
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j) {
+            const bool here = i == j && out[i].p == in[i].p && (n_tokens == 1 || out[i].stride == in[i].stride);
+            same[i] |= here;
+            if (!here && rows_overlap(out[i], in[j], n_tokens, size))
+                return set_error(MOE_ERR_INVALID_ARG, "moe_rope: %s overlaps %s (in place: the same rows)", names[i][1], names[j][0]);
+        }
+    if (n == 2 && rows_overlap(out[0], out[1], n_tokens, size))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope: q_out overlaps k_out");
+    moe::RopeArgs a{r->turns, position, q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, n_tokens, q_heads,
+                    k_heads, head_dim, r->rot_dim, r->layout, type, r->mscale, !(same[0] && (n == 1 || same[1])), 0, 0};
+    const cudaError_t e = moe::launch_rope(a, o->num_sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_rope");
+}
+
+int moe_kv_plan(moe_ops* o, const moe_kv_pool* p, const int* n_new, const int* kv_len, const int* state, int n_tokens, int* cu,
+                int* kv_len_out, int* state_out, int* admitted, int* seq, int* position, long long* slot, void* stream)
+{
+    if (!o || !p || !p->ring || !p->table || !n_new || !kv_len || !state || !cu || !kv_len_out || !state_out)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: only admitted, seq, position and slot may be NULL");
+    if (p->n_seqs < 1 || p->n_seqs > moe::kMaxSeqs)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: n_seqs=%d out of range 1..%d", p->n_seqs, moe::kMaxSeqs);
+    if (p->ring_size < 1)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: ring_size=%d must be positive", p->ring_size);
+    if (p->table_stride < 1)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: table_stride=%d must be positive", p->table_stride);
+    if (p->block != 32 && p->block != 64 && p->block != 128)
+        return set_error(MOE_ERR_UNSUPPORTED, "moe_kv_plan: block=%d (32, 64 or 128)", p->block);
+    if (n_tokens < 1 || n_tokens > moe::kMaxBatchQ)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: n_tokens=%d out of range 1..%d", n_tokens, moe::kMaxBatchQ);
+    const long long n = p->n_seqs;
+    // what is read, then what is written; kv_len and state may be updated in place
+    const struct { const void* p; long long bytes; const char* name; } t[] = {
+        {n_new, n * 4, "n_new"}, {kv_len, n * 4, "kv_len"}, {state, 8, "state"}, {p->ring, p->ring_size * 4ll, "ring"},
+        {p->table, n * p->table_stride * 4, "table"}, {cu, (n + 1) * 4, "cu"}, {kv_len_out, n * 4, "kv_len_out"},
+        {state_out, 8, "state_out"}, {admitted, 4, "admitted"}, {seq, n_tokens * 4ll, "seq"}, {position, n_tokens * 4ll, "position"},
+        {slot, n_tokens * 8ll, "slot"}};
+    constexpr int N = sizeof t / sizeof *t;
+    for (int i = 0; i < N; ++i) {
+        if (!aligned(t[i].p, t[i].p == slot ? 8 : 4))
+            return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: every array must be aligned to its type (%s is not)", t[i].name);
+        for (int j = i > 3 ? i : 3; j < N; ++j)
+            if (i != j && t[i].p && t[j].p && !(i == 1 && j == 6 && t[i].p == t[j].p) && !(i == 2 && j == 7 && t[i].p == t[j].p) &&
+                overlap(t[i].p, t[i].bytes, t[j].p, t[j].bytes))
+                return set_error(MOE_ERR_INVALID_ARG, "moe_kv_plan: %s overlaps %s", t[j].name, t[i].name);
+    }
+    moe::PlanArgs a{p->ring, p->table, p->ring_size, p->n_seqs, p->table_stride, p->block, n_new, kv_len, state, cu, kv_len_out,
+                    state_out, admitted, seq, position, slot, n_tokens, o->status};
+    const cudaError_t e = moe::launch_plan(a, o->num_sms, reinterpret_cast<unsigned*>(o->ws), (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_kv_plan");
+}
+
+int moe_lora(moe_ops* o, const moe_lora_weights* w, const int* index, const void* x_bf16, long long x_stride, int M, const void* y,
+             long long y_stride, void* out, long long out_stride, int type, void* stream)
+{
+    if (!o || !w || !index)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: the handle, the weights and index must not be NULL");
+    if (w->n_adapters < 1 || w->n_adapters > 65536)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: n_adapters=%d out of range 1..65536", w->n_adapters);
+    if (w->rank < 8 || w->rank > 128 || w->rank % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: rank=%d must be a multiple of 8, at most 128", w->rank);
+    if (w->rows < 1 || w->rows > 1 << 24)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: rows=%d out of range 1..2^24", w->rows);
+    if (w->cols < 8 || w->cols > 32768 || w->cols % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: cols=%d must be a multiple of 8, at most 32768", w->cols);
+    if (!w->a || !w->b || !aligned(w->a, 16) || !aligned(w->b, 16) || !aligned(w->scale, 4) || !aligned(index, 4))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: a and b must be 16-byte aligned (and not NULL), scale and index 4-byte");
+    if (M < 1 || M > 64)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: M=%d out of range 1..64", M);
+    const int rc = check_rows("moe_lora", "x", x_bf16, x_stride, w->cols);
+    if (rc != MOE_OK)
+        return rc;
+    if (type != MOE_DT_F32 && type != MOE_DT_BF16)
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: unknown type %d", type);
+    const int size = type == MOE_DT_BF16 ? 2 : 4;
+    if (!out || !aligned(out, size) || !aligned(y, size))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: out (not NULL) and y must be aligned to their type");
+    if (out_stride < w->rows || (y && y_stride < w->rows))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: the stride of out (%lld) or y (%lld) is less than a row (%d)", out_stride,
+                         y_stride, w->rows);
+    if (overlap(x_bf16, ((M - 1) * x_stride + w->cols) * 2, out, ((M - 1) * out_stride + w->rows) * size))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: x overlaps out");
+    const bool same = y == out && (M == 1 || y_stride == out_stride);
+    if (y && !same && rows_overlap(Rows{y, y_stride, w->rows}, Rows{out, out_stride, w->rows}, M, size))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_lora: y overlaps out (in place: the same rows)");
+    moe::LoraArgs a{static_cast<const uint16_t*>(w->a), static_cast<const uint16_t*>(w->b), w->scale, index, w->n_adapters, w->rank,
+                    w->rows, w->cols, M, type, static_cast<const uint16_t*>(x_bf16), y, out, x_stride, y_stride, out_stride,
+                    reinterpret_cast<float*>(o->ws + moe::kCounterBytes), o->status, 0};
+    const cudaError_t e = moe::launch_lora(a, o->num_sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_lora");
 }

@@ -86,6 +86,47 @@ struct SampleArgs {
 cudaError_t prepare_sample_kernels();
 cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t s);
 
+struct RopeArgs {
+    const unsigned long long* turns;   // [rot / 2]
+    const int* position;               // [T]
+    const void *q, *k;                 // [T] rows of heads * D, strides apart
+    void *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+    int n_tokens, q_heads, k_heads, D, rot, layout, type;
+    float mscale;
+    bool copy_rest;                    // what is not turned goes from one tensor to another
+    int per_cta, heads_per_cta;        // of the launch
+};
+cudaError_t launch_rope(RopeArgs a, int num_sms, cudaStream_t s);
+
+struct PlanArgs {
+    int *ring, *table;
+    int ring_size, n_seqs, table_stride, block;
+    const int *n_new, *kv_len, *state;
+    int *cu, *kv_len_out, *state_out;
+    int *admitted, *seq, *position;    // or nullptr
+    long long* slot;                   // or nullptr
+    int n_tokens;
+    int* status;
+};
+cudaError_t launch_plan(const PlanArgs& a, int num_sms, unsigned* cnt, cudaStream_t s);
+
+struct LoraArgs {
+    const uint16_t *a, *b;             // [n_adapters][rank][cols], [n_adapters][rows][rank]
+    const float* scale;                // [n_adapters] or nullptr
+    const int* index;                  // [M]
+    int n_adapters, rank, rows, cols, M, type;
+    const uint16_t* x;
+    const void* y;                     // or nullptr
+    void* out;
+    long long x_stride, y_stride, out_stride;
+    float* h;                          // workspace
+    int* status;
+    int ctas;                          // of the launches, at most
+};
+cudaError_t launch_lora(LoraArgs a, int num_sms, cudaStream_t s);
+size_t lora_workspace_bytes();
+
 size_t attention_workspace_bytes(int num_sms);
 
 }  // namespace moe

@@ -427,7 +427,7 @@ void moe_destroy(moe_handle* h);
  * (status codes, checks before anything is enqueued, streams, one thread and
  * one stream at a time per handle, nothing allocated by a call, no host work
  * that depends on device values) hold for it too.  Each call is one launch
- * (moe_linear: one for each pass of up to 16 tokens) and can be captured in a CUDA
+ * (moe_linear: one for each pass of up to 16 tokens; moe_lora: two) and can be captured in a CUDA
  * graph.  What a device-side check finds (metadata that does not describe the
  * batch, a block number outside the cache) sets MOE_ERR_DEVICE_FAULT in the
  * handle's status word and skips that sequence or block.
@@ -530,7 +530,91 @@ int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* bat
                   long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,
                   float* lse, void* stream);
 
+/* A step's batch, made on the GPU from the requests' lengths: block tables, and for
+ * each token its sequence, position and slot.
+ *
+ * Free blocks lie in a ring: entries state[0], state[0] + 1, ... (modulo ring_size) of
+ * `ring`, state[1] of them.  ring_size is the number of the cache's blocks, so that
+ * the ring holds them all. */
+typedef struct {
+    int* ring;                    /* [ring_size] */
+    int* table;                   /* [n_seqs][table_stride]: the sequences' blocks, as in moe_kv_batch */
+    int ring_size, n_seqs, table_stride, block;
+} moe_kv_pool;
+
+/* For each sequence b, n_new[b] tokens are to be added to the kv_len[b] that it has
+ * (-1: it has ended, and its blocks go back to the ring).  All arrays are the caller's
+ * device memory.
+ *   - Sequences are served in order.  The first whose tokens pass n_tokens, or whose new
+ *     blocks pass the free ones, and every one after it, get no tokens in this step;
+ *     admitted[0] is the number of those before it (n_seqs: all).
+ *   - The blocks that sequence b comes to need, ceil((kv_len + n) / block) less those
+ *     that it has, are taken from the ring's front, in order, and entered in its row of
+ *     the table; its other entries stay as they are.
+ *   - Blocks of ended sequences, admitted or not, go to the ring's end, in order (and
+ *     are free from the next call on); their rows of the table stay as they are.
+ *   - cu [n_seqs + 1] and kv_len_out [n_seqs] are what a moe_kv_batch takes: the served
+ *     tokens' prefix sums, and the lengths with them (0 for an ended sequence).
+ *   - state_out [2]: the ring's state after it.
+ *   - For token t < cu[n_seqs]: seq[t], position[t] (of its sequence) and slot[t] = its
+ *     block * `block` + its place in it; all three are -1 from cu[n_seqs] to n_tokens - 1.
+ * admitted, seq, position and slot may be NULL.  kv_len_out may be kv_len and state_out
+ * may be state (updated in place); else a call with the same inputs gives the same
+ * outputs, whatever an earlier one did.  No other arrays may overlap (checked).
+ * A sequence whose length is negative, or whose tokens do not fit its row of the table,
+ * gets none and keeps its length; a state outside the ring serves no one; where more
+ * blocks come back than the ring has room for none does, and ended sequences keep their
+ * lengths: each sets MOE_ERR_DEVICE_FAULT.  So does a block number outside 0 ..
+ * ring_size - 1; it is passed on as it is, and its tokens' slots are -1.
+ * n_seqs 1..1024, n_tokens 1..2^20, block as in moe_kv_cache. */
+int moe_kv_plan(moe_ops* o, const moe_kv_pool* pool, const int* n_new, const int* kv_len, const int* state,
+                int n_tokens, int* cu, int* kv_len_out, int* state_out, int* admitted, int* seq, int* position,
+                long long* slot, void* stream);
+
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
+
+/* Rotary positions.  Of each head's head_dim values the first rot_dim turn, in pairs:
+ * (u, v) becomes mscale (u cos t - v sin t, v cos t + u sin t), t = position * f_i for
+ * pair i; the others stay.  Pair i is (i, i + rot_dim / 2) or (2 i, 2 i + 1). */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
+
+/* f_i = base^(-2 i / rot_dim), and for longer contexts than a model was trained on:
+ *   LINEAR      f_i / factor;
+ *   PARTS       f_i (1 - x) + f_i / factor * x, x = (i - a) / max(b - a, 0.001) held to
+ *               0..1, a = max(at(high), 0), b = min(at(low), rot_dim / 2 - 1),
+ *               at(n) = rot_dim log(length / (2 pi n)) / (2 log base): pairs that turn
+ *               more than `high` times within `length` positions keep their speed, those
+ *               that turn less than `low` times are slowed down;
+ *   WAVELENGTH  f_i x + f_i / factor (1 - x), x = (length f_i / (2 pi) - low) /
+ *               (high - low) held to 0..1. */
+typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_PARTS = 2, MOE_ROPE_WAVELENGTH = 3 } moe_rope_scaling;
+typedef struct {
+    int rot_dim, scaling;
+    double base, factor, length, low, high;
+} moe_rope_config;
+
+/* The table of a configuration: turns[i] = f_i / (2 pi), modulo 1, times 2^64, for
+ * rot_dim / 2 pairs, in host memory (no GPU is needed); copy it to the device once. */
+int moe_rope_turns(const moe_rope_config* c, unsigned long long* turns);
+
+typedef struct {
+    const unsigned long long* turns;    /* [rot_dim / 2], device */
+    int rot_dim, layout;
+    float mscale;
+} moe_rope_table;
+
+/* Turn queries [n_tokens][q_heads][head_dim] and keys [n_tokens][k_heads][head_dim] (k_heads
+ * 0: none) by their positions, int32 [n_tokens]; a negative one leaves the row's output as
+ * it is.  All of one type (moe_dtype), rows strides elements apart, 16-byte aligned, the
+ * strides multiples of 16 bytes; the rows may be parts of a fused projection.  q_out may be
+ * q and k_out k (the same rows, in place); else outputs must not overlap anything (checked).
+ * position * f_i / (2 pi) is kept modulo 1 in 64 bits, so an angle is off by no more than
+ * position * 2^-55 turns beside fp32 rounding of what is left; cosine, sine and products
+ * are fp32, the result is rounded once.  head_dim a multiple of 8, 8..512; rot_dim even,
+ * 2..head_dim; n_tokens 1..2^20. */
+int moe_rope(moe_ops* o, const moe_rope_table* r, const int* position, int n_tokens, int head_dim, int type,
+             const void* q, long long q_stride, int q_heads, void* q_out, long long q_out_stride, const void* k,
+             long long k_stride, int k_heads, void* k_out, long long k_out_stride, void* stream);
 
 /* A matrix of 4-bit weights W [rows][cols], format and group as in moe_config:
  *   codes  u8 [rows][cols/2]; scales u8 [rows][cols/32] (MXFP4) or fp16
@@ -557,6 +641,31 @@ typedef struct {
  * out must not overlap. */
 int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long long x_stride, int M, void* out,
                long long out_stride, int out_type, void* stream);
+
+/* Low-rank adapters beside a shared projection, one for each token:
+ *   a bf16 [n_adapters][rank][cols], b bf16 [n_adapters][rows][rank], 16-byte aligned;
+ *   scale fp32 [n_adapters] or NULL (1).
+ * rank a multiple of 8, 8..128 (pad with zeros); cols a multiple of 8, at most 32768;
+ * rows 1..2^24; n_adapters 1..65536. */
+typedef struct {
+    const void* a;
+    const void* b;
+    const float* scale;
+    int n_adapters, rank, rows, cols;
+} moe_lora_weights;
+
+/* out[m] = y[m] + scale[i] * b[i] (a[i] x[m]), i = index[m], for M = 1..64 tokens: index
+ * int32 [M], -1 (or less): no adapter, out[m] = y[m]; one that is not below n_adapters sets
+ * MOE_ERR_DEVICE_FAULT and counts as -1.  x bf16 [M][cols], rows x_stride elements apart
+ * (16-byte aligned, a multiple of 8); y and out fp32 or bf16 [M][rows], rows y_stride and
+ * out_stride elements apart; y may be NULL (0), or out (what moe_linear left there); else
+ * they must not overlap, nor x and out (checked).  An adapter's weights are read once for
+ * every eight tokens that share it.  a x is kept in fp32, sums are fp32, the result is rounded
+ * once; a token's result does not depend on the others, but for the order of its sums.  A
+ * token with an infinity or NaN in x, or whose a x overflows, has no finite result.  Two
+ * launches. */
+int moe_lora(moe_ops* o, const moe_lora_weights* w, const int* index, const void* x_bf16, long long x_stride, int M,
+             const void* y, long long y_stride, void* out, long long out_stride, int type, void* stream);
 
 /* Per-row device arrays [M]; every one but u may be NULL. */
 typedef struct {
