@@ -41,6 +41,7 @@ MOE_BATCHED_MXFP4 = 0
 MOE_BATCHED_BF16 = 1
 MOE_KV_E4M3 = 1
 MOE_KV_INT8 = 2
+MOE_KV_MXFP4 = 4
 MOE_DT_F32 = 0
 MOE_DT_BF16 = 1
 MOE_ROPE_HALF = 0
@@ -409,15 +410,20 @@ def moe_ops_destroy(o) -> None:
 
 def moe_kv_cache_of(codes, scales, block, head_dim, format) -> moe_kv_cache:
     """The cache in codes uint8 [num_blocks][kv_heads][2][block * head_dim] and scales fp32
-    [num_blocks][kv_heads][2]."""
+    [num_blocks][kv_heads][2]; MOE_KV_MXFP4: codes [num_blocks][kv_heads][2][block * head_dim * 17 / 32], scales None."""
     import torch
+    mx = format == MOE_KV_MXFP4
     _dense(codes, "codes", torch.uint8, 4)
-    _dense(scales, "scales", torch.float32, 3)
     nb, heads = codes.shape[:2]
-    if tuple(codes.shape[2:]) != (2, block * head_dim) or tuple(scales.shape) != (nb, heads, 2):
-        raise ValueError(f"moe_kv_cache_of: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not a cache of "
-                         f"blocks of {block} tokens with head_dim {head_dim}")
-    c = moe_kv_cache(codes.data_ptr(), scales.data_ptr(), nb, heads, head_dim, block, format)
+    if mx:
+        if scales is not None:
+            raise ValueError("moe_kv_cache_of: an MXFP4 cache holds its scales with its codes: scales must be None")
+    elif tuple(_dense(scales, "scales", torch.float32, 3).shape) != (nb, heads, 2):
+        raise ValueError(f"moe_kv_cache_of: scales {tuple(scales.shape)} are not [{nb}][{heads}][2]")
+    if tuple(codes.shape[2:]) != (2, block * head_dim * 17 // 32 if mx else block * head_dim):
+        raise ValueError(f"moe_kv_cache_of: codes {tuple(codes.shape)} are not a cache of blocks of {block} tokens with head_dim "
+                         f"{head_dim}")
+    c = moe_kv_cache(codes.data_ptr(), None if mx else scales.data_ptr(), nb, heads, head_dim, block, format)
     c.tensors = (codes, scales)
     return c
 

@@ -38,6 +38,7 @@
 #include <cstdint>
 
 #include "attn_device.cuh"
+#include "kv4_device.cuh"
 
 namespace moe {
 namespace {
@@ -216,9 +217,15 @@ template <int D, int FMT, int BLK>
 struct Decode {
     static constexpr int GW = BLK / kSub;            // warps of a group
     static constexpr int NG = kWarps / GW;           // groups of a CTA
-    static constexpr int STAGE = 2 * BLK * D;        // bytes of a tile
-    static constexpr int NS = D == 64 ? 6 : 3;       // stages of a group's ring: 192 KB per CTA in all
-    static constexpr int OFF_HDR = NG * NS * STAGE;                    // per stage: two scales, valid
+    static constexpr bool MX = FMT == MOE_KV_MXFP4;
+    static constexpr int RECORD = MX ? kv4::record(BLK, D) : BLK * D;  // bytes of K or V of a block
+    static constexpr int STAGE = 2 * RECORD;         // bytes of a tile
+    // stages of a group's ring: 192 KB per CTA in all; MXFP4: 157 or 139 KB, and the warps' O
+    // of a finished run beside it (in 8 bits they go into the stage read last)
+    static constexpr int NS = MX ? (D == 64 ? 9 : 4) : D == 64 ? 6 : 3;
+    static constexpr int OFF_O = NG * NS * STAGE;                      // [kWarps][kRows][D] fp32
+    static constexpr int OFF_VS = OFF_O + (MX ? kWarps * kRows * D * 4 : 0);   // [kWarps][D / 32][kSub] f16
+    static constexpr int OFF_HDR = OFF_VS + (MX ? kWarps * D * 2 : 0); // per stage: two scales, valid
     static constexpr int OFF_BAR = OFF_HDR + NG * NS * 16;
     static constexpr int OFF_ML = OFF_BAR + NG * NS * 16;              // full and empty barriers
     static constexpr int OFF_PIECE = OFF_ML + kWarps * kRows * 8;
@@ -226,6 +233,239 @@ struct Decode {
     static constexpr int WHOLE = 2 * NG;             // items of at most so many tiles are not split over CTAs
     static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 4; }
 };
+
+// max and sum of each half, unsigned
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+{
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One warp's 32 tokens of a block in 4 bits: scores, running maximum, P V.
+//  - K.  A key's codes become f16 times 2^(13 + e_g - e), e_g a group's exponent and e the
+//    key's largest: exact down to 2^-27, and no key's size touches another's.  Its score
+//    is then multiplied by 2^e.
+//  - V.  A group's scale goes into P, 2^(e - unit), unit the exponent that the 32 columns
+//    of O are kept in.  Scales within [unit - 7, unit + 1] go as they are; where one is
+//    not, the unit moves to the largest, and what is more than 2^7 below goes in passes of
+//    its own, each with a unit of its own.
+template <int D, int BLK>
+__device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* scratch, const uint32_t (&qf)[D / 16][4], const float (&f)[2],
+                                        float (&o)[D / 8][4], float (&m)[2], float (&l)[2], int& unit, int& vmax, int p0, const int (&plo)[2],
+                                        const int (&phi)[2], bool whole, int any_lo, int any_hi)
+{
+    constexpr int REC = kv4::record(BLK, D), G = D / 32, W = D / 32;       // W: words of a thread's codes of a key
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const uint8_t* kt = stage + sub * (kSub * D / 2);
+    const uint8_t* ks = stage + BLK * D / 2 + sub * D;
+    const uint8_t* vt = stage + REC + sub * (kSub * D / 2);
+    const uint8_t* vs = stage + REC + BLK * D / 2 + sub * D;
+
+    // this thread's four keys' scales (key of score tile i: 8 (r / 2) + 2 i + r % 2), two and two
+    const uint32_t kb = *reinterpret_cast<const uint32_t*>(ks + (r * G + (D == 128 ? c : c >> 1)) * 4);
+    uint32_t e2[2] = {kb & 0x00ff00ffu, kb >> 8 & 0x00ff00ffu}, top[2], col[2][2];
+    uint32_t ksc[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        top[h] = e2[h];
+        if (D == 128)
+            top[h] = max2(top[h], __shfl_xor_sync(~0u, top[h], 1));
+        top[h] = max2(top[h], __shfl_xor_sync(~0u, top[h], 2));
+        // f16 2^(13 + e_g - e): exponent field 28 - (e - e_g), 0 where that is 28 or more
+        const uint32_t x = (0x001c001cu - min2(top[h] - e2[h], 0x001c001cu)) << 10;
+        ksc[h] = __byte_perm(x, 0, 0x1010);
+        ksc[h + 2] = __byte_perm(x, 0, 0x3232);
+        // the exponents of the keys whose scores this thread holds: 8 c + 2 i + j
+        col[h][0] = __shfl_sync(~0u, top[h], 8 * c);
+        col[h][1] = __shfl_sync(~0u, top[h], 8 * c + 4);
+    }
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+    {
+        const uint8_t* kp = kt + (8 * (r >> 1) + (r & 1)) * (D / 2) + (D / 8) * c;
+        uint32_t w[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(kp + i * D);
+                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(kp + i * D);
+                w[i][0] = x.x, w[i][1] = x.y;
+            }
+        }
+#pragma unroll
+        for (int ch = 0; ch < W; ++ch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[4];
+                kv4::to_f16(w[i][ch], h);
+                mma16816(s[i], qf[2 * ch], mul2(h[0], ksc[i]), mul2(h[1], ksc[i]));
+                mma16816(s[i], qf[2 * ch + 1], mul2(h[2], ksc[i]), mul2(h[3], ksc[i]));
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t e = col[i & 1][j];
+            const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
+            s[i][j] *= k * f[0];
+            s[i][2 + j] *= k * f[1];
+        }
+    if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = p0 + 8 * c + 2 * i + (k & 1), e = k >> 1;
+                if (p < plo[e] || p > phi[e])
+                    s[i][k] = -INFINITY;
+            }
+    }
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mx[k >> 1] = fmaxf(mx[k >> 1], s[i][k]);
+    if (__any_sync(~0u, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
+            const float mn = fmaxf(m[e], mx[e]);
+            al[e] = ex2(m[e] - mn);
+            m[e] = mn;
+            l[e] *= al[e];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= al[0];
+            o[i][1] *= al[0];
+            o[i][2] *= al[1];
+            o[i][3] *= al[1];
+        }
+    }
+    uint32_t pf[2][4];
+    {
+        const float mm[2] = {m[0] - kRoom, m[1] - kRoom};
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p[k] = ex2(s[i][k] - mm[k >> 1]);
+                sum[k >> 1] += p[k];
+            }
+            pf[i >> 1][(i & 1) * 2] = pack_f16(p[0], p[1]);
+            pf[i >> 1][(i & 1) * 2 + 1] = pack_f16(p[2], p[3]);
+        }
+        l[0] += sum[0];
+        l[1] += sum[1];
+    }
+
+    // V's scales: four tokens' bytes of one group a lane, those that no row sees left out
+    uint32_t vb = D == 128 || lane < 16 ? *reinterpret_cast<const uint32_t*>(vs + 4 * lane) : 0u;
+    if (!whole) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int p = p0 + 4 * (lane & 7) + k;
+            if (p < any_lo || p > any_hi)
+                vb &= ~(0xffu << 8 * k);
+        }
+    }
+#pragma unroll 1
+    for (;;) {
+        uint32_t x[2] = {__byte_perm(vb, 0, 0x4140), __byte_perm(vb, 0, 0x4342)};
+        uint32_t left = 0;
+        {
+            // each byte but 0 within [unit - 7, unit + 1]?
+            const uint32_t lo = (uint32_t)max(unit - 8, 0) * 0x10001u, hi = (uint32_t)(unit + 1) * 0x10001u;
+            uint32_t below;
+            asm("add.u16x2 %0, %1, %2;" : "=r"(below) : "r"(x[0]), "r"(0xffffffffu));
+            uint32_t y;
+            asm("add.u16x2 %0, %1, %2;" : "=r"(y) : "r"(x[1]), "r"(0xffffffffu));
+            const bool out = min2(min2(below, y), lo) != lo || max2(max2(x[0], x[1]), hi) != hi;
+            const unsigned outs = __ballot_sync(~0u, out);
+            if (outs) {
+                uint32_t big = max2(x[0], x[1]);
+                big = max(big & 0xffffu, big >> 16);
+                big = max(big, __shfl_xor_sync(~0u, big, 1));
+                big = max(big, __shfl_xor_sync(~0u, big, 2));
+                big = max(big, __shfl_xor_sync(~0u, big, 4));
+                vmax = max(vmax, (int)big);
+                const int was = unit;
+                const int least = max(vmax - 80, 16);
+                if ((outs >> (lane & 24) & 0xffu) && big > 0)
+                    unit = max((int)big, least);
+                const float by = ex2((float)max(was - unit, -126));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float ch = __shfl_sync(~0u, by, 8 * g);
+#pragma unroll
+                    for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                        o[i][0] *= ch;
+                        o[i][1] *= ch;
+                        o[i][2] *= ch;
+                        o[i][3] *= ch;
+                    }
+                }
+                // what is further below goes in a later pass, or is nothing beside the largest
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int b = vb >> 8 * k & 0xff;
+                    if (b < unit - 7) {
+                        x[k >> 1] &= ~(0xffffu << 16 * (k & 1));
+                        if (b >= least - 7)
+                            left |= (uint32_t)b << 8 * k;
+                    }
+                }
+            }
+        }
+        // 2^(e - unit) in f16: exponent field e - unit + 15, 0 for no scale
+        const uint32_t base = (uint32_t)max(unit - 15, 0) * 0x10001u;      // unit >= 16, or no scale yet
+        const uint32_t z0 = (max2(x[0], base) - base) << 10, z1 = (max2(x[1], base) - base) << 10;
+        __syncwarp();
+        if (D == 128 || lane < 16)
+            *reinterpret_cast<uint2*>(scratch + 8 * lane) = make_uint2(z0, z1);
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint4 z = *reinterpret_cast<const uint4*>(scratch + g * (kSub * 2) + c * 16);
+            const uint4 w = *reinterpret_cast<const uint4*>(vt + (g * 32 + lane) * 16);
+            const uint32_t pa[4] = {mul2(pf[0][0], z.x), mul2(pf[0][1], z.x), mul2(pf[0][2], z.y), mul2(pf[0][3], z.y)};
+            const uint32_t pb[4] = {mul2(pf[1][0], z.z), mul2(pf[1][1], z.z), mul2(pf[1][2], z.w), mul2(pf[1][3], z.w)};
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t h[4];
+                kv4::to_f16(words[e], h);
+                mma16816(o[4 * g + e], pa, h[0], h[1]);
+                mma16816(o[4 * g + e], pb, h[2], h[3]);
+            }
+        }
+        if (!__any_sync(~0u, left))
+            break;
+        vb = left;
+    }
+}
 
 template <int D, int FMT, int BLK>
 __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
@@ -356,9 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             if (valid) {
                 const i64 at = ((i64)pid * a.c.H + pit.h) * 2;
                 tc::mbar_expect_tx(full + st, C::STAGE);
-                tc::bulk_copy_hint(ring + st * C::STAGE, a.c.codes + at * (BLK * D), C::STAGE, full + st, pol);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::su32(hd)), "l"(a.c.scales + at) : "memory");
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::su32(full + st)) : "memory");
+                tc::bulk_copy_hint(ring + st * C::STAGE, a.c.codes + at * C::RECORD, C::STAGE, full + st, pol);
+                if constexpr (C::MX) {
+                    tc::mbar_arrive(full + st);
+                } else {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::su32(hd)), "l"(a.c.scales + at) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::su32(full + st)) : "memory");
+                }
             } else {
                 atomicExch(status, MOE_ERR_DEVICE_FAULT);
                 tc::mbar_arrive(full + st);
@@ -409,10 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 plo[e] = in && a.window > 0 ? phi[e] - a.window + 1 : 0;
                 uint32_t (&w)[D / 64][8] = qw[e];
                 if (in) {
-                    const uint16_t* q = a.q + (i64)(it.c0 + i) * a.q_stride + (i64)(it.h * a.group + row % a.group) * D + 16 * c;
+                    // which of the d's a thread takes: those of its 16 bytes of K's codes
+                    constexpr int mine = C::MX ? D / 4 : 16, step = C::MX ? 16 : 64;
+                    const uint16_t* q = a.q + (i64)(it.c0 + i) * a.q_stride + (i64)(it.h * a.group + row % a.group) * D + mine * c;
 #pragma unroll
                     for (int ch = 0; ch < D / 64; ++ch) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(q + 64 * ch), y = *reinterpret_cast<const uint4*>(q + 64 * ch + 8);
+                        const uint4 x = *reinterpret_cast<const uint4*>(q + step * ch), y = *reinterpret_cast<const uint4*>(q + step * ch + 8);
                         w[ch][0] = x.x, w[ch][1] = x.y, w[ch][2] = x.z, w[ch][3] = x.w;
                         w[ch][4] = y.x, w[ch][5] = y.y, w[ch][6] = y.z, w[ch][7] = y.w;
                     }
@@ -453,9 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 for (int k = 0; k < 4; ++k)
                     o[i][k] = 0.0f;
             float ref = 0.0f, vmax = 0.0f;
+            // MXFP4: the unit of O's 32 columns of group g, as a scale byte, and the largest byte seen:
+            // in the lanes that look after g's bytes
+            int unit4 = 0, vmax4 = 0;
             // positions that every row of the tile sees
             const int all_lo = a.window > 0 ? it.len - it.n + (it.rt * kRows + rows - 1) / a.group - a.window + 1 : 0;
             const int all_hi = it.len - it.n + it.rt * kRows / a.group;
+            // and that any does
+            const int any_lo = a.window > 0 ? all_hi - a.window + 1 : 0;
+            const int any_hi = it.len - it.n + (it.rt * kRows + rows - 1) / a.group;
 
             int st = 0;
             for (; t < seg_end; ++t, ++j) {
@@ -470,7 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 const uint8_t* kt = ring + st * C::STAGE + sub * kSub * D;
                 const uint8_t* vt = ring + st * C::STAGE + BLK * D + sub * kSub;
                 const int p0 = j * BLK + sub * kSub;     // position of this warp's first token
-                if (hd.z != 0.0f) {
+                if (C::MX && hd.z != 0.0f) {
+                    if constexpr (C::MX)
+                        mx_tile<D, BLK>(ring + st * C::STAGE, sub, reinterpret_cast<uint8_t*>(sm + C::OFF_VS) + warp * (D * 2), qf, f, o, m, l,
+                                        unit4, vmax4, p0, plo, phi, p0 >= all_lo && p0 + kSub - 1 <= all_hi, any_lo, any_hi);
+                } else if (!C::MX && hd.z != 0.0f) {
                     float s[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -593,15 +849,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                     mls[warp * kRows + r + 8 * e] = make_float2(m[e], l[e] * kUnroom);
             }
             group_sync(1 + grp, C::GW * 32);
-            float* od = reinterpret_cast<float*>(ring + st * C::STAGE);
-            const float unit = ref * kUnroom;
+            float* od = reinterpret_cast<float*>(C::MX ? sm + C::OFF_O + grp * C::GW * (kRows * D * 4) : ring + st * C::STAGE);
+            float unit[D / 32];
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g)
+                unit[g] = (C::MX ? kv4::scale_of(__shfl_sync(~0u, unit4, 8 * g)) : ref) * kUnroom;
             // column group i of row x lies at i ^ (x % 8)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * D + (i ^ r) * 8 + 2 * c) =
-                        make_float2(o[i][2 * e] * unit, o[i][2 * e + 1] * unit);
+                        make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
             const Place place{it.c0, it.rt * kRows, it.h, rows};
             if (t == t_end) {
                 // the group's last: finished with the CTA's others
@@ -660,7 +919,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         int ods[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            ods[w] = (w / C::GW * C::NS + __shfl_sync(~0u, stage, w)) * C::STAGE + w % C::GW * (kRows * D * 4);
+            ods[w] = C::MX ? C::OFF_O + w * (kRows * D * 4)
+                           : (w / C::GW * C::NS + __shfl_sync(~0u, stage, w)) * C::STAGE + w % C::GW * (kRows * D * 4);
         const bool done = t0 >= ct0 && t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
@@ -847,14 +1107,17 @@ cudaError_t prepare_attention_kernels()
     if ((e = prepare_blocks<64, MOE_KV_E4M3>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_INT8>()) != cudaSuccess ||
         (e = prepare_blocks<128, MOE_KV_E4M3>()) != cudaSuccess)
         return e;
-    if ((e = prepare_blocks<128, MOE_KV_INT8>()) != cudaSuccess)
+    if ((e = prepare_blocks<128, MOE_KV_INT8>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_MXFP4>()) != cudaSuccess ||
+        (e = prepare_blocks<128, MOE_KV_MXFP4>()) != cudaSuccess)
         return e;
     return prepare_prompt_kernels();
 }
 
 static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
-    if (a.c.D == 64)
+    if (a.c.fmt == MOE_KV_MXFP4)
+        a.c.D == 64 ? launch_blocks<64, MOE_KV_MXFP4>(a, num_sms, s) : launch_blocks<128, MOE_KV_MXFP4>(a, num_sms, s);
+    else if (a.c.D == 64)
         a.c.fmt == MOE_KV_E4M3 ? launch_blocks<64, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<64, MOE_KV_INT8>(a, num_sms, s);
     else
         a.c.fmt == MOE_KV_E4M3 ? launch_blocks<128, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<128, MOE_KV_INT8>(a, num_sms, s);
@@ -875,7 +1138,7 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
     const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
     const long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
-    return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
+    return decode > prompt && a.c.fmt != MOE_KV_MXFP4 ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
 }  // namespace moe

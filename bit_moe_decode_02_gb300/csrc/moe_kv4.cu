@@ -1,0 +1,303 @@
+// moe_kv4.cu -- the 4-bit paged key/value cache: tokens quantised as they are written,
+// and read back.
+//
+// A group of 32 values of one token and head has a power-of-two scale of its own, so a
+// token's codes depend on nothing but its values: no block is quantised again as it
+// grows.  V lies transposed (kv4_device.cuh); 8 x 8 nibbles are turned in registers.
+#include <cstdint>
+#include <type_traits>
+
+#include "kv4_device.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;                 // 16-byte loads of a thread that are out at once, for K and for V each
+
+// The idx-th block that a batch's tokens touch, as kv::find_touched, found by the whole
+// CTA: four sequences a thread at most.
+struct Found {
+    kv::Touched t;
+    int warps[kThreads / 32];
+    int hit;
+};
+__device__ __forceinline__ bool find(const KvView& c, int idx, Found& f)
+{
+    const int tid = threadIdx.x, lane = tid & 31, per = (c.n_seqs + kThreads - 1) / kThreads;
+    auto blocks = [&](int b, int& c0, int& n, int& len) {
+        if (!kv::sequence(c, b, c0, n, len)) {
+            atomicExch(c.status, MOE_ERR_DEVICE_FAULT);
+            n = 0;
+        }
+        return n > 0 ? (len - 1) / c.blk - (len - n) / c.blk + 1 : 0;
+    };
+    int sum = 0, c0, n, len;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i)
+        if (per * tid + i < c.n_seqs)
+            sum += blocks(per * tid + i, c0, n, len);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    if (lane == 31)
+        f.warps[tid >> 5] = incl;
+    if (tid == 0)
+        f.hit = 0;
+    __syncthreads();
+    for (int w = 0; w < tid >> 5; ++w)
+        incl += f.warps[w];
+    if (idx < incl && idx >= incl - sum) {
+        int at = incl - sum;
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) {
+            const int b = per * tid + i, cnt = b < c.n_seqs ? blocks(b, c0, n, len) : 0;
+            if (idx < at + cnt) {
+                f.t = kv::Touched{b, c0, n, len, (len - n) / c.blk + idx - at};
+                f.hit = 1;
+                break;
+            }
+            at += cnt;
+        }
+    }
+    __syncthreads();
+    return f.hit;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w)
+{
+    const uint32_t x = w & 0x7fffu, y = w >> 16 & 0x7fffu;
+    return max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u);
+}
+__device__ __forceinline__ float no_nan(float x) { return x == x ? x : 0.0f; }
+
+// Eight of a group's 32 values, the others in the quad's other lanes -> eight codes, and
+// the group's scale byte.
+__device__ __forceinline__ uint32_t encode8(const uint4& q, uint32_t& byte)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t big = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        big = max(big, finite_bits(w[e]));
+    big = max(big, __shfl_xor_sync(~0u, big, 1));
+    big = max(big, __shfl_xor_sync(~0u, big, 2));
+    byte = kv4::scale_byte(big);
+    const float inv = __uint_as_float((254u - byte) << 23);    // 2^-e
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        r |= tc::e2m1x2(no_nan(lo_bf16(w[e]) * inv), no_nan(hi_bf16(w[e]) * inv)) << 8 * e;
+    return byte ? r : 0u;
+}
+
+// One CTA per (touched block, some heads): heads, as many as fit the buffer, at a time.
+template <int D, int blk>
+__global__ void __launch_bounds__(kThreads)
+kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __restrict__ vsrc, long long kstride, long long vstride,
+                 int heads_per_cta)
+{
+    __shared__ uint32_t codes[blk * (D / 8)];                  // V as written by token: [head][token][D / 8] words
+    __shared__ Found found;
+    constexpr int W = D / 8, REC = kv4::record(blk, D);
+    const int tid = threadIdx.x;
+    if (!find(c, blockIdx.x, found))
+        return;
+    const kv::Touched t = found.t;
+    const int id = kv::physical(c, t.b, t.j);
+    if (id < 0)
+        return;
+    const int start = t.len - t.n - t.j * blk;                 // offset of the sequence's first new token
+    const int lo = start > 0 ? start : 0, hi = min(t.len - t.j * blk, blk), n = hi - lo;
+    const bool fresh = lo == 0;
+    const long long row0 = t.c0 - start + lo;
+    const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, c.H), batch = blk / n;
+    for (int hb = h0; hb < h1; hb += batch) {
+        const int nh = min(batch, h1 - hb), units = nh * n * W;
+        uint8_t* rec = c.codes + ((long long)id * c.H + hb) * 2 * REC;
+        for (int i0 = tid; i0 - tid < units; i0 += kAhead * kThreads) {
+            uint4 k[kAhead], v[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int i = i0 + e * kThreads, x = i % W, r = i / W % n, h = i / W / n;
+                k[e] = v[e] = make_uint4(0, 0, 0, 0);
+                if (i < units) {
+                    const long long col = (long long)(hb + h) * D + x * 8;
+                    k[e] = *reinterpret_cast<const uint4*>(ksrc + (row0 + r) * kstride + col);
+                    v[e] = *reinterpret_cast<const uint4*>(vsrc + (row0 + r) * vstride + col);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int i = i0 + e * kThreads, x = i % W, r = i / W % n, h = i / W / n, tok = lo + r;
+                if (i0 - tid + e * kThreads >= units)
+                    break;
+                uint32_t kb, vb;
+                const uint32_t kc = encode8(k[e], kb), vc = encode8(v[e], vb);
+                if (i >= units)
+                    continue;
+                uint8_t* kr = rec + (long long)h * 2 * REC;
+                reinterpret_cast<uint32_t*>(kr)[tok * W + x] = kc;
+                codes[i] = vc;
+                if (x % 4 == 0) {
+                    kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)] = (uint8_t)kb;
+                    kr[REC + blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)] = (uint8_t)vb;
+                }
+            }
+        }
+        __syncthreads();
+        // V: eight tokens by eight d's; words that hold other tokens too are merged
+        const int t8lo = lo / 8, nt8 = (fresh ? blk / 8 : (hi + 7) / 8) - t8lo, pieces = nh * nt8 * W;
+        for (int i = tid; i < pieces; i += kThreads) {
+            const int x = i % W, t8 = t8lo + i / W % nt8, h = i / W / nt8;
+            uint32_t w[8], keep = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int tok = t8 * 8 + k;
+                const bool in = tok >= lo && tok < hi;
+                w[k] = in ? codes[(h * n + tok - lo) * W + x] : 0u;
+                keep |= in || fresh ? 0u : 0xfu << 4 * k;
+            }
+            kv4::transpose(w);
+            uint32_t* vr = reinterpret_cast<uint32_t*>(rec + ((long long)h * 2 + 1) * REC);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                uint32_t* p = vr + kv4::v_word_at<D>(t8, x / 4, x % 4, r);
+                *p = keep ? (w[r] & ~keep) | (*p & keep) : w[r];
+            }
+        }
+        if (fresh && hi < blk) {
+            // unwritten tokens of a block whose first token came
+            for (int i = tid; i < nh * (blk - hi) * W; i += kThreads) {
+                const int x = i % W, r = i / W % (blk - hi), h = i / W / (blk - hi), tok = hi + r;
+                uint8_t* kr = rec + (long long)h * 2 * REC;
+                reinterpret_cast<uint32_t*>(kr)[tok * W + x] = 0u;
+                if (x % 4 == 0) {
+                    kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)] = 0;
+                    kr[REC + blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)] = 0;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Eight codes -> eight bf16, times the scale, rounded once.
+__device__ __forceinline__ uint4 decode8(uint32_t w, float s)
+{
+    uint32_t h[4], o[4];
+    kv4::to_f16(w, h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+        o[e] = kv::bf16x2(f.x * s, f.y * s);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One CTA per (touched block, head): V's nibbles are turned back into shared memory, then
+// both go out by token.
+template <int D, int blk>
+__global__ void __launch_bounds__(kThreads)
+kv4_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vdst, long long kstride, long long vstride)
+{
+    __shared__ uint32_t codes[blk * (D / 8 + 1)];
+    __shared__ Found found;
+    constexpr int W = D / 8, REC = kv4::record(blk, D);
+    const int tid = threadIdx.x, h = blockIdx.y;
+    if (!find(c, blockIdx.x, found))
+        return;
+    const kv::Touched t = found.t;
+    const int id = kv::physical(c, t.b, t.j);
+    if (id < 0)
+        return;
+    const int start = t.len - t.n - t.j * blk;
+    const int lo = start > 0 ? start : 0, hi = min(t.len - t.j * blk, blk), n = hi - lo;
+    const long long row0 = t.c0 - start + lo;
+    const uint8_t* kr = c.codes + ((long long)id * c.H + h) * 2 * REC;
+    const uint8_t* vr = kr + REC;
+    const int t8lo = lo / 8, nt8 = (hi + 7) / 8 - t8lo;
+    for (int i = tid; i < nt8 * W; i += kThreads) {
+        const int x = i % W, t8 = t8lo + i / W;
+        uint32_t w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            w[r] = reinterpret_cast<const uint32_t*>(vr)[kv4::v_word_at<D>(t8, x / 4, x % 4, r)];
+        kv4::transpose(w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            codes[(t8 * 8 + k) * (W + 1) + x] = w[k];
+    }
+    kdst += row0 * kstride + (long long)h * D;
+    vdst += row0 * vstride + (long long)h * D;
+    for (int i = tid; i < n * W; i += kThreads) {
+        const int x = i % W, r = i / W, tok = lo + r;
+        const uint32_t w = reinterpret_cast<const uint32_t*>(kr)[tok * W + x];
+        *reinterpret_cast<uint4*>(kdst + r * kstride + x * 8) = decode8(w, kv4::scale_of(kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)]));
+    }
+    __syncthreads();
+    for (int i = tid; i < n * W; i += kThreads) {
+        const int x = i % W, r = i / W, tok = lo + r;
+        *reinterpret_cast<uint4*>(vdst + r * vstride + x * 8) =
+            decode8(codes[tok * (W + 1) + x], kv4::scale_of(vr[blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)]));
+    }
+}
+
+// As for the 8-bit cache: an upper bound on the blocks that a batch touches, and one more,
+// whose CTA finds none and so checks every sequence.
+unsigned touched_grid(const KvView& c)
+{
+    const long long most = (long long)c.n_tokens / c.blk + 2ll * c.n_seqs;
+    return (unsigned)(most < c.n_tokens ? most : c.n_tokens) + 1;
+}
+
+template <class F>
+void by_size(const KvView& c, F f)
+{
+    auto block = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (c.blk == 32)
+            f(d, std::integral_constant<int, 32>());
+        else if (c.blk == 64)
+            f(d, std::integral_constant<int, 64>());
+        else
+            f(d, std::integral_constant<int, 128>());
+        (void)D;
+    };
+    if (c.D == 64)
+        block(std::integral_constant<int, 64>());
+    else
+        block(std::integral_constant<int, 128>());
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, cudaStream_t s)
+{
+    // single tokens: as many heads a CTA as fill it
+    const int tokens = (c.n_tokens + c.n_seqs - 1) / c.n_seqs, fit = kThreads / (c.D / 8) / tokens;
+    const int heads = fit < 1 ? 1 : fit < c.H ? fit : c.H;
+    const dim3 grid(touched_grid(c), (c.H + heads - 1) / heads);
+    by_size(c, [&](auto d, auto b) {
+        kv4_write_kernel<decltype(d)::value, decltype(b)::value><<<grid, kThreads, 0, s>>>(c, k, v, k_stride, v_stride, heads);
+    });
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride, cudaStream_t s)
+{
+    const dim3 grid(touched_grid(c), c.H);
+    by_size(c, [&](auto d, auto b) {
+        kv4_read_kernel<decltype(d)::value, decltype(b)::value><<<grid, kThreads, 0, s>>>(c, k, v, k_stride, v_stride);
+    });
+    return cudaGetLastError();
+}
+
+}  // namespace moe

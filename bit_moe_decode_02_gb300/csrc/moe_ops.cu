@@ -29,10 +29,13 @@ int check_cache(const char* who, const moe_ops* o, const moe_kv_cache* c, const 
 {
     if (!o || !c || !b)
         return set_error(MOE_ERR_INVALID_ARG, "%s: the handle, the cache and the batch must not be NULL", who);
-    if (!c->codes || !c->scales || !b->cu || !b->kv_len || !b->table)
+    const bool mx = c->format == MOE_KV_MXFP4;
+    if (!c->codes || (!c->scales && !mx) || !b->cu || !b->kv_len || !b->table)
         return set_error(MOE_ERR_INVALID_ARG, "%s: a pointer of the cache or the batch is NULL", who);
-    if (c->format != MOE_KV_E4M3 && c->format != MOE_KV_INT8)
+    if (c->format != MOE_KV_E4M3 && c->format != MOE_KV_INT8 && !mx)
         return set_error(MOE_ERR_INVALID_ARG, "%s: unknown cache format %d", who, c->format);
+    if (mx && c->scales)
+        return set_error(MOE_ERR_INVALID_ARG, "%s: scales must be NULL (an MXFP4 cache holds them with its codes)", who);
     if (c->block != 32 && c->block != 64 && c->block != 128)
         return set_error(MOE_ERR_UNSUPPORTED, "%s: block=%d (32, 64 or 128)", who, c->block);
     if (c->head_dim != 64 && c->head_dim != 128)
@@ -182,8 +185,9 @@ int moe_kv_write(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batc
         rc = check_rows("moe_kv_write", "v", v_bf16, v_stride, (long long)v.H * v.D);
     if (rc != MOE_OK)
         return rc;
-    const cudaError_t e = moe::launch_kv_write(v, static_cast<const uint16_t*>(k_bf16), static_cast<const uint16_t*>(v_bf16),
-                                               k_stride, v_stride, (cudaStream_t)stream);
+    const auto launch = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_write : moe::launch_kv_write;
+    const cudaError_t e = launch(v, static_cast<const uint16_t*>(k_bf16), static_cast<const uint16_t*>(v_bf16), k_stride, v_stride,
+                                 (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_kv_write");
 }
 
@@ -198,8 +202,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
         rc = check_rows("moe_kv_read", "v", v_bf16, v_stride, (long long)v.H * v.D);
     if (rc != MOE_OK)
         return rc;
-    const cudaError_t e = moe::launch_kv_read(v, static_cast<uint16_t*>(k_bf16), static_cast<uint16_t*>(v_bf16), k_stride,
-                                              v_stride, (cudaStream_t)stream);
+    const auto launch = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_read : moe::launch_kv_read;
+    const cudaError_t e = launch(v, static_cast<uint16_t*>(k_bf16), static_cast<uint16_t*>(v_bf16), k_stride, v_stride,
+                                 (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_kv_read");
 }
 

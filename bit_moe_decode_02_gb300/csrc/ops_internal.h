@@ -1,5 +1,5 @@
 // ops_internal.h -- what the operators around the expert block share: the
-// handle, the kernels' view of an 8-bit paged cache, and the launches that
+// handle, the kernels' view of a paged cache, and the launches that
 // moe_ops.cu makes after its argument checks.  Not part of the public interface.
 #pragma once
 #include <cstddef>
@@ -26,8 +26,8 @@ constexpr int kMaxBatchQ = 1 << 20;     // tokens of one batch
 
 // One batch over one cache, as the kernels see it.
 struct KvView {
-    uint8_t* codes;          // [num_blocks][H][2][blk * D]
-    float* scales;           // [num_blocks][H][2]
+    uint8_t* codes;          // [num_blocks][H][2][blk * D]; MXFP4: [num_blocks][H][2][blk * D / 32 * 17]
+    float* scales;           // [num_blocks][H][2]; MXFP4: nullptr
     const int* cu;           // [n_seqs + 1]
     const int* len;          // [n_seqs]
     const int* table;        // [n_seqs][table_stride]
@@ -40,6 +40,11 @@ cudaError_t launch_kv_write(const KvView& c, const uint16_t* k, const uint16_t* 
                             long long v_stride, cudaStream_t s);
 cudaError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride,
                            cudaStream_t s);
+
+cudaError_t launch_kv4_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride,
+                             long long v_stride, cudaStream_t s);
+cudaError_t launch_kv4_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride,
+                            cudaStream_t s);
 
 struct AttnArgs {
     KvView c;

@@ -415,7 +415,7 @@ void moe_destroy(moe_handle* h);
 
 /* ======================================================================
  * The operators around the expert block in a decode step, and in the prompt
- * before it: an 8-bit paged key/value cache, attention over it, projections
+ * before it: a paged key/value cache in 8 or 4 bits, attention over it, projections
  * with 4-bit weights, and sampling.  The pages name them as the rest of the
  * decode ("Sovereign gpt-oss-20B (MXFP4) on Apple Silicon", sections 1 and 3:
  * attention with sinks and a sliding window, the LM head; the "greedy, KV"
@@ -458,8 +458,22 @@ void moe_ops_destroy(moe_ops* o);
  * holds no NaN code (0x7f, 0xff: none is ever written) and no scale that is negative,
  * infinite or NaN; what attention makes of one is not defined, but stays in the
  * sequences whose tables name the block.  block 32, 64 or 128; head_dim 64 or 128; kv_heads
- * 1..256. */
-typedef enum { MOE_KV_E4M3 = 1, MOE_KV_INT8 = 2 } moe_kv_format;
+ * 1..256.
+ *
+ * In 4 bits, MOE_KV_MXFP4: FP4 E2M1 codes with an E8M0 scale byte s (the value is the
+ * code times 2^(s - 127); 0: a group of zeros) for each group of 32 values of one token
+ * and head, d = 32 g .. 32 g + 31.  `scales` is NULL:
+ *   codes  u8 [num_blocks][kv_heads][2][block * head_dim * 17 / 32], 16-byte aligned: for
+ *          K, then for V, the block's codes and after them its scale bytes, 32 tokens at
+ *          a time.  With t of the block, u = t % 32, d = 32 g + 8 e + r (e 0..3, r 0..7):
+ *   K code  byte t * head_dim / 2 + d / 2, the even d in the low nibble;
+ *   K scale byte (t / 32) * head_dim + ((2 (u / 8) + u % 2) * head_dim / 32 + g) * 4 +
+ *           (u / 2) % 4;
+ *   V code  byte (((t / 32) * head_dim / 32 + g) * 8 + r) * 64 + (u / 8) * 16 + 4 e +
+ *           (u % 8) / 2, the even t in the low nibble;
+ *   V scale byte ((t / 32) * head_dim / 32 + g) * 32 + u.
+ * An MXFP4 cache holds no scale byte 255 where a token is. */
+typedef enum { MOE_KV_E4M3 = 1, MOE_KV_INT8 = 2, MOE_KV_MXFP4 = 4 } moe_kv_format;
 typedef struct {
     void* codes;
     float* scales;
@@ -493,13 +507,19 @@ typedef struct {
  *   earlier tokens' codes c become round(c * (old * (1 / new)));
  *   code = round(x * (1 / scale)), to nearest even, saturating; a NaN becomes
  *   0 and an infinity the largest code.
- * (1 / scale and the products are single fp32 operations.)  Sequences must
- * not share a block that is written.  The rows are 16-byte aligned and the
- * strides multiples of 8. */
+ * (1 / scale and the products are single fp32 operations.)  MXFP4, for each group
+ * apart, with a its largest finite magnitude: below 2^-100 its codes and its scale
+ * byte are 0; else the scale is the smallest 2^e with a <= 6 * 2^e, the byte e + 127,
+ * and a code the nearest E2M1 value to x / 2^e, ties to the even code, saturating; a NaN
+ * becomes 0 and an infinity +-6.  What a token becomes depends on nothing else, and
+ * other tokens' codes stay; a block whose first token is written has its unwritten
+ * tokens' codes and scale bytes set to 0.  Sequences must not share a block that is
+ * written.  The rows are 16-byte aligned and the strides multiples of 8. */
 int moe_kv_write(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k_bf16,
                  long long k_stride, const void* v_bf16, long long v_stride, void* stream);
 
-/* Read the batch's tokens back: code * scale, rounded to bf16, into rows
+/* Read the batch's tokens back: code * scale, rounded to bf16 (MXFP4: exact, but for
+ * magnitudes that round up to 2^128, which are infinite), into rows
  * k_stride / v_stride elements apart.  Conditions as for moe_kv_write; the
  * same batch names the tokens (so cu and kv_len of another batch, say all of
  * a prefix, read those). */
@@ -523,7 +543,10 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * and so is its lse; other rows are not touched by it.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
- * product as 11 bits down to 2^-20, below that within 2^-31.  The (sequence,
+ * product as 11 bits down to 2^-20, below that within 2^-31.  MXFP4: of a key, the groups whose
+ * scale is less than 2^-27 of its largest group's count as 0; where the V scales of one
+ * group of the head are 2^7 apart or more within 32 tokens, 11 bits down to 2^-12, below
+ * that within 2^-23 of the largest.  The (sequence,
  * 16 rows, kv head, block) combinations of one call number less than 2^31 (else
  * nothing is written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,

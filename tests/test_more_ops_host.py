@@ -167,3 +167,20 @@ def test_binding_refuses_tensors_of_another_form(o):
         moe.moe_lora(o, moe.moe_lora_weights(A, A, None, 1, 8, 4, 64), i, torch.zeros(4, 64), torch.zeros(4, 4))
     with pytest.raises(ValueError, match="n_tokens"):
         moe.moe_kv_plan(o, moe.moe_kv_pool(A, A, 4, 2, 2, 64), i, i, i, i, i, i)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(scales=A), INV, "scales must be NULL"), (dict(codes=None), INV, "NULL"), (dict(codes=A + 8), INV, "aligned"), (dict(block=16), UNS, "block"),
+    (dict(head_dim=96), UNS, "head_dim"), (dict(format=3), INV, "format"), (dict(format=5), INV, "format"), (dict(kv_heads=0), INV, "kv_heads")])
+def test_mxfp4_cache_refusals(L, o, kw, code, word):
+    d = dict(codes=A, scales=None, num_blocks=10, kv_heads=2, head_dim=64, block=64, format=moe.MOE_KV_MXFP4)
+    d.update(kw)
+    c = moe.moe_kv_cache(*[d[f] for f, _ in moe.moe_kv_cache._fields_])
+    b = moe.moe_kv_batch(A, A, A, 2, 3, 4)
+    if d["format"] in (3, 5):
+        c.scales = A
+    for name, call in (("moe_kv_write", lambda: L.moe_kv_write(o, c, b, A, 128, A, 128, None)),
+                       ("moe_kv_read", lambda: L.moe_kv_read(o, c, b, A, 128, A, 128, None)),
+                       ("moe_attention", lambda: L.moe_attention(o, c, b, A, 256, 4 if c.kv_heads else 1, 0.1, 0, None, 2 * A, None, None))):
+        assert call() == code, name
+        assert word in moe.moe_last_error() and name in moe.moe_last_error()
