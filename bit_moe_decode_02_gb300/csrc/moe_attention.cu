@@ -234,25 +234,6 @@ struct Decode {
     static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 4; }
 };
 
-// max and sum of each half, unsigned
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
-{
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // One warp's 32 tokens of a block in 4 bits: scores, running maximum, P V.
 //  - K.  A key's codes become f16 times 2^(13 + e_g - e), e_g a group's exponent and e the
 //    key's largest: exact down to 2^-27, and no key's size touches another's.  Its score
@@ -314,8 +295,8 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
             for (int i = 0; i < 4; ++i) {
                 uint32_t h[4];
                 kv4::to_f16(w[i][ch], h);
-                mma16816(s[i], qf[2 * ch], mul2(h[0], ksc[i]), mul2(h[1], ksc[i]));
-                mma16816(s[i], qf[2 * ch + 1], mul2(h[2], ksc[i]), mul2(h[3], ksc[i]));
+                mma16816(s[i], qf[2 * ch], mul_f16(h[0], ksc[i]), mul_f16(h[1], ksc[i]));
+                mma16816(s[i], qf[2 * ch + 1], mul_f16(h[2], ksc[i]), mul_f16(h[3], ksc[i]));
             }
     }
 #pragma unroll
@@ -450,8 +431,8 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
         for (int g = 0; g < G; ++g) {
             const uint4 z = *reinterpret_cast<const uint4*>(scratch + g * (kSub * 2) + c * 16);
             const uint4 w = *reinterpret_cast<const uint4*>(vt + (g * 32 + lane) * 16);
-            const uint32_t pa[4] = {mul2(pf[0][0], z.x), mul2(pf[0][1], z.x), mul2(pf[0][2], z.y), mul2(pf[0][3], z.y)};
-            const uint32_t pb[4] = {mul2(pf[1][0], z.z), mul2(pf[1][1], z.z), mul2(pf[1][2], z.w), mul2(pf[1][3], z.w)};
+            const uint32_t pa[4] = {mul_f16(pf[0][0], z.x), mul_f16(pf[0][1], z.x), mul_f16(pf[0][2], z.y), mul_f16(pf[0][3], z.y)};
+            const uint32_t pb[4] = {mul_f16(pf[1][0], z.z), mul_f16(pf[1][1], z.z), mul_f16(pf[1][2], z.w), mul_f16(pf[1][3], z.w)};
             const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -1138,7 +1119,7 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
     const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
     const long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
-    return decode > prompt && a.c.fmt != MOE_KV_MXFP4 ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
+    return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
 }  // namespace moe

@@ -29,6 +29,7 @@
 #include <cstdint>
 
 #include "attn_device.cuh"
+#include "kv4_device.cuh"
 
 namespace moe {
 namespace {
@@ -40,11 +41,24 @@ constexpr int kRows = 256;                // of a CTA
 constexpr int kKeys = 128;                // of a tile
 constexpr int kRing = 8;                  // tiles whose scales are kept: the loads are at most four ahead of the softmax
 
-template <int D, int BLK>
+// A pass of a tile over a 4-bit cache: which of its keys take part, what their K's are scaled
+// by, and the units of O's columns.
+struct Pass {
+    uint32_t keys[4];                     // a bit a key
+    int kref;                             // K's f16 operand is its value times 2^(13 + 127 - kref)
+    int unit[4];                          // of each group's V: its f16 operand is the value times 2^(13 + 127 - unit)
+    int most[4];                          // largest exponent field of those operands' scales: 28, less in a later pass (0: none)
+    uint32_t flags;                       // kCount: the probabilities join the sums; kAll: all keys
+};
+enum : uint32_t { kCount = 1, kAll = 2 };
+
+template <int D, int FMT, int BLK>
 struct Layout {
+    static constexpr bool MX = FMT == MOE_KV_MXFP4;
     static constexpr int NB = kKeys / BLK;                // cache blocks of a tile
     static constexpr int OP = kKeys * D * 2;              // bytes of an f16 operand: Q tile, K tile, V tile
-    static constexpr int RAW = kKeys * D;                 // bytes of a tile's K or V codes
+    static constexpr int REC = MX ? kv4::record(BLK, D) : BLK * D;     // bytes of a block's K or V
+    static constexpr int RAW = NB * REC;                  // bytes of a tile's K or V codes
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = 2 * OP;
     static constexpr int OFF_V = OFF_K + 2 * OP;
@@ -53,7 +67,8 @@ struct Layout {
     static constexpr int OFF_BAR = OFF_SC + kRing * 4 * 8;
     static constexpr int OFF_INFO = OFF_BAR + 24 * 8;     // [kRing]: position of the first key, bit 0: the last tile
     static constexpr int OFF_MAX = OFF_INFO + kRing * 4;  // [2 row tiles][2 halves][128]
-    static constexpr int SMEM = OFF_MAX + 2 * 2 * 128 * 4;   // 226.4 KB for D = 128, of 227
+    static constexpr int OFF_PASS = OFF_MAX + 2 * 2 * 128 * 4;         // MXFP4: [kRing]
+    [[maybe_unused]] static constexpr int SMEM = OFF_PASS + (MX ? kRing * (int)sizeof(Pass) : 0);   // 226.4 KB for D = 128 in 8 bits, of 227
 };
 
 // The whole warp executes these, one elected lane (`one` != 0) issues: outside a
@@ -193,10 +208,168 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int idx, Work& w)
     return false;
 }
 
+// The producer of a 4-bit cache: a tile's raw records, and how it goes through.  Keys whose
+// largest scales are within 2^9 go together (K's f16 operand holds 2^36), the others in passes
+// of their own; V's groups each have a unit that O's 32 columns are kept in, which moves where
+// a tile's largest scale leaves [unit - 16, unit], and scales 2^28 and more below it go in
+// passes of their own with the same probabilities.  One warp; nearly every tile is one pass.
+template <int D, int BLK>
+__device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pass* passes, int* info, uint8_t* raw, uint64_t* raw_full,
+                                           uint64_t* raw_empty, int tile0, int nt, int jlo, int jhi, int see_lo, int see_hi)
+{
+    using L = Layout<D, MOE_KV_MXFP4, BLK>;
+    constexpr int G = D / 32, N = D / 32;                 // N: words of a lane's scales, K's and V's
+    const int lane = threadIdx.x & 31, sub = lane >> 3, r = lane & 7;
+    int* status = a.c.status;
+    auto block_of = [&](int t) {
+        const int j = (tile0 + t) * L::NB + lane;
+        return lane < L::NB && t < nt && j >= jlo && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
+    };
+    // K: four keys (8 (r / 2) + 2 i + r % 2 of the 32, a byte each) in every group; V: 4 N keys of one group
+    struct Scales {
+        uint32_t k[N], v[N];
+    };
+    auto scales_of = [&](int id) {
+        Scales z;
+        const int mine = __shfl_sync(~0u, id, sub * 32 / BLK);
+        const uint8_t* p = a.c.codes + ((long long)mine * a.c.H + w.h) * 2 * L::REC + BLK * D / 2 + sub * 32 % BLK / 32 * D + r * (4 * N);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint2 x = mine >= 0 ? *reinterpret_cast<const uint2*>(p + 4 * i) : make_uint2(0, 0);
+            const uint2 y = mine >= 0 ? *reinterpret_cast<const uint2*>(p + L::REC + 4 * i) : make_uint2(0, 0);
+            z.k[i] = x.x, z.k[i + 1] = x.y, z.v[i] = y.x, z.v[i + 1] = y.y;
+        }
+        return z;
+    };
+    const int g = r * 4 * N / 32, t4 = r * 4 * N % 32;    // V: this lane's group, its first key of the 32
+    int unit = 28, vmax = 28;                             // of group g
+    int id = block_of(0);
+    Scales z = scales_of(id);
+    int t = 0;
+#pragma unroll 1
+    for (int tile = 0; tile < nt; ++tile) {
+        const int next = block_of(tile + 1);
+        const int base = (tile0 + tile) * kKeys, here = base + 32 * sub;
+        const bool block = __shfl_sync(~0u, id, sub * 32 / BLK) >= 0;
+        int ke[4];                                        // a key's largest scale byte, -1: no row sees it
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = here + 8 * (r >> 1) + 2 * i + (r & 1);
+            int e = 0;
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                e = max(e, (int)(z.k[x] >> 8 * i & 0xff));
+            ke[i] = block && p >= see_lo && p <= see_hi ? e : -1;
+        }
+        uint32_t vb[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            vb[x] = z.v[x];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = here + t4 + 4 * x + k;
+                if (p < see_lo || p > see_hi)
+                    vb[x] &= ~(0xffu << 8 * k);
+            }
+        }
+        const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * L::REC;
+        const int n = __popc(__ballot_sync(~0u, id >= 0));
+        unsigned rest = (ke[0] >= 0) | (ke[1] >= 0) << 1 | (ke[2] >= 0) << 2 | (ke[3] >= 0) << 3;
+        bool again_k = false, again_v = false;
+        uint32_t left[N];
+        unsigned in = 0;
+        int kref = 0;
+#pragma unroll 1
+        do {
+            if (!again_v) {
+                // the keys of this pass: the largest, and those within 2^9 of it (keys of zeros with the first)
+                int big = -1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rest >> i & 1)
+                        big = max(big, ke[i]);
+                kref = max(__reduce_max_sync(~0u, big), 40);
+                in = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((rest >> i & 1) && (ke[i] >= kref - 9 || ke[i] == 0))
+                        in |= 1u << i;
+                rest &= ~in;
+                again_k = __any_sync(~0u, rest != 0);
+#pragma unroll
+                for (int x = 0; x < N; ++x)
+                    left[x] = vb[x];
+            }
+            int big = 0;
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                big = max(max(big, max((int)(left[x] & 0xff), (int)(left[x] >> 8 & 0xff))), max((int)(left[x] >> 16 & 0xff), (int)(left[x] >> 24)));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                if (o < 8 / G || o >= 8)
+                    big = max(big, __shfl_xor_sync(~0u, big, o));
+            vmax = max(vmax, big);
+            const int done = again_v ? unit - 28 : 254;       // larger scales have been in an earlier pass
+            if (big > 0 && (big > unit || big < unit - 16))
+                unit = min(max(max(big + 1, vmax - 64), 28), 254);
+            const int field = big > 0 ? min(done - unit, 0) + 28 : 0;
+            bool more = false;
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int b = left[x] >> 8 * k & 0xff;
+                    if (b > 0 && b <= unit - 28 && b > vmax - 92)
+                        keep |= 0xffu << 8 * k;
+                }
+                left[x] &= keep;
+                more |= keep != 0;
+            }
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                bits |= (in >> i & 1) << (8 * (r >> 1) + 2 * i + (r & 1));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                bits |= __shfl_xor_sync(~0u, bits, o);
+            Pass& p = passes[t % kRing];
+            const bool first = !again_v;
+            again_v = __any_sync(~0u, more);
+            const bool last = tile + 1 == nt && !again_k && !again_v, whole = __all_sync(~0u, in == 15);
+            if (r == 0)
+                p.keys[sub] = bits;
+            if (sub == 0 && r % (8 / G) == 0) {
+                p.unit[g] = unit;
+                p.most[g] = field;
+            }
+            if (lane == 0) {
+                p.flags = (first ? kCount : 0u) | (whole ? kAll : 0u);
+                p.kref = kref;
+                info[t % kRing] = base | (int)last;
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                if (t >= 1)
+                    tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_expect_tx(raw_full + v, (uint32_t)n * L::REC);
+                __syncwarp();
+                if (id >= 0)
+                    tc::bulk_copy(raw + v * L::RAW + lane * L::REC, src + v * L::REC, L::REC, raw_full + v);
+            }
+            ++t;
+        } while (again_k || again_v);
+        id = next;
+        z = scales_of(id);
+    }
+}
+
 template <int D, int FMT, int BLK>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
 {
-    using L = Layout<D, BLK>;
+    using L = Layout<D, FMT, BLK>;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -216,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     const int pos0 = w.len - w.n + i0, pos1 = w.len - w.n + i1;
     const int tile0 = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kKeys : 0, nt = pos1 / kKeys - tile0 + 1;
     // `info` says which tile is the last one; this bounds the loops should a wait have given up
-    const int most = nt * L::NB;
+    const int most = nt * (L::MX ? 256 : L::NB);
+    Pass* passes = reinterpret_cast<Pass*>(sm + L::OFF_PASS);
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -246,56 +420,61 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         // ---- raw codes and scales of each tile's blocks, of those that a row sees: a caller may
         // have given the ones before a window to other sequences
         const int jlo = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / BLK : 0, jhi = pos1 / BLK;
-        auto block_of = [&](int t) {
-            const int j = (tile0 + t) * L::NB + lane;
-            return lane < L::NB && t < nt && j >= jlo && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
-        };
-        auto scales_of = [&](int id) {
-            return id >= 0 ? *reinterpret_cast<const float2*>(a.c.scales + ((long long)id * a.c.H + w.h) * 2) : make_float2(-1.0f, 0.0f);
-        };
-        int id = block_of(0);
-        float2 s = scales_of(id);
-        int t = 0;
+        if constexpr (L::MX)
+            mx_produce<D, BLK>(a, w, passes, info, sm + L::OFF_RAW, raw_full, raw_empty, tile0, nt, jlo, jhi,
+                               a.window > 0 && pos0 >= a.window ? pos0 - a.window + 1 : 0, pos1);
+        else {
+            auto block_of = [&](int t) {
+                const int j = (tile0 + t) * L::NB + lane;
+                return lane < L::NB && t < nt && j >= jlo && j <= jhi ? kv::physical(a.c, w.b, j) : -1;
+            };
+            auto scales_of = [&](int id) {
+                return id >= 0 ? *reinterpret_cast<const float2*>(a.c.scales + ((long long)id * a.c.H + w.h) * 2) : make_float2(-1.0f, 0.0f);
+            };
+            int id = block_of(0);
+            float2 s = scales_of(id);
+            int t = 0;
 #pragma unroll 1
-        for (int tile = 0; tile < nt; ++tile) {
-            const int next = block_of(tile + 1);
-            const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * (BLK * D);
-            // blocks with V scales far apart go one after another
-            bool split = false;
-            if constexpr (L::NB > 1) {
-                float big = id >= 0 ? s.y : 0.0f, small = big > 0.0f ? big : INFINITY;
+            for (int tile = 0; tile < nt; ++tile) {
+                const int next = block_of(tile + 1);
+                const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * (BLK * D);
+                // blocks with V scales far apart go one after another
+                bool split = false;
+                if constexpr (L::NB > 1) {
+                    float big = id >= 0 ? s.y : 0.0f, small = big > 0.0f ? big : INFINITY;
 #pragma unroll
-                for (int o = 1; o < L::NB; o <<= 1) {
-                    big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-                    small = fminf(small, __shfl_xor_sync(~0u, small, o));
+                    for (int o = 1; o < L::NB; o <<= 1) {
+                        big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+                        small = fminf(small, __shfl_xor_sync(~0u, small, o));
+                    }
+                    split = __shfl_sync(~0u, big > 64.0f * small, 0);
                 }
-                split = __shfl_sync(~0u, big > 64.0f * small, 0);
-            }
-            unsigned left = split ? __ballot_sync(~0u, id >= 0) : 0u;
-            do {
-                const unsigned now = split ? left & (~left + 1) : ~0u;
-                left &= ~now;
-                const bool have = id >= 0 && (now >> lane & 1);
-                if (lane < L::NB)
-                    sc[(t % kRing) * 4 + lane] = have ? s : make_float2(-1.0f, 0.0f);
-                if (lane == 0)
-                    info[t % kRing] = (tile0 + tile) * kKeys | (tile + 1 == nt && !left);
-                const int n = __popc(__ballot_sync(~0u, have));
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (t >= 1)
-                        tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
-                    __syncwarp();
+                unsigned left = split ? __ballot_sync(~0u, id >= 0) : 0u;
+                do {
+                    const unsigned now = split ? left & (~left + 1) : ~0u;
+                    left &= ~now;
+                    const bool have = id >= 0 && (now >> lane & 1);
+                    if (lane < L::NB)
+                        sc[(t % kRing) * 4 + lane] = have ? s : make_float2(-1.0f, 0.0f);
                     if (lane == 0)
-                        tc::mbar_expect_tx(raw_full + v, (uint32_t)n * (BLK * D));
-                    __syncwarp();
-                    if (have)
-                        tc::bulk_copy(sm + L::OFF_RAW + v * L::RAW + lane * (BLK * D), src + v * (BLK * D), BLK * D, raw_full + v);
-                }
-                ++t;
-            } while (left);
-            id = next;
-            s = scales_of(id);
+                        info[t % kRing] = (tile0 + tile) * kKeys | (tile + 1 == nt && !left);
+                    const int n = __popc(__ballot_sync(~0u, have));
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        if (t >= 1)
+                            tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_expect_tx(raw_full + v, (uint32_t)n * (BLK * D));
+                        __syncwarp();
+                        if (have)
+                            tc::bulk_copy(sm + L::OFF_RAW + v * L::RAW + lane * (BLK * D), src + v * (BLK * D), BLK * D, raw_full + v);
+                    }
+                    ++t;
+                } while (left);
+                id = next;
+                s = scales_of(id);
+            }
         }
     } else if (warp == 1) {
         // ---- MMAs, the row tiles in turn: P V of a tile of keys and the scores of the
@@ -364,7 +543,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             const bool last = info[t % kRing] & 1;
             if (t >= 2)
                 tc::mbar_wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
-            {
+            if constexpr (L::MX) {
+                // K: this thread's token, a group's 16 bytes at a time in an order that spreads the banks
+                const Pass& p = passes[t % kRing];
+                const uint8_t* rec = sm + L::OFF_RAW + ct / BLK * L::REC;
+                uint8_t* out = sm + L::OFF_K + st * L::OP + (ct >> 3) * (D * 16) + (ct & 7) * 16;
+                const bool have = p.keys[ct >> 5] >> (ct & 31) & 1;
+                uint4 w[D / 32];
+                uint32_t z[D / 32];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int g = (i + ct / (256 / D)) & (D / 32 - 1);
+                    w[i] = *reinterpret_cast<const uint4*>(rec + ct % BLK * (D / 2) + 16 * g);
+                    // 2^(13 + 127 + e - kref) in f16, with its subnormal numbers
+                    const int e = rec[BLK * D / 2 + kv4::k_scale_at<D>(ct % BLK, g)];
+                    const float f = have ? __uint_as_float((uint32_t)max(e - p.kref + 140, 0) << 23) : 0.0f;
+                    z[i] = pack_f16(f, f);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int g = (i + ct / (256 / D)) & (D / 32 - 1);
+                    const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t h[4];
+                        kv4::to_f16(words[k], h);
+                        *reinterpret_cast<uint4*>(out + 512 * g + 128 * k) = make_uint4(mul_f16(h[0], z[i]), mul_f16(h[1], z[i]), mul_f16(h[2], z[i]), mul_f16(h[3], z[i]));
+                    }
+                }
+            } else {
                 // K: this thread's token; its 16-code pieces in an order that spreads the banks
                 const uint8_t* raw = sm + L::OFF_RAW + ct * D;
                 uint8_t* out = sm + L::OFF_K + st * L::OP + (ct >> 3) * (D * 16) + (ct & 7) * 16;
@@ -391,7 +598,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             tc::mbar_wait(raw_full + 1, (uint32_t)(t & 1), status);
             if (t >= 2)
                 tc::mbar_wait(v_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
-            {
+            if constexpr (L::MX) {
+                // V: eight tokens of four d's at a time, as the record's words lie
+                const Pass& p = passes[t % kRing];
+                const int cw = ct >> 5, r = lane >> 2, c = lane & 3;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int sub = i * 4 / (D / 32) + cw / (D / 32), g = (i * 4 + cw) % (D / 32);
+                    const uint8_t* rec = sm + L::OFF_RAW + L::RAW + sub * 32 / BLK * L::REC;
+                    const int in = sub * 32 % BLK / 32 * (D / 32) + g;
+                    const uint4 w = *reinterpret_cast<const uint4*>(rec + (in * 32 + lane) * 16);
+                    const uint2 b = *reinterpret_cast<const uint2*>(rec + BLK * D / 2 + in * 32 + 8 * c);
+                    // 2^(13 + e - unit): exponent field e - unit + 28, where that is 1 to 28
+                    const uint32_t base = (uint32_t)(p.unit[g] - 28) * 0x10001u, top = (uint32_t)p.most[g];
+                    const uint32_t bytes[4] = {__byte_perm(b.x, 0, 0x4140), __byte_perm(b.x, 0, 0x4342), __byte_perm(b.y, 0, 0x4140),
+                                               __byte_perm(b.y, 0, 0x4342)};
+                    uint32_t z[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t x = max2(bytes[k], base) - base;
+                        // above: a token that no row sees, or one that an earlier pass has had
+                        z[k] = ((x & 0xffffu) <= top ? x & 0xffffu : 0u) << 10 | ((x >> 16) <= top ? x >> 16 : 0u) << 26;
+                    }
+                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t h[4];
+                        kv4::to_f16(words[e], h);
+                        *reinterpret_cast<uint4*>(sm + L::OFF_V + st * L::OP + (4 * g + e) * 2048 + r * 16 + (4 * sub + c) * 128) =
+                            make_uint4(mul_f16(h[0], z[0]), mul_f16(h[1], z[1]), mul_f16(h[2], z[2]), mul_f16(h[3], z[3]));
+                    }
+                }
+            } else {
                 // V: this thread's d, 16 tokens at a time
                 const int d = ct & (D - 1), part = ct / D;
                 const uint8_t* raw = sm + L::OFF_RAW + L::RAW + d * BLK;
@@ -469,6 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             const int all_hi = w.len - w.n + (w.rt * kRows + x * 128) / a.group;
             const int all_lo = a.window > 0 ? w.len - w.n + (w.rt * kRows + min(rows, x * 128 + 128) - 1) / a.group - a.window + 1 : 0;
             float m = kNone, l = 0.0f, ref = 0.0f, vmax = 0.0f;
+            int was[D / 32];                  // MXFP4: O's units
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g)
+                was[g] = 28;
+            auto was_of = [&](int ch) { return half ? was[D / 64 + ch] : was[ch]; };       // of this thread's columns
 #pragma unroll 1
             for (int t = 0; t < most; ++t) {
                 tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
@@ -476,21 +719,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 const int word = info[t % kRing], p0 = word & ~1;
                 float top = 0.0f;
                 bool whole = p0 >= all_lo && p0 + kKeys - 1 <= all_hi;
+                const Pass& pass = passes[t % kRing];
+                if constexpr (L::MX) {
+                    whole = whole && (pass.flags & kAll);
+                } else {
 #pragma unroll
-                for (int b = 0; b < L::NB; ++b) {
-                    const float2 v = sc[(t % kRing) * 4 + b];
-                    top = fmaxf(top, v.y);
-                    whole = whole && v.x >= 0.0f;
+                    for (int b = 0; b < L::NB; ++b) {
+                        const float2 v = sc[(t % kRing) * 4 + b];
+                        top = fmaxf(top, v.y);
+                        whole = whole && v.x >= 0.0f;
+                    }
                 }
+                // the scales of 32 keys: K's, V's
+                const float kscale = L::MX ? __uint_as_float((uint32_t)pass.kref << 23) * 0x1p-13f : 0.0f;
+                auto scales = [&](int g) { return L::MX ? make_float2(kscale, 1.0f) : sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK]; };
                 // scores of 32 keys of this row, -inf where it does not see them
                 auto take = [&](int g, uint32_t (&v)[32], float ks) {
                     tm_ld32(ts + 32 * g, v);
                     tm_wait_ld(v);
                     if (!whole) {
+                        const uint32_t keys = L::MX ? pass.keys[2 * half + g] : ks < 0.0f ? 0u : ~0u;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const int p = p0 + 64 * half + 32 * g + k;
-                            if (ks < 0.0f || p < plo || p > phi)
+                            if (!(keys >> k & 1) || p < plo || p > phi)
                                 v[k] = 0xff800000u;
                         }
                     }
@@ -498,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 float mx = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float ks = sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK].x;
+                    const float ks = scales(g).x;
                     uint32_t v[32];
                     take(g, v, ks);
                     float y[4];
@@ -515,13 +767,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 *mine = mx;
                 pair_sync();
                 mx = fmaxf(mx, *other);
-                const bool unit = !(top <= 2.0f * ref && top >= 0.5f * ref);            // the same for all warps
+                bool unit = !(top <= 2.0f * ref && top >= 0.5f * ref);                  // the same for all warps
+                if constexpr (L::MX) {
+                    unit = false;
+#pragma unroll
+                    for (int g = 0; g < D / 32; ++g)
+                        unit |= pass.unit[g] != was[g];
+                }
                 if (__any_sync(~0u, unit || mx > m + kSlack)) {                         // the same for both of a pair
                     const float mn = fmaxf(m, mx);
                     float al = ex2(m - mn);
                     m = mn;
                     l *= al;
-                    if (unit) {
+                    if (!L::MX && unit) {
                         vmax = fmaxf(vmax, top);
                         const float now = new_unit(top, vmax);
                         al *= ref / now;
@@ -531,18 +789,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
 #pragma unroll 1
                         for (int ch = 0; ch < D / 64; ++ch) {
                             uint32_t v[32];
+                            const float by = L::MX ? al * ex2((float)max(was_of(ch) - pass.unit[half * (D / 64) + ch], -126)) : al;
                             tm_ld32(to + 32 * ch, v);
                             tm_wait_ld(v);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                                v[k] = __float_as_uint(__uint_as_float(v[k]) * by);
                             tm_st32(to + 32 * ch, v);
                         }
+                    if constexpr (L::MX) {
+#pragma unroll
+                        for (int g = 0; g < D / 32; ++g)
+                            was[g] = pass.unit[g];
+                    }
                 }
-                const float iref = rcp(ref);
+                const float iref = L::MX ? 1.0f : rcp(ref);
+                // scores so large that their rounding is more than the room that a probability has: the
+                // product is rounded as the maximum's was
+                const bool far = __any_sync(~0u, fabsf(m) > 4194304.0f && m != kNone);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float2 kv = sc[(t % kRing) * 4 + (64 * half + 32 * g) / BLK];
+                    const float2 kv = scales(g);
                     const float c = fmaxf(kv.x * f, 1e-37f), ratio = fmaxf(kv.y * iref, 8.673617379884035e-19f);   // 2^-60
                     const float off = lg2(ratio) - m + kRoom;
                     uint32_t v[32], p[16];
@@ -551,14 +818,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     float2 part[2];
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        float2 z = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), cc, oo);
+                        const float2 x = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        float2 z = far ? make_float2(__fadd_rn(__fmul_rn(x.x, c), off), __fadd_rn(__fmul_rn(x.y, c), off)) : fma2(x, cc, oo);
                         z.x = ex2(z.x);
                         z.y = ex2(z.y);
                         part[k / 2 & 1] = k > 2 ? add2(part[k / 2 & 1], z) : z;
                         p[k / 2] = pack_f16(z.x, z.y);
                     }
                     const float2 both = add2(part[0], part[1]);
-                    l += (both.x + both.y) * rcp(ratio);
+                    if (!L::MX)
+                        l += (both.x + both.y) * rcp(ratio);
+                    else if (pass.flags & kCount)
+                        l += both.x + both.y;
                     tm_st16(ts + 16 * g, p);
                 }
                 tm_wait_st();
@@ -577,10 +848,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             tc::mbar_wait(o_full + x, 0, status);
             tc::tc_fence_after();
             const Final fin = finish(m, l, a.sinks, hq);
-            const float mul = fin.mul * ref * kUnroom;
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
+                const float mul = fin.mul * kUnroom * (L::MX ? __uint_as_float((uint32_t)was_of(ch) << 23) * 0x1p-13f : ref);
                 uint32_t v[32];
                 tm_ld32(to + 32 * ch, v);
                 tm_wait_ld(v);
@@ -615,20 +886,29 @@ Kernel pick(int blk)
 }
 Kernel kernel_for(int d, int fmt, int blk)
 {
+    if (fmt == MOE_KV_MXFP4)
+        return d == 64 ? pick<64, MOE_KV_MXFP4>(blk) : pick<128, MOE_KV_MXFP4>(blk);
     if (d == 64)
         return fmt == MOE_KV_E4M3 ? pick<64, MOE_KV_E4M3>(blk) : pick<64, MOE_KV_INT8>(blk);
     return fmt == MOE_KV_E4M3 ? pick<128, MOE_KV_E4M3>(blk) : pick<128, MOE_KV_INT8>(blk);
 }
-int smem_of(int d) { return d == 64 ? Layout<64, 64>::SMEM : Layout<128, 64>::SMEM; }   // whatever the block
+// whatever the block
+int smem_of(int d, int fmt)
+{
+    if (fmt == MOE_KV_MXFP4)
+        return d == 64 ? Layout<64, MOE_KV_MXFP4, 64>::SMEM : Layout<128, MOE_KV_MXFP4, 64>::SMEM;
+    return d == 64 ? Layout<64, MOE_KV_INT8, 64>::SMEM : Layout<128, MOE_KV_INT8, 64>::SMEM;
+}
 
 }  // namespace
 
 cudaError_t prepare_prompt_kernels()
 {
     for (int d = 64; d <= 128; d *= 2)
-        for (int fmt : {MOE_KV_E4M3, MOE_KV_INT8})
+        for (int fmt : {MOE_KV_E4M3, MOE_KV_INT8, MOE_KV_MXFP4})
             for (int blk = 32; blk <= 128; blk *= 2) {
-                const cudaError_t e = cudaFuncSetAttribute(kernel_for(d, fmt, blk), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(d));
+                const cudaError_t e = cudaFuncSetAttribute(kernel_for(d, fmt, blk), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           smem_of(d, fmt));
                 if (e != cudaSuccess)
                     return e;
             }
@@ -639,7 +919,7 @@ cudaError_t launch_attention_prompt(const AttnArgs& a, int, cudaStream_t s)
 {
     // an upper bound on the groups of 256 rows: CTAs beyond the last one end at once
     const long long groups = ((long long)a.c.n_tokens * a.group / kRows + a.c.n_seqs) * a.c.H;
-    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)groups, kThreads, smem_of(a.c.D), s>>>(a);
+    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)groups, kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a);
     return cudaGetLastError();
 }
 
