@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -212,8 +213,16 @@ def lib() -> ctypes.CDLL:
         L.moe_rope.restype = i
         L.moe_lora.argtypes = [p, ctypes.POINTER(moe_lora_weights), p, p, ll, i, p, ll, p, ll, i, p]
         L.moe_lora.restype = i
+        # the same calls with their arguments as 64-bit words (moe_ops.cu): one conversion instead of many
+        for name in ("rope", "kv_plan", "lora"):
+            f = getattr(L, "moe_words_" + name)
+            f.argtypes = [ctypes.c_char_p]
+            f.restype = i
         _lib = L
     return _lib
+
+
+_WORDS_ROPE, _WORDS_PLAN, _WORDS_LORA = struct.Struct("=17q").pack, struct.Struct("=14q").pack, struct.Struct("=12q").pack
 
 
 def moe_last_error() -> str:
@@ -505,30 +514,31 @@ def moe_kv_pool_of(ring, table, block) -> moe_kv_pool:
     return c
 
 
+def _array(t, name, dtype, n):
+    """Address of a contiguous CUDA tensor [n] of that type."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype} [{n}] is needed (got {t.dtype} {tuple(t.shape)} on {t.device})")
+    return t.data_ptr()
+
+
 def moe_kv_plan(o, pool, n_new, kv_len, state, cu, kv_len_out, state_out, admitted=None, seq=None, position=None, slot=None,
                 n_tokens=None, stream=None):
     """n_new, kv_len, kv_len_out int32 [n_seqs], state, state_out int32 [2], cu int32 [n_seqs + 1], admitted int32 [1], seq and
     position int32 and slot int64 [n_tokens]; n_tokens (their length) has to be given where all three are None."""
     import torch
     i, n = torch.int32, pool.n_seqs
-    for t in (seq, position, slot):
-        if t is not None and n_tokens is None:
-            n_tokens = t.shape[0]
     if n_tokens is None:
-        raise ValueError("moe_kv_plan: n_tokens is needed where seq, position and slot are None")
-
-    def at(t, name, dtype, size, optional=False):
-        if t is None and optional:
-            return None
-        if t.shape != (size,) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"moe_kv_plan: {name} must be a contiguous CUDA tensor of {dtype} [{size}] (got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device})")
-        return t.data_ptr()
-    return _check(lib().moe_kv_plan(o, pool, at(n_new, "n_new", i, n), at(kv_len, "kv_len", i, n), at(state, "state", i, 2), n_tokens,
-                                    at(cu, "cu", i, n + 1), at(kv_len_out, "kv_len_out", i, n), at(state_out, "state_out", i, 2),
-                                    at(admitted, "admitted", i, 1, True), at(seq, "seq", i, n_tokens, True),
-                                    at(position, "position", i, n_tokens, True), at(slot, "slot", torch.int64, n_tokens, True),
-                                    _raw_stream(stream, n_new)))
+        t = slot if slot is not None else position if position is not None else seq
+        if t is None:
+            raise ValueError("moe_kv_plan: n_tokens is needed where seq, position and slot are None")
+        n_tokens = t.shape[0]
+    rc = lib().moe_words_kv_plan(_WORDS_PLAN(
+        o, ctypes.addressof(pool), _array(n_new, "n_new", i, n), _array(kv_len, "kv_len", i, n), _array(state, "state", i, 2), n_tokens,
+        _array(cu, "cu", i, n + 1), _array(kv_len_out, "kv_len_out", i, n), _array(state_out, "state_out", i, 2),
+        0 if admitted is None else _array(admitted, "admitted", i, 1), 0 if seq is None else _array(seq, "seq", i, n_tokens),
+        0 if position is None else _array(position, "position", i, n_tokens),
+        0 if slot is None else _array(slot, "slot", torch.int64, n_tokens), _raw_stream(stream, n_new)))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def moe_rope_turns(rot_dim, base, scaling=MOE_ROPE_PLAIN, factor=1.0, length=0.0, low=0.0, high=0.0):
@@ -551,36 +561,41 @@ def moe_rope_of(rot_dim, base, layout=MOE_ROPE_HALF, scaling=MOE_ROPE_PLAIN, fac
     return r
 
 
+def _head_rows(t, name, kind, T, heads, D):
+    """Address and row stride of rows [T][heads][D] of a type, with contiguous heads."""
+    st = t.stride()
+    if t.dtype is not kind or not t.is_cuda or t.shape != (T, heads, D) or st[2] != 1 or (st[1] != D and heads > 1):
+        raise ValueError(f"{name}: CUDA rows [{T}][{heads}][{D}] of {kind} with contiguous heads are needed (got {t.dtype} {tuple(t.shape)}, "
+                         f"strides {st}, on {t.device})")
+    return t.data_ptr(), st[0] if T > 1 else heads * D
+
+
 def moe_rope(o, rope, position, q, k=None, q_out=None, k_out=None, stream=None):
     """q [T][q_heads][head_dim], k [T][k_heads][head_dim] or None, of bf16 or fp32; q_out, k_out like them (None: in place);
     position int32 [T].  Rows may be strided, heads are contiguous."""
     import torch
-    if position.dim() != 1 or position.dtype is not torch.int32 or not position.is_cuda or not position.is_contiguous():
-        raise ValueError(f"moe_rope: position must be a contiguous CUDA int32 tensor [T] (got {position.dtype} "
-                         f"{tuple(position.shape)} on {position.device})")
-    T, kind = position.shape[0], q.dtype
-    if kind is not torch.bfloat16 and kind is not torch.float32:
-        raise ValueError(f"moe_rope: q must be bf16 or fp32 (got {kind})")
-
-    def rows(t, name, like=None):
-        st = t.stride()
-        if (t.dim() != 3 or t.shape[0] != T or t.dtype is not kind or not t.is_cuda or (like is not None and t.shape != like.shape) or
-                t.shape[2] != q.shape[2] or st[2] != 1 or (st[1] != t.shape[2] and t.shape[1] > 1)):
-            raise ValueError(f"moe_rope: {name} must be CUDA rows [{T}][heads][head_dim] of {kind} with contiguous heads (got {t.dtype} "
-                             f"{tuple(t.shape)}, strides {st}, on {t.device})")
-        return t.data_ptr(), st[0] if T > 1 else t.shape[1] * t.shape[2]
-    qp, qs = rows(q, "q")
-    op, os_ = (qp, qs) if q_out is None else rows(q_out, "q_out", q)
-    if k is None:
-        if k_out is not None:
-            raise ValueError("moe_rope: k_out without k")
-        kp, ks, kh, lp, ls = None, 0, 0, None, 0
+    T, heads, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    kind = q.dtype
+    if kind is torch.bfloat16:
+        code = MOE_DT_BF16
+    elif kind is torch.float32:
+        code = MOE_DT_F32
     else:
-        kp, ks = rows(k, "k")
-        kh = k.shape[1]
-        lp, ls = (kp, ks) if k_out is None else rows(k_out, "k_out", k)
-    return _check(lib().moe_rope(o, rope, position.data_ptr(), T, q.shape[2], MOE_DT_BF16 if kind is torch.bfloat16 else MOE_DT_F32,
-                                 qp, qs, q.shape[1], op, os_, kp, ks, kh, lp, ls, _raw_stream(stream, q)))
+        raise ValueError(f"moe_rope: q must be bf16 or fp32 (got {kind})")
+    pos = _array(position, "position", torch.int32, T)
+    qp, qs = _head_rows(q, "q", kind, T, heads, D)
+    op, os_ = (qp, qs) if q_out is None else _head_rows(q_out, "q_out", kind, T, heads, D)
+    if k is not None:
+        kh = k.shape[1] if k.dim() == 3 else 0
+        kp, ks = _head_rows(k, "k", kind, T, kh, D)
+        lp, ls = (kp, ks) if k_out is None else _head_rows(k_out, "k_out", kind, T, kh, D)
+    elif k_out is None:
+        kp = lp = kh = ks = ls = 0
+    else:
+        raise ValueError("moe_rope: k_out without k")
+    rc = lib().moe_words_rope(_WORDS_ROPE(o, ctypes.addressof(rope), pos, T, D, code, qp, qs, heads, op, os_, kp, ks, kh, lp, ls,
+                                          _raw_stream(stream, q)))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def moe_lora_of(a, b, scale=None) -> moe_lora_weights:
@@ -598,26 +613,37 @@ def moe_lora_of(a, b, scale=None) -> moe_lora_weights:
     return w
 
 
+def _out_rows(t, name, kind, M, rows):
+    """Address and stride of rows [M][rows] of a type."""
+    st = t.stride()
+    if t.dtype is not kind or t.shape != (M, rows) or not t.is_cuda or (st[1] != 1 and rows > 1):
+        raise ValueError(f"moe_lora: {name} must be CUDA {kind} rows [{M}][{rows}], y and out of one type (got {t.dtype} {tuple(t.shape)}, "
+                         f"strides {st}, on {t.device})")
+    return t.data_ptr(), st[0] if M > 1 else rows
+
+
 def moe_lora(o, w, index, x, y, out=None, stream=None):
     """x bf16 [M][cols], y fp32 or bf16 [M][rows] or None (0), out like y (None: y, in place); rows may be strided; index int32
     [M], -1: no adapter."""
     import torch
-    out = y if out is None else out
-    M, rows, cols, kind = x.shape[0], w.rows, w.cols, out.dtype
-    if index.shape != (M,) or index.dtype is not torch.int32 or not index.is_cuda or not index.is_contiguous():
-        raise ValueError(f"moe_lora: index must be a contiguous CUDA int32 tensor [{M}] (got {index.dtype} {tuple(index.shape)} on "
-                         f"{index.device})")
-    if x.shape != (M, cols) or x.dtype is not torch.bfloat16 or not x.is_cuda or x.stride(1) != 1:
-        raise ValueError(f"moe_lora: x must be CUDA bf16 rows [M][{cols}] (got {x.dtype} {tuple(x.shape)}, strides {x.stride()})")
-    for t, name in ((y, "y"), (out, "out")):
-        if t is not None and (t.shape != (M, rows) or t.dtype is not kind or kind not in (torch.bfloat16, torch.float32) or not t.is_cuda or
-                              (t.stride(1) != 1 and rows > 1)):
-            raise ValueError(f"moe_lora: {name} must be CUDA fp32 or bf16 rows [{M}][{rows}], y and out of one type (got {t.dtype} "
-                             f"{tuple(t.shape)}, strides {t.stride()})")
-    row = lambda t, n: t.stride(0) if M > 1 else n         # noqa: E731
-    return _check(lib().moe_lora(o, w, index.data_ptr(), x.data_ptr(), row(x, cols), M, None if y is None else y.data_ptr(),
-                                 0 if y is None else row(y, rows), out.data_ptr(), row(out, rows),
-                                 MOE_DT_BF16 if kind is torch.bfloat16 else MOE_DT_F32, _raw_stream(stream, x)))
+    rows, cols = w.rows, w.cols
+    if out is None:
+        out = y
+    M, kind, sx = x.shape[0], out.dtype, x.stride()
+    at = _array(index, "index", torch.int32, M)
+    if x.dtype is not torch.bfloat16 or x.shape != (M, cols) or not x.is_cuda or sx[1] != 1:
+        raise ValueError(f"moe_lora: x must be CUDA bf16 rows [M][{cols}] (got {x.dtype} {tuple(x.shape)}, strides {sx}, on {x.device})")
+    if kind is torch.bfloat16:
+        code = MOE_DT_BF16
+    elif kind is torch.float32:
+        code = MOE_DT_F32
+    else:
+        raise ValueError(f"moe_lora: y and out must be bf16 or fp32 (got {kind})")
+    op, so = _out_rows(out, "out", kind, M, rows)
+    yp, sy = (0, 0) if y is None else (op, so) if y is out else _out_rows(y, "y", kind, M, rows)
+    rc = lib().moe_words_lora(_WORDS_LORA(o, ctypes.addressof(w), at, x.data_ptr(), sx[0] if M > 1 else cols, M, yp, sy, op, so, code,
+                                          _raw_stream(stream, x)))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def moe_linear_of(codes, scales, bias, format, group) -> moe_linear_weights:

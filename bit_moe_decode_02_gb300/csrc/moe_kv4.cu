@@ -14,18 +14,20 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;                 // 16-byte loads of a thread that are out at once, for K and for V each
+constexpr int kAhead = 2;                 // 16-byte loads of a thread that are out at once, for K and for V each
 
-// The idx-th block that a batch's tokens touch, as kv::find_touched, found by the whole
-// CTA: four sequences a thread at most.
+// The idx-th block that a batch's tokens touch: by each warp for itself, or of more than 32
+// sequences by the whole CTA, four sequences a thread at most.
 struct Found {
     kv::Touched t;
     int warps[kThreads / 32];
     int hit;
 };
-__device__ __forceinline__ bool find(const KvView& c, int idx, Found& f)
+__device__ __forceinline__ bool find(const KvView& c, int idx, Found& f, kv::Touched& t)
 {
     const int tid = threadIdx.x, lane = tid & 31, per = (c.n_seqs + kThreads - 1) / kThreads;
+    if (c.n_seqs <= 32)
+        return kv::find_touched(c, idx, t);
     auto blocks = [&](int b, int& c0, int& n, int& len) {
         if (!kv::sequence(c, b, c0, n, len)) {
             atomicExch(c.status, MOE_ERR_DEVICE_FAULT);
@@ -66,6 +68,7 @@ __device__ __forceinline__ bool find(const KvView& c, int idx, Found& f)
         }
     }
     __syncthreads();
+    t = f.t;
     return f.hit;
 }
 
@@ -76,31 +79,68 @@ __device__ __forceinline__ uint32_t finite_bits(uint32_t w)
     const uint32_t x = w & 0x7fffu, y = w >> 16 & 0x7fffu;
     return max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u);
 }
-__device__ __forceinline__ float no_nan(float x) { return x == x ? x : 0.0f; }
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t quad_max2(uint32_t m)
+{
+    m = max2(m, __shfl_xor_sync(~0u, m, 1));
+    return max2(m, __shfl_xor_sync(~0u, m, 2));
+}
+// Two bf16 times a power of two, exact but below 2^-126.
+__device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Eight values -> eight codes, each rounded once to nearest even, saturating.
+__device__ __forceinline__ uint32_t to_codes(const uint32_t (&w)[4])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(lo_bf16(w[0])), "f"(hi_bf16(w[0])), "f"(lo_bf16(w[1])), "f"(hi_bf16(w[1])), "f"(lo_bf16(w[2])), "f"(hi_bf16(w[2])),
+          "f"(lo_bf16(w[3])), "f"(hi_bf16(w[3])));
+    return r;
+}
 
 // Eight of a group's 32 values, the others in the quad's other lanes -> eight codes, and
 // the group's scale byte.
 __device__ __forceinline__ uint32_t encode8(const uint4& q, uint32_t& byte)
 {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t big = 0;
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    // largest magnitude of each half of the words, as bits: NaN and infinities above all others
+    uint32_t m = quad_max2(max2(max2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+    uint32_t big = max(m & 0xffffu, m >> 16);
+    if (__any_sync(~0u, big >= 0x7f80u)) {
+        // NaN or infinity among the warp's values: the largest of the others; NaN becomes 0
+        m = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        big = max(big, finite_bits(w[e]));
-    big = max(big, __shfl_xor_sync(~0u, big, 1));
-    big = max(big, __shfl_xor_sync(~0u, big, 2));
+        for (int e = 0; e < 4; ++e) {
+            m = max(m, finite_bits(w[e]));
+            w[e] &= ((w[e] & 0x7fffu) > 0x7f80u ? 0u : 0xffffu) | ((w[e] & 0x7fff0000u) > 0x7f800000u ? 0u : 0xffff0000u);
+        }
+        big = quad_max2(m);
+    }
     byte = kv4::scale_byte(big);
-    const float inv = __uint_as_float((254u - byte) << 23);    // 2^-e
-    uint32_t r = 0;
+    const uint32_t inv = ((254u - byte) << 7) * 0x10001u;      // 2^-e
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        r |= tc::e2m1x2(no_nan(lo_bf16(w[e]) * inv), no_nan(hi_bf16(w[e]) * inv)) << 8 * e;
+        w[e] = mul_bf16(w[e], inv);
+    const uint32_t r = to_codes(w);
     return byte ? r : 0u;
 }
 
 // One CTA per (touched block, some heads): heads, as many as fit the buffer, at a time.
 template <int D, int blk>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
 kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __restrict__ vsrc, long long kstride, long long vstride,
                  int heads_per_cta)
 {
@@ -108,9 +148,9 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
     __shared__ Found found;
     constexpr int W = D / 8, REC = kv4::record(blk, D);
     const int tid = threadIdx.x;
-    if (!find(c, blockIdx.x, found))
+    kv::Touched t;
+    if (!find(c, blockIdx.x, found, t))
         return;
-    const kv::Touched t = found.t;
     const int id = kv::physical(c, t.b, t.j);
     if (id < 0)
         return;
@@ -122,11 +162,18 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
     for (int hb = h0; hb < h1; hb += batch) {
         const int nh = min(batch, h1 - hb), units = nh * n * W;
         uint8_t* rec = c.codes + ((long long)id * c.H + hb) * 2 * REC;
+        // row i of a head's `per`
+        auto split = [&](int i, int per, int& h, int& r) {
+            h = nh == 1 ? 0 : i / per;
+            r = i - h * per;
+        };
         for (int i0 = tid; i0 - tid < units; i0 += kAhead * kThreads) {
             uint4 k[kAhead], v[kAhead];
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads, x = i % W, r = i / W % n, h = i / W / n;
+                const int i = i0 + e * kThreads, x = i % W;
+                int h, r;
+                split(i / W, n, h, r);
                 k[e] = v[e] = make_uint4(0, 0, 0, 0);
                 if (i < units) {
                     const long long col = (long long)(hb + h) * D + x * 8;
@@ -136,13 +183,16 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
             }
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads, x = i % W, r = i / W % n, h = i / W / n, tok = lo + r;
+                const int i = i0 + e * kThreads, x = i % W;
                 if (i0 - tid + e * kThreads >= units)
                     break;
                 uint32_t kb, vb;
                 const uint32_t kc = encode8(k[e], kb), vc = encode8(v[e], vb);
                 if (i >= units)
                     continue;
+                int h, r;
+                split(i / W, n, h, r);
+                const int tok = lo + r;
                 uint8_t* kr = rec + (long long)h * 2 * REC;
                 reinterpret_cast<uint32_t*>(kr)[tok * W + x] = kc;
                 codes[i] = vc;
@@ -156,7 +206,10 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
         // V: eight tokens by eight d's; words that hold other tokens too are merged
         const int t8lo = lo / 8, nt8 = (fresh ? blk / 8 : (hi + 7) / 8) - t8lo, pieces = nh * nt8 * W;
         for (int i = tid; i < pieces; i += kThreads) {
-            const int x = i % W, t8 = t8lo + i / W % nt8, h = i / W / nt8;
+            const int x = i % W;
+            int h, t8;
+            split(i / W, nt8, h, t8);
+            t8 += t8lo;
             uint32_t w[8], keep = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -176,7 +229,10 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
         if (fresh && hi < blk) {
             // unwritten tokens of a block whose first token came
             for (int i = tid; i < nh * (blk - hi) * W; i += kThreads) {
-                const int x = i % W, r = i / W % (blk - hi), h = i / W / (blk - hi), tok = hi + r;
+                const int x = i % W;
+                int h, r;
+                split(i / W, blk - hi, h, r);
+                const int tok = hi + r;
                 uint8_t* kr = rec + (long long)h * 2 * REC;
                 reinterpret_cast<uint32_t*>(kr)[tok * W + x] = 0u;
                 if (x % 4 == 0) {
@@ -212,9 +268,9 @@ kv4_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vd
     __shared__ Found found;
     constexpr int W = D / 8, REC = kv4::record(blk, D);
     const int tid = threadIdx.x, h = blockIdx.y;
-    if (!find(c, blockIdx.x, found))
+    kv::Touched t;
+    if (!find(c, blockIdx.x, found, t))
         return;
-    const kv::Touched t = found.t;
     const int id = kv::physical(c, t.b, t.j);
     if (id < 0)
         return;

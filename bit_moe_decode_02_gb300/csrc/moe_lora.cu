@@ -23,54 +23,80 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxM = 64;                 // tokens of a call
 constexpr int kGroup = 8;                 // tokens of a group
 constexpr int kMaxParts = 16;             // of h, over the columns
-constexpr int kTiles = 4;                 // tiles of 16 rows of B that a warp takes at once
 
-// Tokens by adapter: groups of at most eight, in the order of their first tokens.
+// Tokens by adapter: groups of at most eight, in the order of their first tokens.  One warp
+// finds them, two tokens a lane.
 struct Groups {
     int n;
     int adapter[kMaxM];
     int member[kMaxM][kGroup];            // tokens, -1: none
-    int of[kMaxM];                        // a token's adapter, -1: none
-    int heads[2];
+    __align__(16) int of[kMaxM];          // a token's adapter, -1: none
 };
 __device__ __forceinline__ void find_groups(const LoraArgs& a, Groups& g)
 {
-    const int tid = threadIdx.x;
-    int mine = -1;
-    if (tid < kMaxM) {
-        mine = tid < a.M ? a.index[tid] : -1;
-        if (mine >= a.n_adapters) {
-            atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
-            mine = -1;
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid >= 32) {
+        for (int i = tid - 32; i < kMaxM * kGroup; i += kThreads - 32)
+            g.member[i / kGroup][i % kGroup] = -1;
+    }
+    int mine[2] = {-1, -1};
+    unsigned same[2][2];                  // the tokens of either half with this one's adapter
+    if (tid < 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = lane + 32 * h;
+            if (m < a.M)
+                mine[h] = a.index[m];
+            if (mine[h] >= a.n_adapters)
+                atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
+            if (mine[h] < 0 || mine[h] >= a.n_adapters)
+                mine[h] = -1;
+            g.of[m] = mine[h];
         }
-        mine = mine < 0 ? -1 : mine;
-        g.of[tid] = mine;
+        same[0][1] = same[1][0] = same[1][1] = 0;
+        if (a.M > 32) {
+            __syncwarp();
+            same[0][0] = 0;
+#pragma unroll
+            for (int i = 0; i < kMaxM; i += 4) {
+                const int4 x = *reinterpret_cast<const int4*>(g.of + i);
+                const int y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        same[h][i / 32] |= (y[k] == mine[h] ? 1u : 0u) << (i % 32 + k);
+            }
+        } else {
+            same[0][0] = __match_any_sync(~0u, mine[0]);
+        }
     }
-    for (int i = tid; i < kMaxM * kGroup; i += kThreads)
-        g.member[i / kGroup][i % kGroup] = -1;
-    __syncthreads();
-    int before = 0, head = tid;           // tokens before this one with its adapter; the first of its group
-    if (tid < kMaxM) {
-        if (mine >= 0)
-            for (int m = 0; m < tid; ++m)
-                before += g.of[m] == mine;
-        const unsigned first = __ballot_sync(~0u, mine >= 0 && before % kGroup == 0);
-        if ((tid & 31) == 0)
-            g.heads[tid >> 5] = (int)first;
+    __syncthreads();                      // the members are cleared
+    if (tid < 32) {
+        // tokens before this one with its adapter; its group's first, the groups before that
+        int before[2];
+        before[0] = __popc(same[0][0] & ((1u << lane) - 1));
+        before[1] = __popc(same[1][0]) + __popc(same[1][1] & ((1u << lane) - 1));
+        const unsigned heads[2] = {__ballot_sync(~0u, mine[0] >= 0 && before[0] % kGroup == 0),
+                                   __ballot_sync(~0u, mine[1] >= 0 && before[1] % kGroup == 0)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (mine[h] < 0)
+                continue;
+            unsigned lo = same[h][0], hi = h || a.M > 32 ? same[h][1] : 0u;
+            for (int i = before[h] / kGroup * kGroup; i > 0; --i) {      // to the group's first
+                if (lo)
+                    lo &= lo - 1;
+                else
+                    hi &= hi - 1;
+            }
+            const int at = lo ? __popc(heads[0] & ((lo & (~lo + 1)) - 1)) : __popc(heads[0]) + __popc(heads[1] & ((hi & (~hi + 1)) - 1));
+            g.member[at][before[h] % kGroup] = lane + 32 * h;
+            g.adapter[at] = mine[h];
+        }
+        if (lane == 0)
+            g.n = __popc(heads[0]) + __popc(heads[1]);
     }
-    __syncthreads();
-    if (tid < kMaxM && mine >= 0) {
-        int skip = before / kGroup * kGroup;
-        for (int m = 0; m <= tid; ++m)
-            if (g.of[m] == mine && skip-- == 0)
-                head = m;
-        const unsigned lo = g.heads[0], hi = g.heads[1];
-        const int at = head < 32 ? __popc(lo & ((1u << head) - 1)) : __popc(lo) + __popc(hi & ((1u << (head - 32)) - 1));
-        g.member[at][before % kGroup] = tid;
-        g.adapter[at] = mine;
-    }
-    if (tid == 0)
-        g.n = __popc((unsigned)g.heads[0]) + __popc((unsigned)g.heads[1]);
     __syncthreads();
 }
 
@@ -118,20 +144,30 @@ __global__ void __launch_bounds__(kThreads, 2) lora_a_kernel(LoraArgs a)
         const uint16_t* hi = lo + 8ll * a.cols;
         const uint16_t* x = a.x + (i64)max(token, 0) * a.x_stride + 8 * c;
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int U = 6;
-        for (int k = k0; k < k1; k += 32 * U) {
-            uint4 wl[U], wh[U], wx[U];
+        // the next U chunks are on their way while these are multiplied
+        constexpr int U = 3;
+        uint4 wl[2][U], wh[2][U], wx[2][U];
+        auto load = [&](int buf, int k) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = k + 32 * u;
                 const bool in = at + 8 * c < k1;
-                wl[u] = ldg(lo + at, in && lo_in);
-                wh[u] = ldg(hi + at, in && hi_in);
-                wx[u] = ldg(x + at, in && token >= 0);
+                wl[buf][u] = ldg(lo + at, in && lo_in);
+                wh[buf][u] = ldg(hi + at, in && hi_in);
+                wx[buf][u] = ldg(x + at, in && token >= 0);
             }
+        };
+        auto multiply = [&](int buf) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                mma32(d, wl[u], wh[u], wx[u]);
+                mma32(d, wl[buf][u], wh[buf][u], wx[buf][u]);
+        };
+        load(0, k0);
+        for (int k = k0; k < k1; k += 64 * U) {
+            load(1, k + 32 * U);
+            multiply(0);
+            load(0, k + 64 * U);
+            multiply(1);
         }
         // rows r, r + 8 of this tile by tokens 2c, 2c + 1
         __syncthreads();
@@ -167,84 +203,126 @@ __device__ __forceinline__ T rounded(float x)
         return x;
 }
 
-// out = y + s B h
-template <class T>
+// out = y + s B h.  A CTA takes a run of (group, NT tiles of 16 rows) and goes through it
+// group by group: the parts of the group's h are added up in shared memory, then every warp
+// takes every eighth of the group's tiles, with all CH chunks of 32 of the rank.
+template <class T, int CH, int NT>
 __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
 {
     __shared__ Groups g;
+    __shared__ __align__(16) float s_h[kGroup][32 * CH + 4];
     find_groups(a, g);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const T* y = static_cast<const T*>(a.y);
     T* out = static_cast<T*>(a.out);
-    const int parts = parts_of(a, g.n), chunks = (a.rank + 31) / 32;
-    const int tiles = (a.rows + 16 * kTiles - 1) / (16 * kTiles);
-    const i64 items = (i64)g.n * tiles;
-    bool waited = false;
-    for (i64 item = (i64)blockIdx.x * kWarps + warp; item < items; item += (i64)gridDim.x * kWarps) {
-        const int grp = (int)(item / tiles), n0 = (int)(item % tiles) * 16 * kTiles;
-        const int adapter = g.adapter[grp], token = g.member[grp][r];
-        float d[kTiles][4];
+    const int parts = parts_of(a, g.n), tiles = (a.rows + 16 * NT - 1) / (16 * NT);
+    const i64 items = (i64)g.n * tiles, first = items * blockIdx.x / gridDim.x, last = items * (blockIdx.x + 1) / gridDim.x;
+    uint4 lo[CH][NT], hi[CH][NT];
+    T yv[NT][2][2];
+    auto load = [&](int grp, int tile) {
+        const int n0 = tile * 16 * NT;
+        const uint16_t* b = a.b + ((i64)g.adapter[grp] * a.rows + n0 + r) * a.rank + 8 * c;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-            d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.0f;
-        for (int ch = 0; ch < chunks; ++ch) {
-            const int at = 32 * ch + 8 * c;
-            uint4 wl[kTiles], wh[kTiles];
+        for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 const int row = n0 + 16 * t + r;
-                const uint16_t* p = a.b + ((i64)adapter * a.rows + row) * a.rank + at;
-                wl[t] = ldg(p, at < a.rank && row < a.rows);
-                wh[t] = ldg(p + 8ll * a.rank, at < a.rank && row + 8 < a.rows);
+                const bool in = 32 * ch + 8 * c < a.rank;
+                lo[ch][t] = ldg(b + 16ll * t * a.rank + 32 * ch, in && row < a.rows);
+                hi[ch][t] = ldg(b + (16ll * t + 8) * a.rank + 32 * ch, in && row + 8 < a.rows);
             }
-            if (!waited) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                waited = true;
-            }
-            // this lane's eight of the group's h, in three bf16 terms
-            float h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                h[e] = 0.0f;
-            if (token >= 0 && at < a.rank)
-                for (int p = 0; p < parts; ++p) {
-                    const float4* q = reinterpret_cast<const float4*>(a.h + ((i64)p * kMaxM + token) * a.rank + at);
-                    const float4 u = __ldcg(q), v = __ldcg(q + 1);
-                    h[0] += u.x, h[1] += u.y, h[2] += u.z, h[3] += u.w, h[4] += v.x, h[5] += v.y, h[6] += v.z, h[7] += v.w;
-                }
-            uint32_t t3[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float u = h[2 * e], v = h[2 * e + 1];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    t3[i][e] = kv::bf16x2(u, v);
-                    u -= __uint_as_float(t3[i][e] << 16);
-                    v -= __uint_as_float(t3[i][e] & 0xffff0000u);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    mma32(d[t], wl[t], wh[t], make_uint4(t3[i][0], t3[i][1], t3[i][2], t3[i][3]));
-        }
-        const float s = a.scale ? a.scale[adapter] : 1.0f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int m = g.member[grp][2 * c + e];
-            if (m < 0)
-                continue;
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int row = n0 + 16 * t + r + 8 * k;
-                    if (row < a.rows) {
-                        const float base = y ? value(y + m * a.y_stride + row) : 0.0f;
-                        out[m * a.out_stride + row] = rounded<T>(base + s * d[t][2 * k + e]);
-                    }
+                    yv[t][e][k] = y && m >= 0 && row < a.rows ? y[m * a.y_stride + row] : T(0);
                 }
+        }
+    };
+    bool waited = false;
+    for (i64 item = first; item < last;) {
+        const int grp = (int)(item / tiles), tile0 = (int)(item - (i64)grp * tiles);
+        const int tile1 = (int)min((i64)tiles, tile0 + (last - item));
+        item += tile1 - tile0;
+        if (tile0 + warp < tile1)
+            load(grp, tile0 + warp);
+        if (!waited)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        else
+            __syncthreads();                                   // the last group's h is read no more
+        waited = true;
+        for (int i = tid; i < kGroup * 8 * CH; i += kThreads) {
+            const int n = i / (8 * CH), x = i % (8 * CH) * 4, m = g.member[grp][n];
+            float4 sum = make_float4(0, 0, 0, 0);
+            if (m >= 0 && x < a.rank) {
+                const float* h = a.h + (i64)m * a.rank + x;
+                constexpr int U = 8;                           // parts whose loads go out together
+                for (int p = 0; p < parts; p += U) {
+                    float4 v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        v[u] = p + u < parts ? __ldcg(reinterpret_cast<const float4*>(h + (i64)(p + u) * kMaxM * a.rank)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        sum.x += v[u].x, sum.y += v[u].y, sum.z += v[u].z, sum.w += v[u].w;
+                }
+            }
+            *reinterpret_cast<float4*>(&s_h[n][x]) = sum;
+        }
+        __syncthreads();
+        const float s = a.scale ? a.scale[g.adapter[grp]] : 1.0f;
+        uint32_t h3[CH][3][4];            // this lane's eight of a chunk of its token's h, in three bf16 terms
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 h = *reinterpret_cast<const float2*>(&s_h[r][32 * ch + 8 * c + 2 * e]);
+                float u = h.x, v = h.y;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    h3[ch][i][e] = kv::bf16x2(u, v);
+                    u -= __uint_as_float(h3[ch][i][e] << 16);
+                    v -= __uint_as_float(h3[ch][i][e] & 0xffff0000u);
+                }
+            }
+        for (int tile = tile0 + warp; tile < tile1; tile += kWarps) {
+            float d[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.0f;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma32(d[t], lo[ch][t], hi[ch][t], make_uint4(h3[ch][i][0], h3[ch][i][1], h3[ch][i][2], h3[ch][i][3]));
+            T base[NT][2][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    base[t][e / 2][e % 2] = yv[t][e / 2][e % 2];
+            if (tile + kWarps < tile1)
+                load(grp, tile + kWarps);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int m = g.member[grp][2 * c + e];
+                if (m < 0)
+                    continue;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = tile * 16 * NT + 16 * t + r + 8 * k;
+                        if (row < a.rows)
+                            out[m * a.out_stride + row] = rounded<T>(value(&base[t][e][k]) + s * d[t][2 * k + e]);
+                    }
+            }
         }
     }
     if (!waited)
@@ -255,6 +333,15 @@ __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
             if (g.of[m] < 0)
                 for (int row = tid; row < a.rows; row += kThreads)
                     out[m * a.out_stride + row] = y ? y[m * a.y_stride + row] : T(0);
+}
+
+typedef void (*KernelB)(LoraArgs);
+// NT: 8 KB of B a warp and step, whatever the rank
+template <class T>
+KernelB pick(int rank, int& rows)
+{
+    rows = rank <= 32 ? 64 : rank <= 64 ? 32 : 16;
+    return rank <= 32 ? lora_b_kernel<T, 1, 4> : rank <= 64 ? lora_b_kernel<T, 2, 2> : lora_b_kernel<T, 4, 1>;
 }
 
 }  // namespace
@@ -269,7 +356,9 @@ cudaError_t launch_lora(LoraArgs a, int num_sms, cudaStream_t s)
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    const i64 tiles = (i64)a.M * ((a.rows + 16 * kTiles - 1) / (16 * kTiles)), ctas = (tiles + kWarps - 1) / kWarps;
+    int rows;
+    const KernelB b = a.type == MOE_DT_BF16 ? pick<uint16_t>(a.rank, rows) : pick<float>(a.rank, rows);
+    const i64 items = (i64)a.M * ((a.rows + rows - 1) / rows), ctas = (items + kWarps - 1) / kWarps;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(ctas < a.ctas ? ctas : a.ctas));
     cfg.blockDim = dim3(kThreads);
@@ -279,7 +368,7 @@ cudaError_t launch_lora(LoraArgs a, int num_sms, cudaStream_t s)
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return a.type == MOE_DT_BF16 ? cudaLaunchKernelEx(&cfg, lora_b_kernel<uint16_t>, a) : cudaLaunchKernelEx(&cfg, lora_b_kernel<float>, a);
+    return cudaLaunchKernelEx(&cfg, b, a);
 }
 
 }  // namespace moe

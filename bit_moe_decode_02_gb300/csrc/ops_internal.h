@@ -100,13 +100,13 @@ struct RopeArgs {
     int n_tokens, q_heads, k_heads, D, rot, layout, type;
     float mscale;
     bool copy_rest;                    // what is not turned goes from one tensor to another
-    int per_cta, heads_per_cta;        // of the launch
+    int heads_per_cta;                 // of the launch
 };
 cudaError_t launch_rope(RopeArgs a, int num_sms, cudaStream_t s);
 
 struct PlanArgs {
     int *ring, *table;
-    int ring_size, n_seqs, table_stride, block;
+    int ring_size, n_seqs, table_stride, log_block;
     const int *n_new, *kv_len, *state;
     int *cu, *kv_len_out, *state_out;
     int *admitted, *seq, *position;    // or nullptr
