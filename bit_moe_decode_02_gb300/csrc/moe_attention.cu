@@ -45,15 +45,13 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;                 // rows of an item: (token, query head of the kv head) pairs
 constexpr int kSub = 32;                  // tokens of a block that one warp takes
 
 typedef long long i64;
 
 // fp32 workspace: partial results of the groups' first and last items, then of the CTAs'.
-constexpr int kMaxGroups = 8;
+constexpr int kMaxGroups = 12;
 __host__ __device__ constexpr i64 slot_floats() { return kRows * 128 + 2 * kRows; }
 
 struct Item {
@@ -215,20 +213,21 @@ struct Piece {
 
 template <int D, int FMT, int BLK>
 struct Decode {
-    static constexpr int GW = BLK / kSub;            // warps of a group
-    static constexpr int NG = kWarps / GW;           // groups of a CTA
     static constexpr bool MX = FMT == MOE_KV_MXFP4;
+    static constexpr int WARPS = MX ? 12 : 8, THREADS = WARPS * 32;
+    static constexpr int GW = BLK / kSub;            // warps of a group
+    static constexpr int NG = WARPS / GW;            // groups of a CTA
     static constexpr int RECORD = MX ? kv4::record(BLK, D) : BLK * D;  // bytes of K or V of a block
     static constexpr int STAGE = 2 * RECORD;         // bytes of a tile
-    // stages of a group's ring: 192 KB per CTA in all; MXFP4: 157 or 139 KB, and the warps' O
-    // of a finished run beside it (in 8 bits they go into the stage read last)
-    static constexpr int NS = MX ? (D == 64 ? 9 : 4) : D == 64 ? 6 : 3;
-    static constexpr int OFF_O = NG * NS * STAGE;                      // [kWarps][kRows][D] fp32
-    static constexpr int OFF_VS = OFF_O + (MX ? kWarps * kRows * D * 4 : 0);   // [kWarps][D / 32][kSub] f16
-    static constexpr int OFF_HDR = OFF_VS + (MX ? kWarps * D * 2 : 0); // per stage: two scales, valid
+    // stages of a group's ring: 192 KB per CTA in all; MXFP4: 157 KB, and 64 columns of the warps'
+    // O where an item ends within a run (in 8 bits, and at a run's end, they go into the ring)
+    static constexpr int NS = D == 64 ? 6 : 3;
+    static constexpr int OFF_O = NG * NS * STAGE;                      // [WARPS][kRows][64] fp32
+    static constexpr int OFF_VS = OFF_O + (MX ? WARPS * kRows * 64 * 4 : 0);   // [WARPS][D / 32][kSub] f16
+    static constexpr int OFF_HDR = OFF_VS + (MX ? WARPS * D * 2 : 0); // per stage: two scales, valid
     static constexpr int OFF_BAR = OFF_HDR + NG * NS * 16;
     static constexpr int OFF_ML = OFF_BAR + NG * NS * 16;              // full and empty barriers
-    static constexpr int OFF_PIECE = OFF_ML + kWarps * kRows * 8;
+    static constexpr int OFF_PIECE = OFF_ML + WARPS * kRows * 8;
     static constexpr int OFF_PRE = OFF_PIECE + NG * 2 * (int)sizeof(Piece);
     static constexpr int WHOLE = 2 * NG;             // items of at most so many tiles are not split over CTAs
     static constexpr int smem(int n_seqs) { return OFF_PRE + (n_seqs + 1) * 4; }
@@ -449,11 +448,11 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
 }
 
 template <int D, int FMT, int BLK>
-__global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
+__global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
 {
     using C = Decode<D, FMT, BLK>;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ i64 scan[kWarps];
+    __shared__ i64 scan[Decode<D, FMT, BLK>::WARPS];
     __shared__ int s_flag;
     int* pre = reinterpret_cast<int*>(sm + C::OFF_PRE);
     Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
     // prefix sums of the sequences' tiles: up to four sequences a thread
     i64 all;
     {
-        const int per = (a.c.n_seqs + kThreads - 1) / kThreads;
+        const int per = (a.c.n_seqs + C::THREADS - 1) / C::THREADS;
         i64 sum = 0;
 #pragma unroll 1
         for (int i = 0; i < per; ++i)
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         i64 at = incl - sum;
         all = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < C::WARPS; ++w) {
             at += w < warp ? scan[w] : 0;
             all += scan[w];
         }
@@ -830,38 +829,52 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                     mls[warp * kRows + r + 8 * e] = make_float2(m[e], l[e] * kUnroom);
             }
             group_sync(1 + grp, C::GW * 32);
-            float* od = reinterpret_cast<float*>(C::MX ? sm + C::OFF_O + grp * C::GW * (kRows * D * 4) : ring + st * C::STAGE);
+            // MXFP4: at a run's end nothing of the ring is wanted any more, and it holds all of O; else 64
+            // columns at a time go beside it
+            constexpr int PART = C::MX ? 64 : D;
+            const bool ends = t == t_end;
+            float* od = reinterpret_cast<float*>(!C::MX ? ring + st * C::STAGE : ends ? ring : sm + C::OFF_O + grp * C::GW * (kRows * PART * 4));
             float unit[D / 32];
 #pragma unroll
             for (int g = 0; g < D / 32; ++g)
                 unit[g] = (C::MX ? kv4::scale_of(__shfl_sync(~0u, unit4, 8 * g)) : ref) * kUnroom;
-            // column group i of row x lies at i ^ (x % 8)
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * D + (i ^ r) * 8 + 2 * c) =
-                        make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
             const Place place{it.c0, it.rt * kRows, it.h, rows};
-            if (t == t_end) {
+            const bool done = it.t0 >= t_begin;
+            // column group i of row x lies at i ^ (x % 8)
+            auto put = [&](int i0, int i1, int width) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    if (i >= i0 && i < i1)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * width + ((i - i0) ^ r) * 8 + 2 * c) =
+                                make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
+            };
+            if (ends) {
+                put(0, D / 8, D);
                 // the group's last: finished with the CTA's others
                 if (sub == 0 && lane == 0)
                     pieces[grp * 2 + 1] = Piece{it.t0, item_end, place, kStage, st};
                 break;
             }
-            group_sync(1 + grp, C::GW * 32);
-            const bool done = it.t0 >= t_begin;
-            for (int x = sub * 32 + lane; x < rows * (D / 4); x += C::GW * 32) {
-                const int row = x / (D / 4), col = x % (D / 4) * 4;
-                Sum sum;
 #pragma unroll
-                for (int w = 0; w < C::GW; ++w)
-                    sum.add(mls[(grp * C::GW + w) * kRows + row],
-                            *reinterpret_cast<const float4*>(od + (w * kRows + row) * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
-                if (done)
-                    store_row4(a, place, row, col, sum.v, finish(sum.m, sum.l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
-                else
-                    sum.to_slot(slot, D, row, col);
+            for (int p = 0; p < D / PART; ++p) {
+                if (p > 0)
+                    group_sync(1 + grp, C::GW * 32);
+                put(p * (PART / 8), (p + 1) * (PART / 8), PART);
+                group_sync(1 + grp, C::GW * 32);
+                for (int x = sub * 32 + lane; x < rows * (PART / 4); x += C::GW * 32) {
+                    const int row = x / (PART / 4), col = x % (PART / 4) * 4;
+                    Sum sum;
+#pragma unroll
+                    for (int w = 0; w < C::GW; ++w)
+                        sum.add(mls[(grp * C::GW + w) * kRows + row],
+                                *reinterpret_cast<const float4*>(od + (w * kRows + row) * PART + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+                    if (done)
+                        store_row4(a, place, row, p * PART + col, sum.v, finish(sum.m, sum.l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
+                    else
+                        sum.to_slot(slot, D, row, p * PART + col);
+                }
             }
             if (!done && sub == 0 && lane == 0)
                 pieces[grp * 2] = Piece{it.t0, item_end, place, kSlot, 0};
@@ -894,26 +907,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         const unsigned in_slot = __ballot_sync(~0u, of_it && own.where == kSlot);
         const int slot_at = in_slot ? (__ffs(in_slot) - 1) >> 1 : -1;
         // the warps whose results lie in their groups' stages, a lane each
-        const int piece_of = (lane & (kWarps - 1)) / C::GW * 2 + 1, stage = __shfl_sync(~0u, own.stage, piece_of);
+        const int piece_of = min(lane, C::WARPS - 1) / C::GW * 2 + 1, stage = __shfl_sync(~0u, own.stage, piece_of);
         const unsigned staged = __ballot_sync(~0u, of_it && own.where == kStage);
-        const unsigned warps = __ballot_sync(~0u, lane < kWarps && (staged >> piece_of & 1));
-        int ods[kWarps];
+        const unsigned warps = __ballot_sync(~0u, lane < C::WARPS && (staged >> piece_of & 1));
+        int ods[C::WARPS];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            ods[w] = C::MX ? C::OFF_O + w * (kRows * D * 4)
-                           : (w / C::GW * C::NS + __shfl_sync(~0u, stage, w)) * C::STAGE + w % C::GW * (kRows * D * 4);
+        for (int w = 0; w < C::WARPS; ++w)
+            ods[w] = (w / C::GW * C::NS + (C::MX ? 0 : __shfl_sync(~0u, stage, w))) * C::STAGE + w % C::GW * (kRows * D * 4);
         const bool done = t0 >= ct0 && t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
-        for (int x = tid; x < place.nrows * (D / 4); x += kThreads) {
+        for (int x = tid; x < place.nrows * (D / 4); x += C::THREADS) {
             const int row = x / (D / 4), col = x % (D / 4) * 4, at = row * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
             Sum sum;
             if (slot_at >= 0)
                 sum.from_slot(gslots + slot_at * slot_floats(), D, row, col);
             // all maxima first: the parts' weights then do not wait for one another
-            float2 ml[kWarps];
+            float2 ml[C::WARPS];
             float M = sum.m;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < C::WARPS; ++w) {
                 ml[w] = mls[w * kRows + row];
                 if (!(warps >> w & 1))
                     ml[w] = make_float2(kNone, 0.0f);
@@ -924,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
             sum.l *= keep;
             sum.v.x *= keep, sum.v.y *= keep, sum.v.z *= keep, sum.v.w *= keep;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
+            for (int w = 0; w < C::WARPS; ++w)
                 if (warps >> w & 1) {
                     const float4 y = *reinterpret_cast<const float4*>(sm + ods[w] + at * 4);
                     const float f = ex2(ml[w].x - M);
@@ -969,10 +981,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         // maxima and sums of every part and row, then their weights, in the ring; every 4
         // columns' parts are summed by `split` threads, then those.  The first parts are
         // on their way while the weights are worked out
-        const int K = cb - ca + 1, rows = place.nrows, n4 = rows * (D / 4), split = n4 <= kThreads / 2 ? kThreads / n4 : 1;
+        const int K = cb - ca + 1, rows = place.nrows, n4 = rows * (D / 4), split = n4 <= C::THREADS / 2 ? C::THREADS / n4 : 1;
         float2* part = reinterpret_cast<float2*>(sm);                    // [K][kRows]; .x becomes the weight
         float2* total = part + gridDim.x * kRows;                        // [kRows]
-        float4* acc = reinterpret_cast<float4*>(total + kRows);          // [kThreads]
+        float4* acc = reinterpret_cast<float4*>(total + kRows);          // [C::THREADS]
         auto slot_of = [&](int k) { return ws + ((i64)(ca + k) * 2 + (k == 0)) * slot_floats(); };
         constexpr int AHEAD = 8;
         float4 y[AHEAD];
@@ -984,11 +996,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
         };
         const int from = split > 1 ? tid / n4 : 0, x_first = split > 1 ? (from < split ? tid % n4 : n4) : tid;
         load_parts(x_first, from);
-        for (int i = tid; i < K * rows; i += kThreads)
+        for (int i = tid; i < K * rows; i += C::THREADS)
             part[i / rows * kRows + i % rows] = __ldcg(reinterpret_cast<const float2*>(slot_of(i / rows) + kRows * D + 2 * (i % rows)));
         __syncthreads();
         // a warp takes a row, its lanes the parts
-        for (int row = warp; row < rows; row += kWarps) {
+        for (int row = warp; row < rows; row += C::WARPS) {
             float M = kNone, L = 0.0f;
             for (int k = lane; k < K; k += 32)
                 M = fmaxf(M, part[k * kRows + row].x);
@@ -1008,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_attn_kernel(AttnArgs a, fl
                 total[row] = make_float2(M, L);
         }
         __syncthreads();
-        for (int x0 = 0; x0 < n4; x0 += kThreads) {
+        for (int x0 = 0; x0 < n4; x0 += C::THREADS) {
             const int x = x0 + x_first, row = x / (D / 4), col = x % (D / 4) * 4;
             float4 v = make_float4(0, 0, 0, 0);
             if (x0)
@@ -1060,7 +1072,7 @@ template <int D, int FMT, int BLK>
 void launch_one(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     unsigned* cnt = reinterpret_cast<unsigned*>(a.ws);
-    decode_attn_kernel<D, FMT, BLK><<<num_sms, kThreads, Decode<D, FMT, BLK>::smem(a.c.n_seqs), s>>>(
+    decode_attn_kernel<D, FMT, BLK><<<num_sms, Decode<D, FMT, BLK>::THREADS, Decode<D, FMT, BLK>::smem(a.c.n_seqs), s>>>(
         a, reinterpret_cast<float*>(a.ws + kCounterBytes), cnt);
 }
 
