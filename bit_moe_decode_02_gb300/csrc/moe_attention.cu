@@ -51,7 +51,7 @@ constexpr int kSub = 32;                  // tokens of a block that one warp tak
 typedef long long i64;
 
 // fp32 workspace: partial results of the groups' first and last items, then of the CTAs'.
-constexpr int kMaxGroups = 12;
+constexpr int kMaxGroups = 16;
 __host__ __device__ constexpr i64 slot_floats() { return kRows * 128 + 2 * kRows; }
 
 struct Item {
@@ -61,18 +61,19 @@ struct Item {
     int t0;              // its first tile
 };
 
-template <int BLK>
+template <int BLK, int R>
 __device__ __forceinline__ void block_range(const AttnArgs& a, int n, int len, int rt, int& jlo, int& jhi)
 {
-    const int r0 = rt * kRows, r1 = min(r0 + kRows, n * a.group) - 1;
+    const int r0 = rt * R, r1 = min(r0 + R, n * a.group) - 1;
     const int p0 = len - n + r0 / a.group, p1 = len - n + r1 / a.group;
     jhi = p1 / BLK;
     jlo = a.window > 0 && p0 >= a.window ? (p0 - a.window + 1) / BLK : 0;
 }
 
-__device__ __forceinline__ int row_tiles(const AttnArgs& a, int n) { return (n * a.group + kRows - 1) / kRows; }
+template <int R>
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, int n) { return (n * a.group + R - 1) / R; }
 
-template <int BLK>
+template <int BLK, int R>
 __device__ __forceinline__ i64 tiles_of(const AttnArgs& a, int b)
 {
     int c0, n, len;
@@ -82,16 +83,16 @@ __device__ __forceinline__ i64 tiles_of(const AttnArgs& a, int b)
     }
     i64 t = 0;
 #pragma unroll 1
-    for (int rt = 0, nrt = row_tiles(a, n); rt < nrt; ++rt) {
+    for (int rt = 0, nrt = row_tiles<R>(a, n); rt < nrt; ++rt) {
         int lo, hi;
-        block_range<BLK>(a, n, len, rt, lo, hi);
+        block_range<BLK, R>(a, n, len, rt, lo, hi);
         t += hi - lo + 1;
     }
     return t * a.c.H;
 }
 
 // Sequence b's item that holds tile t >= pre[b].
-template <int BLK>
+template <int BLK, int R>
 __device__ __forceinline__ void item_in(const AttnArgs& a, const int* pre, int b, int t, Item& it)
 {
     it.b = b;
@@ -99,7 +100,7 @@ __device__ __forceinline__ void item_in(const AttnArgs& a, const int* pre, int b
     int at = pre[b];
 #pragma unroll 1
     for (it.rt = 0;; ++it.rt) {
-        block_range<BLK>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+        block_range<BLK, R>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
         const int here = (it.jhi - it.jlo + 1) * a.c.H;
         if (t < at + here)
             break;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void item_in(const AttnArgs& a, const int* pre, int b
 }
 
 // The item that holds tile t, from the prefix sums of the sequences' tiles.
-template <int BLK>
+template <int BLK, int R>
 __device__ __forceinline__ void find_item(const AttnArgs& a, const int* pre, int t, Item& it)
 {
     int lo = 0, hi = a.c.n_seqs;
@@ -123,25 +124,25 @@ __device__ __forceinline__ void find_item(const AttnArgs& a, const int* pre, int
         else
             hi = mid;
     }
-    item_in<BLK>(a, pre, lo, t, it);
+    item_in<BLK, R>(a, pre, lo, t, it);
 }
 
-template <int BLK>
+template <int BLK, int R>
 __device__ __forceinline__ void next_item(const AttnArgs& a, const int* pre, Item& it)
 {
     it.t0 += it.jhi - it.jlo + 1;
     if (++it.h < a.c.H)
         return;
     it.h = 0;
-    if (++it.rt < row_tiles(a, it.n)) {
-        block_range<BLK>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
+    if (++it.rt < row_tiles<R>(a, it.n)) {
+        block_range<BLK, R>(a, it.n, it.len, it.rt, it.jlo, it.jhi);
         return;
     }
     int b = it.b + 1;
 #pragma unroll 1
     while (pre[b + 1] <= it.t0)
         ++b;
-    item_in<BLK>(a, pre, b, it.t0, it);
+    item_in<BLK, R>(a, pre, b, it.t0, it);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -211,19 +212,20 @@ struct Piece {
     int where, stage;
 };
 
-template <int D, int FMT, int BLK>
+template <int D, int FMT, int BLK, int R>
 struct Decode {
     static constexpr bool MX = FMT == MOE_KV_MXFP4;
-    static constexpr int WARPS = MX ? 12 : 8, THREADS = WARPS * 32;
+    static constexpr int WARPS = R == 8 ? 16 : MX ? 12 : 8, THREADS = WARPS * 32;
     static constexpr int GW = BLK / kSub;            // warps of a group
     static constexpr int NG = WARPS / GW;            // groups of a CTA
     static constexpr int RECORD = MX ? kv4::record(BLK, D) : BLK * D;  // bytes of K or V of a block
     static constexpr int STAGE = 2 * RECORD;         // bytes of a tile
-    // stages of a group's ring: 192 KB per CTA in all; MXFP4: 157 KB, and 64 columns of the warps'
-    // O where an item ends within a run (in 8 bits, and at a run's end, they go into the ring)
-    static constexpr int NS = D == 64 ? 6 : 3;
-    static constexpr int OFF_O = NG * NS * STAGE;                      // [WARPS][kRows][64] fp32
-    static constexpr int OFF_VS = OFF_O + (MX ? WARPS * kRows * 64 * 4 : 0);   // [WARPS][D / 32][kSub] f16
+    // stages of a group's ring: 192 KB per CTA in all; MXFP4: 157 KB (139 for items of 8 rows), and 64
+    // columns of the warps' O where an item ends within a run (in 8 bits, and at a run's end, they go
+    // into the ring)
+    static constexpr int NS = R == 8 ? (D == 64 ? 4 : 2) : D == 64 ? 6 : 3;
+    static constexpr int OFF_O = NG * NS * STAGE;                      // [WARPS][R][64] fp32
+    static constexpr int OFF_VS = OFF_O + (MX ? WARPS * R * 64 * 4 : 0);       // [WARPS][D / 32][kSub] f16
     static constexpr int OFF_HDR = OFF_VS + (MX ? WARPS * D * 2 : 0); // per stage: two scales, valid
     static constexpr int OFF_BAR = OFF_HDR + NG * NS * 16;
     static constexpr int OFF_ML = OFF_BAR + NG * NS * 16;              // full and empty barriers
@@ -241,9 +243,9 @@ struct Decode {
 //    of O are kept in.  Scales within [unit - 7, unit + 1] go as they are; where one is
 //    not, the unit moves to the largest, and what is more than 2^7 below goes in passes of
 //    its own, each with a unit of its own.
-template <int D, int BLK>
-__device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* scratch, const uint32_t (&qf)[D / 16][4], const float (&f)[2],
-                                        float (&o)[D / 8][4], float (&m)[2], float (&l)[2], int& unit, int& vmax, int p0, const int (&plo)[2],
+template <int D, int BLK, int R>
+__device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* scratch, const uint32_t (&qf)[D / 16][R / 4], const float (&f)[2],
+                                        float (&o)[D * R / 128][4], float (&m)[2], float (&l)[2], int& unit, int& vmax, int p0, const int (&plo)[2],
                                         const int (&phi)[2], bool whole, int any_lo, int any_hi)
 {
     constexpr int REC = kv4::record(BLK, D), G = D / 32, W = D / 32;       // W: words of a thread's codes of a key
@@ -267,17 +269,17 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
         const uint32_t x = (0x001c001cu - min2(top[h] - e2[h], 0x001c001cu)) << 10;
         ksc[h] = __byte_perm(x, 0, 0x1010);
         ksc[h + 2] = __byte_perm(x, 0, 0x3232);
-        // the exponents of the keys whose scores this thread holds: 8 c + 2 i + j
-        col[h][0] = __shfl_sync(~0u, top[h], 8 * c);
-        col[h][1] = __shfl_sync(~0u, top[h], 8 * c + 4);
+        if constexpr (R == 16) {
+            col[h][0] = __shfl_sync(~0u, top[h], 8 * c);
+            col[h][1] = __shfl_sync(~0u, top[h], 8 * c + 4);
+        }
     }
-    float s[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+    constexpr int OT = D * R / 128;
+    // a key's or a pair of keys' codes of this thread; the keys' own exponents, and those of the
+    // keys whose scores it holds: of 16 rows 8 c + 2 i + j, of 8 its own four
+    uint32_t w[4][W];
     {
         const uint8_t* kp = kt + (8 * (r >> 1) + (r & 1)) * (D / 2) + (D / 8) * c;
-        uint32_t w[4][W];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (D == 128) {
@@ -288,77 +290,161 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
                 w[i][0] = x.x, w[i][1] = x.y;
             }
         }
+    }
+    // P, as the second product's operand: of 16 rows pf[i / 2][i % 2 * 2 + e], of 8 pf[0][i], for the
+    // keys 8 c + 2 i, 8 c + 2 i + 1
+    uint32_t pf[2][4];
+    if constexpr (R == 8) {
+        // keys in the MMA's 16 rows, queries in its 8 columns
+        float s[4][2];                   // key 8 (r / 2) + 2 i + r % 2 by rows 2 c, 2 c + 1
+        {
+            float d[2][4];
 #pragma unroll
-        for (int ch = 0; ch < W; ++ch)
+            for (int i = 0; i < 2; ++i)
+                d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
+#pragma unroll
+            for (int ch = 0; ch < W; ++ch)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t x[4], y[4];
+                    kv4::to_f16(w[2 * i][ch], x);
+                    kv4::to_f16(w[2 * i + 1][ch], y);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const uint32_t ka[4] = {mul_f16(x[k], ksc[2 * i]), mul_f16(y[k], ksc[2 * i + 1]), mul_f16(x[k + 1], ksc[2 * i]),
+                                                mul_f16(y[k + 1], ksc[2 * i + 1])};
+                        mma16816(d[i], ka, qf[2 * ch + k / 2][0], qf[2 * ch + k / 2][1]);
+                    }
+                }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t h[4];
-                kv4::to_f16(w[i][ch], h);
-                mma16816(s[i], qf[2 * ch], mul_f16(h[0], ksc[i]), mul_f16(h[1], ksc[i]));
-                mma16816(s[i], qf[2 * ch + 1], mul_f16(h[2], ksc[i]), mul_f16(h[3], ksc[i]));
+                const uint32_t e = top[i & 1];
+                const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
+                s[i][0] = d[i / 2][i % 2 * 2] * (k * f[0]);
+                s[i][1] = d[i / 2][i % 2 * 2 + 1] * (k * f[1]);
             }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t e = col[i & 1][j];
-            const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
-            s[i][j] *= k * f[0];
-            s[i][2 + j] *= k * f[1];
         }
-    if (!whole) {
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int p = p0 + 8 * (r >> 1) + 2 * i + (r & 1);
+                    if (p < plo[e] || p > phi[e])
+                        s[i][e] = -INFINITY;
+                }
+        }
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            mx[e] = fmaxf(fmaxf(s[0][e], s[1][e]), fmaxf(s[2][e], s[3][e]));
+        if (__any_sync(~0u, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1)
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], k));
+                const float mn = fmaxf(m[e], mx[e]);
+                al[e] = ex2(m[e] - mn);
+                m[e] = mn;
+                l[e] *= al[e];
+            }
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+                o[i][0] *= al[0];
+                o[i][1] *= al[1];
+                o[i][2] *= al[0];
+                o[i][3] *= al[1];
+            }
+        }
+        const float mm[2] = {m[0] - kRoom, m[1] - kRoom};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = ex2(s[i][0] - mm[0]), y = ex2(s[i][1] - mm[1]);
+            l[0] += x;
+            l[1] += y;
+            // keys r by rows -> rows r by keys 2 c, 2 c + 1 of the eight, which are 8 c + 2 i and the next
+            asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pf[0][i]) : "r"(pack_f16(x, y)));
+            pf[1][i] = 0;
+        }
+    } else {
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+        {
+#pragma unroll
+            for (int ch = 0; ch < W; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h[4];
+                    kv4::to_f16(w[i][ch], h);
+                    mma16816(s[i], qf[2 * ch], mul_f16(h[0], ksc[i]), mul_f16(h[1], ksc[i]));
+                    mma16816(s[i], qf[2 * ch + 1], mul_f16(h[2], ksc[i]), mul_f16(h[3], ksc[i]));
+                }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int p = p0 + 8 * c + 2 * i + (k & 1), e = k >> 1;
-                if (p < plo[e] || p > phi[e])
-                    s[i][k] = -INFINITY;
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t e = col[i & 1][j];
+                const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
+                s[i][j] *= k * f[0];
+                s[i][2 + j] *= k * f[1];
             }
-    }
-    float mx[2] = {-INFINITY, -INFINITY};
+        if (!whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            mx[k >> 1] = fmaxf(mx[k >> 1], s[i][k]);
-    if (__any_sync(~0u, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
-        float al[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
-            const float mn = fmaxf(m[e], mx[e]);
-            al[e] = ex2(m[e] - mn);
-            m[e] = mn;
-            l[e] *= al[e];
+                for (int k = 0; k < 4; ++k) {
+                    const int p = p0 + 8 * c + 2 * i + (k & 1), e = k >> 1;
+                    if (p < plo[e] || p > phi[e])
+                        s[i][k] = -INFINITY;
+                }
         }
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= al[0];
-            o[i][1] *= al[0];
-            o[i][2] *= al[1];
-            o[i][3] *= al[1];
-        }
-    }
-    uint32_t pf[2][4];
-    {
-        const float mm[2] = {m[0] - kRoom, m[1] - kRoom};
-        float sum[2] = {0.0f, 0.0f};
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float p[4];
+            for (int k = 0; k < 4; ++k)
+                mx[k >> 1] = fmaxf(mx[k >> 1], s[i][k]);
+        if (__any_sync(~0u, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+            float al[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                p[k] = ex2(s[i][k] - mm[k >> 1]);
-                sum[k >> 1] += p[k];
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
+                mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
+                const float mn = fmaxf(m[e], mx[e]);
+                al[e] = ex2(m[e] - mn);
+                m[e] = mn;
+                l[e] *= al[e];
             }
-            pf[i >> 1][(i & 1) * 2] = pack_f16(p[0], p[1]);
-            pf[i >> 1][(i & 1) * 2 + 1] = pack_f16(p[2], p[3]);
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+                o[i][0] *= al[0];
+                o[i][1] *= al[0];
+                o[i][2] *= al[1];
+                o[i][3] *= al[1];
+            }
         }
-        l[0] += sum[0];
-        l[1] += sum[1];
+        {
+            const float mm[2] = {m[0] - kRoom, m[1] - kRoom};
+            float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = ex2(s[i][k] - mm[k >> 1]);
+                    sum[k >> 1] += p[k];
+                }
+                pf[i >> 1][(i & 1) * 2] = pack_f16(p[0], p[1]);
+                pf[i >> 1][(i & 1) * 2 + 1] = pack_f16(p[2], p[3]);
+            }
+            l[0] += sum[0];
+            l[1] += sum[1];
+        }
     }
 
     // V's scales: four tokens' bytes of one group a lane, those that no row sees left out
@@ -400,7 +486,7 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
                 for (int g = 0; g < G; ++g) {
                     const float ch = __shfl_sync(~0u, by, 8 * g);
 #pragma unroll
-                    for (int i = 4 * g; i < 4 * g + 4; ++i) {
+                    for (int i = OT / G * g; i < OT / G * (g + 1); ++i) {
                         o[i][0] *= ch;
                         o[i][1] *= ch;
                         o[i][2] *= ch;
@@ -430,9 +516,24 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
         for (int g = 0; g < G; ++g) {
             const uint4 z = *reinterpret_cast<const uint4*>(scratch + g * (kSub * 2) + c * 16);
             const uint4 w = *reinterpret_cast<const uint4*>(vt + (g * 32 + lane) * 16);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            if constexpr (R == 8) {
+                const uint32_t p[4] = {mul_f16(pf[0][0], z.x), mul_f16(pf[0][1], z.y), mul_f16(pf[0][2], z.z), mul_f16(pf[0][3], z.w)};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    uint32_t x[4], y[4];
+                    kv4::to_f16(words[e], x);
+                    kv4::to_f16(words[e + 1], y);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const uint32_t va[4] = {x[k], y[k], x[k + 1], y[k + 1]};
+                        mma16816(o[2 * g + e / 2], va, p[k], p[k + 1]);
+                    }
+                }
+                continue;
+            }
             const uint32_t pa[4] = {mul_f16(pf[0][0], z.x), mul_f16(pf[0][1], z.x), mul_f16(pf[0][2], z.y), mul_f16(pf[0][3], z.y)};
             const uint32_t pb[4] = {mul_f16(pf[1][0], z.z), mul_f16(pf[1][1], z.z), mul_f16(pf[1][2], z.w), mul_f16(pf[1][3], z.w)};
-            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 uint32_t h[4];
@@ -447,12 +548,12 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
     }
 }
 
-template <int D, int FMT, int BLK>
-__global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
+template <int D, int FMT, int BLK, int R>
+__global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_attn_kernel(AttnArgs a, float* ws, unsigned* cnt)
 {
-    using C = Decode<D, FMT, BLK>;
+    using C = Decode<D, FMT, BLK, R>;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ i64 scan[Decode<D, FMT, BLK>::WARPS];
+    __shared__ i64 scan[Decode<D, FMT, BLK, R>::WARPS];
     __shared__ int s_flag;
     int* pre = reinterpret_cast<int*>(sm + C::OFF_PRE);
     Piece* pieces = reinterpret_cast<Piece*>(sm + C::OFF_PIECE);
@@ -477,7 +578,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
 #pragma unroll 1
         for (int i = 0; i < per; ++i)
             if (per * tid + i < a.c.n_seqs)
-                sum += tiles_of<BLK>(a, per * tid + i);
+                sum += tiles_of<BLK, R>(a, per * tid + i);
         i64 incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -502,7 +603,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
             if (b < a.c.n_seqs) {
                 pre[b] = (int)at;
                 if (per > 1)
-                    at += tiles_of<BLK>(a, b);
+                    at += tiles_of<BLK, R>(a, b);
             }
         }
         if (tid == 0)
@@ -534,7 +635,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
     int at = lane == 0 ? ct0 : lane == 1 ? ct1 : t_begin;
 #pragma unroll 1
     for (bool again = false;; again = true) {
-        find_item<BLK>(a, pre, min(at, N - 1), it);
+        find_item<BLK, R>(a, pre, min(at, N - 1), it);
         if (again)
             break;
         const int end = at < N && it.jhi - it.jlo + 1 <= C::WHOLE ? it.t0 : at, guess = t_begin;
@@ -592,7 +693,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
         __syncwarp();
         if (++pt < t_end) {
             if (++pj > pit.jhi) {
-                next_item<BLK>(a, pre, pit);
+                next_item<BLK, R>(a, pre, pit);
                 pj = pit.jlo;
             }
             pid = table_at(pit, pj);     // used by the next call, a tile later
@@ -620,19 +721,25 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
         while (t < t_end) {
             // ---- an item, or the part of it in this group's run
             const int item_end = it.t0 + it.jhi - it.jlo + 1, seg_end = min(item_end, t_end);
-            const int rows = min(kRows, it.n * a.group - it.rt * kRows);
-            uint32_t qf[D / 16][4];
+            const int rows = min(R, it.n * a.group - it.rt * R);
+            // this thread's two rows: r and r + 8 of 16, 2 c and 2 c + 1 of 8
+            auto my_row = [&](int e) { return R == 8 ? 2 * c + e : r + 8 * e; };
+            uint32_t qf[D / 16][R / 4];
             float f[2];                  // score = sum * block's scale * f
-            int plo[2], phi[2];          // first and last visible position of this thread's two rows
-            uint32_t qw[2][D / 64][8];
+            int plo[2], phi[2];          // first and last visible position of the rows
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = it.rt * kRows + r + 8 * e, i = row / a.group;
-                const bool in = r + 8 * e < rows;
-                phi[e] = in ? it.len - it.n + i : -1;
+                const bool in = my_row(e) < rows;
+                phi[e] = in ? it.len - it.n + (it.rt * R + my_row(e)) / a.group : -1;
                 plo[e] = in && a.window > 0 ? phi[e] - a.window + 1 : 0;
+            }
+            constexpr int QR = R / 8;    // rows whose queries this thread holds a part of: r (and r + 8)
+            uint32_t qw[QR][D / 64][8];
+#pragma unroll
+            for (int e = 0; e < QR; ++e) {
+                const int row = it.rt * R + r + 8 * e, i = row / a.group;
                 uint32_t (&w)[D / 64][8] = qw[e];
-                if (in) {
+                if (r + 8 * e < rows) {
                     // which of the d's a thread takes: those of its 16 bytes of K's codes
                     constexpr int mine = C::MX ? D / 4 : 16, step = C::MX ? 16 : 64;
                     const uint16_t* q = a.q + (i64)(it.c0 + i) * a.q_stride + (i64)(it.h * a.group + row % a.group) * D + mine * c;
@@ -654,7 +761,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
             fill(t);
             {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < QR; ++e) {
                     uint32_t big = 0;    // largest finite magnitude of the row
 #pragma unroll
                     for (int ch = 0; ch < D / 64; ++ch)
@@ -669,12 +776,18 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
                     for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            qf[ch * 4 + k / 2][(k & 1) * 2 + e] = scale_pair(qw[e][ch][k], rs);
+                            qf[ch * 4 + k / 2][(k & 1) * QR + e] = scale_pair(qw[e][ch][k], rs);
+                }
+                if constexpr (R == 8) {
+                    const float mine = f[0];
+                    f[0] = __shfl_sync(~0u, mine, 8 * c);
+                    f[1] = __shfl_sync(~0u, mine, 8 * c + 4);
                 }
             }
-            float o[D / 8][4], m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+            constexpr int OT = D * R / 128;      // tiles of O: 16 rows by 8 columns, or 16 columns by 8 rows
+            float o[OT][4], m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int i = 0; i < OT; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     o[i][k] = 0.0f;
@@ -683,11 +796,11 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
             // in the lanes that look after g's bytes
             int unit4 = 0, vmax4 = 0;
             // positions that every row of the tile sees
-            const int all_lo = a.window > 0 ? it.len - it.n + (it.rt * kRows + rows - 1) / a.group - a.window + 1 : 0;
-            const int all_hi = it.len - it.n + it.rt * kRows / a.group;
+            const int all_lo = a.window > 0 ? it.len - it.n + (it.rt * R + rows - 1) / a.group - a.window + 1 : 0;
+            const int all_hi = it.len - it.n + it.rt * R / a.group;
             // and that any does
             const int any_lo = a.window > 0 ? all_hi - a.window + 1 : 0;
-            const int any_hi = it.len - it.n + (it.rt * kRows + rows - 1) / a.group;
+            const int any_hi = it.len - it.n + (it.rt * R + rows - 1) / a.group;
 
             int st = 0;
             for (; t < seg_end; ++t, ++j) {
@@ -702,11 +815,11 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
                 const uint8_t* kt = ring + st * C::STAGE + sub * kSub * D;
                 const uint8_t* vt = ring + st * C::STAGE + BLK * D + sub * kSub;
                 const int p0 = j * BLK + sub * kSub;     // position of this warp's first token
-                if (C::MX && hd.z != 0.0f) {
-                    if constexpr (C::MX)
-                        mx_tile<D, BLK>(ring + st * C::STAGE, sub, reinterpret_cast<uint8_t*>(sm + C::OFF_VS) + warp * (D * 2), qf, f, o, m, l,
+                if constexpr (C::MX) {
+                    if (hd.z != 0.0f)
+                        mx_tile<D, BLK, R>(ring + st * C::STAGE, sub, reinterpret_cast<uint8_t*>(sm + C::OFF_VS) + warp * (D * 2), qf, f, o, m, l,
                                         unit4, vmax4, p0, plo, phi, p0 >= all_lo && p0 + kSub - 1 <= all_hi, any_lo, any_hi);
-                } else if (!C::MX && hd.z != 0.0f) {
+                } else if (hd.z != 0.0f) {
                     float s[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -823,32 +936,49 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
             // ---- join the group's warps in the stage they have just read
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(~0u, l[e], 1);
-                l[e] += __shfl_xor_sync(~0u, l[e], 2);
-                if (c == 0)
-                    mls[warp * kRows + r + 8 * e] = make_float2(m[e], l[e] * kUnroom);
+                if constexpr (R == 8) {
+                    l[e] += __shfl_xor_sync(~0u, l[e], 4);
+                    l[e] += __shfl_xor_sync(~0u, l[e], 8);
+                    l[e] += __shfl_xor_sync(~0u, l[e], 16);
+                } else {
+                    l[e] += __shfl_xor_sync(~0u, l[e], 1);
+                    l[e] += __shfl_xor_sync(~0u, l[e], 2);
+                }
+                if ((R == 8 ? r : c) == 0)
+                    mls[warp * kRows + my_row(e)] = make_float2(m[e], l[e] * kUnroom);
             }
             group_sync(1 + grp, C::GW * 32);
             // MXFP4: at a run's end nothing of the ring is wanted any more, and it holds all of O; else 64
             // columns at a time go beside it
             constexpr int PART = C::MX ? 64 : D;
             const bool ends = t == t_end;
-            float* od = reinterpret_cast<float*>(!C::MX ? ring + st * C::STAGE : ends ? ring : sm + C::OFF_O + grp * C::GW * (kRows * PART * 4));
+            float* od = reinterpret_cast<float*>(!C::MX ? ring + st * C::STAGE : ends ? ring : sm + C::OFF_O + grp * C::GW * (R * PART * 4));
             float unit[D / 32];
 #pragma unroll
             for (int g = 0; g < D / 32; ++g)
                 unit[g] = (C::MX ? kv4::scale_of(__shfl_sync(~0u, unit4, 8 * g)) : ref) * kUnroom;
-            const Place place{it.c0, it.rt * kRows, it.h, rows};
+            const Place place{it.c0, it.rt * R, it.h, rows};
             const bool done = it.t0 >= t_begin;
             // column group i of row x lies at i ^ (x % 8)
             auto put = [&](int i0, int i1, int width) {
+                if constexpr (R == 8) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    if (i >= i0 && i < i1)
+                    for (int i = 0; i < OT; ++i)
+                        if (2 * i >= i0 && 2 * i < i1)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2*>(od + (sub * kRows + r + 8 * e) * width + ((i - i0) ^ r) * 8 + 2 * c) =
-                                make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
+                            for (int k = 0; k < 4; ++k) {
+                                const int row = 2 * c + (k & 1);
+                                od[(sub * R + row) * width + ((2 * i + (k >> 1) - i0) ^ row) * 8 + r] = o[i][k] * unit[i / 2];
+                            }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < OT; ++i)
+                        if (i >= i0 && i < i1)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<float2*>(od + (sub * R + r + 8 * e) * width + ((i - i0) ^ r) * 8 + 2 * c) =
+                                    make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
+                }
             };
             if (ends) {
                 put(0, D / 8, D);
@@ -869,7 +999,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
 #pragma unroll
                     for (int w = 0; w < C::GW; ++w)
                         sum.add(mls[(grp * C::GW + w) * kRows + row],
-                                *reinterpret_cast<const float4*>(od + (w * kRows + row) * PART + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+                                *reinterpret_cast<const float4*>(od + (w * R + row) * PART + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
                     if (done)
                         store_row4(a, place, row, p * PART + col, sum.v, finish(sum.m, sum.l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
                     else
@@ -882,7 +1012,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
             group_sync(1 + grp, C::GW * 32);
             if (lane == 0)
                 tc::mbar_arrive(empty + st);
-            next_item<BLK>(a, pre, it);
+            next_item<BLK, R>(a, pre, it);
             j = it.jlo;
         }
     }
@@ -913,7 +1043,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
         int ods[C::WARPS];
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w)
-            ods[w] = (w / C::GW * C::NS + (C::MX ? 0 : __shfl_sync(~0u, stage, w))) * C::STAGE + w % C::GW * (kRows * D * 4);
+            ods[w] = (w / C::GW * C::NS + (C::MX ? 0 : __shfl_sync(~0u, stage, w))) * C::STAGE + w % C::GW * (R * D * 4);
         const bool done = t0 >= ct0 && t1 <= ct1;
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += C::THREADS) {
@@ -1052,39 +1182,52 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK>::THREADS), 1) decode_attn
     }
 }
 
-template <int D, int FMT, int BLK>
+template <int D, int FMT, int BLK, int R>
 cudaError_t prepare_one()
 {
-    return cudaFuncSetAttribute(decode_attn_kernel<D, FMT, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Decode<D, FMT, BLK>::smem(kMaxSeqs));
+    return cudaFuncSetAttribute(decode_attn_kernel<D, FMT, BLK, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Decode<D, FMT, BLK, R>::smem(kMaxSeqs));
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int R>
 cudaError_t prepare_blocks()
 {
     cudaError_t e;
-    if ((e = prepare_one<D, FMT, 32>()) != cudaSuccess || (e = prepare_one<D, FMT, 64>()) != cudaSuccess)
+    if ((e = prepare_one<D, FMT, 32, R>()) != cudaSuccess || (e = prepare_one<D, FMT, 64, R>()) != cudaSuccess)
         return e;
-    return prepare_one<D, FMT, 128>();
+    return prepare_one<D, FMT, 128, R>();
 }
 
-template <int D, int FMT, int BLK>
+template <int D, int FMT, int BLK, int R>
 void launch_one(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     unsigned* cnt = reinterpret_cast<unsigned*>(a.ws);
-    decode_attn_kernel<D, FMT, BLK><<<num_sms, Decode<D, FMT, BLK>::THREADS, Decode<D, FMT, BLK>::smem(a.c.n_seqs), s>>>(
+    decode_attn_kernel<D, FMT, BLK, R><<<num_sms, Decode<D, FMT, BLK, R>::THREADS, Decode<D, FMT, BLK, R>::smem(a.c.n_seqs), s>>>(
         a, reinterpret_cast<float*>(a.ws + kCounterBytes), cnt);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int R>
 void launch_blocks(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     if (a.c.blk == 32)
-        launch_one<D, FMT, 32>(a, num_sms, s);
+        launch_one<D, FMT, 32, R>(a, num_sms, s);
     else if (a.c.blk == 64)
-        launch_one<D, FMT, 64>(a, num_sms, s);
+        launch_one<D, FMT, 64, R>(a, num_sms, s);
     else
-        launch_one<D, FMT, 128>(a, num_sms, s);
+        launch_one<D, FMT, 128, R>(a, num_sms, s);
+}
+
+template <int D>
+void launch_format(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    if (a.c.fmt == MOE_KV_E4M3)
+        return launch_blocks<D, MOE_KV_E4M3, 16>(a, num_sms, s);
+    if (a.c.fmt == MOE_KV_INT8)
+        return launch_blocks<D, MOE_KV_INT8, 16>(a, num_sms, s);
+    // eight rows at most for a sequence's kv head, on average: queries in an MMA's columns, not its rows
+    if ((long long)a.c.n_tokens * a.group <= 8ll * a.c.n_seqs)
+        return launch_blocks<D, MOE_KV_MXFP4, 8>(a, num_sms, s);
+    launch_blocks<D, MOE_KV_MXFP4, 16>(a, num_sms, s);
 }
 
 }  // namespace
@@ -1097,23 +1240,21 @@ size_t attention_workspace_bytes(int num_sms)
 cudaError_t prepare_attention_kernels()
 {
     cudaError_t e;
-    if ((e = prepare_blocks<64, MOE_KV_E4M3>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_INT8>()) != cudaSuccess ||
-        (e = prepare_blocks<128, MOE_KV_E4M3>()) != cudaSuccess)
+    if ((e = prepare_blocks<64, MOE_KV_E4M3, 16>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_INT8, 16>()) != cudaSuccess ||
+        (e = prepare_blocks<128, MOE_KV_E4M3, 16>()) != cudaSuccess || (e = prepare_blocks<128, MOE_KV_INT8, 16>()) != cudaSuccess)
         return e;
-    if ((e = prepare_blocks<128, MOE_KV_INT8>()) != cudaSuccess || (e = prepare_blocks<64, MOE_KV_MXFP4>()) != cudaSuccess ||
-        (e = prepare_blocks<128, MOE_KV_MXFP4>()) != cudaSuccess)
+    if ((e = prepare_blocks<64, MOE_KV_MXFP4, 16>()) != cudaSuccess || (e = prepare_blocks<128, MOE_KV_MXFP4, 16>()) != cudaSuccess ||
+        (e = prepare_blocks<64, MOE_KV_MXFP4, 8>()) != cudaSuccess || (e = prepare_blocks<128, MOE_KV_MXFP4, 8>()) != cudaSuccess)
         return e;
     return prepare_prompt_kernels();
 }
 
 static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
-    if (a.c.fmt == MOE_KV_MXFP4)
-        a.c.D == 64 ? launch_blocks<64, MOE_KV_MXFP4>(a, num_sms, s) : launch_blocks<128, MOE_KV_MXFP4>(a, num_sms, s);
-    else if (a.c.D == 64)
-        a.c.fmt == MOE_KV_E4M3 ? launch_blocks<64, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<64, MOE_KV_INT8>(a, num_sms, s);
+    if (a.c.D == 64)
+        launch_format<64>(a, num_sms, s);
     else
-        a.c.fmt == MOE_KV_E4M3 ? launch_blocks<128, MOE_KV_E4M3>(a, num_sms, s) : launch_blocks<128, MOE_KV_INT8>(a, num_sms, s);
+        launch_format<128>(a, num_sms, s);
     return cudaGetLastError();
 }
 

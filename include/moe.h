@@ -435,7 +435,7 @@ void moe_destroy(moe_handle* h);
 
 typedef struct moe_ops moe_ops;
 
-/* A handle on the current device: allocates the workspace (17.7 MB on 152 SMs,
+/* A handle on the current device: allocates the workspace (22.7 MB on 152 SMs,
  * whatever the sizes of later calls). */
 int moe_ops_create(moe_ops** out);
 
