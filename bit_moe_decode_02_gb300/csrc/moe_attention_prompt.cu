@@ -56,6 +56,7 @@ template <int D, int FMT, int BLK>
 struct Layout {
     static constexpr bool MX = FMT == MOE_KV_MXFP4;
     static constexpr int NB = kKeys / BLK;                // cache blocks of a tile
+    static constexpr int CONVERT = MX ? 6 : 4;            // warps that make codes f16: the last of warps 0 to 7
     static constexpr int OP = kKeys * D * 2;              // bytes of an f16 operand: Q tile, K tile, V tile
     static constexpr int REC = MX ? kv4::record(BLK, D) : BLK * D;     // bytes of a block's K or V
     static constexpr int RAW = NB * REC;                  // bytes of a tile's K or V codes
@@ -243,34 +244,43 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
     };
     const int g = r * 4 * N / 32, t4 = r * 4 * N % 32;    // V: this lane's group, its first key of the 32
     int unit = 28, vmax = 28;                             // of group g
-    int id = block_of(0);
+    // block numbers two tiles ahead, scales one
+    int id = block_of(0), next = block_of(1);
     Scales z = scales_of(id);
     int t = 0;
 #pragma unroll 1
     for (int tile = 0; tile < nt; ++tile) {
-        const int next = block_of(tile + 1);
+        const int after = block_of(tile + 2);
+        const Scales zn = scales_of(next);
         const int base = (tile0 + tile) * kKeys, here = base + 32 * sub;
         const bool block = __shfl_sync(~0u, id, sub * 32 / BLK) >= 0;
+        const bool seen = __all_sync(~0u, block) && base >= see_lo && base + kKeys - 1 <= see_hi;       // every key, by some row
+        uint32_t vb[N];
         int ke[4];                                        // a key's largest scale byte, -1: no row sees it
+        {
+            uint32_t even = 0, odd = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = here + 8 * (r >> 1) + 2 * i + (r & 1);
-            int e = 0;
+            for (int x = 0; x < N; ++x) {
+                even = max2(even, z.k[x] & 0x00ff00ffu);
+                odd = max2(odd, z.k[x] >> 8 & 0x00ff00ffu);
+                vb[x] = z.v[x];
+            }
+            ke[0] = even & 0xffffu, ke[1] = odd & 0xffffu, ke[2] = even >> 16, ke[3] = odd >> 16;
+        }
+        if (!seen) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = here + 8 * (r >> 1) + 2 * i + (r & 1);
+                ke[i] = block && p >= see_lo && p <= see_hi ? ke[i] : -1;
+            }
 #pragma unroll
             for (int x = 0; x < N; ++x)
-                e = max(e, (int)(z.k[x] >> 8 * i & 0xff));
-            ke[i] = block && p >= see_lo && p <= see_hi ? e : -1;
-        }
-        uint32_t vb[N];
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-            vb[x] = z.v[x];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int p = here + t4 + 4 * x + k;
-                if (p < see_lo || p > see_hi)
-                    vb[x] &= ~(0xffu << 8 * k);
-            }
+                for (int k = 0; k < 4; ++k) {
+                    const int p = here + t4 + 4 * x + k;
+                    if (p < see_lo || p > see_hi)
+                        vb[x] &= ~(0xffu << 8 * k);
+                }
         }
         const uint8_t* src = a.c.codes + ((long long)id * a.c.H + w.h) * 2 * L::REC;
         const int n = __popc(__ballot_sync(~0u, id >= 0));
@@ -300,10 +310,21 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
                 for (int x = 0; x < N; ++x)
                     left[x] = vb[x];
             }
-            int big = 0;
+            int big, small;                               // of the scales left, but 0
+            {
+                uint32_t top = 0, low = ~0u;
 #pragma unroll
-            for (int x = 0; x < N; ++x)
-                big = max(max(big, max((int)(left[x] & 0xff), (int)(left[x] >> 8 & 0xff))), max((int)(left[x] >> 16 & 0xff), (int)(left[x] >> 24)));
+                for (int x = 0; x < N; ++x) {
+                    const uint32_t e = left[x] & 0x00ff00ffu, o = left[x] >> 8 & 0x00ff00ffu;
+                    uint32_t e1, o1;                      // 0 becomes the largest
+                    asm("add.u16x2 %0, %1, %2;" : "=r"(e1) : "r"(e), "r"(0xffffffffu));
+                    asm("add.u16x2 %0, %1, %2;" : "=r"(o1) : "r"(o), "r"(0xffffffffu));
+                    top = max2(top, max2(e, o));
+                    low = min2(low, min2(e1, o1));
+                }
+                big = max(top & 0xffffu, top >> 16);
+                small = min(low & 0xffffu, low >> 16) + 1;
+            }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
                 if (o < 8 / G || o >= 8)
@@ -314,17 +335,19 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
                 unit = min(max(max(big + 1, vmax - 64), 28), 254);
             const int field = big > 0 ? min(done - unit, 0) + 28 : 0;
             bool more = false;
+            if (__any_sync(~0u, small <= unit - 28)) {
 #pragma unroll
-            for (int x = 0; x < N; ++x) {
-                uint32_t keep = 0;
+                for (int x = 0; x < N; ++x) {
+                    uint32_t keep = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int b = left[x] >> 8 * k & 0xff;
-                    if (b > 0 && b <= unit - 28 && b > vmax - 92)
-                        keep |= 0xffu << 8 * k;
+                    for (int k = 0; k < 4; ++k) {
+                        const int b = left[x] >> 8 * k & 0xff;
+                        if (b > 0 && b <= unit - 28 && b > vmax - 92)
+                            keep |= 0xffu << 8 * k;
+                    }
+                    left[x] &= keep;
+                    more |= keep != 0;
                 }
-                left[x] &= keep;
-                more |= keep != 0;
             }
             uint32_t bits = 0;
 #pragma unroll
@@ -362,7 +385,8 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
             ++t;
         } while (again_k || again_v);
         id = next;
-        z = scales_of(id);
+        next = after;
+        z = zn;
     }
 }
 
@@ -395,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(raw_full + i, 1);
-            tc::mbar_init(raw_empty + i, 4);
-            tc::mbar_init(k_full + i, 4);
+            tc::mbar_init(raw_empty + i, L::CONVERT);
+            tc::mbar_init(k_full + i, L::CONVERT);
             tc::mbar_init(k_empty + i, na);
-            tc::mbar_init(v_full + i, 4);
+            tc::mbar_init(v_full + i, L::CONVERT);
             tc::mbar_init(v_empty + i, na);
             tc::mbar_init(s_full + i, 1);
             tc::mbar_init(p_full + i, 8);
@@ -523,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             if (last)
                 break;
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 8 - L::CONVERT && warp < 8) {
         // ---- codes -> f16 operands (zero where there is no block)
         const int ct = tid - 128;
         const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -544,31 +568,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             if (t >= 2)
                 tc::mbar_wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
             if constexpr (L::MX) {
-                // K: this thread's token, a group's 16 bytes at a time in an order that spreads the banks
+                // K: a key a lane, a group's 16 bytes of it at a time in an order that spreads the banks
                 const Pass& p = passes[t % kRing];
-                const uint8_t* rec = sm + L::OFF_RAW + ct / BLK * L::REC;
-                uint8_t* out = sm + L::OFF_K + st * L::OP + (ct >> 3) * (D * 16) + (ct & 7) * 16;
-                const bool have = p.keys[ct >> 5] >> (ct & 31) & 1;
-                uint4 w[D / 32];
-                uint32_t z[D / 32];
+                const int kref = p.kref;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int g = (i + ct / (256 / D)) & (D / 32 - 1);
-                    w[i] = *reinterpret_cast<const uint4*>(rec + ct % BLK * (D / 2) + 16 * g);
+                for (int i = 0; i < (D / 8 + L::CONVERT - 1) / L::CONVERT; ++i) {
+                    const int u = i * L::CONVERT + warp - (8 - L::CONVERT);                // of 4 times 32 keys and D / 32 groups
+                    if (u >= D / 8)
+                        break;
+                    const int key = u / (D / 32) * 32 + lane, g = (u + lane / (256 / D)) & (D / 32 - 1);
+                    const uint8_t* rec = sm + L::OFF_RAW + key / BLK * L::REC;
+                    const uint4 w = *reinterpret_cast<const uint4*>(rec + key % BLK * (D / 2) + 16 * g);
                     // 2^(13 + 127 + e - kref) in f16, with its subnormal numbers
-                    const int e = rec[BLK * D / 2 + kv4::k_scale_at<D>(ct % BLK, g)];
-                    const float f = have ? __uint_as_float((uint32_t)max(e - p.kref + 140, 0) << 23) : 0.0f;
-                    z[i] = pack_f16(f, f);
-                }
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int g = (i + ct / (256 / D)) & (D / 32 - 1);
-                    const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    const int e = rec[BLK * D / 2 + kv4::k_scale_at<D>(key % BLK, g)];
+                    const bool have = p.keys[key >> 5] >> lane & 1;
+                    const float f = have ? __uint_as_float((uint32_t)max(e - kref + 140, 0) << 23) : 0.0f;
+                    const uint32_t z = pack_f16(f, f), words[4] = {w.x, w.y, w.z, w.w};
+                    uint8_t* out = sm + L::OFF_K + st * L::OP + (key >> 3) * (D * 16) + (key & 7) * 16 + 512 * g;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t h[4];
                         kv4::to_f16(words[k], h);
-                        *reinterpret_cast<uint4*>(out + 512 * g + 128 * k) = make_uint4(mul_f16(h[0], z[i]), mul_f16(h[1], z[i]), mul_f16(h[2], z[i]), mul_f16(h[3], z[i]));
+                        *reinterpret_cast<uint4*>(out + 128 * k) = make_uint4(mul_f16(h[0], z), mul_f16(h[1], z), mul_f16(h[2], z), mul_f16(h[3], z));
                     }
                 }
             } else {
@@ -601,10 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             if constexpr (L::MX) {
                 // V: eight tokens of four d's at a time, as the record's words lie
                 const Pass& p = passes[t % kRing];
-                const int cw = ct >> 5, r = lane >> 2, c = lane & 3;
+                const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int sub = i * 4 / (D / 32) + cw / (D / 32), g = (i * 4 + cw) % (D / 32);
+                for (int i = 0; i < (D / 8 + L::CONVERT - 1) / L::CONVERT; ++i) {
+                    const int u = i * L::CONVERT + warp - (8 - L::CONVERT);
+                    if (u >= D / 8)
+                        break;
+                    const int sub = u / (D / 32), g = u % (D / 32);
                     const uint8_t* rec = sm + L::OFF_RAW + L::RAW + sub * 32 / BLK * L::REC;
                     const int in = sub * 32 % BLK / 32 * (D / 32) + g;
                     const uint4 w = *reinterpret_cast<const uint4*>(rec + (in * 32 + lane) * 16);
