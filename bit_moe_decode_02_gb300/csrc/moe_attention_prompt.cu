@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             if constexpr (L::MX) {
                 // V: eight tokens of four d's at a time, as the record's words lie
                 const Pass& p = passes[t % kRing];
-                const int r = lane >> 2, c = lane & 3;
+                // (r, c) so that eight lanes meet in no bank, neither loading nor storing
+                const int r = lane & 7, c = ((r >> 1) + (lane >> 3)) & 3;
 #pragma unroll
                 for (int i = 0; i < (D / 8 + L::CONVERT - 1) / L::CONVERT; ++i) {
                     const int u = i * L::CONVERT + warp - (8 - L::CONVERT);
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     const int sub = u / (D / 32), g = u % (D / 32);
                     const uint8_t* rec = sm + L::OFF_RAW + L::RAW + sub * 32 / BLK * L::REC;
                     const int in = sub * 32 % BLK / 32 * (D / 32) + g;
-                    const uint4 w = *reinterpret_cast<const uint4*>(rec + (in * 32 + lane) * 16);
+                    const uint4 w = *reinterpret_cast<const uint4*>(rec + (in * 32 + r * 4 + c) * 16);
                     const uint2 b = *reinterpret_cast<const uint2*>(rec + BLK * D / 2 + in * 32 + 8 * c);
                     // 2^(13 + e - unit): exponent field e - unit + 28, where that is 1 to 28
                     const uint32_t base = (uint32_t)(p.unit[g] - 28) * 0x10001u, top = (uint32_t)p.most[g];
