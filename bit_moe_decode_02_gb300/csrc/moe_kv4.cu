@@ -262,12 +262,12 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, float s)
 // both go out by token.
 template <int D, int blk>
 __global__ void __launch_bounds__(kThreads)
-kv4_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vdst, long long kstride, long long vstride)
+kv4_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vdst, long long kstride, long long vstride, int heads_per_cta)
 {
     __shared__ uint32_t codes[blk * (D / 8 + 1)];
     __shared__ Found found;
     constexpr int W = D / 8, REC = kv4::record(blk, D);
-    const int tid = threadIdx.x, h = blockIdx.y;
+    const int tid = threadIdx.x;
     kv::Touched t;
     if (!find(c, blockIdx.x, found, t))
         return;
@@ -277,32 +277,57 @@ kv4_read_kernel(KvView c, uint16_t* __restrict__ kdst, uint16_t* __restrict__ vd
     const int start = t.len - t.n - t.j * blk;
     const int lo = start > 0 ? start : 0, hi = min(t.len - t.j * blk, blk), n = hi - lo;
     const long long row0 = t.c0 - start + lo;
-    const uint8_t* kr = c.codes + ((long long)id * c.H + h) * 2 * REC;
-    const uint8_t* vr = kr + REC;
-    const int t8lo = lo / 8, nt8 = (hi + 7) / 8 - t8lo;
-    for (int i = tid; i < nt8 * W; i += kThreads) {
-        const int x = i % W, t8 = t8lo + i / W;
-        uint32_t w[8];
+    const int t8lo = lo / 8, nt8 = (hi + 7) / 8 - t8lo, h1 = min((int)(blockIdx.y + 1) * heads_per_cta, c.H);
+    for (int h = blockIdx.y * heads_per_cta; h < h1; ++h) {
+        const uint8_t* kr = c.codes + ((long long)id * c.H + h) * 2 * REC;
+        const uint8_t* vr = kr + REC;
+        // all of a thread's words of K, and its share of V's, are on their way before the first is used
+        constexpr int kK = (blk * W + kThreads - 1) / kThreads, kV = (blk / 8 * W + kThreads - 1) / kThreads;
+        uint32_t kw[kK], vw[kV][8];
+        uint8_t kb[kK], vb[kK];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            w[r] = reinterpret_cast<const uint32_t*>(vr)[kv4::v_word_at<D>(t8, x / 4, x % 4, r)];
-        kv4::transpose(w);
+        for (int j = 0; j < kV; ++j) {
+            const int i = tid + j * kThreads, x = i % W, t8 = t8lo + i / W;
+            if (i < nt8 * W)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            codes[(t8 * 8 + k) * (W + 1) + x] = w[k];
-    }
-    kdst += row0 * kstride + (long long)h * D;
-    vdst += row0 * vstride + (long long)h * D;
-    for (int i = tid; i < n * W; i += kThreads) {
-        const int x = i % W, r = i / W, tok = lo + r;
-        const uint32_t w = reinterpret_cast<const uint32_t*>(kr)[tok * W + x];
-        *reinterpret_cast<uint4*>(kdst + r * kstride + x * 8) = decode8(w, kv4::scale_of(kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)]));
-    }
-    __syncthreads();
-    for (int i = tid; i < n * W; i += kThreads) {
-        const int x = i % W, r = i / W, tok = lo + r;
-        *reinterpret_cast<uint4*>(vdst + r * vstride + x * 8) =
-            decode8(codes[tok * (W + 1) + x], kv4::scale_of(vr[blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)]));
+                for (int r = 0; r < 8; ++r)
+                    vw[j][r] = reinterpret_cast<const uint32_t*>(vr)[kv4::v_word_at<D>(t8, x / 4, x % 4, r)];
+        }
+#pragma unroll
+        for (int j = 0; j < kK; ++j) {
+            const int i = tid + j * kThreads, x = i % W, tok = lo + i / W;
+            if (i < n * W) {
+                kw[j] = reinterpret_cast<const uint32_t*>(kr)[tok * W + x];
+                kb[j] = kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)];
+                vb[j] = vr[blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int i = tid + j * kThreads, x = i % W, t8 = t8lo + i / W;
+            if (i < nt8 * W) {
+                kv4::transpose(vw[j]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    codes[(t8 * 8 + k) * (W + 1) + x] = vw[j][k];
+            }
+        }
+        uint16_t* const kd = kdst + row0 * kstride + (long long)h * D;
+        uint16_t* const vd = vdst + row0 * vstride + (long long)h * D;
+#pragma unroll
+        for (int j = 0; j < kK; ++j) {
+            const int i = tid + j * kThreads, x = i % W, r = i / W;
+            if (i < n * W)
+                *reinterpret_cast<uint4*>(kd + r * kstride + x * 8) = decode8(kw[j], kv4::scale_of(kb[j]));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kK; ++j) {
+            const int i = tid + j * kThreads, x = i % W, r = i / W;
+            if (i < n * W)
+                *reinterpret_cast<uint4*>(vd + r * vstride + x * 8) = decode8(codes[(lo + r) * (W + 1) + x], kv4::scale_of(vb[j]));
+        }
+        __syncthreads();                                       // before the next head's V
     }
 }
 
@@ -312,6 +337,16 @@ unsigned touched_grid(const KvView& c)
 {
     const long long most = (long long)c.n_tokens / c.blk + 2ll * c.n_seqs;
     return (unsigned)(most < c.n_tokens ? most : c.n_tokens) + 1;
+}
+
+// Heads of a CTA: finding the block costs as much as a third of a head's work, so several
+// as long as every SM has three CTAs.
+int heads_for(const KvView& c, int num_sms)
+{
+    int heads = 1;
+    while (2 * heads <= c.H && (long long)touched_grid(c) * (c.H / (2 * heads)) >= 3 * num_sms)
+        heads *= 2;
+    return heads;
 }
 
 template <class F>
@@ -347,11 +382,12 @@ cudaError_t launch_kv4_write(const KvView& c, const uint16_t* k, const uint16_t*
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv4_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride, cudaStream_t s)
+cudaError_t launch_kv4_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride, int num_sms, cudaStream_t s)
 {
-    const dim3 grid(touched_grid(c), c.H);
+    const int heads = heads_for(c, num_sms);
+    const dim3 grid(touched_grid(c), (c.H + heads - 1) / heads);
     by_size(c, [&](auto d, auto b) {
-        kv4_read_kernel<decltype(d)::value, decltype(b)::value><<<grid, kThreads, 0, s>>>(c, k, v, k_stride, v_stride);
+        kv4_read_kernel<decltype(d)::value, decltype(b)::value><<<grid, kThreads, 0, s>>>(c, k, v, k_stride, v_stride, heads);
     });
     return cudaGetLastError();
 }

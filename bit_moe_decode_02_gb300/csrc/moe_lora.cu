@@ -24,80 +24,76 @@ constexpr int kMaxM = 64;                 // tokens of a call
 constexpr int kGroup = 8;                 // tokens of a group
 constexpr int kMaxParts = 16;             // of h, over the columns
 
-// Tokens by adapter: groups of at most eight, in the order of their first tokens.  One warp
-// finds them, two tokens a lane.
+// Tokens by adapter: groups of at most eight, in the order of their first tokens.  Every
+// warp finds them for itself, two tokens a lane.
 struct Groups {
+    int mine[2];                          // adapters of tokens lane and lane + 32, -1: none
+    unsigned heads[2];                    // the first tokens of the groups
     int n;
-    int adapter[kMaxM];
-    int member[kMaxM][kGroup];            // tokens, -1: none
-    __align__(16) int of[kMaxM];          // a token's adapter, -1: none
 };
-__device__ __forceinline__ void find_groups(const LoraArgs& a, Groups& g)
+__device__ __forceinline__ Groups find_groups(const LoraArgs& a)
 {
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid >= 32) {
-        for (int i = tid - 32; i < kMaxM * kGroup; i += kThreads - 32)
-            g.member[i / kGroup][i % kGroup] = -1;
+    const int lane = threadIdx.x & 31;
+    const unsigned below = (1u << lane) - 1;
+    Groups g;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int m = lane + 32 * h;
+        g.mine[h] = m < a.M ? a.index[m] : -1;
     }
-    int mine[2] = {-1, -1};
-    unsigned same[2][2];                  // the tokens of either half with this one's adapter
-    if (tid < 32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int m = lane + 32 * h;
-            if (m < a.M)
-                mine[h] = a.index[m];
-            if (mine[h] >= a.n_adapters)
-                atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
-            if (mine[h] < 0 || mine[h] >= a.n_adapters)
-                mine[h] = -1;
-            g.of[m] = mine[h];
-        }
-        same[0][1] = same[1][0] = same[1][1] = 0;
-        if (a.M > 32) {
-            __syncwarp();
-            same[0][0] = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxM; i += 4) {
-                const int4 x = *reinterpret_cast<const int4*>(g.of + i);
-                const int y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        same[h][i / 32] |= (y[k] == mine[h] ? 1u : 0u) << (i % 32 + k);
-            }
-        } else {
-            same[0][0] = __match_any_sync(~0u, mine[0]);
-        }
+    for (int h = 0; h < 2; ++h) {
+        if (g.mine[h] >= a.n_adapters)
+            atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
+        if (g.mine[h] < 0 || g.mine[h] >= a.n_adapters)
+            g.mine[h] = -1;
     }
-    __syncthreads();                      // the members are cleared
-    if (tid < 32) {
-        // tokens before this one with its adapter; its group's first, the groups before that
-        int before[2];
-        before[0] = __popc(same[0][0] & ((1u << lane) - 1));
-        before[1] = __popc(same[1][0]) + __popc(same[1][1] & ((1u << lane) - 1));
-        const unsigned heads[2] = {__ballot_sync(~0u, mine[0] >= 0 && before[0] % kGroup == 0),
-                                   __ballot_sync(~0u, mine[1] >= 0 && before[1] % kGroup == 0)};
+    int before = __popc(__match_any_sync(~0u, g.mine[0]) & below);       // tokens before this one with its adapter
+    g.heads[0] = __ballot_sync(~0u, g.mine[0] >= 0 && before % kGroup == 0);
+    g.heads[1] = 0;
+    if (a.M > 32) {
+        before = __popc(__match_any_sync(~0u, g.mine[1]) & below);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (mine[h] < 0)
-                continue;
-            unsigned lo = same[h][0], hi = h || a.M > 32 ? same[h][1] : 0u;
-            for (int i = before[h] / kGroup * kGroup; i > 0; --i) {      // to the group's first
-                if (lo)
-                    lo &= lo - 1;
-                else
-                    hi &= hi - 1;
-            }
-            const int at = lo ? __popc(heads[0] & ((lo & (~lo + 1)) - 1)) : __popc(heads[0]) + __popc(heads[1] & ((hi & (~hi + 1)) - 1));
-            g.member[at][before[h] % kGroup] = lane + 32 * h;
-            g.adapter[at] = mine[h];
-        }
-        if (lane == 0)
-            g.n = __popc(heads[0]) + __popc(heads[1]);
+        for (int i = 0; i < 32; ++i)
+            before += __shfl_sync(~0u, g.mine[0], i) == g.mine[1];
+        g.heads[1] = __ballot_sync(~0u, g.mine[1] >= 0 && before % kGroup == 0);
     }
-    __syncthreads();
+    g.n = __popc(g.heads[0]) + __popc(g.heads[1]);
+    return g;
+}
+__device__ __forceinline__ int adapter_of(const Groups& g, int m) { return __shfl_sync(~0u, m < 32 ? g.mine[0] : g.mine[1], m & 31); }
+
+// One group: its adapter, and its tokens (-1: none).
+struct Group {
+    int adapter, member[kGroup];
+};
+__device__ __forceinline__ Group group_at(const Groups& g, int i)
+{
+    const int lane = threadIdx.x & 31;
+    const unsigned below = (1u << lane) - 1;
+    const bool lo = (g.heads[0] >> lane & 1) && __popc(g.heads[0] & below) == i;
+    const bool hi = (g.heads[1] >> lane & 1) && __popc(g.heads[0]) + __popc(g.heads[1] & below) == i;
+    const unsigned in_lo = __ballot_sync(~0u, lo), in_hi = __ballot_sync(~0u, hi);
+    const int head = in_lo ? __ffs(in_lo) - 1 : __ffs(in_hi) + 31;
+    Group x;
+    x.adapter = adapter_of(g, head);
+    unsigned long long m = (unsigned long long)__ballot_sync(~0u, g.mine[1] == x.adapter) << 32 | __ballot_sync(~0u, g.mine[0] == x.adapter);
+    m &= ~0ull << head;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+        x.member[k] = __ffsll((long long)m) - 1;
+        m &= m - 1;
+    }
+    return x;
+}
+// Member k of this lane's choice.
+__device__ __forceinline__ int member_of(const Group& x, int k)
+{
+    int m = x.member[0];
+#pragma unroll
+    for (int i = 1; i < kGroup; ++i)
+        m = k == i ? x.member[i] : m;
+    return m;
 }
 
 // Parts of h: as many as fill the CTAs, of 256 columns at least.
@@ -127,15 +123,15 @@ __device__ __forceinline__ uint4 ldg(const uint16_t* p, bool in)
 // h[part][token][rank] = A x over a part of the columns
 __global__ void __launch_bounds__(kThreads, 2) lora_a_kernel(LoraArgs a)
 {
-    __shared__ Groups g;
     __shared__ float red[kWarps][16 * kGroup];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    find_groups(a, g);
+    const Groups g = find_groups(a);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int rts = (a.rank + 15) / 16, parts = parts_of(a, g.n), items = g.n * rts * parts;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int part = item % parts, rt = item / parts % rts, grp = item / parts / rts;
-        const int adapter = g.adapter[grp], token = g.member[grp][r];
+        const Group group = group_at(g, grp);
+        const int adapter = group.adapter, token = member_of(group, r);
         // chunks of 32 columns, in equal runs for the parts and their warps
         const int chunks = (a.cols + 31) / 32, runs = parts * kWarps, run = part * kWarps + warp;
         const int k0 = (int)((i64)chunks * run / runs) * 32, k1 = min((int)((i64)chunks * (run + 1) / runs) * 32, a.cols);
@@ -175,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_a_kernel(LoraArgs a)
         red[warp][(r + 8) * kGroup + 2 * c] = d[2], red[warp][(r + 8) * kGroup + 2 * c + 1] = d[3];
         __syncthreads();
         if (tid < 16 * kGroup) {
-            const int row = tid % 16, n = tid / 16, m = g.member[grp][n];
+            const int row = tid % 16, n = tid / 16, m = member_of(group, n);
             float sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
@@ -203,60 +199,56 @@ __device__ __forceinline__ T rounded(float x)
         return x;
 }
 
-// out = y + s B h.  A CTA takes a run of (group, NT tiles of 16 rows) and goes through it
-// group by group: the parts of the group's h are added up in shared memory, then every warp
-// takes every eighth of the group's tiles, with all CH chunks of 32 of the rank.
+// out = y + s B h.  A CTA takes a part of one group's tiles of NT times 16 rows: the parts
+// of the group's h are added up in shared memory, then every warp takes every eighth tile,
+// with all CH chunks of 32 of the rank.
 template <class T, int CH, int NT>
 __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
 {
-    __shared__ Groups g;
     __shared__ __align__(16) float s_h[kGroup][32 * CH + 4];
-    find_groups(a, g);
+    const Groups g = find_groups(a);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const T* y = static_cast<const T*>(a.y);
     T* out = static_cast<T*>(a.out);
     const int parts = parts_of(a, g.n), tiles = (a.rows + 16 * NT - 1) / (16 * NT);
-    const i64 items = (i64)g.n * tiles, first = items * blockIdx.x / gridDim.x, last = items * (blockIdx.x + 1) / gridDim.x;
-    uint4 lo[CH][NT], hi[CH][NT];
-    T yv[NT][2][2];
-    auto load = [&](int grp, int tile) {
-        const int n0 = tile * 16 * NT;
-        const uint16_t* b = a.b + ((i64)g.adapter[grp] * a.rows + n0 + r) * a.rank + 8 * c;
+    const int split = g.n ? max(1, min((int)gridDim.x / g.n, (tiles + kWarps - 1) / kWarps)) : 1;       // CTAs of a group
+    for (int item = blockIdx.x; item < g.n * split; item += gridDim.x) {
+        const Group group = group_at(g, item / split);
+        const int part = item % split, tile0 = (int)((i64)tiles * part / split), tile1 = (int)((i64)tiles * (part + 1) / split);
+        const int mine[2] = {member_of(group, 2 * c), member_of(group, 2 * c + 1)};
+        uint4 lo[CH][NT], hi[CH][NT];
+        T yv[NT][2][2];
+        auto load = [&](int tile) {
+            const int n0 = tile * 16 * NT;
+            const uint16_t* b = a.b + ((i64)group.adapter * a.rows + n0 + r) * a.rank + 8 * c;
 #pragma unroll
-        for (int ch = 0; ch < CH; ++ch)
+            for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int row = n0 + 16 * t + r;
-                const bool in = 32 * ch + 8 * c < a.rank;
-                lo[ch][t] = ldg(b + 16ll * t * a.rank + 32 * ch, in && row < a.rows);
-                hi[ch][t] = ldg(b + (16ll * t + 8) * a.rank + 32 * ch, in && row + 8 < a.rows);
-            }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = g.member[grp][2 * c + e];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int row = n0 + 16 * t + r + 8 * k;
-                    yv[t][e][k] = y && m >= 0 && row < a.rows ? y[m * a.y_stride + row] : T(0);
+                for (int t = 0; t < NT; ++t) {
+                    const int row = n0 + 16 * t + r;
+                    const bool in = 32 * ch + 8 * c < a.rank;
+                    lo[ch][t] = ldg(b + 16ll * t * a.rank + 32 * ch, in && row < a.rows);
+                    hi[ch][t] = ldg(b + (16ll * t + 8) * a.rank + 32 * ch, in && row + 8 < a.rows);
                 }
-        }
-    };
-    bool waited = false;
-    for (i64 item = first; item < last;) {
-        const int grp = (int)(item / tiles), tile0 = (int)(item - (i64)grp * tiles);
-        const int tile1 = (int)min((i64)tiles, tile0 + (last - item));
-        item += tile1 - tile0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = n0 + 16 * t + r + 8 * k;
+                        yv[t][e][k] = y && mine[e] >= 0 && row < a.rows ? y[mine[e] * a.y_stride + row] : T(0);
+                    }
+        };
         if (tile0 + warp < tile1)
-            load(grp, tile0 + warp);
-        if (!waited)
+            load(tile0 + warp);
+        const float s = a.scale ? a.scale[group.adapter] : 1.0f;
+        if (item == blockIdx.x)
             asm volatile("griddepcontrol.wait;" ::: "memory");
         else
             __syncthreads();                                   // the last group's h is read no more
-        waited = true;
         for (int i = tid; i < kGroup * 8 * CH; i += kThreads) {
-            const int n = i / (8 * CH), x = i % (8 * CH) * 4, m = g.member[grp][n];
+            const int n = i / (8 * CH), x = i % (8 * CH) * 4, m = member_of(group, n);
             float4 sum = make_float4(0, 0, 0, 0);
             if (m >= 0 && x < a.rank) {
                 const float* h = a.h + (i64)m * a.rank + x;
@@ -274,7 +266,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
             *reinterpret_cast<float4*>(&s_h[n][x]) = sum;
         }
         __syncthreads();
-        const float s = a.scale ? a.scale[g.adapter[grp]] : 1.0f;
         uint32_t h3[CH][3][4];            // this lane's eight of a chunk of its token's h, in three bf16 terms
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch)
@@ -308,11 +299,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
                 for (int e = 0; e < 4; ++e)
                     base[t][e / 2][e % 2] = yv[t][e / 2][e % 2];
             if (tile + kWarps < tile1)
-                load(grp, tile + kWarps);
+                load(tile + kWarps);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int m = g.member[grp][2 * c + e];
-                if (m < 0)
+                if (mine[e] < 0)
                     continue;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -320,17 +310,17 @@ __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
                     for (int k = 0; k < 2; ++k) {
                         const int row = tile * 16 * NT + 16 * t + r + 8 * k;
                         if (row < a.rows)
-                            out[m * a.out_stride + row] = rounded<T>(value(&base[t][e][k]) + s * d[t][2 * k + e]);
+                            out[mine[e] * a.out_stride + row] = rounded<T>(value(&base[t][e][k]) + s * d[t][2 * k + e]);
                     }
             }
         }
     }
-    if (!waited)
+    if ((int)blockIdx.x >= g.n * split)
         asm volatile("griddepcontrol.wait;" ::: "memory");
     // tokens without an adapter
     if (a.y != a.out)
         for (int m = blockIdx.x; m < a.M; m += gridDim.x)
-            if (g.of[m] < 0)
+            if (adapter_of(g, m) < 0)
                 for (int row = tid; row < a.rows; row += kThreads)
                     out[m * a.out_stride + row] = y ? y[m * a.y_stride + row] : T(0);
 }

@@ -187,9 +187,9 @@ int moe_kv_write(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batc
         rc = check_rows("moe_kv_write", "v", v_bf16, v_stride, (long long)v.H * v.D);
     if (rc != MOE_OK)
         return rc;
-    const auto launch = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_write : moe::launch_kv_write;
-    const cudaError_t e = launch(v, static_cast<const uint16_t*>(k_bf16), static_cast<const uint16_t*>(v_bf16), k_stride, v_stride,
-                                 (cudaStream_t)stream);
+    const uint16_t *k = static_cast<const uint16_t*>(k_bf16), *x = static_cast<const uint16_t*>(v_bf16);
+    const cudaError_t e = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_write(v, k, x, k_stride, v_stride, (cudaStream_t)stream)
+                                                : moe::launch_kv_write(v, k, x, k_stride, v_stride, (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_kv_write");
 }
 
@@ -204,9 +204,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
         rc = check_rows("moe_kv_read", "v", v_bf16, v_stride, (long long)v.H * v.D);
     if (rc != MOE_OK)
         return rc;
-    const auto launch = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_read : moe::launch_kv_read;
-    const cudaError_t e = launch(v, static_cast<uint16_t*>(k_bf16), static_cast<uint16_t*>(v_bf16), k_stride, v_stride,
-                                 (cudaStream_t)stream);
+    uint16_t *k = static_cast<uint16_t*>(k_bf16), *x = static_cast<uint16_t*>(v_bf16);
+    const cudaError_t e = v.fmt == MOE_KV_MXFP4 ? moe::launch_kv4_read(v, k, x, k_stride, v_stride, o->num_sms, (cudaStream_t)stream)
+                                                : moe::launch_kv_read(v, k, x, k_stride, v_stride, (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_kv_read");
 }
 

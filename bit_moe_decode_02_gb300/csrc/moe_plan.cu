@@ -3,7 +3,8 @@
 // Three running sums over at most 1,024 sequences (new tokens, new blocks, blocks that
 // come back), which every CTA makes for itself in shared memory; after that each
 // token, new block and returned block is an element of its own, found by a search in
-// those sums.  Bound by latency: lengths -> sums -> search -> table or ring -> slot.
+// those sums (a warp's 128 tokens by one).  Bound by latency: lengths -> sums -> search
+// -> table or ring -> slot.
 #include <cstdint>
 
 #include "ops_internal.h"
@@ -13,9 +14,9 @@ namespace {
 
 typedef long long i64;
 
-constexpr int kThreads = 1024;            // a sequence each; 256 where those are enough
-constexpr int kAhead = 4;                 // tokens that a thread looks up together
-static_assert(kThreads == kMaxSeqs, "a thread a sequence");
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPer = kMaxSeqs / kThreads; // sequences of a thread
+constexpr int kAhead = 4;                 // tokens that a thread takes together
 
 // Tokens and taken blocks of a sequence are held to what cannot fit in any call before they
 // are summed, so that 1,024 of them stay within 31 bits; what comes back saturates.
@@ -29,104 +30,120 @@ __device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b)
     return {a.tokens + b.tokens, a.taken + b.taken, back < a.back ? ~0u : back};
 }
 
-// Sums over all threads up to and with each; the whole CTA calls it.
-__device__ __forceinline__ Sums scan(Sums v, Sums* warps, Sums& all)
+// Sums over all threads before each; the whole CTA calls it.
+__device__ __forceinline__ Sums scan(const Sums& mine, Sums* warps, Sums& all)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
-    auto up = [&](const Sums& x, int o) {
-        return Sums{__shfl_up_sync(~0u, x.tokens, o), __shfl_up_sync(~0u, x.taken, o), __shfl_up_sync(~0u, x.back, o)};
-    };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Sums x = up(v, o);
+        const Sums x{__shfl_up_sync(~0u, v.tokens, o), __shfl_up_sync(~0u, v.taken, o), __shfl_up_sync(~0u, v.back, o)};
         if (lane >= o)
             v = v + x;
     }
     if (lane == 31)
         warps[warp] = v;
+    const Sums up{__shfl_up_sync(~0u, v.tokens, 1), __shfl_up_sync(~0u, v.taken, 1), __shfl_up_sync(~0u, v.back, 1)};
     __syncthreads();
-    Sums w = lane < n ? warps[lane] : Sums{0, 0, 0};
+    Sums before{0, 0, 0};
+    all = before;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Sums x = up(w, o);
-        if (lane >= o)
-            w = w + x;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp)
+            before = all;
+        all = all + warps[w];
     }
-    auto at = [&](int src) {
-        return Sums{__shfl_sync(~0u, w.tokens, src), __shfl_sync(~0u, w.taken, src), __shfl_sync(~0u, w.back, src)};
-    };
-    all = at(n - 1);
-    if (warp > 0)
-        v = at(warp - 1) + v;
-    return v;
+    return lane ? before + up : before;
 }
 
-// The sequences that elements i belong to: the last b < n with sum[b] <= i.
-template <int N>
-__device__ __forceinline__ void owners(const int* sum, int n, const int (&i)[N], int (&b)[N])
+// The sequence that element i belongs to: the last b < n with sum[b] <= i.
+__device__ __forceinline__ int owner(const int* sum, int n, int i)
 {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        b[k] = 0;
+    int b = 0;
 #pragma unroll 1
     for (int step = 1 << (31 - __clz(n)); step; step >>= 1)
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (b[k] + step < n && sum[b[k] + step] <= i[k])
-                b[k] += step;
+        if (b + step < n && sum[b + step] <= i)
+            b += step;
+    return b;
+}
+// The same for a whole warp's one element: 32 sums at a time.
+__device__ __forceinline__ int owner_of_warp(const int* sum, int n, int i)
+{
+    const int lane = threadIdx.x & 31, at = lane * 32;
+    const int first = 32 * (__popc(__ballot_sync(~0u, at < n && sum[at] <= i)) - 1);
+    return first + __popc(__ballot_sync(~0u, first + lane < n && sum[first + lane] <= i)) - 1;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, unsigned* cnt)
+__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a, unsigned* cnt)
 {
     __shared__ int s_cu[kMaxSeqs + 1], s_taken[kMaxSeqs + 1], s_back[kMaxSeqs + 1], s_had[kMaxSeqs];
-    __shared__ Sums s_warps[32];
+    __shared__ Sums s_warps[kWarps];
     __shared__ int s_last;
-    const int b = threadIdx.x, n = a.n_seqs, log = a.log_block, blk = 1 << log;
-    int want = 0, had = 0;
-    if (b < n) {
-        want = a.n_new[b];
-        had = a.kv_len[b];
+    const int tid = threadIdx.x, n = a.n_seqs, log = a.log_block, blk = 1 << log;
+    const int per = (n + kThreads - 1) / kThreads, b0 = tid * per;
+    int want[kPer], had[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const bool in = i < per && b0 + i < n;
+        want[i] = in ? a.n_new[b0 + i] : 0;
+        had[i] = in ? a.kv_len[b0 + i] : 0;
     }
     const int head = a.state[0], count = a.state[1];
     const bool pool = head >= 0 && head < a.ring_size && count >= 0 && count <= a.ring_size;
-    const i64 room = (i64)a.table_stride * blk;
-    const bool good = pool && had >= 0 && want >= -1 && (i64)had + (want > 0 ? want : 0) <= (room < 0x7fffffffll ? room : 0x7fffffffll);
+    const i64 held_most = (i64)a.table_stride << log;
+    const i64 room = held_most < 0x7fffffffll ? held_most : 0x7fffffffll;
     auto blocks_of = [&](int len) { return (int)(((unsigned)len + blk - 1) >> log); };
-    const int blocks = blocks_of(had);
-    Sums mine{0, 0, 0}, all;
-    if (good && b < n) {
-        mine.tokens = want > 0 ? min(want, a.n_tokens + 1) : 0;
-        mine.taken = want > 0 ? blocks_of(had + mine.tokens) - blocks : 0;
-        mine.back = want < 0 ? blocks : 0;
+    Sums each[kPer], mine{0, 0, 0}, all;
+    unsigned good = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        each[i] = Sums{0, 0, 0};
+        if (pool && had[i] >= 0 && want[i] >= -1 && (i64)had[i] + (want[i] > 0 ? want[i] : 0) <= room) {
+            good |= 1u << i;
+            const int blocks = blocks_of(had[i]), tokens = want[i] > 0 ? min(want[i], a.n_tokens + 1) : 0;
+            each[i] = Sums{tokens, tokens > 0 ? blocks_of(had[i] + tokens) - blocks : 0, want[i] < 0 ? (unsigned)blocks : 0u};
+        } else if (i < per && b0 + i < n) {
+            atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
+        }
+        mine = mine + each[i];
     }
-    if (!good && threadIdx.x < n)
-        atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
-    Sums incl = scan(mine, s_warps, all);
-    // the first sequence whose blocks or tokens do not fit, and all after it, get none
-    const bool fits = pool && incl.taken <= count && incl.tokens <= a.n_tokens;
+    Sums sum = scan(mine, s_warps, all);
     const bool come_back = pool && all.back <= (unsigned)(a.ring_size - count);      // else some block is free and held
-    if (!come_back && pool && threadIdx.x == 0)
+    if (!come_back && pool && tid == 0)
         atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
-    const int served = __syncthreads_count(b < n && fits);
-    if (b < n && fits) {
-        s_cu[b + 1] = incl.tokens;
-        s_taken[b + 1] = incl.taken;
+    // the first sequence whose blocks or tokens do not fit, and all after it, get none
+    int mine_served = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (i >= per || b0 + i >= n)
+            break;
+        sum = sum + each[i];
+        if (pool && sum.taken <= count && sum.tokens <= a.n_tokens) {
+            ++mine_served;
+            s_cu[b0 + i + 1] = sum.tokens;
+            s_taken[b0 + i + 1] = sum.taken;
+        }
+        s_back[b0 + i + 1] = come_back ? (int)sum.back : 0;
+        s_had[b0 + i] = had[i];
     }
-    if (b < n) {
-        s_back[b + 1] = come_back ? (int)incl.back : 0;
-        s_had[b] = had;
-    }
-    if (b == 0)
+    if (tid == 0) {
         s_cu[0] = s_taken[0] = s_back[0] = 0;
-    __syncthreads();
-    const int tokens = s_cu[served], taken = s_taken[served], back = s_back[n];
-    if (b < n && !fits) {
-        s_cu[b + 1] = tokens;
-        s_taken[b + 1] = taken;
+        s_last = 0;
     }
+    __syncthreads();
+    if (mine_served)
+        atomicAdd(&s_last, mine_served);
+    __syncthreads();
+    const int served = s_last, tokens = s_cu[served], taken = s_taken[served], back = s_back[n];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i < per && b0 + i < n && b0 + i >= served) {
+            s_cu[b0 + i + 1] = tokens;
+            s_taken[b0 + i + 1] = taken;
+        }
     __syncthreads();
 
-    const int step = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
+    const int lane = tid & 31;
     auto ring_at = [&](i64 k) {                                // the k-th free block
         i64 at = head + k;
         at -= at >= a.ring_size ? a.ring_size : 0;
@@ -134,54 +151,60 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, unsigned*
     };
     auto held = [&](int q) { return blocks_of(s_had[q]); };
     bool fault = false;
-    for (int t0 = first; t0 < a.n_tokens; t0 += kAhead * step) {
-        int t[kAhead], q[kAhead], pos[kAhead], id[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-            t[e] = t0 + e * step;                              // below 2^20 + 4 * 152 * 1024
-        owners(s_cu, n, t, q);
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            const bool in = t[e] < tokens;
-            pos[e] = in ? s_had[q[e]] + t[e] - s_cu[q[e]] : -1;
-            id[e] = 0;
-            if (in && a.slot) {
-                const int j = pos[e] >> log, h = held(q[e]);
-                id[e] = j < h ? a.table[(i64)q[e] * a.table_stride + j] : ring_at((i64)s_taken[q[e]] + j - h);
+    // a warp takes 32 new blocks, 32 that come back, or 128 tokens in a row, most often of one sequence
+    const int chunk = 32 * kAhead, taken_at = (taken + 31) / 32, back_at = taken_at + (back + 31) / 32;
+    const int units = back_at + (a.n_tokens + chunk - 1) / chunk;
+    for (int u = blockIdx.x * kWarps + (tid >> 5); u < units; u += gridDim.x * kWarps) {
+        if (u < taken_at) {
+            const int k = u * 32 + lane;
+            if (k < taken) {
+                const int id = ring_at(k), q = owner(s_taken, n, k);
+                fault |= id < 0 || id >= a.ring_size;
+                a.table[(i64)q * a.table_stride + held(q) + k - s_taken[q]] = id;
             }
-            q[e] = in ? q[e] : -1;
-        }
+        } else if (u < back_at) {
+            const int k = (u - taken_at) * 32 + lane;
+            if (k < back) {
+                const int q = owner(s_back, n, k), id = a.table[(i64)q * a.table_stride + k - s_back[q]];
+                fault |= id < 0 || id >= a.ring_size;
+                i64 at = (i64)head + count + k;
+                at -= at >= a.ring_size ? a.ring_size : 0;
+                a.ring[at] = id;
+            }
+        } else {
+            const int t0 = (u - back_at) * chunk, q0 = owner_of_warp(s_cu, n, t0);
+            int q[kAhead], pos[kAhead], id[kAhead];
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            if (t[e] >= a.n_tokens)
-                break;
-            const bool known = id[e] >= 0 && id[e] < a.ring_size;
-            fault |= !known;
-            if (a.seq)
-                a.seq[t[e]] = q[e];
-            if (a.position)
-                a.position[t[e]] = pos[e];
-            if (a.slot)
-                a.slot[t[e]] = known && pos[e] >= 0 ? ((i64)id[e] << log) + (pos[e] & (blk - 1)) : -1;
+            for (int e = 0; e < kAhead; ++e) {
+                const int t = t0 + 32 * e + lane;
+                q[e] = pos[e] = -1;
+                id[e] = 0;
+                if (t < tokens) {
+                    q[e] = q0;
+                    if (t >= s_cu[q0 + 1])
+                        q[e] = owner(s_cu, n, t);
+                    pos[e] = s_had[q[e]] + t - s_cu[q[e]];
+                    if (a.slot) {
+                        const int j = pos[e] >> log, h = held(q[e]);
+                        id[e] = j < h ? a.table[(i64)q[e] * a.table_stride + j] : ring_at((i64)s_taken[q[e]] + j - h);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int t = t0 + 32 * e + lane;
+                if (t >= a.n_tokens)
+                    break;
+                const bool known = id[e] >= 0 && id[e] < a.ring_size;
+                fault |= !known;
+                if (a.seq)
+                    a.seq[t] = q[e];
+                if (a.position)
+                    a.position[t] = pos[e];
+                if (a.slot)
+                    a.slot[t] = known && pos[e] >= 0 ? ((i64)id[e] << log) + (pos[e] & (blk - 1)) : -1;
+            }
         }
-    }
-    for (int k = first; k < taken; k += step) {
-        const int at_k[1] = {k};
-        int q[1];
-        owners(s_taken, n, at_k, q);
-        const int id = ring_at(k);
-        fault |= id < 0 || id >= a.ring_size;
-        a.table[(i64)q[0] * a.table_stride + held(q[0]) + k - s_taken[q[0]]] = id;
-    }
-    for (int k = first; k < back; k += step) {
-        const int at_k[1] = {k};
-        int q[1];
-        owners(s_back, n, at_k, q);
-        const int id = a.table[(i64)q[0] * a.table_stride + k - s_back[q[0]]];
-        fault |= id < 0 || id >= a.ring_size;
-        i64 at = (i64)head + count + k;
-        at -= at >= a.ring_size ? a.ring_size : 0;
-        a.ring[at] = id;
     }
     if (fault)
         atomicExch(a.status, MOE_ERR_DEVICE_FAULT);
@@ -201,11 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, unsigned*
     } else if (blockIdx.x) {
         return;
     }
-    if (b < n) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = b0 + i;
+        if (i >= per || b >= n)
+            break;
         a.cu[b + 1] = s_cu[b + 1];
-        a.kv_len_out[b] = good && want < 0 && come_back ? 0 : had + (s_cu[b + 1] - s_cu[b]);
+        a.kv_len_out[b] = (good >> i & 1) && want[i] < 0 && come_back ? 0 : had[i] + (s_cu[b + 1] - s_cu[b]);
     }
-    if (b == 0) {
+    if (tid == 0) {
         a.cu[0] = 0;
         i64 at = (i64)head + taken;
         at -= pool && at >= a.ring_size ? a.ring_size : 0;
@@ -220,14 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanArgs a, unsigned*
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, unsigned* cnt, cudaStream_t s)
 {
-    // elements at most: a token each, and a block each that is taken or comes back
-    const i64 held = (i64)a.n_seqs * a.table_stride, most = a.n_tokens + (held < a.ring_size ? held : a.ring_size);
-    // one CTA of 256 threads, or of 1,024 each: many threads make the sums slower
-    const int threads = a.n_seqs <= 256 && most <= 2048 ? 256 : kThreads;
-    const i64 ctas = (most + 2 * threads - 1) / (2 * threads);
-    const int grid = threads < kThreads ? 1 : (int)(ctas < num_sms ? ctas : num_sms);
+    // a warp's units at most: 128 tokens, or 32 blocks that are taken or come back
+    const i64 held = (i64)a.n_seqs * a.table_stride, blocks = held < a.ring_size ? held : a.ring_size;
+    const i64 ctas = (a.n_tokens / (32 * kAhead) + blocks / 32 + 3 + kWarps - 1) / kWarps;
+    const int grid = (int)(ctas < 4 * num_sms ? ctas : 4 * num_sms);
     const bool in_place = a.kv_len_out == a.kv_len || a.state_out == a.state;
-    plan_kernel<<<grid, threads, 0, s>>>(a, grid > 1 && in_place ? cnt : nullptr);
+    plan_kernel<<<grid, kThreads, 0, s>>>(a, grid > 1 && in_place ? cnt : nullptr);
     return cudaGetLastError();
 }
 

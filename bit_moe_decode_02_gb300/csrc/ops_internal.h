@@ -44,7 +44,7 @@ cudaError_t launch_kv_read(const KvView& c, uint16_t* k, uint16_t* v, long long 
 cudaError_t launch_kv4_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride,
                              long long v_stride, cudaStream_t s);
 cudaError_t launch_kv4_read(const KvView& c, uint16_t* k, uint16_t* v, long long k_stride, long long v_stride,
-                            cudaStream_t s);
+                            int num_sms, cudaStream_t s);
 
 struct AttnArgs {
     KvView c;
