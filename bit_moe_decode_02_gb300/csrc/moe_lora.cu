@@ -96,11 +96,15 @@ __device__ __forceinline__ int member_of(const Group& x, int k)
     return m;
 }
 
-// Parts of h: as many as fill the CTAs, of 256 columns at least.
+// Parts of h, over the columns: as many (of 256 columns at least) as let the CTAs of the
+// first kernel end together.  A lane for each number, every warp for itself.
 __device__ __forceinline__ int parts_of(const LoraArgs& a, int groups)
 {
-    const int items = groups * ((a.rank + 15) / 16), most = min(kMaxParts, (a.cols + 255) / 256);
-    return items ? max(1, min(most, a.ctas / items)) : 1;
+    const int p = (threadIdx.x & 31) + 1, items = groups * ((a.rank + 15) / 16), most = min(kMaxParts, (a.cols + 255) / 256);
+    // rounds of a CTA in 1/256 of an item, and what a round costs beside its loads
+    const int rounds = (items * p + a.ctas - 1) / a.ctas, cost = rounds * (256 / p + 8);
+    const unsigned best = __reduce_min_sync(~0u, p <= most ? (unsigned)cost << 5 | (unsigned)(p - 1) : ~0u);
+    return (int)(best & 31) + 1;
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -132,16 +136,17 @@ __global__ void __launch_bounds__(kThreads, 2) lora_a_kernel(LoraArgs a)
         const int part = item % parts, rt = item / parts % rts, grp = item / parts / rts;
         const Group group = group_at(g, grp);
         const int adapter = group.adapter, token = member_of(group, r);
-        // chunks of 32 columns, in equal runs for the parts and their warps
-        const int chunks = (a.cols + 31) / 32, runs = parts * kWarps, run = part * kWarps + warp;
-        const int k0 = (int)((i64)chunks * run / runs) * 32, k1 = min((int)((i64)chunks * (run + 1) / runs) * 32, a.cols);
+        // chunks of 32 columns in equal runs for the parts; the warps take U of them in turn, so that the
+        // CTA reads its rows in long pieces
+        constexpr int U = 3;
+        const int chunks = (a.cols + 31) / 32;
+        const int k0 = ((int)((i64)chunks * part / parts) + warp * U) * 32, k1 = min((int)((i64)chunks * (part + 1) / parts) * 32, a.cols);
         const bool lo_in = rt * 16 + r < a.rank, hi_in = rt * 16 + r + 8 < a.rank;
         const uint16_t* lo = a.a + ((i64)adapter * a.rank + rt * 16 + r) * a.cols + 8 * c;
         const uint16_t* hi = lo + 8ll * a.cols;
         const uint16_t* x = a.x + (i64)max(token, 0) * a.x_stride + 8 * c;
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         // the next U chunks are on their way while these are multiplied
-        constexpr int U = 3;
         uint4 wl[2][U], wh[2][U], wx[2][U];
         auto load = [&](int buf, int k) {
 #pragma unroll
@@ -158,11 +163,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_a_kernel(LoraArgs a)
             for (int u = 0; u < U; ++u)
                 mma32(d, wl[buf][u], wh[buf][u], wx[buf][u]);
         };
+        constexpr int step = 32 * U * kWarps;
         load(0, k0);
-        for (int k = k0; k < k1; k += 64 * U) {
-            load(1, k + 32 * U);
+        for (int k = k0; k < k1; k += 2 * step) {
+            load(1, k + step);
             multiply(0);
-            load(0, k + 64 * U);
+            load(0, k + 2 * step);
             multiply(1);
         }
         // rows r, r + 8 of this tile by tokens 2c, 2c + 1
@@ -350,7 +356,7 @@ cudaError_t launch_lora(LoraArgs a, int num_sms, cudaStream_t s)
     const KernelB b = a.type == MOE_DT_BF16 ? pick<uint16_t>(a.rank, rows) : pick<float>(a.rank, rows);
     const i64 items = (i64)a.M * ((a.rows + rows - 1) / rows), ctas = (items + kWarps - 1) / kWarps;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ctas < a.ctas ? ctas : a.ctas));
+    cfg.gridDim = dim3((unsigned)(ctas < 2 * num_sms ? ctas : 2 * num_sms));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute at{};
