@@ -214,7 +214,7 @@ def lib() -> ctypes.CDLL:
         L.moe_lora.argtypes = [p, ctypes.POINTER(moe_lora_weights), p, p, ll, i, p, ll, p, ll, i, p]
         L.moe_lora.restype = i
         # the same calls with their arguments as 64-bit words (moe_ops.cu): one conversion instead of many
-        for name in ("rope", "kv_plan", "lora"):
+        for name in ("kv_write", "kv_read", "rope", "kv_plan", "lora"):
             f = getattr(L, "moe_words_" + name)
             f.argtypes = [ctypes.c_char_p]
             f.restype = i
@@ -222,6 +222,7 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_WORDS_KV = struct.Struct("=8q").pack
 _WORDS_ROPE, _WORDS_PLAN, _WORDS_LORA = struct.Struct("=17q").pack, struct.Struct("=14q").pack, struct.Struct("=12q").pack
 
 
@@ -452,12 +453,18 @@ def moe_kv_batch_of(cu, kv_len, table, n_tokens) -> moe_kv_batch:
     return b
 
 
+_current = None
+
+
 def _raw_stream(stream, t):
     """The stream's handle; None: the current stream of the tensor's device (asked for by its handle alone: building a
     torch.cuda.Stream takes as long as a launch)."""
+    global _current
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        if _current is None:
+            import torch
+            _current = torch._C._cuda_getCurrentRawStream
+        return _current(t.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -475,14 +482,16 @@ def moe_kv_write(o, cache, batch, k, v, stream=None):
     T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
     kp, ks = _heads(k, "k", T, H, D)
     vp, vs = _heads(v, "v", T, H, D)
-    return _check(lib().moe_kv_write(o, cache, batch, kp, ks, vp, vs, _raw_stream(stream, k)))
+    rc = lib().moe_words_kv_write(_WORDS_KV(o, ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def moe_kv_read(o, cache, batch, k, v, stream=None):
     T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
     kp, ks = _heads(k, "k", T, H, D)
     vp, vs = _heads(v, "v", T, H, D)
-    return _check(lib().moe_kv_read(o, cache, batch, kp, ks, vp, vs, _raw_stream(stream, k)))
+    rc = lib().moe_words_kv_read(_WORDS_KV(o, ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
+    return rc if rc == MOE_OK else _check(rc)
 
 
 def moe_attention(o, cache, batch, q, out, lse=None, sinks=None, window=0, scale=None, stream=None):
@@ -514,6 +523,18 @@ def moe_kv_pool_of(ring, table, block) -> moe_kv_pool:
     return c
 
 
+_kinds = None
+
+
+def _types():
+    """torch.bfloat16, float32, int32, int64, looked up once."""
+    global _kinds
+    if _kinds is None:
+        import torch
+        _kinds = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    return _kinds
+
+
 def _array(t, name, dtype, n):
     """Address of a contiguous CUDA tensor [n] of that type."""
     if t.dtype is not dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
@@ -525,8 +546,7 @@ def moe_kv_plan(o, pool, n_new, kv_len, state, cu, kv_len_out, state_out, admitt
                 n_tokens=None, stream=None):
     """n_new, kv_len, kv_len_out int32 [n_seqs], state, state_out int32 [2], cu int32 [n_seqs + 1], admitted int32 [1], seq and
     position int32 and slot int64 [n_tokens]; n_tokens (their length) has to be given where all three are None."""
-    import torch
-    i, n = torch.int32, pool.n_seqs
+    i, n = _types()[2], pool.n_seqs
     if n_tokens is None:
         t = slot if slot is not None else position if position is not None else seq
         if t is None:
@@ -537,7 +557,7 @@ def moe_kv_plan(o, pool, n_new, kv_len, state, cu, kv_len_out, state_out, admitt
         _array(cu, "cu", i, n + 1), _array(kv_len_out, "kv_len_out", i, n), _array(state_out, "state_out", i, 2),
         0 if admitted is None else _array(admitted, "admitted", i, 1), 0 if seq is None else _array(seq, "seq", i, n_tokens),
         0 if position is None else _array(position, "position", i, n_tokens),
-        0 if slot is None else _array(slot, "slot", torch.int64, n_tokens), _raw_stream(stream, n_new)))
+        0 if slot is None else _array(slot, "slot", _types()[3], n_tokens), _raw_stream(stream, n_new)))
     return rc if rc == MOE_OK else _check(rc)
 
 
@@ -573,16 +593,16 @@ def _head_rows(t, name, kind, T, heads, D):
 def moe_rope(o, rope, position, q, k=None, q_out=None, k_out=None, stream=None):
     """q [T][q_heads][head_dim], k [T][k_heads][head_dim] or None, of bf16 or fp32; q_out, k_out like them (None: in place);
     position int32 [T].  Rows may be strided, heads are contiguous."""
-    import torch
+    bf16, fp32, i32, _ = _types()
     T, heads, D = q.shape if q.dim() == 3 else (0, 0, 0)
     kind = q.dtype
-    if kind is torch.bfloat16:
+    if kind is bf16:
         code = MOE_DT_BF16
-    elif kind is torch.float32:
+    elif kind is fp32:
         code = MOE_DT_F32
     else:
         raise ValueError(f"moe_rope: q must be bf16 or fp32 (got {kind})")
-    pos = _array(position, "position", torch.int32, T)
+    pos = _array(position, "position", i32, T)
     qp, qs = _head_rows(q, "q", kind, T, heads, D)
     op, os_ = (qp, qs) if q_out is None else _head_rows(q_out, "q_out", kind, T, heads, D)
     if k is not None:
@@ -625,17 +645,17 @@ def _out_rows(t, name, kind, M, rows):
 def moe_lora(o, w, index, x, y, out=None, stream=None):
     """x bf16 [M][cols], y fp32 or bf16 [M][rows] or None (0), out like y (None: y, in place); rows may be strided; index int32
     [M], -1: no adapter."""
-    import torch
+    bf16, fp32, i32, _ = _types()
     rows, cols = w.rows, w.cols
     if out is None:
         out = y
     M, kind, sx = x.shape[0], out.dtype, x.stride()
-    at = _array(index, "index", torch.int32, M)
-    if x.dtype is not torch.bfloat16 or x.shape != (M, cols) or not x.is_cuda or sx[1] != 1:
+    at = _array(index, "index", i32, M)
+    if x.dtype is not bf16 or x.shape != (M, cols) or not x.is_cuda or sx[1] != 1:
         raise ValueError(f"moe_lora: x must be CUDA bf16 rows [M][{cols}] (got {x.dtype} {tuple(x.shape)}, strides {sx}, on {x.device})")
-    if kind is torch.bfloat16:
+    if kind is bf16:
         code = MOE_DT_BF16
-    elif kind is torch.float32:
+    elif kind is fp32:
         code = MOE_DT_F32
     else:
         raise ValueError(f"moe_lora: y and out must be bf16 or fp32 (got {kind})")

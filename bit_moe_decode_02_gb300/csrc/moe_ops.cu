@@ -500,6 +500,8 @@ int call(int (*f)(A...), const long long* w)
 }
 }  // namespace
 
+extern "C" int moe_words_kv_write(const long long* w) { return call(moe_kv_write, w); }
+extern "C" int moe_words_kv_read(const long long* w) { return call(moe_kv_read, w); }
 extern "C" int moe_words_rope(const long long* w) { return call(moe_rope, w); }
 extern "C" int moe_words_kv_plan(const long long* w) { return call(moe_kv_plan, w); }
 extern "C" int moe_words_lora(const long long* w) { return call(moe_lora, w); }
