@@ -318,8 +318,8 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t e = top[i & 1];
-                const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
+                const uint32_t e = top[i & 1];                 // a byte in each half: the upper one leaves the float at the top
+                const float k = kv4::scale_of(i < 2 ? e : e >> 16);
                 s[i][0] = d[i / 2][i % 2 * 2] * (k * f[0]);
                 s[i][1] = d[i / 2][i % 2 * 2 + 1] * (k * f[1]);
             }
@@ -389,7 +389,7 @@ __device__ __forceinline__ void mx_tile(const uint8_t* stage, int sub, uint8_t* 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t e = col[i & 1][j];
-                const float k = kv4::scale_of(i < 2 ? e & 0xffu : e >> 16) * 0x1p-13f;
+                const float k = kv4::scale_of(i < 2 ? e : e >> 16);
                 s[i][j] *= k * f[0];
                 s[i][2 + j] *= k * f[1];
             }
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
     auto table_at = [&](const Item& it, int j) { return a.c.table[(i64)it.b * a.c.table_stride + j]; };
     auto produce = [&]() {
         const int st = pst;
-        if (pround > 0)
+        if (pround > 0 && !tc::mbar_try_wait(empty + st, (uint32_t)((pround - 1) & 1)))
             tc::mbar_wait(empty + st, (uint32_t)((pround - 1) & 1), status);
         if (++pst == C::NS) {
             pst = 0;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                     big = max(big, __shfl_xor_sync(~0u, big, 1));
                     big = max(big, __shfl_xor_sync(~0u, big, 2));
                     const RowScale rs = row_scale(big, a.scale);
-                    f[e] = rs.f;
+                    f[e] = C::MX ? rs.f * 0x1p-13f : rs.f;       // K's f16 operands are 2^13 up there
 #pragma unroll
                     for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
@@ -806,7 +806,8 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
             for (; t < seg_end; ++t, ++j) {
                 fill(t);
                 st = cst;
-                tc::mbar_wait(full + st, phase, status);
+                if (!tc::mbar_try_wait(full + st, phase))
+                    tc::mbar_wait(full + st, phase, status);
                 if (++cst == C::NS) {
                     cst = 0;
                     phase ^= 1;
