@@ -72,6 +72,13 @@ struct Layout {
     [[maybe_unused]] static constexpr int SMEM = OFF_PASS + (MX ? kRing * (int)sizeof(Pass) : 0);   // 226.4 KB for D = 128 in 8 bits, of 227
 };
 
+// A wait that is over costs no call.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int* status)
+{
+    if (!tc::mbar_try_wait(bar, parity))
+        tc::mbar_wait(bar, parity, status);
+}
+
 // The whole warp executes these, one elected lane (`one` != 0) issues: outside a
 // branch the operands, the same in all lanes, stay in uniform registers.
 __device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
@@ -374,7 +381,7 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 if (t >= 1)
-                    tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                    wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_expect_tx(raw_full + v, (uint32_t)n * L::REC);
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         if (t >= 1)
-                            tc::mbar_wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
+                            wait(raw_empty + v, (uint32_t)((t - 1) & 1), status);
                         __syncwarp();
                         if (lane == 0)
                             tc::mbar_expect_tx(raw_full + v, (uint32_t)n * (BLK * D));
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         const uint32_t one = elect_one();
         auto scores = [&](int x, int t) {
             const int st = t & 1;
-            tc::mbar_wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
+            wait(k_full + st, (uint32_t)(t >> 1 & 1), status);
             tc::tc_fence_after();
             {
 #pragma unroll
@@ -522,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             }
             __syncwarp();
         };
-        tc::mbar_wait(q_full, 0, status);
+        wait(q_full, 0, status);
         for (int x = 0; x < na; ++x)
             scores(x, 0);
         for (int t = 0; t < most; ++t) {
             const int st = t & 1;
             const bool last = info[t % kRing] & 1;
-            tc::mbar_wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
+            wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
             for (int x = 0; x < na; ++x) {
-                tc::mbar_wait(p_full + x, (uint32_t)(t & 1), status);
+                wait(p_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
                 {
 #pragma unroll
@@ -563,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         for (int t = 0; t < most; ++t) {
             const int st = t & 1;
             const float2* tsc = sc + (t % kRing) * 4;
-            tc::mbar_wait(raw_full, (uint32_t)(t & 1), status);
+            wait(raw_full, (uint32_t)(t & 1), status);
             const bool last = info[t % kRing] & 1;
             if (t >= 2)
-                tc::mbar_wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
+                wait(k_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
             if constexpr (L::MX) {
                 // K: a key a lane, a group's 16 bytes of it at a time in an order that spreads the banks
                 const Pass& p = passes[t % kRing];
@@ -616,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             }
             arrive(k_full + st, raw_empty);
 
-            tc::mbar_wait(raw_full + 1, (uint32_t)(t & 1), status);
+            wait(raw_full + 1, (uint32_t)(t & 1), status);
             if (t >= 2)
-                tc::mbar_wait(v_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
+                wait(v_empty + st, (uint32_t)((t >> 1) - 1 & 1), status);
             if constexpr (L::MX) {
                 // V: eight tokens of four d's at a time, as the record's words lie
                 const Pass& p = passes[t % kRing];
@@ -739,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             auto was_of = [&](int ch) { return half ? was[D / 64 + ch] : was[ch]; };       // of this thread's columns
 #pragma unroll 1
             for (int t = 0; t < most; ++t) {
-                tc::mbar_wait(s_full + x, (uint32_t)(t & 1), status);
+                wait(s_full + x, (uint32_t)(t & 1), status);
                 tc::tc_fence_after();
                 const int word = info[t % kRing], p0 = word & ~1;
                 float top = 0.0f;
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             *mine = l;
             pair_sync();
             l = (l + *other) * kUnroom;
-            tc::mbar_wait(o_full + x, 0, status);
+            wait(o_full + x, 0, status);
             tc::tc_fence_after();
             const Final fin = finish(m, l, a.sinks, hq);
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
