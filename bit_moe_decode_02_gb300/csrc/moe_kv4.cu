@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;                 // 16-byte loads of a thread that are out at once, for K and for V each
+constexpr int kAhead = 2;                 // units of 16 values of K, and of V, of a thread whose loads are out at once
 
 // The idx-th block that a batch's tokens touch: by each warp for itself, or of more than 32
 // sequences by the whole CTA, four sequences a thread at most.
@@ -86,11 +86,6 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t quad_max2(uint32_t m)
-{
-    m = max2(m, __shfl_xor_sync(~0u, m, 1));
-    return max2(m, __shfl_xor_sync(~0u, m, 2));
-}
 // Two bf16 times a power of two, exact but below 2^-126.
 __device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b)
 {
@@ -111,42 +106,51 @@ __device__ __forceinline__ uint32_t to_codes(const uint32_t (&w)[4])
     return r;
 }
 
-// Eight of a group's 32 values, the others in the quad's other lanes -> eight codes, and
-// the group's scale byte.
-__device__ __forceinline__ uint32_t encode8(const uint4& q, uint32_t& byte)
+// Half of a group's 32 values, the others in the lane beside it -> sixteen codes, and the
+// group's scale byte.
+__device__ __forceinline__ uint2 encode16(const uint4& p, const uint4& q, uint32_t& byte)
 {
-    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t w[2][4] = {{p.x, p.y, p.z, p.w}, {q.x, q.y, q.z, q.w}};
     // largest magnitude of each half of the words, as bits: NaN and infinities above all others
-    uint32_t m = quad_max2(max2(max2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m = max2(m, w[h][e] & 0x7fff7fffu);
+    m = max2(m, __shfl_xor_sync(~0u, m, 1));
     uint32_t big = max(m & 0xffffu, m >> 16);
     if (__any_sync(~0u, big >= 0x7f80u)) {
         // NaN or infinity among the warp's values: the largest of the others; NaN becomes 0
         m = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            m = max(m, finite_bits(w[e]));
-            w[e] &= ((w[e] & 0x7fffu) > 0x7f80u ? 0u : 0xffffu) | ((w[e] & 0x7fff0000u) > 0x7f800000u ? 0u : 0xffff0000u);
-        }
-        big = quad_max2(m);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                m = max(m, finite_bits(w[h][e]));
+                w[h][e] &= ((w[h][e] & 0x7fffu) > 0x7f80u ? 0u : 0xffffu) | ((w[h][e] & 0x7fff0000u) > 0x7f800000u ? 0u : 0xffff0000u);
+            }
+        big = max(m, __shfl_xor_sync(~0u, m, 1));
     }
     byte = kv4::scale_byte(big);
     const uint32_t inv = ((254u - byte) << 7) * 0x10001u;      // 2^-e
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        w[e] = mul_bf16(w[e], inv);
-    const uint32_t r = to_codes(w);
-    return byte ? r : 0u;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[h][e] = mul_bf16(w[h][e], inv);
+    return byte ? make_uint2(to_codes(w[0]), to_codes(w[1])) : make_uint2(0, 0);
 }
 
 // One CTA per (touched block, some heads): heads, as many as fit the buffer, at a time.
 template <int D, int blk>
-__global__ void __launch_bounds__(kThreads, 6)
+__global__ void __launch_bounds__(kThreads, 4)
 kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __restrict__ vsrc, long long kstride, long long vstride,
                  int heads_per_cta)
 {
-    __shared__ uint32_t codes[blk * (D / 8)];                  // V as written by token: [head][token][D / 8] words
+    __shared__ __align__(8) uint32_t codes[blk * (D / 8)];     // V as written by token: [head][token][D / 8] words
     __shared__ Found found;
-    constexpr int W = D / 8, REC = kv4::record(blk, D);
+    constexpr int W = D / 8, U = D / 16, REC = kv4::record(blk, D);     // words and units of a token's head
     const int tid = threadIdx.x;
     kv::Touched t;
     if (!find(c, blockIdx.x, found, t))
@@ -160,7 +164,7 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
     const long long row0 = t.c0 - start + lo;
     const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, c.H), batch = blk / n;
     for (int hb = h0; hb < h1; hb += batch) {
-        const int nh = min(batch, h1 - hb), units = nh * n * W;
+        const int nh = min(batch, h1 - hb), units = nh * n * U;
         uint8_t* rec = c.codes + ((long long)id * c.H + hb) * 2 * REC;
         // row i of a head's `per`
         auto split = [&](int i, int per, int& h, int& r) {
@@ -168,38 +172,42 @@ kv4_write_kernel(KvView c, const uint16_t* __restrict__ ksrc, const uint16_t* __
             r = i - h * per;
         };
         for (int i0 = tid; i0 - tid < units; i0 += kAhead * kThreads) {
-            uint4 k[kAhead], v[kAhead];
+            uint4 k[kAhead][2], v[kAhead][2];
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads, x = i % W;
+                const int i = i0 + e * kThreads, x = i % U;
                 int h, r;
-                split(i / W, n, h, r);
-                k[e] = v[e] = make_uint4(0, 0, 0, 0);
+                split(i / U, n, h, r);
+                k[e][0] = k[e][1] = v[e][0] = v[e][1] = make_uint4(0, 0, 0, 0);
                 if (i < units) {
-                    const long long col = (long long)(hb + h) * D + x * 8;
-                    k[e] = *reinterpret_cast<const uint4*>(ksrc + (row0 + r) * kstride + col);
-                    v[e] = *reinterpret_cast<const uint4*>(vsrc + (row0 + r) * vstride + col);
+                    const long long col = (long long)(hb + h) * D + x * 16;
+                    const uint4* kp = reinterpret_cast<const uint4*>(ksrc + (row0 + r) * kstride + col);
+                    const uint4* vp = reinterpret_cast<const uint4*>(vsrc + (row0 + r) * vstride + col);
+                    k[e][0] = kp[0], k[e][1] = kp[1];
+                    v[e][0] = vp[0], v[e][1] = vp[1];
                 }
             }
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int i = i0 + e * kThreads, x = i % W;
+                const int i = i0 + e * kThreads, x = i % U;
                 if (i0 - tid + e * kThreads >= units)
                     break;
                 uint32_t kb, vb;
-                const uint32_t kc = encode8(k[e], kb), vc = encode8(v[e], vb);
+                const uint2 kc = encode16(k[e][0], k[e][1], kb), vc = encode16(v[e][0], v[e][1], vb);
                 if (i >= units)
                     continue;
                 int h, r;
-                split(i / W, n, h, r);
+                split(i / U, n, h, r);
                 const int tok = lo + r;
                 uint8_t* kr = rec + (long long)h * 2 * REC;
-                reinterpret_cast<uint32_t*>(kr)[tok * W + x] = kc;
-                codes[i] = vc;
-                if (x % 4 == 0) {
-                    kr[blk * D / 2 + kv4::k_scale_at<D>(tok, x / 4)] = (uint8_t)kb;
-                    kr[REC + blk * D / 2 + kv4::v_scale_at<D>(tok, x / 4)] = (uint8_t)vb;
-                }
+                reinterpret_cast<uint2*>(kr)[tok * U + x] = kc;
+                reinterpret_cast<uint2*>(codes)[i] = vc;
+                // a lane of the group's two writes K's scale, the other V's
+                const int g = x / 2;
+                if (x % 2 == 0)
+                    kr[blk * D / 2 + kv4::k_scale_at<D>(tok, g)] = (uint8_t)kb;
+                else
+                    kr[REC + blk * D / 2 + kv4::v_scale_at<D>(tok, g)] = (uint8_t)vb;
             }
         }
         __syncthreads();
@@ -373,7 +381,7 @@ void by_size(const KvView& c, F f)
 cudaError_t launch_kv4_write(const KvView& c, const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, cudaStream_t s)
 {
     // single tokens: as many heads a CTA as fill it
-    const int tokens = (c.n_tokens + c.n_seqs - 1) / c.n_seqs, fit = kThreads / (c.D / 8) / tokens;
+    const int tokens = (c.n_tokens + c.n_seqs - 1) / c.n_seqs, fit = kThreads / (c.D / 16) / tokens;
     const int heads = fit < 1 ? 1 : fit < c.H ? fit : c.H;
     const dim3 grid(touched_grid(c), (c.H + heads - 1) / heads);
     by_size(c, [&](auto d, auto b) {
