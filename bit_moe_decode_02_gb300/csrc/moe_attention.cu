@@ -1272,7 +1272,16 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
     // in two; 255 and a prompt of 600 over 1,000 keys: 213 us, 88 + 27 in two.
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
     const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
-    const long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
+    long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
+    if (a.c.fmt == MOE_KV_MXFP4) {
+        // Codes cost the decode kernel less here (D = 64: 0.33 us for 16 rows and 128 keys, 0.56 for 128), beside
+        // about 12 us whatever the work; the prompt kernel 1.65 us up to 128 rows and 2.1 on 256 (1.95, 2.4).  8
+        // sequences of 4,000 keys, 64 heads of 64 on 8: 64 rows 44 / 52 us, 104 rows 65 / 52, 216 rows 115 / 66; one
+        // such sequence, 432 rows: 42 / 69; 32 heads of 128 on 4: 8 sequences, 64 rows 42 / 61, 128 rows 64 / 63, 256
+        // rows 107 / 75.
+        decode += a.c.D == 64 ? 1000 : 600;
+        prompt = (a.c.D == 64 ? (rows > 128 ? 41 : 32) : rows > 128 ? 28 : 22) * waves * num_sms;
+    }
     return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
