@@ -1,4 +1,4 @@
-// attn_device.cuh -- what the attention kernels over the 8-bit cache share.
+// attn_device.cuh -- what the attention kernels over the cache share.
 // Included by .cu files only.
 #pragma once
 #include <cuda_fp16.h>

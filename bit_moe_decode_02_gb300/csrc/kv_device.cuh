@@ -1,5 +1,5 @@
-// kv_device.cuh -- device helpers of the 8-bit paged cache: which block a work
-// item is, block scales, codes.  Included by .cu files only.
+// kv_device.cuh -- device helpers of the paged cache: which block a work item is,
+// and block scales and codes in 8 bits.  Included by .cu files only.
 #pragma once
 #include <cuda_fp16.h>
 

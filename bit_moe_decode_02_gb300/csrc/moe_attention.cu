@@ -1,4 +1,4 @@
-// moe_attention.cu -- attention over the 8-bit paged cache.
+// moe_attention.cu -- attention over the paged cache, in 8 or 4 bits.
 //
 // out_i = sum_j e^{s_ij - m_i} v_j / (sum_j e^{s_ij - m_i} + e^{sink - m_i}),
 // s_ij = scale q_i . k_j over the keys j that token i sees: its own position
@@ -29,12 +29,17 @@
 //    what its subnormals lose of p is below 2^-31 a key: 2^20 keys lose less than the
 //    output's rounding.
 // Measured: 64 sequences of 12,000 tokens on average, 32 heads of 128 on 4 (INT8),
-// 154 us, 5.35 TB/s of codes, 0.79 of a plain copy's rate.  Two warps a scheduler (230
+// 145 us, 5.7 TB/s of codes, 0.83 of a plain copy's rate.  Two warps a scheduler (230
 // registers) are two chains of conversions and MMAs, which issue 0.4 instructions a
 // cycle: that, not the loads in flight, is what is left.  One sequence of 4,300
 // tokens, 64 heads of 64 on 8: 11.4 us, nearly all of it the way through: 1.9 us to
 // find the tiles, 1.3 for the first loads, 0.9 for the tiles, a join in the CTA (1.1)
 // and one over the CTAs (5); the same heads within a window of 128, 4 sequences: 7.0 us.
+// In 4 bits (mx_tile): the 64 sequences take 99 us, 4.4 TB/s (0.65 of a copy), bound by
+// issue: 630 instructions for 32 keys and 8 rows at 0.55 a cycle, of which the conversions
+// (one for two codes, at half rate) and products with scales are a third.  With items of 16
+// rows, as in 8 bits, and 12 warps 149 us, with 8 warps 159; one sequence of 6,070 tokens
+// 11.4 us, the same way through.
 #include <cstdint>
 
 #include "attn_device.cuh"
@@ -1225,7 +1230,9 @@ void launch_format(const AttnArgs& a, int num_sms, cudaStream_t s)
         return launch_blocks<D, MOE_KV_E4M3, 16>(a, num_sms, s);
     if (a.c.fmt == MOE_KV_INT8)
         return launch_blocks<D, MOE_KV_INT8, 16>(a, num_sms, s);
-    // eight rows at most for a sequence's kv head, on average: queries in an MMA's columns, not its rows
+    // Eight rows at most for a sequence's kv head, on average: queries in an MMA's columns, not its rows.
+    // 64 sequences of 12,000 tokens, 32 heads of 128 on 4: 99 us, 149 in items of 16 rows; of 4,000 tokens, 64
+    // heads of 64 on 8: 56 and 70; 8 of them with 16 rows: 25.5 and 23.2, with 64 rows 57 and 44.
     if ((long long)a.c.n_tokens * a.group <= 8ll * a.c.n_seqs)
         return launch_blocks<D, MOE_KV_MXFP4, 8>(a, num_sms, s);
     launch_blocks<D, MOE_KV_MXFP4, 16>(a, num_sms, s);

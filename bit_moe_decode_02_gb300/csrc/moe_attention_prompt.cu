@@ -1,4 +1,4 @@
-// moe_attention_prompt.cu -- attention of many tokens over the 8-bit paged cache
+// moe_attention_prompt.cu -- attention of many tokens over the paged cache
 // (prompts and their chunks), on tcgen05.
 //
 // 4 D multiply-adds a (row, key) pair, both products as kind::f16 MMAs of 128 rows
@@ -12,7 +12,7 @@
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.
 //  - Roles (24 warps).  Warp 0 streams the raw codes of a tile's blocks (bulk copies,
-//    K and V apart) and their scales.  Warps 4-7 make them the f16 operands, in the
+//    K and V apart) and their scales.  Warps 4-7 (2-7 in 4 bits) make them the f16 operands, in the
 //    canonical K-major order, exactly: K as it lies, V as it lies too (transposed in
 //    the cache).  Warp 1 issues the MMAs.  Warps 8-15 and 16-23 do the softmax of
 //    one row tile each, two threads a row with 64 keys each: while one tile's is
@@ -26,6 +26,10 @@
 //    largest V scale of a tile, whether a row sees that block or not, which takes bits
 //    of the other blocks' probabilities: a tile whose V scales are more than 2^6 apart
 //    goes through as several, one block each.
+//  - In 4 bits a token's groups have scales of their own, which go into the f16 operands:
+//    K's relative to the largest of a tile (Pass), V's to units of 32 columns of O each, so
+//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 305 us (350
+//    before V's operands were stored without bank conflicts, 324 with a call at every wait).
 #include <cstdint>
 
 #include "attn_device.cuh"

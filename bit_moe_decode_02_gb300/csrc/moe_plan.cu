@@ -4,7 +4,9 @@
 // come back), which every CTA makes for itself in shared memory; after that each
 // token, new block and returned block is an element of its own, found by a search in
 // those sums (a warp's 128 tokens by one).  Bound by latency: lengths -> sums -> search
-// -> table or ring -> slot.
+// -> table or ring -> slot.  Measured: 61 sequences of a step 3.3 us; 1,000 requests whose
+// prompts make 510,000 tokens (10 MB out) 8.3 us, of which the sums, which 608 CTAs make
+// each for itself, are half the instructions (on 304 CTAs 8.9 us, on 152 11.6).
 #include <cstdint>
 
 #include "ops_internal.h"

@@ -543,10 +543,11 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * and so is its lse; other rows are not touched by it.
  * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
- * product as 11 bits down to 2^-20, below that within 2^-31.  MXFP4: of a key, the groups whose
- * scale is less than 2^-27 of its largest group's count as 0; where the V scales of one
- * group of the head are 2^7 apart or more within 32 tokens, 11 bits down to 2^-12, below
- * that within 2^-23 of the largest.  The (sequence,
+ * product as 11 bits down to 2^-20, below that within 2^-31.  MXFP4: of a key, groups whose
+ * scale is below 2^-27 of its largest group's count as 0; V's groups whose scale is below
+ * 2^-64 of the largest that the call's earlier keys of that sequence have in that group, or
+ * below 2^-118, may count as 0; and a probability loses at most 2^-31 in units of that largest
+ * scale.  The (sequence,
  * 16 rows, kv head, block) combinations of one call number less than 2^31 (else
  * nothing is written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
