@@ -76,11 +76,24 @@ struct Layout {
     [[maybe_unused]] static constexpr int SMEM = OFF_PASS + (MX ? kRing * (int)sizeof(Pass) : 0);   // 226.4 KB for D = 128 in 8 bits, of 227
 };
 
+// A bounded wait, short where another one has given up already: a tile may go through in
+// many passes, and the kernel has to end soon with its status set.
+static __device__ __noinline__ void wait_on(uint64_t* bar, uint32_t parity, int* status)
+{
+#pragma unroll 1
+    for (int i = 1; i < 1 << 22; ++i) {
+        if (tc::mbar_try_wait(bar, parity))
+            return;
+        if (i % 4096 == 0 && *(volatile int*)status == MOE_ERR_DEVICE_TIMEOUT)
+            return;
+    }
+    atomicExch(status, MOE_ERR_DEVICE_TIMEOUT);
+}
 // A wait that is over costs no call.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, int* status)
 {
     if (!tc::mbar_try_wait(bar, parity))
-        tc::mbar_wait(bar, parity, status);
+        wait_on(bar, parity, status);
 }
 
 // The whole warp executes these, one elected lane (`one` != 0) issues: outside a
@@ -399,6 +412,9 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
         next = after;
         z = zn;
     }
+    // nothing is on its way when the kernel ends, whoever gave up
+    for (int v = 0; v < 2 && t > 0; ++v)
+        wait(raw_full + v, (uint32_t)((t - 1) & 1), status);
 }
 
 template <int D, int FMT, int BLK>

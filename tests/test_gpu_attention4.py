@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
 
 import bit_moe_decode_02_gb300 as moe  # noqa: E402
 from kv4_testlib import Cache4  # noqa: E402
-from ops_testlib import attention, handle, i32, ok  # noqa: E402
+from ops_testlib import Cache, attention, handle, i32, ok  # noqa: E402
 
 
 def check(c, new, lens, heads, window=0, sinks=None, scale=None, qscale=1.0, seed=0, q=None):
@@ -299,3 +299,37 @@ def test_written_and_attended():
         kv = torch.randn(sum(new), 2, H, D, generator=g, device="cuda").bfloat16()
         moe.moe_kv_write(o, c.desc, c.batch(new, lens), kv[:, 0], kv[:, 1])
         check(c, new, lens, 12, seed=sum(lens))
+
+
+@pytest.mark.parametrize("fmt", [moe.MOE_KV_E4M3, moe.MOE_KV_INT8, moe.MOE_KV_MXFP4])
+@pytest.mark.parametrize("heads,kv,new", [(32, 16, [700, 400]), (8, 2, [1, 1])])
+@pytest.mark.parametrize("power", [10, 17, 30])
+def test_scores_far_beyond_the_exponent(fmt, heads, kv, new, power):
+    """Scores of 2^13 to 2^33: a score's rounding is larger than the room that a probability has.  The largest score takes all;
+    rows whose two largest are nearer than what their rounding may be are left out.  The output is rounded to bf16 (2^-8 at most);
+    an INT8 block's scale is no power of two and enters the largest probability's exponent, which is rounded to f16: 2^-11 and as
+    much from the logarithm and the power, 2^-10 in all."""
+    o = handle()
+    lens, T = [700, 1100], sum(new)
+    c = (Cache4(lens, kv, 64, 64, seed=2) if fmt == moe.MOE_KV_MXFP4 else Cache(lens, kv, 64, 64, fmt, seed=2)).fill(seed=8)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = (torch.randn(T, heads, 64, generator=g, device="cuda") * 2.0 ** power).bfloat16()
+    out = torch.empty_like(q)
+    moe.moe_attention(o, c.desc, c.batch(new, lens), q, out)
+    ok(o)
+    assert torch.isfinite(out).all()
+    at = 0
+    for b, (n, t) in enumerate(zip(new, lens)):
+        k, v = (x.repeat_interleave(heads // kv, 1).permute(1, 0, 2) for x in c.values(b, t))
+        qq = q[at:at + n].double().permute(1, 0, 2)
+        s = qq @ k.transpose(1, 2) / 8
+        mag = (qq.abs() @ k.abs().transpose(1, 2) / 8).amax(-1)
+        see = torch.arange(t, device="cuda")[None] <= torch.arange(t - n, t, device="cuda")[:, None]
+        s = torch.where(see, s, -math.inf)
+        top = s.topk(2, -1) if t > 1 else None
+        clear = top.values[..., 0] - top.values[..., 1] > mag * 2.0 ** -18 + 40                  # e^-40: nothing in bf16
+        want = v.gather(1, top.indices[..., :1].expand(-1, -1, 64))
+        err = (out[at:at + n].double().permute(1, 0, 2) - want).abs()
+        assert clear.float().mean() > 0.5
+        assert (err <= want.abs() * (2.0 ** -8 + 2.0 ** -10) + v.abs().amax() * 1e-12)[clear].all()
+        at += n
