@@ -4,10 +4,10 @@
 // 4 D multiply-adds a (row, key) pair, both products as kind::f16 MMAs of 128 rows
 // with fp32 accumulators in tensor memory.  What bounds it: a tile of 128 keys moves
 // 320 KB through shared memory (192 KB of it MMA operands), 2,500 cycles at 128
-// bytes a cycle, where the MMAs need 2,048; it takes 4,200, because a row tile's
+// bytes a cycle, where the MMAs need 2,048; it takes 4,000, because a row tile's
 // softmax (2,300) and its MMAs (1,300) wait for one another and only the other row
 // tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
-// heads: 287 us, 953 TFLOP/s (0.51 of the measured bf16 rate).
+// heads: 275 us, 995 TFLOP/s (0.52 of the measured bf16 rate).
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.
@@ -28,8 +28,9 @@
 //    goes through as several, one block each.
 //  - In 4 bits a token's groups have scales of their own, which go into the f16 operands:
 //    K's relative to the largest of a tile (Pass), V's to units of 32 columns of O each, so
-//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 305 us (350
-//    before V's operands were stored without bank conflicts, 324 with a call at every wait).
+//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 285 us (350
+//    before V's operands were stored without bank conflicts, 324 with a call at every wait, 305 with both
+//    forms of a score's rounding in one loop).
 #include <cstdint>
 
 #include "attn_device.cuh"
@@ -866,12 +867,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     const float off = lg2(ratio) - m + kRoom;
                     uint32_t v[32], p[16];
                     take(g, v, kv.x);
-                    const float2 cc = make_float2(c, c), oo = make_float2(off, off);
+                    if (far)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]), c));
+                    const float by = far ? 1.0f : c;
+                    const float2 cc = make_float2(by, by), oo = make_float2(off, off);
                     float2 part[2];
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         const float2 x = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                        float2 z = far ? make_float2(__fadd_rn(__fmul_rn(x.x, c), off), __fadd_rn(__fmul_rn(x.y, c), off)) : fma2(x, cc, oo);
+                        float2 z = fma2(x, cc, oo);
                         z.x = ex2(z.x);
                         z.y = ex2(z.y);
                         part[k / 2 & 1] = k > 2 ? add2(part[k / 2 & 1], z) : z;
