@@ -4,10 +4,11 @@
 // 4 D multiply-adds a (row, key) pair, both products as kind::f16 MMAs of 128 rows
 // with fp32 accumulators in tensor memory.  What bounds it: a tile of 128 keys moves
 // 320 KB through shared memory (192 KB of it MMA operands), 2,500 cycles at 128
-// bytes a cycle, where the MMAs need 2,048; it takes 4,000, because a row tile's
-// softmax (2,300) and its MMAs (1,300) wait for one another and only the other row
-// tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
-// heads: 275 us, 995 TFLOP/s (0.52 of the measured bf16 rate).
+// bytes a cycle, where the MMAs need 2,048; it takes 3,900, because a row tile's
+// softmax and its MMAs (1,300) wait for one another, but for the first half of P V, and
+// otherwise only the other row tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
+// heads: 265 us, 1,031 TFLOP/s (0.54 of the measured bf16 rate); 275 with P handed over
+// whole, 264.6 in quarters.
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.
@@ -28,7 +29,7 @@
 //    goes through as several, one block each.
 //  - In 4 bits a token's groups have scales of their own, which go into the f16 operands:
 //    K's relative to the largest of a tile (Pass), V's to units of 32 columns of O each, so
-//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 285 us (350
+//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 280 us (350
 //    before V's operands were stored without bank conflicts, 324 with a call at every wait, 305 with both
 //    forms of a score's rounding in one loop).
 #include <cstdint>
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
 
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
     uint64_t *raw_full = bar, *raw_empty = bar + 2, *k_full = bar + 4, *k_empty = bar + 6, *v_full = bar + 8, *v_empty = bar + 10;
-    uint64_t *s_full = bar + 12, *p_full = bar + 14, *o_full = bar + 16, *q_full = bar + 18;
+    uint64_t *s_full = bar + 12, *p_full = bar + 14, *o_full = bar + 16, *q_full = bar + 18, *p_half = bar + 20;
     float2* sc = reinterpret_cast<float2*>(sm + L::OFF_SC);
     int* info = reinterpret_cast<int*>(sm + L::OFF_INFO);
 
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             tc::mbar_init(v_full + i, L::CONVERT);
             tc::mbar_init(v_empty + i, na);
             tc::mbar_init(s_full + i, 1);
+            tc::mbar_init(p_half + i, 8);
             tc::mbar_init(p_full + i, 8);
             tc::mbar_init(o_full + i, 1);
         }
@@ -558,16 +560,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             const bool last = info[t % kRing] & 1;
             wait(v_full + st, (uint32_t)(t >> 1 & 1), status);
             for (int x = 0; x < na; ++x) {
-                wait(p_full + x, (uint32_t)(t & 1), status);
-                tc::tc_fence_after();
-                {
+                // the first 32 of every 64 keys, then the others
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
+                for (int g = 0; g < 2; ++g) {
+                    wait((g ? p_full : p_half) + x, (uint32_t)(t & 1), status);
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = i / 2 * 4 + 2 * g + i % 2;
                         mma_ts(one, tmem + 256 + x * 128, tmem + x * 128 + 8 * k + (k >= 4 ? 32 : 0), vd + (st * L::OP + 256 * k >> 4), id_o, t > 0 || k > 0);
-                    commit(one, v_empty + st);
-                    if (last)
-                        commit(one, o_full + x);
+                    }
                 }
+                commit(one, v_empty + st);
+                if (last)
+                    commit(one, o_full + x);
                 __syncwarp();
                 if (!last)
                     scores(x, t + 1);
@@ -889,12 +895,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                     else if (pass.flags & kCount)
                         l += both.x + both.y;
                     tm_st16(ts + 16 * g, p);
+                    tm_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive((g ? p_full : p_half) + x);
                 }
-                tm_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(p_full + x);
                 if (word & 1)
                     break;
             }
