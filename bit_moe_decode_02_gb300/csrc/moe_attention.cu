@@ -1268,27 +1268,21 @@ static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaS
 
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
-    // Against 128 keys the decode kernel spends 0.62 us of an SM on 16 rows (D = 64;
-    // 0.86 for 128), spread over all SMs; the prompt kernel 1.45 us (2.2) on up to
-    // 128 rows and 1.4 times that on 256, on one SM each.  The ratio is 2.3 to 2.6,
-    // taken as 2.5.  Measured, decode / prompt kernel: 8 sequences of 4,000 keys, 64
-    // heads of 64 on 8: 64 rows 48 / 68 us, 106 rows 74 / 73, 217 rows 133 / 88; one
-    // such sequence, 432 rows: 57 / 81; 64 of them, 32 rows 140 / 180, 64 rows 263 / 182.
-    // The lengths are on the device, so the rule sees their average alone.  The same heads, 63
-    // single tokens and a prompt of 1,000 over 4,000 keys each: 267 us in one call, 80 + 117
-    // in two; 255 and a prompt of 600 over 1,000 keys: 213 us, 88 + 27 in two.
+    // Both kernels' costs, in tenths of what the decode kernel spends of an SM on 16 rows against 128 keys (8 bits: 0.55 us
+    // for D = 64, 0.72 for 128; 4 bits: 0.52, 0.79).  It spreads them over all SMs, beside some 10 us whatever the work; the
+    // prompt kernel takes up to 128 rows and, in 1.2 to 1.3 times that, up to 256 on one SM each.  Measured over 4,000 keys,
+    // decode / prompt kernel, 8 bits and 4: 8 sequences, 64 heads of 64 on 8: 64 rows 44 / 44 and 44 / 48 us, 80 rows 51 / 45
+    // and 50 / 48, 216 rows 119 / 58 and 115 / 59; one such sequence, 432 rows: 44 / 60 and 43 / 62; 64 of them, 32 rows
+    // 131 / 172 and 127 / 232, 64 rows 244 / 172 and 234 / 233; 8 sequences, 32 heads of 128 on 4: 104 rows 54 / 54 and
+    // 60 / 57, 128 rows 58 / 55 and 64 / 57, 216 rows 87 / 66 and 96 / 68.
+    // The lengths are on the device, so the rule sees their average alone.  64 heads of 64 on 8 in 8 bits, 63 single tokens
+    // and a prompt of 1,000 over 4,000 keys each: 235 us in one call, 72 + 103 in two; 255 and a prompt of 600 over 1,000
+    // keys: 199 us, 80 + 25 in two.
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
     const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
-    long long decode = 10 * heads * ((rows + 15) / 16), prompt = (rows > 128 ? 35 : 25) * waves * num_sms;
-    if (a.c.fmt == MOE_KV_MXFP4) {
-        // Codes cost the decode kernel less here (D = 64: 0.33 us for 16 rows and 128 keys, 0.56 for 128), beside
-        // about 12 us whatever the work; the prompt kernel 1.65 us up to 128 rows and 2.1 on 256 (1.95, 2.4).  8
-        // sequences of 4,000 keys, 64 heads of 64 on 8: 64 rows 44 / 52 us, 104 rows 65 / 52, 216 rows 115 / 66; one
-        // such sequence, 432 rows: 42 / 69; 32 heads of 128 on 4: 8 sequences, 64 rows 42 / 61, 128 rows 64 / 63, 256
-        // rows 107 / 75.
-        decode += a.c.D == 64 ? 1000 : 600;
-        prompt = (a.c.D == 64 ? (rows > 128 ? 41 : 32) : rows > 128 ? 28 : 22) * waves * num_sms;
-    }
+    const bool mx = a.c.fmt == MOE_KV_MXFP4, two = rows > 128;
+    const long long decode = 10 * heads * ((rows + 15) / 16) + (a.c.D == 128 ? 1000 : mx ? 1300 : 700);
+    const long long prompt = (a.c.D == 128 ? (two ? 27 : mx ? 22 : 23) : mx ? (two ? 35 : 29) : two ? 32 : 25) * waves * num_sms;
     return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
