@@ -529,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 id = next;
                 s = scales_of(id);
             }
+            // nothing is on its way when the kernel ends, whoever gave up
+            for (int v = 0; v < 2 && t > 0; ++v)
+                wait(raw_full + v, (uint32_t)((t - 1) & 1), status);
         }
     } else if (warp == 1) {
         // ---- MMAs, the row tiles in turn: P V of a tile of keys and the scores of the
