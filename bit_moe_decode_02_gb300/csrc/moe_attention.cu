@@ -40,6 +40,7 @@
 // (one for two codes, at half rate) and products with scales are a third.  With items of 16
 // rows, as in 8 bits, and 12 warps 149 us, with 8 warps 159; one sequence of 6,070 tokens
 // 11.4 us, the same way through.
+#include <algorithm>
 #include <cstdint>
 
 #include "attn_device.cuh"
@@ -1242,7 +1243,8 @@ void launch_format(const AttnArgs& a, int num_sms, cudaStream_t s)
 
 size_t attention_workspace_bytes(int num_sms)
 {
-    return kCounterBytes + (size_t)num_sms * (2 + kMaxGroups) * slot_floats() * sizeof(float);
+    const size_t decode = kCounterBytes + (size_t)num_sms * (2 + kMaxGroups) * slot_floats() * sizeof(float);
+    return std::max(decode, prompt_workspace_bytes(num_sms));
 }
 
 cudaError_t prepare_attention_kernels()
@@ -1269,20 +1271,25 @@ static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaS
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     // Both kernels' costs, in tenths of what the decode kernel spends of an SM on 16 rows against 128 keys (8 bits: 0.55 us
-    // for D = 64, 0.72 for 128; 4 bits: 0.52, 0.79).  It spreads them over all SMs, beside some 10 us whatever the work; the
-    // prompt kernel takes up to 128 rows and, in 1.2 to 1.3 times that, up to 256 on one SM each.  Measured over 4,000 keys,
-    // decode / prompt kernel, 8 bits and 4: 8 sequences, 64 heads of 64 on 8: 64 rows 44 / 44 and 44 / 48 us, 80 rows 51 / 45
-    // and 50 / 48, 216 rows 119 / 58 and 115 / 59; one such sequence, 432 rows: 44 / 60 and 43 / 62; 64 of them, 32 rows
-    // 131 / 172 and 127 / 232, 64 rows 244 / 172 and 234 / 233; 8 sequences, 32 heads of 128 on 4: 104 rows 54 / 54 and
-    // 60 / 57, 128 rows 58 / 55 and 64 / 57, 216 rows 87 / 66 and 96 / 68.
+    // for D = 64, 0.72 for 128; 4 bits: 0.52, 0.79).  It spreads them over all SMs, beside some 10 us whatever the work (less in items of 8 rows); the
+    // prompt kernel takes up to 128 rows and, in 1.2 to 1.3 times that, up to 256 on one SM each, or their keys in parts
+    // on several with 10 to 15 us beside.  Measured over 4,000 keys, decode / prompt kernel, 8 bits and 4: 64 heads of 64 on
+    // 8, 8 sequences: 48 rows 37 / 29 and 37 / 32 us, 80 rows 51 / 44 and 51 / 49, 216 rows 119 / 58 and 115 / 60; one such
+    // sequence, 32 rows 18 / 15 and 17 / 16, 432 rows 44 / 25 and 43 / 27; 64 of them, 32 rows 131 / 172 and 127 / 236, 64
+    // rows 244 / 172 and 235 / 237; 32 heads of 128 on 4, 8 sequences: 32 rows 30 / 32 and 34 / 32, 64 rows 38 / 25 and
+    // 43 / 26, 216 rows 87 / 44 and 96 / 44.
     // The lengths are on the device, so the rule sees their average alone.  64 heads of 64 on 8 in 8 bits, 63 single tokens
-    // and a prompt of 1,000 over 4,000 keys each: 235 us in one call, 72 + 103 in two; 255 and a prompt of 600 over 1,000
-    // keys: 199 us, 80 + 25 in two.
+    // and a prompt of 1,000 over 4,000 keys each: 236 us in one call, 72 + 103 in two; 255 and a prompt of 600 over 1,000
+    // keys: 199 us, 80 + 25 in two.  Nor does it see how many keys there are: one sequence of 600, 64 heads of 64 on 8,
+    // 64 rows in 4 bits: 10 / 15.
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
-    const long long heads = (long long)a.c.n_seqs * a.c.H, waves = (heads * ((rows + 255) / 256) + num_sms - 1) / num_sms;
-    const bool mx = a.c.fmt == MOE_KV_MXFP4, two = rows > 128;
-    const long long decode = 10 * heads * ((rows + 15) / 16) + (a.c.D == 128 ? 1000 : mx ? 1300 : 700);
-    const long long prompt = (a.c.D == 128 ? (two ? 27 : mx ? 22 : 23) : mx ? (two ? 35 : 29) : two ? 32 : 25) * waves * num_sms;
+    const long long heads = (long long)a.c.n_seqs * a.c.H, groups = heads * ((rows + 255) / 256);
+    const int cut = prompt_cut(a, num_sms);
+    const long long rounds = (groups * cut + num_sms - 1) / num_sms;
+    const bool mx = a.c.fmt == MOE_KV_MXFP4, wide = a.c.D == 128, two = rows > 128;
+    const long long decode = 10 * heads * ((rows + 15) / 16) + (mx && rows <= 8 ? 600 : wide || mx ? 1000 : 700);
+    const long long each = wide ? (two ? 27 : mx ? 22 : 23) : mx ? (two ? 35 : 29) : two ? 32 : 25;
+    const long long prompt = each * rounds * num_sms / cut + (cut == 1 ? 0 : mx ? (wide ? 800 : 900) : wide ? 1000 : 700);
     return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 

@@ -21,6 +21,9 @@
 //  - Tensor memory: S0 S1 O0 O1, 128 columns each.  P replaces the scores it comes
 //    from, as f16 (64 keys' in columns 0-31, the others' in 64-95), and is the second
 //    product's A operand from there.
+//  - Few groups of rows leave SMs idle: then the keys of each are cut into parts (prompt_cut; four tiles at
+//    least), a CTA each, whose results a second kernel joins in their order.  One sequence of 4,000 keys, 64 heads
+//    of 64 on 8, 80 tokens: 27 us, 60 by a CTA a group; 8 of them, 32 heads of 128 on 4, 8 tokens: 25 and 53.
 //  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
 //    scores, V's enters the exponent; O is rescaled in tensor memory only where a
 //    row's maximum grows by more than 2^8, or the unit changes.  The unit is the
@@ -45,6 +48,7 @@ using namespace attn;
 constexpr int kThreads = 768;
 constexpr int kRows = 256;                // of a CTA
 constexpr int kKeys = 128;                // of a tile
+constexpr int kPartTiles = 4;             // a part of a group's keys has that many tiles at least
 constexpr int kRing = 8;                  // tiles whose scales are kept: the loads are at most four ahead of the softmax
 
 // A pass of a tile over a 4-bit cache: which of its keys take part, what their K's are scaled
@@ -235,6 +239,27 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int idx, Work& w)
     return false;
 }
 
+// The rows of a group, and the tiles of keys that they see.
+struct Extent {
+    int rows;                             // of 256
+    int pos0, pos1;                       // of the first and the last token
+    int tile0, tiles;
+    __device__ __forceinline__ Extent(const AttnArgs& a, const Work& w)
+    {
+        rows = min(w.n * a.group - w.rt * kRows, kRows);
+        pos0 = w.len - w.n + w.rt * kRows / a.group;
+        pos1 = w.len - w.n + (w.rt * kRows + rows - 1) / a.group;
+        tile0 = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kKeys : 0;
+        tiles = pos1 / kKeys - tile0 + 1;
+    }
+    // how many CTAs share them, of `most`
+    __device__ __forceinline__ int parts(int most) const { return max(min(most, tiles / kPartTiles), 1); }
+};
+
+// A part's results: its 256 rows of O over their own sums, four columns of all rows after
+// another, then the rows' maxima and sums.
+__host__ __device__ constexpr int part_floats(int d) { return kRows * d + 2 * kRows; }
+
 // The producer of a 4-bit cache: a tile's raw records, and how it goes through.  Keys whose
 // largest scales are within 2^9 go together (K's f16 operand holds 2^36), the others in passes
 // of their own; V's groups each have a unit that O's 32 columns are kept in, which moves where
@@ -420,7 +445,7 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
 }
 
 template <int D, int FMT, int BLK>
-__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, int cut)
 {
     using L = Layout<D, FMT, BLK>;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -428,8 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* status = a.c.status;
     Work w;
-    if (!find_work(a, blockIdx.x, w))
+    const int item = blockIdx.x / cut, part = blockIdx.x % cut;
+    if (!find_work(a, item, w))
         return;
+    const Extent e(a, w);
+    const int parts = e.parts(cut);
+    if (part >= parts)
+        return;
+    if (cut > 1)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
     uint64_t *raw_full = bar, *raw_empty = bar + 2, *k_full = bar + 4, *k_empty = bar + 6, *v_full = bar + 8, *v_empty = bar + 10;
@@ -437,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
     float2* sc = reinterpret_cast<float2*>(sm + L::OFF_SC);
     int* info = reinterpret_cast<int*>(sm + L::OFF_INFO);
 
-    const int rows = min(w.n * a.group - w.rt * kRows, kRows), na = rows > 128 ? 2 : 1;     // row tiles with rows
-    const int i0 = w.rt * kRows / a.group, i1 = (w.rt * kRows + rows - 1) / a.group;        // first and last token
-    const int pos0 = w.len - w.n + i0, pos1 = w.len - w.n + i1;
-    const int tile0 = a.window > 0 && pos0 >= a.window ? (pos0 - a.window + 1) / kKeys : 0, nt = pos1 / kKeys - tile0 + 1;
+    const int rows = e.rows, na = rows > 128 ? 2 : 1;                                       // row tiles with rows
+    const int pos0 = e.pos0, pos1 = e.pos1;
+    const int skip = (int)((long long)e.tiles * part / parts);
+    const int tile0 = e.tile0 + skip, nt = (int)((long long)e.tiles * (part + 1) / parts) - skip;
     // `info` says which tile is the last one; this bounds the loops should a wait have given up
     const int most = nt * (L::MX ? 256 : L::NB);
     Pass* passes = reinterpret_cast<Pass*>(sm + L::OFF_PASS);
@@ -914,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
             l = (l + *other) * kUnroom;
             wait(o_full + x, 0, status);
             tc::tc_fence_after();
-            const Final fin = finish(m, l, a.sinks, hq);
+            const Final fin = parts > 1 ? Final{l == 0.0f ? 0.0f : 1.0f / l, 0.0f} : finish(m, l, a.sinks, hq);
+            float* share = reinterpret_cast<float*>(a.ws + kCounterBytes) + ((long long)item * cut + part) * part_floats(D);
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
@@ -922,7 +955,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                 uint32_t v[32];
                 tm_ld32(to + 32 * ch, v);
                 tm_wait_ld(v);
-                if (in)
+                if (parts > 1) {
+                    if (in)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4*>(share + ((half * (D / 8) + 8 * ch + k / 4) * kRows + x * 128 + r) * 4) =
+                                make_float4(__uint_as_float(v[k]) * mul, __uint_as_float(v[k + 1]) * mul, __uint_as_float(v[k + 2]) * mul,
+                                            __uint_as_float(v[k + 3]) * mul);
+                } else if (in)
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
                         uint32_t o[4];
@@ -932,7 +972,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
                         *reinterpret_cast<uint4*>(out + 32 * ch + k) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
             }
-            if (a.lse && in && half == 0)
+            if (parts > 1 && in && half == 0)
+                *reinterpret_cast<float2*>(share + kRows * D + 2 * (x * 128 + r)) = make_float2(m, l);
+            if (parts == 1 && a.lse && in && half == 0)
                 a.lse[(long long)(w.c0 + i) * a.q_heads + hq] = fin.lse;
         }
     }
@@ -944,7 +986,56 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-typedef void (*Kernel)(AttnArgs);
+// Joins the parts of every group that has several, in their order: 32 rows a CTA, a warp for
+// D / 8 columns of them.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, int cut)
+{
+    constexpr int N = D / 32;             // float4 of a thread
+    const int item = blockIdx.x / 8, row = blockIdx.x % 8 * 32 + (threadIdx.x & 31), at = threadIdx.x / 32 * N;
+    Work w;
+    const bool found = find_work(a, item, w);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!found)
+        return;
+    const Extent e(a, w);
+    const int parts = e.parts(cut);
+    if (parts == 1 || row >= e.rows)
+        return;
+    const float* share = reinterpret_cast<const float*>(a.ws + kCounterBytes) + (long long)item * cut * part_floats(D);
+    auto ml_of = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(share + (long long)p * part_floats(D) + kRows * D + 2 * row)); };
+    float M = kNone, L = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p)
+        M = fmaxf(M, ml_of(p).x);
+    float4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float2 ml = ml_of(p);
+        const float f = ml.y * ex2(ml.x - M);
+        L += f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(share + (long long)p * part_floats(D) + ((at + k) * kRows + row) * 4));
+            v[k].x += y.x * f, v[k].y += y.y * f, v[k].z += y.z * f, v[k].w += y.w * f;
+        }
+    }
+    const int i = (w.rt * kRows + row) / a.group, hq = w.h * a.group + (w.rt * kRows + row) % a.group;
+    const Final fin = finish(M, L, a.sinks, hq);
+    uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + 4 * at;
+#pragma unroll
+    for (int k = 0; k < N; k += 2)
+        *reinterpret_cast<uint4*>(out + 4 * k) =
+            make_uint4(kv::bf16x2(v[k].x * fin.mul, v[k].y * fin.mul), kv::bf16x2(v[k].z * fin.mul, v[k].w * fin.mul),
+                       kv::bf16x2(v[k + 1].x * fin.mul, v[k + 1].y * fin.mul), kv::bf16x2(v[k + 1].z * fin.mul, v[k + 1].w * fin.mul));
+    if (a.lse && at == 0)
+        a.lse[(long long)(w.c0 + i) * a.q_heads + hq] = fin.lse;
+}
+
+typedef void (*Kernel)(AttnArgs, int);
 
 template <int D, int FMT>
 Kernel pick(int blk)
@@ -982,12 +1073,43 @@ cudaError_t prepare_prompt_kernels()
     return cudaSuccess;
 }
 
-cudaError_t launch_attention_prompt(const AttnArgs& a, int, cudaStream_t s)
+size_t prompt_workspace_bytes(int num_sms) { return kCounterBytes + (size_t)num_sms * part_floats(128) * sizeof(float); }
+
+// An upper bound on the groups of 256 rows.
+static long long groups_of(const AttnArgs& a)
 {
-    // an upper bound on the groups of 256 rows: CTAs beyond the last one end at once
-    const long long groups = ((long long)a.c.n_tokens * a.group / kRows + a.c.n_seqs) * a.c.H;
-    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)groups, kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a);
-    return cudaGetLastError();
+    const long long seqs = a.c.n_seqs < a.c.n_tokens ? a.c.n_seqs : a.c.n_tokens;
+    return ((long long)a.c.n_tokens * a.group + (kRows - 1) * seqs) / kRows * a.c.H;
+}
+
+// Into how many parts each group's keys are cut where the groups leave SMs idle: one part an SM, for which the
+// workspace has room.  (Up to two, in the fewest rounds, is slower more often than not: 8 sequences of 4,000 keys, 32
+// heads of 128 on 4, 80 and 216 rows 37 and 52 us for 30 and 44.)
+int prompt_cut(const AttnArgs& a, int num_sms)
+{
+    const long long groups = groups_of(a);
+    return groups < num_sms ? (int)(num_sms / groups) : 1;
+}
+
+cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s)
+{
+    // CTAs beyond the last group or its last part end at once
+    const long long groups = groups_of(a);
+    const int cut = prompt_cut(a, num_sms);
+    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)(groups * cut), kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a, cut);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || cut == 1)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(groups * (kRows / 32)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, a.c.D == 64 ? prompt_join_kernel<64> : prompt_join_kernel<128>, a, cut);
 }
 
 }  // namespace moe
