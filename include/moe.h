@@ -427,8 +427,8 @@ void moe_destroy(moe_handle* h);
  * (status codes, checks before anything is enqueued, streams, one thread and
  * one stream at a time per handle, nothing allocated by a call, no host work
  * that depends on device values) hold for it too.  Each call is one launch
- * (moe_linear: one for each pass of up to 16 tokens; moe_lora: two) and can be captured in a CUDA
- * graph.  What a device-side check finds (metadata that does not describe the
+ * (moe_linear: one for each pass of up to 16 tokens; moe_lora: two; moe_attention: two where few rows
+ * share out many keys) and can be captured in a CUDA graph.  What a device-side check finds (metadata that does not describe the
  * batch, a block number outside the cache) sets MOE_ERR_DEVICE_FAULT in the
  * handle's status word and skips that sequence or block.
  * ====================================================================== */
