@@ -1284,12 +1284,14 @@ cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
     // 64 rows in 4 bits: 10 / 15.
     const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
     const long long heads = (long long)a.c.n_seqs * a.c.H, groups = heads * ((rows + 255) / 256);
-    const int cut = prompt_cut(a, num_sms);
-    const long long rounds = (groups * cut + num_sms - 1) / num_sms;
+    const PromptCut cut = prompt_cut(a, num_sms);
+    const long long whole = groups < cut.whole ? groups : cut.whole, rest = (groups - whole) * cut.parts;
+    const long long full = (whole + num_sms - 1) / num_sms, part = (rest + num_sms - 1) / num_sms;       // rounds
     const bool mx = a.c.fmt == MOE_KV_MXFP4, wide = a.c.D == 128, two = rows > 128;
     const long long decode = 10 * heads * ((rows + 15) / 16) + (mx && rows <= 8 ? 600 : wide || mx ? 1000 : 700);
     const long long each = wide ? (two ? 27 : mx ? 22 : 23) : mx ? (two ? 35 : 29) : two ? 32 : 25;
-    const long long prompt = each * rounds * num_sms / cut + (cut == 1 ? 0 : mx ? (wide ? 800 : 900) : wide ? 1000 : 700);
+    const long long prompt = each * num_sms * full + each * num_sms * part / cut.parts +
+                             (part == 0 ? 0 : mx ? (wide ? 800 : 900) : wide ? 1000 : 700);
     return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 

@@ -7,8 +7,8 @@
 // bytes a cycle, where the MMAs need 2,048; it takes 3,900, because a row tile's
 // softmax and its MMAs (1,300) wait for one another, but for the first half of P V, and
 // otherwise only the other row tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
-// heads: 265 us, 1,031 TFLOP/s (0.54 of the measured bf16 rate); 275 with P handed over
-// whole, 264.6 in quarters.
+// heads: 261 us, 1,050 TFLOP/s (0.55 of the measured bf16 rate); 275 with P handed over
+// whole instead of 266 in halves and 264.6 in quarters.
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
 //    the tiles, whatever their number.
@@ -21,9 +21,10 @@
 //  - Tensor memory: S0 S1 O0 O1, 128 columns each.  P replaces the scores it comes
 //    from, as f16 (64 keys' in columns 0-31, the others' in 64-95), and is the second
 //    product's A operand from there.
-//  - Few groups of rows leave SMs idle: then the keys of each are cut into parts (prompt_cut; four tiles at
-//    least), a CTA each, whose results a second kernel joins in their order.  One sequence of 4,000 keys, 64 heads
-//    of 64 on 8, 80 tokens: 27 us, 60 by a CTA a group; 8 of them, 32 heads of 128 on 4, 8 tokens: 25 and 53.
+//  - Few groups of rows leave SMs idle, or the last ones of many do: then the keys of each of those are cut into
+//    parts (prompt_cut; four tiles at least), a CTA each, whose results a second kernel joins in their order.
+//    One sequence of 4,000 keys, 64 heads of 64 on 8, 80 tokens: 27 us, 60 by a CTA a group; 8 of them, 32 heads
+//    of 128 on 4, 8 tokens: 25 and 53; 160 groups 65 and 85; the two prompts above 261 and 266.
 //  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
 //    scores, V's enters the exponent; O is rescaled in tensor memory only where a
 //    row's maximum grows by more than 2^8, or the unit changes.  The unit is the
@@ -32,7 +33,7 @@
 //    goes through as several, one block each.
 //  - In 4 bits a token's groups have scales of their own, which go into the f16 operands:
 //    K's relative to the largest of a tile (Pass), V's to units of 32 columns of O each, so
-//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 280 us (350
+//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 273 us (350
 //    before V's operands were stored without bank conflicts, 324 with a call at every wait, 305 with both
 //    forms of a score's rounding in one loop).
 #include <cstdint>
@@ -445,7 +446,7 @@ __device__ __forceinline__ void mx_produce(const AttnArgs& a, const Work& w, Pas
 }
 
 template <int D, int FMT, int BLK>
-__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, int cut)
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, PromptCut cut)
 {
     using L = Layout<D, FMT, BLK>;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -453,14 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, in
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* status = a.c.status;
     Work w;
-    const int item = blockIdx.x / cut, part = blockIdx.x % cut;
+    const int after = (int)blockIdx.x - cut.whole;
+    const int item = after < 0 ? blockIdx.x : cut.whole + after / cut.parts, part = after < 0 ? 0 : after % cut.parts;
     if (!find_work(a, item, w))
         return;
     const Extent e(a, w);
-    const int parts = e.parts(cut);
+    const int parts = after < 0 ? 1 : e.parts(cut.parts);
     if (part >= parts)
         return;
-    if (cut > 1)
+    if (cut.parts > 1)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
@@ -947,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, in
             wait(o_full + x, 0, status);
             tc::tc_fence_after();
             const Final fin = parts > 1 ? Final{l == 0.0f ? 0.0f : 1.0f / l, 0.0f} : finish(m, l, a.sinks, hq);
-            float* share = reinterpret_cast<float*>(a.ws + kCounterBytes) + ((long long)item * cut + part) * part_floats(D);
+            float* share = reinterpret_cast<float*>(a.ws + kCounterBytes) + (long long)after * part_floats(D);
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
@@ -989,20 +991,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, in
 // Joins the parts of every group that has several, in their order: 32 rows a CTA, a warp for
 // D / 8 columns of them.
 template <int D>
-__global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, int cut)
+__global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut cut)
 {
     constexpr int N = D / 32;             // float4 of a thread
-    const int item = blockIdx.x / 8, row = blockIdx.x % 8 * 32 + (threadIdx.x & 31), at = threadIdx.x / 32 * N;
+    const int after = blockIdx.x / 8, row = blockIdx.x % 8 * 32 + (threadIdx.x & 31), at = threadIdx.x / 32 * N;
     Work w;
-    const bool found = find_work(a, item, w);
+    const bool found = find_work(a, cut.whole + after, w);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!found)
         return;
     const Extent e(a, w);
-    const int parts = e.parts(cut);
+    const int parts = e.parts(cut.parts);
     if (parts == 1 || row >= e.rows)
         return;
-    const float* share = reinterpret_cast<const float*>(a.ws + kCounterBytes) + (long long)item * cut * part_floats(D);
+    const float* share = reinterpret_cast<const float*>(a.ws + kCounterBytes) + (long long)after * cut.parts * part_floats(D);
     auto ml_of = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(share + (long long)p * part_floats(D) + kRows * D + 2 * row)); };
     float M = kNone, L = 0.0f;
 #pragma unroll 4
@@ -1035,7 +1037,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, int cut)
         a.lse[(long long)(w.c0 + i) * a.q_heads + hq] = fin.lse;
 }
 
-typedef void (*Kernel)(AttnArgs, int);
+typedef void (*Kernel)(AttnArgs, PromptCut);
 
 template <int D, int FMT>
 Kernel pick(int blk)
@@ -1082,26 +1084,26 @@ static long long groups_of(const AttnArgs& a)
     return ((long long)a.c.n_tokens * a.group + (kRows - 1) * seqs) / kRows * a.c.H;
 }
 
-// Into how many parts each group's keys are cut where the groups leave SMs idle: one part an SM, for which the
-// workspace has room.  (Up to two, in the fewest rounds, is slower more often than not: 8 sequences of 4,000 keys, 32
-// heads of 128 on 4, 80 and 216 rows 37 and 52 us for 30 and 44.)
-int prompt_cut(const AttnArgs& a, int num_sms)
+// Which groups' keys are cut, and into how many parts: those that would be the last round of CTAs and leave SMs idle,
+// one part an SM, for which the workspace has room.  (Up to two, in the fewest rounds, is slower more often than not: 8
+// sequences of 4,000 keys, 32 heads of 128 on 4, 80 and 216 rows 37 and 52 us for 30 and 44.)
+PromptCut prompt_cut(const AttnArgs& a, int num_sms)
 {
-    const long long groups = groups_of(a);
-    return groups < num_sms ? (int)(num_sms / groups) : 1;
+    const long long groups = groups_of(a), rest = groups % num_sms;
+    const int parts = rest > 0 ? (int)(num_sms / rest) : 1;
+    return PromptCut{(int)(parts > 1 ? groups - rest : groups), parts, (int)(parts > 1 ? rest : 0)};
 }
 
 cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     // CTAs beyond the last group or its last part end at once
-    const long long groups = groups_of(a);
-    const int cut = prompt_cut(a, num_sms);
-    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)(groups * cut), kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a, cut);
+    const PromptCut cut = prompt_cut(a, num_sms);
+    kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)(cut.whole + cut.rest * cut.parts), kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a, cut);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || cut == 1)
+    if (e != cudaSuccess || cut.rest == 0)
         return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(groups * (kRows / 32)));
+    cfg.gridDim = dim3((unsigned)(cut.rest * (kRows / 32)));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at{};

@@ -61,7 +61,11 @@ struct AttnArgs {
 cudaError_t prepare_attention_kernels();
 cudaError_t prepare_prompt_kernels();
 cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s);
-int prompt_cut(const AttnArgs& a, int num_sms);
+// Groups of 256 rows of the prompt kernel: `whole` by a CTA each, `rest` more in up to `parts` parts each.
+struct PromptCut {
+    int whole, parts, rest;
+};
+PromptCut prompt_cut(const AttnArgs& a, int num_sms);
 size_t prompt_workspace_bytes(int num_sms);
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s);
 

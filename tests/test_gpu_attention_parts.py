@@ -40,6 +40,8 @@ def check(fmt, *args, **kw):
     (32, 4, [16, 0, 40, 1], [1100, 300, 2049, 1537], 0),              # parts of some, none of others
     (32, 4, [1, 60, 13], [5000, 60, 1024], 1300),
     (12, 4, [200], [1700], 0),                                        # three heads a kv head: tokens across groups of rows
+    (64, 8, [700], [3000], 0),                                        # more groups than SMs: the last 24 in parts
+    (64, 8, [700, 90], [1500, 2600], 900),                            # the last 56 of 208 by the bound on their number
 ])
 def test_parts(fmt, blk, D, heads, kv, new, lens, window):
     c = make(fmt, lens, kv, D, blk)
