@@ -109,6 +109,14 @@ bool rows_overlap(const Rows& a, const Rows& b, int n, int size)
     d += d < 0 ? pitch : 0;
     return !(d >= a.width * size && pitch - d >= b.width * size);
 }
+// The same for rows and one contiguous array.
+bool rows_overlap(const Rows& a, int n, int size, const void* p, long long bytes)
+{
+    if (!overlap(a.p, ((n - 1) * a.stride + a.width) * size, p, bytes))
+        return false;
+    const long long pitch = a.stride * size, d = (long long)((intptr_t)p - (intptr_t)a.p), at = d % pitch;
+    return d < 0 || at < a.width * size || at + bytes > pitch;
+}
 
 }  // namespace
 
@@ -391,6 +399,11 @@ int moe_rope(moe_ops* o, const moe_rope_table* r, const int* position, int n_tok
             if (!here && rows_overlap(out[i], in[j], n_tokens, size))
                 return set_error(MOE_ERR_INVALID_ARG, "moe_rope: %s overlaps %s (in place: the same rows)", names[i][1], names[j][0]);
         }
+    for (int i = 0; i < n; ++i) {
+        const bool at = rows_overlap(out[i], n_tokens, size, position, n_tokens * 4ll);
+        if (at || rows_overlap(out[i], n_tokens, size, r->turns, r->rot_dim / 2 * 8ll))
+            return set_error(MOE_ERR_INVALID_ARG, "moe_rope: %s overlaps %s", names[i][1], at ? "position" : "turns");
+    }
     if (n == 2 && rows_overlap(out[0], out[1], n_tokens, size))
         return set_error(MOE_ERR_INVALID_ARG, "moe_rope: q_out overlaps k_out");
     moe::RopeArgs a{r->turns, position, q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, n_tokens, q_heads,

@@ -631,7 +631,7 @@ typedef struct {
  * 0: none) by their positions, int32 [n_tokens]; a negative one leaves the row's output as
  * it is.  All of one type (moe_dtype), rows strides elements apart, 16-byte aligned, the
  * strides multiples of 16 bytes; the rows may be parts of a fused projection.  q_out may be
- * q and k_out k (the same rows, in place); else outputs must not overlap anything (checked).
+ * q and k_out k (the same rows, in place); else outputs must not overlap any array of the call (checked).
  * position * f_i / (2 pi) is kept modulo 1 in 64 bits, so an angle is off by no more than
  * position * 2^-55 turns beside fp32 rounding of what is left; cosine, sine and products
  * are fp32, the result is rounded once.  head_dim a multiple of 8, 8..512; rot_dim even,
