@@ -453,6 +453,11 @@ def moe_kv_batch_of(cu, kv_len, table, n_tokens) -> moe_kv_batch:
     return b
 
 
+def _word(handle) -> int:
+    """A handle as a 64-bit word: an address, None or what ctypes takes for a pointer (None: 0, which the library refuses)."""
+    return handle if type(handle) is int else ctypes.cast(handle, ctypes.c_void_p).value or 0
+
+
 _current = None
 
 
@@ -482,7 +487,7 @@ def moe_kv_write(o, cache, batch, k, v, stream=None):
     T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
     kp, ks = _heads(k, "k", T, H, D)
     vp, vs = _heads(v, "v", T, H, D)
-    rc = lib().moe_words_kv_write(_WORDS_KV(o, ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
+    rc = lib().moe_words_kv_write(_WORDS_KV(_word(o), ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
     return rc if rc == MOE_OK else _check(rc)
 
 
@@ -490,7 +495,7 @@ def moe_kv_read(o, cache, batch, k, v, stream=None):
     T, H, D = batch.n_tokens, cache.kv_heads, cache.head_dim
     kp, ks = _heads(k, "k", T, H, D)
     vp, vs = _heads(v, "v", T, H, D)
-    rc = lib().moe_words_kv_read(_WORDS_KV(o, ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
+    rc = lib().moe_words_kv_read(_WORDS_KV(_word(o), ctypes.addressof(cache), ctypes.addressof(batch), kp, ks, vp, vs, _raw_stream(stream, k)))
     return rc if rc == MOE_OK else _check(rc)
 
 
@@ -553,7 +558,7 @@ def moe_kv_plan(o, pool, n_new, kv_len, state, cu, kv_len_out, state_out, admitt
             raise ValueError("moe_kv_plan: n_tokens is needed where seq, position and slot are None")
         n_tokens = t.shape[0]
     rc = lib().moe_words_kv_plan(_WORDS_PLAN(
-        o, ctypes.addressof(pool), _array(n_new, "n_new", i, n), _array(kv_len, "kv_len", i, n), _array(state, "state", i, 2), n_tokens,
+        _word(o), ctypes.addressof(pool), _array(n_new, "n_new", i, n), _array(kv_len, "kv_len", i, n), _array(state, "state", i, 2), n_tokens,
         _array(cu, "cu", i, n + 1), _array(kv_len_out, "kv_len_out", i, n), _array(state_out, "state_out", i, 2),
         0 if admitted is None else _array(admitted, "admitted", i, 1), 0 if seq is None else _array(seq, "seq", i, n_tokens),
         0 if position is None else _array(position, "position", i, n_tokens),
@@ -613,8 +618,8 @@ def moe_rope(o, rope, position, q, k=None, q_out=None, k_out=None, stream=None):
         kp = lp = kh = ks = ls = 0
     else:
         raise ValueError("moe_rope: k_out without k")
-    rc = lib().moe_words_rope(_WORDS_ROPE(o, ctypes.addressof(rope), pos, T, D, code, qp, qs, heads, op, os_, kp, ks, kh, lp, ls,
-                                          _raw_stream(stream, q)))
+    rc = lib().moe_words_rope(_WORDS_ROPE(_word(o), 0 if rope is None else ctypes.addressof(rope), pos, T, D, code, qp, qs, heads, op, os_,
+                                          kp, ks, kh, lp, ls, _raw_stream(stream, q)))
     return rc if rc == MOE_OK else _check(rc)
 
 
@@ -661,7 +666,7 @@ def moe_lora(o, w, index, x, y, out=None, stream=None):
         raise ValueError(f"moe_lora: y and out must be bf16 or fp32 (got {kind})")
     op, so = _out_rows(out, "out", kind, M, rows)
     yp, sy = (0, 0) if y is None else (op, so) if y is out else _out_rows(y, "y", kind, M, rows)
-    rc = lib().moe_words_lora(_WORDS_LORA(o, ctypes.addressof(w), at, x.data_ptr(), sx[0] if M > 1 else cols, M, yp, sy, op, so, code,
+    rc = lib().moe_words_lora(_WORDS_LORA(_word(o), ctypes.addressof(w), at, x.data_ptr(), sx[0] if M > 1 else cols, M, yp, sy, op, so, code,
                                           _raw_stream(stream, x)))
     return rc if rc == MOE_OK else _check(rc)
 
