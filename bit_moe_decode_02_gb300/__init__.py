@@ -654,6 +654,8 @@ def moe_lora(o, w, index, x, y, out=None, stream=None):
     rows, cols = w.rows, w.cols
     if out is None:
         out = y
+    if out is None:
+        raise ValueError("moe_lora: out is needed where y is None")
     M, kind, sx = x.shape[0], out.dtype, x.stride()
     at = _array(index, "index", i32, M)
     if x.dtype is not bf16 or x.shape != (M, cols) or not x.is_cuda or sx[1] != 1:

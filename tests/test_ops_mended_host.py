@@ -84,3 +84,10 @@ def test_rope_without_a_table(L, o):  # noqa: F811
     torch = pytest.importorskip("torch")
     with pytest.raises(moe.MoeError, match="moe_rope: the handle, the table"):
         moe.moe_rope(o, None, Fake(torch.int32, 3), Fake(torch.bfloat16, 3, 2, 64), stream=1)
+
+
+def test_adapters_without_an_output(o):  # noqa: F811
+    torch = pytest.importorskip("torch")
+    w = moe.moe_lora_weights(A, A, None, 1, 8, 64, 64)
+    with pytest.raises(ValueError, match="moe_lora: out"):
+        moe.moe_lora(o, w, Fake(torch.int32, 3), Fake(torch.bfloat16, 3, 64), None, stream=1)
