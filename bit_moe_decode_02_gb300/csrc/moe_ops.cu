@@ -328,8 +328,9 @@ int moe_rope_turns(const moe_rope_config* c, unsigned long long* turns)
         return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: unknown scaling %d", c->scaling);
     if (!(c->base > 1.0) || !std::isfinite(c->base))
         return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: base must be finite and above 1");
-    if (c->scaling != MOE_ROPE_PLAIN && (!(c->factor > 0.0) || !std::isfinite(c->factor)))
-        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: factor must be finite and positive");
+    // (a speed above 2^53 would have no fraction of a turn left, and its rest no place in 64 bits)
+    if (c->scaling != MOE_ROPE_PLAIN && (!(c->factor >= 0x1p-32) || !std::isfinite(c->factor)))
+        return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: factor must be finite and at least 2^-32");
     if (c->scaling > MOE_ROPE_LINEAR && (!(c->length > 0.0) || !(c->low > 0.0) || !(c->high > c->low) || !std::isfinite(c->length) ||
                                          !std::isfinite(c->high)))
         return set_error(MOE_ERR_INVALID_ARG, "moe_rope_turns: length and low must be positive and high above low, all finite");

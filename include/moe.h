@@ -602,7 +602,8 @@ typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype;
  * pair i; the others stay.  Pair i is (i, i + rot_dim / 2) or (2 i, 2 i + 1). */
 typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
 
-/* f_i = base^(-2 i / rot_dim), and for longer contexts than a model was trained on:
+/* f_i = base^(-2 i / rot_dim), and for longer contexts than a model was trained on (factor at
+ * least 2^-32):
  *   LINEAR      f_i / factor;
  *   PARTS       f_i (1 - x) + f_i / factor * x, x = (i - a) / max(b - a, 0.001) held to
  *               0..1, a = max(at(high), 0), b = min(at(low), rot_dim / 2 - 1),
@@ -631,11 +632,11 @@ typedef struct {
  * 0: none) by their positions, int32 [n_tokens]; a negative one leaves the row's output as
  * it is.  All of one type (moe_dtype), rows strides elements apart, 16-byte aligned, the
  * strides multiples of 16 bytes; the rows may be parts of a fused projection.  q_out may be
- * q and k_out k (the same rows, in place); else outputs must not overlap any array of the call (checked).
- * position * f_i / (2 pi) is kept modulo 1 in 64 bits, so an angle is off by no more than
- * position * 2^-55 turns beside fp32 rounding of what is left; cosine, sine and products
- * are fp32, the result is rounded once.  head_dim a multiple of 8, 8..512; rot_dim even,
- * 2..head_dim; n_tokens 1..2^20. */
+ * q and k_out k (the same rows, in place); else outputs must not overlap any array of the
+ * call (checked).  position * f_i / (2 pi) is kept modulo 1 in 64 bits, so an angle is off by no
+ * more than position * 2^-55 turns (times f_i where that is above 1) beside fp32 rounding of
+ * what is left; cosine, sine and products are fp32, the result is rounded once.  head_dim a
+ * multiple of 8, 8..512; rot_dim even, 2..head_dim; n_tokens 1..2^20. */
 int moe_rope(moe_ops* o, const moe_rope_table* r, const int* position, int n_tokens, int head_dim, int type,
              const void* q, long long q_stride, int q_heads, void* q_out, long long q_out_stride, const void* k,
              long long k_stride, int k_heads, void* k_out, long long k_out_stride, void* stream);

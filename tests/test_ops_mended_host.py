@@ -6,6 +6,7 @@ import pytest
 
 import bit_moe_decode_02_gb300 as moe
 from test_more_ops_host import A, INV, L, o, rope  # noqa: F401
+from test_more_ops_host import test_turns as check_turns
 
 
 @pytest.mark.parametrize("kw,word", [
@@ -91,3 +92,14 @@ def test_adapters_without_an_output(o):  # noqa: F811
     w = moe.moe_lora_weights(A, A, None, 1, 8, 64, 64)
     with pytest.raises(ValueError, match="moe_lora: out"):
         moe.moe_lora(o, w, Fake(torch.int32, 3), Fake(torch.bfloat16, 3, 64), None, stream=1)
+
+
+@pytest.mark.parametrize("kind", [moe.MOE_ROPE_LINEAR, moe.MOE_ROPE_PARTS, moe.MOE_ROPE_WAVELENGTH])
+def test_factors_that_leave_no_fraction(L, kind):  # noqa: F811
+    """A speed above 2^53 has no fraction of a turn in a double: such factors are refused, and down to 2^-32 the table holds what
+    tests/test_more_ops_host.py asks of every table."""
+    par = dict(length=4096.0, low=1.0, high=32.0)
+    for factor in (1e-300, 2.0 ** -33):
+        with pytest.raises(moe.MoeError, match="factor"):
+            moe.moe_rope_turns(64, 10000.0, kind, factor, **par)
+    check_turns(64, 10000.0, kind, (2.0 ** -32, *par.values()))
