@@ -124,5 +124,24 @@ __device__ __forceinline__ Final finish(float m, float l, const float* sinks, in
     return f;
 }
 
+// What is left of a row's sums for a join with others': not the sums, which may pass fp32's
+// range where the values do not, but their mean, kDown below itself (codes reach 2^9 above
+// a scale; what it loses lies below 2^-139), with m and l.
+constexpr float kDown = 9.765625e-4f;     // 2^-10
+// (l is 1 at least where there is a key: 1 / l within 2^-22.)
+__device__ __forceinline__ float inverse(float l)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
+    return l == 0.0f ? 0.0f : y;
+}
+// A row's result from its mean and the sums of all its keys.
+__device__ __forceinline__ Final finish_mean(float m, float l, const float* sinks, int hq)
+{
+    Final f = finish(m, l, sinks, hq);
+    f.mul = l == 0.0f ? 0.0f : f.mul * l * (1.0f / kDown);
+    return f;
+}
+
 }  // namespace attn
 }  // namespace moe

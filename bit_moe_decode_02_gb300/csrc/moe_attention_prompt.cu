@@ -257,8 +257,8 @@ struct Extent {
     __device__ __forceinline__ int parts(int most) const { return max(min(most, tiles / kPartTiles), 1); }
 };
 
-// A part's results: its 256 rows of O over their own sums, four columns of all rows after
-// another, then the rows' maxima and sums.
+// A part's results: its 256 rows' means (kDown of them, attn_device.cuh), four columns of all
+// rows after another, then the rows' maxima and sums.
 __host__ __device__ constexpr int part_floats(int d) { return kRows * d + 2 * kRows; }
 
 // The producer of a 4-bit cache: a tile's raw records, and how it goes through.  Keys whose
@@ -948,12 +948,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, Pr
             l = (l + *other) * kUnroom;
             wait(o_full + x, 0, status);
             tc::tc_fence_after();
-            const Final fin = parts > 1 ? Final{l == 0.0f ? 0.0f : 1.0f / l, 0.0f} : finish(m, l, a.sinks, hq);
+            const Final fin = parts > 1 ? Final{inverse(l) * kDown, 0.0f} : finish(m, l, a.sinks, hq);
             float* share = reinterpret_cast<float*>(a.ws + kCounterBytes) + (long long)after * part_floats(D);
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
-                const float mul = fin.mul * kUnroom * (L::MX ? __uint_as_float((uint32_t)was_of(ch) << 23) * 0x1p-13f : ref);
+                const float sums = fin.mul * kUnroom, unit = L::MX ? __uint_as_float((uint32_t)was_of(ch) << 23) * 0x1p-13f : ref, mul = sums * unit;
                 uint32_t v[32];
                 tm_ld32(to + 32 * ch, v);
                 tm_wait_ld(v);
@@ -962,8 +962,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, Pr
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4*>(share + ((half * (D / 8) + 8 * ch + k / 4) * kRows + x * 128 + r) * 4) =
-                                make_float4(__uint_as_float(v[k]) * mul, __uint_as_float(v[k + 1]) * mul, __uint_as_float(v[k + 2]) * mul,
-                                            __uint_as_float(v[k + 3]) * mul);
+                                make_float4(__uint_as_float(v[k]) * sums * unit, __uint_as_float(v[k + 1]) * sums * unit,
+                                            __uint_as_float(v[k + 2]) * sums * unit, __uint_as_float(v[k + 3]) * sums * unit);
                 } else if (in)
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
@@ -1008,8 +1008,13 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut 
     auto ml_of = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(share + (long long)p * part_floats(D) + kRows * D + 2 * row)); };
     float M = kNone, L = 0.0f;
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p)
-        M = fmaxf(M, ml_of(p).x);
+    for (int p = 0; p < parts; ++p) {
+        const float2 ml = ml_of(p);
+        const float m = fmaxf(M, ml.x);
+        L = L * ex2(M - m) + ml.y * ex2(ml.x - m);
+        M = m;
+    }
+    const float whole = inverse(L);
     float4 v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -1017,8 +1022,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut 
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) {
         const float2 ml = ml_of(p);
-        const float f = ml.y * ex2(ml.x - M);
-        L += f;
+        const float f = ml.y * ex2(ml.x - M) * whole;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const float4 y = __ldcg(reinterpret_cast<const float4*>(share + (long long)p * part_floats(D) + ((at + k) * kRows + row) * 4));
@@ -1026,7 +1030,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut 
         }
     }
     const int i = (w.rt * kRows + row) / a.group, hq = w.h * a.group + (w.rt * kRows + row) % a.group;
-    const Final fin = finish(M, L, a.sinks, hq);
+    const Final fin = finish_mean(M, L, a.sinks, hq);
     uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + 4 * at;
 #pragma unroll
     for (int k = 0; k < N; k += 2)
