@@ -184,28 +184,13 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, const Place& p, in
         a.lse[(i64)tok * a.q_heads + hq] = f.lse;
 }
 
-// Partial results joined one after another.
-struct Sum {
-    float m = kNone, l = 0.0f;
-    float4 v = make_float4(0, 0, 0, 0);
-    __device__ __forceinline__ void add(float2 ml, float4 y)
-    {
-        const float mn = fmaxf(m, ml.x), w0 = ex2(m - mn), w1 = ex2(ml.x - mn);
-        m = mn;
-        l = l * w0 + ml.y * w1;
-        v.x = v.x * w0 + y.x * w1, v.y = v.y * w0 + y.y * w1, v.z = v.z * w0 + y.z * w1, v.w = v.w * w0 + y.w * w1;
-    }
-    __device__ __forceinline__ void from_slot(const float* s, int D, int row, int col)
-    {
-        add(__ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row)), __ldcg(reinterpret_cast<const float4*>(s + row * D + col)));
-    }
-    __device__ __forceinline__ void to_slot(float* s, int D, int row, int col) const
-    {
-        __stcg(reinterpret_cast<float4*>(s + row * D + col), v);
-        if (col == 0)
-            __stcg(reinterpret_cast<float2*>(s + kRows * D + 2 * row), make_float2(m, l));
-    }
-};
+// A partial result: four columns of a row's mean, kDown of it (attn_device.cuh).
+__device__ __forceinline__ void to_slot(float* s, int D, int row, int col, float m, float l, float4 v)
+{
+    __stcg(reinterpret_cast<float4*>(s + row * D + col), v);
+    if (col == 0)
+        __stcg(reinterpret_cast<float2*>(s + kRows * D + 2 * row), make_float2(m, l));
+}
 
 // A group's part of an item that is left for the CTA to finish: its first one if
 // that began in an earlier group's run (kSlot: joined over the group's warps, in
@@ -941,6 +926,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
             }
 
             // ---- join the group's warps in the stage they have just read
+            float by[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if constexpr (R == 8) {
@@ -953,6 +939,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                 }
                 if ((R == 8 ? r : c) == 0)
                     mls[warp * kRows + my_row(e)] = make_float2(m[e], l[e] * kUnroom);
+                by[e] = inverse(l[e]) * kDown;         // of O, whose probabilities are as far up as l's
             }
             group_sync(1 + grp, C::GW * 32);
             // MXFP4: at a run's end nothing of the ring is wanted any more, and it holds all of O; else 64
@@ -963,7 +950,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
             float unit[D / 32];
 #pragma unroll
             for (int g = 0; g < D / 32; ++g)
-                unit[g] = (C::MX ? kv4::scale_of(__shfl_sync(~0u, unit4, 8 * g)) : ref) * kUnroom;
+                unit[g] = C::MX ? kv4::scale_of(__shfl_sync(~0u, unit4, 8 * g)) : ref;
             const Place place{it.c0, it.rt * R, it.h, rows};
             const bool done = it.t0 >= t_begin;
             // column group i of row x lies at i ^ (x % 8)
@@ -975,7 +962,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const int row = 2 * c + (k & 1);
-                                od[(sub * R + row) * width + ((2 * i + (k >> 1) - i0) ^ row) * 8 + r] = o[i][k] * unit[i / 2];
+                                od[(sub * R + row) * width + ((2 * i + (k >> 1) - i0) ^ row) * 8 + r] = o[i][k] * by[k & 1] * unit[i / 2];
                             }
                 } else {
 #pragma unroll
@@ -984,7 +971,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 *reinterpret_cast<float2*>(od + (sub * R + r + 8 * e) * width + ((i - i0) ^ r) * 8 + 2 * c) =
-                                    make_float2(o[i][2 * e] * unit[i / 4], o[i][2 * e + 1] * unit[i / 4]);
+                                    make_float2(o[i][2 * e] * by[e] * unit[i / 4], o[i][2 * e + 1] * by[e] * unit[i / 4]);
                 }
             };
             if (ends) {
@@ -1002,15 +989,27 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                 group_sync(1 + grp, C::GW * 32);
                 for (int x = sub * 32 + lane; x < rows * (PART / 4); x += C::GW * 32) {
                     const int row = x / (PART / 4), col = x % (PART / 4) * 4;
-                    Sum sum;
+                    float M = kNone, l = 0.0f, f[C::GW];
 #pragma unroll
                     for (int w = 0; w < C::GW; ++w)
-                        sum.add(mls[(grp * C::GW + w) * kRows + row],
-                                *reinterpret_cast<const float4*>(od + (w * R + row) * PART + ((col >> 3) ^ (row & 7)) * 8 + (col & 7)));
+                        M = fmaxf(M, mls[(grp * C::GW + w) * kRows + row].x);
+#pragma unroll
+                    for (int w = 0; w < C::GW; ++w) {
+                        const float2 ml = mls[(grp * C::GW + w) * kRows + row];
+                        l += f[w] = ml.y * ex2(ml.x - M);
+                    }
+                    const float whole = inverse(l);
+                    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int w = 0; w < C::GW; ++w) {
+                        const float4 y = *reinterpret_cast<const float4*>(od + (w * R + row) * PART + ((col >> 3) ^ (row & 7)) * 8 + (col & 7));
+                        const float x = f[w] * whole;
+                        v.x += y.x * x, v.y += y.y * x, v.z += y.z * x, v.w += y.w * x;
+                    }
                     if (done)
-                        store_row4(a, place, row, p * PART + col, sum.v, finish(sum.m, sum.l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
+                        store_row4(a, place, row, p * PART + col, v, finish_mean(M, l, a.sinks, it.h * a.group + (place.r0 + row) % a.group));
                     else
-                        sum.to_slot(slot, D, row, p * PART + col);
+                        to_slot(slot, D, row, p * PART + col, M, l, v);
                 }
             }
             if (!done && sub == 0 && lane == 0)
@@ -1055,12 +1054,15 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
         const int which = t0 < ct0 ? 0 : 1;
         for (int x = tid; x < place.nrows * (D / 4); x += C::THREADS) {
             const int row = x / (D / 4), col = x % (D / 4) * 4, at = row * D + ((col >> 3) ^ (row & 7)) * 8 + (col & 7);
-            Sum sum;
-            if (slot_at >= 0)
-                sum.from_slot(gslots + slot_at * slot_floats(), D, row, col);
-            // all maxima first: the parts' weights then do not wait for one another
-            float2 ml[C::WARPS];
-            float M = sum.m;
+            // all maxima and sums first: the parts' weights then do not wait for one another
+            float2 ml[C::WARPS], first_ml = make_float2(kNone, 0.0f);
+            float4 v = make_float4(0, 0, 0, 0);
+            if (slot_at >= 0) {
+                const float* s = gslots + slot_at * slot_floats();
+                first_ml = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+                v = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
+            }
+            float M = first_ml.x;
 #pragma unroll
             for (int w = 0; w < C::WARPS; ++w) {
                 ml[w] = mls[w * kRows + row];
@@ -1068,22 +1070,29 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                     ml[w] = make_float2(kNone, 0.0f);
                 M = fmaxf(M, ml[w].x);
             }
-            const float keep = ex2(sum.m - M);
-            sum.m = M;
-            sum.l *= keep;
-            sum.v.x *= keep, sum.v.y *= keep, sum.v.z *= keep, sum.v.w *= keep;
+            // (added up in pairs: ml[w].x is wanted no more)
+            first_ml.y *= ex2(first_ml.x - M);
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w)
+                ml[w].x = ml[w].y *= ex2(ml[w].x - M);
+#pragma unroll
+            for (int s = 1; s < C::WARPS; s *= 2)
+#pragma unroll
+                for (int w = 0; w + s < C::WARPS; w += 2 * s)
+                    ml[w].x += ml[w + s].x;
+            const float l = first_ml.y + ml[0].x, whole = inverse(l), keep = first_ml.y * whole;
+            v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
 #pragma unroll
             for (int w = 0; w < C::WARPS; ++w)
                 if (warps >> w & 1) {
                     const float4 y = *reinterpret_cast<const float4*>(sm + ods[w] + at * 4);
-                    const float f = ex2(ml[w].x - M);
-                    sum.l += ml[w].y * f;
-                    sum.v.x += y.x * f, sum.v.y += y.y * f, sum.v.z += y.z * f, sum.v.w += y.w * f;
+                    const float f = ml[w].y * whole;
+                    v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
                 }
             if (done)
-                store_row4(a, place, row, col, sum.v, finish(sum.m, sum.l, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
+                store_row4(a, place, row, col, v, finish_mean(M, l, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
             else
-                sum.to_slot(cslots + which * slot_floats(), D, row, col);
+                to_slot(cslots + which * slot_floats(), D, row, col, M, l, v);
         }
         if (!done) {
             across |= 1 << which;
@@ -1146,8 +1155,8 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                 M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
             for (int k = lane; k < K; k += 32) {
                 const float2 ml = part[k * kRows + row];
-                const float f = ex2(ml.x - M);
-                L += ml.y * f;
+                const float f = ml.y * ex2(ml.x - M);
+                L += f;
                 part[k * kRows + row].x = f;
             }
 #pragma unroll
@@ -1162,17 +1171,19 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
             float4 v = make_float4(0, 0, 0, 0);
             if (x0)
                 load_parts(x, from);
-            if (x < n4)
+            if (x < n4) {
+                const float whole = inverse(total[row].y);
                 for (int k0 = from; k0 < K;) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i)
                         if (k0 + i * split < K) {
-                            const float w = part[(k0 + i * split) * kRows + row].x;
+                            const float w = part[(k0 + i * split) * kRows + row].x * whole;
                             v.x += y[i].x * w, v.y += y[i].y * w, v.z += y[i].z * w, v.w += y[i].w * w;
                         }
                     k0 += AHEAD * split;
                     load_parts(x, k0);
                 }
+            }
             if (split > 1) {
                 acc[tid] = v;
                 __syncthreads();
@@ -1183,7 +1194,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                     }
             }
             if (x < n4 && from == 0)
-                store_row4(a, place, row, col, v, finish(total[row].x, total[row].y, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
+                store_row4(a, place, row, col, v, finish_mean(total[row].x, total[row].y, a.sinks, place.h * a.group + (place.r0 + row) % a.group));
         }
         __syncthreads();
     }

@@ -56,3 +56,15 @@ def test_prompts_in_parts_and_whole(fmt, blk, D, end, qscale):
     power = powers(fmt)[end]
     for heads, kv, new, lens in ((16, 2, [40], [4000]), (32, 4, [16, 1, 40], [1100, 2049, 3000]), (32, 16, [600], [1500])):
         check(cache(fmt, lens, kv, D, blk, power), new, lens, heads, qscale)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("blk,D", [(32, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("end", [0, 1])
+@pytest.mark.parametrize("qscale", [0.0, 0.05, 1.0])
+def test_single_tokens(fmt, blk, D, end, qscale):
+    """Items of 8 and 16 rows; one that all CTAs share, several that end within a CTA and within a group's run."""
+    power = powers(fmt)[end]
+    for heads, kv, new, lens in ((8, 1, [1], [9000]), (16, 1, [1], [9000]), (8, 2, [1] * 5, [4000, 70, 1, 1300, 700]),
+                                 (4, 4, [1] * 60, [300, 90, 500] * 20), (40, 4, [2] * 3, [900, 2000, 150])):
+        check(cache(fmt, lens, kv, D, blk, power), new, lens, heads, qscale)
