@@ -1245,7 +1245,7 @@ void launch_format(const AttnArgs& a, int num_sms, cudaStream_t s)
     // Eight rows at most for a sequence's kv head, on average: queries in an MMA's columns, not its rows.
     // 64 sequences of 12,000 tokens, 32 heads of 128 on 4: 99 us, 149 in items of 16 rows; of 4,000 tokens, 64
     // heads of 64 on 8: 56 and 70; 8 of them with 16 rows: 25.5 and 23.2, with 64 rows 57 and 44.
-    if ((long long)a.c.n_tokens * a.group <= 8ll * a.c.n_seqs)
+    if (narrow(a.call()))
         return launch_blocks<D, MOE_KV_MXFP4, 8>(a, num_sms, s);
     launch_blocks<D, MOE_KV_MXFP4, 16>(a, num_sms, s);
 }
@@ -1281,29 +1281,16 @@ static cudaError_t launch_attention_decode(const AttnArgs& a, int num_sms, cudaS
 
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
-    // Both kernels' costs, in tenths of what the decode kernel spends of an SM on 16 rows against 128 keys (8 bits: 0.55 us
-    // for D = 64, 0.72 for 128; 4 bits: 0.52, 0.79).  It spreads them over all SMs, beside some 10 us whatever the work (less in items of 8 rows); the
-    // prompt kernel takes up to 128 rows and, in 1.2 to 1.3 times that, up to 256 on one SM each, or their keys in parts
-    // on several with 10 to 15 us beside.  Measured over 4,000 keys, decode / prompt kernel, 8 bits and 4: 64 heads of 64 on
-    // 8, 8 sequences: 48 rows 37 / 29 and 37 / 32 us, 80 rows 51 / 44 and 51 / 49, 216 rows 119 / 58 and 115 / 60; one such
-    // sequence, 32 rows 18 / 15 and 17 / 16, 432 rows 44 / 25 and 43 / 27; 64 of them, 32 rows 131 / 172 and 127 / 236, 64
-    // rows 244 / 172 and 235 / 237; 32 heads of 128 on 4, 8 sequences: 32 rows 30 / 32 and 34 / 32, 64 rows 38 / 25 and
-    // 43 / 26, 216 rows 87 / 44 and 96 / 44.
-    // The lengths are on the device, so the rule sees their average alone.  64 heads of 64 on 8 in 8 bits, 63 single tokens
-    // and a prompt of 1,000 over 4,000 keys each: 236 us in one call, 72 + 103 in two; 255 and a prompt of 600 over 1,000
-    // keys: 199 us, 80 + 25 in two.  Nor does it see how many keys there are: one sequence of 600, 64 heads of 64 on 8,
-    // 64 rows in 4 bits: 10 / 15.
-    const long long rows = ((long long)a.c.n_tokens * a.group + a.c.n_seqs - 1) / a.c.n_seqs;     // of a sequence's kv head, on average
-    const long long heads = (long long)a.c.n_seqs * a.c.H, groups = heads * ((rows + 255) / 256);
-    const PromptCut cut = prompt_cut(a, num_sms);
-    const long long whole = groups < cut.whole ? groups : cut.whole, rest = (groups - whole) * cut.parts;
-    const long long full = (whole + num_sms - 1) / num_sms, part = (rest + num_sms - 1) / num_sms;       // rounds
-    const bool mx = a.c.fmt == MOE_KV_MXFP4, wide = a.c.D == 128, two = rows > 128;
-    const long long decode = 10 * heads * ((rows + 15) / 16) + (mx && rows <= 8 ? 600 : wide || mx ? 1000 : 700);
-    const long long each = wide ? (two ? 27 : mx ? 22 : 23) : mx ? (two ? 35 : 29) : two ? 32 : 25;
-    const long long prompt = each * num_sms * full + each * num_sms * part / cut.parts +
-                             (part == 0 ? 0 : mx ? (wide ? 800 : 900) : wide ? 1000 : 700);
-    return decode > prompt ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
+    // By both kernels' expected times (attn_plan.h).  The decode kernel spreads 16 rows against 128 keys over all SMs; the
+    // prompt kernel takes up to 256 rows on one SM each, or their keys in parts on several.  Measured, decode / prompt
+    // kernel, 8 bits: 64 heads of 64 on 8, one sequence, 64 rows: of 600 keys 14.8 / 13.0 us, of 4,000 19.9 / 15.2, of
+    // 16,000 29.4 / 24.4, within a window of 128 8.6 / 10.9; 8 sequences of 4,000 keys, 32 rows 30.0 / 28.6, 128 rows 75 / 45,
+    // 216 rows 119 / 57; 32 heads of 128 on 4, one sequence, 64 rows: of 600 keys 14.2 / 16.5, of 4,000 24.9 / 18.5.
+    // The lengths are on the device, so the rule sees the average tokens of a sequence, and of its keys what its row of the
+    // table can hold or a window lets through: a table much wider than the keys in it counts as full.  64 heads of 64 on 8
+    // in 8 bits, 63 single tokens and a prompt of 1,000 over 4,000 keys each: 236 us in one call, 72 + 103 in two; 255 and a
+    // prompt of 600 over 1,000 keys: 199 us, 80 + 25 in two.
+    return attn::takes_prompt_kernel(a.call(), num_sms) ? launch_attention_prompt(a, num_sms, s) : launch_attention_decode(a, num_sms, s);
 }
 
 }  // namespace moe

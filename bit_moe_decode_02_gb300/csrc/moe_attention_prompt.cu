@@ -47,9 +47,8 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 768;
-constexpr int kRows = 256;                // of a CTA
-constexpr int kKeys = 128;                // of a tile
-constexpr int kPartTiles = 4;             // a part of a group's keys has that many tiles at least
+constexpr int kRows = kGroupRows;         // of a CTA
+constexpr int kKeys = kTileKeys;          // of a tile
 constexpr int kRing = 8;                  // tiles whose scales are kept: the loads are at most four ahead of the softmax
 
 // A pass of a tile over a 4-bit cache: which of its keys take part, what their K's are scaled
@@ -1081,27 +1080,10 @@ cudaError_t prepare_prompt_kernels()
 
 size_t prompt_workspace_bytes(int num_sms) { return kCounterBytes + (size_t)num_sms * part_floats(128) * sizeof(float); }
 
-// An upper bound on the groups of 256 rows.
-static long long groups_of(const AttnArgs& a)
-{
-    const long long seqs = a.c.n_seqs < a.c.n_tokens ? a.c.n_seqs : a.c.n_tokens;
-    return ((long long)a.c.n_tokens * a.group + (kRows - 1) * seqs) / kRows * a.c.H;
-}
-
-// Which groups' keys are cut, and into how many parts: those that would be the last round of CTAs and leave SMs idle,
-// one part an SM, for which the workspace has room.  (Up to two, in the fewest rounds, is slower more often than not: 8
-// sequences of 4,000 keys, 32 heads of 128 on 4, 80 and 216 rows 37 and 52 us for 30 and 44.)
-PromptCut prompt_cut(const AttnArgs& a, int num_sms)
-{
-    const long long groups = groups_of(a), rest = groups % num_sms;
-    const int parts = rest > 0 ? (int)(num_sms / rest) : 1;
-    return PromptCut{(int)(parts > 1 ? groups - rest : groups), parts, (int)(parts > 1 ? rest : 0)};
-}
-
 cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s)
 {
     // CTAs beyond the last group or its last part end at once
-    const PromptCut cut = prompt_cut(a, num_sms);
+    const PromptCut cut = attn::prompt_cut(a.call(), num_sms);
     kernel_for(a.c.D, a.c.fmt, a.c.blk)<<<(unsigned)(cut.whole + cut.rest * cut.parts), kThreads, smem_of(a.c.D, a.c.fmt), s>>>(a, cut);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || cut.rest == 0)

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
+#include "attn_plan.h"
 
 struct moe_ops {
     int device = 0;
@@ -57,15 +58,11 @@ struct AttnArgs {
     uint16_t* out;           // [T][q_heads][D]
     float* lse;              // [T][q_heads] or nullptr
     uint8_t* ws;
+    attn::Call call() const { return attn::Call{c.n_seqs, c.n_tokens, group, c.H, c.D, c.blk, c.fmt, c.table_stride, window}; }
 };
 cudaError_t prepare_attention_kernels();
 cudaError_t prepare_prompt_kernels();
 cudaError_t launch_attention_prompt(const AttnArgs& a, int num_sms, cudaStream_t s);
-// Groups of 256 rows of the prompt kernel: `whole` by a CTA each, `rest` more in up to `parts` parts each.
-struct PromptCut {
-    int whole, parts, rest;
-};
-PromptCut prompt_cut(const AttnArgs& a, int num_sms);
 size_t prompt_workspace_bytes(int num_sms);
 cudaError_t launch_attention(const AttnArgs& a, int num_sms, cudaStream_t s);
 
