@@ -91,24 +91,25 @@ int check_rows_of(const char* who, const char* name, const void* p, long long st
     return MOE_OK;
 }
 
-// Rows of a tensor: `n` of them, `width` elements each, `stride` elements apart.
+// Rows of a tensor: `width` elements each, `stride` elements apart.
 struct Rows {
     const void* p;
     long long stride, width;
 };
-// Whether two tensors' rows share a byte.  Rows that lie within one another's
-// strides (parts of a fused projection) do not where their columns do not.
-bool rows_overlap(const Rows& a, const Rows& b, int n, int size)
+// Whether two tensors' n rows, of as and bs bytes an element, share a byte.  Rows that lie within
+// one another's strides (parts of a fused projection) do not where their columns do not.
+bool rows_overlap(const Rows& a, int as, const Rows& b, int bs, int n)
 {
-    if (!overlap(a.p, ((n - 1) * a.stride + a.width) * size, b.p, ((n - 1) * b.stride + b.width) * size))
+    if (!overlap(a.p, ((n - 1) * a.stride + a.width) * as, b.p, ((n - 1) * b.stride + b.width) * bs))
         return false;
-    if (n == 1 || a.stride != b.stride)
+    const long long pitch = a.stride * as;
+    if (n == 1 || pitch != b.stride * bs)
         return true;
-    const long long pitch = a.stride * size;
     long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % pitch;
     d += d < 0 ? pitch : 0;
-    return !(d >= a.width * size && pitch - d >= b.width * size);
+    return !(d >= a.width * as && pitch - d >= b.width * bs);
 }
+bool rows_overlap(const Rows& a, const Rows& b, int n, int size) { return rows_overlap(a, size, b, size, n); }
 // The same for rows and one contiguous array.
 bool rows_overlap(const Rows& a, int n, int size, const void* p, long long bytes)
 {
@@ -285,7 +286,7 @@ int moe_linear(moe_ops* o, const moe_linear_weights* w, const void* x_bf16, long
         return set_error(MOE_ERR_INVALID_ARG, "moe_linear: out must be aligned to its type (and not NULL)");
     if (out_stride < w->rows)
         return set_error(MOE_ERR_INVALID_ARG, "moe_linear: the stride of out (%lld) is less than a row (%d)", out_stride, w->rows);
-    if (overlap(x_bf16, ((M - 1) * x_stride + w->cols) * 2, out, ((M - 1) * out_stride + w->rows) * size))
+    if (rows_overlap(Rows{x_bf16, x_stride, w->cols}, 2, Rows{out, out_stride, w->rows}, size, M))
         return set_error(MOE_ERR_INVALID_ARG, "moe_linear: x overlaps out");
     moe::LinearArgs a{static_cast<const uint8_t*>(w->codes), w->scales, static_cast<const uint16_t*>(w->bias), w->rows, w->cols,
                       w->format, w->group, static_cast<const uint16_t*>(x_bf16), x_stride, M, out, out_stride, out_type,
@@ -478,7 +479,7 @@ int moe_lora(moe_ops* o, const moe_lora_weights* w, const int* index, const void
     if (out_stride < w->rows || (y && y_stride < w->rows))
         return set_error(MOE_ERR_INVALID_ARG, "moe_lora: the stride of out (%lld) or y (%lld) is less than a row (%d)", out_stride,
                          y_stride, w->rows);
-    if (overlap(x_bf16, ((M - 1) * x_stride + w->cols) * 2, out, ((M - 1) * out_stride + w->rows) * size))
+    if (rows_overlap(Rows{x_bf16, x_stride, w->cols}, 2, Rows{out, out_stride, w->rows}, size, M))
         return set_error(MOE_ERR_INVALID_ARG, "moe_lora: x overlaps out");
     const bool same = y == out && (M == 1 || y_stride == out_stride);
     if (y && !same && rows_overlap(Rows{y, y_stride, w->rows}, Rows{out, out_stride, w->rows}, M, size))

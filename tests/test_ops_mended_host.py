@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import bit_moe_decode_02_gb300 as moe
-from test_more_ops_host import A, INV, L, o, rope  # noqa: F401
+from test_more_ops_host import A, INV, L, lora, o, rope  # noqa: F401
 from test_more_ops_host import test_turns as check_turns
 
 
@@ -103,3 +103,16 @@ def test_factors_that_leave_no_fraction(L, kind):  # noqa: F811
         with pytest.raises(moe.MoeError, match="factor"):
             moe.moe_rope_turns(64, 10000.0, kind, factor, **par)
     check_turns(64, 10000.0, kind, (2.0 ** -32, *par.values()))
+
+
+def test_adapters_beside_their_input(L, o):  # noqa: F811
+    """x and out as columns of one buffer share no byte: the check after theirs, of y and out, is what refuses these; a row more to the
+    left, a row too wide, or another pitch, and they do."""
+    w = dict(rows=100, cols=256)
+    for kw in (dict(x=8 * A, xs=512, out=8 * A + 512, os=512), dict(x=8 * A + 256, xs=512, out=8 * A, os=512),
+               dict(x=8 * A, xs=512, out=8 * A + 512, os=256, type=0)):
+        size = 4 if kw.get("type") == 0 else 2
+        assert lora(L, o, w, y=kw["out"] + size, ys=kw["os"], **kw) == INV and "y overlaps out" in moe.moe_last_error()
+    for kw in (dict(x=8 * A, xs=512, out=8 * A + 510, os=512), dict(x=8 * A + 192, xs=512, out=8 * A, os=512),
+               dict(x=8 * A, xs=512, out=8 * A + 512, os=520), dict(x=8 * A, xs=512, out=8 * A + 512, os=512, type=0)):
+        assert lora(L, o, w, y=None, ys=0, **kw) == INV and "x overlaps out" in moe.moe_last_error()
