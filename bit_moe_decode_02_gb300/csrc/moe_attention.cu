@@ -1100,29 +1100,39 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
         }
     }
 
-    // ---- items that span CTAs: the last one to arrive joins them all
+    // ---- items that span CTAs: the last one to arrive joins them all.  A CTA arrives at both of its
+    // items before it joins either: else the other's join, in another CTA, would wait for this one
+    if (!across)
+        return;
     auto cta_of = [&](int t) {
         const int big = more * (each + 1);
         return t < big ? t / (each + 1) : more + (t - big) / each;
     };
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        int last = 0;
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+            if (across >> which & 1) {
+                const Piece& p = pieces[cross[which]];
+                const int ca = cta_of(p.t0);
+                if (atomicAdd(cnt + ca, 1u) == (unsigned)(cta_of(p.t1 - 1) - ca)) {
+                    last |= 1 << which;
+                    cnt[ca] = 0;
+                }
+            }
+        s_flag = last;
+    }
+    __syncthreads();
+    const int mine = s_flag;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        if (!(across >> which & 1))
+        if (!(mine >> which & 1))
             continue;
         const Piece& p = pieces[cross[which]];
         const Place place = p.p;
         const int ca = cta_of(p.t0), cb = cta_of(p.t1 - 1);               // of its first and last tile
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-            const unsigned old = atomicAdd(cnt + ca, 1u);
-            s_flag = old == (unsigned)(cb - ca);
-            if (s_flag)
-                cnt[ca] = 0;
-        }
-        __syncthreads();
-        if (!s_flag)
-            continue;
         __threadfence();
         // maxima and sums of every part and row, then their weights, in the ring; every 4
         // columns' parts are summed by `split` threads, then those.  The first parts are
