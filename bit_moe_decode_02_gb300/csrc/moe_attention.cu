@@ -1110,19 +1110,18 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
     };
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        int last = 0;
-#pragma unroll
-        for (int which = 0; which < 2; ++which)
-            if (across >> which & 1) {
-                const Piece& p = pieces[cross[which]];
-                const int ca = cta_of(p.t0);
-                if (atomicAdd(cnt + ca, 1u) == (unsigned)(cta_of(p.t1 - 1) - ca)) {
-                    last |= 1 << which;
-                    cnt[ca] = 0;
-                }
-            }
-        s_flag = last;
+    if (warp == 0) {
+        bool last = false;
+        if (lane < 2 && (across >> lane & 1)) {
+            const Piece& p = pieces[lane ? cross[1] : cross[0]];
+            const int ca = cta_of(p.t0);
+            last = atomicAdd(cnt + ca, 1u) == (unsigned)(cta_of(p.t1 - 1) - ca);
+            if (last)
+                cnt[ca] = 0;
+        }
+        const unsigned both = __ballot_sync(~0u, last);
+        if (lane == 0)
+            s_flag = both;
     }
     __syncthreads();
     const int mine = s_flag;
