@@ -7,7 +7,7 @@
 // bytes a cycle, where the MMAs need 2,048; it takes 3,900, because a row tile's
 // softmax and its MMAs (1,300) wait for one another, but for the first half of P V, and
 // otherwise only the other row tile's overlap.  Two prompts of 2,100 tokens over 3,000, 32 heads of 128 on 4 kv
-// heads: 261 us, 1,050 TFLOP/s (0.55 of the measured bf16 rate); 275 with P handed over
+// heads: 259 us, 1,058 TFLOP/s (0.56 of the measured bf16 rate); 275 with P handed over
 // whole instead of 266 in halves and 264.6 in quarters.
 //  - Work.  A CTA takes 256 rows (token, query head of one kv head) of one sequence,
 //    as two tiles of 128, against tiles of 128 keys.  Heads that share K and V share
@@ -24,7 +24,7 @@
 //  - Few groups of rows leave SMs idle, or the last ones of many do: then the keys of each of those are cut into
 //    parts (prompt_cut; four tiles at least), a CTA each, whose results a second kernel joins in their order.
 //    One sequence of 4,000 keys, 64 heads of 64 on 8, 80 tokens: 27 us, 60 by a CTA a group; 8 of them, 32 heads
-//    of 128 on 4, 8 tokens: 25 and 53; 160 groups 65 and 85; the two prompts above 261 and 266.
+//    of 128 on 4, 8 tokens: 25 and 53; 160 groups 65 and 85; the two prompts above 259 and 266.
 //  - Scales and maxima as in the decode kernel: K's scale multiplies a block's
 //    scores, V's enters the exponent; O is rescaled in tensor memory only where a
 //    row's maximum grows by more than 2^8, or the unit changes.  The unit is the
@@ -33,7 +33,7 @@
 //    goes through as several, one block each.
 //  - In 4 bits a token's groups have scales of their own, which go into the f16 operands:
 //    K's relative to the largest of a tile (Pass), V's to units of 32 columns of O each, so
-//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 273 us (350
+//    that the softmax knows one scale a tile.  The same prompts, sinks besides: 271 us (350
 //    before V's operands were stored without bank conflicts, 324 with a call at every wait, 305 with both
 //    forms of a score's rounding in one loop).
 #include <cstdint>

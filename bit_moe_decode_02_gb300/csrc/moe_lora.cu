@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_b_kernel(LoraArgs a)
 }
 
 typedef void (*KernelB)(LoraArgs);
-// NT: 8 KB of B a warp and step, whatever the rank
+// NT: 4 KB of B a warp and step at the largest rank of each, 1 KB at rank 8
 template <class T>
 KernelB pick(int rank, int& rows)
 {

@@ -548,8 +548,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * 2^-64 of the largest that the call's earlier keys of that sequence have in that group, or
  * below 2^-118, may count as 0; and a probability loses at most 2^-31 in units of that largest
  * scale.  The (sequence,
- * 16 rows, kv head, block) combinations of one call number less than 2^31 (else
- * nothing is written, MOE_ERR_DEVICE_FAULT). */
+ * 16 rows, kv head, block) combinations of one call number less than 2^31, of MXFP4 with
+ * 8 rows or fewer a sequence and kv head on average those of 8 rows (else nothing is
+ * written, MOE_ERR_DEVICE_FAULT). */
 int moe_attention(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q_bf16,
                   long long q_stride, int q_heads, float scale, int window, const float* sinks, void* out_bf16,
                   float* lse, void* stream);
@@ -585,8 +586,8 @@ typedef struct {
  * admitted, seq, position and slot may be NULL.  kv_len_out may be kv_len and state_out
  * may be state (updated in place); else a call with the same inputs gives the same
  * outputs, whatever an earlier one did.  No other arrays may overlap (checked).
- * A sequence whose length is negative, or whose tokens do not fit its row of the table,
- * gets none and keeps its length; a state outside the ring serves no one; where more
+ * A sequence whose length is negative or whose n_new is below -1, or whose tokens do not
+ * fit its row of the table, gets none and keeps its length; a state outside the ring serves no one; where more
  * blocks come back than the ring has room for none does, and ended sequences keep their
  * lengths: each sets MOE_ERR_DEVICE_FAULT.  So does a block number outside 0 ..
  * ring_size - 1; it is passed on as it is, and its tokens' slots are -1.
@@ -609,7 +610,9 @@ typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
  *               0..1, a = max(at(high), 0), b = min(at(low), rot_dim / 2 - 1),
  *               at(n) = rot_dim log(length / (2 pi n)) / (2 log base): pairs that turn
  *               more than `high` times within `length` positions keep their speed, those
- *               that turn less than `low` times are slowed down;
+ *               that turn less than `low` times are slowed down.  Some models round a and b
+ *               to whole pairs, or hold b to rot_dim - 1: their tables are the caller's to
+ *               make (moe_rope_table takes any);
  *   WAVELENGTH  f_i x + f_i / factor (1 - x), x = (length f_i / (2 pi) - low) /
  *               (high - low) held to 0..1. */
 typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_PARTS = 2, MOE_ROPE_WAVELENGTH = 3 } moe_rope_scaling;
