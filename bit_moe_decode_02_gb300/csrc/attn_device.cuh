@@ -125,21 +125,17 @@ __device__ __forceinline__ Final finish(float m, float l, const float* sinks, in
 }
 
 // What is left of a row's sums for a join with others': not the sums, which may pass fp32's
-// range where the values do not, but their mean, kDown below itself (codes reach 2^9 above
-// a scale; what it loses lies below 2^-139), with m and l.
-constexpr float kDown = 9.765625e-4f;     // 2^-10
-// (l is 1 at least where there is a key: 1 / l within 2^-22.)
-__device__ __forceinline__ float inverse(float l)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(l));
-    return l == 0.0f ? 0.0f : y;
-}
-// A row's result from its mean and the sums of all its keys.
+// range where the values do not, but half to all of their mean, the sums over the power of two
+// in l (exact, and no division in the way), kDown below that (codes reach 2^9 above a scale;
+// what it loses lies below 2^-137), with m and l.  l is 1 at least where there is a key.
+constexpr float kDown = 2.44140625e-4f;   // 2^-12
+__device__ __forceinline__ float pow2_in(float l) { return __uint_as_float(__float_as_uint(l) & 0x7f800000u); }
+__device__ __forceinline__ float pow2_under(float l) { return __uint_as_float(0x7f000000u - (__float_as_uint(l) & 0x7f800000u)); }   // 1 / pow2_in
+// A row's result from such a mean of all its keys.
 __device__ __forceinline__ Final finish_mean(float m, float l, const float* sinks, int hq)
 {
     Final f = finish(m, l, sinks, hq);
-    f.mul = l == 0.0f ? 0.0f : f.mul * l * (1.0f / kDown);
+    f.mul *= pow2_in(l) * (1.0f / kDown);
     return f;
 }
 

@@ -942,7 +942,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                 }
                 if ((R == 8 ? r : c) == 0)
                     mls[warp * kRows + my_row(e)] = make_float2(m[e], l[e] * kUnroom);
-                by[e] = inverse(l[e]) * kDown;         // of O, whose probabilities are as far up as l's
+                by[e] = pow2_under(l[e]) * kDown;      // of O, whose probabilities are as far up as l's
             }
             group_sync(1 + grp, C::GW * 32);
             // MXFP4: at a run's end nothing of the ring is wanted any more, and it holds all of O; else 64
@@ -999,9 +999,11 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
 #pragma unroll
                     for (int w = 0; w < C::GW; ++w) {
                         const float2 ml = mls[(grp * C::GW + w) * kRows + row];
-                        l += f[w] = ml.y * ex2(ml.x - M);
+                        const float x = ex2(ml.x - M);
+                        l += ml.y * x;
+                        f[w] = pow2_in(ml.y) * x;
                     }
-                    const float whole = inverse(l);
+                    const float whole = pow2_under(l);
                     float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
                     for (int w = 0; w < C::GW; ++w) {
@@ -1073,23 +1075,26 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                     ml[w] = make_float2(kNone, 0.0f);
                 M = fmaxf(M, ml[w].x);
             }
-            // (added up in pairs: ml[w].x is wanted no more)
-            first_ml.y *= ex2(first_ml.x - M);
+            // (l added up in pairs in ml[w].y, the weights in ml[w].x)
+            first_ml.x = ex2(first_ml.x - M);
 #pragma unroll
-            for (int w = 0; w < C::WARPS; ++w)
-                ml[w].x = ml[w].y *= ex2(ml[w].x - M);
+            for (int w = 0; w < C::WARPS; ++w) {
+                const float x = ex2(ml[w].x - M);
+                ml[w].x = pow2_in(ml[w].y) * x;
+                ml[w].y *= x;
+            }
 #pragma unroll
             for (int s = 1; s < C::WARPS; s *= 2)
 #pragma unroll
                 for (int w = 0; w + s < C::WARPS; w += 2 * s)
-                    ml[w].x += ml[w + s].x;
-            const float l = first_ml.y + ml[0].x, whole = inverse(l), keep = first_ml.y * whole;
+                    ml[w].y += ml[w + s].y;
+            const float l = first_ml.y * first_ml.x + ml[0].y, whole = pow2_under(l), keep = pow2_in(first_ml.y) * first_ml.x * whole;
             v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
 #pragma unroll
             for (int w = 0; w < C::WARPS; ++w)
                 if (warps >> w & 1) {
                     const float4 y = *reinterpret_cast<const float4*>(sm + ods[w] + at * 4);
-                    const float f = ml[w].y * whole;
+                    const float f = ml[w].x * whole;
                     v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
                 }
             if (done)
@@ -1167,9 +1172,9 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
                 M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
             for (int k = lane; k < K; k += 32) {
                 const float2 ml = part[k * kRows + row];
-                const float f = ml.y * ex2(ml.x - M);
-                L += f;
-                part[k * kRows + row].x = f;
+                const float x = ex2(ml.x - M);
+                L += ml.y * x;
+                part[k * kRows + row].x = pow2_in(ml.y) * x;
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1)
@@ -1184,7 +1189,7 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
             if (x0)
                 load_parts(x, from);
             if (x < n4) {
-                const float whole = inverse(total[row].y);
+                const float whole = pow2_under(total[row].y);
                 for (int k0 = from; k0 < K;) {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i)

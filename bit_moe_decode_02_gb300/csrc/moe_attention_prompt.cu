@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(AttnArgs a, Pr
             l = (l + *other) * kUnroom;
             wait(o_full + x, 0, status);
             tc::tc_fence_after();
-            const Final fin = parts > 1 ? Final{inverse(l) * kDown, 0.0f} : finish(m, l, a.sinks, hq);
+            const Final fin = parts > 1 ? Final{pow2_under(l) * kDown, 0.0f} : finish(m, l, a.sinks, hq);
             float* share = reinterpret_cast<float*>(a.ws + kCounterBytes) + (long long)after * part_floats(D);
             uint16_t* out = a.out + ((long long)(w.c0 + i) * a.q_heads + hq) * D + half * (D / 2);
 #pragma unroll
@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut 
         L = L * ex2(M - m) + ml.y * ex2(ml.x - m);
         M = m;
     }
-    const float whole = inverse(L);
+    const float whole = pow2_under(L);
     float4 v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(AttnArgs a, PromptCut 
 #pragma unroll 4
     for (int p = 0; p < parts; ++p) {
         const float2 ml = ml_of(p);
-        const float f = ml.y * ex2(ml.x - M) * whole;
+        const float f = pow2_in(ml.y) * ex2(ml.x - M) * whole;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const float4 y = __ldcg(reinterpret_cast<const float4*>(share + (long long)p * part_floats(D) + ((at + k) * kRows + row) * 4));
