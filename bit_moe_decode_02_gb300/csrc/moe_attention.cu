@@ -1116,14 +1116,21 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
         const int big = more * (each + 1);
         return t < big ? t / (each + 1) : more + (t - big) / each;
     };
+    int first_cta[2], last_cta[2];                                        // of the items' tiles
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+        if (across >> which & 1) {
+            const Piece& p = pieces[cross[which]];
+            first_cta[which] = cta_of(p.t0);
+            last_cta[which] = cta_of(p.t1 - 1);
+        }
     __threadfence();
     __syncthreads();
     if (warp == 0) {
         bool last = false;
         if (lane < 2 && (across >> lane & 1)) {
-            const Piece& p = pieces[lane ? cross[1] : cross[0]];
-            const int ca = cta_of(p.t0);
-            last = atomicAdd(cnt + ca, 1u) == (unsigned)(cta_of(p.t1 - 1) - ca);
+            const int ca = lane ? first_cta[1] : first_cta[0], cb = lane ? last_cta[1] : last_cta[0];
+            last = atomicAdd(cnt + ca, 1u) == (unsigned)(cb - ca);
             if (last)
                 cnt[ca] = 0;
         }
@@ -1137,9 +1144,8 @@ __global__ void __launch_bounds__((Decode<D, FMT, BLK, R>::THREADS), 1) decode_a
     for (int which = 0; which < 2; ++which) {
         if (!(mine >> which & 1))
             continue;
-        const Piece& p = pieces[cross[which]];
-        const Place place = p.p;
-        const int ca = cta_of(p.t0), cb = cta_of(p.t1 - 1);               // of its first and last tile
+        const Place place = pieces[which ? cross[1] : cross[0]].p;
+        const int ca = which ? first_cta[1] : first_cta[0], cb = which ? last_cta[1] : last_cta[0];
         __threadfence();
         // maxima and sums of every part and row, then their weights, in the ring; every 4
         // columns' parts are summed by `split` threads, then those.  The first parts are
