@@ -13,8 +13,9 @@
 //    device, so the cut is made there.  Runs that end inside an item leave
 //    partial results, which are joined in a fixed order (results do not depend
 //    on timing): within a CTA, then by the last CTA to arrive at an item's
-//    counter.  A part is the mean of its keys' values with its maximum and sum, not
-//    the sum of the values: that may pass fp32's range where no value does.
+//    counter.  A part is its keys' weighted sum over a power of two, half to all of their
+//    mean, with its maximum and sum of weights: the weighted sum itself may pass fp32's
+//    range where no value does.
 //  - Loads.  A block's K and V codes of one head are contiguous: one bulk copy
 //    per tile into the group's ring (192 KB in flight per SM), its scales with
 //    an 8-byte cp.async on the same barrier.
@@ -30,7 +31,7 @@
 //    what its subnormals lose of p is below 2^-31 a key: 2^20 keys lose less than the
 //    output's rounding.
 // Measured: 64 sequences of 12,000 tokens on average, 32 heads of 128 on 4 (INT8),
-// 146 us, 5.7 TB/s of codes, 0.83 of a plain copy's rate.  Two warps a scheduler (230
+// 145 us, 5.7 TB/s of codes, 0.83 of a plain copy's rate.  Two warps a scheduler (230
 // registers) are two chains of conversions and MMAs, which issue 0.4 instructions a
 // cycle: that, not the loads in flight, is what is left.  One sequence of 4,300
 // tokens, 64 heads of 64 on 8: 11.8 us, nearly all of it the way through: 1.9 us to
@@ -38,11 +39,11 @@
 // and one over the CTAs (5); the same heads within a window of 128, 4 sequences: 7.2 us.
 // Lengths differ by more than their keys: of 700 to 9,000 tokens most take 14 to 18 us and
 // one in four 10 to 12, by where the runs of tiles meet the items' ends.
-// In 4 bits (mx_tile): the 64 sequences take 100 us, 4.4 TB/s (0.65 of a copy), bound by
+// In 4 bits (mx_tile): the 64 sequences take 99 us, 4.4 TB/s (0.65 of a copy), bound by
 // issue: 630 instructions for 32 keys and 8 rows at 0.55 a cycle, of which the conversions
 // (one for two codes, at half rate) and products with scales are a third.  With items of 16
 // rows, as in 8 bits, and 12 warps 149 us, with 8 warps 159; one sequence of 6,070 tokens
-// 12.0 us, the same way through.
+// 11.7 us, the same way through.
 #include <algorithm>
 #include <cstdint>
 
@@ -187,7 +188,7 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, const Place& p, in
         a.lse[(i64)tok * a.q_heads + hq] = f.lse;
 }
 
-// A partial result: four columns of a row's mean, kDown of it (attn_device.cuh).
+// A partial result: four columns of a row, as attn_device.cuh keeps them.
 __device__ __forceinline__ void to_slot(float* s, int D, int row, int col, float m, float l, float4 v)
 {
     __stcg(reinterpret_cast<float4*>(s + row * D + col), v);

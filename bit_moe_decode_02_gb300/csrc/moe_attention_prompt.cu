@@ -256,8 +256,8 @@ struct Extent {
     __device__ __forceinline__ int parts(int most) const { return max(min(most, tiles / kPartTiles), 1); }
 };
 
-// A part's results: its 256 rows' means (kDown of them, attn_device.cuh), four columns of all
-// rows after another, then the rows' maxima and sums.
+// A part's results: its 256 rows as attn_device.cuh keeps them, four columns of all rows after
+// another, then the rows' maxima and sums.
 __host__ __device__ constexpr int part_floats(int d) { return kRows * d + 2 * kRows; }
 
 // The producer of a 4-bit cache: a tile's raw records, and how it goes through.  Keys whose
