@@ -55,12 +55,11 @@ inline PromptCut prompt_cut(const Call& c, int num_sms)
     return PromptCut{(int)(groups - rest), (int)parts, (int)rest};
 }
 
-// What a call is expected to take with each kernel, in ns.  Fitted to 9,400 calls of each: E4M3
-// and 4 bits; 64 heads of 64 on 8, 16 of 64 on 2, 32 of 128 on 4 and on 8; 1 to 64 sequences of
-// 130 to 16,000 keys, whole and within windows of 128 to 1,024; 1 to 100 tokens each.  Over them,
-// and over 1,500 others (INT8, other heads, blocks and lengths that differ), the kernel that is
-// taken is 1 % behind the better one on average, more than a tenth in one call of 27, nearly
-// always the decode kernel.
+// What a call is expected to take with each kernel, in ns.  Fitted to 15,400 calls of each: every
+// format, block and head size; 16 to 80 heads on 1 to 16; 1 to 200 sequences of 50 to 20,000
+// keys, whole and within windows, of one length and of several; 1 to 1,500 tokens each.  Over 3,000
+// others the kernel that is taken is 0.6 % behind the better one on average, more than a tenth
+// in one call of 38, mostly the decode kernel.
 // Rows are the average of a sequence's kv head, keys the bound of `pieces`.
 
 // Beside its start: a tile of 128 keys of an item, over all SMs, or for an item that is not cut
@@ -71,8 +70,8 @@ inline double decode_ns(const Call& c, int num_sms)
     struct Cost {
         double start, tile, join, item, row;
     };
-    static const Cost costs[2][3] = {{{6962, 500, 7913, 1039, 15}, {7154, 471, 8684, 1079, 15}, {7540, 303, 10010, 609, 29}},
-                                     {{7760, 657, 10372, 1884, 16}, {8900, 704, 12961, 2259, 15}, {7685, 463, 10688, 779, 126}}};
+    static const Cost costs[2][3] = {{{6502, 460, 8455, 1265, 18}, {7233, 449, 8827, 1081, 16}, {6141, 268, 10126, 1299, 199}},
+                                     {{7675, 614, 10922, 2143, 19}, {9014, 671, 13229, 2354, 16}, {7475, 412, 11032, 1228, 166}}};
     const bool mx = c.fmt == MOE_KV_MXFP4, eight = narrow(c);
     const Cost& k = costs[c.D == 128][eight ? 2 : mx];
     const long long rows = ((long long)c.n_tokens * c.group + c.n_seqs - 1) / c.n_seqs, of = eight ? 8 : 16;
@@ -92,10 +91,10 @@ inline double prompt_ns(const Call& c, int num_sms)
     struct Cost {
         double start, tile, join, part, round;
     };
-    static const Cost costs[2][2][2] = {{{{8577, 1131, 499, 380, 6242}, {12855, 1426, 304, 385, 11201}},
-                                         {{8817, 1295, 403, 378, 6481}, {13593, 1490, 0, 373, 11846}}},
-                                        {{{10453, 1369, 949, 352, 8113}, {17991, 1599, 153, 339, 8113}},
-                                         {{10106, 1516, 611, 343, 7693}, {17747, 1730, 8, 311, 7693}}}};
+    static const Cost costs[2][2][2] = {{{{8138, 1147, 1296, 332, 6223}, {13135, 1419, 777, 337, 9764}},
+                                         {{8560, 1321, 706, 363, 6330}, {13928, 1508, 0, 352, 10186}}},
+                                        {{{10000, 1389, 1573, 352, 8060}, {18063, 1586, 1033, 327, 13407}},
+                                         {{9864, 1538, 820, 356, 7581}, {18231, 1705, 325, 338, 13418}}}};
     const long long rows = ((long long)c.n_tokens * c.group + c.n_seqs - 1) / c.n_seqs;
     const Cost& k = costs[c.D == 128][c.fmt == MOE_KV_MXFP4][rows > 128];
     const long long groups = (long long)c.n_seqs * c.H * ((rows + kGroupRows - 1) / kGroupRows);
