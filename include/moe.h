@@ -541,7 +541,9 @@ int moe_kv_read(moe_ops* o, const moe_kv_cache* cache, const moe_kv_batch* batch
  * denominator.  A row of which nothing is visible (its blocks are missing)
  * is 0, with the sink (or -inf) as its lse.  A row whose q or sink has a NaN is NaN,
  * and so is its lse; other rows are not touched by it.
- * Scores and sums are fp32; q enters as f16 after an exact power-of-two rescale
+ * Scores and sums are fp32, and parts of a row that are summed apart are joined so that out
+ * is finite wherever its value is (and off by no more than 2^-137 beside the rest, which
+ * shows below 2^-126 only); q enters as f16 after an exact power-of-two rescale
  * of each row, codes are exact in f16, and e^(s_j - m) enters the second
  * product as 11 bits down to 2^-20, below that within 2^-31.  MXFP4: of a key, groups whose
  * scale is below 2^-27 of its largest group's count as 0; V's groups whose scale is below
