@@ -32,7 +32,8 @@ def cache(fmt, lens, kv, D, blk, power):
 
 def check(c, new, lens, heads, qscale):
     """The bound that every format's tests use (`attention`: f16 probabilities and one rounding to bf16), without its smallest term,
-    which is above the smallest values here.  A part's mean is held 2^-10 down: a value of 2^-107 keeps 32 - 2 bits there."""
+    which is above the smallest values here.  A part's values are held at least at 2^-13 of themselves: one of 2^-107 keeps all of fp32's
+    bits there, one of 2^-112 its 24."""
     g = torch.Generator(device="cuda").manual_seed(3)
     q = (torch.randn(sum(new), heads, c.D, generator=g, device="cuda") * qscale).bfloat16()
     out = torch.empty_like(q)
